@@ -1,0 +1,304 @@
+// la_api.cu -- C ABI of the decayed linear attention, the query/key preparation and the
+// state pool (declared in include/kda.h): argument checks, workspace layout, dispatch.
+#include <stdint.h>
+
+#include <cmath>
+
+#include "kda_la.cuh"
+
+namespace kda {
+cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int64_t seg_tokens,
+                           int32_t *seg_off, int32_t *bnd_off, int32_t *multi_off, StatusWord *st,
+                           const float *h0, float *hT, int H, int64_t dkdv, cudaStream_t s);
+cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
+                           int64_t dkdv, int sms, cudaStream_t s);
+cudaError_t launch_la_simt(bool out, int dtype, int dk, int dv, const la::Plan &p, const void *q,
+                           const void *k, const void *v, int64_t qs, int64_t ks, int64_t vs,
+                           const float *g, int gpt, const float *h0, float *hT, void *o,
+                           float *bnd, float *bnd_log, StatusWord *st, int64_t max_items,
+                           cudaStream_t s);
+cudaError_t launch_la_decode(int dtype, int dk, int dv, const void *q, const void *k,
+                             const void *v, const float *g, float *state, void *o, int N, int H,
+                             int Hk, int64_t qs, int64_t ks, int64_t vs, int gpt,
+                             const int32_t *idx, int P, StatusWord *st, cudaStream_t s);
+cudaError_t launch_qk(int dtype, int D, const void *q, const void *k, void *qo, void *ko,
+                      int64_t T_tot, int Hq, int Hk, int64_t qs, int64_t ks, int64_t qos,
+                      int64_t kos, const float *qw, const float *kw, int norm, float eps,
+                      float q_scale, float k_scale, const int32_t *pos, const float *inv_freq,
+                      int rot, int interleaved, float rope_scale, int sms, cudaStream_t s);
+cudaError_t launch_pool_copy(float *p, int P, int64_t elems, const int32_t *src,
+                             const int32_t *dst, int n, StatusWord *st, int sms, cudaStream_t s);
+cudaError_t launch_pool_compact(float *p, int P, int64_t elems, const uint8_t *live,
+                                int32_t *new_index, int32_t *n_live, int32_t *moves, int sms,
+                                cudaStream_t s);
+}  // namespace kda
+
+using namespace kda;
+
+namespace {
+
+inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+inline bool head_ok(int32_t d) { return d == 32 || d == 64 || d == 128; }
+inline bool dtype_ok(int32_t d) { return d == KDA_F32 || d == KDA_BF16; }
+inline int64_t elt(int32_t dtype) { return dtype == KDA_BF16 ? 2 : 4; }
+kda_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+
+// SMs of the current device; a GB300's where there is none (sizing on a host without a GPU).
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 152;
+    return sms;
+}
+
+// A strided [T, heads, D] tensor: rows in 16-byte steps, no overlap between tokens (an input
+// of plain loads may repeat one token, stride 0), and no offset past 2^62 bytes.
+bool stride_ok(int64_t stride, int64_t T, int32_t heads, int32_t D, int32_t dtype,
+               bool repeat = false) {
+    return (stride >= (int64_t)heads * D || (repeat && stride == 0)) && (stride * elt(dtype)) % 16 == 0 &&
+           (T == 0 || stride <= ((int64_t)1 << 59) / T);
+}
+
+// Tokens of a segment: chunks are 128 tokens, and the SMs should be evenly busy.  The cost
+// of a choice is counted in chunk times: the output pass walks a segment's chunks one after
+// the other with a start-up of about two, the waves of segments over the SMs follow each
+// other; cutting sequences at all adds a pass over k and v at about half the cost, and two
+// launches.  Lengths are on the device, so the average one stands for all.
+constexpr int64_t kUnit = 128;
+int64_t segment_tokens(int64_t T, int32_t N, int32_t H, int sms) {
+    if (N <= 0 || T <= 0) return kUnit;
+    const int64_t avg = (T + kUnit * N - 1) / (kUnit * N);   // chunks of the average sequence
+    const int64_t most = avg < 64 ? avg : 64;
+    int64_t best = most;
+    double best_cost = 1e300;
+    for (int64_t L = most; L >= 1; L = L > 16 ? L - 4 : L - 1) {
+        const int64_t segs = (avg + L - 1) / L;
+        const int64_t items = segs * N * H;
+        const double waves = (double)((items + sms - 1) / sms);
+        double cost = waves * (L + 2.0);
+        if (segs > 1) cost += (double)(((segs - 1) * N * H + sms - 1) / sms) * (0.5 * L + 2.0) + 4.0;
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = L;
+        }
+    }
+    // one segment for the average sequence: longer ones are cut at four times the average
+    return (best == avg ? 4 * best : best) * kUnit;
+}
+
+struct LaLayout {
+    int64_t seg_tokens, max_segs, max_bnd;
+    size_t plan_off, log_off, bnd_off, total;
+};
+
+LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t dk, int32_t dv, int sms) {
+    LaLayout L{};
+    L.seg_tokens = segment_tokens(T, N, H, sms);
+    L.max_segs = T / L.seg_tokens + N;
+    // inner boundaries, and one kept initial state for each sequence that has one
+    L.max_bnd = T / L.seg_tokens + (T / L.seg_tokens < N ? T / L.seg_tokens : N);
+    L.plan_off = kHeaderBytes;
+    L.log_off = L.plan_off + round_up(3 * sizeof(int32_t) * ((size_t)N + 1), 256);
+    L.bnd_off = L.log_off + round_up(sizeof(float) * (size_t)L.max_bnd * H, 256);
+    L.total = L.bnd_off + sizeof(float) * (size_t)L.max_bnd * H * dk * dv;
+    return L;
+}
+
+bool la_sizes_ok(int64_t T, int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t dv) {
+    return N >= 0 && T >= 0 && H > 0 && Hk > 0 && H % Hk == 0 && (T == 0 || N > 0) &&
+           T < ((int64_t)1 << 31) && T <= ((int64_t)1 << 40) / ((int64_t)H * (dk > dv ? dk : dv)) &&
+           (int64_t)N * H <= 0x7fffffffLL;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_la_chunk_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H,
+                                       int32_t Hk, int32_t dk, int32_t dv, int32_t dtype) {
+    if (!dtype_ok(dtype) || !head_ok(dk) || !head_ok(dv) ||
+        !la_sizes_ok(total_tokens, num_seqs, H, Hk, dk, dv))
+        return 0;
+    return la_layout(total_tokens, num_seqs, H, dk, dv, sm_count()).total;
+}
+
+kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
+                            const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                            int32_t H, int32_t Hk, int32_t dk, int32_t dv, int32_t dtype,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            int32_t g_per_token, const float *initial_state,
+                            float *final_state, void *o, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    if (!dtype_ok(dtype) || !head_ok(dk) || !head_ok(dv)) return KDA_ERR_UNSUPPORTED;
+    if (!la_sizes_ok(total_tokens, num_seqs, H, Hk, dk, dv)) return KDA_ERR_INVALID_ARG;
+    if (!stride_ok(q_stride, total_tokens, Hk, dk, dtype) ||
+        !stride_ok(k_stride, total_tokens, Hk, dk, dtype) ||
+        !stride_ok(v_stride, total_tokens, H, dv, dtype))
+        return KDA_ERR_INVALID_ARG;
+    if (!cu_seqlens || !workspace) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!q || !k || !v || !g || !o)) return KDA_ERR_INVALID_ARG;
+    const void *al16[] = {q, k, v, o, initial_state, final_state};
+    for (const void *p : al16)
+        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(g, 4) || !aligned(cu_seqlens, 4) || !aligned(workspace, 256))
+        return KDA_ERR_INVALID_ARG;
+    if (o && (o == q || o == k || o == v)) return KDA_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    const LaLayout L = la_layout(total_tokens, num_seqs, H, dk, dv, sms);
+    if (workspace_bytes < L.total) return KDA_ERR_INVALID_ARG;
+
+    cudaStream_t s = (cudaStream_t)stream;
+    StatusWord *st = (StatusWord *)workspace;
+    if (num_seqs == 0) return cuda_status(cudaMemsetAsync(st, 0, sizeof(StatusWord), s));
+    uint8_t *ws = (uint8_t *)workspace;
+    int32_t *plan = (int32_t *)(ws + L.plan_off);
+    float *bnd_log = (float *)(ws + L.log_off), *bnd = (float *)(ws + L.bnd_off);
+    const int64_t dkdv = (int64_t)dk * dv;
+    const la::Plan p{cu_seqlens, plan, plan + num_seqs + 1, plan + 2 * (num_seqs + 1), num_seqs, H,
+                     Hk, L.seg_tokens, initial_state && initial_state == final_state};
+    cudaError_t e = launch_la_plan(cu_seqlens, num_seqs, total_tokens, L.seg_tokens, plan,
+                                   plan + num_seqs + 1, plan + 2 * (num_seqs + 1), st,
+                                   initial_state, final_state, H, dkdv, s);
+    if (e != cudaSuccess) return KDA_ERR_CUDA;
+    if (total_tokens == 0) return KDA_OK;
+    if (total_tokens > L.seg_tokens) {   // else no sequence has an inner boundary
+        e = launch_la_simt(false, dtype, dk, dv, p, q, k, v, q_stride, k_stride, v_stride, g,
+                           g_per_token, nullptr, nullptr, nullptr, bnd, bnd_log, st,
+                           L.max_bnd * H, s);
+        if (e == cudaSuccess) e = launch_la_scan(p, initial_state, bnd, bnd_log, dkdv, sms, s);
+        if (e != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    return cuda_status(launch_la_simt(true, dtype, dk, dv, p, q, k, v, q_stride, k_stride, v_stride,
+                                      g, g_per_token, initial_state, final_state, o, bnd, bnd_log,
+                                      st, L.max_segs * H, s));
+}
+
+static kda_status la_decode_impl(const void *q, const void *k, const void *v, const float *g,
+                                 float *state, const int32_t *idx, int32_t P, void *o, int32_t N,
+                                 int32_t H, int32_t Hk, int32_t dk, int32_t dv, int32_t dtype,
+                                 int64_t qs, int64_t ks, int64_t vs, int32_t gpt, StatusWord *st,
+                                 void *stream) {
+    if (!dtype_ok(dtype) || !head_ok(dk) || !head_ok(dv)) return KDA_ERR_UNSUPPORTED;
+    if (N < 0 || P < 0 || H <= 0 || Hk <= 0 || H % Hk != 0 || (int64_t)N * H > 0x1fffffffLL)
+        return KDA_ERR_INVALID_ARG;
+    if (!stride_ok(qs, N, Hk, dk, dtype, true) || !stride_ok(ks, N, Hk, dk, dtype, true) ||
+        !stride_ok(vs, N, H, dv, dtype, true))
+        return KDA_ERR_INVALID_ARG;
+    if (N > 0 && (!q || !k || !v || !g || !state || !o)) return KDA_ERR_INVALID_ARG;
+    const void *al16[] = {q, k, v, o, state};
+    for (const void *p : al16)
+        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(g, 4) || !aligned(idx, 4)) return KDA_ERR_INVALID_ARG;
+    if (o && (o == q || o == k || o == v || o == (void *)state)) return KDA_ERR_INVALID_ARG;
+    if (st && cudaMemsetAsync(st, 0, sizeof(StatusWord), (cudaStream_t)stream) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    if (N == 0) return KDA_OK;
+    return cuda_status(launch_la_decode(dtype, dk, dv, q, k, v, g, state, o, N, H, Hk, qs, ks, vs,
+                                        gpt, idx, P, st, (cudaStream_t)stream));
+}
+
+kda_status kda_la_decode_step(const void *q, const void *k, const void *v, const float *g,
+                              float *state, void *o, int32_t N, int32_t H, int32_t Hk,
+                              int32_t dk, int32_t dv, int32_t dtype, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int32_t g_per_token,
+                              void *stream) {
+    return la_decode_impl(q, k, v, g, state, nullptr, N, o, N, H, Hk, dk, dv, dtype, q_stride,
+                          k_stride, v_stride, g_per_token, nullptr, stream);
+}
+
+kda_status kda_la_decode_step_indexed(const void *q, const void *k, const void *v,
+                                      const float *g, float *state_pool,
+                                      const int32_t *state_idx, int32_t P, void *o, int32_t N,
+                                      int32_t H, int32_t Hk, int32_t dk, int32_t dv,
+                                      int32_t dtype, int64_t q_stride, int64_t k_stride,
+                                      int64_t v_stride, int32_t g_per_token, void *workspace,
+                                      size_t workspace_bytes, void *stream) {
+    if (N > 0 && !state_idx) return KDA_ERR_INVALID_ARG;
+    if (workspace && (workspace_bytes < kHeaderBytes || !aligned(workspace, 256)))
+        return KDA_ERR_INVALID_ARG;
+    return la_decode_impl(q, k, v, g, state_pool, state_idx, P, o, N, H, Hk, dk, dv, dtype,
+                          q_stride, k_stride, v_stride, g_per_token, (StatusWord *)workspace,
+                          stream);
+}
+
+kda_status kda_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                            int64_t total_tokens, int32_t Hq, int32_t Hk, int32_t D,
+                            int32_t dtype, int64_t q_stride, int64_t k_stride,
+                            int64_t q_out_stride, int64_t k_out_stride, const float *q_weight,
+                            const float *k_weight, int32_t norm, float eps, float q_scale,
+                            float k_scale, const int32_t *positions, const float *inv_freq,
+                            int32_t rot_dim, int32_t layout, float rope_scale, void *stream) {
+    if (!dtype_ok(dtype) || !head_ok(D)) return KDA_ERR_UNSUPPORTED;
+    if (norm < KDA_NORM_NONE || norm > KDA_NORM_RMS ||
+        (layout != KDA_ROPE_HALF && layout != KDA_ROPE_INTERLEAVED))
+        return KDA_ERR_INVALID_ARG;
+    if (rot_dim < 0 || rot_dim > D) return KDA_ERR_INVALID_ARG;
+    if (rot_dim % 16 != 0) return KDA_ERR_UNSUPPORTED;
+    if (total_tokens < 0 || total_tokens >= ((int64_t)1 << 31) || Hq <= 0 || Hk < 0 ||
+        (int64_t)Hq + Hk > 65536 || !(eps >= 0.f) || std::isinf(eps))
+        return KDA_ERR_INVALID_ARG;
+    if (!stride_ok(q_stride, total_tokens, Hq, D, dtype, true) ||
+        !stride_ok(q_out_stride, total_tokens, Hq, D, dtype) ||
+        (Hk > 0 && (!stride_ok(k_stride, total_tokens, Hk, D, dtype, true) ||
+                    !stride_ok(k_out_stride, total_tokens, Hk, D, dtype))))
+        return KDA_ERR_INVALID_ARG;
+    if (total_tokens == 0) return KDA_OK;
+    if (!q || !q_out || (Hk > 0 && (!k || !k_out)) || (rot_dim > 0 && (!positions || !inv_freq)))
+        return KDA_ERR_INVALID_ARG;
+    const void *al16[] = {q, k, q_out, k_out, q_weight, k_weight};
+    for (const void *p : al16)
+        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(positions, 4) || !aligned(inv_freq, 4)) return KDA_ERR_INVALID_ARG;
+    // in place only with the input's own stride
+    if ((q_out == q && q_out_stride != q_stride) || (Hk > 0 && k_out == k && k_out_stride != k_stride))
+        return KDA_ERR_INVALID_ARG;
+    if (Hk > 0 && (q_out == k || k_out == q || q_out == k_out)) return KDA_ERR_INVALID_ARG;
+    return cuda_status(launch_qk(dtype, D, q, k, q_out, k_out, total_tokens, Hq, Hk, q_stride,
+                                 k_stride, q_out_stride, k_out_stride, q_weight, k_weight, norm,
+                                 eps, q_scale, k_scale, positions, inv_freq, rot_dim,
+                                 layout == KDA_ROPE_INTERLEAVED, rope_scale, sm_count(),
+                                 (cudaStream_t)stream));
+}
+
+size_t kda_state_pool_workspace_size(int32_t P) {
+    return P < 0 ? 0 : kHeaderBytes + round_up(sizeof(int32_t) * (4 + 2 * ((size_t)P / 2 + 1)), 256);
+}
+
+static bool pool_ok(const float *pool, int32_t P, int64_t slot_elems) {
+    return P >= 0 && slot_elems > 0 && slot_elems % 4 == 0 &&
+           (P == 0 || slot_elems <= ((int64_t)1 << 58) / P) && (P == 0 || pool) && aligned(pool, 16);
+}
+
+kda_status kda_state_pool_copy(float *pool, int32_t P, int64_t slot_elems,
+                               const int32_t *src_idx, const int32_t *dst_idx, int32_t n,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+    if (!pool_ok(pool, P, slot_elems) || n < 0 || n > (1 << 24)) return KDA_ERR_INVALID_ARG;
+    if (n > 0 && (!src_idx || !dst_idx || !aligned(src_idx, 4) || !aligned(dst_idx, 4)))
+        return KDA_ERR_INVALID_ARG;
+    if (workspace && (workspace_bytes < kHeaderBytes || !aligned(workspace, 256)))
+        return KDA_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (workspace && cudaMemsetAsync(workspace, 0, sizeof(StatusWord), s) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    if (n == 0) return KDA_OK;
+    return cuda_status(launch_pool_copy(pool, P, slot_elems, src_idx, dst_idx, n,
+                                        (StatusWord *)workspace, sm_count(), s));
+}
+
+kda_status kda_state_pool_compact(float *pool, int32_t P, int64_t slot_elems,
+                                  const uint8_t *live, int32_t *new_index, int32_t *n_live,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    if (!pool_ok(pool, P, slot_elems) || !n_live || !aligned(n_live, 4)) return KDA_ERR_INVALID_ARG;
+    if (P > 0 && (!live || !new_index || !aligned(new_index, 4))) return KDA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kda_state_pool_workspace_size(P) || !aligned(workspace, 256))
+        return KDA_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (P == 0) return cuda_status(cudaMemsetAsync(n_live, 0, sizeof(int32_t), s));
+    return cuda_status(launch_pool_compact(pool, P, slot_elems, live, new_index, n_live,
+                                           (int32_t *)((uint8_t *)workspace + kHeaderBytes),
+                                           sm_count(), s));
+}
+
+}  // extern "C"

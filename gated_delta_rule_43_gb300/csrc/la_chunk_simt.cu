@@ -1,0 +1,374 @@
+// la_chunk_simt.cu -- linear attention with one decay per head, chunked, on the CUDA cores;
+// the plan and the boundary scan of kda_la_chunk_fwd.
+//
+// With G_t = g_1 + ... + g_t inside a chunk that starts from state S:
+//   O  = [(Q K^T) * D] V + exp(G_t) Q S,   D_ts = exp(G_t - G_s) for t >= s, else 0
+//   S' = exp(G_C) S + (K * exp(g_{s+1} + ... + g_C))^T V
+// The state product's weights come from suffix sums, not from differences of prefix sums:
+// a suffix sum keeps its relative precision next to the chunk's end, where the weights
+// matter, however fast the earlier tokens decay.
+#include "kda_la.cuh"
+
+namespace kda {
+namespace la {
+
+// ------------------------------------------------------------------------- plan
+// One CTA: validates cu_seqlens (see plan_chunks_kernel), counts segments and inner
+// boundaries.  Every CTA: final states of sequences without tokens (S_out not NULL).
+constexpr int kPlanThreads = 256;
+__global__ void __launch_bounds__(kPlanThreads)
+la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int64_t seg_tokens,
+               int32_t *__restrict__ seg_off, int32_t *__restrict__ bnd_off,
+               int32_t *__restrict__ multi_off, StatusWord *st, const float *h0, float *S_out, int H, int64_t dkdv4) {
+    if (S_out) {
+        for (int64_t nh = blockIdx.x; nh < (int64_t)N * H; nh += gridDim.x) {
+            const int n = (int)(nh / H);
+            const int64_t b = cu[n], e = cu[n + 1];
+            if (b < e && b >= 0 && e <= T_tot) continue;
+            float4 *dst = reinterpret_cast<float4 *>(S_out) + nh * dkdv4;
+            const float4 *src = h0 ? reinterpret_cast<const float4 *>(h0) + nh * dkdv4 : nullptr;
+            for (int64_t i = threadIdx.x; i < dkdv4; i += blockDim.x)
+                dst[i] = src ? src[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    if (blockIdx.x != 0) return;
+    constexpr int NW = kPlanThreads / 32;
+    __shared__ int3 s_warp[NW];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    if (tid == 0) {
+        st->code = 0u;
+        st->site = 0u;
+        st->info = 0ull;
+    }
+    __syncthreads();
+    if (tid == 0 && (cu[0] != 0 || (int64_t)cu[N] != T_tot)) report(st, KDA_ERR_SEQLENS, N, 1);
+    __syncthreads();
+    int3 carry = make_int3(0, 0, 0);   // segments, inner boundaries, sequences of several
+    auto add = [](int3 &x, const int3 &y) { x.x += y.x; x.y += y.y; x.z += y.z; };
+    for (int base = 0; base < N; base += kPlanThreads) {
+        const int n = base + tid;
+        int segs = 0;
+        if (n < N) {
+            const int64_t b = cu[n], e = cu[n + 1];
+            if (b < 0 || e < b || e > T_tot)
+                report(st, KDA_ERR_SEQLENS, n, 2);
+            else
+                segs = (int)((e - b + seg_tokens - 1) / seg_tokens);
+        }
+        const int3 own = make_int3(segs, max(segs - 1, 0), segs > 1 ? 1 : 0);
+        int3 x = own;   // inclusive warp scan
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int3 y = make_int3(__shfl_up_sync(0xffffffffu, x.x, o),
+                                     __shfl_up_sync(0xffffffffu, x.y, o),
+                                     __shfl_up_sync(0xffffffffu, x.z, o));
+            if (lane >= o) add(x, y);
+        }
+        if (lane == 31) s_warp[wid] = x;
+        __syncthreads();
+        int3 before = carry;
+        for (int w = 0; w < NW; ++w) {
+            if (w < wid) add(before, s_warp[w]);
+            add(carry, s_warp[w]);
+        }
+        if (n < N) {
+            seg_off[n] = before.x + x.x - own.x;
+            bnd_off[n] = before.y + x.y - own.y;
+            multi_off[n] = before.z + x.z - own.z;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        seg_off[N] = carry.x;
+        bnd_off[N] = carry.y;
+        multi_off[N] = carry.z;
+    }
+}
+
+// ------------------------------------------------------------------------- scan
+// bnd[b] holds what segment b's own tokens leave at its end; afterwards it holds the state
+// there: S_b = exp(bnd_log[b]) S_{b-1} + bnd[b] along each sequence, from h0 (or zeros).
+// One thread per four state values; the loads of kAhead boundaries are in flight at a time.
+constexpr int kScanThreads = 256, kAhead = 4;
+__global__ void __launch_bounds__(kScanThreads)
+la_scan_kernel(Plan p, const float *__restrict__ h0, float *__restrict__ bnd,
+               const float *__restrict__ bnd_log, int64_t dkdv4) {
+    const int64_t per_head = dkdv4;
+    const int64_t total = (int64_t)p.N * p.H * per_head;
+    for (int64_t x = (int64_t)blockIdx.x * kScanThreads + threadIdx.x; x < total;
+         x += (int64_t)gridDim.x * kScanThreads) {
+        const int64_t nh = x / per_head, i = x - nh * per_head;
+        const int n = (int)(nh / p.H), h = (int)(nh - (int64_t)n * p.H);
+        const int32_t b0 = p.bnd_off[n], b1 = p.bnd_off[n + 1];
+        if (b0 >= b1) continue;
+        float4 S = h0 ? reinterpret_cast<const float4 *>(h0)[x] : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.in_place)
+            reinterpret_cast<float4 *>(bnd)[((int64_t)(p.bnd_off[p.N] + p.multi_off[n]) * p.H + h) *
+                                                per_head + i] = S;
+        float4 *col = reinterpret_cast<float4 *>(bnd) + ((int64_t)b0 * p.H + h) * per_head + i;
+        const float *lg = bnd_log + (int64_t)b0 * p.H + h;
+        const int64_t step = (int64_t)p.H * per_head;
+        for (int32_t b = 0; b < b1 - b0; b += kAhead) {
+            float4 add[kAhead];
+            float a[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (b + j < b1 - b0) {
+                    add[j] = col[(b + j) * step];
+                    a[j] = lg[(int64_t)(b + j) * p.H];
+                }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (b + j < b1 - b0) {
+                    const float e = expf(a[j]);
+                    S.x = e * S.x + add[j].x;
+                    S.y = e * S.y + add[j].y;
+                    S.z = e * S.z + add[j].z;
+                    S.w = e * S.w + add[j].w;
+                    col[(b + j) * step] = S;
+                }
+        }
+    }
+}
+
+// ----------------------------------------------------------------------- chunks
+constexpr int kThreads = 256;
+constexpr int C = 32;   // chunk: one warp scans its decays
+
+template <int DK, int DVB> struct Smem {
+    static constexpr int LK = DK + 4;   // padded rows: 16-byte reads of 8 rows miss no bank twice
+    float q[C][LK], k[C][LK];
+    float v[C][DVB];
+    float S[DK][DVB];
+    float p[C][C + 1];
+    float G[C], eG[C], w[C];            // prefix sums, their exponentials, weights to the end
+    float total, total_log;             // the chunk's decay and its log
+};
+
+// OUT: outputs and final states of the segments `items` = (slot, head, column block);
+// else the contributions of the segments that end at an inner boundary.
+template <int DK, int DV, int DVB, bool OUT, typename T>
+__global__ void __launch_bounds__(kThreads)
+la_chunk_simt_kernel(Plan p, const T *__restrict__ q, const T *__restrict__ k,
+                     const T *__restrict__ v, int64_t qs, int64_t ks, int64_t vs,
+                     const float *__restrict__ g, int g_per_token, const float *h0,
+                     float *hT, T *__restrict__ o, float *__restrict__ bnd,
+                     float *__restrict__ bnd_log, StatusWord *st) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    using Sm = Smem<DK, DVB>;
+    Sm &sm = *reinterpret_cast<Sm *>(raw);
+    constexpr int NB = DV / DVB;
+    constexpr int TC = DVB / 4;              // threads across the columns, four each
+    constexpr int TR = kThreads / TC;        // thread rows
+    constexpr int SR = DK / TR;              // state rows per thread
+    constexpr int OR = C / TR > 0 ? C / TR : 1;   // output rows per thread
+    static_assert(DK % TR == 0 && SR >= 1 && C % OR == 0, "shape");
+    const int tid = threadIdx.x;
+    const int c4 = (tid % TC) * 4, rg = tid / TC;
+    const int64_t items = (int64_t)(OUT ? p.seg_off[p.N] : p.bnd_off[p.N]) * p.H * NB;
+    const int64_t dkdv = (int64_t)DK * DV;
+
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int blk = (int)(item % NB);
+        const int h = (int)(item / NB % p.H);
+        const int32_t slot = (int32_t)(item / ((int64_t)NB * p.H));
+        const Item it = OUT ? segment(p, slot) : inner_segment(p, slot);
+        const int hk = h / (p.H / p.Hk);
+        const int j0 = blk * DVB;
+        const int64_t nh = ((int64_t)it.n * p.H + h) * dkdv;
+        const float *start = OUT ? start_state(p, it, h, h0, bnd, dkdv) : nullptr;
+        float S[SR][4];
+#pragma unroll
+        for (int r = 0; r < SR; ++r) {
+            const float4 x = start ? *reinterpret_cast<const float4 *>(
+                                         start + (int64_t)(rg * SR + r) * DV + j0 + c4)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[r][0] = x.x; S[r][1] = x.y; S[r][2] = x.z; S[r][3] = x.w;
+        }
+        float log_sum = 0.f;
+        for (int64_t t0 = it.t0; t0 < it.t1; t0 += C) {
+            const int len = (int)min((int64_t)C, it.t1 - t0);
+            // this chunk's tokens; rows past the segment are zeros whatever memory holds there
+            for (int x = tid; x < C * DK; x += kThreads) {
+                const int r = x / DK, c = x % DK;
+                const bool in = r < len;
+                if (OUT) sm.q[r][c] = in ? to_f(q[(t0 + r) * qs + (int64_t)hk * DK + c]) : 0.f;
+                sm.k[r][c] = in ? to_f(k[(t0 + r) * ks + (int64_t)hk * DK + c]) : 0.f;
+            }
+            for (int x = tid; x < C * DVB; x += kThreads) {
+                const int r = x / DVB, c = x % DVB;
+                sm.v[r][c] = r < len ? to_f(v[(t0 + r) * vs + (int64_t)h * DV + j0 + c]) : 0.f;
+            }
+            if (OUT) {
+#pragma unroll
+                for (int r = 0; r < SR; ++r)
+                    *reinterpret_cast<float4 *>(&sm.S[rg * SR + r][c4]) =
+                        make_float4(S[r][0], S[r][1], S[r][2], S[r][3]);
+            }
+            if (tid < 32) {
+                float x = 0.f;
+                if (tid < len) {
+                    x = g_per_token ? g[(t0 + tid) * p.H + h] : g[h];
+                    if (!log_decay_ok(x) && blk == 0)
+                        report(st, KDA_ERR_DECAY_RANGE, g_per_token ? (t0 + tid) * p.H + h : h, 30);
+                }
+                float pre = x < kLogZero ? kLogZero : x;   // (a comparison, so that NaN spreads)
+                float suf = x;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const float a = __shfl_up_sync(0xffffffffu, pre, d);
+                    const float b = __shfl_down_sync(0xffffffffu, suf, d);
+                    if (tid >= d) pre += a;
+                    if (tid + d < 32) suf += b;
+                }
+                const float after = __shfl_down_sync(0xffffffffu, suf, 1);
+                sm.G[tid] = pre;
+                sm.eG[tid] = expf(pre);
+                sm.w[tid] = tid == 31 ? 1.f : expf(after);
+                if (tid == 0) {
+                    sm.total_log = suf;
+                    sm.total = expf(suf);
+                }
+            }
+            __syncthreads();
+            if (OUT) {
+                const int t = tid / 8, s0 = tid % 8;   // row t, columns s0 + 8 j
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int d = 0; d < DK; d += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(&sm.q[t][d]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 b = *reinterpret_cast<const float4 *>(&sm.k[s0 + 8 * j][d]);
+                        acc[j] += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int s = s0 + 8 * j;
+                    sm.p[t][s] = t >= s ? acc[j] * expf(sm.G[t] - sm.G[s]) : 0.f;
+                }
+                __syncthreads();
+                if (rg * OR < C) {
+                    float oi[OR][4] = {}, oa[OR][4] = {};
+                    for (int i = 0; i < DK; ++i) {
+                        const float4 s4 = *reinterpret_cast<const float4 *>(&sm.S[i][c4]);
+#pragma unroll
+                        for (int r = 0; r < OR; ++r) {
+                            const float a = sm.q[rg * OR + r][i];
+                            oi[r][0] += a * s4.x; oi[r][1] += a * s4.y;
+                            oi[r][2] += a * s4.z; oi[r][3] += a * s4.w;
+                        }
+                    }
+                    for (int s = 0; s < C; ++s) {
+                        const float4 v4 = *reinterpret_cast<const float4 *>(&sm.v[s][c4]);
+#pragma unroll
+                        for (int r = 0; r < OR; ++r) {
+                            const float a = sm.p[rg * OR + r][s];
+                            oa[r][0] += a * v4.x; oa[r][1] += a * v4.y;
+                            oa[r][2] += a * v4.z; oa[r][3] += a * v4.w;
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < OR; ++r) {
+                        const int row = rg * OR + r;
+                        if (row < len) {
+                            T *dst = o + ((t0 + row) * p.H + h) * (int64_t)DV + j0 + c4;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                dst[j] = from_f<T>(oa[r][j] + sm.eG[row] * oi[r][j]);
+                        }
+                    }
+                }
+            }
+            float add[SR][4] = {};
+            for (int s = 0; s < C; ++s) {
+                const float4 v4 = *reinterpret_cast<const float4 *>(&sm.v[s][c4]);
+                const float w = sm.w[s];
+#pragma unroll
+                for (int r = 0; r < SR; ++r) {
+                    const float a = sm.k[s][rg * SR + r] * w;
+                    add[r][0] += a * v4.x; add[r][1] += a * v4.y;
+                    add[r][2] += a * v4.z; add[r][3] += a * v4.w;
+                }
+            }
+            const float e = sm.total;
+            log_sum += sm.total_log;
+#pragma unroll
+            for (int r = 0; r < SR; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[r][j] = e * S[r][j] + add[r][j];
+            __syncthreads();
+        }
+        float *dst = OUT ? (it.seg == it.nseg - 1 && hT ? hT + nh : nullptr)
+                         : bnd + (it.bnd * p.H + h) * dkdv;
+        if (dst) {
+#pragma unroll
+            for (int r = 0; r < SR; ++r)
+                *reinterpret_cast<float4 *>(dst + (int64_t)(rg * SR + r) * DV + j0 + c4) =
+                    make_float4(S[r][0], S[r][1], S[r][2], S[r][3]);
+        }
+        if (!OUT && blk == 0 && tid == 0) bnd_log[it.bnd * p.H + h] = log_sum;
+    }
+}
+
+template <int DK, int DV, typename T>
+static cudaError_t launch_dims(bool out, const Plan &p, const void *q, const void *k,
+                               const void *v, int64_t qs, int64_t ks, int64_t vs, const float *g,
+                               int gpt, const float *h0, float *hT, void *o, float *bnd,
+                               float *bnd_log, StatusWord *st, int64_t max_items, cudaStream_t s) {
+    constexpr int DVB = DV < 64 ? DV : 64;
+    constexpr size_t bytes = sizeof(Smem<DK, DVB>);
+    auto *f = out ? la_chunk_simt_kernel<DK, DV, DVB, true, T>
+                  : la_chunk_simt_kernel<DK, DV, DVB, false, T>;
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = max_items * (DV / DVB);
+    f<<<(unsigned)(grid < 4096 ? grid : 4096), kThreads, bytes, s>>>(
+        p, (const T *)q, (const T *)k, (const T *)v, qs, ks, vs, g, gpt, h0, hT, (T *)o, bnd,
+        bnd_log, st);
+    return cudaGetLastError();
+}
+
+}  // namespace la
+
+cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int64_t seg_tokens,
+                           int32_t *seg_off, int32_t *bnd_off, int32_t *multi_off, StatusWord *st,
+                           const float *h0, float *hT, int H, int64_t dkdv, cudaStream_t s) {
+    float *S_out = hT != h0 ? hT : nullptr;   // an in-place update leaves empty ones as they are
+    const int64_t nh = (int64_t)N * H;
+    const int grid = S_out && nh > 1 ? (int)(nh < 256 ? nh : 256) : 1;
+    la::la_plan_kernel<<<grid, la::kPlanThreads, 0, s>>>(cu, N, T_tot, seg_tokens, seg_off, bnd_off,
+                                                        multi_off, st, h0, S_out, H, dkdv / 4);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
+                           int64_t dkdv, int sms, cudaStream_t s) {
+    const int64_t blocks = ((int64_t)p.N * p.H * (dkdv / 4) + la::kScanThreads - 1) / la::kScanThreads;
+    const int64_t most = 8 * (int64_t)sms;
+    la::la_scan_kernel<<<(unsigned)(blocks < most ? blocks : most), la::kScanThreads, 0, s>>>(
+        p, h0, bnd, bnd_log, dkdv / 4);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_la_simt(bool out, int dtype, int dk, int dv, const la::Plan &p, const void *q,
+                           const void *k, const void *v, int64_t qs, int64_t ks, int64_t vs,
+                           const float *g, int gpt, const float *h0, float *hT, void *o,
+                           float *bnd, float *bnd_log, StatusWord *st, int64_t max_items,
+                           cudaStream_t s) {
+#define KDA_LA(DK_, DV_)                                                                       \
+    if (dk == DK_ && dv == DV_)                                                                \
+        return dtype == KDA_BF16                                                               \
+                   ? la::launch_dims<DK_, DV_, __nv_bfloat16>(out, p, q, k, v, qs, ks, vs, g, gpt, \
+                                                              h0, hT, o, bnd, bnd_log, st,     \
+                                                              max_items, s)                    \
+                   : la::launch_dims<DK_, DV_, float>(out, p, q, k, v, qs, ks, vs, g, gpt, h0, hT, \
+                                                      o, bnd, bnd_log, st, max_items, s);
+    KDA_LA(32, 32) KDA_LA(32, 64) KDA_LA(32, 128)
+    KDA_LA(64, 32) KDA_LA(64, 64) KDA_LA(64, 128)
+    KDA_LA(128, 32) KDA_LA(128, 64) KDA_LA(128, 128)
+#undef KDA_LA
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace kda

@@ -7,7 +7,9 @@ calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -20,9 +22,12 @@ KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_DECAY_RANGE = 0, 1, 2,
 KDA_ERR_TIMEOUT, KDA_ERR_CUDA, KDA_ERR_SEQLENS = 4, 5, 6
 KDA_F32, KDA_BF16 = 0, 1
 _DT = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
+_NORM = {"none": 0, "l2": 1, "rms": 2}
+_LAYOUT = {"half": 0, "interleaved": 1}
 
 # name -> (restype, argtypes) of every symbol include/kda.h declares
 P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+F32 = ctypes.c_float
 SIGNATURES = {
     "kda_abi_version": (I32, []),
     "kda_status_string": (ctypes.c_char_p, [I32]),
@@ -44,6 +49,18 @@ SIGNATURES = {
     "kda_gate_cumsum": (I32, [P, P, P, I32, I64, I32, I32, I32, I32, I32, P, P, SZ, P]),
     "kda_query_status": (I32, [P, P, ctypes.POINTER(ctypes.c_int64)]),
     "kda_test_chain_fault": (I32, [I64, I32]),
+    "kda_la_chunk_fwd_workspace_size": (SZ, [I64, I32, I32, I32, I32, I32, I32]),
+    "kda_la_chunk_fwd": (I32, [P, P, P, P, P, I32, I64, I32, I32, I32, I32, I32, I64, I64, I64,
+                               I32, P, P, P, P, SZ, P]),
+    "kda_la_decode_step": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I64, I64, I64,
+                                 I32, P]),
+    "kda_la_decode_step_indexed": (I32, [P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32,
+                                         I64, I64, I64, I32, P, SZ, P]),
+    "kda_qk_norm_rope": (I32, [P, P, P, P, I64, I32, I32, I32, I32, I64, I64, I64, I64, P, P, I32,
+                               F32, F32, F32, P, P, I32, I32, F32, P]),
+    "kda_state_pool_workspace_size": (SZ, [I32]),
+    "kda_state_pool_copy": (I32, [P, I32, I64, P, P, I32, P, SZ, P]),
+    "kda_state_pool_compact": (I32, [P, I32, I64, P, P, P, P, SZ, P]),
 }
 
 _lock = threading.Lock()
@@ -90,6 +107,16 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _allocating(stream):
+    """Buffers that a call allocates belong to the stream that it runs on, so that the caching
+    allocator hands their memory on in that stream's order."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _check_cuda(*ts):
@@ -353,6 +380,285 @@ def gate_cumsum(z, A_log, cu_seqlens, chunk: int = 64, *, softplus: bool = False
     if check:
         query_status(workspace, stream, raise_on_error=True)
     return G, workspace
+
+
+def _rows(name, t, T, heads, D, dtype):
+    """Checks a [T, heads, D] tensor whose tokens may lie further apart than heads * D (a
+    slice of a fused projection); returns the distance in elements.  A single token or none
+    has no distance: the packed one stands for it."""
+    _expect(name, t, (T, heads, D), dtype)
+    s = t.stride()
+    if (s[2] != 1 and D > 1) or (s[1] != D and heads > 1):
+        raise ValueError(f"{name}: heads and channels must be packed (strides {s})")
+    return s[0] if T > 1 else heads * D
+
+
+def _on_gpu(*ts):
+    dev = None
+    for t in ts:
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError("every tensor must live on a CUDA device (no CPU fallback)")
+            if dev is not None and t.device != dev:
+                raise ValueError("tensors must live on one device")
+            dev = t.device
+
+
+def _check_la(q, k, v, g):
+    """q, k [T, Hk, dk], v [T, H, dv] (token strides free), g [T, H] or [H] fp32.
+    Returns (T, H, Hk, dk, dv, token strides, g per token)."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be [T, Hk, dk] and v [T, H, dv]")
+    if q.dtype not in _DT:
+        raise TypeError(f"q has dtype {q.dtype}; fp32 and bf16 are supported")
+    T, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} value heads cannot share {Hk} query/key heads")
+    strides = (_rows("q", q, T, Hk, dk, q.dtype), _rows("k", k, T, Hk, dk, q.dtype),
+               _rows("v", v, T, H, dv, q.dtype))
+    per_token = g.dim() == 2
+    _expect("g", g, (T, H) if per_token else (H,), torch.float32)
+    return T, H, Hk, dk, dv, strides, 1 if per_token else 0
+
+
+def la_chunk_fwd(q, k, v, g, cu_seqlens, initial_state=None, *, output_final_state: bool = True,
+                 o=None, final_state=None, workspace=None, stream=None, check: bool = False):
+    """Chunked prefill of linear attention with one decay per head (kda_la_chunk_fwd).
+
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t over packed sequences: q, k
+    [T, Hk, dk] and v [T, H, dv] (fp32 or bf16, one dtype; tokens may be slices of wider
+    rows), Hk divides H; g the log decays, <= 0, fp32, [T, H] or [H]; cu_seqlens [N+1] int32;
+    initial_state [N, H, dk, dv] fp32 or None.  Returns (o [T, H, dv], final_state fp32 or
+    None).  ``final_state`` may be ``initial_state``.  ``check=True`` synchronises the stream
+    and raises device-found errors.
+    """
+    lib = load()
+    T, H, Hk, dk, dv, (qs, ks, vs), gpt = _check_la(q, k, v, g)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or cu_seqlens.dtype != torch.int32:
+        raise TypeError("cu_seqlens must be a 1-D int32 tensor [N + 1]")
+    N = cu_seqlens.numel() - 1
+    _expect("initial_state", initial_state, (N, H, dk, dv), torch.float32)
+    _expect("final_state", final_state, (N, H, dk, dv), torch.float32)
+    _expect("o", o, (T, H, dv), q.dtype)
+    _on_gpu(q, k, v, g, cu_seqlens, initial_state, o, final_state, workspace)
+    _check_cuda(g, cu_seqlens, initial_state, o, final_state, workspace)
+    dt = _DT[q.dtype]
+    need = int(lib.kda_la_chunk_fwd_workspace_size(T, N, H, Hk, dk, dv, dt))
+    with _allocating(stream):
+        if o is None:
+            o = torch.empty(T, H, dv, dtype=q.dtype, device=q.device)
+        if final_state is None and output_final_state:
+            final_state = torch.empty(N, H, dk, dv, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = alloc_workspace(need, q.device)
+    rc = lib.kda_la_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), N, T, H, Hk,
+                              dk, dv, dt, qs, ks, vs, gpt, _ptr(initial_state),
+                              _ptr(final_state), _ptr(o), _ptr(workspace), _nbytes(workspace),
+                              _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_la_chunk_fwd")
+    if check:
+        query_status(workspace, stream, raise_on_error=True)
+    return o, final_state
+
+
+def la_decode_step(q, k, v, g, state, *, o=None, stream=None):
+    """One token of the decayed linear attention for N sequences (kda_la_decode_step).
+
+    q, k [N, Hk, dk], v [N, H, dv], g [N, H] or [H] fp32; state [N, H, dk, dv] fp32, updated
+    in place.  Returns o [N, H, dv].
+    """
+    lib = load()
+    N, H, Hk, dk, dv, (qs, ks, vs), gpt = _check_la(q, k, v, g)
+    _expect("state", state, (N, H, dk, dv), torch.float32)
+    _expect("o", o, (N, H, dv), q.dtype)
+    _on_gpu(q, k, v, g, state, o)
+    _check_cuda(g, state, o)
+    if o is None:
+        with _allocating(stream):
+            o = torch.empty(N, H, dv, dtype=q.dtype, device=q.device)
+    rc = lib.kda_la_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(o), N, H, Hk,
+                                dk, dv, _DT[q.dtype], qs, ks, vs, gpt, _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_la_decode_step")
+    return o
+
+
+def la_decode_step_indexed(q, k, v, g, state_pool, state_idx, *, o=None, workspace=None,
+                           stream=None, check: bool = False):
+    """la_decode_step where sequence n owns slot state_idx[n] (distinct, int32) of state_pool
+    [P, H, dk, dv].  With a workspace (or check=True) an index outside the pool is recorded
+    in its status word; that sequence is skipped either way and its row of o not written."""
+    lib = load()
+    N, H, Hk, dk, dv, (qs, ks, vs), gpt = _check_la(q, k, v, g)
+    if state_pool.dim() != 4:
+        raise ValueError("state_pool must be [P, H, dk, dv]")
+    _expect("state_pool", state_pool, (state_pool.shape[0], H, dk, dv), torch.float32)
+    _expect("state_idx", state_idx, (N,), torch.int32)
+    _expect("o", o, (N, H, dv), q.dtype)
+    _on_gpu(q, k, v, g, state_pool, state_idx, o, workspace)
+    _check_cuda(g, state_pool, state_idx, o, workspace)
+    with _allocating(stream):
+        if o is None:
+            o = torch.empty(N, H, dv, dtype=q.dtype, device=q.device)
+        if workspace is None and check:
+            workspace = alloc_workspace(int(lib.kda_decode_workspace_size()), q.device)
+    rc = lib.kda_la_decode_step_indexed(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state_pool),
+                                        _ptr(state_idx), state_pool.shape[0], _ptr(o), N, H, Hk,
+                                        dk, dv, _DT[q.dtype], qs, ks, vs, gpt, _ptr(workspace),
+                                        _nbytes(workspace), _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_la_decode_step_indexed")
+    if check:
+        query_status(workspace, stream, raise_on_error=True)
+    return o
+
+
+def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str = "none",
+                  factor: float = 1.0, original_length: int = 8192, fast_turns: float = 32.0,
+                  slow_turns: float = 1.0, device=None):
+    """(inv_freq [rot_dim / 2] fp32, rope_scale) for qk_norm_rope.
+
+    The rates are base^(-2 i / rot_dim).  For contexts ``factor`` times as long as the
+    ``original_length`` a model was trained with, scaling "linear" divides every rate by the
+    factor (positions are interpolated), "base" raises the base so that only the slowest
+    rate is divided by it, and "parts" divides the rates that turn less than ``slow_turns``
+    times over the original length, keeps those that turn more than ``fast_turns`` times,
+    and blends linearly in between; it returns rope_scale = 1 + 0.1 ln(factor), which
+    sharpens the scores of the longer context (1 for the others).
+    """
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be even")
+    if scaling not in ("none", "linear", "base", "parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not factor >= 1.0:
+        raise ValueError("factor must be at least 1")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "base" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    rate = base ** (-2.0 * i / max(rot_dim, 1))
+    scale = 1.0
+    if scaling == "linear":
+        rate = rate / factor
+    elif scaling == "parts":
+        turns = original_length * rate / (2.0 * math.pi)
+        keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0.0, 1.0)
+        rate = rate * (keep + (1.0 - keep) / factor)
+        scale = 1.0 + 0.1 * math.log(factor)
+    return rate.to(torch.float32).to(device or "cpu"), scale
+
+
+def qk_norm_rope(q, k, positions, inv_freq, *, norm: str = "l2", layout: str = "half",
+                 eps: float = 1e-6, q_weight=None, k_weight=None, q_scale: float = 1.0,
+                 k_scale: float = 1.0, rope_scale: float = 1.0, q_out=None, k_out=None,
+                 stream=None):
+    """Per-head norm of queries and keys and their position rotation (kda_qk_norm_rope).
+
+    q [T, Hq, D] and k [T, Hk, D] or None (fp32 or bf16; tokens may be slices of wider rows);
+    positions [T] int32 and inv_freq [rot_dim / 2] fp32 (see rope_inv_freq), or None and None
+    for no rotation; norm "none", "l2" or "rms"; layout "half" or "interleaved"; weights [D]
+    fp32 or None.  q_out and k_out may be q and k (in place); by default new packed tensors
+    are returned.
+    """
+    lib = load()
+    if q.dim() != 3 or q.dtype not in _DT:
+        raise TypeError("q must be [T, Hq, D], fp32 or bf16")
+    if norm not in _NORM or layout not in _LAYOUT:
+        raise ValueError(f"unknown norm {norm!r} or layout {layout!r}")
+    T, Hq, D = q.shape
+    qs, ks, kos, Hk = _rows("q", q, T, Hq, D, q.dtype), 0, 0, 0
+    if k is not None:
+        Hk = k.shape[1] if k.dim() == 3 else 0
+        ks = _rows("k", k, T, Hk, D, q.dtype)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq come together")
+    rot = 0
+    if inv_freq is not None:
+        _expect("positions", positions, (T,), torch.int32)
+        _expect("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32)
+        rot = 2 * inv_freq.numel()
+    _expect("q_weight", q_weight, (D,), torch.float32)
+    _expect("k_weight", k_weight, (D,), torch.float32)
+    _on_gpu(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    _check_cuda(positions, inv_freq, q_weight, k_weight)
+    with _allocating(stream):
+        if q_out is None:
+            q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(T, Hk, D, dtype=q.dtype, device=q.device)
+    qos = _rows("q_out", q_out, T, Hq, D, q.dtype)
+    if k is not None:
+        kos = _rows("k_out", k_out, T, Hk, D, q.dtype)
+    rc = lib.kda_qk_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), T, Hq, Hk, D,
+                              _DT[q.dtype], qs, ks, qos, kos, _ptr(q_weight), _ptr(k_weight),
+                              _NORM[norm], eps, q_scale, k_scale, _ptr(positions),
+                              _ptr(inv_freq), rot, _LAYOUT[layout], rope_scale, _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_qk_norm_rope")
+    return q_out, k_out
+
+
+def _check_pool(pool):
+    if pool.dim() < 2 or pool.dtype != torch.float32:
+        raise TypeError("a state pool is [P, ...] fp32")
+    return pool.shape[0], pool[0].numel() if pool.shape[0] else 4
+
+
+def state_pool_copy(pool, src_idx, dst_idx, *, workspace=None, stream=None, check: bool = False):
+    """Slot dst_idx[i] of the pool [P, ...] fp32 becomes slot src_idx[i], or zeros where
+    src_idx[i] is -1 (kda_state_pool_copy): copies, forks and clears.  No destination may be
+    named twice or be another copy's source; copies that break this or leave the pool are
+    left out, and recorded in the workspace's status word when there is one (check=True
+    raises)."""
+    lib = load()
+    slots, elems = _check_pool(pool)
+    if src_idx.dim() != 1:
+        raise ValueError("src_idx must be [n]")
+    _expect("src_idx", src_idx, (src_idx.numel(),), torch.int32)
+    _expect("dst_idx", dst_idx, (src_idx.numel(),), torch.int32)
+    _on_gpu(pool, src_idx, dst_idx, workspace)
+    _check_cuda(pool, src_idx, dst_idx, workspace)
+    if workspace is None and check:
+        with _allocating(stream):
+            workspace = alloc_workspace(int(lib.kda_decode_workspace_size()), pool.device)
+    rc = lib.kda_state_pool_copy(_ptr(pool), slots, elems, _ptr(src_idx), _ptr(dst_idx),
+                                 src_idx.numel(), _ptr(workspace), _nbytes(workspace),
+                                 _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_state_pool_copy")
+    if check:
+        query_status(workspace, stream, raise_on_error=True)
+
+
+def state_pool_compact(pool, live, *, new_index=None, n_live=None, workspace=None, stream=None):
+    """Packs the live slots of a pool to its front with the fewest moves
+    (kda_state_pool_compact).  live [P] bool or uint8.  Returns (new_index [P] int32: where
+    each live slot is now, -1 for dead ones; n_live [1] int32), both on the device."""
+    lib = load()
+    slots, elems = _check_pool(pool)
+    if live.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"live has dtype {live.dtype}, expected bool or uint8")
+    _expect("live", live, (slots,))
+    _expect("new_index", new_index, (slots,), torch.int32)
+    _expect("n_live", n_live, (1,), torch.int32)
+    _on_gpu(pool, live, new_index, n_live, workspace)
+    _check_cuda(pool, live, new_index, n_live, workspace)
+    with _allocating(stream):
+        if new_index is None:
+            new_index = torch.empty(slots, dtype=torch.int32, device=pool.device)
+        if n_live is None:
+            n_live = torch.empty(1, dtype=torch.int32, device=pool.device)
+        if workspace is None:
+            workspace = alloc_workspace(int(lib.kda_state_pool_workspace_size(slots)), pool.device)
+    rc = lib.kda_state_pool_compact(_ptr(pool), slots, elems, _ptr(live), _ptr(new_index),
+                                    _ptr(n_live), _ptr(workspace), _nbytes(workspace),
+                                    _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_state_pool_compact")
+    return new_index, n_live
 
 
 def query_status(workspace, stream=None, *, raise_on_error: bool = False):

@@ -311,6 +311,136 @@ kda_status kda_gate_cumsum(const void *z, const float *A_log, const int32_t *cu_
                            int32_t dtype, int32_t chunk, int32_t gate_mode, float *g_cumsum,
                            void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with one decay per head.  The layers below carry the same
+ * fixed-size fp32 states as the delta-rule layer above, with a plainer update:
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,      o_t = S_t^T q_t
+ * where g_t <= 0 is the log of the head's decay at token t (0: keep everything,
+ * -inf: forget everything before this token).  H value heads share Hk query/key
+ * heads: value head h reads query/key head h / (H / Hk).
+ *
+ *  - q, k [T, Hk, dk] and v [T, H, dv] may be slices of wider rows (a fused
+ *    projection's output): x_stride is the distance in elements from one token to the
+ *    next, a multiple of 16 bytes and at least heads x D; heads and channels are packed.
+ *    The inputs of a decode step and of kda_qk_norm_rope may repeat one token (stride 0).
+ *  - g is fp32: [T, H] when g_per_token != 0, else [H], one fixed decay per head.
+ *  - o [T, H, dv] is packed.  dtype, head sizes (dk, dv in {32, 64, 128}), alignment,
+ *    streams and errors are those of the file header; Hk must divide H.
+ */
+
+/*
+ * Bytes of workspace kda_la_chunk_fwd needs (0 for arguments it would reject).  The
+ * workspace holds the status word, the plan of the packed sequences and the states at
+ * the inner segment boundaries; it needs no initialisation.
+ */
+size_t kda_la_chunk_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H,
+                                       int32_t Hk, int32_t dk, int32_t dv, int32_t dtype);
+
+/*
+ * Chunked prefill over packed variable-length sequences (arguments as kda_chunk_fwd where
+ * they have the same names).  Every sequence is cut into segments of equal length; a first
+ * pass forms each segment's own contribution to the state (all segments but a sequence's
+ * last), a scan turns these into the segments' start states, and a second pass walks the
+ * segments in parallel.  Inside a segment the tokens go through dense products over
+ * chunks.  The result equals the token-by-token recurrence up to rounding: states are
+ * accumulated and kept in fp32; with bf16 storage the scores and the copy of the state
+ * that meets the queries are rounded to bf16 (the state that is carried on is not).
+ *   initial_state, final_state  [num_seqs, H, dk, dv] fp32 or NULL; may be the same buffer
+ * Device-found errors: KDA_ERR_SEQLENS (the offending sequence is skipped),
+ * KDA_ERR_DECAY_RANGE (a g that is positive or NaN; info = token * H + head, or the head
+ * when g is [H]; that head's outputs are not meaningful), KDA_ERR_TIMEOUT.
+ */
+kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
+                            const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                            int32_t H, int32_t Hk, int32_t dk, int32_t dv, int32_t dtype,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            int32_t g_per_token, const float *initial_state,
+                            float *final_state, void *o, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
+ * One token for each of N sequences against its state [N, H, dk, dv], updated in place.
+ * g is [N, H] (g_per_token != 0) or [H].  Memory-bound: the state is read once and written
+ * once.  g is used as it is (no range check; a NaN spreads as in the definition).
+ */
+kda_status kda_la_decode_step(const void *q, const void *k, const void *v, const float *g,
+                              float *state, void *o, int32_t N, int32_t H, int32_t Hk,
+                              int32_t dk, int32_t dv, int32_t dtype, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int32_t g_per_token,
+                              void *stream);
+
+/*
+ * kda_la_decode_step against slot state_idx[n] of state_pool [P, H, dk, dv] (distinct
+ * indices; see kda_decode_step_indexed).  A sequence whose index lies outside [0, P) is
+ * skipped: its state does not exist and its output row is not written.  workspace: NULL, or
+ * >= kda_decode_workspace_size() bytes whose status word then receives
+ * KDA_ERR_INVALID_ARG (info = the sequence).
+ */
+kda_status kda_la_decode_step_indexed(const void *q, const void *k, const void *v,
+                                      const float *g, float *state_pool,
+                                      const int32_t *state_idx, int32_t P, void *o, int32_t N,
+                                      int32_t H, int32_t Hk, int32_t dk, int32_t dv,
+                                      int32_t dtype, int64_t q_stride, int64_t k_stride,
+                                      int64_t v_stride, int32_t g_per_token, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/*
+ * Queries and keys made ready for the layers above, in one pass: per head
+ *   y = x * rsqrt(sum(x^2) + eps)            norm = KDA_NORM_L2
+ *   y = x * rsqrt(sum(x^2) / D + eps)        norm = KDA_NORM_RMS     (y = x: KDA_NORM_NONE)
+ *   y = y * weight                           where a weight [D] (fp32) is given
+ *   (a, b) = (a cos - b sin, b cos + a sin) * rope_scale, angle = position * inv_freq[i],
+ *            on the first rot_dim channels: pair i is channels (i, i + rot_dim / 2) with
+ *            KDA_ROPE_HALF, (2 i, 2 i + 1) with KDA_ROPE_INTERLEAVED
+ *   out = y * scale                          (q_scale, k_scale)
+ * in fp32, rounded once.  Angles are reduced to one turn in 64-bit integers before cos and
+ * sin, so they are as exact at position 2^31 - 1 as at 0.
+ *   q [T, Hq, D], k [T, Hk, D]   dtype, token strides as above; Hk may be 0 (k, k_out NULL)
+ *   q_out, k_out                 strided too; the same buffer and stride as the input
+ *                                (in place) or memory apart from both inputs
+ *   positions [T]                int32, any sign; inv_freq [rot_dim / 2] fp32, |inv_freq|
+ *                                < 2^30; both may be NULL when rot_dim is 0
+ *   D in {32, 64, 128}; rot_dim a multiple of 16 in 0 ..= D
+ */
+typedef enum kda_norm { KDA_NORM_NONE = 0, KDA_NORM_L2 = 1, KDA_NORM_RMS = 2 } kda_norm;
+typedef enum kda_rope { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 } kda_rope;
+kda_status kda_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                            int64_t total_tokens, int32_t Hq, int32_t Hk, int32_t D,
+                            int32_t dtype, int64_t q_stride, int64_t k_stride,
+                            int64_t q_out_stride, int64_t k_out_stride, const float *q_weight,
+                            const float *k_weight, int32_t norm, float eps, float q_scale,
+                            float k_scale, const int32_t *positions, const float *inv_freq,
+                            int32_t rot_dim, int32_t layout, float rope_scale, void *stream);
+
+/* Bytes of workspace kda_state_pool_compact needs for a pool of P slots. */
+size_t kda_state_pool_workspace_size(int32_t P);
+
+/*
+ * Copies slots of a pool of P slots of slot_elems fp32 each (a multiple of 4):
+ * slot dst_idx[i] becomes slot src_idx[i], or zeros where src_idx[i] is -1, for i < n.  One
+ * source may feed many destinations (forking a sequence).  Copies are independent, in no
+ * order: no destination may be named twice, nor be the source of another copy.  A copy
+ * that breaks this (each of those that share a destination; the one whose destination is
+ * read by another), or whose index lies outside the pool, is left out and recorded as
+ * KDA_ERR_INVALID_ARG (info = i) in the workspace's status word when a workspace (>=
+ * kda_decode_workspace_size() bytes) is given.  src == dst is a copy that does nothing.
+ */
+kda_status kda_state_pool_copy(float *pool, int32_t P, int64_t slot_elems,
+                               const int32_t *src_idx, const int32_t *dst_idx, int32_t n,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Packs the live slots of a pool to its front: with L = the number of slots whose live[i]
+ * is not 0, the j-th dead slot below L takes the state of the j-th live slot at or above L
+ * (the fewest moves; both in ascending order).  new_index[i] is where live slot i now is,
+ * -1 for a dead one; n_live[0] = L.  Slots at and above L keep their old contents.
+ *   live [P] one byte each; new_index [P] int32; n_live [1] int32
+ *   workspace  >= kda_state_pool_workspace_size(P) bytes, 256-byte aligned
+ */
+kda_status kda_state_pool_compact(float *pool, int32_t P, int64_t slot_elems,
+                                  const uint8_t *live, int32_t *new_index, int32_t *n_live,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
 /*
  * Waits for `stream`, then returns the status recorded in `workspace` by the
  * last call that used it (KDA_OK if none).  When `info` is not NULL it
