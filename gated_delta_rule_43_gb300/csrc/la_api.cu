@@ -1,5 +1,6 @@
 // la_api.cu -- C ABI of the decayed linear attention, the query/key preparation and the
 // state pool (declared in include/kda.h): argument checks, workspace layout, dispatch.
+#include <cuda.h>
 #include <stdint.h>
 
 #include <cmath>
@@ -12,11 +13,18 @@ cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int64_t seg_
                            const float *h0, float *hT, int H, int64_t dkdv, cudaStream_t s);
 cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
                            int64_t dkdv, int sms, cudaStream_t s);
-cudaError_t launch_la_simt(bool out, int dtype, int dk, int dv, const la::Plan &p, const void *q,
-                           const void *k, const void *v, int64_t qs, int64_t ks, int64_t vs,
-                           const float *g, int gpt, const float *h0, float *hT, void *o,
+cudaError_t launch_la_simt(bool out, int dk, int dv, const la::Plan &p, const float *q,
+                           const float *k, const float *v, int64_t qs, int64_t ks, int64_t vs,
+                           const float *g, int gpt, const float *h0, float *hT, float *o,
                            float *bnd, float *bnd_log, StatusWord *st, int64_t max_items,
                            cudaStream_t s);
+cudaError_t la_tensor_maps(CUtensorMap (&m)[3], const void *q, const void *k, const void *v,
+                           int64_t T, int H, int Hk, int dk, int dv, int64_t qs, int64_t ks,
+                           int64_t vs);
+cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[3], const float *g,
+                         int gpt, const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
+                         float *bnd_log, StatusWord *st, int64_t max_items, int sms,
+                         cudaStream_t s);
 cudaError_t launch_la_decode(int dtype, int dk, int dv, const void *q, const void *k,
                              const void *v, const float *g, float *state, void *o, int N, int H,
                              int Hk, int64_t qs, int64_t ks, int64_t vs, int gpt,
@@ -163,16 +171,26 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
                                    initial_state, final_state, H, dkdv, s);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (total_tokens == 0) return KDA_OK;
+    CUtensorMap maps[3];
+    if (dtype == KDA_BF16 &&
+        la_tensor_maps(maps, q, k, v, total_tokens, H, Hk, dk, dv, q_stride, k_stride, v_stride) !=
+            cudaSuccess)
+        return KDA_ERR_CUDA;
+    auto pass = [&](bool out) {
+        const int64_t most = (out ? L.max_segs : L.max_bnd) * H;
+        if (dtype == KDA_BF16)
+            return launch_la_tc(out, p, maps, g, g_per_token, initial_state, final_state, o, dk, dv,
+                                bnd, bnd_log, st, most, sms, s);
+        return launch_la_simt(out, dk, dv, p, (const float *)q, (const float *)k, (const float *)v,
+                              q_stride, k_stride, v_stride, g, g_per_token, initial_state,
+                              final_state, (float *)o, bnd, bnd_log, st, most, s);
+    };
     if (total_tokens > L.seg_tokens) {   // else no sequence has an inner boundary
-        e = launch_la_simt(false, dtype, dk, dv, p, q, k, v, q_stride, k_stride, v_stride, g,
-                           g_per_token, nullptr, nullptr, nullptr, bnd, bnd_log, st,
-                           L.max_bnd * H, s);
+        e = pass(false);
         if (e == cudaSuccess) e = launch_la_scan(p, initial_state, bnd, bnd_log, dkdv, sms, s);
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
-    return cuda_status(launch_la_simt(true, dtype, dk, dv, p, q, k, v, q_stride, k_stride, v_stride,
-                                      g, g_per_token, initial_state, final_state, o, bnd, bnd_log,
-                                      st, L.max_segs * H, s));
+    return cuda_status(pass(true));
 }
 
 static kda_status la_decode_impl(const void *q, const void *k, const void *v, const float *g,

@@ -1,5 +1,5 @@
-// la_chunk_simt.cu -- linear attention with one decay per head, chunked, on the CUDA cores;
-// the plan and the boundary scan of kda_la_chunk_fwd.
+// la_chunk_simt.cu -- linear attention with one decay per head, chunked, in fp32 on the CUDA
+// cores; the plan and the boundary scan of kda_la_chunk_fwd.
 //
 // With G_t = g_1 + ... + g_t inside a chunk that starts from state S:
 //   O  = [(Q K^T) * D] V + exp(G_t) Q S,   D_ts = exp(G_t - G_s) for t >= s, else 0
@@ -147,12 +147,12 @@ template <int DK, int DVB> struct Smem {
 
 // OUT: outputs and final states of the segments `items` = (slot, head, column block);
 // else the contributions of the segments that end at an inner boundary.
-template <int DK, int DV, int DVB, bool OUT, typename T>
+template <int DK, int DV, int DVB, bool OUT>
 __global__ void __launch_bounds__(kThreads)
-la_chunk_simt_kernel(Plan p, const T *__restrict__ q, const T *__restrict__ k,
-                     const T *__restrict__ v, int64_t qs, int64_t ks, int64_t vs,
+la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restrict__ k,
+                     const float *__restrict__ v, int64_t qs, int64_t ks, int64_t vs,
                      const float *__restrict__ g, int g_per_token, const float *h0,
-                     float *hT, T *__restrict__ o, float *__restrict__ bnd,
+                     float *hT, float *__restrict__ o, float *__restrict__ bnd,
                      float *__restrict__ bnd_log, StatusWord *st) {
     extern __shared__ __align__(16) uint8_t raw[];
     using Sm = Smem<DK, DVB>;
@@ -192,12 +192,12 @@ la_chunk_simt_kernel(Plan p, const T *__restrict__ q, const T *__restrict__ k,
             for (int x = tid; x < C * DK; x += kThreads) {
                 const int r = x / DK, c = x % DK;
                 const bool in = r < len;
-                if (OUT) sm.q[r][c] = in ? to_f(q[(t0 + r) * qs + (int64_t)hk * DK + c]) : 0.f;
-                sm.k[r][c] = in ? to_f(k[(t0 + r) * ks + (int64_t)hk * DK + c]) : 0.f;
+                if (OUT) sm.q[r][c] = in ? q[(t0 + r) * qs + (int64_t)hk * DK + c] : 0.f;
+                sm.k[r][c] = in ? k[(t0 + r) * ks + (int64_t)hk * DK + c] : 0.f;
             }
             for (int x = tid; x < C * DVB; x += kThreads) {
                 const int r = x / DVB, c = x % DVB;
-                sm.v[r][c] = r < len ? to_f(v[(t0 + r) * vs + (int64_t)h * DV + j0 + c]) : 0.f;
+                sm.v[r][c] = r < len ? v[(t0 + r) * vs + (int64_t)h * DV + j0 + c] : 0.f;
             }
             if (OUT) {
 #pragma unroll
@@ -272,10 +272,10 @@ la_chunk_simt_kernel(Plan p, const T *__restrict__ q, const T *__restrict__ k,
                     for (int r = 0; r < OR; ++r) {
                         const int row = rg * OR + r;
                         if (row < len) {
-                            T *dst = o + ((t0 + row) * p.H + h) * (int64_t)DV + j0 + c4;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                dst[j] = from_f<T>(oa[r][j] + sm.eG[row] * oi[r][j]);
+                            const float e = sm.eG[row];
+                            *reinterpret_cast<float4 *>(o + ((t0 + row) * p.H + h) * (int64_t)DV + j0 + c4) =
+                                make_float4(oa[r][0] + e * oi[r][0], oa[r][1] + e * oi[r][1],
+                                            oa[r][2] + e * oi[r][2], oa[r][3] + e * oi[r][3]);
                         }
                     }
                 }
@@ -311,21 +311,19 @@ la_chunk_simt_kernel(Plan p, const T *__restrict__ q, const T *__restrict__ k,
     }
 }
 
-template <int DK, int DV, typename T>
-static cudaError_t launch_dims(bool out, const Plan &p, const void *q, const void *k,
-                               const void *v, int64_t qs, int64_t ks, int64_t vs, const float *g,
-                               int gpt, const float *h0, float *hT, void *o, float *bnd,
+template <int DK, int DV>
+static cudaError_t launch_dims(bool out, const Plan &p, const float *q, const float *k,
+                               const float *v, int64_t qs, int64_t ks, int64_t vs, const float *g,
+                               int gpt, const float *h0, float *hT, float *o, float *bnd,
                                float *bnd_log, StatusWord *st, int64_t max_items, cudaStream_t s) {
     constexpr int DVB = DV < 64 ? DV : 64;
     constexpr size_t bytes = sizeof(Smem<DK, DVB>);
-    auto *f = out ? la_chunk_simt_kernel<DK, DV, DVB, true, T>
-                  : la_chunk_simt_kernel<DK, DV, DVB, false, T>;
+    auto *f = out ? la_chunk_simt_kernel<DK, DV, DVB, true> : la_chunk_simt_kernel<DK, DV, DVB, false>;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     const int64_t grid = max_items * (DV / DVB);
-    f<<<(unsigned)(grid < 4096 ? grid : 4096), kThreads, bytes, s>>>(
-        p, (const T *)q, (const T *)k, (const T *)v, qs, ks, vs, g, gpt, h0, hT, (T *)o, bnd,
-        bnd_log, st);
+    f<<<(unsigned)(grid < 4096 ? grid : 4096), kThreads, bytes, s>>>(p, q, k, v, qs, ks, vs, g, gpt,
+                                                                     h0, hT, o, bnd, bnd_log, st);
     return cudaGetLastError();
 }
 
@@ -351,19 +349,15 @@ cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const
     return cudaGetLastError();
 }
 
-cudaError_t launch_la_simt(bool out, int dtype, int dk, int dv, const la::Plan &p, const void *q,
-                           const void *k, const void *v, int64_t qs, int64_t ks, int64_t vs,
-                           const float *g, int gpt, const float *h0, float *hT, void *o,
+cudaError_t launch_la_simt(bool out, int dk, int dv, const la::Plan &p, const float *q,
+                           const float *k, const float *v, int64_t qs, int64_t ks, int64_t vs,
+                           const float *g, int gpt, const float *h0, float *hT, float *o,
                            float *bnd, float *bnd_log, StatusWord *st, int64_t max_items,
                            cudaStream_t s) {
 #define KDA_LA(DK_, DV_)                                                                       \
     if (dk == DK_ && dv == DV_)                                                                \
-        return dtype == KDA_BF16                                                               \
-                   ? la::launch_dims<DK_, DV_, __nv_bfloat16>(out, p, q, k, v, qs, ks, vs, g, gpt, \
-                                                              h0, hT, o, bnd, bnd_log, st,     \
-                                                              max_items, s)                    \
-                   : la::launch_dims<DK_, DV_, float>(out, p, q, k, v, qs, ks, vs, g, gpt, h0, hT, \
-                                                      o, bnd, bnd_log, st, max_items, s);
+        return la::launch_dims<DK_, DV_>(out, p, q, k, v, qs, ks, vs, g, gpt, h0, hT, o, bnd,  \
+                                         bnd_log, st, max_items, s);
     KDA_LA(32, 32) KDA_LA(32, 64) KDA_LA(32, 128)
     KDA_LA(64, 32) KDA_LA(64, 64) KDA_LA(64, 128)
     KDA_LA(128, 32) KDA_LA(128, 64) KDA_LA(128, 128)
