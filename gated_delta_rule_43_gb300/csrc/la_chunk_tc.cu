@@ -48,7 +48,7 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 
 // What one chunk's decays give, for one stage.
 struct Gates {
-    float G[C];        // prefix sums
+    float G[C];        // prefix sums times log2(e)
     float w[C];        // exp(g_{s+1} + ... + g_C)
     float cf[96];      // exp(R - G_s); the last block needs none
 };
@@ -109,6 +109,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float2 unpack2(uint32_t u) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
 }
+
+// 2^x by the special-function unit (relative error near 2^-22)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Waits that end: after kWaitNs, or when another role of the CTA has given up.
 struct Waits {
@@ -202,8 +210,9 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 tc_fence_after();
                 const Gates &G = gates[b];
                 const float Gt = G.G[t];
-                const float eG = expf(Gt);
-#pragma unroll
+                const float eG = ex2(Gt);
+                // (loops that stay loops: the roles' code shares one instruction cache)
+#pragma unroll 1
                 for (int cb = 0; cb < 4; ++cb) {
                     uint32_t pk[16];
                     if (cb <= warp) {
@@ -211,19 +220,21 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         tmem_ld32(tA + lanes + 32 * cb, a);
                         tmem_ld_wait();
                         if (cb < warp) {
-                            const float rf = expf(Gt - G.G[32 * cb + 31]);
+                            const float rf = ex2(Gt - G.G[32 * cb + 31]);
 #pragma unroll
                             for (int j = 0; j < 32; j += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(&G.cf[(32 * cb + j) % 96]);
+                                const float4 f = *reinterpret_cast<const float4 *>(&G.cf[32 * cb + j]);
                                 pk[j / 2] = pack2(a[j] * (rf * f.x), a[j + 1] * (rf * f.y));
                                 pk[j / 2 + 1] = pack2(a[j + 2] * (rf * f.z), a[j + 3] * (rf * f.w));
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                const float2 f = *reinterpret_cast<const float2 *>(&G.G[32 * cb + j]);
-                                pk[j / 2] = pack2(j <= lane ? a[j] * expf(Gt - f.x) : 0.f,
-                                                  j + 1 <= lane ? a[j + 1] * expf(Gt - f.y) : 0.f);
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(&G.G[32 * cb + j]);
+                                pk[j / 2] = pack2(j <= lane ? a[j] * ex2(Gt - f.x) : 0.f,
+                                                  j + 1 <= lane ? a[j + 1] * ex2(Gt - f.y) : 0.f);
+                                pk[j / 2 + 1] = pack2(j + 2 <= lane ? a[j + 2] * ex2(Gt - f.z) : 0.f,
+                                                      j + 3 <= lane ? a[j + 3] * ex2(Gt - f.w) : 0.f);
                             }
                         }
                     } else {
@@ -245,7 +256,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 tc_fence_after();
                 const bool here = t0 + t < it.t1;
                 __nv_bfloat16 *dst = o + ((t0 + t) * p.H + h) * (int64_t)dv;
-#pragma unroll
+#pragma unroll 1
                 for (int cb = 0; cb < DVP / 32; ++cb) {
                     float x[32], y[32];
                     tmem_ld32(tQS + lanes + 32 * cb, x);
@@ -314,7 +325,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const float w = gates[b].w[r];
                 const float decay = tot[b];
                 constexpr int UK = DKP / 16, UV = DVP / 16;   // 16-byte pieces of a thread
-#pragma unroll
+#pragma unroll 2
                 for (int u = 0; u < UK; ++u) {
                     const uint32_t off = sw128_offset(r, 8 * (half * UK + u), C);
                     uint4 *kp = reinterpret_cast<uint4 *>(stage + M::kK + off);
@@ -336,7 +347,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     *reinterpret_cast<uint4 *>(stage + M::kQ + off) = y;
                 }
                 if (r >= len) {   // rows of other sequences must not meet the zeros of P and K~
-#pragma unroll
+#pragma unroll 1
                     for (int u = 0; u < UV; ++u)
                         *reinterpret_cast<uint4 *>(stage + M::kV +
                                                    sw128_offset(r, 8 * (half * UV + u), C)) =
@@ -498,7 +509,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
 #pragma unroll
                 for (int m = 2; m >= 0; --m) suf[m] = suf[m + 1] + x[m + 1];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) pre[m] += before;
+                for (int m = 0; m < 4; ++m) pre[m] = (pre[m] + before) * kLog2e;
                 const float R = __shfl_sync(0xffffffffu, pre[3], lane | 7);   // end of the block
                 const float total = __shfl_sync(0xffffffffu, down, 0);
                 log_sum += total;
@@ -512,7 +523,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     const int s = 4 * lane + m;
                     G.G[s] = pre[m];
                     G.w[s] = expf(suf[m]);
-                    if (s < 96) G.cf[s] = expf(R - pre[m]);
+                    if (s < 96) G.cf[s] = ex2(R - pre[m]);
                 }
                 if (lane == 0) tot[b] = expf(total);
                 __syncwarp();
