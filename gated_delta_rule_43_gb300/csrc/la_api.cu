@@ -18,10 +18,10 @@ cudaError_t launch_la_simt(bool out, int dk, int dv, const la::Plan &p, const fl
                            const float *g, int gpt, const float *h0, float *hT, float *o,
                            float *bnd, float *bnd_log, StatusWord *st, int64_t max_items,
                            cudaStream_t s);
-cudaError_t la_tensor_maps(CUtensorMap (&m)[3], const void *q, const void *k, const void *v,
-                           int64_t T, int H, int Hk, int dk, int dv, int64_t qs, int64_t ks,
+cudaError_t la_tensor_maps(CUtensorMap (&m)[4], const void *q, const void *k, const void *v,
+                           const void *o, int64_t T, int H, int Hk, int dk, int dv, int64_t qs, int64_t ks,
                            int64_t vs);
-cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[3], const float *g,
+cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[4], const float *g,
                          int gpt, const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
                          float *bnd_log, StatusWord *st, int64_t max_items, int sms,
                          cudaStream_t s);
@@ -171,10 +171,10 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
                                    initial_state, final_state, H, dkdv, s);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (total_tokens == 0) return KDA_OK;
-    CUtensorMap maps[3];
+    CUtensorMap maps[4];
     if (dtype == KDA_BF16 &&
-        la_tensor_maps(maps, q, k, v, total_tokens, H, Hk, dk, dv, q_stride, k_stride, v_stride) !=
-            cudaSuccess)
+        la_tensor_maps(maps, q, k, v, o, total_tokens, H, Hk, dk, dv, q_stride, k_stride,
+                       v_stride) != cudaSuccess)
         return KDA_ERR_CUDA;
     auto pass = [&](bool out) {
         const int64_t most = (out ? L.max_segs : L.max_bnd) * H;

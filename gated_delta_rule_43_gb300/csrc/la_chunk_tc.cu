@@ -21,7 +21,9 @@
 //
 // One CTA an SM walks segments (see kda_la.cuh), every role for itself through the same
 // list of (segment, head, chunk):
-//   warps 0-3    rows of P (tensor memory, as the A operand of P V), rows of O
+//   warps 0-3    rows of P (tensor memory, as the A operand of P V), rows of O (through
+//                shared memory, over the image of S, in one bulk store: rows stored straight
+//                from registers cost 2k cycles a chunk and held up everyone's shared memory)
 //   warps 4-11   K~ (over K and Q, whose products are done by then), and the state: thread
 //                (row, half) holds its columns of S
 //   warp 12      issues the products          warp 13   loads q, k, v (two stages)
@@ -53,17 +55,6 @@ struct Gates {
     float cf[96];      // exp(R - G_s); the last block needs none
 };
 
-template <int DKP, int DVP> struct Map {
-    static constexpr uint32_t kQ = 0, kK = DKP * 256, kV = 2 * DKP * 256;   // within a stage
-    static constexpr uint32_t kStage = kV + DVP * 256;
-    static constexpr uint32_t kS = 2 * kStage;                 // S image, [DKP rows][DVP]
-    static constexpr uint32_t kGates = kS + DKP * DVP * 2;
-    static constexpr uint32_t kTot = kGates + 2 * sizeof(Gates);   // decay of the chunk, [2]
-    static constexpr uint32_t kBar = kTot + 8;
-    static constexpr uint32_t kBytes = kBar + 18 * 8 + 8;
-    static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kStage % 1024 == 0 && kBytes <= 232448, "layout");
-};
-
 enum Bar {
     kFull = 0,      // [2] a stage's tiles have landed
     kGate = 2,      // [2] a stage's decays are there
@@ -76,7 +67,20 @@ enum Bar {
     kKtReady = 13,  // K~ is in shared memory
     kSReady = 14,   // the image of S is
     kOFree = 15,    // the accumulators of O have been read
-    kDrain = 16
+    kSFree = 16,    // the outputs that lay over the image of S have left
+    kDrain = 17,
+    kBars = 18
+};
+
+template <int DKP, int DVP> struct Map {
+    static constexpr uint32_t kQ = 0, kK = DKP * 256, kV = 2 * DKP * 256;   // within a stage
+    static constexpr uint32_t kStage = kV + DVP * 256;
+    static constexpr uint32_t kS = 2 * kStage;                 // S image, [DKP rows][DVP]
+    static constexpr uint32_t kGates = kS + C * DVP * 2;       // ... or a chunk's outputs, [C][DVP]
+    static constexpr uint32_t kTot = kGates + 2 * sizeof(Gates);   // decay of the chunk, [2]
+    static constexpr uint32_t kBar = kTot + 8;
+    static constexpr uint32_t kBytes = kBar + kBars * 8 + 8;
+    static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kStage % 1024 == 0 && kBytes <= 232448, "layout");
 };
 
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
@@ -102,6 +106,14 @@ __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// shared -> global through a tensor map (full boxes; what lies outside the tensor is dropped)
+__device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, int32_t c0,
+                                             int32_t c1, int32_t c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&x);
@@ -117,6 +129,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+
+// The parts of w x: x two bf16, hi the product rounded to bf16, lo the rounded rest.
+__device__ __forceinline__ void split2(uint32_t x, float w, uint32_t &hi, uint32_t &lo) {
+    const float a0 = w * __uint_as_float(x << 16), a1 = w * __uint_as_float(x & 0xffff0000u);
+    hi = pack2(a0, a1);
+    lo = pack2(a0 - __uint_as_float(hi << 16), a1 - __uint_as_float(hi & 0xffff0000u));
+}
 
 // Waits that end: after kWaitNs, or when another role of the CTA has given up.
 struct Waits {
@@ -138,6 +157,7 @@ template <int DKP, int DVP, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                   const __grid_constant__ CUtensorMap to,
                    const float *__restrict__ g, int g_per_token, const float *h0, float *hT,
                    __nv_bfloat16 *__restrict__ o, int dk, int dv, float *__restrict__ bnd,
                    float *__restrict__ bnd_log, StatusWord *st) {
@@ -147,8 +167,8 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     const int64_t items = (int64_t)(OUT ? p.seg_off[p.N] : p.bnd_off[p.N]) * p.H;
     if (blockIdx.x >= items) return;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + M::kBar);
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + M::kBar + 18 * 8);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + M::kBar + 18 * 8 + 4);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + M::kBar + kBars * 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + M::kBar + kBars * 8 + 4);
     Gates *gates = reinterpret_cast<Gates *>(sm + M::kGates);
     float *tot = reinterpret_cast<float *>(sm + M::kTot);
     const uint32_t base = smem_u32(sm);
@@ -170,6 +190,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         mbar_init(&bar[kKtReady], kStateWarps);
         mbar_init(&bar[kSReady], kStateWarps);
         mbar_init(&bar[kOFree], kRowWarps);
+        mbar_init(&bar[kSFree], 1);
         mbar_init(&bar[kDrain], 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -205,81 +226,100 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             for (int c = 0; c < chunks; ++c, ++gi) {
                 const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
                 const int64_t t0 = it.t0 + (int64_t)c * C;
-                ok = wait(kGate + b, ph) && wait(kQkDone, gi & 1);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                tc_fence_after();
-                const Gates &G = gates[b];
-                const float Gt = G.G[t];
-                const float eG = ex2(Gt);
-                // (loops that stay loops: the roles' code shares one instruction cache)
+                ok = __all_sync(0xffffffffu, wait(kGate + b, ph) && wait(kQkDone, gi & 1));
+                float eG = 0.f;
+                if (ok) {
+                    tc_fence_after();
+                    const Gates &G = gates[b];
+                    const float Gt = G.G[t];
+                    eG = ex2(Gt);
+                    // (loops that stay loops: the roles' code shares one instruction cache)
 #pragma unroll 1
-                for (int cb = 0; cb < 4; ++cb) {
-                    uint32_t pk[16];
-                    if (cb <= warp) {
-                        float a[32];
-                        tmem_ld32(tA + lanes + 32 * cb, a);
-                        tmem_ld_wait();
-                        if (cb < warp) {
-                            const float rf = ex2(Gt - G.G[32 * cb + 31]);
+                    for (int cb = 0; cb < 4; ++cb) {
+                        uint32_t pk[16];
+                        if (cb <= warp) {
+                            float a[32];
+                            tmem_ld32(tA + lanes + 32 * cb, a);
+                            tmem_ld_wait();
+                            if (cb < warp) {
+                                const float rf = ex2(Gt - G.G[32 * cb + 31]);
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(&G.cf[32 * cb + j]);
-                                pk[j / 2] = pack2(a[j] * (rf * f.x), a[j + 1] * (rf * f.y));
-                                pk[j / 2 + 1] = pack2(a[j + 2] * (rf * f.z), a[j + 3] * (rf * f.w));
+                                for (int j = 0; j < 32; j += 4) {
+                                    const float4 f = *reinterpret_cast<const float4 *>(&G.cf[32 * cb + j]);
+                                    pk[j / 2] = pack2(a[j] * (rf * f.x), a[j + 1] * (rf * f.y));
+                                    pk[j / 2 + 1] = pack2(a[j + 2] * (rf * f.z), a[j + 3] * (rf * f.w));
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 32; j += 4) {
+                                    const float4 f = *reinterpret_cast<const float4 *>(&G.G[32 * cb + j]);
+                                    pk[j / 2] = pack2(j <= lane ? a[j] * ex2(Gt - f.x) : 0.f,
+                                                      j + 1 <= lane ? a[j + 1] * ex2(Gt - f.y) : 0.f);
+                                    pk[j / 2 + 1] = pack2(j + 2 <= lane ? a[j + 2] * ex2(Gt - f.z) : 0.f,
+                                                          j + 3 <= lane ? a[j + 3] * ex2(Gt - f.w) : 0.f);
+                                }
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(&G.G[32 * cb + j]);
-                                pk[j / 2] = pack2(j <= lane ? a[j] * ex2(Gt - f.x) : 0.f,
-                                                  j + 1 <= lane ? a[j + 1] * ex2(Gt - f.y) : 0.f);
-                                pk[j / 2 + 1] = pack2(j + 2 <= lane ? a[j + 2] * ex2(Gt - f.z) : 0.f,
-                                                      j + 3 <= lane ? a[j + 3] * ex2(Gt - f.w) : 0.f);
-                            }
+                            for (int j = 0; j < 16; ++j) pk[j] = 0;
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) pk[j] = 0;
+                        // (columns of scores that this warp has read)
+                        tmem_st16(tA + lanes + 16 * cb, pk);
                     }
-                    // (columns of scores that this warp has read)
-                    tmem_st16(tA + lanes + 16 * cb, pk);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bar[kPReady]);
+                        mbar_arrive(&bar[kGateFree + b]);
+                    }
+                    ok = __all_sync(0xffffffffu, wait(kPvDone + b, ph));
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bar[kPReady]);
-                    mbar_arrive(&bar[kGateFree + b]);
-                }
-                ok = wait(kPvDone + b, ph);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                // these warps stop together: the barriers below have no time limit
+                ok = bar_and(2, 32 * kRowWarps, ok);
+                if (!ok) break;
                 tc_fence_after();
-                const bool here = t0 + t < it.t1;
-                __nv_bfloat16 *dst = o + ((t0 + t) * p.H + h) * (int64_t)dv;
+                // the outputs over the image of S, which Q S was the last to read
 #pragma unroll 1
                 for (int cb = 0; cb < DVP / 32; ++cb) {
                     float x[32], y[32];
                     tmem_ld32(tQS + lanes + 32 * cb, x);
                     tmem_ld32(tPV + lanes + 32 * cb, y);
                     tmem_ld_wait();
-                    if (cb == DVP / 32 - 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar[kOFree]);
-                    }
-                    if (here && 32 * cb < dv) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint4 u;
-                            u.x = pack2(eG * x[j] + y[j], eG * x[j + 1] + y[j + 1]);
-                            u.y = pack2(eG * x[j + 2] + y[j + 2], eG * x[j + 3] + y[j + 3]);
-                            u.z = pack2(eG * x[j + 4] + y[j + 4], eG * x[j + 5] + y[j + 5]);
-                            u.w = pack2(eG * x[j + 6] + y[j + 6], eG * x[j + 7] + y[j + 7]);
-                            *reinterpret_cast<uint4 *>(dst + 32 * cb + j) = u;
-                        }
+                    for (int j = 0; j < 32; j += 8) {
+                        uint4 u;
+                        u.x = pack2(eG * x[j] + y[j], eG * x[j + 1] + y[j + 1]);
+                        u.y = pack2(eG * x[j + 2] + y[j + 2], eG * x[j + 3] + y[j + 3]);
+                        u.z = pack2(eG * x[j + 4] + y[j + 4], eG * x[j + 5] + y[j + 5]);
+                        u.w = pack2(eG * x[j + 6] + y[j + 6], eG * x[j + 7] + y[j + 7]);
+                        *reinterpret_cast<uint4 *>(sm + M::kS + sw128_offset(t, 32 * cb + j, C)) = u;
                     }
-                    __syncwarp();
                 }
+                tc_fence_before();
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kOFree]);
+                named_bar_sync(1, 32 * kRowWarps);
+                const int len = (int)min((int64_t)C, it.t1 - t0);
+                if (len == C) {
+                    if (tid == 0) {
+#pragma unroll
+                        for (int x = 0; x < DVP / 64; ++x)
+                            tma_store_3d(&to, sm + M::kS + x * 16384, 64 * x, h, (int32_t)t0);
+                        bulk_commit();
+                        bulk_wait_read_all();
+                    }
+                } else {   // rows past the segment belong to others
+                    const int per = dv / 8;
+                    for (int x = tid; x < len * per; x += 32 * kRowWarps) {
+                        const int r = x / per, j = 8 * (x - r * per);
+                        *reinterpret_cast<uint4 *>(o + ((t0 + r) * p.H + h) * (int64_t)dv + j) =
+                            *reinterpret_cast<const uint4 *>(sm + M::kS + sw128_offset(r, j, C));
+                    }
+                    named_bar_sync(1, 32 * kRowWarps);
+                }
+                if (tid == 0) mbar_arrive(&bar[kSFree]);
             }
         } else if (warp < kRowWarps + kStateWarps) {
             constexpr int NC = DVP / 2;
@@ -298,7 +338,10 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                                                : make_float4(0.f, 0.f, 0.f, 0.f);
                 S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
             }
-            auto put_image = [&] {
+            // the image of S for chunk number `gn`, once the outputs of the one before have left
+            auto put_image = [&](uint32_t gn) {
+                const bool free = gn == 0 || wait(kSFree, (gn - 1) & 1);
+                if (!__all_sync(0xffffffffu, free)) return false;
                 if (i < DKP) {
 #pragma unroll
                     for (int j = 0; j < NC; j += 8) {
@@ -313,9 +356,10 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kSReady]);
+                return true;
             };
-            if (OUT) put_image();
-            for (int c = 0; c < chunks; ++c, ++gi) {
+            if (OUT) ok = put_image(gi);
+            for (int c = 0; c < chunks && ok; ++c, ++gi) {
                 const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
                 const int len = (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)c * C);
                 uint8_t *stage = sm + b * M::kStage;
@@ -325,26 +369,26 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const float w = gates[b].w[r];
                 const float decay = tot[b];
                 constexpr int UK = DKP / 16, UV = DVP / 16;   // 16-byte pieces of a thread
-#pragma unroll 2
-                for (int u = 0; u < UK; ++u) {
-                    const uint32_t off = sw128_offset(r, 8 * (half * UK + u), C);
-                    uint4 *kp = reinterpret_cast<uint4 *>(stage + M::kK + off);
-                    uint4 x = *kp, y = make_uint4(0, 0, 0, 0);
-                    if (r < len) {
-                        uint32_t *xs = &x.x, *ys = &y.x;
+#pragma unroll 1
+                for (int u = 0; u < UK; u += 4) {   // four in flight
+                    uint4 x[4];
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const float2 f = unpack2(xs[m]);
-                            const float a0 = w * f.x, a1 = w * f.y;
-                            xs[m] = pack2(a0, a1);
-                            const float2 hi = unpack2(xs[m]);
-                            ys[m] = pack2(a0 - hi.x, a1 - hi.y);
+                    for (int m = 0; m < 4; ++m)
+                        x[m] = *reinterpret_cast<const uint4 *>(
+                            stage + M::kK + sw128_offset(r, 8 * (half * UK + u + m), C));
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+                        if (r < len) {
+                            split2(x[m].x, w, hi.x, lo.x);
+                            split2(x[m].y, w, hi.y, lo.y);
+                            split2(x[m].z, w, hi.z, lo.z);
+                            split2(x[m].w, w, hi.w, lo.w);
                         }
-                    } else {
-                        x = y;
+                        const uint32_t off = sw128_offset(r, 8 * (half * UK + u + m), C);
+                        *reinterpret_cast<uint4 *>(stage + M::kK + off) = hi;
+                        *reinterpret_cast<uint4 *>(stage + M::kQ + off) = lo;
                     }
-                    *kp = x;
-                    *reinterpret_cast<uint4 *>(stage + M::kQ + off) = y;
                 }
                 if (r >= len) {   // rows of other sequences must not meet the zeros of P and K~
 #pragma unroll 1
@@ -371,7 +415,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     for (int j = 0; j < 32; ++j) S[jb + j] = decay * S[jb + j] + x[j];
                 }
                 tc_fence_before();
-                if (OUT && c + 1 < chunks) put_image();
+                if (OUT && c + 1 < chunks) ok = put_image(gi + 1);
             }
             float *dst = OUT ? (it.seg == it.nseg - 1 && hT ? hT + ((int64_t)it.n * p.H + h) * dkdv
                                                             : nullptr)
@@ -608,7 +652,7 @@ template <int DKP, int DVP, bool OUT> static cudaError_t allow_smem(int dev) {
 }
 
 template <int DKP, int DVP, bool OUT>
-static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[3], const float *g, int gpt,
+static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[4], const float *g, int gpt,
                           const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
                           float *bnd_log, StatusWord *st, int64_t max_items, int sms,
                           cudaStream_t s) {
@@ -618,23 +662,24 @@ static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[3], const float 
     if (e != cudaSuccess) return e;
     la_chunk_tc_kernel<DKP, DVP, OUT>
         <<<(unsigned)(max_items < sms ? max_items : sms), kThreads, Map<DKP, DVP>::kBytes, s>>>(
-            p, m[0], m[1], m[2], g, gpt, h0, hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
+            p, m[0], m[1], m[2], m[3], g, gpt, h0, hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
     return cudaGetLastError();
 }
 
 }  // namespace tc
 }  // namespace la
 
-cudaError_t la_tensor_maps(CUtensorMap (&m)[3], const void *q, const void *k, const void *v,
-                           int64_t T, int H, int Hk, int dk, int dv, int64_t qs, int64_t ks,
+cudaError_t la_tensor_maps(CUtensorMap (&m)[4], const void *q, const void *k, const void *v,
+                           const void *o, int64_t T, int H, int Hk, int dk, int dv, int64_t qs, int64_t ks,
                            int64_t vs) {
     cudaError_t e = la::tc::tensor_map(&m[0], q, T, Hk, dk, qs);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[1], k, T, Hk, dk, ks);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[2], v, T, H, dv, vs);
+    if (e == cudaSuccess) e = la::tc::tensor_map(&m[3], o, T, H, dv, (int64_t)H * dv);
     return e;
 }
 
-cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[3], const float *g,
+cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[4], const float *g,
                          int gpt, const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
                          float *bnd_log, StatusWord *st, int64_t max_items, int sms,
                          cudaStream_t s) {
