@@ -1,13 +1,16 @@
-// kda_la.cuh -- what the translation units of the decayed linear attention share: the plan
-// of the packed sequences, the work items of a launch, and the gate's values in a chunk.
+// kda_la.cuh -- how a prefill of the decayed linear attention is cut over the GPU.
 //
-// Every sequence is cut into segments of seg_tokens tokens.  seg_off[n] counts the segments
-// of the sequences before n, bnd_off[n] the inner boundaries (a sequence of s segments has
-// s - 1); boundary bnd_off[n] + j lies between the segments j and j + 1 of sequence n.
-// When the final states overwrite the initial ones, the last segment of a sequence may write
-// before the first one has read: then the scan keeps a copy of the initial state of every
-// sequence of several segments behind the boundaries' states, at index
-// bnd_off[N] + multi_off[n] (multi_off counts such sequences before n).
+// A unit is one head of one sequence, a run of 128-token chunks; the units of all sequences,
+// heads inside sequences, stand in one row of `total` chunks.  The row is cut into `ranges`
+// equal parts, one for each CTA (CTA group on the CUDA cores), wherever that falls: every SM
+// has the same work whatever the lengths are.  A cut inside a unit is an inner boundary: a
+// first pass forms the state that the tokens before it, back to the unit's start or the cut
+// before, leave there; a scan along the cuts of each unit turns these into the states at the
+// cuts; and the output pass starts its ranges from them.
+// A cut moves out of a unit of at most kWhole chunks to its nearer end: for so few chunks the
+// extra pass costs more than the evener load gives.  When there are more SMs than work, every
+// unit has a range of its own, and one of at least 2 kMinRange chunks several, of kMinRange or
+// more.
 #pragma once
 
 #include "kda_common.cuh"
@@ -15,67 +18,93 @@
 namespace kda {
 namespace la {
 
+constexpr int kChunk = 128;
+constexpr int kMinRange = 8;
+constexpr int kWhole = 8;
+
+// A place in the row of chunks: before chunk c of head h of sequence n.
+struct Cut {
+    int64_t x;
+    int32_t n, h, c, inner;   // inner: inside a unit (c > 0)
+};
+
 struct Plan {
     const int32_t *cu;        // [N + 1]
-    const int32_t *seg_off;   // [N + 1]
-    const int32_t *bnd_off;   // [N + 1]
-    const int32_t *multi_off; // [N + 1]
-    int N;
-    int H, Hk;
-    int64_t seg_tokens;
+    const int32_t *off;       // [N + 1]: chunks of the sequences before n
+    const Cut *cuts;          // [ranges + 1], the last at the row's end
+    int N, H, Hk;
+    int ranges;
     int in_place;             // the final states overwrite the initial ones
 };
 
+// The chunks [c0, c1) of one unit.
 struct Item {
-    int n, seg, nseg;
+    int n, h;
+    int c0, c1, nc;           // of nc
     int64_t t0, t1;           // tokens [t0, t1) of the packed tensors
-    int64_t bnd;              // boundary that ends this segment (the one before starts it)
 };
 
-// The largest n with off[n] <= x (off is non-decreasing, off[0] = 0, x < off[N]).
-__device__ __forceinline__ int find_owner(const int32_t *off, int N, int32_t x) {
-    int lo = 0, hi = N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (off[mid] <= x) lo = mid; else hi = mid - 1;
+__device__ __forceinline__ void set_tokens(const Plan &p, Item &it) {
+    const int64_t b = p.cu[it.n], e = p.cu[it.n + 1];
+    it.t0 = b + (int64_t)it.c0 * kChunk;
+    it.t1 = min(b + (int64_t)it.c1 * kChunk, e);
+}
+
+// Walks the items of the range between two cuts.
+struct Walk {
+    const Plan &p;
+    int64_t x, end;
+    int n, h, c;
+    __device__ __forceinline__ Walk(const Plan &plan, int range)
+        : p(plan), x(plan.cuts[range].x), end(plan.cuts[range + 1].x), n(plan.cuts[range].n),
+          h(plan.cuts[range].h), c(plan.cuts[range].c) {}
+    __device__ __forceinline__ bool next(Item &it) {
+        if (x >= end) return false;
+        int nc;
+        while ((nc = p.off[n + 1] - p.off[n]) == 0) ++n;   // (sequences without tokens)
+        it.n = n;
+        it.h = h;
+        it.c0 = c;
+        it.nc = nc;
+        it.c1 = (int)min((int64_t)nc, c + (end - x));
+        set_tokens(p, it);
+        x += it.c1 - c;
+        c = 0;
+        if (++h == p.H) {
+            h = 0;
+            ++n;
+        }
+        return true;
     }
-    return lo;
+};
+
+// What the range before cut `i` (1 ..) contributes to it; false when that cut is none inside
+// a unit.
+__device__ __forceinline__ bool before_cut(const Plan &p, int i, Item &it) {
+    const Cut e = p.cuts[i];
+    if (!e.inner) return false;
+    it.n = e.n;
+    it.h = e.h;
+    it.c1 = e.c;
+    it.c0 = (int)max((int64_t)0, e.c - (e.x - p.cuts[i - 1].x));
+    it.nc = p.off[e.n + 1] - p.off[e.n];
+    set_tokens(p, it);
+    return true;
 }
 
-__device__ __forceinline__ Item segment(const Plan &p, int32_t slot) {
-    Item it;
-    it.n = p.N == 1 ? 0 : find_owner(p.seg_off, p.N, slot);
-    const int32_t first = p.seg_off[it.n];
-    it.seg = slot - first;
-    it.nseg = p.seg_off[it.n + 1] - first;
-    it.t0 = p.cu[it.n] + it.seg * p.seg_tokens;
-    it.t1 = min(it.t0 + p.seg_tokens, (int64_t)p.cu[it.n + 1]);
-    it.bnd = p.bnd_off[it.n] + it.seg;
-    return it;
-}
+// The states of the inner boundaries: cut i at index i - 1.  Where the final states overwrite
+// the initial ones, the last range of a unit may write before the first one has read: the
+// scan keeps a copy of the initial state of such a unit, for range i at index ranges + i.
+__device__ __forceinline__ int64_t cut_state(int i) { return i - 1; }
 
-// Segment j < bnd_off[N] of those that end at an inner boundary.
-__device__ __forceinline__ Item inner_segment(const Plan &p, int32_t j) {
-    Item it;
-    it.n = p.N == 1 ? 0 : find_owner(p.bnd_off, p.N, j);
-    it.seg = j - p.bnd_off[it.n];
-    it.nseg = p.seg_off[it.n + 1] - p.seg_off[it.n];
-    it.t0 = p.cu[it.n] + it.seg * p.seg_tokens;
-    it.t1 = it.t0 + p.seg_tokens;
-    it.bnd = j;
-    return it;
-}
-
-// Where segment `it` of head h starts from: boundary states, the initial state or its copy;
-// NULL for zeros.
-__device__ __forceinline__ const float *start_state(const Plan &p, const Item &it, int h,
+// Where an item of range `range` starts from; NULL for zeros.
+__device__ __forceinline__ const float *start_state(const Plan &p, const Item &it, int range,
                                                     const float *h0, const float *bnd,
                                                     int64_t dkdv) {
-    if (it.seg > 0) return bnd + ((it.bnd - 1) * p.H + h) * dkdv;
+    if (it.c0 > 0) return bnd + cut_state(range) * dkdv;
     if (!h0) return nullptr;
-    if (it.nseg > 1 && p.in_place)
-        return bnd + ((int64_t)(p.bnd_off[p.N] + p.multi_off[it.n]) * p.H + h) * dkdv;
-    return h0 + ((int64_t)it.n * p.H + h) * dkdv;
+    if (it.c1 < it.nc && p.in_place) return bnd + (int64_t)(p.ranges + range) * dkdv;
+    return h0 + ((int64_t)it.n * p.H + it.h) * dkdv;
 }
 
 // A log decay below this is e^g = 0 in fp32.  Prefix sums, whose differences give the decay

@@ -8,23 +8,21 @@
 #include "kda_la.cuh"
 
 namespace kda {
-cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int64_t seg_tokens,
-                           int32_t *seg_off, int32_t *bnd_off, int32_t *multi_off, StatusWord *st,
-                           const float *h0, float *hT, int H, int64_t dkdv, cudaStream_t s);
+cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off,
+                           int32_t *piece_off, la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
+                           int H, int64_t dkdv, cudaStream_t s);
 cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
-                           int64_t dkdv, int sms, cudaStream_t s);
+                           int64_t dkdv, cudaStream_t s);
 cudaError_t launch_la_simt(bool out, int dk, int dv, const la::Plan &p, const float *q,
                            const float *k, const float *v, int64_t qs, int64_t ks, int64_t vs,
                            const float *g, int gpt, const float *h0, float *hT, float *o,
-                           float *bnd, float *bnd_log, StatusWord *st, int64_t max_items,
-                           cudaStream_t s);
+                           float *bnd, float *bnd_log, StatusWord *st, cudaStream_t s);
 cudaError_t la_tensor_maps(CUtensorMap (&m)[4], const void *q, const void *k, const void *v,
                            const void *o, int64_t T, int H, int Hk, int dk, int dv, int64_t qs, int64_t ks,
                            int64_t vs);
 cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[4], const float *g,
                          int gpt, const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
-                         float *bnd_log, StatusWord *st, int64_t max_items, int sms,
-                         cudaStream_t s);
+                         float *bnd_log, StatusWord *st, cudaStream_t s);
 cudaError_t launch_la_decode(int dtype, int dk, int dv, const void *q, const void *k,
                              const void *v, const float *g, float *state, void *o, int N, int H,
                              int Hk, int64_t qs, int64_t ks, int64_t vs, int gpt,
@@ -69,48 +67,24 @@ bool stride_ok(int64_t stride, int64_t T, int32_t heads, int32_t D, int32_t dtyp
            (T == 0 || stride <= ((int64_t)1 << 59) / T);
 }
 
-// Tokens of a segment: chunks are 128 tokens, and the SMs should be evenly busy.  The cost
-// of a choice is counted in chunk times: the output pass walks a segment's chunks one after
-// the other with a start-up of about two, the waves of segments over the SMs follow each
-// other; cutting sequences at all adds a pass over k and v at about half the cost, and two
-// launches.  Lengths are on the device, so the average one stands for all.
-constexpr int64_t kUnit = 128;
-int64_t segment_tokens(int64_t T, int32_t N, int32_t H, int sms) {
-    if (N <= 0 || T <= 0) return kUnit;
-    const int64_t avg = (T + kUnit * N - 1) / (kUnit * N);   // chunks of the average sequence
-    const int64_t most = avg < 64 ? avg : 64;
-    int64_t best = most;
-    double best_cost = 1e300;
-    for (int64_t L = most; L >= 1; L = L > 16 ? L - 4 : L - 1) {
-        const int64_t segs = (avg + L - 1) / L;
-        const int64_t items = segs * N * H;
-        const double waves = (double)((items + sms - 1) / sms);
-        double cost = waves * (L + 2.0);
-        if (segs > 1) cost += (double)(((segs - 1) * N * H + sms - 1) / sms) * (0.5 * L + 2.0) + 4.0;
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = L;
-        }
-    }
-    // one segment for the average sequence: longer ones are cut at four times the average
-    return (best == avg ? 4 * best : best) * kUnit;
-}
-
 struct LaLayout {
-    int64_t seg_tokens, max_segs, max_bnd;
-    size_t plan_off, log_off, bnd_off, total;
+    int ranges;
+    bool split;
+    size_t cuts_off, off_off, log_off, bnd_off, total;
 };
 
+// One range an SM, and no more than there can be chunks.  Sequences are cut only where one
+// may be longer than a range of the least length (the lengths are on the device).
 LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t dk, int32_t dv, int sms) {
     LaLayout L{};
-    L.seg_tokens = segment_tokens(T, N, H, sms);
-    L.max_segs = T / L.seg_tokens + N;
-    // inner boundaries, and one kept initial state for each sequence that has one
-    L.max_bnd = T / L.seg_tokens + (T / L.seg_tokens < N ? T / L.seg_tokens : N);
-    L.plan_off = kHeaderBytes;
-    L.log_off = L.plan_off + round_up(3 * sizeof(int32_t) * ((size_t)N + 1), 256);
-    L.bnd_off = L.log_off + round_up(sizeof(float) * (size_t)L.max_bnd * H, 256);
-    L.total = L.bnd_off + sizeof(float) * (size_t)L.max_bnd * H * dk * dv;
+    const int64_t most = (T / la::kChunk + N) * (int64_t)H;
+    L.ranges = (int)(most < 1 ? 1 : most < sms ? most : sms);
+    L.split = L.ranges > 1 && T > la::kWhole * la::kChunk;
+    L.cuts_off = kHeaderBytes;
+    L.off_off = L.cuts_off + round_up(sizeof(la::Cut) * ((size_t)L.ranges + 1), 256);
+    L.log_off = L.off_off + round_up(2 * sizeof(int32_t) * ((size_t)N + 1), 256);
+    L.bnd_off = L.log_off + round_up(sizeof(float) * (size_t)L.ranges, 256);
+    L.total = L.bnd_off + (L.split ? sizeof(float) * 2 * (size_t)L.ranges * dk * dv : 0);
     return L;
 }
 
@@ -153,22 +127,21 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     if (!aligned(g, 4) || !aligned(cu_seqlens, 4) || !aligned(workspace, 256))
         return KDA_ERR_INVALID_ARG;
     if (o && (o == q || o == k || o == v)) return KDA_ERR_INVALID_ARG;
-    const int sms = sm_count();
-    const LaLayout L = la_layout(total_tokens, num_seqs, H, dk, dv, sms);
+    const LaLayout L = la_layout(total_tokens, num_seqs, H, dk, dv, sm_count());
     if (workspace_bytes < L.total) return KDA_ERR_INVALID_ARG;
 
     cudaStream_t s = (cudaStream_t)stream;
     StatusWord *st = (StatusWord *)workspace;
     if (num_seqs == 0) return cuda_status(cudaMemsetAsync(st, 0, sizeof(StatusWord), s));
     uint8_t *ws = (uint8_t *)workspace;
-    int32_t *plan = (int32_t *)(ws + L.plan_off);
+    la::Cut *cuts = (la::Cut *)(ws + L.cuts_off);
+    int32_t *off = (int32_t *)(ws + L.off_off);
     float *bnd_log = (float *)(ws + L.log_off), *bnd = (float *)(ws + L.bnd_off);
     const int64_t dkdv = (int64_t)dk * dv;
-    const la::Plan p{cu_seqlens, plan, plan + num_seqs + 1, plan + 2 * (num_seqs + 1), num_seqs, H,
-                     Hk, L.seg_tokens, initial_state && initial_state == final_state};
-    cudaError_t e = launch_la_plan(cu_seqlens, num_seqs, total_tokens, L.seg_tokens, plan,
-                                   plan + num_seqs + 1, plan + 2 * (num_seqs + 1), st,
-                                   initial_state, final_state, H, dkdv, s);
+    const la::Plan p{cu_seqlens, off, cuts, num_seqs, H, Hk, L.ranges,
+                     initial_state && initial_state == final_state};
+    cudaError_t e = launch_la_plan(cu_seqlens, num_seqs, total_tokens, off, off + num_seqs + 1, cuts,
+                                   L.ranges, L.split, st, initial_state, final_state, H, dkdv, s);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (total_tokens == 0) return KDA_OK;
     CUtensorMap maps[4];
@@ -177,17 +150,16 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
                        v_stride) != cudaSuccess)
         return KDA_ERR_CUDA;
     auto pass = [&](bool out) {
-        const int64_t most = (out ? L.max_segs : L.max_bnd) * H;
         if (dtype == KDA_BF16)
             return launch_la_tc(out, p, maps, g, g_per_token, initial_state, final_state, o, dk, dv,
-                                bnd, bnd_log, st, most, sms, s);
+                                bnd, bnd_log, st, s);
         return launch_la_simt(out, dk, dv, p, (const float *)q, (const float *)k, (const float *)v,
                               q_stride, k_stride, v_stride, g, g_per_token, initial_state,
-                              final_state, (float *)o, bnd, bnd_log, st, most, s);
+                              final_state, (float *)o, bnd, bnd_log, st, s);
     };
-    if (total_tokens > L.seg_tokens) {   // else no sequence has an inner boundary
+    if (L.split) {
         e = pass(false);
-        if (e == cudaSuccess) e = launch_la_scan(p, initial_state, bnd, bnd_log, dkdv, sms, s);
+        if (e == cudaSuccess) e = launch_la_scan(p, initial_state, bnd, bnd_log, dkdv, s);
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     return cuda_status(pass(true));

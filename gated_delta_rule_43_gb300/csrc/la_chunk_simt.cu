@@ -13,13 +13,40 @@ namespace kda {
 namespace la {
 
 // ------------------------------------------------------------------------- plan
-// One CTA: validates cu_seqlens (see plan_chunks_kernel), counts segments and inner
-// boundaries.  Every CTA: final states of sequences without tokens (S_out not NULL).
+// CTA 0: validates cu_seqlens (see plan_chunks_kernel), counts chunks and places the cuts.
+// Every CTA: final states of sequences without tokens (S_out not NULL).
 constexpr int kPlanThreads = 256;
+
+// The largest n with off[n] * H <= x, for x < off[N] * H: entry n spans x.
+__device__ __forceinline__ int owner(const int32_t *off, int N, int H, int64_t x) {
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)off[mid] * H <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ Cut place(const int32_t *off, int N, int H, int64_t total, int64_t x) {
+    Cut r{x, N, 0, 0, 0};
+    if (x >= total) return r;
+    r.n = owner(off, N, H, x);
+    const int64_t nc = off[r.n + 1] - off[r.n], rest = x - (int64_t)off[r.n] * H;
+    r.h = (int)(rest / nc);
+    r.c = (int)(rest - r.h * nc);
+    r.inner = r.c > 0;
+    return r;
+}
+
+// Ranges a unit of nc chunks is worth when there are SMs to spare
+__device__ __forceinline__ int pieces(int nc, int split) {
+    return nc == 0 ? 0 : !split || nc < 2 * kMinRange ? 1 : nc / kMinRange;
+}
+
 __global__ void __launch_bounds__(kPlanThreads)
-la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int64_t seg_tokens,
-               int32_t *__restrict__ seg_off, int32_t *__restrict__ bnd_off,
-               int32_t *__restrict__ multi_off, StatusWord *st, const float *h0, float *S_out, int H, int64_t dkdv4) {
+la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *off,
+               int32_t *piece_off, Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *S_out, int H,
+               int64_t dkdv4) {
     if (S_out) {
         for (int64_t nh = blockIdx.x; nh < (int64_t)N * H; nh += gridDim.x) {
             const int n = (int)(nh / H);
@@ -33,7 +60,7 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int64_t seg
     }
     if (blockIdx.x != 0) return;
     constexpr int NW = kPlanThreads / 32;
-    __shared__ int3 s_warp[NW];
+    __shared__ int2 s_warp[NW];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     if (tid == 0) {
         st->code = 0u;
@@ -42,92 +69,117 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int64_t seg
     }
     __syncthreads();
     if (tid == 0 && (cu[0] != 0 || (int64_t)cu[N] != T_tot)) report(st, KDA_ERR_SEQLENS, N, 1);
-    __syncthreads();
-    int3 carry = make_int3(0, 0, 0);   // segments, inner boundaries, sequences of several
-    auto add = [](int3 &x, const int3 &y) { x.x += y.x; x.y += y.y; x.z += y.z; };
+    int2 carry = make_int2(0, 0);   // chunks, pieces
     for (int base = 0; base < N; base += kPlanThreads) {
         const int n = base + tid;
-        int segs = 0;
+        int2 own = make_int2(0, 0);
         if (n < N) {
             const int64_t b = cu[n], e = cu[n + 1];
             if (b < 0 || e < b || e > T_tot)
                 report(st, KDA_ERR_SEQLENS, n, 2);
             else
-                segs = (int)((e - b + seg_tokens - 1) / seg_tokens);
+                own.x = (int)((e - b + kChunk - 1) / kChunk);
+            own.y = pieces(own.x, split);
         }
-        const int3 own = make_int3(segs, max(segs - 1, 0), segs > 1 ? 1 : 0);
-        int3 x = own;   // inclusive warp scan
+        int2 x = own;   // inclusive warp scan
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int3 y = make_int3(__shfl_up_sync(0xffffffffu, x.x, o),
-                                     __shfl_up_sync(0xffffffffu, x.y, o),
-                                     __shfl_up_sync(0xffffffffu, x.z, o));
-            if (lane >= o) add(x, y);
+            const int y = __shfl_up_sync(0xffffffffu, x.x, o), z = __shfl_up_sync(0xffffffffu, x.y, o);
+            if (lane >= o) {
+                x.x += y;
+                x.y += z;
+            }
         }
         if (lane == 31) s_warp[wid] = x;
         __syncthreads();
-        int3 before = carry;
+        int2 before = carry;
         for (int w = 0; w < NW; ++w) {
-            if (w < wid) add(before, s_warp[w]);
-            add(carry, s_warp[w]);
+            if (w < wid) {
+                before.x += s_warp[w].x;
+                before.y += s_warp[w].y;
+            }
+            carry.x += s_warp[w].x;
+            carry.y += s_warp[w].y;
         }
         if (n < N) {
-            seg_off[n] = before.x + x.x - own.x;
-            bnd_off[n] = before.y + x.y - own.y;
-            multi_off[n] = before.z + x.z - own.z;
+            off[n] = before.x + x.x - own.x;
+            piece_off[n] = before.y + x.y - own.y;
         }
         __syncthreads();
     }
     if (tid == 0) {
-        seg_off[N] = carry.x;
-        bnd_off[N] = carry.y;
-        multi_off[N] = carry.z;
+        off[N] = carry.x;
+        piece_off[N] = carry.y;
+    }
+    __syncthreads();
+    const int64_t total = (int64_t)carry.x * H, fine = (int64_t)carry.y * H;
+    // SMs to spare: every unit gets its own range, a long one several.  Else equal parts
+    // (without a first pass nothing can be cut: the units are dealt out whole).
+    const bool spare = fine <= ranges && total < (int64_t)ranges * kMinRange;
+    for (int i = tid; i <= ranges; i += kPlanThreads) {
+        Cut r;
+        if (spare) {
+            int64_t x = total;
+            if (i < fine) {
+                const int n = owner(piece_off, N, H, i);
+                const int nc = off[n + 1] - off[n], m = piece_off[n + 1] - piece_off[n];
+                const int rest = i - piece_off[n] * H;
+                x = (int64_t)off[n] * H + (int64_t)(rest / m) * nc + (int64_t)(rest % m) * nc / m;
+            }
+            r = place(off, N, H, total, x);
+        } else {
+            r = place(off, N, H, total, (int64_t)i * total / ranges);
+            if (r.inner) {
+                const int nc = off[r.n + 1] - off[r.n];
+                if (!split || nc <= kWhole)
+                    r = place(off, N, H, total, r.x + (2 * r.c >= nc ? nc - r.c : -r.c));
+            }
+        }
+        cuts[i] = r;
     }
 }
 
 // ------------------------------------------------------------------------- scan
-// bnd[b] holds what segment b's own tokens leave at its end; afterwards it holds the state
-// there: S_b = exp(bnd_log[b]) S_{b-1} + bnd[b] along each sequence, from h0 (or zeros).
-// One thread per four state values; the loads of kAhead boundaries are in flight at a time.
-constexpr int kScanThreads = 256, kAhead = 4;
+// Along the cuts of each unit, from its initial state: S <- exp(bnd_log) S + bnd, where bnd
+// holds what the tokens since the cut before leave and then the state.  One thread per four
+// state values; the loads of kAhead cuts are in flight at a time.
+constexpr int kScanThreads = 256, kAhead = 8;
 __global__ void __launch_bounds__(kScanThreads)
 la_scan_kernel(Plan p, const float *__restrict__ h0, float *__restrict__ bnd,
                const float *__restrict__ bnd_log, int64_t dkdv4) {
-    const int64_t per_head = dkdv4;
-    const int64_t total = (int64_t)p.N * p.H * per_head;
-    for (int64_t x = (int64_t)blockIdx.x * kScanThreads + threadIdx.x; x < total;
-         x += (int64_t)gridDim.x * kScanThreads) {
-        const int64_t nh = x / per_head, i = x - nh * per_head;
-        const int n = (int)(nh / p.H), h = (int)(nh - (int64_t)n * p.H);
-        const int32_t b0 = p.bnd_off[n], b1 = p.bnd_off[n + 1];
-        if (b0 >= b1) continue;
-        float4 S = h0 ? reinterpret_cast<const float4 *>(h0)[x] : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.in_place)
-            reinterpret_cast<float4 *>(bnd)[((int64_t)(p.bnd_off[p.N] + p.multi_off[n]) * p.H + h) *
-                                                per_head + i] = S;
-        float4 *col = reinterpret_cast<float4 *>(bnd) + ((int64_t)b0 * p.H + h) * per_head + i;
-        const float *lg = bnd_log + (int64_t)b0 * p.H + h;
-        const int64_t step = (int64_t)p.H * per_head;
-        for (int32_t b = 0; b < b1 - b0; b += kAhead) {
-            float4 add[kAhead];
-            float a[kAhead];
+    const int first = blockIdx.y + 1;
+    const Cut f = p.cuts[first];
+    // a unit's chain starts at its first cut: the range before it holds the unit's start
+    if (!f.inner || p.cuts[first - 1].x > f.x - f.c) return;
+    const int64_t i = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
+    if (i >= dkdv4) return;
+    int last = first;
+    while (last + 1 < p.ranges && p.cuts[last + 1].inner && p.cuts[last + 1].n == f.n &&
+           p.cuts[last + 1].h == f.h)
+        ++last;
+    float4 S = h0 ? reinterpret_cast<const float4 *>(h0)[((int64_t)f.n * p.H + f.h) * dkdv4 + i]
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 *at = reinterpret_cast<float4 *>(bnd) + i;
+    if (p.in_place) at[(int64_t)(p.ranges + first - 1) * dkdv4] = S;
+    for (int b = first; b <= last; b += kAhead) {
+        float4 add[kAhead];
+        float a[kAhead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (b + j < b1 - b0) {
-                    add[j] = col[(b + j) * step];
-                    a[j] = lg[(int64_t)(b + j) * p.H];
-                }
+        for (int j = 0; j < kAhead; ++j)
+            if (b + j <= last) {
+                add[j] = at[cut_state(b + j) * dkdv4];
+                a[j] = bnd_log[cut_state(b + j)];
+            }
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (b + j < b1 - b0) {
-                    const float e = expf(a[j]);
-                    S.x = e * S.x + add[j].x;
-                    S.y = e * S.y + add[j].y;
-                    S.z = e * S.z + add[j].z;
-                    S.w = e * S.w + add[j].w;
-                    col[(b + j) * step] = S;
-                }
-        }
+        for (int j = 0; j < kAhead; ++j)
+            if (b + j <= last) {
+                const float e = expf(a[j]);
+                S.x = e * S.x + add[j].x;
+                S.y = e * S.y + add[j].y;
+                S.z = e * S.z + add[j].z;
+                S.w = e * S.w + add[j].w;
+                at[cut_state(b + j) * dkdv4] = S;
+            }
     }
 }
 
@@ -145,8 +197,8 @@ template <int DK, int DVB> struct Smem {
     float total, total_log;             // the chunk's decay and its log
 };
 
-// OUT: outputs and final states of the segments `items` = (slot, head, column block);
-// else the contributions of the segments that end at an inner boundary.
+// OUT: outputs and final states of the CTA's range.  Else what the end of the range leaves at
+// the cut behind it.  The column blocks of a range are CTAs of their own.
 template <int DK, int DV, int DVB, bool OUT>
 __global__ void __launch_bounds__(kThreads)
 la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restrict__ k,
@@ -165,18 +217,18 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
     static_assert(DK % TR == 0 && SR >= 1 && C % OR == 0, "shape");
     const int tid = threadIdx.x;
     const int c4 = (tid % TC) * 4, rg = tid / TC;
-    const int64_t items = (int64_t)(OUT ? p.seg_off[p.N] : p.bnd_off[p.N]) * p.H * NB;
     const int64_t dkdv = (int64_t)DK * DV;
+    const int blk = blockIdx.x % NB, range = blockIdx.x / NB;
+    Item it;
+    Walk walk(p, range);
+    bool more = OUT ? walk.next(it) : before_cut(p, range + 1, it);
 
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int blk = (int)(item % NB);
-        const int h = (int)(item / NB % p.H);
-        const int32_t slot = (int32_t)(item / ((int64_t)NB * p.H));
-        const Item it = OUT ? segment(p, slot) : inner_segment(p, slot);
+    for (; more; more = OUT && walk.next(it)) {
+        const int h = it.h;
         const int hk = h / (p.H / p.Hk);
         const int j0 = blk * DVB;
         const int64_t nh = ((int64_t)it.n * p.H + h) * dkdv;
-        const float *start = OUT ? start_state(p, it, h, h0, bnd, dkdv) : nullptr;
+        const float *start = OUT ? start_state(p, it, range, h0, bnd, dkdv) : nullptr;
         float S[SR][4];
 #pragma unroll
         for (int r = 0; r < SR; ++r) {
@@ -299,15 +351,15 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
                 for (int j = 0; j < 4; ++j) S[r][j] = e * S[r][j] + add[r][j];
             __syncthreads();
         }
-        float *dst = OUT ? (it.seg == it.nseg - 1 && hT ? hT + nh : nullptr)
-                         : bnd + (it.bnd * p.H + h) * dkdv;
+        float *dst = OUT ? (it.c1 == it.nc && hT ? hT + nh : nullptr)
+                         : bnd + cut_state(range + 1) * dkdv;
         if (dst) {
 #pragma unroll
             for (int r = 0; r < SR; ++r)
                 *reinterpret_cast<float4 *>(dst + (int64_t)(rg * SR + r) * DV + j0 + c4) =
                     make_float4(S[r][0], S[r][1], S[r][2], S[r][3]);
         }
-        if (!OUT && blk == 0 && tid == 0) bnd_log[it.bnd * p.H + h] = log_sum;
+        if (!OUT && blk == 0 && tid == 0) bnd_log[cut_state(range + 1)] = log_sum;
     }
 }
 
@@ -315,49 +367,47 @@ template <int DK, int DV>
 static cudaError_t launch_dims(bool out, const Plan &p, const float *q, const float *k,
                                const float *v, int64_t qs, int64_t ks, int64_t vs, const float *g,
                                int gpt, const float *h0, float *hT, float *o, float *bnd,
-                               float *bnd_log, StatusWord *st, int64_t max_items, cudaStream_t s) {
+                               float *bnd_log, StatusWord *st, cudaStream_t s) {
     constexpr int DVB = DV < 64 ? DV : 64;
     constexpr size_t bytes = sizeof(Smem<DK, DVB>);
     auto *f = out ? la_chunk_simt_kernel<DK, DV, DVB, true> : la_chunk_simt_kernel<DK, DV, DVB, false>;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    const int64_t grid = max_items * (DV / DVB);
-    f<<<(unsigned)(grid < 4096 ? grid : 4096), kThreads, bytes, s>>>(p, q, k, v, qs, ks, vs, g, gpt,
-                                                                     h0, hT, o, bnd, bnd_log, st);
+    const int ranges = out ? p.ranges : p.ranges - 1;   // (the last ends at the row's end)
+    f<<<ranges * (DV / DVB), kThreads, bytes, s>>>(p, q, k, v, qs, ks, vs, g, gpt, h0, hT, o, bnd,
+                                                   bnd_log, st);
     return cudaGetLastError();
 }
 
 }  // namespace la
 
-cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int64_t seg_tokens,
-                           int32_t *seg_off, int32_t *bnd_off, int32_t *multi_off, StatusWord *st,
-                           const float *h0, float *hT, int H, int64_t dkdv, cudaStream_t s) {
+cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off,
+                           int32_t *piece_off, la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
+                           int H, int64_t dkdv, cudaStream_t s) {
     float *S_out = hT != h0 ? hT : nullptr;   // an in-place update leaves empty ones as they are
     const int64_t nh = (int64_t)N * H;
     const int grid = S_out && nh > 1 ? (int)(nh < 256 ? nh : 256) : 1;
-    la::la_plan_kernel<<<grid, la::kPlanThreads, 0, s>>>(cu, N, T_tot, seg_tokens, seg_off, bnd_off,
-                                                        multi_off, st, h0, S_out, H, dkdv / 4);
+    la::la_plan_kernel<<<grid, la::kPlanThreads, 0, s>>>(cu, N, T_tot, off, piece_off, cuts, ranges,
+                                                        split, st, h0, S_out, H, dkdv / 4);
     return cudaGetLastError();
 }
 
 cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
-                           int64_t dkdv, int sms, cudaStream_t s) {
-    const int64_t blocks = ((int64_t)p.N * p.H * (dkdv / 4) + la::kScanThreads - 1) / la::kScanThreads;
-    const int64_t most = 8 * (int64_t)sms;
-    la::la_scan_kernel<<<(unsigned)(blocks < most ? blocks : most), la::kScanThreads, 0, s>>>(
-        p, h0, bnd, bnd_log, dkdv / 4);
+                           int64_t dkdv, cudaStream_t s) {
+    const dim3 grid((unsigned)((dkdv / 4 + la::kScanThreads - 1) / la::kScanThreads),
+                    (unsigned)(p.ranges - 1));
+    la::la_scan_kernel<<<grid, la::kScanThreads, 0, s>>>(p, h0, bnd, bnd_log, dkdv / 4);
     return cudaGetLastError();
 }
 
 cudaError_t launch_la_simt(bool out, int dk, int dv, const la::Plan &p, const float *q,
                            const float *k, const float *v, int64_t qs, int64_t ks, int64_t vs,
                            const float *g, int gpt, const float *h0, float *hT, float *o,
-                           float *bnd, float *bnd_log, StatusWord *st, int64_t max_items,
-                           cudaStream_t s) {
+                           float *bnd, float *bnd_log, StatusWord *st, cudaStream_t s) {
 #define KDA_LA(DK_, DV_)                                                                       \
     if (dk == DK_ && dv == DV_)                                                                \
         return la::launch_dims<DK_, DV_>(out, p, q, k, v, qs, ks, vs, g, gpt, h0, hT, o, bnd,  \
-                                         bnd_log, st, max_items, s);
+                                         bnd_log, st, s);
     KDA_LA(32, 32) KDA_LA(32, 64) KDA_LA(32, 128)
     KDA_LA(64, 32) KDA_LA(64, 64) KDA_LA(64, 128)
     KDA_LA(128, 32) KDA_LA(128, 64) KDA_LA(128, 128)

@@ -19,8 +19,8 @@
 // of the 32-token block of s, it is exp(G_t - R) exp(R - G_s), two factors of at most one,
 // for the blocks before that of t, and is formed token by token inside t's own block.
 //
-// One CTA an SM walks segments (see kda_la.cuh), every role for itself through the same
-// list of (segment, head, chunk):
+// One CTA an SM walks its range (see kda_la.cuh), every role for itself through the same
+// items and chunks:
 //   warps 0-3    rows of P (tensor memory, as the A operand of P V), rows of O (through
 //                shared memory, over the image of S, in one bulk store: rows stored straight
 //                from registers cost 2k cycles a chunk and held up everyone's shared memory)
@@ -42,7 +42,7 @@ namespace tc {
 
 using namespace sm100;
 
-constexpr int C = 128;
+constexpr int C = kChunk;
 constexpr int kThreads = 512;
 constexpr int kRowWarps = 4, kStateWarps = 8;
 constexpr int kMmaWarp = 12, kLoadWarp = 13, kGateWarp = 14;
@@ -151,8 +151,8 @@ struct Waits {
     }
 };
 
-// OUT: outputs and final states of all segments.  Else what the segments that end at an inner
-// boundary leave there of their own tokens (only K~^T V; no queries).
+// OUT: outputs and final states of the CTA's range.  Else what the end of the range leaves at
+// the cut behind it (only K~^T V; no queries).
 template <int DKP, int DVP, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
@@ -164,8 +164,8 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     extern __shared__ __align__(1024) uint8_t sm[];
     using M = Map<DKP, DVP>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t items = (int64_t)(OUT ? p.seg_off[p.N] : p.bnd_off[p.N]) * p.H;
-    if (blockIdx.x >= items) return;
+    const int range = blockIdx.x;
+    if (OUT ? p.cuts[range].x >= p.cuts[range + 1].x : !p.cuts[range + 1].inner) return;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + M::kBar);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + M::kBar + kBars * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + M::kBar + kBars * 8 + 4);
@@ -213,11 +213,12 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     bool ok = true;
     uint32_t loaded = 0, landed = 0;   // (load warp)
 
-    for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        const int h = (int)(item % p.H);
-        const int32_t slot = (int32_t)(item / p.H);
-        const Item it = OUT ? segment(p, slot) : inner_segment(p, slot);
-        const int chunks = (int)((it.t1 - it.t0 + C - 1) / C);
+    Item it;
+    Walk walk(p, range);
+    bool more = OUT ? walk.next(it) : before_cut(p, range + 1, it);
+    for (; more && ok; more = OUT && walk.next(it)) {
+        const int h = it.h;
+        const int chunks = it.c1 - it.c0;
 
         if (warp < kRowWarps) {
             if (!OUT) continue;
@@ -331,7 +332,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             const bool mine = i < dk && j0 < dv;
             const int64_t at = (int64_t)i * dv + j0;
             float S[NC];
-            const float *start = OUT ? start_state(p, it, h, h0, bnd, dkdv) : nullptr;
+            const float *start = OUT ? start_state(p, it, range, h0, bnd, dkdv) : nullptr;
 #pragma unroll
             for (int j = 0; j < NC; j += 4) {
                 const float4 x = start && mine ? *reinterpret_cast<const float4 *>(start + at + j)
@@ -417,9 +418,9 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 tc_fence_before();
                 if (OUT && c + 1 < chunks) ok = put_image(gi + 1);
             }
-            float *dst = OUT ? (it.seg == it.nseg - 1 && hT ? hT + ((int64_t)it.n * p.H + h) * dkdv
-                                                            : nullptr)
-                             : bnd + (it.bnd * p.H + h) * dkdv;
+            float *dst = OUT ? (it.c1 == it.nc && hT ? hT + ((int64_t)it.n * p.H + h) * dkdv
+                                                     : nullptr)
+                             : bnd + cut_state(range + 1) * dkdv;
             if (ok && dst && mine) {
 #pragma unroll
                 for (int j = 0; j < NC; j += 4)
@@ -573,11 +574,11 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kGate + b]);
             }
-            if (!OUT && ok && lane == 0) bnd_log[it.bnd * p.H + h] = log_sum;
+            if (!OUT && ok && lane == 0) bnd_log[cut_state(range + 1)] = log_sum;
         }
         if (!ok) {
             *abort_flag = 1;
-            if (lane == 0) report(st, KDA_ERR_TIMEOUT, item, 41 + warp);
+            if (lane == 0) report(st, KDA_ERR_TIMEOUT, range, 41 + warp);
         }
     }
     __syncthreads();
@@ -654,14 +655,13 @@ template <int DKP, int DVP, bool OUT> static cudaError_t allow_smem(int dev) {
 template <int DKP, int DVP, bool OUT>
 static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[4], const float *g, int gpt,
                           const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
-                          float *bnd_log, StatusWord *st, int64_t max_items, int sms,
-                          cudaStream_t s) {
+                          float *bnd_log, StatusWord *st, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = allow_smem<DKP, DVP, OUT>(dev);
     if (e != cudaSuccess) return e;
     la_chunk_tc_kernel<DKP, DVP, OUT>
-        <<<(unsigned)(max_items < sms ? max_items : sms), kThreads, Map<DKP, DVP>::kBytes, s>>>(
+        <<<OUT ? p.ranges : p.ranges - 1, kThreads, Map<DKP, DVP>::kBytes, s>>>(
             p, m[0], m[1], m[2], m[3], g, gpt, h0, hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
     return cudaGetLastError();
 }
@@ -681,14 +681,13 @@ cudaError_t la_tensor_maps(CUtensorMap (&m)[4], const void *q, const void *k, co
 
 cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[4], const float *g,
                          int gpt, const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
-                         float *bnd_log, StatusWord *st, int64_t max_items, int sms,
-                         cudaStream_t s) {
+                         float *bnd_log, StatusWord *st, cudaStream_t s) {
 #define KDA_LA(DK_, DV_)                                                                          \
     if ((dk <= 64) == (DK_ == 64) && (dv <= 64) == (DV_ == 64))                                   \
         return out ? la::tc::launch<DK_, DV_, true>(p, m, g, gpt, h0, hT, o, dk, dv, bnd, bnd_log, \
-                                                    st, max_items, sms, s)                        \
+                                                    st, s)                                        \
                    : la::tc::launch<DK_, DV_, false>(p, m, g, gpt, h0, hT, o, dk, dv, bnd, bnd_log, \
-                                                     st, max_items, sms, s);
+                                                     st, s);
     KDA_LA(64, 64) KDA_LA(64, 128) KDA_LA(128, 64) KDA_LA(128, 128)
 #undef KDA_LA
     return cudaErrorInvalidValue;

@@ -7,7 +7,6 @@ calls raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -107,16 +106,6 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
-
-
-def _allocating(stream):
-    """Buffers that a call allocates belong to the stream that it runs on, so that the caching
-    allocator hands their memory on in that stream's order."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _check_cuda(*ts):
@@ -382,44 +371,88 @@ def gate_cumsum(z, A_log, cu_seqlens, chunk: int = 64, *, softplus: bool = False
     return G, workspace
 
 
+# The calls below are short on the GPU (a decode step of one sequence takes 4 us), so their
+# checks are written to cost little: one comparison where everything fits, the message only
+# where something does not.
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _same_gpu(q, *ts):
+    """The index of q's GPU; every tensor given lives there."""
+    device = q.get_device()
+    for t in ts:
+        if t is not None and t.get_device() != device:
+            device = -1
+            break
+    if device < 0:
+        raise ValueError("every tensor must live on one CUDA device (no CPU fallback)")
+    return device
+
+
+def _dense(name, t, shape, dtype):
+    """t has exactly this shape and dtype and is contiguous; returns its address."""
+    if t.shape != shape or t.dtype != dtype:
+        _expect(name, t, shape, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 def _rows(name, t, T, heads, D, dtype):
     """Checks a [T, heads, D] tensor whose tokens may lie further apart than heads * D (a
     slice of a fused projection); returns the distance in elements.  A single token or none
     has no distance: the packed one stands for it."""
-    _expect(name, t, (T, heads, D), dtype)
+    if t.shape != (T, heads, D) or t.dtype != dtype:
+        _expect(name, t, (T, heads, D), dtype)
     s = t.stride()
     if (s[2] != 1 and D > 1) or (s[1] != D and heads > 1):
         raise ValueError(f"{name}: heads and channels must be packed (strides {s})")
     return s[0] if T > 1 else heads * D
 
 
-def _on_gpu(*ts):
-    dev = None
-    for t in ts:
-        if t is not None:
-            if not t.is_cuda:
-                raise ValueError("every tensor must live on a CUDA device (no CPU fallback)")
-            if dev is not None and t.device != dev:
-                raise ValueError("tensors must live on one device")
-            dev = t.device
+def _new(like, shape, dtype, stream):
+    """Buffers that a call allocates belong to the stream that it runs on, so that the caching
+    allocator hands their memory on in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _workspace(like, nbytes, workspace, stream):
+    """(workspace, its address, its bytes): the caller's, or a new one."""
+    if workspace is None:
+        workspace = _new(like, max(nbytes, 256), torch.uint8, stream)
+        return workspace, workspace.data_ptr(), max(nbytes, 256)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _check_la(q, k, v, g):
     """q, k [T, Hk, dk], v [T, H, dv] (token strides free), g [T, H] or [H] fp32.
-    Returns (T, H, Hk, dk, dv, token strides, g per token)."""
+    Returns (T, H, Hk, dk, dv, dtype, token strides, g per token, g's address)."""
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q must be [T, Hk, dk] and v [T, H, dv]")
-    if q.dtype not in _DT:
-        raise TypeError(f"q has dtype {q.dtype}; fp32 and bf16 are supported")
+    dtype = q.dtype
+    if dtype not in _DT:
+        raise TypeError(f"q has dtype {dtype}; fp32 and bf16 are supported")
     T, Hk, dk = q.shape
-    H, dv = v.shape[1:]
+    _, H, dv = v.shape
     if Hk < 1 or H % Hk:
         raise ValueError(f"{H} value heads cannot share {Hk} query/key heads")
-    strides = (_rows("q", q, T, Hk, dk, q.dtype), _rows("k", k, T, Hk, dk, q.dtype),
-               _rows("v", v, T, H, dv, q.dtype))
+    strides = (_rows("q", q, T, Hk, dk, dtype), _rows("k", k, T, Hk, dk, dtype),
+               _rows("v", v, T, H, dv, dtype))
     per_token = g.dim() == 2
-    _expect("g", g, (T, H) if per_token else (H,), torch.float32)
-    return T, H, Hk, dk, dv, strides, 1 if per_token else 0
+    return (T, H, Hk, dk, dv, dtype, strides, 1 if per_token else 0,
+            _dense("g", g, (T, H) if per_token else (H,), torch.float32))
 
 
 def la_chunk_fwd(q, k, v, g, cu_seqlens, initial_state=None, *, output_final_state: bool = True,
@@ -433,29 +466,32 @@ def la_chunk_fwd(q, k, v, g, cu_seqlens, initial_state=None, *, output_final_sta
     None).  ``final_state`` may be ``initial_state``.  ``check=True`` synchronises the stream
     and raises device-found errors.
     """
-    lib = load()
-    T, H, Hk, dk, dv, (qs, ks, vs), gpt = _check_la(q, k, v, g)
+    lib = _lib or load()
+    T, H, Hk, dk, dv, dtype, (qs, ks, vs), gpt, ga = _check_la(q, k, v, g)
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or cu_seqlens.dtype != torch.int32:
         raise TypeError("cu_seqlens must be a 1-D int32 tensor [N + 1]")
     N = cu_seqlens.numel() - 1
-    _expect("initial_state", initial_state, (N, H, dk, dv), torch.float32)
-    _expect("final_state", final_state, (N, H, dk, dv), torch.float32)
-    _expect("o", o, (T, H, dv), q.dtype)
-    _on_gpu(q, k, v, g, cu_seqlens, initial_state, o, final_state, workspace)
-    _check_cuda(g, cu_seqlens, initial_state, o, final_state, workspace)
-    dt = _DT[q.dtype]
-    need = int(lib.kda_la_chunk_fwd_workspace_size(T, N, H, Hk, dk, dv, dt))
-    with _allocating(stream):
-        if o is None:
-            o = torch.empty(T, H, dv, dtype=q.dtype, device=q.device)
-        if final_state is None and output_final_state:
-            final_state = torch.empty(N, H, dk, dv, dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = alloc_workspace(need, q.device)
-    rc = lib.kda_la_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), N, T, H, Hk,
-                              dk, dv, dt, qs, ks, vs, gpt, _ptr(initial_state),
-                              _ptr(final_state), _ptr(o), _ptr(workspace), _nbytes(workspace),
-                              _stream(stream))
+    ca = _dense("cu_seqlens", cu_seqlens, (N + 1,), torch.int32)
+    ia = None
+    if initial_state is not None:
+        ia = _dense("initial_state", initial_state, (N, H, dk, dv), torch.float32)
+    if final_state is not None:
+        _dense("final_state", final_state, (N, H, dk, dv), torch.float32)
+    if o is not None:
+        _dense("o", o, (T, H, dv), dtype)
+    device = _same_gpu(q, k, v, g, cu_seqlens, initial_state, o, final_state, workspace)
+    if o is None:
+        o = _new(q, (T, H, dv), dtype, stream)
+    if final_state is None and output_final_state:
+        final_state = _new(q, (N, H, dk, dv), torch.float32, stream)
+    dt = _DT[dtype]
+    need = 0
+    if workspace is None:
+        need = lib.kda_la_chunk_fwd_workspace_size(T, N, H, Hk, dk, dv, dt)
+    workspace, wa, wb = _workspace(q, need, workspace, stream)
+    rc = lib.kda_la_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), ga, ca, N, T, H, Hk, dk, dv,
+                              dt, qs, ks, vs, gpt, ia, _addr(final_state), o.data_ptr(), wa, wb,
+                              _raw_stream(stream, device))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_la_chunk_fwd")
     if check:
@@ -469,17 +505,17 @@ def la_decode_step(q, k, v, g, state, *, o=None, stream=None):
     q, k [N, Hk, dk], v [N, H, dv], g [N, H] or [H] fp32; state [N, H, dk, dv] fp32, updated
     in place.  Returns o [N, H, dv].
     """
-    lib = load()
-    N, H, Hk, dk, dv, (qs, ks, vs), gpt = _check_la(q, k, v, g)
-    _expect("state", state, (N, H, dk, dv), torch.float32)
-    _expect("o", o, (N, H, dv), q.dtype)
-    _on_gpu(q, k, v, g, state, o)
-    _check_cuda(g, state, o)
+    lib = _lib or load()
+    N, H, Hk, dk, dv, dtype, (qs, ks, vs), gpt, ga = _check_la(q, k, v, g)
+    sa = _dense("state", state, (N, H, dk, dv), torch.float32)
+    if o is not None:
+        _dense("o", o, (N, H, dv), dtype)
+    device = _same_gpu(q, k, v, g, state, o)
     if o is None:
-        with _allocating(stream):
-            o = torch.empty(N, H, dv, dtype=q.dtype, device=q.device)
-    rc = lib.kda_la_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(o), N, H, Hk,
-                                dk, dv, _DT[q.dtype], qs, ks, vs, gpt, _stream(stream))
+        o = _new(q, (N, H, dv), dtype, stream)
+    rc = lib.kda_la_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), ga, sa, o.data_ptr(), N, H,
+                                Hk, dk, dv, _DT[dtype], qs, ks, vs, gpt,
+                                _raw_stream(stream, device))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_la_decode_step")
     return o
@@ -490,24 +526,24 @@ def la_decode_step_indexed(q, k, v, g, state_pool, state_idx, *, o=None, workspa
     """la_decode_step where sequence n owns slot state_idx[n] (distinct, int32) of state_pool
     [P, H, dk, dv].  With a workspace (or check=True) an index outside the pool is recorded
     in its status word; that sequence is skipped either way and its row of o not written."""
-    lib = load()
-    N, H, Hk, dk, dv, (qs, ks, vs), gpt = _check_la(q, k, v, g)
+    lib = _lib or load()
+    N, H, Hk, dk, dv, dtype, (qs, ks, vs), gpt, ga = _check_la(q, k, v, g)
     if state_pool.dim() != 4:
         raise ValueError("state_pool must be [P, H, dk, dv]")
-    _expect("state_pool", state_pool, (state_pool.shape[0], H, dk, dv), torch.float32)
-    _expect("state_idx", state_idx, (N,), torch.int32)
-    _expect("o", o, (N, H, dv), q.dtype)
-    _on_gpu(q, k, v, g, state_pool, state_idx, o, workspace)
-    _check_cuda(g, state_pool, state_idx, o, workspace)
-    with _allocating(stream):
-        if o is None:
-            o = torch.empty(N, H, dv, dtype=q.dtype, device=q.device)
-        if workspace is None and check:
-            workspace = alloc_workspace(int(lib.kda_decode_workspace_size()), q.device)
-    rc = lib.kda_la_decode_step_indexed(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state_pool),
-                                        _ptr(state_idx), state_pool.shape[0], _ptr(o), N, H, Hk,
-                                        dk, dv, _DT[q.dtype], qs, ks, vs, gpt, _ptr(workspace),
-                                        _nbytes(workspace), _stream(stream))
+    P_ = state_pool.shape[0]
+    sa = _dense("state_pool", state_pool, (P_, H, dk, dv), torch.float32)
+    xa = _dense("state_idx", state_idx, (N,), torch.int32)
+    if o is not None:
+        _dense("o", o, (N, H, dv), dtype)
+    device = _same_gpu(q, k, v, g, state_pool, state_idx, o, workspace)
+    if o is None:
+        o = _new(q, (N, H, dv), dtype, stream)
+    wa, wb = None, 0
+    if workspace is not None or check:
+        workspace, wa, wb = _workspace(q, lib.kda_decode_workspace_size(), workspace, stream)
+    rc = lib.kda_la_decode_step_indexed(q.data_ptr(), k.data_ptr(), v.data_ptr(), ga, sa, xa, P_,
+                                        o.data_ptr(), N, H, Hk, dk, dv, _DT[dtype], qs, ks, vs, gpt,
+                                        wa, wb, _raw_stream(stream, device))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_la_decode_step_indexed")
     if check:
@@ -561,41 +597,42 @@ def qk_norm_rope(q, k, positions, inv_freq, *, norm: str = "l2", layout: str = "
     fp32 or None.  q_out and k_out may be q and k (in place); by default new packed tensors
     are returned.
     """
-    lib = load()
-    if q.dim() != 3 or q.dtype not in _DT:
+    lib = _lib or load()
+    dtype = q.dtype
+    if q.dim() != 3 or dtype not in _DT:
         raise TypeError("q must be [T, Hq, D], fp32 or bf16")
     if norm not in _NORM or layout not in _LAYOUT:
         raise ValueError(f"unknown norm {norm!r} or layout {layout!r}")
     T, Hq, D = q.shape
-    qs, ks, kos, Hk = _rows("q", q, T, Hq, D, q.dtype), 0, 0, 0
+    qs, ks, kos, Hk = _rows("q", q, T, Hq, D, dtype), 0, 0, 0
     if k is not None:
         Hk = k.shape[1] if k.dim() == 3 else 0
-        ks = _rows("k", k, T, Hk, D, q.dtype)
+        ks = _rows("k", k, T, Hk, D, dtype)
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq come together")
-    rot = 0
+    rot, pa, fa, qwa, kwa = 0, None, None, None, None
     if inv_freq is not None:
-        _expect("positions", positions, (T,), torch.int32)
-        _expect("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32)
+        pa = _dense("positions", positions, (T,), torch.int32)
+        fa = _dense("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32)
         rot = 2 * inv_freq.numel()
-    _expect("q_weight", q_weight, (D,), torch.float32)
-    _expect("k_weight", k_weight, (D,), torch.float32)
-    _on_gpu(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
-    _check_cuda(positions, inv_freq, q_weight, k_weight)
-    with _allocating(stream):
-        if q_out is None:
-            q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(T, Hk, D, dtype=q.dtype, device=q.device)
-    qos = _rows("q_out", q_out, T, Hq, D, q.dtype)
+    if q_weight is not None:
+        qwa = _dense("q_weight", q_weight, (D,), torch.float32)
+    if k_weight is not None:
+        kwa = _dense("k_weight", k_weight, (D,), torch.float32)
+    device = _same_gpu(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    if q_out is None:
+        q_out = _new(q, (T, Hq, D), dtype, stream)
+    qos = _rows("q_out", q_out, T, Hq, D, dtype)
     if k is not None:
-        kos = _rows("k_out", k_out, T, Hk, D, q.dtype)
-    rc = lib.kda_qk_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), T, Hq, Hk, D,
-                              _DT[q.dtype], qs, ks, qos, kos, _ptr(q_weight), _ptr(k_weight),
-                              _NORM[norm], eps, q_scale, k_scale, _ptr(positions),
-                              _ptr(inv_freq), rot, _LAYOUT[layout], rope_scale, _stream(stream))
+        if k_out is None:
+            k_out = _new(q, (T, Hk, D), dtype, stream)
+        kos = _rows("k_out", k_out, T, Hk, D, dtype)
+    rc = lib.kda_qk_norm_rope(q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out), T, Hq, Hk, D,
+                              _DT[dtype], qs, ks, qos, kos, qwa, kwa, _NORM[norm], eps, q_scale,
+                              k_scale, pa, fa, rot, _LAYOUT[layout], rope_scale,
+                              _raw_stream(stream, device))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_qk_norm_rope")
     return q_out, k_out
@@ -604,7 +641,10 @@ def qk_norm_rope(q, k, positions, inv_freq, *, norm: str = "l2", layout: str = "
 def _check_pool(pool):
     if pool.dim() < 2 or pool.dtype != torch.float32:
         raise TypeError("a state pool is [P, ...] fp32")
-    return pool.shape[0], pool[0].numel() if pool.shape[0] else 4
+    if not pool.is_contiguous():
+        raise ValueError("the pool must be contiguous")
+    slots = pool.shape[0]
+    return slots, pool.numel() // slots if slots else 4
 
 
 def state_pool_copy(pool, src_idx, dst_idx, *, workspace=None, stream=None, check: bool = False):
@@ -613,20 +653,19 @@ def state_pool_copy(pool, src_idx, dst_idx, *, workspace=None, stream=None, chec
     named twice or be another copy's source; copies that break this or leave the pool are
     left out, and recorded in the workspace's status word when there is one (check=True
     raises)."""
-    lib = load()
+    lib = _lib or load()
     slots, elems = _check_pool(pool)
     if src_idx.dim() != 1:
         raise ValueError("src_idx must be [n]")
-    _expect("src_idx", src_idx, (src_idx.numel(),), torch.int32)
-    _expect("dst_idx", dst_idx, (src_idx.numel(),), torch.int32)
-    _on_gpu(pool, src_idx, dst_idx, workspace)
-    _check_cuda(pool, src_idx, dst_idx, workspace)
-    if workspace is None and check:
-        with _allocating(stream):
-            workspace = alloc_workspace(int(lib.kda_decode_workspace_size()), pool.device)
-    rc = lib.kda_state_pool_copy(_ptr(pool), slots, elems, _ptr(src_idx), _ptr(dst_idx),
-                                 src_idx.numel(), _ptr(workspace), _nbytes(workspace),
-                                 _stream(stream))
+    n = src_idx.numel()
+    sa = _dense("src_idx", src_idx, (n,), torch.int32)
+    da = _dense("dst_idx", dst_idx, (n,), torch.int32)
+    device = _same_gpu(pool, src_idx, dst_idx, workspace)
+    wa, wb = None, 0
+    if workspace is not None or check:
+        workspace, wa, wb = _workspace(pool, lib.kda_decode_workspace_size(), workspace, stream)
+    rc = lib.kda_state_pool_copy(pool.data_ptr(), slots, elems, sa, da, n, wa, wb,
+                                 _raw_stream(stream, device))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_state_pool_copy")
     if check:
@@ -637,25 +676,24 @@ def state_pool_compact(pool, live, *, new_index=None, n_live=None, workspace=Non
     """Packs the live slots of a pool to its front with the fewest moves
     (kda_state_pool_compact).  live [P] bool or uint8.  Returns (new_index [P] int32: where
     each live slot is now, -1 for dead ones; n_live [1] int32), both on the device."""
-    lib = load()
+    lib = _lib or load()
     slots, elems = _check_pool(pool)
     if live.dtype not in (torch.bool, torch.uint8):
         raise TypeError(f"live has dtype {live.dtype}, expected bool or uint8")
-    _expect("live", live, (slots,))
-    _expect("new_index", new_index, (slots,), torch.int32)
-    _expect("n_live", n_live, (1,), torch.int32)
-    _on_gpu(pool, live, new_index, n_live, workspace)
-    _check_cuda(pool, live, new_index, n_live, workspace)
-    with _allocating(stream):
-        if new_index is None:
-            new_index = torch.empty(slots, dtype=torch.int32, device=pool.device)
-        if n_live is None:
-            n_live = torch.empty(1, dtype=torch.int32, device=pool.device)
-        if workspace is None:
-            workspace = alloc_workspace(int(lib.kda_state_pool_workspace_size(slots)), pool.device)
-    rc = lib.kda_state_pool_compact(_ptr(pool), slots, elems, _ptr(live), _ptr(new_index),
-                                    _ptr(n_live), _ptr(workspace), _nbytes(workspace),
-                                    _stream(stream))
+    la = _dense("live", live, (slots,), live.dtype)
+    if new_index is not None:
+        _dense("new_index", new_index, (slots,), torch.int32)
+    if n_live is not None:
+        _dense("n_live", n_live, (1,), torch.int32)
+    device = _same_gpu(pool, live, new_index, n_live, workspace)
+    if new_index is None:
+        new_index = _new(pool, (slots,), torch.int32, stream)
+    if n_live is None:
+        n_live = _new(pool, (1,), torch.int32, stream)
+    need = lib.kda_state_pool_workspace_size(slots) if workspace is None else 0
+    workspace, wa, wb = _workspace(pool, need, workspace, stream)
+    rc = lib.kda_state_pool_compact(pool.data_ptr(), slots, elems, la, new_index.data_ptr(),
+                                    n_live.data_ptr(), wa, wb, _raw_stream(stream, device))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_state_pool_compact")
     return new_index, n_live
