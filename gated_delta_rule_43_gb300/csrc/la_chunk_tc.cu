@@ -5,8 +5,9 @@
 //   P  = (Q K^T) * exp(G_t - G_s) for s <= t, else 0
 //   O  = P V + exp(G_t) Q S
 //   S' = exp(G_C) S + K~^T V,     K~_s = exp(g_{s+1} + ... + g_C) k_s
-// Four products of 128 x 128 x 128 a chunk: 131 kflop a token and head against 1 KB of q, k,
-// v and o, so that a walk at the memory's rate keeps the tensor cores 40% busy.
+// Five products of 128 x 128 x 128 a chunk (K~ counts twice): 164 kflop a token and head
+// against 1 KB of q, k, v and o, half of what the tensor cores do in the time that the memory
+// takes.
 //
 // Roundings.  q, k, v are bf16 as they come.  P and the copy of S that meets the queries are
 // rounded to bf16, like the output they go into.  The state that is carried on is not: K~ is
@@ -21,14 +22,17 @@
 //
 // One CTA an SM walks its range (see kda_la.cuh), every role for itself through the same
 // items and chunks:
-//   warps 0-3    rows of P (tensor memory, as the A operand of P V), rows of O (through
-//                shared memory, over the image of S, in one bulk store: rows stored straight
-//                from registers cost 2k cycles a chunk and held up everyone's shared memory)
-//   warps 4-11   K~ (over K and Q, whose products are done by then), and the state: thread
-//                (row, half) holds its columns of S
+//   warps 0-3    rows of P (tensor memory, as the A operand of P V) and of O (through shared
+//                memory, over the chunk's Q, in one bulk store: rows stored straight from
+//                registers cost 2k cycles a chunk and held up everyone's shared memory)
+//   warps 4-11   K~^T (read transposed, weighted and split into tensor memory as the A operand
+//                of K~^T V) and the state: thread (row, half) holds its columns of S
 //   warp 12      issues the products          warp 13   loads q, k, v (two stages)
 //   warp 14      the chunk's decays, one chunk ahead
-// 96 KB a stage and the 32 KB image of S fill the SM's shared memory.
+// A start state is loaded through a stage of its own, so it is there when the item begins.
+// 96 KB a stage and the 32 KB image of S fill the SM's shared memory; scores / P, O, K~^T V and
+// K~^T (hi, lo) fill its tensor memory.  Loops stay loops: the roles' code shares one
+// instruction cache (unrolled, a chunk took 13k cycles).
 #include <cuda.h>
 
 #include <mutex>
@@ -56,33 +60,41 @@ struct Gates {
 };
 
 enum Bar {
-    kFull = 0,      // [2] a stage's tiles have landed
-    kGate = 2,      // [2] a stage's decays are there
-    kGateFree = 4,  // [2] ... and have been used
-    kKvDone = 6,    // [2] K~^T V, and with it every product that reads the stage
-    kPvDone = 8,    // [2] P V
-    kQkDone = 10,   // Q K^T
-    kQsDone = 11,   // Q S
-    kPReady = 12,   // P is in tensor memory
-    kKtReady = 13,  // K~ is in shared memory
-    kSReady = 14,   // the image of S is
-    kOFree = 15,    // the accumulators of O have been read
-    kSFree = 16,    // the outputs that lay over the image of S have left
-    kDrain = 17,
-    kBars = 18
+    kFull = 0,       // [2] a stage's tiles (or a start state) have landed
+    kFree = 2,       // [2] a stage may be loaded again: products and outputs are done with it
+    kGate = 4,       // [2] a chunk's decays are there
+    kGateFree = 6,   // [2] ... and have been used
+    kQkDone = 8,     // Q K^T
+    kQsDone = 9,     // Q S
+    kPvDone = 10,    // P V
+    kKvDone = 11,    // K~^T V
+    kPReady = 12,    // P and the decayed Q S are in tensor memory
+    kKtReady = 13,   // K~^T is
+    kSReady = 14,    // the image of S is in shared memory
+    kOFree = 15,     // the accumulator of O has been read
+    kDrain = 16,
+    kBars = 17
 };
 
 template <int DKP, int DVP> struct Map {
     static constexpr uint32_t kQ = 0, kK = DKP * 256, kV = 2 * DKP * 256;   // within a stage
     static constexpr uint32_t kStage = kV + DVP * 256;
     static constexpr uint32_t kS = 2 * kStage;                 // S image, [DKP rows][DVP]
-    static constexpr uint32_t kGates = kS + C * DVP * 2;       // ... or a chunk's outputs, [C][DVP]
+    // a chunk's outputs, [C][DVP]: over its Q where they fit
+    static constexpr bool kOverQ = DVP <= DKP;
+    static constexpr uint32_t kO = kS + DKP * DVP * 2;
+    static constexpr uint32_t kGates = kO + (kOverQ ? 0 : C * DVP * 2);
     static constexpr uint32_t kTot = kGates + 2 * sizeof(Gates);   // decay of the chunk, [2]
     static constexpr uint32_t kBar = kTot + 8;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 8;
-    static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kStage % 1024 == 0 && kBytes <= 232448, "layout");
+    // a start state in a stage: rows padded so that lanes reading rows miss no bank twice
+    static constexpr uint32_t kRow = DVP * 4 + 16;
+    static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kStage % 1024 == 0 && kO % 1024 == 0 &&
+                      kBytes <= 232448 && DKP * kRow <= kStage,
+                  "layout");
 };
 
+// A in tensor memory (lane = row, column c = K elements 2 c and 2 c + 1)
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                              uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -92,20 +104,38 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// 16 consecutive columns of the warp's 32 lanes
+#define KDA_R16(r)                                                                              \
+    "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),     \
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+// the warp's 32 lanes, 16 consecutive columns: thread = lane
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
         "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-          "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-          "r"(r[14]), "r"(r[15])
+        ::"r"(taddr), KDA_R16(r)
         : "memory");
 }
+// 16 lanes, 32 consecutive columns: register 2 i + j of thread t is lane t / 4 + 8 j, column
+// 4 i + t % 4
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), KDA_R16(r)
+        : "memory");
+}
+#undef KDA_R16
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-
+// Four 8 x 8 blocks of 16-bit values, transposed: thread t gets row t / 4, columns 2 (t % 4)
+// and the next, of each
+__device__ __forceinline__ void ldmatrix_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 // shared -> global through a tensor map (full boxes; what lies outside the tensor is dropped)
 __device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, int32_t c0,
                                              int32_t c1, int32_t c2) {
@@ -113,15 +143,31 @@ __device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, 
                  ::"l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
                  : "memory");
 }
+// 32 bytes to a 32-byte aligned address
+__device__ __forceinline__ void store8(float *dst, const float *x) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(x[0]),
+                 "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+__device__ __forceinline__ void arrive_n(uint64_t *bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
+                 : "memory");
+}
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&x);
 }
-__device__ __forceinline__ float2 unpack2(uint32_t u) {
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
+// two products in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
-
 // 2^x by the special-function unit (relative error near 2^-22)
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -130,11 +176,12 @@ __device__ __forceinline__ float ex2(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The parts of w x: x two bf16, hi the product rounded to bf16, lo the rounded rest.
-__device__ __forceinline__ void split2(uint32_t x, float w, uint32_t &hi, uint32_t &lo) {
-    const float a0 = w * __uint_as_float(x << 16), a1 = w * __uint_as_float(x & 0xffff0000u);
-    hi = pack2(a0, a1);
-    lo = pack2(a0 - __uint_as_float(hi << 16), a1 - __uint_as_float(hi & 0xffff0000u));
+// x: two bf16 of successive tokens, w their weights; hi = w x rounded to bf16, lo the rounded
+// rest
+__device__ __forceinline__ void split2(uint32_t x, float2 w, uint32_t &hi, uint32_t &lo) {
+    const float2 a = mul2(w, make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)));
+    hi = pack2(a.x, a.y);
+    lo = pack2(a.x - __uint_as_float(hi << 16), a.y - __uint_as_float(hi & 0xffff0000u));
 }
 
 // Waits that end: after kWaitNs, or when another role of the CTA has given up.
@@ -148,6 +195,10 @@ struct Waits {
             if (mbar_try_wait(&bar[which], parity)) return true;
             if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > kWaitNs)) return false;
         }
+    }
+    // the same for a whole warp
+    __device__ __forceinline__ bool warp(int which, uint32_t parity) const {
+        return __all_sync(0xffffffffu, (*this)(which, parity));
     }
 };
 
@@ -176,26 +227,27 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         if (tid == 0) report(st, KDA_ERR_CUDA, 0, 40);
         return;
     }
+    constexpr uint32_t kReleases = OUT ? 2 : 1;   // of a stage: products, outputs
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bar[kFull + b], 1);
+            mbar_init(&bar[kFree + b], kReleases);
             mbar_init(&bar[kGate + b], 1);
             mbar_init(&bar[kGateFree + b], kStateWarps + (OUT ? kRowWarps : 0));
-            mbar_init(&bar[kKvDone + b], 1);
-            mbar_init(&bar[kPvDone + b], 1);
         }
         mbar_init(&bar[kQkDone], 1);
         mbar_init(&bar[kQsDone], 1);
+        mbar_init(&bar[kPvDone], 1);
+        mbar_init(&bar[kKvDone], 1);
         mbar_init(&bar[kPReady], kRowWarps);
         mbar_init(&bar[kKtReady], kStateWarps);
         mbar_init(&bar[kSReady], kStateWarps);
         mbar_init(&bar[kOFree], kRowWarps);
-        mbar_init(&bar[kSFree], 1);
         mbar_init(&bar[kDrain], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    constexpr uint32_t kCols = OUT ? 512 : 128;
+    constexpr uint32_t kCols = OUT ? 512 : 256;
     if (warp == kMmaWarp) {
         tmem_alloc(tslot, kCols);
         tmem_relinquish();
@@ -204,14 +256,12 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    // scores (then P), Q S, P V, K~^T V
-    const uint32_t tA = tmem, tQS = tmem + 128, tPV = tmem + 256, tKV = OUT ? tmem + 384 : tmem;
+    const uint32_t tHi = tmem, tLo = tmem + 64, tKV = tmem + 128, tA = tmem + 256, tO = tmem + 384;
     const Waits wait{bar, abort_flag};
     const int64_t dkdv = (int64_t)dk * dv;
-    const int group = p.H / p.Hk;
-    uint32_t gi = 0;    // chunks so far: stage gi & 1, phase parities
+    uint32_t gi = 0;    // chunks so far: parities of what happens once a chunk
+    uint32_t si = 0;    // stages so far (chunks and start states)
     bool ok = true;
-    uint32_t loaded = 0, landed = 0;   // (load warp)
 
     Item it;
     Walk walk(p, range);
@@ -219,22 +269,22 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     for (; more && ok; more = OUT && walk.next(it)) {
         const int h = it.h;
         const int chunks = it.c1 - it.c0;
+        const float *start = OUT ? start_state(p, it, range, h0, bnd, dkdv) : nullptr;
+        const uint32_t first_si = si;   // a start state's stage
+        if (start) ++si;
 
         if (warp < kRowWarps) {
             if (!OUT) continue;
             const int t = tid;   // this thread's row of the chunk
             const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-            for (int c = 0; c < chunks; ++c, ++gi) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
+            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
                 const int64_t t0 = it.t0 + (int64_t)c * C;
-                ok = __all_sync(0xffffffffu, wait(kGate + b, ph) && wait(kQkDone, gi & 1));
-                float eG = 0.f;
+                ok = wait.warp(kGate + b, ph) && wait.warp(kQkDone, gi & 1);
                 if (ok) {
                     tc_fence_after();
                     const Gates &G = gates[b];
                     const float Gt = G.G[t];
-                    eG = ex2(Gt);
-                    // (loops that stay loops: the roles' code shares one instruction cache)
 #pragma unroll 1
                     for (int cb = 0; cb < 4; ++cb) {
                         uint32_t pk[16];
@@ -243,12 +293,17 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                             tmem_ld32(tA + lanes + 32 * cb, a);
                             tmem_ld_wait();
                             if (cb < warp) {
-                                const float rf = ex2(Gt - G.G[32 * cb + 31]);
+                                const float r = ex2(Gt - G.G[32 * cb + 31]);
+                                const float2 rf = make_float2(r, r);
 #pragma unroll
                                 for (int j = 0; j < 32; j += 4) {
                                     const float4 f = *reinterpret_cast<const float4 *>(&G.cf[32 * cb + j]);
-                                    pk[j / 2] = pack2(a[j] * (rf * f.x), a[j + 1] * (rf * f.y));
-                                    pk[j / 2 + 1] = pack2(a[j + 2] * (rf * f.z), a[j + 3] * (rf * f.w));
+                                    const float2 x = mul2(make_float2(a[j], a[j + 1]),
+                                                          mul2(rf, make_float2(f.x, f.y)));
+                                    const float2 y = mul2(make_float2(a[j + 2], a[j + 3]),
+                                                          mul2(rf, make_float2(f.z, f.w)));
+                                    pk[j / 2] = pack2(x.x, x.y);
+                                    pk[j / 2 + 1] = pack2(y.x, y.y);
                                 }
                             } else {
 #pragma unroll
@@ -267,34 +322,53 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         // (columns of scores that this warp has read)
                         tmem_st16(tA + lanes + 16 * cb, pk);
                     }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&bar[kPReady]);
-                        mbar_arrive(&bar[kGateFree + b]);
+                    ok = wait.warp(kQsDone, gi & 1);
+                    if (ok) {   // P V adds to exp(G_t) Q S
+                        tc_fence_after();
+                        const float e = ex2(Gt);
+                        const float2 eG = make_float2(e, e);
+#pragma unroll 1
+                        for (int j0 = 0; j0 < DVP; j0 += 16) {
+                            float x[16];
+                            uint32_t y[16];
+                            tmem_ld16(tO + lanes + j0, x);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; j += 2) {
+                                const float2 z = mul2(eG, make_float2(x[j], x[j + 1]));
+                                y[j] = __float_as_uint(z.x);
+                                y[j + 1] = __float_as_uint(z.y);
+                            }
+                            tmem_st16(tO + lanes + j0, y);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bar[kPReady]);
+                            mbar_arrive(&bar[kGateFree + b]);
+                        }
+                        ok = wait.warp(kPvDone, gi & 1);
                     }
-                    ok = __all_sync(0xffffffffu, wait(kPvDone + b, ph));
                 }
                 // these warps stop together: the barriers below have no time limit
                 ok = bar_and(2, 32 * kRowWarps, ok);
                 if (!ok) break;
                 tc_fence_after();
-                // the outputs over the image of S, which Q S was the last to read
+                uint8_t *so = sm + (M::kOverQ ? sb * M::kStage + M::kQ : M::kO);
 #pragma unroll 1
                 for (int cb = 0; cb < DVP / 32; ++cb) {
-                    float x[32], y[32];
-                    tmem_ld32(tQS + lanes + 32 * cb, x);
-                    tmem_ld32(tPV + lanes + 32 * cb, y);
+                    float x[32];
+                    tmem_ld32(tO + lanes + 32 * cb, x);
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
                         uint4 u;
-                        u.x = pack2(eG * x[j] + y[j], eG * x[j + 1] + y[j + 1]);
-                        u.y = pack2(eG * x[j + 2] + y[j + 2], eG * x[j + 3] + y[j + 3]);
-                        u.z = pack2(eG * x[j + 4] + y[j + 4], eG * x[j + 5] + y[j + 5]);
-                        u.w = pack2(eG * x[j + 6] + y[j + 6], eG * x[j + 7] + y[j + 7]);
-                        *reinterpret_cast<uint4 *>(sm + M::kS + sw128_offset(t, 32 * cb + j, C)) = u;
+                        u.x = pack2(x[j], x[j + 1]);
+                        u.y = pack2(x[j + 2], x[j + 3]);
+                        u.z = pack2(x[j + 4], x[j + 5]);
+                        u.w = pack2(x[j + 6], x[j + 7]);
+                        *reinterpret_cast<uint4 *>(so + sw128_offset(t, 32 * cb + j, C)) = u;
                     }
                 }
                 tc_fence_before();
@@ -307,7 +381,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     if (tid == 0) {
 #pragma unroll
                         for (int x = 0; x < DVP / 64; ++x)
-                            tma_store_3d(&to, sm + M::kS + x * 16384, 64 * x, h, (int32_t)t0);
+                            tma_store_3d(&to, so + x * 16384, 64 * x, h, (int32_t)t0);
                         bulk_commit();
                         bulk_wait_read_all();
                     }
@@ -316,33 +390,43 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     for (int x = tid; x < len * per; x += 32 * kRowWarps) {
                         const int r = x / per, j = 8 * (x - r * per);
                         *reinterpret_cast<uint4 *>(o + ((t0 + r) * p.H + h) * (int64_t)dv + j) =
-                            *reinterpret_cast<const uint4 *>(sm + M::kS + sw128_offset(r, j, C));
+                            *reinterpret_cast<const uint4 *>(so + sw128_offset(r, j, C));
                     }
+                    fence_proxy_async();   // before the stage is loaded again
                     named_bar_sync(1, 32 * kRowWarps);
                 }
-                if (tid == 0) mbar_arrive(&bar[kSFree]);
+                if (tid == 0) mbar_arrive(&bar[kFree + sb]);
+                if (!M::kOverQ) named_bar_sync(1, 32 * kRowWarps);   // kO is written next chunk
             }
         } else if (warp < kRowWarps + kStateWarps) {
             constexpr int NC = DVP / 2;
-            const int bt = tid - 32 * kRowWarps;
-            const int half = bt >> 7, r = bt & 127;           // token row and half of its channels
-            const int i = 32 * (warp & 3) + lane;             // state row, columns j0 ..
-            const int j0 = NC * ((warp - kRowWarps) >> 2);
-            const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+            const int quarter = warp & 3, half = (warp - kRowWarps) >> 2;
+            const int i = 32 * quarter + lane;                // state row, columns j0 ..
+            const int j0 = NC * half;
+            const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
             const bool mine = i < dk && j0 < dv;
-            const int64_t at = (int64_t)i * dv + j0;
             float S[NC];
-            const float *start = OUT ? start_state(p, it, range, h0, bnd, dkdv) : nullptr;
 #pragma unroll
-            for (int j = 0; j < NC; j += 4) {
-                const float4 x = start && mine ? *reinterpret_cast<const float4 *>(start + at + j)
-                                               : make_float4(0.f, 0.f, 0.f, 0.f);
-                S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+            for (int j = 0; j < NC; ++j) S[j] = 0.f;
+            // These warps stop together too: each failure is carried to the next bar_and.
+            if (start) {
+                const uint32_t sb = first_si & 1;
+                ok = wait.warp(kFull + sb, (first_si >> 1) & 1);
+                if (ok && mine) {
+                    const uint8_t *row = sm + sb * M::kStage + i * M::kRow + j0 * 4;
+#pragma unroll
+                    for (int j = 0; j < NC; j += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(row + 4 * j);
+                        S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+                    }
+                }
+                ok = bar_and(3, 32 * kStateWarps, ok);
+                if (!ok) break;
+                if (tid == 32 * kRowWarps) arrive_n(&bar[kFree + sb], kReleases);
             }
-            // the image of S for chunk number `gn`, once the outputs of the one before have left
+            // the image of S for chunk number `gn`; Q S of the one before has read the old one
             auto put_image = [&](uint32_t gn) {
-                const bool free = gn == 0 || wait(kSFree, (gn - 1) & 1);
-                if (!__all_sync(0xffffffffu, free)) return false;
+                if (gn > 0 && !wait.warp(kQsDone, (gn - 1) & 1)) return false;
                 if (i < DKP) {
 #pragma unroll
                     for (int j = 0; j < NC; j += 8) {
@@ -359,53 +443,66 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 if (lane == 0) mbar_arrive(&bar[kSReady]);
                 return true;
             };
-            if (OUT) ok = put_image(gi);
-            for (int c = 0; c < chunks && ok; ++c, ++gi) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
+            bool fine = !OUT || put_image(gi);
+            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
                 const int len = (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)c * C);
-                uint8_t *stage = sm + b * M::kStage;
-                // K and Q are read by Q K^T and Q S; after these K~ takes their place
-                ok = wait(kGate + b, ph) && wait(kFull + b, ph) && (!OUT || wait(kQsDone, gi & 1));
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                const float w = gates[b].w[r];
-                const float decay = tot[b];
-                constexpr int UK = DKP / 16, UV = DVP / 16;   // 16-byte pieces of a thread
+                uint8_t *stage = sm + sb * M::kStage;
+                fine = fine && wait.warp(kGate + b, ph) && wait.warp(kFull + sb, (si >> 1) & 1);
+                float decay = 0.f;
+                if (fine) {
+                    // K~^T: channels of this warp's quarter, tokens of its half, in blocks of
+                    // 16 x 16.  (K~^T V of the chunk before has been waited for.)
+                    decay = tot[b];
+                    const float *w = gates[b].w + 64 * half;
+                    if (32 * quarter < DKP) {
 #pragma unroll 1
-                for (int u = 0; u < UK; u += 4) {   // four in flight
-                    uint4 x[4];
+                        for (int cg = 0; cg < 32; cg += 16) {
+                            uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        x[m] = *reinterpret_cast<const uint4 *>(
-                            stage + M::kK + sw128_offset(r, 8 * (half * UK + u + m), C));
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-                        if (r < len) {
-                            split2(x[m].x, w, hi.x, lo.x);
-                            split2(x[m].y, w, hi.y, lo.y);
-                            split2(x[m].z, w, hi.z, lo.z);
-                            split2(x[m].w, w, hi.w, lo.w);
+                            for (int tg = 0; tg < 4; ++tg) {
+                                const int s = 16 * tg + 2 * (lane & 3);   // and s + 1, s + 8, s + 9
+                                uint32_t x[4];
+                                ldmatrix_t(smem_u32(stage + M::kK) +
+                                               sw128_offset(64 * half + 16 * tg + (lane >> 4) * 8 + (lane & 7),
+                                                            32 * quarter + cg + ((lane >> 3) & 1) * 8, C),
+                                           x);
+                                if (len < C) {   // tokens past the segment count as zeros
+                                    const int at = 64 * half + s;
+                                    const uint32_t m0 = (at < len ? 0xffffu : 0u) | (at + 1 < len ? 0xffff0000u : 0u);
+                                    const uint32_t m1 = (at + 8 < len ? 0xffffu : 0u) | (at + 9 < len ? 0xffff0000u : 0u);
+                                    x[0] &= m0; x[1] &= m0; x[2] &= m1; x[3] &= m1;
+                                }
+                                const float2 w0 = *reinterpret_cast<const float2 *>(w + s);
+                                const float2 w1 = *reinterpret_cast<const float2 *>(w + s + 8);
+                                split2(x[0], w0, hi[4 * tg], lo[4 * tg]);
+                                split2(x[1], w0, hi[4 * tg + 1], lo[4 * tg + 1]);
+                                split2(x[2], w1, hi[4 * tg + 2], lo[4 * tg + 2]);
+                                split2(x[3], w1, hi[4 * tg + 3], lo[4 * tg + 3]);
+                            }
+                            const uint32_t at = lanes + ((uint32_t)cg << 16) + 32 * half;
+                            tmem_st_16x32(tHi + at, hi);
+                            tmem_st_16x32(tLo + at, lo);
                         }
-                        const uint32_t off = sw128_offset(r, 8 * (half * UK + u + m), C);
-                        *reinterpret_cast<uint4 *>(stage + M::kK + off) = hi;
-                        *reinterpret_cast<uint4 *>(stage + M::kQ + off) = lo;
+                        tmem_st_wait();
                     }
+                    if (len < C) {   // their rows of V must not meet the zeros of P and K~
+                        constexpr int U = DVP / 8;   // 16-byte pieces of a row
+                        for (int x = len * U + (tid - 32 * kRowWarps); x < C * U; x += 32 * kStateWarps)
+                            *reinterpret_cast<uint4 *>(stage + M::kV + sw128_offset(x / U, 8 * (x % U), C)) =
+                                make_uint4(0, 0, 0, 0);
+                        fence_proxy_async();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bar[kKtReady]);
+                        mbar_arrive(&bar[kGateFree + b]);
+                    }
+                    fine = wait.warp(kKvDone, gi & 1);
                 }
-                if (r >= len) {   // rows of other sequences must not meet the zeros of P and K~
-#pragma unroll 1
-                    for (int u = 0; u < UV; ++u)
-                        *reinterpret_cast<uint4 *>(stage + M::kV +
-                                                   sw128_offset(r, 8 * (half * UV + u), C)) =
-                            make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bar[kKtReady]);
-                    mbar_arrive(&bar[kGateFree + b]);
-                }
-                ok = wait(kKvDone + b, ph);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                ok = bar_and(3, 32 * kStateWarps, fine);
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int jb = 0; jb < NC; jb += 32) {
@@ -416,36 +513,39 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     for (int j = 0; j < 32; ++j) S[jb + j] = decay * S[jb + j] + x[j];
                 }
                 tc_fence_before();
-                if (OUT && c + 1 < chunks) ok = put_image(gi + 1);
+                if (OUT && c + 1 < chunks) fine = put_image(gi + 1);
             }
             float *dst = OUT ? (it.c1 == it.nc && hT ? hT + ((int64_t)it.n * p.H + h) * dkdv
                                                      : nullptr)
                              : bnd + cut_state(range + 1) * dkdv;
             if (ok && dst && mine) {
+                float *row = dst + (int64_t)i * dv + j0;
+                if (((uintptr_t)dst & 31) == 0) {   // (a state buffer is 16-byte aligned)
 #pragma unroll
-                for (int j = 0; j < NC; j += 4)
-                    *reinterpret_cast<float4 *>(dst + at + j) =
-                        make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+                    for (int j = 0; j < NC; j += 8) store8(row + j, S + j);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NC; j += 4)
+                        *reinterpret_cast<float4 *>(row + j) =
+                            make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+                }
             }
         } else if (warp == kMmaWarp) {
             const uint32_t id_kk = idesc_bf16(128, 128, false, false);   // Q K^T
-            const uint32_t id_km = idesc_bf16(128, DVP, false, true);    // Q S, P V
-            const uint32_t id_mm = idesc_bf16(128, DVP, true, true);     // K~^T V
-            for (int c = 0; c < chunks; ++c, ++gi) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
-                const int len = (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)c * C);
-                const uint32_t stage = base + b * M::kStage;
+            const uint32_t id_km = idesc_bf16(128, DVP, false, true);    // the others: B is V or S
+            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
+                const uint32_t sb = si & 1;
+                const uint32_t stage = base + sb * M::kStage;
                 const uint64_t dq = sdesc_sw128(stage + M::kQ, 16, 1024);
                 const uint64_t dkk = sdesc_sw128(stage + M::kK, 16, 1024);
-                // token-major tiles as operands whose K dimension is the token
-                const uint64_t dkt = sdesc_sw128(stage + M::kK, C * 128, 1024);
-                const uint64_t dlo = sdesc_sw128(stage + M::kQ, C * 128, 1024);
+                // token-major V and channel-major S: the K dimension is the row
                 const uint64_t dvt = sdesc_sw128(stage + M::kV, C * 128, 1024);
                 const uint64_t ds = sdesc_sw128(base + M::kS, DKP * 128, 1024);
                 if (OUT) {
-                    ok = wait(kFull + b, ph) &&
-                         (gi == 0 || wait(kPvDone + (b ^ 1), ((gi - 1) >> 1) & 1));
-                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    // P of the chunk before lies over the scores
+                    ok = wait.warp(kFull + sb, (si >> 1) & 1) &&
+                         (gi == 0 || wait.warp(kPvDone, (gi - 1) & 1));
+                    if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -455,54 +555,66 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         umma_commit(&bar[kQkDone]);
                     }
                     __syncwarp();
-                    ok = wait(kSReady, gi & 1) && (gi == 0 || wait(kOFree, (gi - 1) & 1));
-                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    ok = wait.warp(kSReady, gi & 1) && (gi == 0 || wait.warp(kOFree, (gi - 1) & 1));
+                    if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int s = 0; s < DKP / 16; ++s)
-                            umma_bf16(tQS, desc_add(dq, (s >> 2) * 16384 + (s & 3) * 32),
+                            umma_bf16(tO, desc_add(dq, (s >> 2) * 16384 + (s & 3) * 32),
                                       desc_add(ds, s * 2048), id_km, s > 0);
                         umma_commit(&bar[kQsDone]);
                     }
                     __syncwarp();
-                    // (the rows of V past the segment are cleared together with K~)
-                    ok = wait(kPReady, gi & 1) && (len == C || wait(kKtReady, gi & 1));
-                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int s = 0; s < C / 16; ++s)
-                            umma_bf16_ts(tPV, tA + 8 * s, desc_add(dvt, s * 2048), id_km, s > 0);
-                        umma_commit(&bar[kPvDone + b]);
-                    }
-                    __syncwarp();
                 }
-                ok = wait(kKtReady, gi & 1);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                ok = wait.warp(kKtReady, gi & 1) && wait.warp(kFull + sb, (si >> 1) & 1);
+                if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < C / 16; ++s)
-                        umma_bf16(tKV, desc_add(dkt, s * 2048), desc_add(dvt, s * 2048), id_mm, s > 0);
+                        umma_bf16_ts(tKV, tHi + 8 * s, desc_add(dvt, s * 2048), id_km, s > 0);
 #pragma unroll
                     for (int s = 0; s < C / 16; ++s)
-                        umma_bf16(tKV, desc_add(dlo, s * 2048), desc_add(dvt, s * 2048), id_mm, 1);
-                    umma_commit(&bar[kKvDone + b]);
+                        umma_bf16_ts(tKV, tLo + 8 * s, desc_add(dvt, s * 2048), id_km, 1);
+                    umma_commit(&bar[kKvDone]);
+                    if (!OUT) umma_commit(&bar[kFree + sb]);
                 }
                 __syncwarp();
+                if (OUT) {
+                    ok = wait.warp(kPReady, gi & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int s = 0; s < C / 16; ++s)
+                            umma_bf16_ts(tO, tA + 8 * s, desc_add(dvt, s * 2048), id_km, 1);
+                        umma_commit(&bar[kPvDone]);
+                        umma_commit(&bar[kFree + sb]);
+                    }
+                    __syncwarp();
+                }
             }
         } else if (warp == kLoadWarp) {
-            const int hk = h / group;
-            for (int c = 0; c < chunks; ++c, ++gi) {
-                const uint32_t b = gi & 1;
-                if (gi >= 2) {
-                    ok = wait(kKvDone + b, ((gi - 2) >> 1) & 1);
-                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                }
+            const int hk = h / (p.H / p.Hk);
+            if (start) {
+                const uint32_t sb = first_si & 1;
+                if (first_si >= 2) ok = wait.warp(kFree + sb, ((first_si - 2) >> 1) & 1);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&bar[kFull + sb], (uint32_t)dkdv * 4);
+                __syncwarp();
+                for (int r = lane; r < dk; r += 32)
+                    bulk_g2s(sm + sb * M::kStage + r * M::kRow, start + (int64_t)r * dv, dv * 4,
+                             &bar[kFull + sb]);
+                __syncwarp();
+            }
+            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
+                const uint32_t sb = si & 1;
+                if (si >= 2) ok = wait.warp(kFree + sb, ((si - 2) >> 1) & 1);
+                if (!ok) break;
                 if (lane == 0) {
-                    uint8_t *stage = sm + b * M::kStage;
-                    uint64_t *full = &bar[kFull + b];
+                    uint8_t *stage = sm + sb * M::kStage;
+                    uint64_t *full = &bar[kFull + sb];
                     const int32_t t0 = (int32_t)(it.t0 + (int64_t)c * C);
                     mbar_arrive_expect_tx(full, M::kStage - (OUT ? 0 : M::kK));
 #pragma unroll
@@ -514,7 +626,6 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     for (int x = 0; x < DVP / 64; ++x)
                         tma_load_3d(stage + M::kV + x * 16384, &tv, 64 * x, h, t0, full);
                 }
-                loaded = gi + 1;
                 __syncwarp();
             }
         } else if (warp == kGateWarp) {
@@ -558,10 +669,8 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const float R = __shfl_sync(0xffffffffu, pre[3], lane | 7);   // end of the block
                 const float total = __shfl_sync(0xffffffffu, down, 0);
                 log_sum += total;
-                if (gi >= 2) {
-                    ok = wait(kGateFree + b, ((gi - 2) >> 1) & 1);
-                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                }
+                if (gi >= 2) ok = wait.warp(kGateFree + b, ((gi - 2) >> 1) & 1);
+                if (!ok) break;
                 Gates &G = gates[b];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
@@ -576,10 +685,10 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             }
             if (!OUT && ok && lane == 0) bnd_log[cut_state(range + 1)] = log_sum;
         }
-        if (!ok) {
-            *abort_flag = 1;
-            if (lane == 0) report(st, KDA_ERR_TIMEOUT, range, 41 + warp);
-        }
+    }
+    if (!ok) {
+        *abort_flag = 1;
+        if (lane == 0) report(st, KDA_ERR_TIMEOUT, range, 41 + warp);
     }
     __syncthreads();
     if (*abort_flag) {
@@ -591,11 +700,9 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             __syncwarp();
             mbar_wait(&bar[kDrain], 0, kWaitNs);
         }
-        if (warp == kLoadWarp) {
-            landed = loaded >= 2 ? loaded - 2 : 0;
-            for (; landed < loaded; ++landed)
-                mbar_wait(&bar[kFull + (landed & 1)], (landed >> 1) & 1, kWaitNs);
-        }
+        if (warp == kLoadWarp)   // (si: loads issued; only each stage's last can be in flight)
+            for (uint32_t x = si >= 2 ? si - 2 : 0; x < si; ++x)
+                mbar_wait(&bar[kFull + (x & 1)], (x >> 1) & 1, kWaitNs);
         __syncthreads();
     }
     if (warp == kMmaWarp) {
