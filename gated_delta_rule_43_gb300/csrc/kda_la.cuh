@@ -97,14 +97,17 @@ __device__ __forceinline__ bool before_cut(const Plan &p, int i, Item &it) {
 // scan keeps a copy of the initial state of such a unit, for range i at index ranges + i.
 __device__ __forceinline__ int64_t cut_state(int i) { return i - 1; }
 
-// Where an item of range `range` starts from; NULL for zeros.
-__device__ __forceinline__ const float *start_state(const Plan &p, const Item &it, int range,
-                                                    const float *h0, const float *bnd,
-                                                    int64_t dkdv) {
-    if (it.c0 > 0) return bnd + cut_state(range) * dkdv;
-    if (!h0) return nullptr;
-    if (it.c1 < it.nc && p.in_place) return bnd + (int64_t)(p.ranges + range) * dkdv;
-    return h0 + ((int64_t)it.n * p.H + it.h) * dkdv;
+// Where an item of range `range` starts from: the index of a state among the boundaries' or
+// the initial ones; -1 for zeros.
+struct Start {
+    int32_t index;
+    bool in_bnd;
+};
+__device__ __forceinline__ Start start_state(const Plan &p, const Item &it, int range, bool h0) {
+    if (it.c0 > 0) return {(int32_t)cut_state(range), true};
+    if (!h0) return {-1, false};
+    if (it.c1 < it.nc && p.in_place) return {p.ranges + range, true};
+    return {it.n * p.H + it.h, false};
 }
 
 // A log decay below this is e^g = 0 in fp32.  Prefix sums, whose differences give the decay

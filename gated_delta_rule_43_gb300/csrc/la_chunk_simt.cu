@@ -228,7 +228,8 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
         const int hk = h / (p.H / p.Hk);
         const int j0 = blk * DVB;
         const int64_t nh = ((int64_t)it.n * p.H + h) * dkdv;
-        const float *start = OUT ? start_state(p, it, range, h0, bnd, dkdv) : nullptr;
+        const Start from = OUT ? start_state(p, it, range, h0 != nullptr) : Start{-1, false};
+        const float *start = from.index < 0 ? nullptr : (from.in_bnd ? bnd : h0) + from.index * dkdv;
         float S[SR][4];
 #pragma unroll
         for (int r = 0; r < SR; ++r) {

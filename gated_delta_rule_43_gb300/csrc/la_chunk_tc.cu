@@ -22,18 +22,20 @@
 //
 // One CTA an SM walks its range (see kda_la.cuh), every role for itself through the same
 // items and chunks:
-//   warps 0-3    rows of P (tensor memory, as the A operand of P V) and of O (through shared
-//                memory, over the chunk's Q, in one bulk store: rows stored straight from
-//                registers cost 2k cycles a chunk and held up everyone's shared memory)
+//   warps 0-3    rows of P (tensor memory, as the A operand of P V) and of O
 //   warps 4-11   K~^T (read transposed, weighted and split into tensor memory as the A operand
 //                of K~^T V) and the state: thread (row, half) holds its columns of S
 //   warp 12      issues the products          warp 13   loads q, k, v (two stages)
 //   warp 14      the chunk's decays, one chunk ahead
+//   warp 15      stores O, a bulk store a chunk (2k cycles, 16 bytes a cycle, however it is
+//                done; done by plain stores it holds up everyone's shared memory meanwhile)
 // A start state is loaded through a stage of its own, so it is there when the item begins.
-// 96 KB a stage and the 32 KB image of S fill the SM's shared memory; scores / P, O, K~^T V and
-// K~^T (hi, lo) fill its tensor memory.  Loops stay loops: the roles' code shares one
-// instruction cache (unrolled, a chunk took 13k cycles).
+// Two stages of q, k and v (32 KB each, each free as soon as its own readers are done) and the
+// 32 KB image of S fill the SM's shared memory; scores / P, O, K~^T V and K~^T (hi, lo) fill
+// its tensor memory.  Loops stay loops: the roles' code shares one instruction cache
+// (unrolled, a chunk took 13k cycles).
 #include <cuda.h>
+#include <string.h>
 
 #include <mutex>
 
@@ -49,7 +51,7 @@ using namespace sm100;
 constexpr int C = kChunk;
 constexpr int kThreads = 512;
 constexpr int kRowWarps = 4, kStateWarps = 8;
-constexpr int kMmaWarp = 12, kLoadWarp = 13, kGateWarp = 14;
+constexpr int kMmaWarp = 12, kLoadWarp = 13, kGateWarp = 14, kStoreWarp = 15;
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 // What one chunk's decays give, for one stage.
@@ -60,37 +62,42 @@ struct Gates {
 };
 
 enum Bar {
-    kFull = 0,       // [2] a stage's tiles (or a start state) have landed
-    kFree = 2,       // [2] a stage may be loaded again: products and outputs are done with it
-    kGate = 4,       // [2] a chunk's decays are there
-    kGateFree = 6,   // [2] ... and have been used
-    kQkDone = 8,     // Q K^T
-    kQsDone = 9,     // Q S
-    kPvDone = 10,    // P V
-    kKvDone = 11,    // K~^T V
-    kPReady = 12,    // P and the decayed Q S are in tensor memory
-    kKtReady = 13,   // K~^T is
-    kSReady = 14,    // the image of S is in shared memory
-    kOFree = 15,     // the accumulator of O has been read
-    kDrain = 16,
-    kBars = 17
+    kFullQ = 0,      // [2] a stage's q has landed
+    kFullK = 2,      // [2] k (or a start state, over both)
+    kFullV = 4,      // [2] v
+    kFreeQ = 6,      // [2] q has been read, and the outputs that took its place have left
+    kFreeK = 8,      // [2] k (or a start state) has been read
+    kFreeV = 10,     // [2] v
+    kGate = 12,      // [2] a chunk's decays are there
+    kGateFree = 14,  // [2] ... and have been used
+    kKtReady = 16,   // [2] K~^T is in tensor memory (two buffers without outputs)
+    kKvDone = 18,    // [2] K~^T V
+    kQkDone = 20,    // Q K^T
+    kQsDone = 21,    // Q S
+    kPvDone = 22,    // P V
+    kPReady = 23,    // P and the decayed Q S are in tensor memory
+    kSReady = 24,    // the image of S is in shared memory
+    kOFree = 25,     // the accumulator of O has been read: the outputs are in shared memory
+    kOStored = 26,   // ... and have left it
+    kDrain = 27,
+    kBars = 28
 };
 
+// Two stages of q, k and v, the image of S ([DKP rows][DVP]), the decays.  A start state
+// (fp32, in 32-column blocks of 128-byte rows) takes the place of q and k; a chunk's outputs
+// are laid out for their store over its q, or, wider than that, in a place of their own.
 template <int DKP, int DVP> struct Map {
-    static constexpr uint32_t kQ = 0, kK = DKP * 256, kV = 2 * DKP * 256;   // within a stage
-    static constexpr uint32_t kStage = kV + DVP * 256;
-    static constexpr uint32_t kS = 2 * kStage;                 // S image, [DKP rows][DVP]
-    // a chunk's outputs, [C][DVP]: over its Q where they fit
+    static constexpr uint32_t kQ = 0, kK = DKP * 256, kQK = 2 * DKP * 256;   // within a stage
+    static constexpr uint32_t kV = 2 * kQK, kVBytes = DVP * 256;
+    static constexpr uint32_t kS = kV + 2 * kVBytes;
     static constexpr bool kOverQ = DVP <= DKP;
     static constexpr uint32_t kO = kS + DKP * DVP * 2;
     static constexpr uint32_t kGates = kO + (kOverQ ? 0 : C * DVP * 2);
     static constexpr uint32_t kTot = kGates + 2 * sizeof(Gates);   // decay of the chunk, [2]
     static constexpr uint32_t kBar = kTot + 8;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 8;
-    // a start state in a stage: rows padded so that lanes reading rows miss no bank twice
-    static constexpr uint32_t kRow = DVP * 4 + 16;
-    static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kStage % 1024 == 0 && kO % 1024 == 0 &&
-                      kBytes <= 232448 && DKP * kRow <= kStage,
+    static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kO % 1024 == 0 && kQK % 1024 == 0 &&
+                      kV % 1024 == 0 && kBytes <= 232448 && DKP * DVP * 4 <= kQK,
                   "layout");
 };
 
@@ -115,13 +122,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         ::"r"(taddr), KDA_R16(r)
         : "memory");
 }
-// 16 lanes, 32 consecutive columns: register 2 i + j of thread t is lane t / 4 + 8 j, column
+// 16 lanes, 16 consecutive columns: register 2 i + j of thread t is lane t / 4 + 8 j, column
 // 4 i + t % 4
-__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(taddr), KDA_R16(r)
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+          "r"(r[7])
         : "memory");
 }
 #undef KDA_R16
@@ -133,15 +140,7 @@ __device__ __forceinline__ void tmem_st_wait() {
 __device__ __forceinline__ void ldmatrix_t(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-// shared -> global through a tensor map (full boxes; what lies outside the tensor is dropped)
-__device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, int32_t c0,
-                                             int32_t c1, int32_t c2) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
-                 ::"l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
-                 : "memory");
+                 : "r"(addr));
 }
 // 32 bytes to a 32-byte aligned address
 __device__ __forceinline__ void store8(float *dst, const float *x) {
@@ -149,8 +148,11 @@ __device__ __forceinline__ void store8(float *dst, const float *x) {
                  "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
                  : "memory");
 }
-__device__ __forceinline__ void arrive_n(uint64_t *bar, uint32_t n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
+// shared -> global through a tensor map (full boxes; what lies outside the tensor is dropped)
+__device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int32_t c0, int32_t c1,
+                                             int32_t c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(src)
                  : "memory");
 }
 
@@ -184,17 +186,27 @@ __device__ __forceinline__ void split2(uint32_t x, float2 w, uint32_t &hi, uint3
     lo = pack2(a.x - __uint_as_float(hi << 16), a.y - __uint_as_float(hi & 0xffff0000u));
 }
 
-// Waits that end: after kWaitNs, or when another role of the CTA has given up.
+// Waits that end: a limited number of tries (each may sleep in hardware, none is shorter than
+// 20 cycles: at least 20 ms).  Small code, for there are many of them.
 struct Waits {
-    uint64_t *bar;
-    volatile int *abort;
+    uint32_t bar;   // shared-memory address of the first barrier
     __device__ __forceinline__ bool operator()(int which, uint32_t parity) const {
-        if (mbar_try_wait(&bar[which], parity)) return true;
-        const uint64_t t0 = globaltimer_ns();
-        for (uint32_t i = 1;; ++i) {
-            if (mbar_try_wait(&bar[which], parity)) return true;
-            if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > kWaitNs)) return false;
-        }
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 i;\n\t"
+            "mov.u32 i, 0;\n"
+            "again_%=:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "@p bra done_%=;\n\t"
+            "add.u32 i, i, 1;\n\t"
+            "setp.lt.u32 q, i, 2000000;\n\t"
+            "@q bra again_%=;\n"
+            "done_%=:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar + 8 * which), "r"(parity)
+            : "memory");
+        return ok != 0;
     }
     // the same for a whole warp
     __device__ __forceinline__ bool warp(int which, uint32_t parity) const {
@@ -208,7 +220,8 @@ template <int DKP, int DVP, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                   const __grid_constant__ CUtensorMap to,
+                   const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap th0,
+                   const __grid_constant__ CUtensorMap tbnd,
                    const float *__restrict__ g, int g_per_token, const float *h0, float *hT,
                    __nv_bfloat16 *__restrict__ o, int dk, int dv, float *__restrict__ bnd,
                    float *__restrict__ bnd_log, StatusWord *st) {
@@ -227,27 +240,31 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         if (tid == 0) report(st, KDA_ERR_CUDA, 0, 40);
         return;
     }
-    constexpr uint32_t kReleases = OUT ? 2 : 1;   // of a stage: products, outputs
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&bar[kFull + b], 1);
-            mbar_init(&bar[kFree + b], kReleases);
+            mbar_init(&bar[kFullQ + b], 1);
+            mbar_init(&bar[kFullK + b], 1);
+            mbar_init(&bar[kFullV + b], 1);
+            mbar_init(&bar[kFreeQ + b], 1);
+            mbar_init(&bar[kFreeK + b], 1);
+            mbar_init(&bar[kFreeV + b], 1);
             mbar_init(&bar[kGate + b], 1);
             mbar_init(&bar[kGateFree + b], kStateWarps + (OUT ? kRowWarps : 0));
+            mbar_init(&bar[kKtReady + b], kStateWarps);
+            mbar_init(&bar[kKvDone + b], 1);
         }
         mbar_init(&bar[kQkDone], 1);
         mbar_init(&bar[kQsDone], 1);
         mbar_init(&bar[kPvDone], 1);
-        mbar_init(&bar[kKvDone], 1);
         mbar_init(&bar[kPReady], kRowWarps);
-        mbar_init(&bar[kKtReady], kStateWarps);
         mbar_init(&bar[kSReady], kStateWarps);
         mbar_init(&bar[kOFree], kRowWarps);
+        mbar_init(&bar[kOStored], 1);
         mbar_init(&bar[kDrain], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    constexpr uint32_t kCols = OUT ? 512 : 256;
+    constexpr uint32_t kCols = 512;
     if (warp == kMmaWarp) {
         tmem_alloc(tslot, kCols);
         tmem_relinquish();
@@ -256,12 +273,16 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    const uint32_t tHi = tmem, tLo = tmem + 64, tKV = tmem + 128, tA = tmem + 256, tO = tmem + 384;
-    const Waits wait{bar, abort_flag};
+    // K~^T (hi, lo) and K~^T V; then, of a second chunk's, or scores (then P) and O
+    const uint32_t tHi = tmem, tLo = tmem + 64, tKV = tmem + 128;
+    constexpr uint32_t kOther = 256;
+    const uint32_t tA = tmem + 256, tO = tmem + 384;
+    const Waits wait{smem_u32(bar)};
     const int64_t dkdv = (int64_t)dk * dv;
     uint32_t gi = 0;    // chunks so far: parities of what happens once a chunk
-    uint32_t si = 0;    // stages so far (chunks and start states)
+    uint32_t si = 0;    // stages of q and k so far (chunks and start states)
     bool ok = true;
+    uint32_t issued_q = 0, issued_k = 0, issued_v = 0;   // (load warp)
 
     Item it;
     Walk walk(p, range);
@@ -269,9 +290,9 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     for (; more && ok; more = OUT && walk.next(it)) {
         const int h = it.h;
         const int chunks = it.c1 - it.c0;
-        const float *start = OUT ? start_state(p, it, range, h0, bnd, dkdv) : nullptr;
+        const Start start = OUT ? start_state(p, it, range, h0 != nullptr) : Start{-1, false};
         const uint32_t first_si = si;   // a start state's stage
-        if (start) ++si;
+        if (start.index >= 0) ++si;
 
         if (warp < kRowWarps) {
             if (!OUT) continue;
@@ -279,83 +300,81 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             const uint32_t lanes = (uint32_t)(32 * warp) << 16;
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
                 const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
-                const int64_t t0 = it.t0 + (int64_t)c * C;
                 ok = wait.warp(kGate + b, ph) && wait.warp(kQkDone, gi & 1);
-                if (ok) {
-                    tc_fence_after();
-                    const Gates &G = gates[b];
-                    const float Gt = G.G[t];
+                if (!ok) break;
+                tc_fence_after();
+                const Gates &G = gates[b];
+                const float Gt = G.G[t];
 #pragma unroll 1
-                    for (int cb = 0; cb < 4; ++cb) {
-                        uint32_t pk[16];
-                        if (cb <= warp) {
-                            float a[32];
-                            tmem_ld32(tA + lanes + 32 * cb, a);
-                            tmem_ld_wait();
-                            if (cb < warp) {
-                                const float r = ex2(Gt - G.G[32 * cb + 31]);
-                                const float2 rf = make_float2(r, r);
+                for (int cb = 0; cb < 4; ++cb) {
+                    uint32_t pk[16];
+                    if (cb <= warp) {
+                        float a[32];
+                        tmem_ld32(tA + lanes + 32 * cb, a);
+                        tmem_ld_wait();
+                        if (cb < warp) {
+                            const float r = ex2(Gt - G.G[32 * cb + 31]);
+                            const float2 rf = make_float2(r, r);
 #pragma unroll
-                                for (int j = 0; j < 32; j += 4) {
-                                    const float4 f = *reinterpret_cast<const float4 *>(&G.cf[32 * cb + j]);
-                                    const float2 x = mul2(make_float2(a[j], a[j + 1]),
-                                                          mul2(rf, make_float2(f.x, f.y)));
-                                    const float2 y = mul2(make_float2(a[j + 2], a[j + 3]),
-                                                          mul2(rf, make_float2(f.z, f.w)));
-                                    pk[j / 2] = pack2(x.x, x.y);
-                                    pk[j / 2 + 1] = pack2(y.x, y.y);
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 32; j += 4) {
-                                    const float4 f = *reinterpret_cast<const float4 *>(&G.G[32 * cb + j]);
-                                    pk[j / 2] = pack2(j <= lane ? a[j] * ex2(Gt - f.x) : 0.f,
-                                                      j + 1 <= lane ? a[j + 1] * ex2(Gt - f.y) : 0.f);
-                                    pk[j / 2 + 1] = pack2(j + 2 <= lane ? a[j + 2] * ex2(Gt - f.z) : 0.f,
-                                                          j + 3 <= lane ? a[j + 3] * ex2(Gt - f.w) : 0.f);
-                                }
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(&G.cf[32 * cb + j]);
+                                const float2 x = mul2(make_float2(a[j], a[j + 1]),
+                                                      mul2(rf, make_float2(f.x, f.y)));
+                                const float2 y = mul2(make_float2(a[j + 2], a[j + 3]),
+                                                      mul2(rf, make_float2(f.z, f.w)));
+                                pk[j / 2] = pack2(x.x, x.y);
+                                pk[j / 2 + 1] = pack2(y.x, y.y);
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) pk[j] = 0;
-                        }
-                        // (columns of scores that this warp has read)
-                        tmem_st16(tA + lanes + 16 * cb, pk);
-                    }
-                    ok = wait.warp(kQsDone, gi & 1);
-                    if (ok) {   // P V adds to exp(G_t) Q S
-                        tc_fence_after();
-                        const float e = ex2(Gt);
-                        const float2 eG = make_float2(e, e);
-#pragma unroll 1
-                        for (int j0 = 0; j0 < DVP; j0 += 16) {
-                            float x[16];
-                            uint32_t y[16];
-                            tmem_ld16(tO + lanes + j0, x);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int j = 0; j < 16; j += 2) {
-                                const float2 z = mul2(eG, make_float2(x[j], x[j + 1]));
-                                y[j] = __float_as_uint(z.x);
-                                y[j + 1] = __float_as_uint(z.y);
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(&G.G[32 * cb + j]);
+                                pk[j / 2] = pack2(j <= lane ? a[j] * ex2(Gt - f.x) : 0.f,
+                                                  j + 1 <= lane ? a[j + 1] * ex2(Gt - f.y) : 0.f);
+                                pk[j / 2 + 1] = pack2(j + 2 <= lane ? a[j + 2] * ex2(Gt - f.z) : 0.f,
+                                                      j + 3 <= lane ? a[j + 3] * ex2(Gt - f.w) : 0.f);
                             }
-                            tmem_st16(tO + lanes + j0, y);
                         }
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&bar[kPReady]);
-                            mbar_arrive(&bar[kGateFree + b]);
-                        }
-                        ok = wait.warp(kPvDone, gi & 1);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) pk[j] = 0;
                     }
+                    // (columns of scores that this warp has read)
+                    tmem_st16(tA + lanes + 16 * cb, pk);
                 }
-                // these warps stop together: the barriers below have no time limit
-                ok = bar_and(2, 32 * kRowWarps, ok);
+                ok = wait.warp(kQsDone, gi & 1);
+                if (!ok) break;
+                tc_fence_after();   // P V adds to exp(G_t) Q S
+                const float e = ex2(Gt);
+                const float2 eG = make_float2(e, e);
+#pragma unroll 1
+                for (int j0 = 0; j0 < DVP; j0 += 16) {
+                    float x[16];
+                    uint32_t y[16];
+                    tmem_ld16(tO + lanes + j0, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 z = mul2(eG, make_float2(x[j], x[j + 1]));
+                        y[j] = __float_as_uint(z.x);
+                        y[j + 1] = __float_as_uint(z.y);
+                    }
+                    tmem_st16(tO + lanes + j0, y);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar[kPReady]);
+                    mbar_arrive(&bar[kGateFree + b]);
+                }
+                ok = wait.warp(kPvDone, gi & 1);
                 if (!ok) break;
                 tc_fence_after();
-                uint8_t *so = sm + (M::kOverQ ? sb * M::kStage + M::kQ : M::kO);
+                // the outputs, for the store warp
+                if (!M::kOverQ && gi > 0) ok = wait.warp(kOStored, (gi - 1) & 1);
+                if (!ok) break;
+                uint8_t *so = sm + (M::kOverQ ? sb * M::kQK + M::kQ : M::kO);
 #pragma unroll 1
                 for (int cb = 0; cb < DVP / 32; ++cb) {
                     float x[32];
@@ -375,28 +394,6 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kOFree]);
-                named_bar_sync(1, 32 * kRowWarps);
-                const int len = (int)min((int64_t)C, it.t1 - t0);
-                if (len == C) {
-                    if (tid == 0) {
-#pragma unroll
-                        for (int x = 0; x < DVP / 64; ++x)
-                            tma_store_3d(&to, so + x * 16384, 64 * x, h, (int32_t)t0);
-                        bulk_commit();
-                        bulk_wait_read_all();
-                    }
-                } else {   // rows past the segment belong to others
-                    const int per = dv / 8;
-                    for (int x = tid; x < len * per; x += 32 * kRowWarps) {
-                        const int r = x / per, j = 8 * (x - r * per);
-                        *reinterpret_cast<uint4 *>(o + ((t0 + r) * p.H + h) * (int64_t)dv + j) =
-                            *reinterpret_cast<const uint4 *>(so + sw128_offset(r, j, C));
-                    }
-                    fence_proxy_async();   // before the stage is loaded again
-                    named_bar_sync(1, 32 * kRowWarps);
-                }
-                if (tid == 0) mbar_arrive(&bar[kFree + sb]);
-                if (!M::kOverQ) named_bar_sync(1, 32 * kRowWarps);   // kO is written next chunk
             }
         } else if (warp < kRowWarps + kStateWarps) {
             constexpr int NC = DVP / 2;
@@ -408,112 +405,139 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             float S[NC];
 #pragma unroll
             for (int j = 0; j < NC; ++j) S[j] = 0.f;
-            // These warps stop together too: each failure is carried to the next bar_and.
-            if (start) {
-                const uint32_t sb = first_si & 1;
-                ok = wait.warp(kFull + sb, (first_si >> 1) & 1);
-                if (ok && mine) {
-                    const uint8_t *row = sm + sb * M::kStage + i * M::kRow + j0 * 4;
-#pragma unroll
-                    for (int j = 0; j < NC; j += 4) {
-                        const float4 x = *reinterpret_cast<const float4 *>(row + 4 * j);
-                        S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
-                    }
-                }
-                ok = bar_and(3, 32 * kStateWarps, ok);
-                if (!ok) break;
-                if (tid == 32 * kRowWarps) arrive_n(&bar[kFree + sb], kReleases);
-            }
-            // the image of S for chunk number `gn`; Q S of the one before has read the old one
-            auto put_image = [&](uint32_t gn) {
-                if (gn > 0 && !wait.warp(kQsDone, (gn - 1) & 1)) return false;
-                if (i < DKP) {
-#pragma unroll
-                    for (int j = 0; j < NC; j += 8) {
-                        uint4 u;
-                        u.x = pack2(S[j], S[j + 1]);
-                        u.y = pack2(S[j + 2], S[j + 3]);
-                        u.z = pack2(S[j + 4], S[j + 5]);
-                        u.w = pack2(S[j + 6], S[j + 7]);
-                        *reinterpret_cast<uint4 *>(sm + M::kS + sw128_offset(i, j0 + j, DKP)) = u;
-                    }
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kSReady]);
-                return true;
-            };
-            bool fine = !OUT || put_image(gi);
-            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
-                const int len = (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)c * C);
-                uint8_t *stage = sm + sb * M::kStage;
-                fine = fine && wait.warp(kGate + b, ph) && wait.warp(kFull + sb, (si >> 1) & 1);
-                float decay = 0.f;
-                if (fine) {
-                    // K~^T: channels of this warp's quarter, tokens of its half, in blocks of
-                    // 16 x 16.  (K~^T V of the chunk before has been waited for.)
-                    decay = tot[b];
-                    const float *w = gates[b].w + 64 * half;
-                    if (32 * quarter < DKP) {
+            // These warps stop together: each failure is carried to the next bar_and.  Round c
+            // ends chunk c (adds its product to S) and makes K~^T and the image of S for chunk
+            // c + 1: K~^T before anything that its product does not need, that is with outputs
+            // right after the tensor memory is free, without (two buffers) before the wait.
+            bool fine = true;
+            float decay = 0.f, decay_next = 0.f;   // of chunk c, c + 1
+            // (gi and si here: of chunk c + 1)
 #pragma unroll 1
-                        for (int cg = 0; cg < 32; cg += 16) {
-                            uint32_t hi[16], lo[16];
+            for (int c = -1; c < chunks; ++c) {
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
+                const bool next = c + 1 < chunks;
+                auto end_chunk = [&] {
+                    fine = fine && wait.warp(kKvDone + (b ^ 1), ((gi - 1) >> 1) & 1);
+                    ok = bar_and(3, 32 * kStateWarps, fine);
+                    if (!ok) return;
+                    tc_fence_after();
 #pragma unroll
-                            for (int tg = 0; tg < 4; ++tg) {
-                                const int s = 16 * tg + 2 * (lane & 3);   // and s + 1, s + 8, s + 9
-                                uint32_t x[4];
-                                ldmatrix_t(smem_u32(stage + M::kK) +
-                                               sw128_offset(64 * half + 16 * tg + (lane >> 4) * 8 + (lane & 7),
-                                                            32 * quarter + cg + ((lane >> 3) & 1) * 8, C),
-                                           x);
-                                if (len < C) {   // tokens past the segment count as zeros
-                                    const int at = 64 * half + s;
-                                    const uint32_t m0 = (at < len ? 0xffffu : 0u) | (at + 1 < len ? 0xffff0000u : 0u);
-                                    const uint32_t m1 = (at + 8 < len ? 0xffffu : 0u) | (at + 9 < len ? 0xffff0000u : 0u);
-                                    x[0] &= m0; x[1] &= m0; x[2] &= m1; x[3] &= m1;
-                                }
-                                const float2 w0 = *reinterpret_cast<const float2 *>(w + s);
-                                const float2 w1 = *reinterpret_cast<const float2 *>(w + s + 8);
-                                split2(x[0], w0, hi[4 * tg], lo[4 * tg]);
-                                split2(x[1], w0, hi[4 * tg + 1], lo[4 * tg + 1]);
-                                split2(x[2], w1, hi[4 * tg + 2], lo[4 * tg + 2]);
-                                split2(x[3], w1, hi[4 * tg + 3], lo[4 * tg + 3]);
-                            }
-                            const uint32_t at = lanes + ((uint32_t)cg << 16) + 32 * half;
-                            tmem_st_16x32(tHi + at, hi);
-                            tmem_st_16x32(tLo + at, lo);
-                        }
-                        tmem_st_wait();
-                    }
-                    if (len < C) {   // their rows of V must not meet the zeros of P and K~
-                        constexpr int U = DVP / 8;   // 16-byte pieces of a row
-                        for (int x = len * U + (tid - 32 * kRowWarps); x < C * U; x += 32 * kStateWarps)
-                            *reinterpret_cast<uint4 *>(stage + M::kV + sw128_offset(x / U, 8 * (x % U), C)) =
-                                make_uint4(0, 0, 0, 0);
-                        fence_proxy_async();
+                    for (int jb = 0; jb < NC; jb += 32) {
+                        float x[32];
+                        tmem_ld32(tKV + (OUT ? 0 : (b ^ 1) * kOther) + lanes + j0 + jb, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) S[jb + j] = decay * S[jb + j] + x[j];
                     }
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&bar[kKtReady]);
-                        mbar_arrive(&bar[kGateFree + b]);
+                };
+                if (OUT && c >= 0) {
+                    end_chunk();
+                    if (!ok) break;
+                }
+                if (next) {
+                    const int len = (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)(c + 1) * C);
+                    fine = fine && wait.warp(kGate + b, ph) && wait.warp(kFullK + sb, (si >> 1) & 1) &&
+                           (len == C || wait.warp(kFullV + b, ph));
+                    if (fine) {
+                        // channels of this warp's quarter, tokens of its half, 16 x 32 a turn
+                        decay_next = tot[b];
+                        if (32 * quarter < DKP) {
+#pragma unroll 1
+                            for (int turn = 0; turn < 4; ++turn) {
+                                const int cg = 16 * (turn >> 1), tg = 32 * (turn & 1);
+                                uint32_t hi[8], lo[8];
+#pragma unroll
+                                for (int m = 0; m < 2; ++m) {
+                                    const int s = 64 * half + tg + 16 * m;   // first of 16 tokens
+                                    uint32_t x[4];
+                                    ldmatrix_t(base + sb * M::kQK + M::kK +
+                                                   sw128_offset(s + (lane >> 4) * 8 + (lane & 7),
+                                                                32 * quarter + cg + ((lane >> 3) & 1) * 8, C),
+                                               x);
+                                    const int at = s + 2 * (lane & 3);   // and at + 1, at + 8, at + 9
+                                    if (len < C) {   // tokens past the sequence count as zeros
+                                        const uint32_t m0 = (at < len ? 0xffffu : 0u) | (at + 1 < len ? 0xffff0000u : 0u);
+                                        const uint32_t m1 = (at + 8 < len ? 0xffffu : 0u) | (at + 9 < len ? 0xffff0000u : 0u);
+                                        x[0] &= m0; x[1] &= m0; x[2] &= m1; x[3] &= m1;
+                                    }
+                                    const float2 w0 = *reinterpret_cast<const float2 *>(&gates[b].w[at]);
+                                    const float2 w1 = *reinterpret_cast<const float2 *>(&gates[b].w[at + 8]);
+                                    split2(x[0], w0, hi[4 * m], lo[4 * m]);
+                                    split2(x[1], w0, hi[4 * m + 1], lo[4 * m + 1]);
+                                    split2(x[2], w1, hi[4 * m + 2], lo[4 * m + 2]);
+                                    split2(x[3], w1, hi[4 * m + 3], lo[4 * m + 3]);
+                                }
+                                const uint32_t at = lanes + ((uint32_t)cg << 16) + 32 * half + tg / 2 + (OUT ? 0 : b * kOther);
+                                tmem_st_16x16(tHi + at, hi);
+                                tmem_st_16x16(tLo + at, lo);
+                            }
+                            tmem_st_wait();
+                        }
+                        if (len < C) {   // their rows of V must not meet the zeros of P and K~
+                            constexpr int U = DVP / 8;   // 16-byte pieces of a row
+#pragma unroll 1
+                            for (int x = len * U + (tid - 32 * kRowWarps); x < C * U; x += 32 * kStateWarps)
+                                *reinterpret_cast<uint4 *>(sm + M::kV + b * M::kVBytes + sw128_offset(x / U, 8 * (x % U), C)) =
+                                    make_uint4(0, 0, 0, 0);
+                            fence_proxy_async();
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bar[kKtReady + b]);
+                            mbar_arrive(&bar[kGateFree + b]);
+                        }
                     }
-                    fine = wait.warp(kKvDone, gi & 1);
                 }
-                ok = bar_and(3, 32 * kStateWarps, fine);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int jb = 0; jb < NC; jb += 32) {
-                    float x[32];
-                    tmem_ld32(tKV + lanes + j0 + jb, x);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) S[jb + j] = decay * S[jb + j] + x[j];
+                if (!OUT && c >= 0) {
+                    end_chunk();
+                    if (!ok) break;
                 }
-                tc_fence_before();
-                if (OUT && c + 1 < chunks) fine = put_image(gi + 1);
+                if (c < 0 && start.index >= 0) {
+                    const uint32_t fb = first_si & 1;
+                    fine = fine && wait.warp(kFullK + fb, (first_si >> 1) & 1);
+                    if (fine && mine) {
+                        const uint8_t *at = sm + fb * M::kQK;
+#pragma unroll
+                        for (int j = 0; j < NC; j += 4) {
+                            const int col = j0 + j;
+                            const float4 x = *reinterpret_cast<const float4 *>(
+                                at + (col / 32) * dk * 128 + i * 128 + ((((col % 32) / 4) ^ (i & 7)) << 4));
+                            S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+                        }
+                    }
+                    ok = bar_and(3, 32 * kStateWarps, fine);
+                    if (!ok) break;
+                    if (tid == 32 * kRowWarps) {
+                        mbar_arrive(&bar[kFreeK + fb]);
+                        mbar_arrive(&bar[kFreeQ + fb]);
+                    }
+                }
+                if (OUT && next) {   // Q S of the chunk before has read the old image
+                    fine = fine && (gi == 0 || wait.warp(kQsDone, (gi - 1) & 1));
+                    if (fine) {
+                        if (i < DKP) {
+#pragma unroll
+                            for (int j = 0; j < NC; j += 8) {
+                                uint4 u;
+                                u.x = pack2(S[j], S[j + 1]);
+                                u.y = pack2(S[j + 2], S[j + 3]);
+                                u.z = pack2(S[j + 4], S[j + 5]);
+                                u.w = pack2(S[j + 6], S[j + 7]);
+                                *reinterpret_cast<uint4 *>(sm + M::kS + sw128_offset(i, j0 + j, DKP)) = u;
+                            }
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[kSReady]);
+                    }
+                }
+                decay = decay_next;
+                if (next) {
+                    ++gi;
+                    ++si;
+                }
             }
             float *dst = OUT ? (it.c1 == it.nc && hT ? hT + ((int64_t)it.n * p.H + h) * dkdv
                                                      : nullptr)
@@ -534,99 +558,127 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             const uint32_t id_kk = idesc_bf16(128, 128, false, false);   // Q K^T
             const uint32_t id_km = idesc_bf16(128, DVP, false, true);    // the others: B is V or S
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
-                const uint32_t sb = si & 1;
-                const uint32_t stage = base + sb * M::kStage;
-                const uint64_t dq = sdesc_sw128(stage + M::kQ, 16, 1024);
-                const uint64_t dkk = sdesc_sw128(stage + M::kK, 16, 1024);
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
+                const uint32_t qk = base + sb * M::kQK;
+                const uint64_t dq = sdesc_sw128(qk + M::kQ, 16, 1024);
+                const uint64_t dkk = sdesc_sw128(qk + M::kK, 16, 1024);
                 // token-major V and channel-major S: the K dimension is the row
-                const uint64_t dvt = sdesc_sw128(stage + M::kV, C * 128, 1024);
+                const uint64_t dvt = sdesc_sw128(base + M::kV + b * M::kVBytes, C * 128, 1024);
                 const uint64_t ds = sdesc_sw128(base + M::kS, DKP * 128, 1024);
                 if (OUT) {
                     // P of the chunk before lies over the scores
-                    ok = wait.warp(kFull + sb, (si >> 1) & 1) &&
+                    ok = wait.warp(kFullK + sb, (si >> 1) & 1) &&
+                         wait.warp(kFullQ + sb, (si >> 1) & 1) &&
                          (gi == 0 || wait.warp(kPvDone, (gi - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
                         for (int s = 0; s < DKP / 16; ++s)
                             umma_bf16(tA, desc_add(dq, (s >> 2) * 16384 + (s & 3) * 32),
                                       desc_add(dkk, (s >> 2) * 16384 + (s & 3) * 32), id_kk, s > 0);
                         umma_commit(&bar[kQkDone]);
                     }
                     __syncwarp();
+                }
+                ok = wait.warp(kKtReady + b, ph) && wait.warp(kFullV + b, ph);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t other = OUT ? 0 : b * kOther;
+                if (elect_one()) {
+                    umma_commit(&bar[kFreeK + sb]);   // (Q K^T so far)
+#pragma unroll 2
+                    for (int s = 0; s < C / 16; ++s)
+                        umma_bf16_ts(tKV + other, tHi + other + 8 * s, desc_add(dvt, s * 2048), id_km, s > 0);
+#pragma unroll 2
+                    for (int s = 0; s < C / 16; ++s)
+                        umma_bf16_ts(tKV + other, tLo + other + 8 * s, desc_add(dvt, s * 2048), id_km, 1);
+                    umma_commit(&bar[kKvDone + b]);
+                    if (!OUT) umma_commit(&bar[kFreeV + b]);
+                }
+                __syncwarp();
+                if (OUT) {
                     ok = wait.warp(kSReady, gi & 1) && (gi == 0 || wait.warp(kOFree, (gi - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
                         for (int s = 0; s < DKP / 16; ++s)
                             umma_bf16(tO, desc_add(dq, (s >> 2) * 16384 + (s & 3) * 32),
                                       desc_add(ds, s * 2048), id_km, s > 0);
                         umma_commit(&bar[kQsDone]);
                     }
                     __syncwarp();
-                }
-                ok = wait.warp(kKtReady, gi & 1) && wait.warp(kFull + sb, (si >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int s = 0; s < C / 16; ++s)
-                        umma_bf16_ts(tKV, tHi + 8 * s, desc_add(dvt, s * 2048), id_km, s > 0);
-#pragma unroll
-                    for (int s = 0; s < C / 16; ++s)
-                        umma_bf16_ts(tKV, tLo + 8 * s, desc_add(dvt, s * 2048), id_km, 1);
-                    umma_commit(&bar[kKvDone]);
-                    if (!OUT) umma_commit(&bar[kFree + sb]);
-                }
-                __syncwarp();
-                if (OUT) {
                     ok = wait.warp(kPReady, gi & 1);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
                         for (int s = 0; s < C / 16; ++s)
                             umma_bf16_ts(tO, tA + 8 * s, desc_add(dvt, s * 2048), id_km, 1);
                         umma_commit(&bar[kPvDone]);
-                        umma_commit(&bar[kFree + sb]);
+                        umma_commit(&bar[kFreeV + b]);
                     }
                     __syncwarp();
                 }
             }
         } else if (warp == kLoadWarp) {
             const int hk = h / (p.H / p.Hk);
-            if (start) {
+            if (start.index >= 0) {
                 const uint32_t sb = first_si & 1;
-                if (first_si >= 2) ok = wait.warp(kFree + sb, ((first_si - 2) >> 1) & 1);
+                const uint32_t before = ((first_si - 2) >> 1) & 1;
+                if (first_si >= 2) ok = wait.warp(kFreeK + sb, before) && wait.warp(kFreeQ + sb, before);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&bar[kFull + sb], (uint32_t)dkdv * 4);
-                __syncwarp();
-                for (int r = lane; r < dk; r += 32)
-                    bulk_g2s(sm + sb * M::kStage + r * M::kRow, start + (int64_t)r * dv, dv * 4,
-                             &bar[kFull + sb]);
+                if (lane == 0) {
+                    uint64_t *full = &bar[kFullK + sb];
+                    mbar_arrive(&bar[kFullQ + sb]);
+                    mbar_arrive_expect_tx(full, (uint32_t)dkdv * 4);
+                    for (int x = 0; x < dv / 32; ++x)
+                        tma_load_3d(sm + sb * M::kQK + x * dk * 128, start.in_bnd ? &tbnd : &th0, 32 * x,
+                                    0, start.index, full);
+                }
+                ++issued_k;
                 __syncwarp();
             }
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
-                const uint32_t sb = si & 1;
-                if (si >= 2) ok = wait.warp(kFree + sb, ((si - 2) >> 1) & 1);
+                const uint32_t b = gi & 1, sb = si & 1, before = ((si - 2) >> 1) & 1;
+                const int32_t t0 = (int32_t)(it.t0 + (int64_t)c * C);
+                uint8_t *qk = sm + sb * M::kQK;
+                if (si >= 2) ok = wait.warp(kFreeK + sb, before);
                 if (!ok) break;
                 if (lane == 0) {
-                    uint8_t *stage = sm + sb * M::kStage;
-                    uint64_t *full = &bar[kFull + sb];
-                    const int32_t t0 = (int32_t)(it.t0 + (int64_t)c * C);
-                    mbar_arrive_expect_tx(full, M::kStage - (OUT ? 0 : M::kK));
+                    uint64_t *full = &bar[kFullK + sb];
+                    mbar_arrive_expect_tx(full, M::kK);
 #pragma unroll
-                    for (int x = 0; x < DKP / 64; ++x) {
-                        if (OUT) tma_load_3d(stage + M::kQ + x * 16384, &tq, 64 * x, hk, t0, full);
-                        tma_load_3d(stage + M::kK + x * 16384, &tk, 64 * x, hk, t0, full);
-                    }
+                    for (int x = 0; x < DKP / 64; ++x)
+                        tma_load_3d(qk + M::kK + x * 16384, &tk, 64 * x, hk, t0, full);
+                }
+                ++issued_k;
+                __syncwarp();
+                if (gi >= 2) ok = wait.warp(kFreeV + b, ((gi - 2) >> 1) & 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    uint64_t *full = &bar[kFullV + b];
+                    mbar_arrive_expect_tx(full, M::kVBytes);
 #pragma unroll
                     for (int x = 0; x < DVP / 64; ++x)
-                        tma_load_3d(stage + M::kV + x * 16384, &tv, 64 * x, h, t0, full);
+                        tma_load_3d(sm + M::kV + b * M::kVBytes + x * 16384, &tv, 64 * x, h, t0, full);
                 }
+                ++issued_v;
                 __syncwarp();
+                if (OUT) {
+                    if (si >= 2) ok = wait.warp(kFreeQ + sb, before);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        uint64_t *full = &bar[kFullQ + sb];
+                        mbar_arrive_expect_tx(full, M::kK);
+#pragma unroll
+                        for (int x = 0; x < DKP / 64; ++x)
+                            tma_load_3d(qk + M::kQ + x * 16384, &tq, 64 * x, hk, t0, full);
+                    }
+                    issued_q = si + 1;
+                    __syncwarp();
+                }
             }
         } else if (warp == kGateWarp) {
             float log_sum = 0.f;
@@ -635,6 +687,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const int64_t t0 = it.t0 + (int64_t)c * C;
                 const int len = (int)min((int64_t)C, it.t1 - t0);
                 float x[4], pre[4], suf[4];
+                int bad = -1;
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const int s = 4 * lane + m;
@@ -642,12 +695,12 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 }
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    if (!log_decay_ok(x[m]))
-                        report(st, KDA_ERR_DECAY_RANGE,
-                               g_per_token ? (t0 + 4 * lane + m) * p.H + h : h, 30);
+                    if (!log_decay_ok(x[m])) bad = m;
                     const float y = x[m] < kLogZero ? kLogZero : x[m];
                     pre[m] = m ? pre[m - 1] + y : y;
                 }
+                if (bad >= 0)
+                    report(st, KDA_ERR_DECAY_RANGE, g_per_token ? (t0 + 4 * lane + bad) * p.H + h : h, 30);
                 const float all = x[0] + x[1] + x[2] + x[3];
                 float up = pre[3], down = all;   // inclusive scans over the lanes
 #pragma unroll
@@ -684,6 +737,37 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 if (lane == 0) mbar_arrive(&bar[kGate + b]);
             }
             if (!OUT && ok && lane == 0) bnd_log[cut_state(range + 1)] = log_sum;
+        } else if (OUT && warp == kStoreWarp) {
+            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
+                const uint32_t sb = si & 1;
+                const int64_t t0 = it.t0 + (int64_t)c * C;
+                const int len = (int)min((int64_t)C, it.t1 - t0);
+                const uint32_t so = M::kOverQ ? sb * M::kQK + M::kQ : M::kO;
+                ok = wait.warp(kOFree, gi & 1);
+                if (!ok) break;
+                if (len == C) {
+                    if (lane == 0) {
+#pragma unroll
+                        for (int x = 0; x < DVP / 64; ++x)
+                            tma_store_3d(&to, base + so + x * 16384, 64 * x, h, (int32_t)t0);
+                        bulk_commit();
+                        bulk_wait_read_all();
+                    }
+                } else {   // rows past the sequence belong to others
+                    const int per = dv / 8;   // 16-byte pieces of a row
+                    for (int x = lane; x < len * per; x += 32) {
+                        const int r = x / per, j = 8 * (x - r * per);
+                        *reinterpret_cast<uint4 *>(o + ((t0 + r) * p.H + h) * (int64_t)dv + j) =
+                            *reinterpret_cast<const uint4 *>(sm + so + sw128_offset(r, j, C));
+                    }
+                    fence_proxy_async();   // before q of a later chunk takes the place
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar[kFreeQ + sb]);
+                    mbar_arrive(&bar[kOStored]);
+                }
+            }
         }
     }
     if (!ok) {
@@ -700,9 +784,14 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             __syncwarp();
             mbar_wait(&bar[kDrain], 0, kWaitNs);
         }
-        if (warp == kLoadWarp)   // (si: loads issued; only each stage's last can be in flight)
-            for (uint32_t x = si >= 2 ? si - 2 : 0; x < si; ++x)
-                mbar_wait(&bar[kFull + (x & 1)], (x >> 1) & 1, kWaitNs);
+        if (warp == kLoadWarp) {   // (only each stage's last load can be in flight)
+            for (uint32_t x = issued_q >= 2 ? issued_q - 2 : 0; x < issued_q; ++x)
+                mbar_wait(&bar[kFullQ + (x & 1)], (x >> 1) & 1, kWaitNs);
+            for (uint32_t x = issued_k >= 2 ? issued_k - 2 : 0; x < issued_k; ++x)
+                mbar_wait(&bar[kFullK + (x & 1)], (x >> 1) & 1, kWaitNs);
+            for (uint32_t x = issued_v >= 2 ? issued_v - 2 : 0; x < issued_v; ++x)
+                mbar_wait(&bar[kFullV + (x & 1)], (x >> 1) & 1, kWaitNs);
+        }
         __syncthreads();
     }
     if (warp == kMmaWarp) {
@@ -728,22 +817,33 @@ static EncodeTiledFn encode_tiled() {
     return fn;
 }
 
+static cudaError_t encode(CUtensorMap *m, CUtensorMapDataType type, const void *x,
+                          const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                          const cuuint32_t (&box)[3]) {
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(m, type, 3, const_cast<void *>(x), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // [T, heads, D] bf16, tokens `stride` elements apart, in boxes of 128 tokens x 1 head x 64
 // channels with the 128-byte swizzle; what lies outside (channels of 32-wide heads, tokens
 // past the last) reads as zeros.
 static cudaError_t tensor_map(CUtensorMap *m, const void *x, int64_t T, int heads, int D,
                               int64_t stride) {
-    EncodeTiledFn enc = encode_tiled();
-    if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
-    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, 1, C};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(x), dims,
-                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x,
+                  {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T},
+                  {(cuuint64_t)D * 2, (cuuint64_t)stride * 2}, {64, 1, C});
+}
+
+// [states, dk, dv] fp32 in boxes of one state's rows x 32 columns
+static cudaError_t state_map(CUtensorMap *m, const float *x, int64_t states, int dk, int dv) {
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, x,
+                  {(cuuint64_t)dv, (cuuint64_t)dk, (cuuint64_t)states},
+                  {(cuuint64_t)dv * 4, (cuuint64_t)dk * dv * 4}, {32, (cuuint32_t)dk, 1});
 }
 
 // Shared memory above 48 KB, once per kernel and device.
@@ -760,7 +860,7 @@ template <int DKP, int DVP, bool OUT> static cudaError_t allow_smem(int dev) {
 }
 
 template <int DKP, int DVP, bool OUT>
-static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[4], const float *g, int gpt,
+static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[6], const float *g, int gpt,
                           const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
                           float *bnd_log, StatusWord *st, cudaStream_t s) {
     int dev = 0;
@@ -769,24 +869,29 @@ static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[4], const float 
     if (e != cudaSuccess) return e;
     la_chunk_tc_kernel<DKP, DVP, OUT>
         <<<OUT ? p.ranges : p.ranges - 1, kThreads, Map<DKP, DVP>::kBytes, s>>>(
-            p, m[0], m[1], m[2], m[3], g, gpt, h0, hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
+            p, m[0], m[1], m[2], m[3], m[4], m[5], g, gpt, h0, hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
     return cudaGetLastError();
 }
 
 }  // namespace tc
 }  // namespace la
 
-cudaError_t la_tensor_maps(CUtensorMap (&m)[4], const void *q, const void *k, const void *v,
-                           const void *o, int64_t T, int H, int Hk, int dk, int dv, int64_t qs, int64_t ks,
-                           int64_t vs) {
-    cudaError_t e = la::tc::tensor_map(&m[0], q, T, Hk, dk, qs);
-    if (e == cudaSuccess) e = la::tc::tensor_map(&m[1], k, T, Hk, dk, ks);
-    if (e == cudaSuccess) e = la::tc::tensor_map(&m[2], v, T, H, dv, vs);
-    if (e == cudaSuccess) e = la::tc::tensor_map(&m[3], o, T, H, dv, (int64_t)H * dv);
+// The maps of one call: q, k, v, o and, where they are read, the initial states and the states
+// at the cuts.
+cudaError_t la_tensor_maps(CUtensorMap (&m)[6], const void *q, const void *k, const void *v,
+                           const void *o, const float *h0, const float *bnd, const la::Plan &p,
+                           int64_t T, int dk, int dv, int64_t qs, int64_t ks, int64_t vs) {
+    memset(&m[4], 0, 2 * sizeof m[4]);
+    cudaError_t e = la::tc::tensor_map(&m[0], q, T, p.Hk, dk, qs);
+    if (e == cudaSuccess) e = la::tc::tensor_map(&m[1], k, T, p.Hk, dk, ks);
+    if (e == cudaSuccess) e = la::tc::tensor_map(&m[2], v, T, p.H, dv, vs);
+    if (e == cudaSuccess) e = la::tc::tensor_map(&m[3], o, T, p.H, dv, (int64_t)p.H * dv);
+    if (e == cudaSuccess && h0) e = la::tc::state_map(&m[4], h0, (int64_t)p.N * p.H, dk, dv);
+    if (e == cudaSuccess && bnd) e = la::tc::state_map(&m[5], bnd, 2 * (int64_t)p.ranges, dk, dv);
     return e;
 }
 
-cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[4], const float *g,
+cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[6], const float *g,
                          int gpt, const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
                          float *bnd_log, StatusWord *st, cudaStream_t s) {
 #define KDA_LA(DK_, DV_)                                                                          \
