@@ -29,7 +29,6 @@
 //   warp 14      the chunk's decays, one chunk ahead
 //   warp 15      stores O, a bulk store a chunk (2k cycles, 16 bytes a cycle, however it is
 //                done; done by plain stores it holds up everyone's shared memory meanwhile)
-// A start state is loaded through a stage of its own, so it is there when the item begins.
 // Two stages of q, k and v (32 KB each, each free as soon as its own readers are done) and the
 // 32 KB image of S fill the SM's shared memory; scores / P, O, K~^T V and K~^T (hi, lo) fill
 // its tensor memory.  Loops stay loops: the roles' code shares one instruction cache
@@ -57,17 +56,18 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 // What one chunk's decays give, for one stage.
 struct Gates {
     float G[C];        // prefix sums times log2(e)
-    float w[C];        // exp(g_{s+1} + ... + g_C)
+    // w_s = exp(g_{s+1} + ... + g_C) as the sum of two bf16, in pairs of tokens: hi, lo
+    uint2 w[C / 2];
     float cf[96];      // exp(R - G_s); the last block needs none
 };
 
 enum Bar {
     kFullQ = 0,      // [2] a stage's q has landed
-    kFullK = 2,      // [2] k (or a start state, over both)
+    kFullK = 2,      // [2] k
     kFullV = 4,      // [2] v
     kFreeQ = 6,      // [2] q has been read, and the outputs that took its place have left
-    kFreeK = 8,      // [2] k (or a start state) has been read
-    kFreeV = 10,     // [2] v
+    kFreeK = 8,      // [2] k has been read, and a final state that took its place has left
+    kFreeV = 10,     // [2] v, likewise
     kGate = 12,      // [2] a chunk's decays are there
     kGateFree = 14,  // [2] ... and have been used
     kKtReady = 16,   // [2] K~^T is in tensor memory (two buffers without outputs)
@@ -79,13 +79,13 @@ enum Bar {
     kSReady = 24,    // the image of S is in shared memory
     kOFree = 25,     // the accumulator of O has been read: the outputs are in shared memory
     kOStored = 26,   // ... and have left it
-    kDrain = 27,
-    kBars = 28
+    kEndReady = 27,  // an item's final state is in shared memory
+    kDrain = 28,
+    kBars = 29
 };
 
-// Two stages of q, k and v, the image of S ([DKP rows][DVP]), the decays.  A start state
-// (fp32, in 32-column blocks of 128-byte rows) takes the place of q and k; a chunk's outputs
-// are laid out for their store over its q, or, wider than that, in a place of their own.
+// Two stages of q, k and v, the image of S ([DKP rows][DVP]), the decays.  A chunk's outputs are
+// laid out for their store over its q, or, wider than that, in a place of their own.
 template <int DKP, int DVP> struct Map {
     static constexpr uint32_t kQ = 0, kK = DKP * 256, kQK = 2 * DKP * 256;   // within a stage
     static constexpr uint32_t kV = 2 * kQK, kVBytes = DVP * 256;
@@ -97,7 +97,7 @@ template <int DKP, int DVP> struct Map {
     static constexpr uint32_t kBar = kTot + 8;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 8;
     static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kO % 1024 == 0 && kQK % 1024 == 0 &&
-                      kV % 1024 == 0 && kBytes <= 232448 && DKP * DVP * 4 <= kQK,
+                      kV % 1024 == 0 && kBytes <= 232448,
                   "layout");
 };
 
@@ -142,17 +142,20 @@ __device__ __forceinline__ void ldmatrix_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-// 32 bytes to a 32-byte aligned address
-__device__ __forceinline__ void store8(float *dst, const float *x) {
-    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(x[0]),
-                 "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
-}
 // shared -> global through a tensor map (full boxes; what lies outside the tensor is dropped)
 __device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int32_t c0, int32_t c1,
                                              int32_t c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
                  ::"l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(src)
+                 : "memory");
+}
+
+// 32 bytes from a 32-byte aligned address
+__device__ __forceinline__ void load8(const float *src, float *x) {
+    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]),
+                   "=f"(x[7])
+                 : "l"(src)
                  : "memory");
 }
 
@@ -178,12 +181,18 @@ __device__ __forceinline__ float ex2(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// x: two bf16 of successive tokens, w their weights; hi = w x rounded to bf16, lo the rounded
-// rest
-__device__ __forceinline__ void split2(uint32_t x, float2 w, uint32_t &hi, uint32_t &lo) {
-    const float2 a = mul2(w, make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)));
-    hi = pack2(a.x, a.y);
-    lo = pack2(a.x - __uint_as_float(hi << 16), a.y - __uint_as_float(hi & 0xffff0000u));
+// x: two bf16 of successive tokens, w their weights (hi, lo); hi + lo = w x but for 2^-17 of it:
+// x w.hi less its own rounding is a bf16 exactly, so the second line loses nothing, and the
+// third rounds what is 2^-8 of the product.
+__device__ __forceinline__ void split2(uint32_t x, uint2 w, uint32_t &hi, uint32_t &lo) {
+    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&x);
+    const __nv_bfloat162 wh = *reinterpret_cast<const __nv_bfloat162 *>(&w.x);
+    const __nv_bfloat162 wl = *reinterpret_cast<const __nv_bfloat162 *>(&w.y);
+    const __nv_bfloat162 h = __hmul2(v, wh);
+    const __nv_bfloat162 rest = __hfma2(v, wh, __hneg2(h));
+    const __nv_bfloat162 l = __hfma2(v, wl, rest);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
 // Waits that end: a limited number of tries (each may sleep in hardware, none is shorter than
@@ -220,9 +229,8 @@ template <int DKP, int DVP, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                   const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap th0,
-                   const __grid_constant__ CUtensorMap tbnd,
-                   const float *__restrict__ g, int g_per_token, const float *h0, float *hT,
+                   const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap thT,
+                   const float *__restrict__ g, int g_per_token, const float *h0, int has_hT,
                    __nv_bfloat16 *__restrict__ o, int dk, int dv, float *__restrict__ bnd,
                    float *__restrict__ bnd_log, StatusWord *st) {
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -260,6 +268,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         mbar_init(&bar[kSReady], kStateWarps);
         mbar_init(&bar[kOFree], kRowWarps);
         mbar_init(&bar[kOStored], 1);
+        mbar_init(&bar[kEndReady], kStateWarps);
         mbar_init(&bar[kDrain], 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -279,10 +288,10 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     const uint32_t tA = tmem + 256, tO = tmem + 384;
     const Waits wait{smem_u32(bar)};
     const int64_t dkdv = (int64_t)dk * dv;
-    uint32_t gi = 0;    // chunks so far: parities of what happens once a chunk
-    uint32_t si = 0;    // stages of q and k so far (chunks and start states)
+    uint32_t gi = 0;    // chunks so far: stages, and parities of what happens once a chunk
     bool ok = true;
     uint32_t issued_q = 0, issued_k = 0, issued_v = 0;   // (load warp)
+    uint32_t ends_before = 0;                            // (store warp) final states so far
 
     Item it;
     Walk walk(p, range);
@@ -291,15 +300,14 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         const int h = it.h;
         const int chunks = it.c1 - it.c0;
         const Start start = OUT ? start_state(p, it, range, h0 != nullptr) : Start{-1, false};
-        const uint32_t first_si = si;   // a start state's stage
-        if (start.index >= 0) ++si;
+        const bool ends = OUT && has_hT && it.c1 == it.nc;   // with a final state to store
 
         if (warp < kRowWarps) {
             if (!OUT) continue;
             const int t = tid;   // this thread's row of the chunk
             const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
+            for (int c = 0; c < chunks; ++c, ++gi) {
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
                 ok = wait.warp(kGate + b, ph) && wait.warp(kQkDone, gi & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -348,18 +356,21 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const float e = ex2(Gt);
                 const float2 eG = make_float2(e, e);
 #pragma unroll 1
-                for (int j0 = 0; j0 < DVP; j0 += 16) {
-                    float x[16];
-                    uint32_t y[16];
-                    tmem_ld16(tO + lanes + j0, x);
+                for (int j0 = 0; j0 < DVP; j0 += 32) {
+                    float x[32];
+                    tmem_ld32(tO + lanes + j0, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 z = mul2(eG, make_float2(x[j], x[j + 1]));
-                        y[j] = __float_as_uint(z.x);
-                        y[j + 1] = __float_as_uint(z.y);
+                    for (int m = 0; m < 32; m += 16) {
+                        uint32_t y[16];
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 z = mul2(eG, make_float2(x[m + j], x[m + j + 1]));
+                            y[j] = __float_as_uint(z.x);
+                            y[j + 1] = __float_as_uint(z.y);
+                        }
+                        tmem_st16(tO + lanes + j0 + m, y);
                     }
-                    tmem_st16(tO + lanes + j0, y);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -374,7 +385,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 // the outputs, for the store warp
                 if (!M::kOverQ && gi > 0) ok = wait.warp(kOStored, (gi - 1) & 1);
                 if (!ok) break;
-                uint8_t *so = sm + (M::kOverQ ? sb * M::kQK + M::kQ : M::kO);
+                uint8_t *so = sm + (M::kOverQ ? b * M::kQK + M::kQ : M::kO);
 #pragma unroll 1
                 for (int cb = 0; cb < DVP / 32; ++cb) {
                     float x[32];
@@ -411,10 +422,10 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             // right after the tensor memory is free, without (two buffers) before the wait.
             bool fine = true;
             float decay = 0.f, decay_next = 0.f;   // of chunk c, c + 1
-            // (gi and si here: of chunk c + 1)
+            // (gi here: of chunk c + 1)
 #pragma unroll 1
             for (int c = -1; c < chunks; ++c) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
                 const bool next = c + 1 < chunks;
                 auto end_chunk = [&] {
                     fine = fine && wait.warp(kKvDone + (b ^ 1), ((gi - 1) >> 1) & 1);
@@ -437,7 +448,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 }
                 if (next) {
                     const int len = (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)(c + 1) * C);
-                    fine = fine && wait.warp(kGate + b, ph) && wait.warp(kFullK + sb, (si >> 1) & 1) &&
+                    fine = fine && wait.warp(kGate + b, ph) && wait.warp(kFullK + b, ph) &&
                            (len == C || wait.warp(kFullV + b, ph));
                     if (fine) {
                         // channels of this warp's quarter, tokens of its half, 16 x 32 a turn
@@ -451,7 +462,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                                 for (int m = 0; m < 2; ++m) {
                                     const int s = 64 * half + tg + 16 * m;   // first of 16 tokens
                                     uint32_t x[4];
-                                    ldmatrix_t(base + sb * M::kQK + M::kK +
+                                    ldmatrix_t(base + b * M::kQK + M::kK +
                                                    sw128_offset(s + (lane >> 4) * 8 + (lane & 7),
                                                                 32 * quarter + cg + ((lane >> 3) & 1) * 8, C),
                                                x);
@@ -461,8 +472,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                                         const uint32_t m1 = (at + 8 < len ? 0xffffu : 0u) | (at + 9 < len ? 0xffff0000u : 0u);
                                         x[0] &= m0; x[1] &= m0; x[2] &= m1; x[3] &= m1;
                                     }
-                                    const float2 w0 = *reinterpret_cast<const float2 *>(&gates[b].w[at]);
-                                    const float2 w1 = *reinterpret_cast<const float2 *>(&gates[b].w[at + 8]);
+                                    const uint2 w0 = gates[b].w[at / 2], w1 = gates[b].w[at / 2 + 4];
                                     split2(x[0], w0, hi[4 * m], lo[4 * m]);
                                     split2(x[1], w0, hi[4 * m + 1], lo[4 * m + 1]);
                                     split2(x[2], w1, hi[4 * m + 2], lo[4 * m + 2]);
@@ -494,24 +504,17 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     end_chunk();
                     if (!ok) break;
                 }
-                if (c < 0 && start.index >= 0) {
-                    const uint32_t fb = first_si & 1;
-                    fine = fine && wait.warp(kFullK + fb, (first_si >> 1) & 1);
-                    if (fine && mine) {
-                        const uint8_t *at = sm + fb * M::kQK;
+                if (c < 0 && start.index >= 0 && mine) {
+                    const float *row = (start.in_bnd ? bnd : h0) + start.index * dkdv + (int64_t)i * dv + j0;
+                    if (((uintptr_t)row & 31) == 0) {   // (a state buffer is 16-byte aligned)
+#pragma unroll
+                        for (int j = 0; j < NC; j += 8) load8(row + j, S + j);
+                    } else {
 #pragma unroll
                         for (int j = 0; j < NC; j += 4) {
-                            const int col = j0 + j;
-                            const float4 x = *reinterpret_cast<const float4 *>(
-                                at + (col / 32) * dk * 128 + i * 128 + ((((col % 32) / 4) ^ (i & 7)) << 4));
+                            const float4 x = *reinterpret_cast<const float4 *>(row + j);
                             S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
                         }
-                    }
-                    ok = bar_and(3, 32 * kStateWarps, fine);
-                    if (!ok) break;
-                    if (tid == 32 * kRowWarps) {
-                        mbar_arrive(&bar[kFreeK + fb]);
-                        mbar_arrive(&bar[kFreeQ + fb]);
                     }
                 }
                 if (OUT && next) {   // Q S of the chunk before has read the old image
@@ -534,32 +537,38 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     }
                 }
                 decay = decay_next;
-                if (next) {
-                    ++gi;
-                    ++si;
-                }
+                if (next) ++gi;
             }
-            float *dst = OUT ? (it.c1 == it.nc && hT ? hT + ((int64_t)it.n * p.H + h) * dkdv
-                                                     : nullptr)
-                             : bnd + cut_state(range + 1) * dkdv;
-            if (ok && dst && mine) {
-                float *row = dst + (int64_t)i * dv + j0;
-                if (((uintptr_t)dst & 31) == 0) {   // (a state buffer is 16-byte aligned)
-#pragma unroll
-                    for (int j = 0; j < NC; j += 8) store8(row + j, S + j);
-                } else {
+            if (ends) {
+                // for the store warp: S over the last chunk's k (first half of the columns) and
+                // v, in 32-column blocks of 128-byte rows
+                ok = bar_and(3, 32 * kStateWarps, wait.warp(kPvDone, (gi - 1) & 1));
+                if (!ok) break;
+                if (mine) {
+                    uint8_t *at = sm + (half ? M::kV + ((gi - 1) & 1) * M::kVBytes
+                                             : ((gi - 1) & 1) * M::kQK + M::kK);
 #pragma unroll
                     for (int j = 0; j < NC; j += 4)
-                        *reinterpret_cast<float4 *>(row + j) =
+                        *reinterpret_cast<float4 *>(at + (j / 32) * dk * 128 + i * 128 +
+                                                    ((((j % 32) / 4) ^ (i & 7)) << 4)) =
                             make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
                 }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kEndReady]);
+            }
+            if (!OUT && ok && mine) {
+                float *row = bnd + cut_state(range + 1) * dkdv + (int64_t)i * dv + j0;
+#pragma unroll
+                for (int j = 0; j < NC; j += 4)
+                    *reinterpret_cast<float4 *>(row + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
             }
         } else if (warp == kMmaWarp) {
             const uint32_t id_kk = idesc_bf16(128, 128, false, false);   // Q K^T
             const uint32_t id_km = idesc_bf16(128, DVP, false, true);    // the others: B is V or S
-            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
-                const uint32_t qk = base + sb * M::kQK;
+            for (int c = 0; c < chunks; ++c, ++gi) {
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
+                const uint32_t qk = base + b * M::kQK;
                 const uint64_t dq = sdesc_sw128(qk + M::kQ, 16, 1024);
                 const uint64_t dkk = sdesc_sw128(qk + M::kK, 16, 1024);
                 // token-major V and channel-major S: the K dimension is the row
@@ -567,8 +576,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const uint64_t ds = sdesc_sw128(base + M::kS, DKP * 128, 1024);
                 if (OUT) {
                     // P of the chunk before lies over the scores
-                    ok = wait.warp(kFullK + sb, (si >> 1) & 1) &&
-                         wait.warp(kFullQ + sb, (si >> 1) & 1) &&
+                    ok = wait.warp(kFullK + b, ph) && wait.warp(kFullQ + b, ph) &&
                          (gi == 0 || wait.warp(kPvDone, (gi - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
@@ -586,7 +594,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 tc_fence_after();
                 const uint32_t other = OUT ? 0 : b * kOther;
                 if (elect_one()) {
-                    umma_commit(&bar[kFreeK + sb]);   // (Q K^T so far)
+                    if (!(ends && c + 1 == chunks)) umma_commit(&bar[kFreeK + b]);   // (Q K^T so far)
 #pragma unroll 2
                     for (int s = 0; s < C / 16; ++s)
                         umma_bf16_ts(tKV + other, tHi + other + 8 * s, desc_add(dvt, s * 2048), id_km, s > 0);
@@ -617,37 +625,23 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         for (int s = 0; s < C / 16; ++s)
                             umma_bf16_ts(tO, tA + 8 * s, desc_add(dvt, s * 2048), id_km, 1);
                         umma_commit(&bar[kPvDone]);
-                        umma_commit(&bar[kFreeV + b]);
+                        if (!(ends && c + 1 == chunks)) umma_commit(&bar[kFreeV + b]);
                     }
                     __syncwarp();
                 }
             }
         } else if (warp == kLoadWarp) {
             const int hk = h / (p.H / p.Hk);
-            if (start.index >= 0) {
-                const uint32_t sb = first_si & 1;
-                const uint32_t before = ((first_si - 2) >> 1) & 1;
-                if (first_si >= 2) ok = wait.warp(kFreeK + sb, before) && wait.warp(kFreeQ + sb, before);
-                if (!ok) break;
-                if (lane == 0) {
-                    uint64_t *full = &bar[kFullK + sb];
-                    mbar_arrive(&bar[kFullQ + sb]);
-                    mbar_arrive_expect_tx(full, (uint32_t)dkdv * 4);
-                    for (int x = 0; x < dv / 32; ++x)
-                        tma_load_3d(sm + sb * M::kQK + x * dk * 128, start.in_bnd ? &tbnd : &th0, 32 * x,
-                                    0, start.index, full);
-                }
-                ++issued_k;
-                __syncwarp();
-            }
-            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
-                const uint32_t b = gi & 1, sb = si & 1, before = ((si - 2) >> 1) & 1;
+            if (start.index >= 0 && lane == 0)   // the state warps read it from there
+                bulk_prefetch_l2((start.in_bnd ? bnd : h0) + start.index * dkdv, (uint32_t)dkdv * 4);
+            for (int c = 0; c < chunks; ++c, ++gi) {
+                const uint32_t b = gi & 1, before = ((gi - 2) >> 1) & 1;
                 const int32_t t0 = (int32_t)(it.t0 + (int64_t)c * C);
-                uint8_t *qk = sm + sb * M::kQK;
-                if (si >= 2) ok = wait.warp(kFreeK + sb, before);
+                uint8_t *qk = sm + b * M::kQK;
+                if (gi >= 2) ok = wait.warp(kFreeK + b, before);
                 if (!ok) break;
                 if (lane == 0) {
-                    uint64_t *full = &bar[kFullK + sb];
+                    uint64_t *full = &bar[kFullK + b];
                     mbar_arrive_expect_tx(full, M::kK);
 #pragma unroll
                     for (int x = 0; x < DKP / 64; ++x)
@@ -655,7 +649,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 }
                 ++issued_k;
                 __syncwarp();
-                if (gi >= 2) ok = wait.warp(kFreeV + b, ((gi - 2) >> 1) & 1);
+                if (gi >= 2) ok = wait.warp(kFreeV + b, before);
                 if (!ok) break;
                 if (lane == 0) {
                     uint64_t *full = &bar[kFullV + b];
@@ -667,16 +661,16 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 ++issued_v;
                 __syncwarp();
                 if (OUT) {
-                    if (si >= 2) ok = wait.warp(kFreeQ + sb, before);
+                    if (gi >= 2) ok = wait.warp(kFreeQ + b, before);
                     if (!ok) break;
                     if (lane == 0) {
-                        uint64_t *full = &bar[kFullQ + sb];
+                        uint64_t *full = &bar[kFullQ + b];
                         mbar_arrive_expect_tx(full, M::kK);
 #pragma unroll
                         for (int x = 0; x < DKP / 64; ++x)
                             tma_load_3d(qk + M::kQ + x * 16384, &tq, 64 * x, hk, t0, full);
                     }
-                    issued_q = si + 1;
+                    ++issued_q;
                     __syncwarp();
                 }
             }
@@ -729,8 +723,14 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 for (int m = 0; m < 4; ++m) {
                     const int s = 4 * lane + m;
                     G.G[s] = pre[m];
-                    G.w[s] = expf(suf[m]);
                     if (s < 96) G.cf[s] = ex2(R - pre[m]);
+                }
+#pragma unroll
+                for (int m = 0; m < 4; m += 2) {
+                    const float w0 = expf(suf[m]), w1 = expf(suf[m + 1]);
+                    const uint32_t hi = pack2(w0, w1);
+                    G.w[2 * lane + m / 2] = make_uint2(hi, pack2(w0 - __uint_as_float(hi << 16),
+                                                                 w1 - __uint_as_float(hi & 0xffff0000u)));
                 }
                 if (lane == 0) tot[b] = expf(total);
                 __syncwarp();
@@ -738,11 +738,11 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             }
             if (!OUT && ok && lane == 0) bnd_log[cut_state(range + 1)] = log_sum;
         } else if (OUT && warp == kStoreWarp) {
-            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
-                const uint32_t sb = si & 1;
+            for (int c = 0; c < chunks; ++c, ++gi) {
+                const uint32_t b = gi & 1;
                 const int64_t t0 = it.t0 + (int64_t)c * C;
                 const int len = (int)min((int64_t)C, it.t1 - t0);
-                const uint32_t so = M::kOverQ ? sb * M::kQK + M::kQ : M::kO;
+                const uint32_t so = M::kOverQ ? b * M::kQK + M::kQ : M::kO;
                 ok = wait.warp(kOFree, gi & 1);
                 if (!ok) break;
                 if (len == C) {
@@ -764,8 +764,26 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&bar[kFreeQ + sb]);
+                    mbar_arrive(&bar[kFreeQ + b]);
                     mbar_arrive(&bar[kOStored]);
+                }
+                if (ends && c + 1 == chunks) {
+                    ok = wait.warp(kEndReady, ends_before & 1);
+                    if (!ok) break;
+                    ++ends_before;
+                    if (lane == 0) {
+                        constexpr int kHalf = DVP / 64;   // blocks of a half
+                        for (int x = 0; x < dv / 32; ++x)
+                            tma_store_3d(&thT,
+                                         base + (x < kHalf ? b * M::kQK + M::kK + x * dk * 128
+                                                           : M::kV + b * M::kVBytes + (x - kHalf) * dk * 128),
+                                         32 * x, 0, it.n * p.H + h);
+                        bulk_commit();
+                        bulk_wait_read_all();
+                        mbar_arrive(&bar[kFreeK + b]);
+                        mbar_arrive(&bar[kFreeV + b]);
+                    }
+                    __syncwarp();
                 }
             }
         }
@@ -860,8 +878,8 @@ template <int DKP, int DVP, bool OUT> static cudaError_t allow_smem(int dev) {
 }
 
 template <int DKP, int DVP, bool OUT>
-static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[6], const float *g, int gpt,
-                          const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
+static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[5], const float *g, int gpt,
+                          const float *h0, int has_hT, void *o, int dk, int dv, float *bnd,
                           float *bnd_log, StatusWord *st, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -869,36 +887,34 @@ static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[6], const float 
     if (e != cudaSuccess) return e;
     la_chunk_tc_kernel<DKP, DVP, OUT>
         <<<OUT ? p.ranges : p.ranges - 1, kThreads, Map<DKP, DVP>::kBytes, s>>>(
-            p, m[0], m[1], m[2], m[3], m[4], m[5], g, gpt, h0, hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
+            p, m[0], m[1], m[2], m[3], m[4], g, gpt, h0, has_hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
     return cudaGetLastError();
 }
 
 }  // namespace tc
 }  // namespace la
 
-// The maps of one call: q, k, v, o and, where they are read, the initial states and the states
-// at the cuts.
-cudaError_t la_tensor_maps(CUtensorMap (&m)[6], const void *q, const void *k, const void *v,
-                           const void *o, const float *h0, const float *bnd, const la::Plan &p,
-                           int64_t T, int dk, int dv, int64_t qs, int64_t ks, int64_t vs) {
-    memset(&m[4], 0, 2 * sizeof m[4]);
+// The maps of one call: q, k, v, o and, where they are written, the final states.
+cudaError_t la_tensor_maps(CUtensorMap (&m)[5], const void *q, const void *k, const void *v,
+                           const void *o, const float *hT, const la::Plan &p, int64_t T, int dk,
+                           int dv, int64_t qs, int64_t ks, int64_t vs) {
+    memset(&m[4], 0, sizeof m[4]);
     cudaError_t e = la::tc::tensor_map(&m[0], q, T, p.Hk, dk, qs);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[1], k, T, p.Hk, dk, ks);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[2], v, T, p.H, dv, vs);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[3], o, T, p.H, dv, (int64_t)p.H * dv);
-    if (e == cudaSuccess && h0) e = la::tc::state_map(&m[4], h0, (int64_t)p.N * p.H, dk, dv);
-    if (e == cudaSuccess && bnd) e = la::tc::state_map(&m[5], bnd, 2 * (int64_t)p.ranges, dk, dv);
+    if (e == cudaSuccess && hT) e = la::tc::state_map(&m[4], hT, (int64_t)p.N * p.H, dk, dv);
     return e;
 }
 
-cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[6], const float *g,
-                         int gpt, const float *h0, float *hT, void *o, int dk, int dv, float *bnd,
+cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[5], const float *g,
+                         int gpt, const float *h0, int has_hT, void *o, int dk, int dv, float *bnd,
                          float *bnd_log, StatusWord *st, cudaStream_t s) {
 #define KDA_LA(DK_, DV_)                                                                          \
     if ((dk <= 64) == (DK_ == 64) && (dv <= 64) == (DV_ == 64))                                   \
-        return out ? la::tc::launch<DK_, DV_, true>(p, m, g, gpt, h0, hT, o, dk, dv, bnd, bnd_log, \
+        return out ? la::tc::launch<DK_, DV_, true>(p, m, g, gpt, h0, has_hT, o, dk, dv, bnd, bnd_log, \
                                                     st, s)                                        \
-                   : la::tc::launch<DK_, DV_, false>(p, m, g, gpt, h0, hT, o, dk, dv, bnd, bnd_log, \
+                   : la::tc::launch<DK_, DV_, false>(p, m, g, gpt, h0, has_hT, o, dk, dv, bnd, bnd_log, \
                                                      st, s);
     KDA_LA(64, 64) KDA_LA(64, 128) KDA_LA(128, 64) KDA_LA(128, 128)
 #undef KDA_LA
