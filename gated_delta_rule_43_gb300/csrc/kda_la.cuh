@@ -44,35 +44,41 @@ struct Item {
     int64_t t0, t1;           // tokens [t0, t1) of the packed tensors
 };
 
-__device__ __forceinline__ void set_tokens(const Plan &p, Item &it) {
-    const int64_t b = p.cu[it.n], e = p.cu[it.n + 1];
-    it.t0 = b + (int64_t)it.c0 * kChunk;
-    it.t1 = min(b + (int64_t)it.c1 * kChunk, e);
+__device__ __forceinline__ void set_tokens(Item &it, int64_t begin, int64_t end) {
+    it.t0 = begin + (int64_t)it.c0 * kChunk;
+    it.t1 = min(begin + (int64_t)it.c1 * kChunk, end);
 }
 
-// Walks the items of the range between two cuts.
+// Walks the items of the range between two cuts.  The heads of a sequence follow each other, so
+// what is known of the sequence is kept: its reads take microseconds beside a busy memory.
 struct Walk {
     const Plan &p;
     int64_t x, end;
     int n, h, c;
+    int nc = 0;               // chunks of sequence n, 0: not read yet
+    int64_t begin, stop;      // its tokens
     __device__ __forceinline__ Walk(const Plan &plan, int range)
         : p(plan), x(plan.cuts[range].x), end(plan.cuts[range + 1].x), n(plan.cuts[range].n),
           h(plan.cuts[range].h), c(plan.cuts[range].c) {}
     __device__ __forceinline__ bool next(Item &it) {
         if (x >= end) return false;
-        int nc;
-        while ((nc = p.off[n + 1] - p.off[n]) == 0) ++n;   // (sequences without tokens)
+        if (nc == 0) {
+            while ((nc = p.off[n + 1] - p.off[n]) == 0) ++n;   // (sequences without tokens)
+            begin = p.cu[n];
+            stop = p.cu[n + 1];
+        }
         it.n = n;
         it.h = h;
         it.c0 = c;
         it.nc = nc;
         it.c1 = (int)min((int64_t)nc, c + (end - x));
-        set_tokens(p, it);
+        set_tokens(it, begin, stop);
         x += it.c1 - c;
         c = 0;
         if (++h == p.H) {
             h = 0;
             ++n;
+            nc = 0;
         }
         return true;
     }
@@ -88,7 +94,7 @@ __device__ __forceinline__ bool before_cut(const Plan &p, int i, Item &it) {
     it.c1 = e.c;
     it.c0 = (int)max((int64_t)0, e.c - (e.x - p.cuts[i - 1].x));
     it.nc = p.off[e.n + 1] - p.off[e.n];
-    set_tokens(p, it);
+    set_tokens(it, p.cu[it.n], p.cu[it.n + 1]);
     return true;
 }
 

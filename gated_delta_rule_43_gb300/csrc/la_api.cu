@@ -17,11 +17,12 @@ cudaError_t launch_la_simt(bool out, int dk, int dv, const la::Plan &p, const fl
                            const float *k, const float *v, int64_t qs, int64_t ks, int64_t vs,
                            const float *g, int gpt, const float *h0, float *hT, float *o,
                            float *bnd, float *bnd_log, StatusWord *st, cudaStream_t s);
-cudaError_t la_tensor_maps(CUtensorMap (&m)[5], const void *q, const void *k, const void *v,
-                           const void *o, const float *hT, const la::Plan &p, int64_t T, int dk,
-                           int dv, int64_t qs, int64_t ks, int64_t vs);
-cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[5], const float *g,
-                         int gpt, const float *h0, int has_hT, void *o, int dk, int dv, float *bnd,
+cudaError_t la_tensor_maps(CUtensorMap (&m)[7], const void *q, const void *k, const void *v,
+                           const void *o, const float *h0, const float *hT, const float *bnd,
+                           const la::Plan &p, int64_t T, int dk, int dv, int64_t qs, int64_t ks,
+                           int64_t vs);
+cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[7], const float *g,
+                         int gpt, int has_h0, int has_hT, void *o, int dk, int dv, float *bnd,
                          float *bnd_log, StatusWord *st, cudaStream_t s);
 cudaError_t launch_la_decode(int dtype, int dk, int dv, const void *q, const void *k,
                              const void *v, const float *g, float *state, void *o, int N, int H,
@@ -144,15 +145,15 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
                                    L.ranges, L.split, st, initial_state, final_state, H, dkdv, s);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (total_tokens == 0) return KDA_OK;
-    CUtensorMap maps[5];
+    CUtensorMap maps[7];
     if (dtype == KDA_BF16 &&
-        la_tensor_maps(maps, q, k, v, o, final_state, p, total_tokens, dk, dv, q_stride, k_stride,
-                       v_stride) != cudaSuccess)
+        la_tensor_maps(maps, q, k, v, o, initial_state, final_state, L.split ? bnd : nullptr, p,
+                       total_tokens, dk, dv, q_stride, k_stride, v_stride) != cudaSuccess)
         return KDA_ERR_CUDA;
     auto pass = [&](bool out) {
         if (dtype == KDA_BF16)
-            return launch_la_tc(out, p, maps, g, g_per_token, initial_state, final_state != nullptr, o,
-                                dk, dv, bnd, bnd_log, st, s);
+            return launch_la_tc(out, p, maps, g, g_per_token, initial_state != nullptr,
+                                final_state != nullptr, o, dk, dv, bnd, bnd_log, st, s);
         return launch_la_simt(out, dk, dv, p, (const float *)q, (const float *)k, (const float *)v,
                               q_stride, k_stride, v_stride, g, g_per_token, initial_state,
                               final_state, (float *)o, bnd, bnd_log, st, s);

@@ -63,11 +63,11 @@ struct Gates {
 
 enum Bar {
     kFullQ = 0,      // [2] a stage's q has landed
-    kFullK = 2,      // [2] k
+    kFullK = 2,      // [2] k (or a start state, over both)
     kFullV = 4,      // [2] v
     kFreeQ = 6,      // [2] q has been read, and the outputs that took its place have left
-    kFreeK = 8,      // [2] k has been read, and a final state that took its place has left
-    kFreeV = 10,     // [2] v, likewise
+    kFreeK = 8,      // [2] k (or a start state) has been read
+    kFreeV = 10,     // [2] v has, and half of a final state that took its place has left
     kGate = 12,      // [2] a chunk's decays are there
     kGateFree = 14,  // [2] ... and have been used
     kKtReady = 16,   // [2] K~^T is in tensor memory (two buffers without outputs)
@@ -80,12 +80,15 @@ enum Bar {
     kOFree = 25,     // the accumulator of O has been read: the outputs are in shared memory
     kOStored = 26,   // ... and have left it
     kEndReady = 27,  // an item's final state is in shared memory
-    kDrain = 28,
-    kBars = 29
+    kEndFree = 28,   // ... and has left the place of the image of S
+    kDrain = 29,
+    kBars = 30
 };
 
-// Two stages of q, k and v, the image of S ([DKP rows][DVP]), the decays.  A chunk's outputs are
-// laid out for their store over its q, or, wider than that, in a place of their own.
+// Two stages of q, k and v, the image of S ([DKP rows][DVP]), the decays.  A start state (fp32, in
+// 32-column blocks of 128-byte rows) takes the place of q and k, a final state that of the
+// image of S and of v.  A chunk's outputs are laid out for their store over its q, or, wider
+// than that, in a place of their own.
 template <int DKP, int DVP> struct Map {
     static constexpr uint32_t kQ = 0, kK = DKP * 256, kQK = 2 * DKP * 256;   // within a stage
     static constexpr uint32_t kV = 2 * kQK, kVBytes = DVP * 256;
@@ -97,7 +100,8 @@ template <int DKP, int DVP> struct Map {
     static constexpr uint32_t kBar = kTot + 8;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 8;
     static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kO % 1024 == 0 && kQK % 1024 == 0 &&
-                      kV % 1024 == 0 && kBytes <= 232448,
+                      kV % 1024 == 0 && kBytes <= 232448 && DKP * DVP * 4 <= kQK &&
+                      DKP * DVP * 2 <= kVBytes,
                   "layout");
 };
 
@@ -147,15 +151,6 @@ __device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int
                                              int32_t c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
                  ::"l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(src)
-                 : "memory");
-}
-
-// 32 bytes from a 32-byte aligned address
-__device__ __forceinline__ void load8(const float *src, float *x) {
-    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]),
-                   "=f"(x[7])
-                 : "l"(src)
                  : "memory");
 }
 
@@ -229,8 +224,9 @@ template <int DKP, int DVP, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                   const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap thT,
-                   const float *__restrict__ g, int g_per_token, const float *h0, int has_hT,
+                   const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap th0,
+                   const __grid_constant__ CUtensorMap thT, const __grid_constant__ CUtensorMap tbnd,
+                   const float *__restrict__ g, int g_per_token, int has_h0, int has_hT,
                    __nv_bfloat16 *__restrict__ o, int dk, int dv, float *__restrict__ bnd,
                    float *__restrict__ bnd_log, StatusWord *st) {
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -269,6 +265,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         mbar_init(&bar[kOFree], kRowWarps);
         mbar_init(&bar[kOStored], 1);
         mbar_init(&bar[kEndReady], kStateWarps);
+        mbar_init(&bar[kEndFree], 1);
         mbar_init(&bar[kDrain], 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -288,26 +285,32 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     const uint32_t tA = tmem + 256, tO = tmem + 384;
     const Waits wait{smem_u32(bar)};
     const int64_t dkdv = (int64_t)dk * dv;
-    uint32_t gi = 0;    // chunks so far: stages, and parities of what happens once a chunk
+    uint32_t gi = 0;    // chunks so far: stages of v, and parities of what happens once a chunk
+    uint32_t si = 0;    // stages of q and k so far (chunks and start states)
     bool ok = true;
     uint32_t issued_q = 0, issued_k = 0, issued_v = 0;   // (load warp)
-    uint32_t ends_before = 0;                            // (store warp) final states so far
+    uint32_t ends_before = 0;                            // (store and state warps) final states so far
 
-    Item it;
-    Walk walk(p, range);
-    bool more = OUT ? walk.next(it) : before_cut(p, range + 1, it);
-    for (; more && ok; more = OUT && walk.next(it)) {
-        const int h = it.h;
-        const int chunks = it.c1 - it.c0;
-        const Start start = OUT ? start_state(p, it, range, h0 != nullptr) : Start{-1, false};
-        const bool ends = OUT && has_hT && it.c1 == it.nc;   // with a final state to store
+    // Each role goes through the range's items for itself: role(item, its start, whether it has a
+    // final state to store).
+    auto each_item = [&](auto role) {
+        Item it;
+        Walk walk(p, range);
+        bool more = OUT ? walk.next(it) : before_cut(p, range + 1, it);
+        for (; more && ok; more = OUT && walk.next(it))
+            role(it, OUT ? start_state(p, it, range, has_h0) : Start{-1, false},
+                 OUT && has_hT && it.c1 == it.nc);
+    };
+    constexpr int NC = DVP / 2;
 
-        if (warp < kRowWarps) {
-            if (!OUT) continue;
+    if (warp < kRowWarps) {
+        if (OUT) each_item([&](const Item &it, const Start &start, bool ends) {
+            const int chunks = it.c1 - it.c0;
+            if (start.index >= 0) ++si;
             const int t = tid;   // this thread's row of the chunk
             const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-            for (int c = 0; c < chunks; ++c, ++gi) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
+            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
                 ok = wait.warp(kGate + b, ph) && wait.warp(kQkDone, gi & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -385,7 +388,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 // the outputs, for the store warp
                 if (!M::kOverQ && gi > 0) ok = wait.warp(kOStored, (gi - 1) & 1);
                 if (!ok) break;
-                uint8_t *so = sm + (M::kOverQ ? b * M::kQK + M::kQ : M::kO);
+                uint8_t *so = sm + (M::kOverQ ? sb * M::kQK + M::kQ : M::kO);
 #pragma unroll 1
                 for (int cb = 0; cb < DVP / 32; ++cb) {
                     float x[32];
@@ -406,26 +409,48 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kOFree]);
             }
-        } else if (warp < kRowWarps + kStateWarps) {
-            constexpr int NC = DVP / 2;
-            const int quarter = warp & 3, half = (warp - kRowWarps) >> 2;
-            const int i = 32 * quarter + lane;                // state row, columns j0 ..
-            const int j0 = NC * half;
-            const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-            const bool mine = i < dk && j0 < dv;
-            float S[NC];
+        });
+    } else if (warp < kRowWarps + kStateWarps) {
+        // state row i, columns j0 .. of half the columns
+        const int quarter = warp & 3, half = ((warp - kRowWarps) >> 2) & 1;
+        const int i = 32 * quarter + lane;                // state row, columns j0 ..
+        const int j0 = NC * half;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const bool mine = i < dk && j0 < dv;
+        float S[NC];
 #pragma unroll
-            for (int j = 0; j < NC; ++j) S[j] = 0.f;
+        for (int j = 0; j < NC; ++j) S[j] = 0.f;
+        uint32_t end_of = 0;   // the item that ended before chunk number end_of (> 0) has a final state
+        // S as the final state of an item, for the store warp: over the image of S (first half of
+        // the columns) and the last chunk's v, in 32-column blocks of 128-byte rows
+        auto put_end = [&] {
+            if (!wait.warp(kPvDone, (end_of - 1) & 1)) return false;
+            if (mine) {
+                uint8_t *at = sm + (half ? M::kV + ((end_of - 1) & 1) * M::kVBytes : M::kS);
+#pragma unroll
+                for (int j = 0; j < NC; j += 4)
+                    *reinterpret_cast<float4 *>(at + (j / 32) * dk * 128 + i * 128 + ((((j % 32) / 4) ^ (i & 7)) << 4)) =
+                        make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[kEndReady]);
+            return true;
+        };
+        each_item([&](const Item &it, const Start &start, bool ends) {
+            const int chunks = it.c1 - it.c0;
+            const uint32_t first_si = si;   // a start state's stage
+            if (start.index >= 0) ++si;
             // These warps stop together: each failure is carried to the next bar_and.  Round c
             // ends chunk c (adds its product to S) and makes K~^T and the image of S for chunk
             // c + 1: K~^T before anything that its product does not need, that is with outputs
             // right after the tensor memory is free, without (two buffers) before the wait.
             bool fine = true;
             float decay = 0.f, decay_next = 0.f;   // of chunk c, c + 1
-            // (gi here: of chunk c + 1)
+            // (gi and si here: of chunk c + 1)
 #pragma unroll 1
             for (int c = -1; c < chunks; ++c) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
                 const bool next = c + 1 < chunks;
                 auto end_chunk = [&] {
                     fine = fine && wait.warp(kKvDone + (b ^ 1), ((gi - 1) >> 1) & 1);
@@ -448,7 +473,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 }
                 if (next) {
                     const int len = (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)(c + 1) * C);
-                    fine = fine && wait.warp(kGate + b, ph) && wait.warp(kFullK + b, ph) &&
+                    fine = fine && wait.warp(kGate + b, ph) && wait.warp(kFullK + sb, (si >> 1) & 1) &&
                            (len == C || wait.warp(kFullV + b, ph));
                     if (fine) {
                         // channels of this warp's quarter, tokens of its half, 16 x 32 a turn
@@ -462,7 +487,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                                 for (int m = 0; m < 2; ++m) {
                                     const int s = 64 * half + tg + 16 * m;   // first of 16 tokens
                                     uint32_t x[4];
-                                    ldmatrix_t(base + b * M::kQK + M::kK +
+                                    ldmatrix_t(base + sb * M::kQK + M::kK +
                                                    sw128_offset(s + (lane >> 4) * 8 + (lane & 7),
                                                                 32 * quarter + cg + ((lane >> 3) & 1) * 8, C),
                                                x);
@@ -504,18 +529,30 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     end_chunk();
                     if (!ok) break;
                 }
-                if (c < 0 && start.index >= 0 && mine) {
-                    const float *row = (start.in_bnd ? bnd : h0) + start.index * dkdv + (int64_t)i * dv + j0;
-                    if (((uintptr_t)row & 31) == 0) {   // (a state buffer is 16-byte aligned)
+                if (OUT && c < 0) {
+                    if (end_of) fine = put_end() && fine;
+                    const uint32_t fb = first_si & 1;
+                    if (start.index >= 0) fine = fine && wait.warp(kFullK + fb, (first_si >> 1) & 1);
 #pragma unroll
-                        for (int j = 0; j < NC; j += 8) load8(row + j, S + j);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < NC; j += 4) {
-                            const float4 x = *reinterpret_cast<const float4 *>(row + j);
-                            S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+                    for (int j = 0; j < NC; j += 4) {
+                        const int col = j0 + j;
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (fine && start.index >= 0 && mine)
+                            x = *reinterpret_cast<const float4 *>(
+                                sm + fb * M::kQK + (col / 32) * dk * 128 + i * 128 + ((((col % 32) / 4) ^ (i & 7)) << 4));
+                        S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+                    }
+                    if (start.index >= 0) {
+                        ok = bar_and(3, 32 * kStateWarps, fine);
+                        if (!ok) break;
+                        if (tid == 32 * kRowWarps) {
+                            mbar_arrive(&bar[kFreeK + fb]);
+                            mbar_arrive(&bar[kFreeQ + fb]);
                         }
                     }
+                    // the old image's place has held a final state
+                    if (end_of) fine = fine && wait.warp(kEndFree, (ends_before - 1) & 1);
+                    end_of = 0;
                 }
                 if (OUT && next) {   // Q S of the chunk before has read the old image
                     fine = fine && (gi == 0 || wait.warp(kQsDone, (gi - 1) & 1));
@@ -537,25 +574,14 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     }
                 }
                 decay = decay_next;
-                if (next) ++gi;
+                if (next) {
+                    ++gi;
+                    ++si;
+                }
             }
             if (ends) {
-                // for the store warp: S over the last chunk's k (first half of the columns) and
-                // v, in 32-column blocks of 128-byte rows
-                ok = bar_and(3, 32 * kStateWarps, wait.warp(kPvDone, (gi - 1) & 1));
-                if (!ok) break;
-                if (mine) {
-                    uint8_t *at = sm + (half ? M::kV + ((gi - 1) & 1) * M::kVBytes
-                                             : ((gi - 1) & 1) * M::kQK + M::kK);
-#pragma unroll
-                    for (int j = 0; j < NC; j += 4)
-                        *reinterpret_cast<float4 *>(at + (j / 32) * dk * 128 + i * 128 +
-                                                    ((((j % 32) / 4) ^ (i & 7)) << 4)) =
-                            make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kEndReady]);
+                end_of = gi;   // put_end at the next item's start, or after the last
+                ++ends_before;
             }
             if (!OUT && ok && mine) {
                 float *row = bnd + cut_state(range + 1) * dkdv + (int64_t)i * dv + j0;
@@ -563,12 +589,17 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 for (int j = 0; j < NC; j += 4)
                     *reinterpret_cast<float4 *>(row + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
             }
-        } else if (warp == kMmaWarp) {
+        });
+        if (OUT && end_of && ok) ok = put_end();   // (the store warp is waiting for it)
+    } else if (warp == kMmaWarp) {
+        each_item([&](const Item &it, const Start &start, bool ends) {
+            const int chunks = it.c1 - it.c0;
+            if (start.index >= 0) ++si;
             const uint32_t id_kk = idesc_bf16(128, 128, false, false);   // Q K^T
             const uint32_t id_km = idesc_bf16(128, DVP, false, true);    // the others: B is V or S
-            for (int c = 0; c < chunks; ++c, ++gi) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
-                const uint32_t qk = base + b * M::kQK;
+            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
+                const uint32_t qk = base + sb * M::kQK;
                 const uint64_t dq = sdesc_sw128(qk + M::kQ, 16, 1024);
                 const uint64_t dkk = sdesc_sw128(qk + M::kK, 16, 1024);
                 // token-major V and channel-major S: the K dimension is the row
@@ -576,7 +607,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const uint64_t ds = sdesc_sw128(base + M::kS, DKP * 128, 1024);
                 if (OUT) {
                     // P of the chunk before lies over the scores
-                    ok = wait.warp(kFullK + b, ph) && wait.warp(kFullQ + b, ph) &&
+                    ok = wait.warp(kFullK + sb, (si >> 1) & 1) && wait.warp(kFullQ + sb, (si >> 1) & 1) &&
                          (gi == 0 || wait.warp(kPvDone, (gi - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
@@ -594,7 +625,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 tc_fence_after();
                 const uint32_t other = OUT ? 0 : b * kOther;
                 if (elect_one()) {
-                    if (!(ends && c + 1 == chunks)) umma_commit(&bar[kFreeK + b]);   // (Q K^T so far)
+                    umma_commit(&bar[kFreeK + sb]);   // (Q K^T so far)
 #pragma unroll 2
                     for (int s = 0; s < C / 16; ++s)
                         umma_bf16_ts(tKV + other, tHi + other + 8 * s, desc_add(dvt, s * 2048), id_km, s > 0);
@@ -630,18 +661,37 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     __syncwarp();
                 }
             }
-        } else if (warp == kLoadWarp) {
+        });
+    } else if (warp == kLoadWarp) {
+        each_item([&](const Item &it, const Start &start, bool ends) {
+            const int h = it.h, chunks = it.c1 - it.c0;
+            const uint32_t first_si = si;   // a start state's stage
+            if (start.index >= 0) ++si;
             const int hk = h / (p.H / p.Hk);
-            if (start.index >= 0 && lane == 0)   // the state warps read it from there
-                bulk_prefetch_l2((start.in_bnd ? bnd : h0) + start.index * dkdv, (uint32_t)dkdv * 4);
-            for (int c = 0; c < chunks; ++c, ++gi) {
-                const uint32_t b = gi & 1, before = ((gi - 2) >> 1) & 1;
+            if (start.index >= 0) {
+                const uint32_t sb = first_si & 1, before = ((first_si - 2) >> 1) & 1;
+                if (first_si >= 2) ok = wait.warp(kFreeK + sb, before) && wait.warp(kFreeQ + sb, before);
+                if (!ok) return;
+                if (lane == 0) {
+                    uint64_t *full = &bar[kFullK + sb];
+                    mbar_arrive(&bar[kFullQ + sb]);
+                    mbar_arrive_expect_tx(full, (uint32_t)dkdv * 4);
+#pragma unroll 1
+                    for (int x = 0; x < dv / 32; ++x)
+                        tma_load_3d(sm + sb * M::kQK + x * dk * 128, start.in_bnd ? &tbnd : &th0, 32 * x,
+                                    0, start.index, full);
+                }
+                ++issued_k;
+                __syncwarp();
+            }
+            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
+                const uint32_t b = gi & 1, sb = si & 1, before = ((si - 2) >> 1) & 1;
                 const int32_t t0 = (int32_t)(it.t0 + (int64_t)c * C);
-                uint8_t *qk = sm + b * M::kQK;
-                if (gi >= 2) ok = wait.warp(kFreeK + b, before);
+                uint8_t *qk = sm + sb * M::kQK;
+                if (si >= 2) ok = wait.warp(kFreeK + sb, before);
                 if (!ok) break;
                 if (lane == 0) {
-                    uint64_t *full = &bar[kFullK + b];
+                    uint64_t *full = &bar[kFullK + sb];
                     mbar_arrive_expect_tx(full, M::kK);
 #pragma unroll
                     for (int x = 0; x < DKP / 64; ++x)
@@ -649,7 +699,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 }
                 ++issued_k;
                 __syncwarp();
-                if (gi >= 2) ok = wait.warp(kFreeV + b, before);
+                if (gi >= 2) ok = wait.warp(kFreeV + b, ((gi - 2) >> 1) & 1);
                 if (!ok) break;
                 if (lane == 0) {
                     uint64_t *full = &bar[kFullV + b];
@@ -661,22 +711,25 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 ++issued_v;
                 __syncwarp();
                 if (OUT) {
-                    if (gi >= 2) ok = wait.warp(kFreeQ + b, before);
+                    if (si >= 2) ok = wait.warp(kFreeQ + sb, before);
                     if (!ok) break;
                     if (lane == 0) {
-                        uint64_t *full = &bar[kFullQ + b];
+                        uint64_t *full = &bar[kFullQ + sb];
                         mbar_arrive_expect_tx(full, M::kK);
 #pragma unroll
                         for (int x = 0; x < DKP / 64; ++x)
                             tma_load_3d(qk + M::kQ + x * 16384, &tq, 64 * x, hk, t0, full);
                     }
-                    ++issued_q;
+                    issued_q = si + 1;
                     __syncwarp();
                 }
             }
-        } else if (warp == kGateWarp) {
+        });
+    } else if (warp == kGateWarp) {
+        each_item([&](const Item &it, const Start &start, bool ends) {
+            const int h = it.h, chunks = it.c1 - it.c0;
             float log_sum = 0.f;
-            for (int c = 0; c < chunks; ++c, ++gi) {
+            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
                 const uint32_t b = gi & 1;
                 const int64_t t0 = it.t0 + (int64_t)c * C;
                 const int len = (int)min((int64_t)C, it.t1 - t0);
@@ -737,12 +790,16 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 if (lane == 0) mbar_arrive(&bar[kGate + b]);
             }
             if (!OUT && ok && lane == 0) bnd_log[cut_state(range + 1)] = log_sum;
-        } else if (OUT && warp == kStoreWarp) {
-            for (int c = 0; c < chunks; ++c, ++gi) {
-                const uint32_t b = gi & 1;
+        });
+    } else if (OUT && warp == kStoreWarp) {
+        each_item([&](const Item &it, const Start &start, bool ends) {
+            const int h = it.h, chunks = it.c1 - it.c0;
+            if (start.index >= 0) ++si;
+            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
+                const uint32_t b = gi & 1, sb = si & 1;
                 const int64_t t0 = it.t0 + (int64_t)c * C;
                 const int len = (int)min((int64_t)C, it.t1 - t0);
-                const uint32_t so = M::kOverQ ? b * M::kQK + M::kQ : M::kO;
+                const uint32_t so = M::kOverQ ? sb * M::kQK + M::kQ : M::kO;
                 ok = wait.warp(kOFree, gi & 1);
                 if (!ok) break;
                 if (len == C) {
@@ -764,7 +821,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&bar[kFreeQ + b]);
+                    mbar_arrive(&bar[kFreeQ + sb]);
                     mbar_arrive(&bar[kOStored]);
                 }
                 if (ends && c + 1 == chunks) {
@@ -773,20 +830,27 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     ++ends_before;
                     if (lane == 0) {
                         constexpr int kHalf = DVP / 64;   // blocks of a half
-                        for (int x = 0; x < dv / 32; ++x)
-                            tma_store_3d(&thT,
-                                         base + (x < kHalf ? b * M::kQK + M::kK + x * dk * 128
-                                                           : M::kV + b * M::kVBytes + (x - kHalf) * dk * 128),
-                                         32 * x, 0, it.n * p.H + h);
+#pragma unroll 1
+                        for (int x = 0; x < 2 * kHalf; ++x) {
+                            if (32 * x < dv)
+                                tma_store_3d(&thT,
+                                             base + (x < kHalf ? M::kS + x * dk * 128
+                                                               : M::kV + b * M::kVBytes + (x - kHalf) * dk * 128),
+                                             32 * x, 0, it.n * p.H + h);
+                            if (x == kHalf - 1) {   // the image's place first
+                                bulk_commit();
+                                bulk_wait_read_all();
+                                mbar_arrive(&bar[kEndFree]);
+                            }
+                        }
                         bulk_commit();
                         bulk_wait_read_all();
-                        mbar_arrive(&bar[kFreeK + b]);
                         mbar_arrive(&bar[kFreeV + b]);
                     }
                     __syncwarp();
                 }
             }
-        }
+        });
     }
     if (!ok) {
         *abort_flag = 1;
@@ -878,8 +942,8 @@ template <int DKP, int DVP, bool OUT> static cudaError_t allow_smem(int dev) {
 }
 
 template <int DKP, int DVP, bool OUT>
-static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[5], const float *g, int gpt,
-                          const float *h0, int has_hT, void *o, int dk, int dv, float *bnd,
+static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[7], const float *g, int gpt,
+                          int has_h0, int has_hT, void *o, int dk, int dv, float *bnd,
                           float *bnd_log, StatusWord *st, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -887,34 +951,39 @@ static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[5], const float 
     if (e != cudaSuccess) return e;
     la_chunk_tc_kernel<DKP, DVP, OUT>
         <<<OUT ? p.ranges : p.ranges - 1, kThreads, Map<DKP, DVP>::kBytes, s>>>(
-            p, m[0], m[1], m[2], m[3], m[4], g, gpt, h0, has_hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
+            p, m[0], m[1], m[2], m[3], m[4], m[5], m[6], g, gpt, has_h0, has_hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
     return cudaGetLastError();
 }
 
 }  // namespace tc
 }  // namespace la
 
-// The maps of one call: q, k, v, o and, where they are written, the final states.
-cudaError_t la_tensor_maps(CUtensorMap (&m)[5], const void *q, const void *k, const void *v,
-                           const void *o, const float *hT, const la::Plan &p, int64_t T, int dk,
-                           int dv, int64_t qs, int64_t ks, int64_t vs) {
-    memset(&m[4], 0, sizeof m[4]);
+// The maps of one call: q, k, v, o and, where they are used, the initial and the final states
+// and those at the cuts.
+cudaError_t la_tensor_maps(CUtensorMap (&m)[7], const void *q, const void *k, const void *v,
+                           const void *o, const float *h0, const float *hT, const float *bnd,
+                           const la::Plan &p, int64_t T, int dk, int dv, int64_t qs, int64_t ks,
+                           int64_t vs) {
+    memset(&m[4], 0, 3 * sizeof m[4]);
+    const int64_t nh = (int64_t)p.N * p.H;
     cudaError_t e = la::tc::tensor_map(&m[0], q, T, p.Hk, dk, qs);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[1], k, T, p.Hk, dk, ks);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[2], v, T, p.H, dv, vs);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[3], o, T, p.H, dv, (int64_t)p.H * dv);
-    if (e == cudaSuccess && hT) e = la::tc::state_map(&m[4], hT, (int64_t)p.N * p.H, dk, dv);
+    if (e == cudaSuccess && h0) e = la::tc::state_map(&m[4], h0, nh, dk, dv);
+    if (e == cudaSuccess && hT) e = la::tc::state_map(&m[5], hT, nh, dk, dv);
+    if (e == cudaSuccess && bnd) e = la::tc::state_map(&m[6], bnd, 2 * (int64_t)p.ranges, dk, dv);
     return e;
 }
 
-cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[5], const float *g,
-                         int gpt, const float *h0, int has_hT, void *o, int dk, int dv, float *bnd,
+cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[7], const float *g,
+                         int gpt, int has_h0, int has_hT, void *o, int dk, int dv, float *bnd,
                          float *bnd_log, StatusWord *st, cudaStream_t s) {
 #define KDA_LA(DK_, DV_)                                                                          \
     if ((dk <= 64) == (DK_ == 64) && (dv <= 64) == (DV_ == 64))                                   \
-        return out ? la::tc::launch<DK_, DV_, true>(p, m, g, gpt, h0, has_hT, o, dk, dv, bnd, bnd_log, \
+        return out ? la::tc::launch<DK_, DV_, true>(p, m, g, gpt, has_h0, has_hT, o, dk, dv, bnd, bnd_log, \
                                                     st, s)                                        \
-                   : la::tc::launch<DK_, DV_, false>(p, m, g, gpt, h0, has_hT, o, dk, dv, bnd, bnd_log, \
+                   : la::tc::launch<DK_, DV_, false>(p, m, g, gpt, has_h0, has_hT, o, dk, dv, bnd, bnd_log, \
                                                      st, s);
     KDA_LA(64, 64) KDA_LA(64, 128) KDA_LA(128, 64) KDA_LA(128, 128)
 #undef KDA_LA
