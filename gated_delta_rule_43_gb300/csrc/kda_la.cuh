@@ -3,7 +3,8 @@
 // A unit is one head of one sequence, a run of 128-token chunks; the units of all sequences,
 // heads inside sequences, stand in one row of `total` chunks.  The row is cut into `ranges`
 // equal parts, one for each CTA (CTA group on the CUDA cores), wherever that falls: every SM
-// has the same work whatever the lengths are.  A cut inside a unit is an inner boundary: a
+// has the same work whatever the lengths are.  (A unit counts as `unit_cost` chunks more than it
+// has, for its states.)  A cut inside a unit is an inner boundary: a
 // first pass forms the state that the tokens before it, back to the unit's start or the cut
 // before, leave there; a scan along the cuts of each unit turns these into the states at the
 // cuts; and the output pass starts its ranges from them.
@@ -25,7 +26,8 @@ constexpr int kWhole = 8;
 // A place in the row of chunks: before chunk c of head h of sequence n.
 struct Cut {
     int64_t x;
-    int32_t n, h, c, inner;   // inner: inside a unit (c > 0)
+    int32_t n, h, c;
+    int32_t inner;            // inside a unit: 1 + the inner cuts of this unit that follow; else 0
 };
 
 struct Plan {
@@ -83,6 +85,29 @@ struct Walk {
         return true;
     }
 };
+
+// Programmatic launches: a kernel may be on the GPU before the one that it depends on has ended.
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                                cudaStream_t s, A... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 
 // What the range before cut `i` (1 ..) contributes to it; false when that cut is none inside
 // a unit.

@@ -15,7 +15,7 @@ namespace la {
 // ------------------------------------------------------------------------- plan
 // CTA 0: validates cu_seqlens (see plan_chunks_kernel), counts chunks and places the cuts.
 // Every CTA: final states of sequences without tokens (S_out not NULL).
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 256, kMaxRanges = 1024;
 
 // The largest n with off[n] * H <= x, for x < off[N] * H: entry n spans x.
 __device__ __forceinline__ int owner(const int32_t *off, int N, int H, int64_t x) {
@@ -29,7 +29,10 @@ __device__ __forceinline__ int owner(const int32_t *off, int N, int H, int64_t x
 
 __device__ Cut place(const int32_t *off, int N, int H, int64_t total, int64_t x) {
     Cut r{x, N, 0, 0, 0};
-    if (x >= total) return r;
+    if (x >= total) {
+        r.x = total;
+        return r;
+    }
     r.n = owner(off, N, H, x);
     const int64_t nc = off[r.n + 1] - off[r.n], rest = x - (int64_t)off[r.n] * H;
     r.h = (int)(rest / nc);
@@ -45,7 +48,8 @@ __device__ __forceinline__ int pieces(int nc, int split) {
 
 __global__ void __launch_bounds__(kPlanThreads)
 la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *off,
-               int32_t *piece_off, Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *S_out, int H,
+               int32_t *piece_off, int32_t *cost_off, int unit_cost, Cut *cuts, int ranges, int split,
+               StatusWord *st, const float *h0, float *S_out, int H,
                int64_t dkdv4) {
     if (S_out) {
         for (int64_t nh = blockIdx.x; nh < (int64_t)N * H; nh += gridDim.x) {
@@ -58,9 +62,11 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
                 dst[i] = src ? src[i] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
+    let_next_start();
     if (blockIdx.x != 0) return;
+    __shared__ Cut s_cut[kMaxRanges + 1];
     constexpr int NW = kPlanThreads / 32;
-    __shared__ int2 s_warp[NW];
+    __shared__ int3 s_warp[NW];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     if (tid == 0) {
         st->code = 0u;
@@ -69,10 +75,11 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
     }
     __syncthreads();
     if (tid == 0 && (cu[0] != 0 || (int64_t)cu[N] != T_tot)) report(st, KDA_ERR_SEQLENS, N, 1);
-    int2 carry = make_int2(0, 0);   // chunks, pieces
+    int3 carry = make_int3(0, 0, 0);   // chunks, pieces, costs
+    auto add = [](int3 &x, const int3 &y) { x.x += y.x; x.y += y.y; x.z += y.z; };
     for (int base = 0; base < N; base += kPlanThreads) {
         const int n = base + tid;
-        int2 own = make_int2(0, 0);
+        int3 own = make_int3(0, 0, 0);
         if (n < N) {
             const int64_t b = cu[n], e = cu[n + 1];
             if (b < 0 || e < b || e > T_tot)
@@ -80,39 +87,38 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
             else
                 own.x = (int)((e - b + kChunk - 1) / kChunk);
             own.y = pieces(own.x, split);
+            own.z = own.x ? own.x + unit_cost : 0;
         }
-        int2 x = own;   // inclusive warp scan
+        int3 x = own;   // inclusive warp scan
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x.x, o), z = __shfl_up_sync(0xffffffffu, x.y, o);
-            if (lane >= o) {
-                x.x += y;
-                x.y += z;
-            }
+            const int3 y = make_int3(__shfl_up_sync(0xffffffffu, x.x, o),
+                                     __shfl_up_sync(0xffffffffu, x.y, o),
+                                     __shfl_up_sync(0xffffffffu, x.z, o));
+            if (lane >= o) add(x, y);
         }
         if (lane == 31) s_warp[wid] = x;
         __syncthreads();
-        int2 before = carry;
+        int3 before = carry;
         for (int w = 0; w < NW; ++w) {
-            if (w < wid) {
-                before.x += s_warp[w].x;
-                before.y += s_warp[w].y;
-            }
-            carry.x += s_warp[w].x;
-            carry.y += s_warp[w].y;
+            if (w < wid) add(before, s_warp[w]);
+            add(carry, s_warp[w]);
         }
         if (n < N) {
             off[n] = before.x + x.x - own.x;
             piece_off[n] = before.y + x.y - own.y;
+            cost_off[n] = before.z + x.z - own.z;
         }
         __syncthreads();
     }
     if (tid == 0) {
         off[N] = carry.x;
         piece_off[N] = carry.y;
+        cost_off[N] = carry.z;
     }
     __syncthreads();
     const int64_t total = (int64_t)carry.x * H, fine = (int64_t)carry.y * H;
+    const int64_t cost = (int64_t)carry.z * H;
     // SMs to spare: every unit gets its own range, a long one several.  Else equal parts
     // (without a first pass nothing can be cut: the units are dealt out whole).
     const bool spare = fine <= ranges && total < (int64_t)ranges * kMinRange;
@@ -128,13 +134,29 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
             }
             r = place(off, N, H, total, x);
         } else {
-            r = place(off, N, H, total, (int64_t)i * total / ranges);
+            const int64_t y = (int64_t)i * cost / ranges;
+            int64_t x = total;
+            if (y < cost) {
+                const int n = owner(cost_off, N, H, y);
+                const int64_t nc = off[n + 1] - off[n], m = nc + unit_cost;
+                const int64_t rest = y - (int64_t)cost_off[n] * H, c = rest % m - unit_cost;
+                x = (int64_t)off[n] * H + rest / m * nc + (c > 0 ? c : 0);
+            }
+            r = place(off, N, H, total, x);
             if (r.inner) {
                 const int nc = off[r.n + 1] - off[r.n];
                 if (!split || nc <= kWhole)
                     r = place(off, N, H, total, r.x + (2 * r.c >= nc ? nc - r.c : -r.c));
             }
         }
+        s_cut[i] = r;
+    }
+    __syncthreads();
+    for (int i = tid; i <= ranges; i += kPlanThreads) {
+        Cut r = s_cut[i];
+        if (r.inner)
+            for (int j = i + 1; j < ranges && s_cut[j].inner && s_cut[j].n == r.n && s_cut[j].h == r.h; ++j)
+                ++r.inner;
         cuts[i] = r;
     }
 }
@@ -147,16 +169,15 @@ constexpr int kScanThreads = 256, kAhead = 8;
 __global__ void __launch_bounds__(kScanThreads)
 la_scan_kernel(Plan p, const float *__restrict__ h0, float *__restrict__ bnd,
                const float *__restrict__ bnd_log, int64_t dkdv4) {
+    wait_for_previous();
+    let_next_start();
     const int first = blockIdx.y + 1;
     const Cut f = p.cuts[first];
     // a unit's chain starts at its first cut: the range before it holds the unit's start
     if (!f.inner || p.cuts[first - 1].x > f.x - f.c) return;
     const int64_t i = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
     if (i >= dkdv4) return;
-    int last = first;
-    while (last + 1 < p.ranges && p.cuts[last + 1].inner && p.cuts[last + 1].n == f.n &&
-           p.cuts[last + 1].h == f.h)
-        ++last;
+    const int last = first + f.inner - 1;
     float4 S = h0 ? reinterpret_cast<const float4 *>(h0)[((int64_t)f.n * p.H + f.h) * dkdv4 + i]
                   : make_float4(0.f, 0.f, 0.f, 0.f);
     float4 *at = reinterpret_cast<float4 *>(bnd) + i;
@@ -382,14 +403,14 @@ static cudaError_t launch_dims(bool out, const Plan &p, const float *q, const fl
 
 }  // namespace la
 
-cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off,
-                           int32_t *piece_off, la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
+cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off, int unit_cost,
+                           la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
                            int H, int64_t dkdv, cudaStream_t s) {
     float *S_out = hT != h0 ? hT : nullptr;   // an in-place update leaves empty ones as they are
     const int64_t nh = (int64_t)N * H;
     const int grid = S_out && nh > 1 ? (int)(nh < 256 ? nh : 256) : 1;
-    la::la_plan_kernel<<<grid, la::kPlanThreads, 0, s>>>(cu, N, T_tot, off, piece_off, cuts, ranges,
-                                                        split, st, h0, S_out, H, dkdv / 4);
+    la::la_plan_kernel<<<grid, la::kPlanThreads, 0, s>>>(
+        cu, N, T_tot, off, off + N + 1, off + 2 * (N + 1), unit_cost, cuts, ranges, split, st, h0, S_out, H, dkdv / 4);
     return cudaGetLastError();
 }
 
@@ -397,8 +418,8 @@ cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const
                            int64_t dkdv, cudaStream_t s) {
     const dim3 grid((unsigned)((dkdv / 4 + la::kScanThreads - 1) / la::kScanThreads),
                     (unsigned)(p.ranges - 1));
-    la::la_scan_kernel<<<grid, la::kScanThreads, 0, s>>>(p, h0, bnd, bnd_log, dkdv / 4);
-    return cudaGetLastError();
+    return la::launch_after(la::la_scan_kernel, grid, dim3(la::kScanThreads), 0, s, p, h0, bnd, bnd_log,
+                            dkdv / 4);
 }
 
 cudaError_t launch_la_simt(bool out, int dk, int dv, const la::Plan &p, const float *q,

@@ -224,7 +224,8 @@ template <int DKP, int DVP, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                   const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap th0,
+                   const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap to8,
+                   const __grid_constant__ CUtensorMap th0,
                    const __grid_constant__ CUtensorMap thT, const __grid_constant__ CUtensorMap tbnd,
                    const float *__restrict__ g, int g_per_token, int has_h0, int has_hT,
                    __nv_bfloat16 *__restrict__ o, int dk, int dv, float *__restrict__ bnd,
@@ -233,6 +234,8 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     using M = Map<DKP, DVP>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int range = blockIdx.x;
+    wait_for_previous();
+    let_next_start();
     if (OUT ? p.cuts[range].x >= p.cuts[range + 1].x : !p.cuts[range + 1].inner) return;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + M::kBar);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + M::kBar + kBars * 8);
@@ -810,13 +813,23 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         bulk_commit();
                         bulk_wait_read_all();
                     }
-                } else {   // rows past the sequence belong to others
-                    const int per = dv / 8;   // 16-byte pieces of a row
-                    for (int x = lane; x < len * per; x += 32) {
+                } else {   // rows past the sequence belong to others: eight at a time, then single
+                    const int eights = len & ~7, per = dv / 8;   // per: 16-byte pieces of a row
+                    if (lane == 0) {
+#pragma unroll 1
+                        for (int r = 0; r < eights; r += 8)
+#pragma unroll
+                            for (int x = 0; x < DVP / 64; ++x)
+                                tma_store_3d(&to8, base + so + x * 16384 + r * 128, 64 * x, h, (int32_t)t0 + r);
+                        bulk_commit();
+                    }
+#pragma unroll 1
+                    for (int x = eights * per + lane; x < len * per; x += 32) {
                         const int r = x / per, j = 8 * (x - r * per);
                         *reinterpret_cast<uint4 *>(o + ((t0 + r) * p.H + h) * (int64_t)dv + j) =
                             *reinterpret_cast<const uint4 *>(sm + so + sw128_offset(r, j, C));
                     }
+                    if (lane == 0) bulk_wait_read_all();
                     fence_proxy_async();   // before q of a later chunk takes the place
                 }
                 __syncwarp();
@@ -911,14 +924,14 @@ static cudaError_t encode(CUtensorMap *m, CUtensorMapDataType type, const void *
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// [T, heads, D] bf16, tokens `stride` elements apart, in boxes of 128 tokens x 1 head x 64
+// [T, heads, D] bf16, tokens `stride` elements apart, in boxes of `rows` tokens x 1 head x 64
 // channels with the 128-byte swizzle; what lies outside (channels of 32-wide heads, tokens
 // past the last) reads as zeros.
 static cudaError_t tensor_map(CUtensorMap *m, const void *x, int64_t T, int heads, int D,
-                              int64_t stride) {
+                              int64_t stride, int rows = C) {
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x,
                   {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T},
-                  {(cuuint64_t)D * 2, (cuuint64_t)stride * 2}, {64, 1, C});
+                  {(cuuint64_t)D * 2, (cuuint64_t)stride * 2}, {64, 1, (cuuint32_t)rows});
 }
 
 // [states, dk, dv] fp32 in boxes of one state's rows x 32 columns
@@ -942,17 +955,16 @@ template <int DKP, int DVP, bool OUT> static cudaError_t allow_smem(int dev) {
 }
 
 template <int DKP, int DVP, bool OUT>
-static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[7], const float *g, int gpt,
+static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[8], const float *g, int gpt,
                           int has_h0, int has_hT, void *o, int dk, int dv, float *bnd,
                           float *bnd_log, StatusWord *st, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = allow_smem<DKP, DVP, OUT>(dev);
     if (e != cudaSuccess) return e;
-    la_chunk_tc_kernel<DKP, DVP, OUT>
-        <<<OUT ? p.ranges : p.ranges - 1, kThreads, Map<DKP, DVP>::kBytes, s>>>(
-            p, m[0], m[1], m[2], m[3], m[4], m[5], m[6], g, gpt, has_h0, has_hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
-    return cudaGetLastError();
+    return launch_after(la_chunk_tc_kernel<DKP, DVP, OUT>, dim3(OUT ? p.ranges : p.ranges - 1),
+                        dim3(kThreads), Map<DKP, DVP>::kBytes, s, p, m[0], m[1], m[2], m[3], m[4], m[5],
+                        m[6], m[7], g, gpt, has_h0, has_hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
 }
 
 }  // namespace tc
@@ -960,23 +972,24 @@ static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[7], const float 
 
 // The maps of one call: q, k, v, o and, where they are used, the initial and the final states
 // and those at the cuts.
-cudaError_t la_tensor_maps(CUtensorMap (&m)[7], const void *q, const void *k, const void *v,
+cudaError_t la_tensor_maps(CUtensorMap (&m)[8], const void *q, const void *k, const void *v,
                            const void *o, const float *h0, const float *hT, const float *bnd,
                            const la::Plan &p, int64_t T, int dk, int dv, int64_t qs, int64_t ks,
                            int64_t vs) {
-    memset(&m[4], 0, 3 * sizeof m[4]);
+    memset(&m[5], 0, 3 * sizeof m[5]);
     const int64_t nh = (int64_t)p.N * p.H;
     cudaError_t e = la::tc::tensor_map(&m[0], q, T, p.Hk, dk, qs);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[1], k, T, p.Hk, dk, ks);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[2], v, T, p.H, dv, vs);
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[3], o, T, p.H, dv, (int64_t)p.H * dv);
-    if (e == cudaSuccess && h0) e = la::tc::state_map(&m[4], h0, nh, dk, dv);
-    if (e == cudaSuccess && hT) e = la::tc::state_map(&m[5], hT, nh, dk, dv);
-    if (e == cudaSuccess && bnd) e = la::tc::state_map(&m[6], bnd, 2 * (int64_t)p.ranges, dk, dv);
+    if (e == cudaSuccess) e = la::tc::tensor_map(&m[4], o, T, p.H, dv, (int64_t)p.H * dv, 8);
+    if (e == cudaSuccess && h0) e = la::tc::state_map(&m[5], h0, nh, dk, dv);
+    if (e == cudaSuccess && hT) e = la::tc::state_map(&m[6], hT, nh, dk, dv);
+    if (e == cudaSuccess && bnd) e = la::tc::state_map(&m[7], bnd, 2 * (int64_t)p.ranges, dk, dv);
     return e;
 }
 
-cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[7], const float *g,
+cudaError_t launch_la_tc(bool out, const la::Plan &p, const CUtensorMap (&m)[8], const float *g,
                          int gpt, int has_h0, int has_hT, void *o, int dk, int dv, float *bnd,
                          float *bnd_log, StatusWord *st, cudaStream_t s) {
 #define KDA_LA(DK_, DV_)                                                                          \
