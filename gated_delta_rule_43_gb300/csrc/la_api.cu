@@ -34,7 +34,7 @@ cudaError_t launch_qk(int dtype, int D, const void *q, const void *k, void *qo, 
                       float q_scale, float k_scale, const int32_t *pos, const float *inv_freq,
                       int rot, int interleaved, float rope_scale, int sms, cudaStream_t s);
 cudaError_t launch_pool_copy(float *p, int P, int64_t elems, const int32_t *src,
-                             const int32_t *dst, int n, StatusWord *st, int sms, cudaStream_t s);
+                             const int32_t *dst, int n, StatusWord *st, cudaStream_t s);
 cudaError_t launch_pool_compact(float *p, int P, int64_t elems, const uint8_t *live,
                                 int32_t *new_index, int32_t *n_live, int32_t *moves, int sms,
                                 cudaStream_t s);
@@ -279,7 +279,7 @@ kda_status kda_state_pool_copy(float *pool, int32_t P, int64_t slot_elems,
         return KDA_ERR_CUDA;
     if (n == 0) return KDA_OK;
     return cuda_status(launch_pool_copy(pool, P, slot_elems, src_idx, dst_idx, n,
-                                        (StatusWord *)workspace, sm_count(), s));
+                                        (StatusWord *)workspace, s));
 }
 
 kda_status kda_state_pool_compact(float *pool, int32_t P, int64_t slot_elems,

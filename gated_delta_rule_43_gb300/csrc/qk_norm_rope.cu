@@ -6,9 +6,10 @@
 //   half layout        channels 8 j .. 8 j + 7 and rot / 2 + 8 j .. of the rotated part
 //   interleaved        channels 16 j .. 16 j + 15
 //   past the rotated part, channels rot + 16 j' .. (no rotation)
-// so a norm is two shuffles-and-adds deep and there is no shared memory.  A warp keeps to
-// one token while it goes through that token's heads: the eight cosines and sines of a lane
-// are worked out once a token.
+// so a norm is a few shuffles deep and rotation needs none.  A CTA takes the heads (or a part of
+// them) of a few tokens: first each thread works out one angle's cosine and sine, which the
+// heads of a token share, into shared memory; then each warp goes through rows, the loads of
+// kAhead rows in flight.
 //
 // The rotation's angle is a whole number of turns plus a fraction, and only the fraction
 // counts.  The rate in turns per position is held as a 64-bit binary fraction, so position *
@@ -21,6 +22,8 @@ namespace kda {
 namespace qk {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kTokens = 4;   // of a CTA, at most: kThreads angles of 64 pairs
+constexpr int kAhead = 2;
 
 struct Side {
     const void *x;
@@ -31,20 +34,31 @@ struct Side {
     float scale;
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&u);
+// Eight channels as they lie in memory, and as fp32
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(b[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __bfloat1622float2(b[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
     }
-}
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+};
+template <> struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
     uint4 u;
     __nv_bfloat162 *b = reinterpret_cast<__nv_bfloat162 *>(&u);
@@ -74,80 +88,102 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
     return (b >> 31) ? 0u - r : r;
 }
 
-// A warp takes (token, part of its heads) units; `parts` units share a token.
+// CTA x: tokens [t0, t0 + tokens) of group x / parts, heads [h0, h1) of part x % parts.
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads)
-qk_norm_rope_kernel(Side q, Side k, int64_t units, int parts, int norm, float eps,
+qk_norm_rope_kernel(Side q, Side k, int64_t T_tot, int tokens, int parts, int norm, float eps,
                     const int32_t *__restrict__ positions, const float *__restrict__ inv_freq,
                     int rot, int interleaved, float rope_scale) {
     constexpr int LPR = D / 16;      // lanes per head
     constexpr int RPW = 32 / LPR;    // heads a warp holds at a time
+    __shared__ __align__(16) float s_cos[kTokens][D / 2], s_sin[kTokens][D / 2];
+    const int64_t t0 = (int64_t)(blockIdx.x / parts) * tokens;
+    const int part = blockIdx.x % parts;
+    const int here = (int)min((int64_t)tokens, T_tot - t0), pairs = rot / 2;
+    for (int x = threadIdx.x; x < here * pairs; x += kThreads) {
+        const int t = x / pairs, i = x - t * pairs;
+        // position * turns modulo 2^64: the angle's fraction of a turn, in [-1/2, 1/2)
+        const int64_t pos = positions[t0 + t];
+        const int64_t f = (int64_t)((uint64_t)pos * turn_fraction(inv_freq[i]));
+        float c, sn;
+        sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &sn, &c);   // 2^-31
+        s_cos[t][i] = c * rope_scale;
+        s_sin[t][i] = sn * rope_scale;
+    }
+    __syncthreads();
     const int lane = threadIdx.x & 31, j = lane % LPR, row = lane / LPR;
     const bool turned = 16 * j < rot;
     const int c0 = turned ? (interleaved ? 16 * j : 8 * j) : 16 * j;
     const int c1 = turned ? (interleaved ? c0 + 8 : rot / 2 + c0) : c0 + 8;
-    // turns per position of this lane's eight pairs, as fractions of 2^64
-    uint64_t rate[8];
-    if (turned) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rate[i] = turn_fraction(inv_freq[8 * j + i]);
-    }
     const int all = q.heads + k.heads;
-    for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units;
-         u += (int64_t)gridDim.x * kWarps) {
-        const int64_t t = u / parts;
-        const int part = (int)(u - t * parts);
-        float cs[8], sn[8];
-        if (turned) {
-            const int64_t pos = positions[t];
+    const int h0 = (int)((int64_t)all * part / parts), h1 = (int)((int64_t)all * (part + 1) / parts);
+    const int rows = here * (h1 - h0);
+    for (int r0 = (threadIdx.x >> 5) * RPW * kAhead; r0 < rows; r0 += kWarps * RPW * kAhead) {
+        Raw<T> xa[kAhead], xb[kAhead];
+        T *dst[kAhead];
+        int tok[kAhead];
+        bool is_k[kAhead];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // the product modulo 2^64 is the angle's fraction of a turn in [-1/2, 1/2)
-                const int64_t f = (int64_t)((uint64_t)pos * rate[i]);
-                sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &sn[i], &cs[i]);   // 2^-31
-                cs[i] *= rope_scale;
-                sn[i] *= rope_scale;
+        for (int m = 0; m < kAhead; ++m) {
+            const int r = r0 + m * RPW + row;
+            tok[m] = -1;
+            dst[m] = nullptr;
+            is_k[m] = false;
+            xa[m] = Raw<T>{};
+            xb[m] = Raw<T>{};
+            if (r < rows) {
+                tok[m] = r / (h1 - h0);
+                const int h = h0 + r - tok[m] * (h1 - h0);
+                is_k[m] = h >= q.heads;
+                const Side &s = is_k[m] ? k : q;
+                const int64_t t = t0 + tok[m], hh = is_k[m] ? h - q.heads : h;
+                const T *src = (const T *)s.x + t * s.xs + hh * D;
+                dst[m] = (T *)s.y + t * s.ys + hh * D;
+                xa[m].load(src + c0);
+                xb[m].load(src + c1);
             }
         }
-        for (int h = part * RPW + row; h - row < all; h += parts * RPW) {
-            const bool here = h < all;
-            const bool is_k = h >= q.heads;
-            const Side &s = is_k ? k : q;
-            const int hh = is_k ? h - q.heads : h;
-            float a[8], b[8];
-            if (here) {
-                const T *x = (const T *)s.x + t * s.xs + (int64_t)hh * D;
-                load8(x + c0, a);
-                load8(x + c1, b);
-            } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.f;
-            }
+        for (int m = 0; m < kAhead; ++m) {
+            float a[8], b[8];
+            xa[m].get(a);
+            xb[m].get(b);
+            const float *w = is_k[m] ? k.w : q.w;
+            float scale = is_k[m] ? k.scale : q.scale;
             if (norm != KDA_NORM_NONE) {
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum += a[i] * a[i] + b[i] * b[i];
 #pragma unroll
                 for (int d = LPR / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const float r = rsqrtf((norm == KDA_NORM_RMS ? sum * (1.f / D) : sum) + eps);
+                const float n = rsqrtf((norm == KDA_NORM_RMS ? sum * (1.f / D) : sum) + eps);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    a[i] *= r;
-                    b[i] *= r;
+                    a[i] *= n;
+                    b[i] *= n;
                 }
             }
-            if (!here) continue;
-            if (s.w) {
-                float wa[8], wb[8];
-                load8(s.w + c0, wa);
-                load8(s.w + c1, wb);
+            if (tok[m] < 0) continue;
+            if (w) {
+                Raw<float> wa, wb;
+                wa.load(w + c0);
+                wb.load(w + c1);
+                float fa[8], fb[8];
+                wa.get(fa);
+                wb.get(fb);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    a[i] *= wa[i];
-                    b[i] *= wb[i];
+                    a[i] *= fa[i];
+                    b[i] *= fb[i];
                 }
             }
             if (turned) {
+                Raw<float> rc, rs;
+                rc.load(&s_cos[tok[m]][8 * j]);
+                rs.load(&s_sin[tok[m]][8 * j]);
+                float cs[8], sn[8];
+                rc.get(cs);
+                rs.get(sn);
                 if (interleaved) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -168,12 +204,11 @@ qk_norm_rope_kernel(Side q, Side k, int64_t units, int parts, int norm, float ep
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                a[i] *= s.scale;
-                b[i] *= s.scale;
+                a[i] *= scale;
+                b[i] *= scale;
             }
-            T *y = (T *)s.y + t * s.ys + (int64_t)hh * D;
-            store8(y + c0, a);
-            store8(y + c1, b);
+            store8(dst[m] + c0, a);
+            store8(dst[m] + c1, b);
         }
     }
 }
@@ -182,15 +217,18 @@ template <int D, typename T>
 static cudaError_t launch_dims(const Side &q, const Side &k, int64_t T_tot, int norm, float eps,
                                const int32_t *pos, const float *inv_freq, int rot, int interleaved,
                                float rope_scale, int sms, cudaStream_t s) {
-    constexpr int RPW = 32 / (D / 16);
-    // a token's heads go to one warp, unless there are too few tokens to fill the SMs
-    const int64_t most = (q.heads + k.heads + RPW - 1) / RPW;
-    int64_t parts = (8LL * kWarps * sms + T_tot - 1) / T_tot;
-    parts = parts < 1 ? 1 : parts > most ? most : parts;
-    const int64_t units = T_tot * parts, blocks = (units + kWarps - 1) / kWarps;
-    const int64_t cap = 8LL * sms;
-    qk_norm_rope_kernel<D, T><<<(unsigned)(blocks < cap ? blocks : cap), kThreads, 0, s>>>(
-        q, k, units, (int)parts, norm, eps, pos, inv_freq, rot, interleaved, rope_scale);
+    constexpr int kRows = kWarps * (32 / (D / 16)) * kAhead;   // of a CTA's turn
+    // Several tokens a CTA while that leaves four CTAs an SM, and a token's heads over several
+    // CTAs (each works out the token's angles again) while there are fewer than two.
+    int tokens = kTokens;
+    while (tokens > 1 && (T_tot + tokens - 1) / tokens < 4LL * sms) tokens >>= 1;
+    const int64_t groups = (T_tot + tokens - 1) / tokens, all = q.heads + k.heads;
+    const int64_t most = (all * tokens + kRows - 1) / kRows;
+    int64_t parts = (2LL * sms + groups - 1) / groups;
+    parts = parts > most ? most : parts;
+    if (groups * parts > 0x7fffffffLL) return cudaErrorInvalidValue;
+    qk_norm_rope_kernel<D, T><<<(unsigned)(groups * parts), kThreads, 0, s>>>(
+        q, k, T_tot, tokens, (int)parts, norm, eps, pos, inv_freq, rot, interleaved, rope_scale);
     return cudaGetLastError();
 }
 

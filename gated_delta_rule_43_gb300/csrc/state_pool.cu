@@ -9,7 +9,8 @@ namespace kda {
 namespace pool {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;   // 16-byte loads a thread has in flight
+constexpr int kAhead = 8;   // 16-byte loads a thread has in flight
+constexpr int kPart = kThreads * kAhead;   // 16-byte values of a task: 32 KB
 
 // vec4 values [begin, end) of one slot
 __device__ __forceinline__ void copy_part(float4 *dst, const float4 *src, int64_t begin,
@@ -26,30 +27,46 @@ __device__ __forceinline__ void copy_part(float4 *dst, const float4 *src, int64_
     }
 }
 
-// Copies src_idx[i] -> dst_idx[i] for i < n (n_dev[0] where the count is on the device),
-// each as `parts` parts.  With `check`, a copy whose indices break the rules is left out:
-// every CTA looks through the n indices for another copy with this destination, or one that
-// reads it.
+// Copy i = task / parts of n, its part task % parts: a CTA a task.  A copy whose indices break
+// the rules is left out: every CTA looks through the n indices for another copy with this
+// destination, or one that reads it.
 __global__ void __launch_bounds__(kThreads)
 copy_kernel(float4 *__restrict__ pool, int P, int64_t vecs, const int32_t *__restrict__ src_idx,
-            const int32_t *__restrict__ dst_idx, int n, const int32_t *__restrict__ n_dev,
-            int parts, int check, StatusWord *st) {
-    const int64_t count = n_dev ? *n_dev : n;
-    const int64_t per = (vecs + parts - 1) / parts;
-    for (int64_t task = blockIdx.x; task < count * parts; task += gridDim.x) {
-        const int64_t i = task / parts, part = task - i * parts;
-        const int src = src_idx[i], dst = dst_idx[i];
-        if (check) {
-            bool bad = src < -1 || src >= P || dst < 0 || dst >= P;
-            for (int64_t m = threadIdx.x; m < count && !bad; m += kThreads)
-                bad = m != i && (dst_idx[m] == dst || src_idx[m] == dst);
-            if (__syncthreads_or(bad)) {
-                if (threadIdx.x == 0 && part == 0) report(st, KDA_ERR_INVALID_ARG, i, 32);
-                continue;
-            }
-        }
-        if (src == dst) continue;
-        copy_part(pool + dst * vecs, src >= 0 ? pool + src * vecs : nullptr, part * per,
+            const int32_t *__restrict__ dst_idx, int n, int parts, int64_t per, StatusWord *st) {
+    const int64_t i = blockIdx.x / parts, part = blockIdx.x - i * parts;
+    const int src = src_idx[i], dst = dst_idx[i];
+    bool bad = src < -1 || src >= P || dst < 0 || dst >= P;
+    for (int m = threadIdx.x; m < n && !bad; m += kThreads)
+        bad = m != i && (dst_idx[m] == dst || src_idx[m] == dst);
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0 && part == 0) report(st, KDA_ERR_INVALID_ARG, i, 32);
+        return;
+    }
+    if (src == dst) return;
+    copy_part(pool + dst * vecs, src >= 0 ? pool + src * vecs : nullptr, part * per,
+              min(vecs, (part + 1) * per));
+}
+
+// The moves that plan_kernel found.  Their number is on the device, so the CTAs of a fixed grid
+// draw tasks from a counter.
+struct Moves {
+    int32_t count;
+    uint32_t next;     // task to be drawn
+};
+__global__ void __launch_bounds__(kThreads)
+move_kernel(float4 *__restrict__ pool, int64_t vecs, Moves *moves, const int32_t *__restrict__ src_idx,
+            const int32_t *__restrict__ dst_idx, int parts, int64_t per) {
+    __shared__ uint32_t s_task;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // (plan_kernel)
+    const uint32_t tasks = (uint32_t)moves->count * (uint32_t)parts;
+    while (true) {
+        __syncthreads();
+        if (threadIdx.x == 0) s_task = atomicAdd(&moves->next, 1u);
+        __syncthreads();
+        const uint32_t task = s_task;
+        if (task >= tasks) return;
+        const uint32_t i = task / parts, part = task - i * parts;
+        copy_part(pool + dst_idx[i] * vecs, pool + src_idx[i] * vecs, part * per,
                   min(vecs, (part + 1) * per));
     }
 }
@@ -59,7 +76,8 @@ constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const uint8_t *__restrict__ live, int P, int32_t *__restrict__ new_index,
             int32_t *__restrict__ n_live, int32_t *__restrict__ src_idx,
-            int32_t *__restrict__ dst_idx, int32_t *__restrict__ n_moves) {
+            int32_t *__restrict__ dst_idx, Moves *__restrict__ moves) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int s_holes[32], s_movers[32], s_total;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     int mine = 0;
@@ -102,44 +120,55 @@ plan_kernel(const uint8_t *__restrict__ live, int P, int32_t *__restrict__ new_i
     for (int m = tid; m < movers; m += kPlanThreads) new_index[src_idx[m]] = dst_idx[m];
     if (tid == 0) {
         *n_live = L;
-        *n_moves = movers;
+        moves->count = movers;
+        moves->next = 0;
     }
 }
 
-// Parts per slot: about four tasks an SM, and no part under 16 KB
-static int parts_of(int64_t vecs, int64_t copies, int sms) {
-    const int64_t want = (4LL * sms + copies - 1) / (copies > 0 ? copies : 1);
-    const int64_t most = vecs / 1024;
-    const int64_t p = want < most ? want : most;
-    return (int)(p < 1 ? 1 : p);
+// 16-byte values a task copies: 32 KB, more where a task first looks through many indices
+static int64_t part_of(int64_t vecs, int64_t looked_through) {
+    const int64_t p = looked_through * 2 > kPart ? (looked_through * 2 + kPart - 1) / kPart * kPart : kPart;
+    return p < vecs ? p : vecs;
 }
 
 }  // namespace pool
 
 cudaError_t launch_pool_copy(float *p, int P, int64_t elems, const int32_t *src,
-                             const int32_t *dst, int n, StatusWord *st, int sms, cudaStream_t s) {
+                             const int32_t *dst, int n, StatusWord *st, cudaStream_t s) {
     const int64_t vecs = elems / 4;
-    const int parts = pool::parts_of(vecs, n, sms);
-    const int64_t tasks = (int64_t)n * parts, cap = 8LL * sms;
-    pool::copy_kernel<<<(unsigned)(tasks < cap ? tasks : cap), pool::kThreads, 0, s>>>(
-        (float4 *)p, P, vecs, src, dst, n, nullptr, parts, 1, st);
+    int64_t per = pool::part_of(vecs, n);
+    while ((vecs + per - 1) / per * n > 0x7fffffffLL) per *= 2;
+    const int64_t parts = (vecs + per - 1) / per;
+    pool::copy_kernel<<<(unsigned)(n * parts), pool::kThreads, 0, s>>>((float4 *)p, P, vecs, src, dst,
+                                                                      n, (int)parts, per, st);
     return cudaGetLastError();
 }
 
 cudaError_t launch_pool_compact(float *p, int P, int64_t elems, const uint8_t *live,
                                 int32_t *new_index, int32_t *n_live, int32_t *moves, int sms,
                                 cudaStream_t s) {
-    // moves: the count, then P / 2 sources and P / 2 destinations (no more slots can move)
+    // moves: the header, then P / 2 sources and P / 2 destinations (no more slots can move)
     const int half = P / 2 + 1;
+    pool::Moves *m = reinterpret_cast<pool::Moves *>(moves);
     int32_t *src = moves + 4, *dst = src + half;
-    pool::plan_kernel<<<1, pool::kPlanThreads, 0, s>>>(live, P, new_index, n_live, src, dst, moves);
+    pool::plan_kernel<<<1, pool::kPlanThreads, 0, s>>>(live, P, new_index, n_live, src, dst, m);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t vecs = elems / 4;
-    const int parts = pool::parts_of(vecs, P / 4, sms);
-    pool::copy_kernel<<<(unsigned)(8 * sms), pool::kThreads, 0, s>>>(
-        (float4 *)p, P, vecs, src, dst, 0, moves, parts, 0, nullptr);
-    return cudaGetLastError();
+    int64_t per = pool::part_of(vecs, 0);
+    while ((vecs + per - 1) / per * half > 0x7fffffffLL) per *= 2;
+    const int64_t parts = (vecs + per - 1) / per;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(half * parts < 8LL * sms ? half * parts : 8LL * sms));
+    cfg.blockDim = dim3(pool::kThreads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pool::move_kernel, (float4 *)p, vecs, m, (const int32_t *)src,
+                              (const int32_t *)dst, (int)parts, per);
 }
 
 }  // namespace kda

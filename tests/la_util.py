@@ -6,7 +6,7 @@ import torch
 
 # Relative L2 tolerances.
 #  o, bf16     storage, scores and the copy of the state that meets the queries are each
-#              rounded once to 8 bits (at most 2^-9 of the value): 3 * 2^-9
+#              rounded once to 8 bits (2^-9 of the value in the mean): 3 * 2^-9
 #  o, f32 and states, both types: sums of fp32 products whose factors carry at most 2^-17
 #              each (a decay weight; in bf16 storage the weighted key, held as a sum of two
 #              bf16): 2 * 2^-17 plus fp32 accumulation, below 2e-5
