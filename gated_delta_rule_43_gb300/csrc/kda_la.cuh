@@ -1,6 +1,6 @@
 // kda_la.cuh -- how a prefill of the decayed linear attention is cut over the GPU.
 //
-// A unit is one head of one sequence, a run of 128-token chunks; the units of all sequences,
+// A unit is one head of one sequence, a run of chunks; the units of all sequences,
 // heads inside sequences, stand in one row of `total` chunks.  The row is cut into `ranges`
 // equal parts, one for each CTA (CTA group on the CUDA cores), wherever that falls: every SM
 // has the same work whatever the lengths are.  (A unit counts as `unit_cost` chunks more than it
@@ -8,10 +8,11 @@
 // first pass forms the state that the tokens before it, back to the unit's start or the cut
 // before, leave there; a scan along the cuts of each unit turns these into the states at the
 // cuts; and the output pass starts its ranges from them.
-// A cut moves out of a unit of at most kWhole chunks to its nearer end: for so few chunks the
+// A cut moves out of a unit of at most min_range chunks to its nearer end: for so few chunks the
 // extra pass costs more than the evener load gives.  When there are more SMs than work, every
-// unit has a range of its own, and one of at least 2 kMinRange chunks several, of kMinRange or
-// more.
+// unit has a range of its own, and one of at least 2 min_range chunks several, of min_range or
+// more.  Chunks are 128 tokens on the tensor cores and 32 on the CUDA cores; min_range is 1024
+// and 128 tokens, about where a walk costs as much as the first pass and the scan.
 #pragma once
 
 #include "kda_common.cuh"
@@ -19,9 +20,8 @@
 namespace kda {
 namespace la {
 
-constexpr int kChunk = 128;
-constexpr int kMinRange = 8;
-constexpr int kWhole = 8;
+constexpr int kTcChunk = 128, kTcMinRange = 8;
+constexpr int kSimtChunk = 32, kSimtMinRange = 4;
 
 // A place in the row of chunks: before chunk c of head h of sequence n.
 struct Cut {
@@ -36,6 +36,7 @@ struct Plan {
     const Cut *cuts;          // [ranges + 1], the last at the row's end
     int N, H, Hk;
     int ranges;
+    int chunk;                // tokens
     int in_place;             // the final states overwrite the initial ones
 };
 
@@ -46,9 +47,9 @@ struct Item {
     int64_t t0, t1;           // tokens [t0, t1) of the packed tensors
 };
 
-__device__ __forceinline__ void set_tokens(Item &it, int64_t begin, int64_t end) {
-    it.t0 = begin + (int64_t)it.c0 * kChunk;
-    it.t1 = min(begin + (int64_t)it.c1 * kChunk, end);
+__device__ __forceinline__ void set_tokens(Item &it, int chunk, int64_t begin, int64_t end) {
+    it.t0 = begin + (int64_t)it.c0 * chunk;
+    it.t1 = min(begin + (int64_t)it.c1 * chunk, end);
 }
 
 // Walks the items of the range between two cuts.  The heads of a sequence follow each other, so
@@ -74,7 +75,7 @@ struct Walk {
         it.c0 = c;
         it.nc = nc;
         it.c1 = (int)min((int64_t)nc, c + (end - x));
-        set_tokens(it, begin, stop);
+        set_tokens(it, p.chunk, begin, stop);
         x += it.c1 - c;
         c = 0;
         if (++h == p.H) {
@@ -119,7 +120,7 @@ __device__ __forceinline__ bool before_cut(const Plan &p, int i, Item &it) {
     it.c1 = e.c;
     it.c0 = (int)max((int64_t)0, e.c - (e.x - p.cuts[i - 1].x));
     it.nc = p.off[e.n + 1] - p.off[e.n];
-    set_tokens(it, p.cu[it.n], p.cu[it.n + 1]);
+    set_tokens(it, p.chunk, p.cu[it.n], p.cu[it.n + 1]);
     return true;
 }
 

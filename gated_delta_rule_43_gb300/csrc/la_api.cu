@@ -9,7 +9,7 @@
 
 namespace kda {
 cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off, int unit_cost,
-                           la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
+                           int chunk, int min_range, la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
                            int H, int64_t dkdv, cudaStream_t s);
 cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
                            int64_t dkdv, cudaStream_t s);
@@ -69,19 +69,21 @@ bool stride_ok(int64_t stride, int64_t T, int32_t heads, int32_t D, int32_t dtyp
 }
 
 struct LaLayout {
-    int ranges;
+    int ranges, chunk, min_range;
     bool split;
     size_t cuts_off, off_off, log_off, bnd_off, total;
 };
 
 // One range an SM, and no more than there can be chunks.  Sequences are cut only where one
 // may be longer than a range of the least length (the lengths are on the device).
-LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t dk, int32_t dv, int sms) {
+LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t dk, int32_t dv, int32_t dtype, int sms) {
     LaLayout L{};
-    const int64_t most = (T / la::kChunk + N) * (int64_t)H;
+    L.chunk = dtype == KDA_BF16 ? la::kTcChunk : la::kSimtChunk;
+    L.min_range = dtype == KDA_BF16 ? la::kTcMinRange : la::kSimtMinRange;
+    const int64_t most = (T / L.chunk + N) * (int64_t)H;
     if (sms > 1024) sms = 1024;   // (the plan's room)
     L.ranges = (int)(most < 1 ? 1 : most < sms ? most : sms);
-    L.split = L.ranges > 1 && T > la::kWhole * la::kChunk;
+    L.split = L.ranges > 1 && T > L.min_range * L.chunk;
     L.cuts_off = kHeaderBytes;
     L.off_off = L.cuts_off + round_up(sizeof(la::Cut) * ((size_t)L.ranges + 1), 256);
     L.log_off = L.off_off + round_up(3 * sizeof(int32_t) * ((size_t)N + 1), 256);
@@ -105,7 +107,7 @@ size_t kda_la_chunk_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, i
     if (!dtype_ok(dtype) || !head_ok(dk) || !head_ok(dv) ||
         !la_sizes_ok(total_tokens, num_seqs, H, Hk, dk, dv))
         return 0;
-    return la_layout(total_tokens, num_seqs, H, dk, dv, sm_count()).total;
+    return la_layout(total_tokens, num_seqs, H, dk, dv, dtype, sm_count()).total;
 }
 
 kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
@@ -129,7 +131,7 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     if (!aligned(g, 4) || !aligned(cu_seqlens, 4) || !aligned(workspace, 256))
         return KDA_ERR_INVALID_ARG;
     if (o && (o == q || o == k || o == v)) return KDA_ERR_INVALID_ARG;
-    const LaLayout L = la_layout(total_tokens, num_seqs, H, dk, dv, sm_count());
+    const LaLayout L = la_layout(total_tokens, num_seqs, H, dk, dv, dtype, sm_count());
     if (workspace_bytes < L.total) return KDA_ERR_INVALID_ARG;
 
     cudaStream_t s = (cudaStream_t)stream;
@@ -140,13 +142,13 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     int32_t *off = (int32_t *)(ws + L.off_off);
     float *bnd_log = (float *)(ws + L.log_off), *bnd = (float *)(ws + L.bnd_off);
     const int64_t dkdv = (int64_t)dk * dv;
-    const la::Plan p{cu_seqlens, off, cuts, num_seqs, H, Hk, L.ranges,
+    const la::Plan p{cu_seqlens, off, cuts, num_seqs, H, Hk, L.ranges, L.chunk,
                      initial_state && initial_state == final_state};
     // A unit's states cost about as much as a chunk each (64 KB in, 64 KB out; measured on 16
     // packed sequences: 11.6k cycles beside 5.4k of a chunk).
     const int unit_cost = (initial_state ? 1 : 0) + (final_state ? 1 : 0);
-    cudaError_t e = launch_la_plan(cu_seqlens, num_seqs, total_tokens, off, unit_cost, cuts, L.ranges,
-                                   L.split, st, initial_state, final_state, H, dkdv, s);
+    cudaError_t e = launch_la_plan(cu_seqlens, num_seqs, total_tokens, off, unit_cost, L.chunk,
+                                   L.min_range, cuts, L.ranges, L.split, st, initial_state, final_state, H, dkdv, s);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (total_tokens == 0) return KDA_OK;
     CUtensorMap maps[8];

@@ -42,13 +42,14 @@ __device__ Cut place(const int32_t *off, int N, int H, int64_t total, int64_t x)
 }
 
 // Ranges a unit of nc chunks is worth when there are SMs to spare
-__device__ __forceinline__ int pieces(int nc, int split) {
-    return nc == 0 ? 0 : !split || nc < 2 * kMinRange ? 1 : nc / kMinRange;
+__device__ __forceinline__ int pieces(int nc, int split, int min_range) {
+    return nc == 0 ? 0 : !split || nc < 2 * min_range ? 1 : nc / min_range;
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
 la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *off,
-               int32_t *piece_off, int32_t *cost_off, int unit_cost, Cut *cuts, int ranges, int split,
+               int32_t *piece_off, int32_t *cost_off, int unit_cost, int chunk,
+               int min_range, Cut *cuts, int ranges, int split,
                StatusWord *st, const float *h0, float *S_out, int H,
                int64_t dkdv4) {
     if (S_out) {
@@ -85,8 +86,8 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
             if (b < 0 || e < b || e > T_tot)
                 report(st, KDA_ERR_SEQLENS, n, 2);
             else
-                own.x = (int)((e - b + kChunk - 1) / kChunk);
-            own.y = pieces(own.x, split);
+                own.x = (int)((e - b + chunk - 1) / chunk);
+            own.y = pieces(own.x, split, min_range);
             own.z = own.x ? own.x + unit_cost : 0;
         }
         int3 x = own;   // inclusive warp scan
@@ -121,7 +122,7 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
     const int64_t cost = (int64_t)carry.z * H;
     // SMs to spare: every unit gets its own range, a long one several.  Else equal parts
     // (without a first pass nothing can be cut: the units are dealt out whole).
-    const bool spare = fine <= ranges && total < (int64_t)ranges * kMinRange;
+    const bool spare = fine <= ranges && total < (int64_t)ranges * min_range;
     for (int i = tid; i <= ranges; i += kPlanThreads) {
         Cut r;
         if (spare) {
@@ -145,7 +146,7 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
             r = place(off, N, H, total, x);
             if (r.inner) {
                 const int nc = off[r.n + 1] - off[r.n];
-                if (!split || nc <= kWhole)
+                if (!split || nc <= min_range)
                     r = place(off, N, H, total, r.x + (2 * r.c >= nc ? nc - r.c : -r.c));
             }
         }
@@ -206,20 +207,28 @@ la_scan_kernel(Plan p, const float *__restrict__ h0, float *__restrict__ bnd,
 
 // ----------------------------------------------------------------------- chunks
 constexpr int kThreads = 256;
-constexpr int C = 32;   // chunk: one warp scans its decays
+constexpr int C = kSimtChunk;   // one warp scans its decays
 
 template <int DK, int DVB> struct Smem {
     static constexpr int LK = DK + 4;   // padded rows: 16-byte reads of 8 rows miss no bank twice
     float q[C][LK], k[C][LK];
     float v[C][DVB];
     float S[DK][DVB];
-    float p[C][C + 1];
+    float p[C][C + 4];
     float G[C], eG[C], w[C];            // prefix sums, their exponentials, weights to the end
     float total, total_log;             // the chunk's decay and its log
 };
 
+__device__ __forceinline__ void fma4(float (&acc)[4], float a, const float4 &b) {
+    acc[0] += a * b.x;
+    acc[1] += a * b.y;
+    acc[2] += a * b.z;
+    acc[3] += a * b.w;
+}
+
 // OUT: outputs and final states of the CTA's range.  Else what the end of the range leaves at
-// the cut behind it.  The column blocks of a range are CTAs of their own.
+// the cut behind it.  The column blocks of a range are CTAs of their own.  The next chunk's
+// tokens are on their way in registers while a chunk is worked on.
 template <int DK, int DV, int DVB, bool OUT>
 __global__ void __launch_bounds__(kThreads)
 la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restrict__ k,
@@ -235,11 +244,13 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
     constexpr int TR = kThreads / TC;        // thread rows
     constexpr int SR = DK / TR;              // state rows per thread
     constexpr int OR = C / TR > 0 ? C / TR : 1;   // output rows per thread
-    static_assert(DK % TR == 0 && SR >= 1 && C % OR == 0, "shape");
+    constexpr int LQ = C * DK / 4 / kThreads, LV = (C * DVB / 4 + kThreads - 1) / kThreads;
+    static_assert(DK % TR == 0 && SR >= 1 && C % OR == 0 && C * DK / 4 % kThreads == 0 && LQ >= 1, "shape");
     const int tid = threadIdx.x;
     const int c4 = (tid % TC) * 4, rg = tid / TC;
     const int64_t dkdv = (int64_t)DK * DV;
     const int blk = blockIdx.x % NB, range = blockIdx.x / NB;
+    const int j0 = blk * DVB;
     Item it;
     Walk walk(p, range);
     bool more = OUT ? walk.next(it) : before_cut(p, range + 1, it);
@@ -247,10 +258,32 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
     for (; more; more = OUT && walk.next(it)) {
         const int h = it.h;
         const int hk = h / (p.H / p.Hk);
-        const int j0 = blk * DVB;
         const int64_t nh = ((int64_t)it.n * p.H + h) * dkdv;
         const Start from = OUT ? start_state(p, it, range, h0 != nullptr) : Start{-1, false};
         const float *start = from.index < 0 ? nullptr : (from.in_bnd ? bnd : h0) + from.index * dkdv;
+        // rows past the sequence are zeros whatever memory holds there
+        float4 nq[LQ], nk[LQ], nv[LV];
+        float ng = 0.f;
+        auto fetch = [&](int64_t t0) {
+            const int len = (int)min((int64_t)C, it.t1 - t0);
+#pragma unroll
+            for (int m = 0; m < LQ; ++m) {
+                const int x = tid + m * kThreads, r = x / (DK / 4), c = 4 * (x % (DK / 4));
+                const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+                const bool in = r < len;
+                if (OUT) nq[m] = in ? *reinterpret_cast<const float4 *>(q + (t0 + r) * qs + (int64_t)hk * DK + c) : zero;
+                nk[m] = in ? *reinterpret_cast<const float4 *>(k + (t0 + r) * ks + (int64_t)hk * DK + c) : zero;
+            }
+#pragma unroll
+            for (int m = 0; m < LV; ++m) {
+                const int x = tid + m * kThreads, r = x / (DVB / 4), c = 4 * (x % (DVB / 4));
+                nv[m] = r < len ? *reinterpret_cast<const float4 *>(v + (t0 + r) * vs + (int64_t)h * DV + j0 + c)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            ng = 0.f;
+            if (tid < len) ng = g_per_token ? g[(t0 + tid) * p.H + h] : g[h];
+        };
+        fetch(it.t0);
         float S[SR][4];
 #pragma unroll
         for (int r = 0; r < SR; ++r) {
@@ -262,16 +295,16 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
         float log_sum = 0.f;
         for (int64_t t0 = it.t0; t0 < it.t1; t0 += C) {
             const int len = (int)min((int64_t)C, it.t1 - t0);
-            // this chunk's tokens; rows past the segment are zeros whatever memory holds there
-            for (int x = tid; x < C * DK; x += kThreads) {
-                const int r = x / DK, c = x % DK;
-                const bool in = r < len;
-                if (OUT) sm.q[r][c] = in ? q[(t0 + r) * qs + (int64_t)hk * DK + c] : 0.f;
-                sm.k[r][c] = in ? k[(t0 + r) * ks + (int64_t)hk * DK + c] : 0.f;
+#pragma unroll
+            for (int m = 0; m < LQ; ++m) {
+                const int x = tid + m * kThreads, r = x / (DK / 4), c = 4 * (x % (DK / 4));
+                if (OUT) *reinterpret_cast<float4 *>(&sm.q[r][c]) = nq[m];
+                *reinterpret_cast<float4 *>(&sm.k[r][c]) = nk[m];
             }
-            for (int x = tid; x < C * DVB; x += kThreads) {
-                const int r = x / DVB, c = x % DVB;
-                sm.v[r][c] = r < len ? v[(t0 + r) * vs + (int64_t)h * DV + j0 + c] : 0.f;
+#pragma unroll
+            for (int m = 0; m < LV; ++m) {
+                const int x = tid + m * kThreads, r = x / (DVB / 4), c = 4 * (x % (DVB / 4));
+                if (r < C) *reinterpret_cast<float4 *>(&sm.v[r][c]) = nv[m];
             }
             if (OUT) {
 #pragma unroll
@@ -280,12 +313,9 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
                         make_float4(S[r][0], S[r][1], S[r][2], S[r][3]);
             }
             if (tid < 32) {
-                float x = 0.f;
-                if (tid < len) {
-                    x = g_per_token ? g[(t0 + tid) * p.H + h] : g[h];
-                    if (!log_decay_ok(x) && blk == 0)
-                        report(st, KDA_ERR_DECAY_RANGE, g_per_token ? (t0 + tid) * p.H + h : h, 30);
-                }
+                const float x = ng;
+                if (!log_decay_ok(x) && blk == 0)
+                    report(st, KDA_ERR_DECAY_RANGE, g_per_token ? (t0 + tid) * p.H + h : h, 30);
                 float pre = x < kLogZero ? kLogZero : x;   // (a comparison, so that NaN spreads)
                 float suf = x;
 #pragma unroll
@@ -305,65 +335,81 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
                 }
             }
             __syncthreads();
+            if (t0 + C < it.t1) fetch(t0 + C);
             if (OUT) {
-                const int t = tid / 8, s0 = tid % 8;   // row t, columns s0 + 8 j
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                // rows ta, ta + 16 and columns sa, sa + 16 of P
+                const int ta = tid / 16, sa = tid % 16;
+                float acc[2][2] = {};
+#pragma unroll 4
                 for (int d = 0; d < DK; d += 4) {
-                    const float4 a = *reinterpret_cast<const float4 *>(&sm.q[t][d]);
+                    float4 a[2], b[2];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 b = *reinterpret_cast<const float4 *>(&sm.k[s0 + 8 * j][d]);
-                        acc[j] += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+                    for (int m = 0; m < 2; ++m) {
+                        a[m] = *reinterpret_cast<const float4 *>(&sm.q[ta + 16 * m][d]);
+                        b[m] = *reinterpret_cast<const float4 *>(&sm.k[sa + 16 * m][d]);
                     }
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+                            acc[m][n] += a[m].x * b[n].x + a[m].y * b[n].y + a[m].z * b[n].z + a[m].w * b[n].w;
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int s = s0 + 8 * j;
-                    sm.p[t][s] = t >= s ? acc[j] * expf(sm.G[t] - sm.G[s]) : 0.f;
-                }
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int t = ta + 16 * m, s = sa + 16 * n;
+                        sm.p[t][s] = t >= s ? acc[m][n] * expf(sm.G[t] - sm.G[s]) : 0.f;
+                    }
                 __syncthreads();
-                if (rg * OR < C) {
-                    float oi[OR][4] = {}, oa[OR][4] = {};
-                    for (int i = 0; i < DK; ++i) {
-                        const float4 s4 = *reinterpret_cast<const float4 *>(&sm.S[i][c4]);
+                float oi[OR][4] = {}, oa[OR][4] = {};
+#pragma unroll 2
+                for (int i = 0; i < DK; i += 4) {
+                    float4 s4[4];
 #pragma unroll
-                        for (int r = 0; r < OR; ++r) {
-                            const float a = sm.q[rg * OR + r][i];
-                            oi[r][0] += a * s4.x; oi[r][1] += a * s4.y;
-                            oi[r][2] += a * s4.z; oi[r][3] += a * s4.w;
-                        }
-                    }
-                    for (int s = 0; s < C; ++s) {
-                        const float4 v4 = *reinterpret_cast<const float4 *>(&sm.v[s][c4]);
-#pragma unroll
-                        for (int r = 0; r < OR; ++r) {
-                            const float a = sm.p[rg * OR + r][s];
-                            oa[r][0] += a * v4.x; oa[r][1] += a * v4.y;
-                            oa[r][2] += a * v4.z; oa[r][3] += a * v4.w;
-                        }
-                    }
+                    for (int m = 0; m < 4; ++m) s4[m] = *reinterpret_cast<const float4 *>(&sm.S[i + m][c4]);
 #pragma unroll
                     for (int r = 0; r < OR; ++r) {
-                        const int row = rg * OR + r;
-                        if (row < len) {
-                            const float e = sm.eG[row];
-                            *reinterpret_cast<float4 *>(o + ((t0 + row) * p.H + h) * (int64_t)DV + j0 + c4) =
-                                make_float4(oa[r][0] + e * oi[r][0], oa[r][1] + e * oi[r][1],
-                                            oa[r][2] + e * oi[r][2], oa[r][3] + e * oi[r][3]);
-                        }
+                        const float4 a = *reinterpret_cast<const float4 *>(&sm.q[rg * OR + r][i]);
+                        fma4(oi[r], a.x, s4[0]);
+                        fma4(oi[r], a.y, s4[1]);
+                        fma4(oi[r], a.z, s4[2]);
+                        fma4(oi[r], a.w, s4[3]);
+                    }
+                }
+#pragma unroll 2
+                for (int s = 0; s < C; s += 4) {
+                    float4 v4[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) v4[m] = *reinterpret_cast<const float4 *>(&sm.v[s + m][c4]);
+#pragma unroll
+                    for (int r = 0; r < OR; ++r) {
+                        const float4 a = *reinterpret_cast<const float4 *>(&sm.p[rg * OR + r][s]);
+                        fma4(oa[r], a.x, v4[0]);
+                        fma4(oa[r], a.y, v4[1]);
+                        fma4(oa[r], a.z, v4[2]);
+                        fma4(oa[r], a.w, v4[3]);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < OR; ++r) {
+                    const int row = rg * OR + r;
+                    if (row < len) {
+                        const float e = sm.eG[row];
+                        *reinterpret_cast<float4 *>(o + ((t0 + row) * p.H + h) * (int64_t)DV + j0 + c4) =
+                            make_float4(oa[r][0] + e * oi[r][0], oa[r][1] + e * oi[r][1],
+                                        oa[r][2] + e * oi[r][2], oa[r][3] + e * oi[r][3]);
                     }
                 }
             }
             float add[SR][4] = {};
+#pragma unroll 4
             for (int s = 0; s < C; ++s) {
-                const float4 v4 = *reinterpret_cast<const float4 *>(&sm.v[s][c4]);
+                float4 v4 = *reinterpret_cast<const float4 *>(&sm.v[s][c4]);
                 const float w = sm.w[s];
+                v4.x *= w; v4.y *= w; v4.z *= w; v4.w *= w;
 #pragma unroll
-                for (int r = 0; r < SR; ++r) {
-                    const float a = sm.k[s][rg * SR + r] * w;
-                    add[r][0] += a * v4.x; add[r][1] += a * v4.y;
-                    add[r][2] += a * v4.z; add[r][3] += a * v4.w;
-                }
+                for (int r = 0; r < SR; ++r) fma4(add[r], sm.k[s][rg * SR + r], v4);
             }
             const float e = sm.total;
             log_sum += sm.total_log;
@@ -404,13 +450,13 @@ static cudaError_t launch_dims(bool out, const Plan &p, const float *q, const fl
 }  // namespace la
 
 cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off, int unit_cost,
-                           la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
+                           int chunk, int min_range, la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
                            int H, int64_t dkdv, cudaStream_t s) {
     float *S_out = hT != h0 ? hT : nullptr;   // an in-place update leaves empty ones as they are
     const int64_t nh = (int64_t)N * H;
     const int grid = S_out && nh > 1 ? (int)(nh < 256 ? nh : 256) : 1;
     la::la_plan_kernel<<<grid, la::kPlanThreads, 0, s>>>(
-        cu, N, T_tot, off, off + N + 1, off + 2 * (N + 1), unit_cost, cuts, ranges, split, st, h0, S_out, H, dkdv / 4);
+        cu, N, T_tot, off, off + N + 1, off + 2 * (N + 1), unit_cost, chunk, min_range, cuts, ranges, split, st, h0, S_out, H, dkdv / 4);
     return cudaGetLastError();
 }
 

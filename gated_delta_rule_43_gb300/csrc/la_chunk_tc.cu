@@ -47,7 +47,7 @@ namespace tc {
 
 using namespace sm100;
 
-constexpr int C = kChunk;
+constexpr int C = kTcChunk;
 constexpr int kThreads = 512;
 constexpr int kRowWarps = 4, kStateWarps = 8;
 constexpr int kMmaWarp = 12, kLoadWarp = 13, kGateWarp = 14, kStoreWarp = 15;

@@ -8,8 +8,8 @@
 //   past the rotated part, channels rot + 16 j' .. (no rotation)
 // so a norm is a few shuffles deep and rotation needs none.  A CTA takes the heads (or a part of
 // them) of a few tokens: first each thread works out one angle's cosine and sine, which the
-// heads of a token share, into shared memory; then each warp goes through rows, the loads of
-// kAhead rows in flight.
+// heads of a token share, into shared memory; then each warp goes through rows, the loads of several
+// rows in flight.
 //
 // The rotation's angle is a whole number of turns plus a fraction, and only the fraction
 // counts.  The rate in turns per position is held as a 64-bit binary fraction, so position *
@@ -23,7 +23,6 @@ namespace qk {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kTokens = 4;   // of a CTA, at most: kThreads angles of 64 pairs
-constexpr int kAhead = 2;
 
 struct Side {
     const void *x;
@@ -89,13 +88,17 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
 }
 
 // CTA x: tokens [t0, t0 + tokens) of group x / parts, heads [h0, h1) of part x % parts.
+// Rows in flight: as many bytes in either type
+template <typename T> constexpr int ahead() { return sizeof(T) == 2 ? 4 : 2; }
+
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 qk_norm_rope_kernel(Side q, Side k, int64_t T_tot, int tokens, int parts, int norm, float eps,
                     const int32_t *__restrict__ positions, const float *__restrict__ inv_freq,
                     int rot, int interleaved, float rope_scale) {
     constexpr int LPR = D / 16;      // lanes per head
     constexpr int RPW = 32 / LPR;    // heads a warp holds at a time
+    constexpr int kAhead = ahead<T>();
     __shared__ __align__(16) float s_cos[kTokens][D / 2], s_sin[kTokens][D / 2];
     const int64_t t0 = (int64_t)(blockIdx.x / parts) * tokens;
     const int part = blockIdx.x % parts;
@@ -217,7 +220,7 @@ template <int D, typename T>
 static cudaError_t launch_dims(const Side &q, const Side &k, int64_t T_tot, int norm, float eps,
                                const int32_t *pos, const float *inv_freq, int rot, int interleaved,
                                float rope_scale, int sms, cudaStream_t s) {
-    constexpr int kRows = kWarps * (32 / (D / 16)) * kAhead;   // of a CTA's turn
+    constexpr int kRows = kWarps * (32 / (D / 16)) * ahead<T>();   // of a CTA's turn
     // Several tokens a CTA while that leaves four CTAs an SM, and a token's heads over several
     // CTAs (each works out the token's angles again) while there are fewer than two.
     int tokens = kTokens;
