@@ -219,7 +219,9 @@ struct Waits {
 };
 
 // OUT: outputs and final states of the CTA's range.  Else what the end of the range leaves at
-// the cut behind it (only K~^T V; no queries).
+// the cut behind it (only K~^T V; no queries): from its last chunk to its first, so that the
+// chunks which the output pass reads first are the ones that L2 still holds, with weights that
+// reach to the cut, so that nothing is decayed on the way.
 template <int DKP, int DVP, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
@@ -475,12 +477,13 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     if (!ok) break;
                 }
                 if (next) {
-                    const int len = (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)(c + 1) * C);
+                    const int at_chunk = OUT ? c + 1 : chunks - 2 - c;
+                    const int len = (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)at_chunk * C);
                     fine = fine && wait.warp(kGate + b, ph) && wait.warp(kFullK + sb, (si >> 1) & 1) &&
                            (len == C || wait.warp(kFullV + b, ph));
                     if (fine) {
                         // channels of this warp's quarter, tokens of its half, 16 x 32 a turn
-                        decay_next = tot[b];
+                        decay_next = OUT ? tot[b] : 1.f;
                         if (32 * quarter < DKP) {
 #pragma unroll 1
                             for (int turn = 0; turn < 4; ++turn) {
@@ -689,7 +692,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             }
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
                 const uint32_t b = gi & 1, sb = si & 1, before = ((si - 2) >> 1) & 1;
-                const int32_t t0 = (int32_t)(it.t0 + (int64_t)c * C);
+                const int32_t t0 = (int32_t)(it.t0 + (int64_t)(OUT ? c : chunks - 1 - c) * C);
                 uint8_t *qk = sm + sb * M::kQK;
                 if (si >= 2) ok = wait.warp(kFreeK + sb, before);
                 if (!ok) break;
@@ -734,7 +737,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             float log_sum = 0.f;
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
                 const uint32_t b = gi & 1;
-                const int64_t t0 = it.t0 + (int64_t)c * C;
+                const int64_t t0 = it.t0 + (int64_t)(OUT ? c : chunks - 1 - c) * C;
                 const int len = (int)min((int64_t)C, it.t1 - t0);
                 float x[4], pre[4], suf[4];
                 int bad = -1;
@@ -764,7 +767,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 float after = __shfl_down_sync(0xffffffffu, down, 1);
                 if (lane == 0) before = 0.f;
                 if (lane == 31) after = 0.f;
-                suf[3] = after;
+                suf[3] = OUT ? after : after + log_sum;
 #pragma unroll
                 for (int m = 2; m >= 0; --m) suf[m] = suf[m + 1] + x[m + 1];
 #pragma unroll
@@ -788,7 +791,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     G.w[2 * lane + m / 2] = make_uint2(hi, pack2(w0 - __uint_as_float(hi << 16),
                                                                  w1 - __uint_as_float(hi & 0xffff0000u)));
                 }
-                if (lane == 0) tot[b] = expf(total);
+                if (OUT && lane == 0) tot[b] = expf(total);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kGate + b]);
             }
