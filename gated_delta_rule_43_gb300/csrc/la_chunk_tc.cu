@@ -126,14 +126,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         ::"r"(taddr), KDA_R16(r)
         : "memory");
 }
-// 16 lanes, 16 consecutive columns: register 2 i + j of thread t is lane t / 4 + 8 j, column
+// 16 lanes, 8 consecutive columns: register 2 i + j of thread t is lane t / 4 + 8 j, column
 // 4 i + t % 4
-__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-          "r"(r[7])
-        : "memory");
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 #undef KDA_R16
 __device__ __forceinline__ void tmem_st_wait() {
@@ -364,20 +362,21 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const float e = ex2(Gt);
                 const float2 eG = make_float2(e, e);
 #pragma unroll 1
-                for (int j0 = 0; j0 < DVP; j0 += 32) {
-                    float x[32];
-                    tmem_ld32(tO + lanes + j0, x);
+                for (int j0 = 0; j0 < DVP; j0 += 64) {
+                    float x[2][32];
+                    tmem_ld32(tO + lanes + j0, x[0]);
+                    tmem_ld32(tO + lanes + j0 + 32, x[1]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int m = 0; m < 32; m += 16) {
+                    for (int m = 0; m < 4; ++m) {
                         uint32_t y[16];
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            const float2 z = mul2(eG, make_float2(x[m + j], x[m + j + 1]));
+                            const float2 z = mul2(eG, make_float2(x[m / 2][16 * (m & 1) + j], x[m / 2][16 * (m & 1) + j + 1]));
                             y[j] = __float_as_uint(z.x);
                             y[j + 1] = __float_as_uint(z.y);
                         }
-                        tmem_st16(tO + lanes + j0 + m, y);
+                        tmem_st16(tO + lanes + j0 + 16 * m, y);
                     }
                 }
                 tmem_st_wait();
@@ -395,17 +394,19 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 if (!ok) break;
                 uint8_t *so = sm + (M::kOverQ ? sb * M::kQK + M::kQ : M::kO);
 #pragma unroll 1
-                for (int cb = 0; cb < DVP / 32; ++cb) {
-                    float x[32];
-                    tmem_ld32(tO + lanes + 32 * cb, x);
+                for (int cb = 0; cb < DVP / 32; cb += 2) {
+                    float x[2][32];
+                    tmem_ld32(tO + lanes + 32 * cb, x[0]);
+                    tmem_ld32(tO + lanes + 32 * cb + 32, x[1]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
+                    for (int j = 0; j < 64; j += 8) {
+                        const float *y = &x[j / 32][j % 32];
                         uint4 u;
-                        u.x = pack2(x[j], x[j + 1]);
-                        u.y = pack2(x[j + 2], x[j + 3]);
-                        u.z = pack2(x[j + 4], x[j + 5]);
-                        u.w = pack2(x[j + 6], x[j + 7]);
+                        u.x = pack2(y[0], y[1]);
+                        u.y = pack2(y[2], y[3]);
+                        u.z = pack2(y[4], y[5]);
+                        u.w = pack2(y[6], y[7]);
                         *reinterpret_cast<uint4 *>(so + sw128_offset(t, 32 * cb + j, C)) = u;
                     }
                 }
@@ -482,36 +483,37 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     fine = fine && wait.warp(kGate + b, ph) && wait.warp(kFullK + sb, (si >> 1) & 1) &&
                            (len == C || wait.warp(kFullV + b, ph));
                     if (fine) {
-                        // channels of this warp's quarter, tokens of its half, 16 x 32 a turn
+                        // channels of this warp's quarter, tokens of its half, 16 x 64 a turn: all
+                        // of a turn's reads first (they take 300 cycles beside the products')
                         decay_next = OUT ? tot[b] : 1.f;
                         if (32 * quarter < DKP) {
 #pragma unroll 1
-                            for (int turn = 0; turn < 4; ++turn) {
-                                const int cg = 16 * (turn >> 1), tg = 32 * (turn & 1);
-                                uint32_t hi[8], lo[8];
+                            for (int cg = 0; cg < 32; cg += 16) {
+                                uint32_t x[4][4];
 #pragma unroll
-                                for (int m = 0; m < 2; ++m) {
-                                    const int s = 64 * half + tg + 16 * m;   // first of 16 tokens
-                                    uint32_t x[4];
+                                for (int m = 0; m < 4; ++m)
                                     ldmatrix_t(base + sb * M::kQK + M::kK +
-                                                   sw128_offset(s + (lane >> 4) * 8 + (lane & 7),
+                                                   sw128_offset(64 * half + 16 * m + (lane >> 4) * 8 + (lane & 7),
                                                                 32 * quarter + cg + ((lane >> 3) & 1) * 8, C),
-                                               x);
-                                    const int at = s + 2 * (lane & 3);   // and at + 1, at + 8, at + 9
+                                               x[m]);
+                                const uint32_t to_col = lanes + ((uint32_t)cg << 16) + 32 * half + (OUT ? 0 : b * kOther);
+#pragma unroll
+                                for (int m = 0; m < 4; ++m) {
+                                    const int at = 64 * half + 16 * m + 2 * (lane & 3);   // and + 1, + 8, + 9
                                     if (len < C) {   // tokens past the sequence count as zeros
                                         const uint32_t m0 = (at < len ? 0xffffu : 0u) | (at + 1 < len ? 0xffff0000u : 0u);
                                         const uint32_t m1 = (at + 8 < len ? 0xffffu : 0u) | (at + 9 < len ? 0xffff0000u : 0u);
-                                        x[0] &= m0; x[1] &= m0; x[2] &= m1; x[3] &= m1;
+                                        x[m][0] &= m0; x[m][1] &= m0; x[m][2] &= m1; x[m][3] &= m1;
                                     }
                                     const uint2 w0 = gates[b].w[at / 2], w1 = gates[b].w[at / 2 + 4];
-                                    split2(x[0], w0, hi[4 * m], lo[4 * m]);
-                                    split2(x[1], w0, hi[4 * m + 1], lo[4 * m + 1]);
-                                    split2(x[2], w1, hi[4 * m + 2], lo[4 * m + 2]);
-                                    split2(x[3], w1, hi[4 * m + 3], lo[4 * m + 3]);
+                                    uint32_t hi[4], lo[4];
+                                    split2(x[m][0], w0, hi[0], lo[0]);
+                                    split2(x[m][1], w0, hi[1], lo[1]);
+                                    split2(x[m][2], w1, hi[2], lo[2]);
+                                    split2(x[m][3], w1, hi[3], lo[3]);
+                                    tmem_st_16x8(tHi + to_col + 8 * m, hi);
+                                    tmem_st_16x8(tLo + to_col + 8 * m, lo);
                                 }
-                                const uint32_t at = lanes + ((uint32_t)cg << 16) + 32 * half + tg / 2 + (OUT ? 0 : b * kOther);
-                                tmem_st_16x16(tHi + at, hi);
-                                tmem_st_16x16(tLo + at, lo);
                             }
                             tmem_st_wait();
                         }

@@ -8,6 +8,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -21,6 +22,7 @@ KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_DECAY_RANGE = 0, 1, 2,
 KDA_ERR_TIMEOUT, KDA_ERR_CUDA, KDA_ERR_SEQLENS = 4, 5, 6
 KDA_F32, KDA_BF16 = 0, 1
 _DT = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
+_F32 = torch.float32
 _NORM = {"none": 0, "l2": 1, "rms": 2}
 _LAYOUT = {"half": 0, "interleaved": 1}
 
@@ -378,21 +380,27 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream, device):
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device)
+    return _current_raw_stream(device)
+
+
+def _off_gpu():
+    raise ValueError("every tensor must live on one CUDA device (no CPU fallback)")
 
 
 def _same_gpu(q, *ts):
     """The index of q's GPU; every tensor given lives there."""
     device = q.get_device()
+    if device < 0:
+        _off_gpu()
     for t in ts:
         if t is not None and t.get_device() != device:
-            device = -1
-            break
-    if device < 0:
-        raise ValueError("every tensor must live on one CUDA device (no CPU fallback)")
+            _off_gpu()
     return device
 
 
@@ -450,9 +458,14 @@ def _check_la(q, k, v, g):
         raise ValueError(f"{H} value heads cannot share {Hk} query/key heads")
     strides = (_rows("q", q, T, Hk, dk, dtype), _rows("k", k, T, Hk, dk, dtype),
                _rows("v", v, T, H, dv, dtype))
-    per_token = g.dim() == 2
-    return (T, H, Hk, dk, dv, dtype, strides, 1 if per_token else 0,
-            _dense("g", g, (T, H) if per_token else (H,), torch.float32))
+    if g.dim() == 2:
+        return T, H, Hk, dk, dv, dtype, strides, 1, _dense("g", g, (T, H), _F32)
+    return T, H, Hk, dk, dv, dtype, strides, 0, _dense("g", g, (H,), _F32)
+
+
+@functools.lru_cache(maxsize=1024)
+def _la_workspace_size(device, *sizes):   # (the size goes by the device's SMs, too)
+    return load().kda_la_chunk_fwd_workspace_size(*sizes)
 
 
 def la_chunk_fwd(q, k, v, g, cu_seqlens, initial_state=None, *, output_final_state: bool = True,
@@ -487,7 +500,7 @@ def la_chunk_fwd(q, k, v, g, cu_seqlens, initial_state=None, *, output_final_sta
     dt = _DT[dtype]
     need = 0
     if workspace is None:
-        need = lib.kda_la_chunk_fwd_workspace_size(T, N, H, Hk, dk, dv, dt)
+        need = _la_workspace_size(device, T, N, H, Hk, dk, dv, dt)
     workspace, wa, wb = _workspace(q, need, workspace, stream)
     rc = lib.kda_la_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), ga, ca, N, T, H, Hk, dk, dv,
                               dt, qs, ks, vs, gpt, ia, _addr(final_state), o.data_ptr(), wa, wb,
