@@ -28,6 +28,7 @@ struct Cut {
     int64_t x;
     int32_t n, h, c;
     int32_t inner;            // inside a unit: 1 + the inner cuts of this unit that follow; else 0
+    int32_t before;           // the inner cuts of this unit before it
 };
 
 struct Plan {
@@ -38,6 +39,7 @@ struct Plan {
     int ranges;
     int chunk;                // tokens
     int in_place;             // the final states overwrite the initial ones
+    int compose;              // no scan: ranges put their start states together themselves
 };
 
 // The chunks [c0, c1) of one unit.
@@ -129,17 +131,37 @@ __device__ __forceinline__ bool before_cut(const Plan &p, int i, Item &it) {
 // scan keeps a copy of the initial state of such a unit, for range i at index ranges + i.
 __device__ __forceinline__ int64_t cut_state(int i) { return i - 1; }
 
-// Where an item of range `range` starts from: the index of a state among the boundaries' or
-// the initial ones; -1 for zeros.
+// Where an item of range `range` starts from: `steps` states, each taken after the decay of what
+// lies between it and the one before.  A unit's start: none (zeros) or the initial state (its
+// copy).  A cut after the scan: the state there.  A cut without it (p.compose): the unit's
+// initial state and what the cuts up to this one hold.
 struct Start {
-    int32_t index;
-    bool in_bnd;
+    int steps;
+    int32_t h0;               // index of the first step's initial state, -1: it is a cut's
+    bool h0_in_bnd;
+    int first_cut;
+    __device__ __forceinline__ bool in_bnd(int s) const { return s > 0 || h0 < 0 || h0_in_bnd; }
+    __device__ __forceinline__ int cut(int s) const { return first_cut + s - (h0 >= 0 ? 1 : 0); }
+    __device__ __forceinline__ int32_t index(int s) const {
+        return s == 0 && h0 >= 0 ? h0 : (int32_t)cut_state(cut(s));
+    }
 };
 __device__ __forceinline__ Start start_state(const Plan &p, const Item &it, int range, bool h0) {
-    if (it.c0 > 0) return {(int32_t)cut_state(range), true};
-    if (!h0) return {-1, false};
-    if (it.c1 < it.nc && p.in_place) return {p.ranges + range, true};
-    return {it.n * p.H + it.h, false};
+    Start r{0, -1, false, range};
+    if (it.c0 > 0) {
+        const int before = p.compose ? p.cuts[range].before : 0;
+        r.first_cut = range - before;
+        r.steps = before + 1;
+        if (p.compose && h0) {
+            r.h0 = it.n * p.H + it.h;
+            ++r.steps;
+        }
+    } else if (h0) {
+        r.steps = 1;
+        r.h0_in_bnd = it.c1 < it.nc && p.in_place;
+        r.h0 = r.h0_in_bnd ? p.ranges + range : it.n * p.H + it.h;
+    }
+    return r;
 }
 
 // A log decay below this is e^g = 0 in fp32.  Prefix sums, whose differences give the decay

@@ -142,8 +142,14 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     int32_t *off = (int32_t *)(ws + L.off_off);
     float *bnd_log = (float *)(ws + L.log_off), *bnd = (float *)(ws + L.bnd_off);
     const int64_t dkdv = (int64_t)dk * dv;
+    // On the tensor cores a range can put its start state together from what the cuts before it
+    // hold: 64 KB a cut against a scan of about 7 us.  A unit has at most ranges / H + 1 cuts (the
+    // cuts are even, and H units are as long as the longest).  In place the initial states may
+    // be gone by then; the scan keeps copies.
+    const bool in_place = initial_state && initial_state == final_state;
+    const bool compose = dtype == KDA_BF16 && !in_place && L.ranges / H + 1 <= 12;
     const la::Plan p{cu_seqlens, off, cuts, num_seqs, H, Hk, L.ranges, L.chunk,
-                     initial_state && initial_state == final_state};
+                     in_place, compose};
     // A unit's states cost about as much as a chunk each (64 KB in, 64 KB out; measured on 16
     // packed sequences: 11.6k cycles beside 5.4k of a chunk).
     const int unit_cost = (initial_state ? 1 : 0) + (final_state ? 1 : 0);
@@ -166,7 +172,7 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     };
     if (L.split) {
         e = pass(false);
-        if (e == cudaSuccess) e = launch_la_scan(p, initial_state, bnd, bnd_log, dkdv, s);
+        if (e == cudaSuccess && !compose) e = launch_la_scan(p, initial_state, bnd, bnd_log, dkdv, s);
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     return cuda_status(pass(true));

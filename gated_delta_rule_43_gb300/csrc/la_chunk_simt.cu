@@ -28,7 +28,7 @@ __device__ __forceinline__ int owner(const int32_t *off, int N, int H, int64_t x
 }
 
 __device__ Cut place(const int32_t *off, int N, int H, int64_t total, int64_t x) {
-    Cut r{x, N, 0, 0, 0};
+    Cut r{x, N, 0, 0, 0, 0};
     if (x >= total) {
         r.x = total;
         return r;
@@ -155,9 +155,12 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
     __syncthreads();
     for (int i = tid; i <= ranges; i += kPlanThreads) {
         Cut r = s_cut[i];
-        if (r.inner)
+        if (r.inner) {
+            for (int j = i - 1; j > 0 && s_cut[j].inner && s_cut[j].n == r.n && s_cut[j].h == r.h; --j)
+                ++r.before;
             for (int j = i + 1; j < ranges && s_cut[j].inner && s_cut[j].n == r.n && s_cut[j].h == r.h; ++j)
                 ++r.inner;
+        }
         cuts[i] = r;
     }
 }
@@ -174,8 +177,7 @@ la_scan_kernel(Plan p, const float *__restrict__ h0, float *__restrict__ bnd,
     let_next_start();
     const int first = blockIdx.y + 1;
     const Cut f = p.cuts[first];
-    // a unit's chain starts at its first cut: the range before it holds the unit's start
-    if (!f.inner || p.cuts[first - 1].x > f.x - f.c) return;
+    if (!f.inner || f.before) return;   // a unit's chain starts at its first cut
     const int64_t i = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
     if (i >= dkdv4) return;
     const int last = first + f.inner - 1;
@@ -259,8 +261,8 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
         const int h = it.h;
         const int hk = h / (p.H / p.Hk);
         const int64_t nh = ((int64_t)it.n * p.H + h) * dkdv;
-        const Start from = OUT ? start_state(p, it, range, h0 != nullptr) : Start{-1, false};
-        const float *start = from.index < 0 ? nullptr : (from.in_bnd ? bnd : h0) + from.index * dkdv;
+        const Start from = OUT ? start_state(p, it, range, h0 != nullptr) : Start{};
+        const float *start = from.steps ? (from.in_bnd(0) ? bnd : h0) + from.index(0) * dkdv : nullptr;
         // rows past the sequence are zeros whatever memory holds there
         float4 nq[LQ], nk[LQ], nv[LV];
         float ng = 0.f;

@@ -301,7 +301,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         Walk walk(p, range);
         bool more = OUT ? walk.next(it) : before_cut(p, range + 1, it);
         for (; more && ok; more = OUT && walk.next(it))
-            role(it, OUT ? start_state(p, it, range, has_h0) : Start{-1, false},
+            role(it, OUT ? start_state(p, it, range, has_h0) : Start{},
                  OUT && has_hT && it.c1 == it.nc);
     };
     constexpr int NC = DVP / 2;
@@ -309,7 +309,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     if (warp < kRowWarps) {
         if (OUT) each_item([&](const Item &it, const Start &start, bool ends) {
             const int chunks = it.c1 - it.c0;
-            if (start.index >= 0) ++si;
+            si += start.steps;
             const int t = tid;   // this thread's row of the chunk
             const uint32_t lanes = (uint32_t)(32 * warp) << 16;
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
@@ -445,14 +445,47 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         };
         each_item([&](const Item &it, const Start &start, bool ends) {
             const int chunks = it.c1 - it.c0;
-            const uint32_t first_si = si;   // a start state's stage
-            if (start.index >= 0) ++si;
+            const uint32_t first_si = si;   // the start states' stages
+            si += start.steps;
             // These warps stop together: each failure is carried to the next bar_and.  Round c
             // ends chunk c (adds its product to S) and makes K~^T and the image of S for chunk
             // c + 1: K~^T before anything that its product does not need, that is with outputs
             // right after the tensor memory is free, without (two buffers) before the wait.
             bool fine = true;
             float decay = 0.f, decay_next = 0.f;   // of chunk c, c + 1
+            auto read_start = [&] {
+#pragma unroll
+                for (int j = 0; j < NC; ++j) S[j] = 0.f;
+#pragma unroll 1
+                for (int s = 0; s < start.steps; ++s) {
+                    const uint32_t fs = first_si + s, fb = fs & 1;
+                    fine = fine && wait.warp(kFullK + fb, (fs >> 1) & 1);
+                    if (fine && mine) {
+                        const float e = s ? expf(bnd_log[cut_state(start.cut(s))]) : 0.f;
+#pragma unroll
+                        for (int j = 0; j < NC; j += 4) {
+                            const int col = j0 + j;
+                            const float4 x = *reinterpret_cast<const float4 *>(
+                                sm + fb * M::kQK + (col / 32) * dk * 128 + i * 128 + ((((col % 32) / 4) ^ (i & 7)) << 4));
+                            S[j] = e * S[j] + x.x;
+                            S[j + 1] = e * S[j + 1] + x.y;
+                            S[j + 2] = e * S[j + 2] + x.z;
+                            S[j + 3] = e * S[j + 3] + x.w;
+                        }
+                    }
+                    ok = bar_and(3, 32 * kStateWarps, fine);
+                    if (!ok) return;
+                    if (tid == 32 * kRowWarps) {
+                        mbar_arrive(&bar[kFreeK + fb]);
+                        mbar_arrive(&bar[kFreeQ + fb]);
+                    }
+                }
+            };
+            // (a start of several states: they come through the stages before the first chunk)
+            if (OUT && start.steps > 1) {
+                read_start();
+                if (!ok) return;
+            }
             // (gi and si here: of chunk c + 1)
 #pragma unroll 1
             for (int c = -1; c < chunks; ++c) {
@@ -539,25 +572,8 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 }
                 if (OUT && c < 0) {
                     if (end_of) fine = put_end() && fine;
-                    const uint32_t fb = first_si & 1;
-                    if (start.index >= 0) fine = fine && wait.warp(kFullK + fb, (first_si >> 1) & 1);
-#pragma unroll
-                    for (int j = 0; j < NC; j += 4) {
-                        const int col = j0 + j;
-                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (fine && start.index >= 0 && mine)
-                            x = *reinterpret_cast<const float4 *>(
-                                sm + fb * M::kQK + (col / 32) * dk * 128 + i * 128 + ((((col % 32) / 4) ^ (i & 7)) << 4));
-                        S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
-                    }
-                    if (start.index >= 0) {
-                        ok = bar_and(3, 32 * kStateWarps, fine);
-                        if (!ok) break;
-                        if (tid == 32 * kRowWarps) {
-                            mbar_arrive(&bar[kFreeK + fb]);
-                            mbar_arrive(&bar[kFreeQ + fb]);
-                        }
-                    }
+                    if (start.steps <= 1) read_start();
+                    if (!ok) break;
                     // the old image's place has held a final state
                     if (end_of) fine = fine && wait.warp(kEndFree, (ends_before - 1) & 1);
                     end_of = 0;
@@ -602,7 +618,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     } else if (warp == kMmaWarp) {
         each_item([&](const Item &it, const Start &start, bool ends) {
             const int chunks = it.c1 - it.c0;
-            if (start.index >= 0) ++si;
+            si += start.steps;
             const uint32_t id_kk = idesc_bf16(128, 128, false, false);   // Q K^T
             const uint32_t id_km = idesc_bf16(128, DVP, false, true);    // the others: B is V or S
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
@@ -673,12 +689,12 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     } else if (warp == kLoadWarp) {
         each_item([&](const Item &it, const Start &start, bool ends) {
             const int h = it.h, chunks = it.c1 - it.c0;
-            const uint32_t first_si = si;   // a start state's stage
-            if (start.index >= 0) ++si;
+            const uint32_t first_si = si;   // the start states' stages
+            si += start.steps;
             const int hk = h / (p.H / p.Hk);
-            if (start.index >= 0) {
-                const uint32_t sb = first_si & 1, before = ((first_si - 2) >> 1) & 1;
-                if (first_si >= 2) ok = wait.warp(kFreeK + sb, before) && wait.warp(kFreeQ + sb, before);
+            for (int s = 0; s < start.steps; ++s) {
+                const uint32_t fs = first_si + s, sb = fs & 1, before = ((fs - 2) >> 1) & 1;
+                if (fs >= 2) ok = wait.warp(kFreeK + sb, before) && wait.warp(kFreeQ + sb, before);
                 if (!ok) return;
                 if (lane == 0) {
                     uint64_t *full = &bar[kFullK + sb];
@@ -686,8 +702,8 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     mbar_arrive_expect_tx(full, (uint32_t)dkdv * 4);
 #pragma unroll 1
                     for (int x = 0; x < dv / 32; ++x)
-                        tma_load_3d(sm + sb * M::kQK + x * dk * 128, start.in_bnd ? &tbnd : &th0, 32 * x,
-                                    0, start.index, full);
+                        tma_load_3d(sm + sb * M::kQK + x * dk * 128, start.in_bnd(s) ? &tbnd : &th0, 32 * x,
+                                    0, start.index(s), full);
                 }
                 ++issued_k;
                 __syncwarp();
@@ -802,7 +818,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     } else if (OUT && warp == kStoreWarp) {
         each_item([&](const Item &it, const Start &start, bool ends) {
             const int h = it.h, chunks = it.c1 - it.c0;
-            if (start.index >= 0) ++si;
+            si += start.steps;
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
                 const uint32_t b = gi & 1, sb = si & 1;
                 const int64_t t0 = it.t0 + (int64_t)c * C;
