@@ -441,6 +441,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kEndReady]);
+            __syncwarp();
             return true;
         };
         each_item([&](const Item &it, const Start &start, bool ends) {
@@ -479,6 +480,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         mbar_arrive(&bar[kFreeK + fb]);
                         mbar_arrive(&bar[kFreeQ + fb]);
                     }
+                    __syncwarp();
                 }
             };
             // (a start of several states: they come through the stages before the first chunk)
@@ -564,6 +566,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                             mbar_arrive(&bar[kKtReady + b]);
                             mbar_arrive(&bar[kGateFree + b]);
                         }
+                        __syncwarp();
                     }
                 }
                 if (!OUT && c >= 0) {
@@ -595,6 +598,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         fence_proxy_async();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar[kSReady]);
+                        __syncwarp();
                     }
                 }
                 decay = decay_next;
@@ -630,8 +634,11 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const uint64_t dvt = sdesc_sw128(base + M::kV + b * M::kVBytes, C * 128, 1024);
                 const uint64_t ds = sdesc_sw128(base + M::kS, DKP * 128, 1024);
                 if (OUT) {
+                    // A start of several states has been through both stages before this chunk:
+                    // K~^T says that this is over, and that a parity names one phase again.
+                    if (c == 0 && start.steps > 1) ok = wait.warp(kKtReady + b, ph);
                     // P of the chunk before lies over the scores
-                    ok = wait.warp(kFullK + sb, (si >> 1) & 1) && wait.warp(kFullQ + sb, (si >> 1) & 1) &&
+                    ok = ok && wait.warp(kFullK + sb, (si >> 1) & 1) && wait.warp(kFullQ + sb, (si >> 1) & 1) &&
                          (gi == 0 || wait.warp(kPvDone, (gi - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
@@ -686,7 +693,11 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 }
             }
         });
+        // nothing arrives at this CTA's barriers after it has left
+        if (ok && gi) ok = wait.warp(kFreeV + ((gi - 1) & 1), ((gi - 1) >> 1) & 1);
     } else if (warp == kLoadWarp) {
+        // (the states at the cuts were written by plain stores)
+        if (OUT) asm volatile("fence.proxy.async.global;" ::: "memory");
         each_item([&](const Item &it, const Start &start, bool ends) {
             const int h = it.h, chunks = it.c1 - it.c0;
             const uint32_t first_si = si;   // the start states' stages

@@ -57,6 +57,24 @@ def test_long_sequences_in_segments(dtype, in_place):
     assert (S is h0) == in_place
 
 
+@pytest.mark.parametrize("lens,H,Hk,dk,dv", [([4153], 16, 4, 128, 128), ([2100, 130, 3000], 14, 7, 64, 128),
+                                             ([9300, 0, 700], 16, 2, 32, 32), ([5000, 4100], 24, 8, 32, 64),
+                                             ([11000], 13, 13, 64, 32)])
+@pytest.mark.parametrize("h0", [True, False])
+def test_many_heads_of_many_segments(lens, H, Hk, dk, dv, h0):
+    """More than one cut in most heads, and ranges that start behind several of them."""
+    check(U.make(lens, H, Hk, dk, dv, BF, seed=H, h0=h0, speed=0.01))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_heads_of_many_segments_in_place(dtype):
+    args = U.make([2900, 1300], 16, 4, 64, 64, dtype, seed=12, speed=0.01)
+    q, k, v, g, cu, h0 = gpu(*args)
+    o, S = kda.la_chunk_fwd(q, k, v, g, cu, h0, final_state=h0, check=True)
+    ro, rS = U.la_ref(*args)
+    assert U.rel(o, ro) <= U.TOL_O[dtype] and U.rel(h0, rS) <= U.TOL_S
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_no_decay_and_fast_decay(dtype):
     args = list(U.make([300, 260], 3, 3, 64, 128, dtype, seed=5))
