@@ -13,6 +13,11 @@
 // unit has a range of its own, and one of at least 2 min_range chunks several, of min_range or
 // more.  Chunks are 128 tokens on the tensor cores and 32 on the CUDA cores; min_range is 1024
 // and 128 tokens, about where a walk costs as much as the first pass and the scan.
+//
+// Value heads that share queries and keys are walked side by side: `lanes` CTAs take the same
+// range of the row of every lanes-th head, so that what one of them reads the others find in
+// L2.  (With four heads a query/key head, tiles read and written without any arithmetic:
+// head after head 5.8k cycles a chunk, side by side 3.9k.)
 #pragma once
 
 #include "kda_common.cuh"
@@ -36,7 +41,8 @@ struct Plan {
     const int32_t *off;       // [N + 1]: chunks of the sequences before n
     const Cut *cuts;          // [ranges + 1], the last at the row's end
     int N, H, Hk;
-    int ranges;
+    int lanes;                // divides H / Hk
+    int ranges;               // of a lane
     int chunk;                // tokens
     int in_place;             // the final states overwrite the initial ones
     int compose;              // no scan: ranges put their start states together themselves
@@ -59,11 +65,12 @@ __device__ __forceinline__ void set_tokens(Item &it, int chunk, int64_t begin, i
 struct Walk {
     const Plan &p;
     int64_t x, end;
+    int lane;
     int n, h, c;
     int nc = 0;               // chunks of sequence n, 0: not read yet
     int64_t begin, stop;      // its tokens
-    __device__ __forceinline__ Walk(const Plan &plan, int range)
-        : p(plan), x(plan.cuts[range].x), end(plan.cuts[range + 1].x), n(plan.cuts[range].n),
+    __device__ __forceinline__ Walk(const Plan &plan, int range, int lane_)
+        : p(plan), x(plan.cuts[range].x), end(plan.cuts[range + 1].x), lane(lane_), n(plan.cuts[range].n),
           h(plan.cuts[range].h), c(plan.cuts[range].c) {}
     __device__ __forceinline__ bool next(Item &it) {
         if (x >= end) return false;
@@ -73,14 +80,14 @@ struct Walk {
             stop = p.cu[n + 1];
         }
         it.n = n;
-        it.h = h;
+        it.h = h * p.lanes + lane;
         it.c0 = c;
         it.nc = nc;
         it.c1 = (int)min((int64_t)nc, c + (end - x));
         set_tokens(it, p.chunk, begin, stop);
         x += it.c1 - c;
         c = 0;
-        if (++h == p.H) {
+        if ((++h) * p.lanes == p.H) {
             h = 0;
             ++n;
             nc = 0;
@@ -114,11 +121,11 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, siz
 
 // What the range before cut `i` (1 ..) contributes to it; false when that cut is none inside
 // a unit.
-__device__ __forceinline__ bool before_cut(const Plan &p, int i, Item &it) {
+__device__ __forceinline__ bool before_cut(const Plan &p, int i, int lane, Item &it) {
     const Cut e = p.cuts[i];
     if (!e.inner) return false;
     it.n = e.n;
-    it.h = e.h;
+    it.h = e.h * p.lanes + lane;
     it.c1 = e.c;
     it.c0 = (int)max((int64_t)0, e.c - (e.x - p.cuts[i - 1].x));
     it.nc = p.off[e.n + 1] - p.off[e.n];
@@ -126,31 +133,35 @@ __device__ __forceinline__ bool before_cut(const Plan &p, int i, Item &it) {
     return true;
 }
 
-// The states of the inner boundaries: cut i at index i - 1.  Where the final states overwrite
+// The states of the inner boundaries, cuts 1 .. of each lane.  Where the final states overwrite
 // the initial ones, the last range of a unit may write before the first one has read: the
-// scan keeps a copy of the initial state of such a unit, for range i at index ranges + i.
-__device__ __forceinline__ int64_t cut_state(int i) { return i - 1; }
+// scan keeps a copy of the initial state of such a unit, for the range that it begins in.
+__device__ __forceinline__ int64_t cut_state(const Plan &p, int i, int lane) {
+    return (int64_t)(i - 1) * p.lanes + lane;
+}
+__device__ __forceinline__ int64_t initial_copy(const Plan &p, int range, int lane) {
+    return (int64_t)(p.ranges + range) * p.lanes + lane;
+}
 
-// Where an item of range `range` starts from: `steps` states, each taken after the decay of what
-// lies between it and the one before.  A unit's start: none (zeros) or the initial state (its
-// copy).  A cut after the scan: the state there.  A cut without it (p.compose): the unit's
-// initial state and what the cuts up to this one hold.
+// Where an item starts from: `steps` states, each taken after the decay of what lies between it
+// and the one before.  A unit's start: none (zeros) or the initial state (its copy).  A cut
+// after the scan: the state there.  A cut without it (p.compose): the unit's initial state and
+// what the cuts up to this one hold.
 struct Start {
     int steps;
     int32_t h0;               // index of the first step's initial state, -1: it is a cut's
-    bool h0_in_bnd;
-    int first_cut;
-    __device__ __forceinline__ bool in_bnd(int s) const { return s > 0 || h0 < 0 || h0_in_bnd; }
-    __device__ __forceinline__ int cut(int s) const { return first_cut + s - (h0 >= 0 ? 1 : 0); }
+    bool h0_copied;
+    int32_t first, lanes;     // the first cut's state; from one to the next
+    __device__ __forceinline__ bool in_bnd(int s) const { return s > 0 || h0 < 0 || h0_copied; }
     __device__ __forceinline__ int32_t index(int s) const {
-        return s == 0 && h0 >= 0 ? h0 : (int32_t)cut_state(cut(s));
+        return s == 0 && h0 >= 0 ? h0 : first + (s - (h0 >= 0 ? 1 : 0)) * lanes;
     }
 };
-__device__ __forceinline__ Start start_state(const Plan &p, const Item &it, int range, bool h0) {
-    Start r{0, -1, false, range};
+__device__ __forceinline__ Start start_state(const Plan &p, const Item &it, int range, int lane, bool h0) {
+    Start r{0, -1, false, 0, p.lanes};
     if (it.c0 > 0) {
         const int before = p.compose ? p.cuts[range].before : 0;
-        r.first_cut = range - before;
+        r.first = (int32_t)cut_state(p, range - before, lane);
         r.steps = before + 1;
         if (p.compose && h0) {
             r.h0 = it.n * p.H + it.h;
@@ -158,8 +169,8 @@ __device__ __forceinline__ Start start_state(const Plan &p, const Item &it, int 
         }
     } else if (h0) {
         r.steps = 1;
-        r.h0_in_bnd = it.c1 < it.nc && p.in_place;
-        r.h0 = r.h0_in_bnd ? p.ranges + range : it.n * p.H + it.h;
+        r.h0_copied = it.c1 < it.nc && p.in_place;
+        r.h0 = r.h0_copied ? (int32_t)initial_copy(p, range, lane) : it.n * p.H + it.h;
     }
     return r;
 }

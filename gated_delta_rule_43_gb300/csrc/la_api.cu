@@ -10,7 +10,7 @@
 namespace kda {
 cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off, int unit_cost,
                            int chunk, int min_range, la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
-                           int H, int64_t dkdv, cudaStream_t s);
+                           int H, int lanes, int64_t dkdv, cudaStream_t s);
 cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
                            int64_t dkdv, cudaStream_t s);
 cudaError_t launch_la_simt(bool out, int dk, int dv, const la::Plan &p, const float *q,
@@ -69,26 +69,32 @@ bool stride_ok(int64_t stride, int64_t T, int32_t heads, int32_t D, int32_t dtyp
 }
 
 struct LaLayout {
-    int ranges, chunk, min_range;
+    int lanes, ranges, chunk, min_range;
     bool split;
     size_t cuts_off, off_off, log_off, bnd_off, total;
 };
 
-// One range an SM, and no more than there can be chunks.  Sequences are cut only where one
-// may be longer than a range of the least length (the lengths are on the device).
-LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t dk, int32_t dv, int32_t dtype, int sms) {
+// One range of one lane an SM, and no more than there can be chunks.  Sequences are cut only where
+// one may be longer than a range of the least length (the lengths are on the device).  On the
+// tensor cores all heads that share queries and keys are lanes, or as many of them as leave no
+// more than 1/24 of the SMs over; the CUDA cores are not bound by what they read.
+LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t dv, int32_t dtype, int sms) {
     LaLayout L{};
     L.chunk = dtype == KDA_BF16 ? la::kTcChunk : la::kSimtChunk;
     L.min_range = dtype == KDA_BF16 ? la::kTcMinRange : la::kSimtMinRange;
-    const int64_t most = (T / L.chunk + N) * (int64_t)H;
     if (sms > 1024) sms = 1024;   // (the plan's room)
+    L.lanes = dtype == KDA_BF16 ? H / Hk : 1;
+    while ((H / Hk) % L.lanes != 0 || L.lanes > sms || sms % L.lanes * 24 > sms) --L.lanes;
+    const int64_t most = (T / L.chunk + N) * (int64_t)(H / L.lanes);
+    sms /= L.lanes;
     L.ranges = (int)(most < 1 ? 1 : most < sms ? most : sms);
     L.split = L.ranges > 1 && T > L.min_range * L.chunk;
+    const size_t all = (size_t)L.ranges * L.lanes;
     L.cuts_off = kHeaderBytes;
     L.off_off = L.cuts_off + round_up(sizeof(la::Cut) * ((size_t)L.ranges + 1), 256);
     L.log_off = L.off_off + round_up(3 * sizeof(int32_t) * ((size_t)N + 1), 256);
-    L.bnd_off = L.log_off + round_up(sizeof(float) * (size_t)L.ranges, 256);
-    L.total = L.bnd_off + (L.split ? sizeof(float) * 2 * (size_t)L.ranges * dk * dv : 0);
+    L.bnd_off = L.log_off + round_up(sizeof(float) * all, 256);
+    L.total = L.bnd_off + (L.split ? sizeof(float) * 2 * all * dk * dv : 0);
     return L;
 }
 
@@ -107,7 +113,7 @@ size_t kda_la_chunk_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, i
     if (!dtype_ok(dtype) || !head_ok(dk) || !head_ok(dv) ||
         !la_sizes_ok(total_tokens, num_seqs, H, Hk, dk, dv))
         return 0;
-    return la_layout(total_tokens, num_seqs, H, dk, dv, dtype, sm_count()).total;
+    return la_layout(total_tokens, num_seqs, H, Hk, dk, dv, dtype, sm_count()).total;
 }
 
 kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
@@ -131,7 +137,7 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     if (!aligned(g, 4) || !aligned(cu_seqlens, 4) || !aligned(workspace, 256))
         return KDA_ERR_INVALID_ARG;
     if (o && (o == q || o == k || o == v)) return KDA_ERR_INVALID_ARG;
-    const LaLayout L = la_layout(total_tokens, num_seqs, H, dk, dv, dtype, sm_count());
+    const LaLayout L = la_layout(total_tokens, num_seqs, H, Hk, dk, dv, dtype, sm_count());
     if (workspace_bytes < L.total) return KDA_ERR_INVALID_ARG;
 
     cudaStream_t s = (cudaStream_t)stream;
@@ -143,18 +149,18 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     float *bnd_log = (float *)(ws + L.log_off), *bnd = (float *)(ws + L.bnd_off);
     const int64_t dkdv = (int64_t)dk * dv;
     // On the tensor cores a range can put its start state together from what the cuts before it
-    // hold: 64 KB a cut against a scan of about 7 us.  A unit has at most ranges / H + 1 cuts (the
+    // hold: 64 KB a cut against a scan of about 7 us.  A unit has at most ranges * lanes / H + 1 cuts (the
     // cuts are even, and H units are as long as the longest).  In place the initial states may
     // be gone by then; the scan keeps copies.
     const bool in_place = initial_state && initial_state == final_state;
-    const bool compose = dtype == KDA_BF16 && !in_place && L.ranges / H + 1 <= 12;
-    const la::Plan p{cu_seqlens, off, cuts, num_seqs, H, Hk, L.ranges, L.chunk,
+    const bool compose = dtype == KDA_BF16 && !in_place && L.ranges * L.lanes / H + 1 <= 12;
+    const la::Plan p{cu_seqlens, off, cuts, num_seqs, H, Hk, L.lanes, L.ranges, L.chunk,
                      in_place, compose};
     // A unit's states cost about as much as a chunk each (64 KB in, 64 KB out; measured on 16
     // packed sequences: 11.6k cycles beside 5.4k of a chunk).
     const int unit_cost = (initial_state ? 1 : 0) + (final_state ? 1 : 0);
     cudaError_t e = launch_la_plan(cu_seqlens, num_seqs, total_tokens, off, unit_cost, L.chunk,
-                                   L.min_range, cuts, L.ranges, L.split, st, initial_state, final_state, H, dkdv, s);
+                                   L.min_range, cuts, L.ranges, L.split, st, initial_state, final_state, H, L.lanes, dkdv, s);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (total_tokens == 0) return KDA_OK;
     CUtensorMap maps[8];

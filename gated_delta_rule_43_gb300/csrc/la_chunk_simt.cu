@@ -50,11 +50,11 @@ __global__ void __launch_bounds__(kPlanThreads)
 la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *off,
                int32_t *piece_off, int32_t *cost_off, int unit_cost, int chunk,
                int min_range, Cut *cuts, int ranges, int split,
-               StatusWord *st, const float *h0, float *S_out, int H,
-               int64_t dkdv4) {
+               StatusWord *st, const float *h0, float *S_out, int all_heads, int H,
+               int64_t dkdv4) {   // H: heads of a lane
     if (S_out) {
-        for (int64_t nh = blockIdx.x; nh < (int64_t)N * H; nh += gridDim.x) {
-            const int n = (int)(nh / H);
+        for (int64_t nh = blockIdx.x; nh < (int64_t)N * all_heads; nh += gridDim.x) {
+            const int n = (int)(nh / all_heads);
             const int64_t b = cu[n], e = cu[n + 1];
             if (b < e && b >= 0 && e <= T_tot) continue;
             float4 *dst = reinterpret_cast<float4 *>(S_out) + nh * dkdv4;
@@ -175,24 +175,24 @@ la_scan_kernel(Plan p, const float *__restrict__ h0, float *__restrict__ bnd,
                const float *__restrict__ bnd_log, int64_t dkdv4) {
     wait_for_previous();
     let_next_start();
-    const int first = blockIdx.y + 1;
+    const int first = blockIdx.y / p.lanes + 1, lane = blockIdx.y % p.lanes;
     const Cut f = p.cuts[first];
     if (!f.inner || f.before) return;   // a unit's chain starts at its first cut
     const int64_t i = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
     if (i >= dkdv4) return;
     const int last = first + f.inner - 1;
-    float4 S = h0 ? reinterpret_cast<const float4 *>(h0)[((int64_t)f.n * p.H + f.h) * dkdv4 + i]
+    float4 S = h0 ? reinterpret_cast<const float4 *>(h0)[((int64_t)f.n * p.H + f.h * p.lanes + lane) * dkdv4 + i]
                   : make_float4(0.f, 0.f, 0.f, 0.f);
     float4 *at = reinterpret_cast<float4 *>(bnd) + i;
-    if (p.in_place) at[(int64_t)(p.ranges + first - 1) * dkdv4] = S;
+    if (p.in_place) at[initial_copy(p, first - 1, lane) * dkdv4] = S;
     for (int b = first; b <= last; b += kAhead) {
         float4 add[kAhead];
         float a[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
             if (b + j <= last) {
-                add[j] = at[cut_state(b + j) * dkdv4];
-                a[j] = bnd_log[cut_state(b + j)];
+                add[j] = at[cut_state(p, b + j, lane) * dkdv4];
+                a[j] = bnd_log[cut_state(p, b + j, lane)];
             }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
@@ -202,7 +202,7 @@ la_scan_kernel(Plan p, const float *__restrict__ h0, float *__restrict__ bnd,
                 S.y = e * S.y + add[j].y;
                 S.z = e * S.z + add[j].z;
                 S.w = e * S.w + add[j].w;
-                at[cut_state(b + j) * dkdv4] = S;
+                at[cut_state(p, b + j, lane) * dkdv4] = S;
             }
     }
 }
@@ -254,14 +254,14 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
     const int blk = blockIdx.x % NB, range = blockIdx.x / NB;
     const int j0 = blk * DVB;
     Item it;
-    Walk walk(p, range);
-    bool more = OUT ? walk.next(it) : before_cut(p, range + 1, it);
+    Walk walk(p, range, 0);   // (one lane)
+    bool more = OUT ? walk.next(it) : before_cut(p, range + 1, 0, it);
 
     for (; more; more = OUT && walk.next(it)) {
         const int h = it.h;
         const int hk = h / (p.H / p.Hk);
         const int64_t nh = ((int64_t)it.n * p.H + h) * dkdv;
-        const Start from = OUT ? start_state(p, it, range, h0 != nullptr) : Start{};
+        const Start from = OUT ? start_state(p, it, range, 0, h0 != nullptr) : Start{};
         const float *start = from.steps ? (from.in_bnd(0) ? bnd : h0) + from.index(0) * dkdv : nullptr;
         // rows past the sequence are zeros whatever memory holds there
         float4 nq[LQ], nk[LQ], nv[LV];
@@ -422,14 +422,14 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
             __syncthreads();
         }
         float *dst = OUT ? (it.c1 == it.nc && hT ? hT + nh : nullptr)
-                         : bnd + cut_state(range + 1) * dkdv;
+                         : bnd + cut_state(p, range + 1, 0) * dkdv;
         if (dst) {
 #pragma unroll
             for (int r = 0; r < SR; ++r)
                 *reinterpret_cast<float4 *>(dst + (int64_t)(rg * SR + r) * DV + j0 + c4) =
                     make_float4(S[r][0], S[r][1], S[r][2], S[r][3]);
         }
-        if (!OUT && blk == 0 && tid == 0) bnd_log[cut_state(range + 1)] = log_sum;
+        if (!OUT && blk == 0 && tid == 0) bnd_log[cut_state(p, range + 1, 0)] = log_sum;
     }
 }
 
@@ -453,19 +453,19 @@ static cudaError_t launch_dims(bool out, const Plan &p, const float *q, const fl
 
 cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off, int unit_cost,
                            int chunk, int min_range, la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
-                           int H, int64_t dkdv, cudaStream_t s) {
+                           int H, int lanes, int64_t dkdv, cudaStream_t s) {
     float *S_out = hT != h0 ? hT : nullptr;   // an in-place update leaves empty ones as they are
     const int64_t nh = (int64_t)N * H;
     const int grid = S_out && nh > 1 ? (int)(nh < 256 ? nh : 256) : 1;
     la::la_plan_kernel<<<grid, la::kPlanThreads, 0, s>>>(
-        cu, N, T_tot, off, off + N + 1, off + 2 * (N + 1), unit_cost, chunk, min_range, cuts, ranges, split, st, h0, S_out, H, dkdv / 4);
+        cu, N, T_tot, off, off + N + 1, off + 2 * (N + 1), unit_cost, chunk, min_range, cuts, ranges, split, st, h0, S_out, H, H / lanes, dkdv / 4);
     return cudaGetLastError();
 }
 
 cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
                            int64_t dkdv, cudaStream_t s) {
     const dim3 grid((unsigned)((dkdv / 4 + la::kScanThreads - 1) / la::kScanThreads),
-                    (unsigned)(p.ranges - 1));
+                    (unsigned)((p.ranges - 1) * p.lanes));
     return la::launch_after(la::la_scan_kernel, grid, dim3(la::kScanThreads), 0, s, p, h0, bnd, bnd_log,
                             dkdv / 4);
 }

@@ -65,43 +65,40 @@ enum Bar {
     kFullQ = 0,      // [2] a stage's q has landed
     kFullK = 2,      // [2] k (or a start state, over both)
     kFullV = 4,      // [2] v
-    kFreeQ = 6,      // [2] q has been read, and the outputs that took its place have left
+    kFreeQ = 6,      // [2] q has been read, and half of a final state that took its place has left
     kFreeK = 8,      // [2] k (or a start state) has been read
-    kFreeV = 10,     // [2] v has, and half of a final state that took its place has left
+    kFreeV = 10,     // [2] v has, and the outputs that took its place have left
     kGate = 12,      // [2] a chunk's decays are there
     kGateFree = 14,  // [2] ... and have been used
-    kKtReady = 16,   // [2] K~^T is in tensor memory (two buffers without outputs)
-    kKvDone = 18,    // [2] K~^T V
+    kKtReady = 16,   // [2] K~^T is in tensor memory, a half of each 64 tokens at a time (without
+                     //     outputs: whole, two buffers)
+    kKvDone = 18,    // [2] K~^T V of a half, of both (of a buffer)
     kQkDone = 20,    // Q K^T
     kQsDone = 21,    // Q S
     kPvDone = 22,    // P V
     kPReady = 23,    // P and the decayed Q S are in tensor memory
     kSReady = 24,    // the image of S is in shared memory
     kOFree = 25,     // the accumulator of O has been read: the outputs are in shared memory
-    kOStored = 26,   // ... and have left it
-    kEndReady = 27,  // an item's final state is in shared memory
-    kEndFree = 28,   // ... and has left the place of the image of S
-    kDrain = 29,
+    kEndReady = 26,  // an item's final state is in shared memory
+    kEndFree = 27,   // ... and has left the place of the image of S
+    kStartRead = 28, // [2] a start state has been read out of its stage
     kBars = 30
 };
 
 // Two stages of q, k and v, the image of S ([DKP rows][DVP]), the decays.  A start state (fp32, in
 // 32-column blocks of 128-byte rows) takes the place of q and k, a final state that of the
-// image of S and of v.  A chunk's outputs are laid out for their store over its q, or, wider
-// than that, in a place of their own.
+// image of S and of q.  A chunk's outputs are laid out for their store over its v, which is read
+// last and needed last (over q, they held up the load of the next but one: 5.0k cycles a chunk).
 template <int DKP, int DVP> struct Map {
     static constexpr uint32_t kQ = 0, kK = DKP * 256, kQK = 2 * DKP * 256;   // within a stage
     static constexpr uint32_t kV = 2 * kQK, kVBytes = DVP * 256;
     static constexpr uint32_t kS = kV + 2 * kVBytes;
-    static constexpr bool kOverQ = DVP <= DKP;
-    static constexpr uint32_t kO = kS + DKP * DVP * 2;
-    static constexpr uint32_t kGates = kO + (kOverQ ? 0 : C * DVP * 2);
+    static constexpr uint32_t kGates = kS + DKP * DVP * 2;
     static constexpr uint32_t kTot = kGates + 2 * sizeof(Gates);   // decay of the chunk, [2]
     static constexpr uint32_t kBar = kTot + 8;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 8;
-    static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kO % 1024 == 0 && kQK % 1024 == 0 &&
-                      kV % 1024 == 0 && kBytes <= 232448 && DKP * DVP * 4 <= kQK &&
-                      DKP * DVP * 2 <= kVBytes,
+    static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kQK % 1024 == 0 && kV % 1024 == 0 &&
+                      kBytes <= 232448 && DKP * DVP * 4 <= kQK && DKP * DVP * 2 <= kK,
                   "layout");
 };
 
@@ -214,6 +211,17 @@ struct Waits {
     __device__ __forceinline__ bool warp(int which, uint32_t parity) const {
         return __all_sync(0xffffffffu, (*this)(which, parity));
     }
+    // Several at a time, a lane each: beside the products' reads of shared memory each look at a
+    // barrier takes 200 cycles, so they are not taken in turn.
+    __device__ __forceinline__ bool warp(int w0, uint32_t p0, int w1, uint32_t p1) const {
+        const bool one = threadIdx.x & 1;
+        return warp(one ? w1 : w0, one ? p1 : p0);
+    }
+    __device__ __forceinline__ bool warp(int w0, uint32_t p0, int w1, uint32_t p1, int w2, uint32_t p2,
+                                         int w3, uint32_t p3) const {
+        const bool two = threadIdx.x & 2;
+        return warp(two ? w2 : w0, two ? p2 : p0, two ? w3 : w1, two ? p3 : p1);
+    }
 };
 
 // OUT: outputs and final states of the CTA's range.  Else what the end of the range leaves at
@@ -233,7 +241,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     extern __shared__ __align__(1024) uint8_t sm[];
     using M = Map<DKP, DVP>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int range = blockIdx.x;
+    const int range = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
     wait_for_previous();
     let_next_start();
     if (OUT ? p.cuts[range].x >= p.cuts[range + 1].x : !p.cuts[range + 1].inner) return;
@@ -259,6 +267,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             mbar_init(&bar[kGateFree + b], kStateWarps + (OUT ? kRowWarps : 0));
             mbar_init(&bar[kKtReady + b], kStateWarps);
             mbar_init(&bar[kKvDone + b], 1);
+            mbar_init(&bar[kStartRead + b], kStateWarps);
         }
         mbar_init(&bar[kQkDone], 1);
         mbar_init(&bar[kQsDone], 1);
@@ -266,10 +275,8 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         mbar_init(&bar[kPReady], kRowWarps);
         mbar_init(&bar[kSReady], kStateWarps);
         mbar_init(&bar[kOFree], kRowWarps);
-        mbar_init(&bar[kOStored], 1);
         mbar_init(&bar[kEndReady], kStateWarps);
         mbar_init(&bar[kEndFree], 1);
-        mbar_init(&bar[kDrain], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -292,16 +299,17 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     uint32_t si = 0;    // stages of q and k so far (chunks and start states)
     bool ok = true;
     uint32_t issued_q = 0, issued_k = 0, issued_v = 0;   // (load warp)
+    uint32_t start_in = 0, starts_read = 0;              // ... a bit a stage: holds a start state; parity of those
     uint32_t ends_before = 0;                            // (store and state warps) final states so far
 
     // Each role goes through the range's items for itself: role(item, its start, whether it has a
     // final state to store).
     auto each_item = [&](auto role) {
         Item it;
-        Walk walk(p, range);
-        bool more = OUT ? walk.next(it) : before_cut(p, range + 1, it);
+        Walk walk(p, range, side);
+        bool more = OUT ? walk.next(it) : before_cut(p, range + 1, side, it);
         for (; more && ok; more = OUT && walk.next(it))
-            role(it, OUT ? start_state(p, it, range, has_h0) : Start{},
+            role(it, OUT ? start_state(p, it, range, side, has_h0) : Start{},
                  OUT && has_hT && it.c1 == it.nc);
     };
     constexpr int NC = DVP / 2;
@@ -309,57 +317,70 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     if (warp < kRowWarps) {
         if (OUT) each_item([&](const Item &it, const Start &start, bool ends) {
             const int chunks = it.c1 - it.c0;
-            si += start.steps;
             const int t = tid;   // this thread's row of the chunk
             const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-            for (int c = 0; c < chunks; ++c, ++gi, ++si) {
-                const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
-                ok = wait.warp(kGate + b, ph) && wait.warp(kQkDone, gi & 1);
+            for (int c = 0; c < chunks; ++c, ++gi) {
+                const uint32_t b = gi & 1, ph = (gi >> 1) & 1;
+                ok = wait.warp(kGate + b, ph);
                 if (!ok) break;
-                tc_fence_after();
+                // All that depends on the decays alone while the scores are formed: the factors of
+                // t's own block and, for the blocks before, exp(G_t - R).
                 const Gates &G = gates[b];
                 const float Gt = G.G[t];
+                const float e = ex2(Gt);
+                float r[3], own[32];
+#pragma unroll
+                for (int cb = 0; cb < 3; ++cb) r[cb] = ex2(Gt - G.G[32 * cb + 31]);
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(&G.G[32 * warp + j]);
+                    own[j] = ex2(Gt - f.x);
+                    own[j + 1] = ex2(Gt - f.y);
+                    own[j + 2] = ex2(Gt - f.z);
+                    own[j + 3] = ex2(Gt - f.w);
+                }
+                ok = wait.warp(kQkDone, gi & 1);
+                if (!ok) break;
+                tc_fence_after();
+                // P, over scores that this warp has read: its own block first, kept until its
+                // columns are free, then the blocks before.
+                uint32_t mine[16];
+                {
+                    float a[32];
+                    tmem_ld32(tA + lanes + 32 * warp, a);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)   // (a score past t may be anything)
+                        mine[j / 2] = pack2(j <= lane ? a[j] * own[j] : 0.f, j < lane ? a[j + 1] * own[j + 1] : 0.f);
+                }
 #pragma unroll 1
-                for (int cb = 0; cb < 4; ++cb) {
+                for (int cb = 0; cb < warp; ++cb) {
+                    const float rb = cb == 0 ? r[0] : cb == 1 ? r[1] : r[2];
+                    const float2 rf = make_float2(rb, rb);
+                    float a[32];
+                    float4 f[8];
+                    tmem_ld32(tA + lanes + 32 * cb, a);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = *reinterpret_cast<const float4 *>(&G.cf[32 * cb + 4 * j]);
+                    tmem_ld_wait();
                     uint32_t pk[16];
-                    if (cb <= warp) {
-                        float a[32];
-                        tmem_ld32(tA + lanes + 32 * cb, a);
-                        tmem_ld_wait();
-                        if (cb < warp) {
-                            const float r = ex2(Gt - G.G[32 * cb + 31]);
-                            const float2 rf = make_float2(r, r);
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(&G.cf[32 * cb + j]);
-                                const float2 x = mul2(make_float2(a[j], a[j + 1]),
-                                                      mul2(rf, make_float2(f.x, f.y)));
-                                const float2 y = mul2(make_float2(a[j + 2], a[j + 3]),
-                                                      mul2(rf, make_float2(f.z, f.w)));
-                                pk[j / 2] = pack2(x.x, x.y);
-                                pk[j / 2 + 1] = pack2(y.x, y.y);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(&G.G[32 * cb + j]);
-                                pk[j / 2] = pack2(j <= lane ? a[j] * ex2(Gt - f.x) : 0.f,
-                                                  j + 1 <= lane ? a[j + 1] * ex2(Gt - f.y) : 0.f);
-                                pk[j / 2 + 1] = pack2(j + 2 <= lane ? a[j + 2] * ex2(Gt - f.z) : 0.f,
-                                                      j + 3 <= lane ? a[j + 3] * ex2(Gt - f.w) : 0.f);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) pk[j] = 0;
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 x = mul2(make_float2(a[4 * j], a[4 * j + 1]), mul2(rf, make_float2(f[j].x, f[j].y)));
+                        const float2 y = mul2(make_float2(a[4 * j + 2], a[4 * j + 3]), mul2(rf, make_float2(f[j].z, f[j].w)));
+                        pk[2 * j] = pack2(x.x, x.y);
+                        pk[2 * j + 1] = pack2(y.x, y.y);
                     }
-                    // (columns of scores that this warp has read)
                     tmem_st16(tA + lanes + 16 * cb, pk);
                 }
+                tmem_st16(tA + lanes + 16 * warp, mine);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) mine[j] = 0;
+#pragma unroll 1
+                for (int cb = warp + 1; cb < 4; ++cb) tmem_st16(tA + lanes + 16 * cb, mine);
                 ok = wait.warp(kQsDone, gi & 1);
                 if (!ok) break;
                 tc_fence_after();   // P V adds to exp(G_t) Q S
-                const float e = ex2(Gt);
                 const float2 eG = make_float2(e, e);
 #pragma unroll 1
                 for (int j0 = 0; j0 < DVP; j0 += 64) {
@@ -390,9 +411,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 if (!ok) break;
                 tc_fence_after();
                 // the outputs, for the store warp
-                if (!M::kOverQ && gi > 0) ok = wait.warp(kOStored, (gi - 1) & 1);
-                if (!ok) break;
-                uint8_t *so = sm + (M::kOverQ ? sb * M::kQK + M::kQ : M::kO);
+                uint8_t *so = sm + M::kV + b * M::kVBytes;
 #pragma unroll 1
                 for (int cb = 0; cb < DVP / 32; cb += 2) {
                     float x[2][32];
@@ -426,13 +445,13 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         float S[NC];
 #pragma unroll
         for (int j = 0; j < NC; ++j) S[j] = 0.f;
-        uint32_t end_of = 0;   // the item that ended before chunk number end_of (> 0) has a final state
+        bool image_taken = false;   // the image's place holds a final state
         // S as the final state of an item, for the store warp: over the image of S (first half of
-        // the columns) and the last chunk's v, in 32-column blocks of 128-byte rows
+        // the columns) and the last chunk's q, in 32-column blocks of 128-byte rows
         auto put_end = [&] {
-            if (!wait.warp(kPvDone, (end_of - 1) & 1)) return false;
+            if (!wait.warp(kQsDone, (gi - 1) & 1)) return false;
             if (mine) {
-                uint8_t *at = sm + (half ? M::kV + ((end_of - 1) & 1) * M::kVBytes : M::kS);
+                uint8_t *at = sm + (half ? ((si - 1) & 1) * M::kQK + M::kQ : M::kS);
 #pragma unroll
                 for (int j = 0; j < NC; j += 4)
                     *reinterpret_cast<float4 *>(at + (j / 32) * dk * 128 + i * 128 + ((((j % 32) / 4) ^ (i & 7)) << 4)) =
@@ -444,15 +463,24 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             __syncwarp();
             return true;
         };
+        // S <- decay S + the product, from tensor memory
+        auto add_product = [&](uint32_t other, float decay) {
+#pragma unroll
+            for (int jb = 0; jb < NC; jb += 32) {
+                float x[32];
+                tmem_ld32(tKV + other + lanes + j0 + jb, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[jb + j] = decay * S[jb + j] + x[j];
+            }
+        };
         each_item([&](const Item &it, const Start &start, bool ends) {
             const int chunks = it.c1 - it.c0;
             const uint32_t first_si = si;   // the start states' stages
             si += start.steps;
-            // These warps stop together: each failure is carried to the next bar_and.  Round c
-            // ends chunk c (adds its product to S) and makes K~^T and the image of S for chunk
-            // c + 1: K~^T before anything that its product does not need, that is with outputs
-            // right after the tensor memory is free, without (two buffers) before the wait.
-            bool fine = true;
+            // Round c ends chunk c (adds its product to S) and makes K~^T and the image of S for
+            // chunk c + 1: the first half of K~^T while the second half's product still runs, the
+            // image last.  (Without outputs, in two buffers: K~^T first.)
             float decay = 0.f, decay_next = 0.f;   // of chunk c, c + 1
             auto read_start = [&] {
 #pragma unroll
@@ -460,9 +488,10 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
 #pragma unroll 1
                 for (int s = 0; s < start.steps; ++s) {
                     const uint32_t fs = first_si + s, fb = fs & 1;
-                    fine = fine && wait.warp(kFullK + fb, (fs >> 1) & 1);
-                    if (fine && mine) {
-                        const float e = s ? expf(bnd_log[cut_state(start.cut(s))]) : 0.f;
+                    ok = wait.warp(kFullK + fb, (fs >> 1) & 1);
+                    if (!ok) return;
+                    if (mine) {
+                        const float e = s ? expf(bnd_log[start.index(s)]) : 0.f;
 #pragma unroll
                         for (int j = 0; j < NC; j += 4) {
                             const int col = j0 + j;
@@ -474,12 +503,8 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                             S[j + 3] = e * S[j + 3] + x.w;
                         }
                     }
-                    ok = bar_and(3, 32 * kStateWarps, fine);
-                    if (!ok) return;
-                    if (tid == 32 * kRowWarps) {
-                        mbar_arrive(&bar[kFreeK + fb]);
-                        mbar_arrive(&bar[kFreeQ + fb]);
-                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[kStartRead + fb]);
                     __syncwarp();
                 }
             };
@@ -493,66 +518,59 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             for (int c = -1; c < chunks; ++c) {
                 const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
                 const bool next = c + 1 < chunks;
-                auto end_chunk = [&] {
-                    fine = fine && wait.warp(kKvDone + (b ^ 1), ((gi - 1) >> 1) & 1);
-                    ok = bar_and(3, 32 * kStateWarps, fine);
-                    if (!ok) return;
-                    tc_fence_after();
-#pragma unroll
-                    for (int jb = 0; jb < NC; jb += 32) {
-                        float x[32];
-                        tmem_ld32(tKV + (OUT ? 0 : (b ^ 1) * kOther) + lanes + j0 + jb, x);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) S[jb + j] = decay * S[jb + j] + x[j];
-                    }
-                    tc_fence_before();
-                };
-                if (OUT && c >= 0) {
-                    end_chunk();
-                    if (!ok) break;
-                }
+                const int at_chunk = OUT ? c + 1 : chunks - 2 - c;
+                const int len = next ? (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)at_chunk * C) : C;
                 if (next) {
-                    const int at_chunk = OUT ? c + 1 : chunks - 2 - c;
-                    const int len = (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)at_chunk * C);
-                    fine = fine && wait.warp(kGate + b, ph) && wait.warp(kFullK + sb, (si >> 1) & 1) &&
-                           (len == C || wait.warp(kFullV + b, ph));
-                    if (fine) {
-                        // channels of this warp's quarter, tokens of its half, 16 x 64 a turn: all
-                        // of a turn's reads first (they take 300 cycles beside the products')
-                        decay_next = OUT ? tot[b] : 1.f;
-                        if (32 * quarter < DKP) {
+                    const bool half_done = OUT && c >= 0;   // (K~^T of chunk c: its first half)
+                    ok = wait.warp(kGate + b, ph, kFullK + sb, (si >> 1) & 1,
+                                   half_done ? kKvDone : kGate + b, half_done ? (gi - 1) & 1 : ph,
+                                   len < C ? kFullV + b : kGate + b, ph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    decay_next = OUT ? tot[b] : 1.f;
+                }
 #pragma unroll 1
-                            for (int cg = 0; cg < 32; cg += 16) {
-                                uint32_t x[4][4];
+                for (int u = 0; u < 2; ++u) {
+                    if (next) {
+                        // channels of this warp's quarter, tokens of its half, 32 x 32 a turn: all of a
+                        // turn's reads first (they take 300 cycles beside the products')
+                        if (32 * quarter < DKP) {
+                            const int first = 64 * half + 32 * u;
+                            uint32_t x[2][2][4];
+                            uint2 w[2][2];
 #pragma unroll
-                                for (int m = 0; m < 4; ++m)
+                            for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                                for (int cg = 0; cg < 2; ++cg)
                                     ldmatrix_t(base + sb * M::kQK + M::kK +
-                                                   sw128_offset(64 * half + 16 * m + (lane >> 4) * 8 + (lane & 7),
-                                                                32 * quarter + cg + ((lane >> 3) & 1) * 8, C),
-                                               x[m]);
-                                const uint32_t to_col = lanes + ((uint32_t)cg << 16) + 32 * half + (OUT ? 0 : b * kOther);
+                                                   sw128_offset(first + 16 * m + (lane >> 4) * 8 + (lane & 7),
+                                                                32 * quarter + 16 * cg + ((lane >> 3) & 1) * 8, C),
+                                               x[m][cg]);
+                                w[m][0] = gates[b].w[first / 2 + 8 * m + (lane & 3)];
+                                w[m][1] = gates[b].w[first / 2 + 8 * m + (lane & 3) + 4];
+                            }
+                            const uint32_t to_col = lanes + first / 2 + (OUT ? 0 : b * kOther);
 #pragma unroll
-                                for (int m = 0; m < 4; ++m) {
-                                    const int at = 64 * half + 16 * m + 2 * (lane & 3);   // and + 1, + 8, + 9
-                                    if (len < C) {   // tokens past the sequence count as zeros
-                                        const uint32_t m0 = (at < len ? 0xffffu : 0u) | (at + 1 < len ? 0xffff0000u : 0u);
-                                        const uint32_t m1 = (at + 8 < len ? 0xffffu : 0u) | (at + 9 < len ? 0xffff0000u : 0u);
-                                        x[m][0] &= m0; x[m][1] &= m0; x[m][2] &= m1; x[m][3] &= m1;
-                                    }
-                                    const uint2 w0 = gates[b].w[at / 2], w1 = gates[b].w[at / 2 + 4];
+                            for (int m = 0; m < 2; ++m) {
+                                const int at = first + 16 * m + 2 * (lane & 3);   // and + 1, + 8, + 9
+                                uint32_t m0 = ~0u, m1 = ~0u;
+                                if (len < C) {   // tokens past the sequence count as zeros
+                                    m0 = (at < len ? 0xffffu : 0u) | (at + 1 < len ? 0xffff0000u : 0u);
+                                    m1 = (at + 8 < len ? 0xffffu : 0u) | (at + 9 < len ? 0xffff0000u : 0u);
+                                }
+#pragma unroll
+                                for (int cg = 0; cg < 2; ++cg) {
                                     uint32_t hi[4], lo[4];
-                                    split2(x[m][0], w0, hi[0], lo[0]);
-                                    split2(x[m][1], w0, hi[1], lo[1]);
-                                    split2(x[m][2], w1, hi[2], lo[2]);
-                                    split2(x[m][3], w1, hi[3], lo[3]);
-                                    tmem_st_16x8(tHi + to_col + 8 * m, hi);
-                                    tmem_st_16x8(tLo + to_col + 8 * m, lo);
+                                    split2(x[m][cg][0] & m0, w[m][0], hi[0], lo[0]);
+                                    split2(x[m][cg][1] & m0, w[m][0], hi[1], lo[1]);
+                                    split2(x[m][cg][2] & m1, w[m][1], hi[2], lo[2]);
+                                    split2(x[m][cg][3] & m1, w[m][1], hi[3], lo[3]);
+                                    tmem_st_16x8(tHi + to_col + ((uint32_t)cg << 20) + 8 * m, hi);
+                                    tmem_st_16x8(tLo + to_col + ((uint32_t)cg << 20) + 8 * m, lo);
                                 }
                             }
-                            tmem_st_wait();
                         }
-                        if (len < C) {   // their rows of V must not meet the zeros of P and K~
+                        if (u == 0 && len < C) {   // their rows of V must not meet the zeros of P and K~
                             constexpr int U = DVP / 8;   // 16-byte pieces of a row
 #pragma unroll 1
                             for (int x = len * U + (tid - 32 * kRowWarps); x < C * U; x += 32 * kStateWarps)
@@ -560,30 +578,32 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                                     make_uint4(0, 0, 0, 0);
                             fence_proxy_async();
                         }
+                    }
+                    if (OUT ? u == 0 && c >= 0 : false) {
+                        ok = wait.warp(kKvDone + 1, (gi - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        add_product(0, decay);
+                    }
+                    if (next) {
+                        if (32 * quarter < DKP) tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(&bar[kKtReady + b]);
-                            mbar_arrive(&bar[kGateFree + b]);
+                            if (OUT || u) mbar_arrive(&bar[kKtReady + (OUT ? u : b)]);
+                            if (u) mbar_arrive(&bar[kGateFree + b]);
                         }
                         __syncwarp();
                     }
-                }
-                if (!OUT && c >= 0) {
-                    end_chunk();
-                    if (!ok) break;
-                }
-                if (OUT && c < 0) {
-                    if (end_of) fine = put_end() && fine;
-                    if (start.steps <= 1) read_start();
-                    if (!ok) break;
-                    // the old image's place has held a final state
-                    if (end_of) fine = fine && wait.warp(kEndFree, (ends_before - 1) & 1);
-                    end_of = 0;
-                }
-                if (OUT && next) {   // Q S of the chunk before has read the old image
-                    fine = fine && (gi == 0 || wait.warp(kQsDone, (gi - 1) & 1));
-                    if (fine) {
+                    if (OUT && u == 0 && c < 0) {
+                        if (start.steps <= 1) read_start();
+                        if (ok && image_taken) ok = wait.warp(kEndFree, (ends_before - 1) & 1);
+                        if (!ok) break;
+                        image_taken = false;
+                    }
+                    if (OUT && u == 0 && next) {   // Q S of the chunk before has read the old image
+                        ok = gi == 0 || wait.warp(kQsDone, (gi - 1) & 1);
+                        if (!ok) break;
                         if (i < DKP) {
 #pragma unroll
                             for (int j = 0; j < NC; j += 8) {
@@ -601,24 +621,32 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         __syncwarp();
                     }
                 }
+                if (!ok) break;
+                if (!OUT && c >= 0) {
+                    ok = wait.warp(kKvDone + (b ^ 1), ((gi - 1) >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    add_product((b ^ 1) * kOther, decay);
+                    tc_fence_before();
+                }
                 decay = decay_next;
                 if (next) {
                     ++gi;
                     ++si;
                 }
             }
-            if (ends) {
-                end_of = gi;   // put_end at the next item's start, or after the last
+            if (ends && ok) {
+                ok = put_end();
+                image_taken = true;
                 ++ends_before;
             }
             if (!OUT && ok && mine) {
-                float *row = bnd + cut_state(range + 1) * dkdv + (int64_t)i * dv + j0;
+                float *row = bnd + cut_state(p, range + 1, side) * dkdv + (int64_t)i * dv + j0;
 #pragma unroll
                 for (int j = 0; j < NC; j += 4)
                     *reinterpret_cast<float4 *>(row + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
             }
         });
-        if (OUT && end_of && ok) ok = put_end();   // (the store warp is waiting for it)
     } else if (warp == kMmaWarp) {
         each_item([&](const Item &it, const Start &start, bool ends) {
             const int chunks = it.c1 - it.c0;
@@ -636,9 +664,10 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 if (OUT) {
                     // A start of several states has been through both stages before this chunk:
                     // K~^T says that this is over, and that a parity names one phase again.
-                    if (c == 0 && start.steps > 1) ok = wait.warp(kKtReady + b, ph);
+                    if (c == 0 && start.steps > 1) ok = wait.warp(kKtReady, gi & 1);
                     // P of the chunk before lies over the scores
-                    ok = ok && wait.warp(kFullK + sb, (si >> 1) & 1) && wait.warp(kFullQ + sb, (si >> 1) & 1) &&
+                    const uint32_t landed = (si >> 1) & 1;
+                    ok = ok && wait.warp(kFullK + sb, landed, kFullQ + sb, landed) &&
                          (gi == 0 || wait.warp(kPvDone, (gi - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
@@ -650,25 +679,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         umma_commit(&bar[kQkDone]);
                     }
                     __syncwarp();
-                }
-                ok = wait.warp(kKtReady + b, ph) && wait.warp(kFullV + b, ph);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t other = OUT ? 0 : b * kOther;
-                if (elect_one()) {
-                    umma_commit(&bar[kFreeK + sb]);   // (Q K^T so far)
-#pragma unroll 2
-                    for (int s = 0; s < C / 16; ++s)
-                        umma_bf16_ts(tKV + other, tHi + other + 8 * s, desc_add(dvt, s * 2048), id_km, s > 0);
-#pragma unroll 2
-                    for (int s = 0; s < C / 16; ++s)
-                        umma_bf16_ts(tKV + other, tLo + other + 8 * s, desc_add(dvt, s * 2048), id_km, 1);
-                    umma_commit(&bar[kKvDone + b]);
-                    if (!OUT) umma_commit(&bar[kFreeV + b]);
-                }
-                __syncwarp();
-                if (OUT) {
-                    ok = wait.warp(kSReady, gi & 1) && (gi == 0 || wait.warp(kOFree, (gi - 1) & 1));
+                    ok = wait.warp(kSReady, gi & 1, gi ? kOFree : kSReady, gi ? (gi - 1) & 1 : gi & 1);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -677,8 +688,37 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                             umma_bf16(tO, desc_add(dq, (s >> 2) * 16384 + (s & 3) * 32),
                                       desc_add(ds, s * 2048), id_km, s > 0);
                         umma_commit(&bar[kQsDone]);
+                        if (!(ends && c + 1 == chunks)) umma_commit(&bar[kFreeQ + sb]);
                     }
                     __syncwarp();
+                }
+                const uint32_t other = OUT ? 0 : b * kOther;
+#pragma unroll 1
+                for (int u = 0; u < 2 && ok; ++u) {   // half of each 64 tokens
+                    if (OUT || u == 0) {
+                        ok = wait.warp(kKtReady + (OUT ? u : b), OUT ? gi & 1 : ph, kFullV + b, ph);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if (elect_one()) {
+                        if (u) umma_commit(&bar[kFreeK + sb]);   // (Q K^T so far)
+#pragma unroll 2
+                        for (int j = 0; j < 4; ++j) {
+                            const int s = 4 * (j >> 1) + 2 * u + (j & 1);
+                            umma_bf16_ts(tKV + other, tHi + other + 8 * s, desc_add(dvt, s * 2048), id_km, u + j > 0);
+                        }
+#pragma unroll 2
+                        for (int j = 0; j < 4; ++j) {
+                            const int s = 4 * (j >> 1) + 2 * u + (j & 1);
+                            umma_bf16_ts(tKV + other, tLo + other + 8 * s, desc_add(dvt, s * 2048), id_km, 1);
+                        }
+                        if (OUT || u) umma_commit(&bar[kKvDone + (OUT ? u : b)]);
+                        if (!OUT && u) umma_commit(&bar[kFreeV + b]);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (OUT) {
                     ok = wait.warp(kPReady, gi & 1);
                     if (!ok) break;
                     tc_fence_after();
@@ -687,7 +727,6 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         for (int s = 0; s < C / 16; ++s)
                             umma_bf16_ts(tO, tA + 8 * s, desc_add(dvt, s * 2048), id_km, 1);
                         umma_commit(&bar[kPvDone]);
-                        if (!(ends && c + 1 == chunks)) umma_commit(&bar[kFreeV + b]);
                     }
                     __syncwarp();
                 }
@@ -703,9 +742,23 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             const uint32_t first_si = si;   // the start states' stages
             si += start.steps;
             const int hk = h / (p.H / p.Hk);
+            // a stage that holds a start state is free when that has been read
+            auto behind_start = [&](uint32_t sb) {
+                if (!(start_in >> sb & 1)) return true;
+                const bool read = wait.warp(kStartRead + sb, (starts_read >> sb) & 1);
+                starts_read ^= 1u << sb;
+                start_in ^= 1u << sb;
+                if (lane == 0) {
+                    mbar_arrive(&bar[kFreeK + sb]);
+                    mbar_arrive(&bar[kFreeQ + sb]);
+                }
+                __syncwarp();
+                return read;
+            };
             for (int s = 0; s < start.steps; ++s) {
                 const uint32_t fs = first_si + s, sb = fs & 1, before = ((fs - 2) >> 1) & 1;
-                if (fs >= 2) ok = wait.warp(kFreeK + sb, before) && wait.warp(kFreeQ + sb, before);
+                ok = behind_start(sb);
+                if (ok && fs >= 2) ok = wait.warp(kFreeK + sb, before, kFreeQ + sb, before);
                 if (!ok) return;
                 if (lane == 0) {
                     uint64_t *full = &bar[kFullK + sb];
@@ -717,13 +770,15 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                                     0, start.index(s), full);
                 }
                 ++issued_k;
+                start_in |= 1u << sb;
                 __syncwarp();
             }
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
                 const uint32_t b = gi & 1, sb = si & 1, before = ((si - 2) >> 1) & 1;
                 const int32_t t0 = (int32_t)(it.t0 + (int64_t)(OUT ? c : chunks - 1 - c) * C);
                 uint8_t *qk = sm + sb * M::kQK;
-                if (si >= 2) ok = wait.warp(kFreeK + sb, before);
+                ok = behind_start(sb);
+                if (ok && si >= 2) ok = wait.warp(kFreeK + sb, before);
                 if (!ok) break;
                 if (lane == 0) {
                     uint64_t *full = &bar[kFullK + sb];
@@ -733,17 +788,6 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         tma_load_3d(qk + M::kK + x * 16384, &tk, 64 * x, hk, t0, full);
                 }
                 ++issued_k;
-                __syncwarp();
-                if (gi >= 2) ok = wait.warp(kFreeV + b, ((gi - 2) >> 1) & 1);
-                if (!ok) break;
-                if (lane == 0) {
-                    uint64_t *full = &bar[kFullV + b];
-                    mbar_arrive_expect_tx(full, M::kVBytes);
-#pragma unroll
-                    for (int x = 0; x < DVP / 64; ++x)
-                        tma_load_3d(sm + M::kV + b * M::kVBytes + x * 16384, &tv, 64 * x, h, t0, full);
-                }
-                ++issued_v;
                 __syncwarp();
                 if (OUT) {
                     if (si >= 2) ok = wait.warp(kFreeQ + sb, before);
@@ -758,6 +802,17 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     issued_q = si + 1;
                     __syncwarp();
                 }
+                if (gi >= 2) ok = wait.warp(kFreeV + b, ((gi - 2) >> 1) & 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    uint64_t *full = &bar[kFullV + b];
+                    mbar_arrive_expect_tx(full, M::kVBytes);
+#pragma unroll
+                    for (int x = 0; x < DVP / 64; ++x)
+                        tma_load_3d(sm + M::kV + b * M::kVBytes + x * 16384, &tv, 64 * x, h, t0, full);
+                }
+                ++issued_v;
+                __syncwarp();
             }
         });
     } else if (warp == kGateWarp) {
@@ -824,7 +879,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kGate + b]);
             }
-            if (!OUT && ok && lane == 0) bnd_log[cut_state(range + 1)] = log_sum;
+            if (!OUT && ok && lane == 0) bnd_log[cut_state(p, range + 1, side)] = log_sum;
         });
     } else if (OUT && warp == kStoreWarp) {
         each_item([&](const Item &it, const Start &start, bool ends) {
@@ -834,7 +889,32 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const uint32_t b = gi & 1, sb = si & 1;
                 const int64_t t0 = it.t0 + (int64_t)c * C;
                 const int len = (int)min((int64_t)C, it.t1 - t0);
-                const uint32_t so = M::kOverQ ? sb * M::kQK + M::kQ : M::kO;
+                const uint32_t so = M::kV + b * M::kVBytes;
+                if (ends && c + 1 == chunks) {
+                    // the final state, which is there before the outputs are, and first the half
+                    // whose place the next item's queries wait for
+                    ok = wait.warp(kEndReady, ends_before & 1);
+                    if (!ok) break;
+                    ++ends_before;
+                    if (lane == 0) {
+                        constexpr int kHalf = DVP / 64;   // blocks of a half
+#pragma unroll 1
+                        for (int x = kHalf; x < 2 * kHalf; ++x)
+                            if (32 * x < dv)
+                                tma_store_3d(&thT, base + sb * M::kQK + M::kQ + (x - kHalf) * dk * 128, 32 * x, 0,
+                                             it.n * p.H + h);
+                        bulk_commit();
+#pragma unroll 1
+                        for (int x = 0; x < kHalf; ++x)
+                            tma_store_3d(&thT, base + M::kS + x * dk * 128, 32 * x, 0, it.n * p.H + h);
+                        bulk_commit();
+                        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        mbar_arrive(&bar[kFreeQ + sb]);
+                        bulk_wait_read_all();
+                        mbar_arrive(&bar[kEndFree]);
+                    }
+                    __syncwarp();
+                }
                 ok = wait.warp(kOFree, gi & 1);
                 if (!ok) break;
                 if (len == C) {
@@ -862,54 +942,28 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                             *reinterpret_cast<const uint4 *>(sm + so + sw128_offset(r, j, C));
                     }
                     if (lane == 0) bulk_wait_read_all();
-                    fence_proxy_async();   // before q of a later chunk takes the place
+                    fence_proxy_async();   // before v of a later chunk takes the place
                 }
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bar[kFreeQ + sb]);
-                    mbar_arrive(&bar[kOStored]);
-                }
-                if (ends && c + 1 == chunks) {
-                    ok = wait.warp(kEndReady, ends_before & 1);
-                    if (!ok) break;
-                    ++ends_before;
-                    if (lane == 0) {
-                        constexpr int kHalf = DVP / 64;   // blocks of a half
-#pragma unroll 1
-                        for (int x = 0; x < 2 * kHalf; ++x) {
-                            if (32 * x < dv)
-                                tma_store_3d(&thT,
-                                             base + (x < kHalf ? M::kS + x * dk * 128
-                                                               : M::kV + b * M::kVBytes + (x - kHalf) * dk * 128),
-                                             32 * x, 0, it.n * p.H + h);
-                            if (x == kHalf - 1) {   // the image's place first
-                                bulk_commit();
-                                bulk_wait_read_all();
-                                mbar_arrive(&bar[kEndFree]);
-                            }
-                        }
-                        bulk_commit();
-                        bulk_wait_read_all();
-                        mbar_arrive(&bar[kFreeV + b]);
-                    }
-                    __syncwarp();
-                }
+                if (lane == 0) mbar_arrive(&bar[kFreeV + b]);
             }
         });
     }
     if (!ok) {
         *abort_flag = 1;
-        if (lane == 0) report(st, KDA_ERR_TIMEOUT, range, 41 + warp);
+        if (lane == 0) report(st, KDA_ERR_TIMEOUT, blockIdx.x, 41 + warp);
     }
     __syncthreads();
     if (*abort_flag) {
         // an expired wait: what is in flight ends (each wait bounded again) before the tensor
         // memory is released and the CTA leaves
         if (warp == kMmaWarp) {
-            tc_fence_after();
-            if (elect_one()) umma_commit(&bar[kDrain]);
+            tc_fence_after();   // (on a barrier whose role has stopped, at whichever phase it is)
+            const uint32_t phase = mbar_try_wait(&bar[kEndFree], 0) ? 1 : 0;
             __syncwarp();
-            mbar_wait(&bar[kDrain], 0, kWaitNs);
+            if (elect_one()) umma_commit(&bar[kEndFree]);
+            __syncwarp();
+            mbar_wait(&bar[kEndFree], phase, kWaitNs);
         }
         if (warp == kLoadWarp) {   // (only each stage's last load can be in flight)
             for (uint32_t x = issued_q >= 2 ? issued_q - 2 : 0; x < issued_q; ++x)
@@ -994,7 +1048,7 @@ static cudaError_t launch(const Plan &p, const CUtensorMap (&m)[8], const float 
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = allow_smem<DKP, DVP, OUT>(dev);
     if (e != cudaSuccess) return e;
-    return launch_after(la_chunk_tc_kernel<DKP, DVP, OUT>, dim3(OUT ? p.ranges : p.ranges - 1),
+    return launch_after(la_chunk_tc_kernel<DKP, DVP, OUT>, dim3((OUT ? p.ranges : p.ranges - 1) * p.lanes),
                         dim3(kThreads), Map<DKP, DVP>::kBytes, s, p, m[0], m[1], m[2], m[3], m[4], m[5],
                         m[6], m[7], g, gpt, has_h0, has_hT, (__nv_bfloat16 *)o, dk, dv, bnd, bnd_log, st);
 }
@@ -1017,7 +1071,7 @@ cudaError_t la_tensor_maps(CUtensorMap (&m)[8], const void *q, const void *k, co
     if (e == cudaSuccess) e = la::tc::tensor_map(&m[4], o, T, p.H, dv, (int64_t)p.H * dv, 8);
     if (e == cudaSuccess && h0) e = la::tc::state_map(&m[5], h0, nh, dk, dv);
     if (e == cudaSuccess && hT) e = la::tc::state_map(&m[6], hT, nh, dk, dv);
-    if (e == cudaSuccess && bnd) e = la::tc::state_map(&m[7], bnd, 2 * (int64_t)p.ranges, dk, dv);
+    if (e == cudaSuccess && bnd) e = la::tc::state_map(&m[7], bnd, 2 * (int64_t)p.ranges * p.lanes, dk, dv);
     return e;
 }
 
