@@ -14,8 +14,8 @@ namespace la {
 
 // ------------------------------------------------------------------------- plan
 // CTA 0: validates cu_seqlens (see plan_chunks_kernel), counts chunks and places the cuts.
-// Every CTA: final states of sequences without tokens (S_out not NULL).
-constexpr int kPlanThreads = 256, kMaxRanges = 1024;
+// The others: final states of sequences without tokens (S_out not NULL).
+constexpr int kPlanThreads = 256, kMaxRanges = 1024, kPlanSeqs = 1024;
 
 // The largest n with off[n] * H <= x, for x < off[N] * H: entry n spans x.
 __device__ __forceinline__ int owner(const int32_t *off, int N, int H, int64_t x) {
@@ -52,8 +52,9 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
                int min_range, Cut *cuts, int ranges, int split,
                StatusWord *st, const float *h0, float *S_out, int all_heads, int H,
                int64_t dkdv4) {   // H: heads of a lane
-    if (S_out) {
-        for (int64_t nh = blockIdx.x; nh < (int64_t)N * all_heads; nh += gridDim.x) {
+    let_next_start();
+    if (blockIdx.x != 0) {
+        for (int64_t nh = blockIdx.x - 1; nh < (int64_t)N * all_heads; nh += gridDim.x - 1) {
             const int n = (int)(nh / all_heads);
             const int64_t b = cu[n], e = cu[n + 1];
             if (b < e && b >= 0 && e <= T_tot) continue;
@@ -62,10 +63,15 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
             for (int64_t i = threadIdx.x; i < dkdv4; i += blockDim.x)
                 dst[i] = src ? src[i] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        return;
     }
-    let_next_start();
-    if (blockIdx.x != 0) return;
     __shared__ Cut s_cut[kMaxRanges + 1];
+    // The prefix sums are searched again and again: in shared memory where they fit.
+    __shared__ int32_t s_sum[3][kPlanSeqs + 1];
+    const bool fits = N <= kPlanSeqs;
+    int32_t *const chunks = fits ? s_sum[0] : off;
+    int32_t *const parts = fits ? s_sum[1] : piece_off;
+    int32_t *const costs = fits ? s_sum[2] : cost_off;
     constexpr int NW = kPlanThreads / 32;
     __shared__ int3 s_warp[NW];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -106,16 +112,16 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
             add(carry, s_warp[w]);
         }
         if (n < N) {
-            off[n] = before.x + x.x - own.x;
-            piece_off[n] = before.y + x.y - own.y;
-            cost_off[n] = before.z + x.z - own.z;
+            off[n] = chunks[n] = before.x + x.x - own.x;
+            parts[n] = before.y + x.y - own.y;
+            costs[n] = before.z + x.z - own.z;
         }
         __syncthreads();
     }
     if (tid == 0) {
-        off[N] = carry.x;
-        piece_off[N] = carry.y;
-        cost_off[N] = carry.z;
+        off[N] = chunks[N] = carry.x;
+        parts[N] = carry.y;
+        costs[N] = carry.z;
     }
     __syncthreads();
     const int64_t total = (int64_t)carry.x * H, fine = (int64_t)carry.y * H;
@@ -128,26 +134,26 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
         if (spare) {
             int64_t x = total;
             if (i < fine) {
-                const int n = owner(piece_off, N, H, i);
-                const int nc = off[n + 1] - off[n], m = piece_off[n + 1] - piece_off[n];
-                const int rest = i - piece_off[n] * H;
-                x = (int64_t)off[n] * H + (int64_t)(rest / m) * nc + (int64_t)(rest % m) * nc / m;
+                const int n = owner(parts, N, H, i);
+                const int nc = chunks[n + 1] - chunks[n], m = parts[n + 1] - parts[n];
+                const int rest = i - parts[n] * H;
+                x = (int64_t)chunks[n] * H + (int64_t)(rest / m) * nc + (int64_t)(rest % m) * nc / m;
             }
-            r = place(off, N, H, total, x);
+            r = place(chunks, N, H, total, x);
         } else {
             const int64_t y = (int64_t)i * cost / ranges;
             int64_t x = total;
             if (y < cost) {
-                const int n = owner(cost_off, N, H, y);
-                const int64_t nc = off[n + 1] - off[n], m = nc + unit_cost;
-                const int64_t rest = y - (int64_t)cost_off[n] * H, c = rest % m - unit_cost;
-                x = (int64_t)off[n] * H + rest / m * nc + (c > 0 ? c : 0);
+                const int n = owner(costs, N, H, y);
+                const int64_t nc = chunks[n + 1] - chunks[n], m = nc + unit_cost;
+                const int64_t rest = y - (int64_t)costs[n] * H, c = rest % m - unit_cost;
+                x = (int64_t)chunks[n] * H + rest / m * nc + (c > 0 ? c : 0);
             }
-            r = place(off, N, H, total, x);
+            r = place(chunks, N, H, total, x);
             if (r.inner) {
-                const int nc = off[r.n + 1] - off[r.n];
+                const int nc = chunks[r.n + 1] - chunks[r.n];
                 if (!split || nc <= min_range)
-                    r = place(off, N, H, total, r.x + (2 * r.c >= nc ? nc - r.c : -r.c));
+                    r = place(chunks, N, H, total, r.x + (2 * r.c >= nc ? nc - r.c : -r.c));
             }
         }
         s_cut[i] = r;
@@ -456,7 +462,7 @@ cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off
                            int H, int lanes, int64_t dkdv, cudaStream_t s) {
     float *S_out = hT != h0 ? hT : nullptr;   // an in-place update leaves empty ones as they are
     const int64_t nh = (int64_t)N * H;
-    const int grid = S_out && nh > 1 ? (int)(nh < 256 ? nh : 256) : 1;
+    const int grid = S_out ? 1 + (int)(nh < 255 ? nh : 255) : 1;
     la::la_plan_kernel<<<grid, la::kPlanThreads, 0, s>>>(
         cu, N, T_tot, off, off + N + 1, off + 2 * (N + 1), unit_cost, chunk, min_range, cuts, ranges, split, st, h0, S_out, H, H / lanes, dkdv / 4);
     return cudaGetLastError();

@@ -242,9 +242,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     using M = Map<DKP, DVP>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int range = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
-    wait_for_previous();
     let_next_start();
-    if (OUT ? p.cuts[range].x >= p.cuts[range + 1].x : !p.cuts[range + 1].inner) return;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + M::kBar);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + M::kBar + kBars * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + M::kBar + kBars * 8 + 4);
@@ -252,6 +250,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     float *tot = reinterpret_cast<float *>(sm + M::kTot);
     const uint32_t base = smem_u32(sm);
     if (base & 1023u) {   // the operand images need their alignment
+        wait_for_previous();
         if (tid == 0) report(st, KDA_ERR_CUDA, 0, 40);
         return;
     }
@@ -289,6 +288,9 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
+    // (so far nothing that another kernel has written)
+    wait_for_previous();
+    const bool work = OUT ? p.cuts[range].x < p.cuts[range + 1].x : p.cuts[range + 1].inner != 0;
     // K~^T (hi, lo) and K~^T V; then, of a second chunk's, or scores (then P) and O
     const uint32_t tHi = tmem, tLo = tmem + 64, tKV = tmem + 128;
     constexpr uint32_t kOther = 256;
@@ -306,6 +308,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     // final state to store).
     auto each_item = [&](auto role) {
         Item it;
+        if (!work) return;
         Walk walk(p, range, side);
         bool more = OUT ? walk.next(it) : before_cut(p, range + 1, side, it);
         for (; more && ok; more = OUT && walk.next(it))
