@@ -34,6 +34,7 @@ struct Cut {
     int32_t n, h, c;
     int32_t inner;            // inside a unit: 1 + the inner cuts of this unit that follow; else 0
     int32_t before;           // the inner cuts of this unit before it
+    int32_t handed;           // the range before hands the state on (see Items)
 };
 
 struct Plan {
@@ -46,11 +47,14 @@ struct Plan {
     int chunk;                // tokens
     int in_place;             // the final states overwrite the initial ones
     int compose;              // no scan: ranges put their start states together themselves
+    uint32_t *flags;          // states handed on, as the states of the cuts; then the CTAs begun (or null)
 };
 
 // The chunks [c0, c1) of one unit.
 struct Item {
+    enum Part { kWhole, kHead, kTail };
     int n, h;
+    int part;                 // kHead, kTail: of a unit whose one cut is handed on
     int c0, c1, nc;           // of nc
     int64_t t0, t1;           // tokens [t0, t1) of the packed tensors
 };
@@ -79,6 +83,7 @@ struct Walk {
             begin = p.cu[n];
             stop = p.cu[n + 1];
         }
+        it.part = Item::kWhole;
         it.n = n;
         it.h = h * p.lanes + lane;
         it.c0 = c;
@@ -124,6 +129,7 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, siz
 __device__ __forceinline__ bool before_cut(const Plan &p, int i, int lane, Item &it) {
     const Cut e = p.cuts[i];
     if (!e.inner) return false;
+    it.part = Item::kHead;
     it.n = e.n;
     it.h = e.h * p.lanes + lane;
     it.c1 = e.c;
@@ -159,7 +165,10 @@ struct Start {
 };
 __device__ __forceinline__ Start start_state(const Plan &p, const Item &it, int range, int lane, bool h0) {
     Start r{0, -1, false, 0, p.lanes};
-    if (it.c0 > 0) {
+    if (it.part == Item::kTail) {
+        r.steps = 1;
+        r.first = (int32_t)cut_state(p, range, lane);
+    } else if (it.c0 > 0) {
         const int before = p.compose ? p.cuts[range].before : 0;
         r.first = (int32_t)cut_state(p, range - before, lane);
         r.steps = before + 1;
@@ -169,11 +178,43 @@ __device__ __forceinline__ Start start_state(const Plan &p, const Item &it, int 
         }
     } else if (h0) {
         r.steps = 1;
-        r.h0_copied = it.c1 < it.nc && p.in_place;
+        r.h0_copied = it.c1 < it.nc && it.part != Item::kHead && p.in_place;
         r.h0 = r.h0_copied ? (int32_t)initial_copy(p, range, lane) : it.n * p.H + it.h;
     }
     return r;
 }
+
+// The items of a range, in the order in which they are walked.  A unit with one cut needs no
+// first pass where the range behind the cut has as much else to do as lies before it: the
+// range before takes its part (the head) first of all and hands the state on, the range
+// behind takes the rest (the tail) last.  A head waits for nothing, and ranges are dealt out in
+// the order in which CTAs begin, so that the one before has begun: the wait ends however few
+// CTAs run at a time.  (16 packed sequences of 18 chunks in the mean, 66 chunks a range: the first pass
+// took 34 of 224 us.)
+struct Items {
+    Walk walk;
+    Item tail;
+    bool head, has_tail;
+    __device__ __forceinline__ Items(const Plan &p, int range, int lane) : walk(p, range, lane) {
+        const Cut &e = p.cuts[range + 1];
+        head = e.handed;
+        has_tail = p.cuts[range].handed;
+        if (has_tail) walk.next(tail);
+        tail.part = Item::kTail;
+        if (head) walk.end -= e.c;
+    }
+    __device__ __forceinline__ bool next(const Plan &p, int range, int lane, Item &it) {
+        if (head) {
+            head = false;
+            return before_cut(p, range + 1, lane, it);
+        }
+        if (walk.next(it)) return true;
+        if (!has_tail) return false;
+        has_tail = false;
+        it = tail;
+        return true;
+    }
+};
 
 // A log decay below this is e^g = 0 in fp32.  Prefix sums, whose differences give the decay
 // between two tokens of a chunk, take g no lower than this, so that a reset (-inf) leaves

@@ -9,7 +9,7 @@
 
 namespace kda {
 cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off, int unit_cost,
-                           int chunk, int min_range, la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
+                           int chunk, int min_range, la::Cut *cuts, int ranges, int split, uint32_t *flags, int n_flags, StatusWord *st, const float *h0, float *hT,
                            int H, int lanes, int64_t dkdv, cudaStream_t s);
 cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
                            int64_t dkdv, cudaStream_t s);
@@ -71,7 +71,8 @@ bool stride_ok(int64_t stride, int64_t T, int32_t heads, int32_t D, int32_t dtyp
 struct LaLayout {
     int lanes, ranges, chunk, min_range;
     bool split;
-    size_t cuts_off, off_off, log_off, bnd_off, total;
+    int flags;                // states that may be handed on, and a count of CTAs (tensor cores)
+    size_t cuts_off, off_off, log_off, flag_off, bnd_off, total;
 };
 
 // One range of one lane an SM, and no more than there can be chunks.  Sequences are cut only where
@@ -93,7 +94,10 @@ LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t Hk, int32_t dk, int3
     L.cuts_off = kHeaderBytes;
     L.off_off = L.cuts_off + round_up(sizeof(la::Cut) * ((size_t)L.ranges + 1), 256);
     L.log_off = L.off_off + round_up(3 * sizeof(int32_t) * ((size_t)N + 1), 256);
-    L.bnd_off = L.log_off + round_up(sizeof(float) * all, 256);
+    // With fewer units than ranges nearly all cuts are in units of several: nothing to hand on.
+    L.flags = dtype == KDA_BF16 && L.split && (int64_t)N * (H / L.lanes) >= L.ranges ? (int)all + 1 : 0;
+    L.flag_off = L.log_off + round_up(sizeof(float) * all, 256);
+    L.bnd_off = L.flag_off + round_up(sizeof(uint32_t) * L.flags, 256);
     L.total = L.bnd_off + (L.split ? sizeof(float) * 2 * all * dk * dv : 0);
     return L;
 }
@@ -155,12 +159,12 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     const bool in_place = initial_state && initial_state == final_state;
     const bool compose = dtype == KDA_BF16 && !in_place && L.ranges * L.lanes / H + 1 <= 12;
     const la::Plan p{cu_seqlens, off, cuts, num_seqs, H, Hk, L.lanes, L.ranges, L.chunk,
-                     in_place, compose};
+                     in_place, compose, L.flags ? (uint32_t *)(ws + L.flag_off) : nullptr};
     // A unit's states cost about as much as a chunk each (64 KB in, 64 KB out; measured on 16
     // packed sequences: 11.6k cycles beside 5.4k of a chunk).
     const int unit_cost = (initial_state ? 1 : 0) + (final_state ? 1 : 0);
     cudaError_t e = launch_la_plan(cu_seqlens, num_seqs, total_tokens, off, unit_cost, L.chunk,
-                                   L.min_range, cuts, L.ranges, L.split, st, initial_state, final_state, H, L.lanes, dkdv, s);
+                                   L.min_range, cuts, L.ranges, L.split, p.flags, L.flags, st, initial_state, final_state, H, L.lanes, dkdv, s);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (total_tokens == 0) return KDA_OK;
     CUtensorMap maps[8];

@@ -28,7 +28,7 @@ __device__ __forceinline__ int owner(const int32_t *off, int N, int H, int64_t x
 }
 
 __device__ Cut place(const int32_t *off, int N, int H, int64_t total, int64_t x) {
-    Cut r{x, N, 0, 0, 0, 0};
+    Cut r{x, N, 0, 0, 0, 0, 0};
     if (x >= total) {
         r.x = total;
         return r;
@@ -49,7 +49,7 @@ __device__ __forceinline__ int pieces(int nc, int split, int min_range) {
 __global__ void __launch_bounds__(kPlanThreads)
 la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *off,
                int32_t *piece_off, int32_t *cost_off, int unit_cost, int chunk,
-               int min_range, Cut *cuts, int ranges, int split,
+               int min_range, Cut *cuts, int ranges, int split, uint32_t *flags, int n_flags,
                StatusWord *st, const float *h0, float *S_out, int all_heads, int H,
                int64_t dkdv4) {   // H: heads of a lane
     let_next_start();
@@ -81,6 +81,7 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
         st->info = 0ull;
     }
     __syncthreads();
+    for (int i = tid; i < n_flags; i += kPlanThreads) flags[i] = 0;
     if (tid == 0 && (cu[0] != 0 || (int64_t)cu[N] != T_tot)) report(st, KDA_ERR_SEQLENS, N, 1);
     int3 carry = make_int3(0, 0, 0);   // chunks, pieces, costs
     auto add = [](int3 &x, const int3 &y) { x.x += y.x; x.y += y.y; x.z += y.z; };
@@ -166,6 +167,9 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
                 ++r.before;
             for (int j = i + 1; j < ranges && s_cut[j].inner && s_cut[j].n == r.n && s_cut[j].h == r.h; ++j)
                 ++r.inner;
+            const int64_t nc = chunks[r.n + 1] - chunks[r.n];
+            r.handed = n_flags > 0 && r.inner == 1 && r.before == 0 &&
+                       r.c <= s_cut[i + 1].x - r.x - (nc - r.c);
         }
         cuts[i] = r;
     }
@@ -183,7 +187,7 @@ la_scan_kernel(Plan p, const float *__restrict__ h0, float *__restrict__ bnd,
     let_next_start();
     const int first = blockIdx.y / p.lanes + 1, lane = blockIdx.y % p.lanes;
     const Cut f = p.cuts[first];
-    if (!f.inner || f.before) return;   // a unit's chain starts at its first cut
+    if (!f.inner || f.before || f.handed) return;   // a unit's chain starts at its first cut
     const int64_t i = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
     if (i >= dkdv4) return;
     const int last = first + f.inner - 1;
@@ -458,13 +462,14 @@ static cudaError_t launch_dims(bool out, const Plan &p, const float *q, const fl
 }  // namespace la
 
 cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off, int unit_cost,
-                           int chunk, int min_range, la::Cut *cuts, int ranges, int split, StatusWord *st, const float *h0, float *hT,
+                           int chunk, int min_range, la::Cut *cuts, int ranges, int split, uint32_t *flags, int n_flags, StatusWord *st, const float *h0, float *hT,
                            int H, int lanes, int64_t dkdv, cudaStream_t s) {
     float *S_out = hT != h0 ? hT : nullptr;   // an in-place update leaves empty ones as they are
     const int64_t nh = (int64_t)N * H;
     const int grid = S_out ? 1 + (int)(nh < 255 ? nh : 255) : 1;
     la::la_plan_kernel<<<grid, la::kPlanThreads, 0, s>>>(
-        cu, N, T_tot, off, off + N + 1, off + 2 * (N + 1), unit_cost, chunk, min_range, cuts, ranges, split, st, h0, S_out, H, H / lanes, dkdv / 4);
+        cu, N, T_tot, off, off + N + 1, off + 2 * (N + 1), unit_cost, chunk, min_range, cuts, ranges, split,
+        flags, n_flags, st, h0, S_out, H, H / lanes, dkdv / 4);
     return cudaGetLastError();
 }
 

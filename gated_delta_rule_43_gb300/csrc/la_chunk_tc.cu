@@ -78,11 +78,11 @@ enum Bar {
     kPvDone = 22,    // P V
     kPReady = 23,    // P and the decayed Q S are in tensor memory
     kSReady = 24,    // the image of S is in shared memory
-    kOFree = 25,     // the accumulator of O has been read: the outputs are in shared memory
-    kEndReady = 26,  // an item's final state is in shared memory
-    kEndFree = 27,   // ... and has left the place of the image of S
-    kStartRead = 28, // [2] a start state has been read out of its stage
-    kBars = 30
+    kOFree = 25,     // [2] the accumulator of O has been read: the outputs are in shared memory
+    kEndReady = 27,  // an item's final state is in shared memory
+    kEndFree = 28,   // ... and has left the place of the image of S
+    kStartRead = 29, // [2] a start state has been read out of its stage
+    kBars = 31
 };
 
 // Two stages of q, k and v, the image of S ([DKP rows][DVP]), the decays.  A start state (fp32, in
@@ -94,9 +94,9 @@ template <int DKP, int DVP> struct Map {
     static constexpr uint32_t kV = 2 * kQK, kVBytes = DVP * 256;
     static constexpr uint32_t kS = kV + 2 * kVBytes;
     static constexpr uint32_t kGates = kS + DKP * DVP * 2;
-    static constexpr uint32_t kTot = kGates + 2 * sizeof(Gates);   // decay of the chunk, [2]
+    static constexpr uint32_t kTot = kGates + 2 * sizeof(Gates);   // decay of the chunk, [2]; at first the TMEM slot
     static constexpr uint32_t kBar = kTot + 8;
-    static constexpr uint32_t kBytes = kBar + kBars * 8 + 8;
+    static constexpr uint32_t kBytes = kBar + kBars * 8;
     static_assert(kBar % 8 == 0 && kS % 1024 == 0 && kQK % 1024 == 0 && kV % 1024 == 0 &&
                       kBytes <= 232448 && DKP * DVP * 4 <= kQK && DKP * DVP * 2 <= kK,
                   "layout");
@@ -241,13 +241,11 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     extern __shared__ __align__(1024) uint8_t sm[];
     using M = Map<DKP, DVP>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int range = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
     let_next_start();
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + M::kBar);
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + M::kBar + kBars * 8);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + M::kBar + kBars * 8 + 4);
     Gates *gates = reinterpret_cast<Gates *>(sm + M::kGates);
     float *tot = reinterpret_cast<float *>(sm + M::kTot);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + M::kTot);
     const uint32_t base = smem_u32(sm);
     if (base & 1023u) {   // the operand images need their alignment
         wait_for_previous();
@@ -267,16 +265,15 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             mbar_init(&bar[kKtReady + b], kStateWarps);
             mbar_init(&bar[kKvDone + b], 1);
             mbar_init(&bar[kStartRead + b], kStateWarps);
+            mbar_init(&bar[kOFree + b], kRowWarps);
         }
         mbar_init(&bar[kQkDone], 1);
         mbar_init(&bar[kQsDone], 1);
         mbar_init(&bar[kPvDone], 1);
         mbar_init(&bar[kPReady], kRowWarps);
         mbar_init(&bar[kSReady], kStateWarps);
-        mbar_init(&bar[kOFree], kRowWarps);
         mbar_init(&bar[kEndReady], kStateWarps);
         mbar_init(&bar[kEndFree], 1);
-        *abort_flag = 0;
         fence_mbar_init();
     }
     constexpr uint32_t kCols = 512;
@@ -290,7 +287,18 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     const uint32_t tmem = *tslot;
     // (so far nothing that another kernel has written)
     wait_for_previous();
-    const bool work = OUT ? p.cuts[range].x < p.cuts[range + 1].x : p.cuts[range + 1].inner != 0;
+    int place = blockIdx.x;
+    if (OUT && p.flags) {   // in the order in which the CTAs begin: a range may wait for the one before
+        if (tid == 0) place = atomicAdd(&p.flags[p.ranges * p.lanes], 1);
+        __syncthreads();   // (all have read the slot)
+        if (tid == 0) *tslot = place;
+        __syncthreads();
+        place = *tslot;
+        __syncthreads();   // (its place is used from here on)
+    }
+    const int range = place / p.lanes, side = place % p.lanes;
+    const bool work = OUT ? p.cuts[range].x < p.cuts[range + 1].x
+                          : p.cuts[range + 1].inner != 0 && !p.cuts[range + 1].handed;
     // K~^T (hi, lo) and K~^T V; then, of a second chunk's, or scores (then P) and O
     const uint32_t tHi = tmem, tLo = tmem + 64, tKV = tmem + 128;
     constexpr uint32_t kOther = 256;
@@ -305,15 +313,18 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     uint32_t ends_before = 0;                            // (store and state warps) final states so far
 
     // Each role goes through the range's items for itself: role(item, its start, whether it has a
-    // final state to store).
+    // state to store at its end, which is a final state or one to hand on).
     auto each_item = [&](auto role) {
-        Item it;
         if (!work) return;
-        Walk walk(p, range, side);
-        bool more = OUT ? walk.next(it) : before_cut(p, range + 1, side, it);
-        for (; more && ok; more = OUT && walk.next(it))
-            role(it, OUT ? start_state(p, it, range, side, has_h0) : Start{},
-                 OUT && has_hT && it.c1 == it.nc);
+        Item it;
+        if (OUT) {
+            Items items(p, range, side);
+            while (ok && items.next(p, range, side, it))
+                role(it, start_state(p, it, range, side, has_h0),
+                     it.part == Item::kHead || (has_hT && it.c1 == it.nc));
+        } else if (before_cut(p, range + 1, side, it)) {
+            role(it, Start{}, false);
+        }
     };
     constexpr int NC = DVP / 2;
 
@@ -435,7 +446,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 tc_fence_before();
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kOFree]);
+                if (lane == 0) mbar_arrive(&bar[kOFree + b]);
             }
         });
     } else if (warp < kRowWarps + kStateWarps) {
@@ -682,7 +693,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         umma_commit(&bar[kQkDone]);
                     }
                     __syncwarp();
-                    ok = wait.warp(kSReady, gi & 1, gi ? kOFree : kSReady, gi ? (gi - 1) & 1 : gi & 1);
+                    ok = wait.warp(kSReady, gi & 1, gi ? kOFree + (b ^ 1) : kSReady, gi ? ((gi - 1) >> 1) & 1 : gi & 1);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -763,6 +774,19 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 ok = behind_start(sb);
                 if (ok && fs >= 2) ok = wait.warp(kFreeK + sb, before, kFreeQ + sb, before);
                 if (!ok) return;
+                if (it.part == Item::kTail) {   // handed on by the range before
+                    bool there = lane != 0;
+                    const uint64_t t0 = globaltimer_ns();
+                    for (uint32_t i = 1; !there; ++i) {
+                        uint32_t flag;
+                        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(flag) : "l"(p.flags + start.index(s)) : "memory");
+                        there = flag != 0;
+                        if ((i & 63u) == 0 && globaltimer_ns() - t0 > kWaitNs) break;
+                    }
+                    ok = __all_sync(0xffffffffu, there);
+                    if (!ok) return;
+                    asm volatile("fence.proxy.async.global;" ::: "memory");
+                }
                 if (lane == 0) {
                     uint64_t *full = &bar[kFullK + sb];
                     mbar_arrive(&bar[kFullQ + sb]);
@@ -901,15 +925,17 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     ++ends_before;
                     if (lane == 0) {
                         constexpr int kHalf = DVP / 64;   // blocks of a half
+                        const void *map = it.part == Item::kHead ? &tbnd : &thT;
+                        const int index = it.part == Item::kHead ? (int)cut_state(p, range + 1, side) : it.n * p.H + h;
 #pragma unroll 1
                         for (int x = kHalf; x < 2 * kHalf; ++x)
                             if (32 * x < dv)
-                                tma_store_3d(&thT, base + sb * M::kQK + M::kQ + (x - kHalf) * dk * 128, 32 * x, 0,
-                                             it.n * p.H + h);
+                                tma_store_3d(map, base + sb * M::kQK + M::kQ + (x - kHalf) * dk * 128, 32 * x, 0,
+                                             index);
                         bulk_commit();
 #pragma unroll 1
                         for (int x = 0; x < kHalf; ++x)
-                            tma_store_3d(&thT, base + M::kS + x * dk * 128, 32 * x, 0, it.n * p.H + h);
+                            tma_store_3d(map, base + M::kS + x * dk * 128, 32 * x, 0, index);
                         bulk_commit();
                         asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                         mbar_arrive(&bar[kFreeQ + sb]);
@@ -918,7 +944,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     }
                     __syncwarp();
                 }
-                ok = wait.warp(kOFree, gi & 1);
+                ok = wait.warp(kOFree + b, (gi >> 1) & 1);
                 if (!ok) break;
                 if (len == C) {
                     if (lane == 0) {
@@ -949,15 +975,23 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kFreeV + b]);
+                if (it.part == Item::kHead && c + 1 == chunks && lane == 0) {
+                    // the state is written, not only read: hand it on
+                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                    asm volatile("fence.proxy.async.global;" ::: "memory");
+                    __threadfence();
+                    asm volatile("st.release.gpu.global.u32 [%0], %1;"
+                                 ::"l"(p.flags + cut_state(p, range + 1, side)), "r"(1u)
+                                 : "memory");
+                }
+                __syncwarp();
             }
         });
     }
     if (!ok) {
-        *abort_flag = 1;
         if (lane == 0) report(st, KDA_ERR_TIMEOUT, blockIdx.x, 41 + warp);
     }
-    __syncthreads();
-    if (*abort_flag) {
+    if (__syncthreads_or(!ok)) {
         // an expired wait: what is in flight ends (each wait bounded again) before the tensor
         // memory is released and the CTA leaves
         if (warp == kMmaWarp) {

@@ -75,6 +75,23 @@ def test_many_heads_of_many_segments_in_place(dtype):
     assert U.rel(o, ro) <= U.TOL_O[dtype] and U.rel(h0, rS) <= U.TOL_S
 
 
+MANY = [1300, 1500, 1250, 0, 1700, 900, 1600, 1, 1100, 2000, 1290, 1410, 300, 1820]
+
+
+@pytest.mark.parametrize("H,Hk,dk,dv", [(16, 16, 32, 32), (16, 4, 32, 64), (24, 8, 64, 32), (16, 16, 128, 128)])
+@pytest.mark.parametrize("start", ["none", "h0", "in place"])
+def test_sequences_cut_once(H, Hk, dk, dv, start):
+    """Many sequences, each cut between two ranges at most."""
+    lens = MANY if dk < 128 else MANY[:11]
+    args = U.make(lens, H, Hk, dk, dv, BF, seed=H + dk, h0=start != "none", speed=0.01)
+    q, k, v, g, cu, h0 = gpu(*args)
+    for _ in range(3):
+        s = None if h0 is None else h0.clone()
+        o, S = kda.la_chunk_fwd(q, k, v, g, cu, s, final_state=s if start == "in place" else None, check=True)
+    ro, rS = U.la_ref(*args)
+    assert U.rel(o, ro) <= U.TOL_O[BF] and U.rel(S, rS) <= U.TOL_S
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_no_decay_and_fast_decay(dtype):
     args = list(U.make([300, 260], 3, 3, 64, 128, dtype, seed=5))
