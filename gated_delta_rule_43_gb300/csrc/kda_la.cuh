@@ -27,10 +27,14 @@ namespace la {
 
 constexpr int kTcChunk = 128, kTcMinRange = 8;
 constexpr int kSimtChunk = 32, kSimtMinRange = 4;
+constexpr int kMaxRanges = 512;   // (the plan's shared memory)
 
-// A place in the row of chunks: before chunk c of head h of sequence n.
+// A place in the row of chunks: before chunk c of head h of sequence n.  (What a walk needs of the
+// sequence stands beside it: one read from memory less before anything can begin.)
 struct Cut {
     int64_t x;
+    int32_t nc;               // chunks of sequence n, 0 at the row's end
+    int32_t begin, stop;      // its tokens
     int32_t n, h, c;
     int32_t inner;            // inside a unit: 1 + the inner cuts of this unit that follow; else 0
     int32_t before;           // the inner cuts of this unit before it
@@ -71,11 +75,12 @@ struct Walk {
     int64_t x, end;
     int lane;
     int n, h, c;
-    int nc = 0;               // chunks of sequence n, 0: not read yet
+    int nc;                   // chunks of sequence n, 0: not read yet
     int64_t begin, stop;      // its tokens
     __device__ __forceinline__ Walk(const Plan &plan, int range, int lane_)
         : p(plan), x(plan.cuts[range].x), end(plan.cuts[range + 1].x), lane(lane_), n(plan.cuts[range].n),
-          h(plan.cuts[range].h), c(plan.cuts[range].c) {}
+          h(plan.cuts[range].h), c(plan.cuts[range].c), nc(plan.cuts[range].nc),
+          begin(plan.cuts[range].begin), stop(plan.cuts[range].stop) {}
     __device__ __forceinline__ bool next(Item &it) {
         if (x >= end) return false;
         if (nc == 0) {
@@ -134,8 +139,8 @@ __device__ __forceinline__ bool before_cut(const Plan &p, int i, int lane, Item 
     it.h = e.h * p.lanes + lane;
     it.c1 = e.c;
     it.c0 = (int)max((int64_t)0, e.c - (e.x - p.cuts[i - 1].x));
-    it.nc = p.off[e.n + 1] - p.off[e.n];
-    set_tokens(it, p.chunk, p.cu[it.n], p.cu[it.n + 1]);
+    it.nc = e.nc;
+    set_tokens(it, p.chunk, e.begin, e.stop);
     return true;
 }
 

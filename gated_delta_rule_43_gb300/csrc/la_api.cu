@@ -83,7 +83,7 @@ LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t Hk, int32_t dk, int3
     LaLayout L{};
     L.chunk = dtype == KDA_BF16 ? la::kTcChunk : la::kSimtChunk;
     L.min_range = dtype == KDA_BF16 ? la::kTcMinRange : la::kSimtMinRange;
-    if (sms > 1024) sms = 1024;   // (the plan's room)
+    if (sms > la::kMaxRanges) sms = la::kMaxRanges;
     L.lanes = dtype == KDA_BF16 ? H / Hk : 1;
     while ((H / Hk) % L.lanes != 0 || L.lanes > sms || sms % L.lanes * 24 > sms) --L.lanes;
     const int64_t most = (T / L.chunk + N) * (int64_t)(H / L.lanes);

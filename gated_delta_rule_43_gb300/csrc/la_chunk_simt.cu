@@ -15,7 +15,7 @@ namespace la {
 // ------------------------------------------------------------------------- plan
 // CTA 0: validates cu_seqlens (see plan_chunks_kernel), counts chunks and places the cuts.
 // The others: final states of sequences without tokens (S_out not NULL).
-constexpr int kPlanThreads = 256, kMaxRanges = 1024, kPlanSeqs = 1024;
+constexpr int kPlanThreads = 256, kPlanSeqs = 1024;
 
 // The largest n with off[n] * H <= x, for x < off[N] * H: entry n spans x.
 __device__ __forceinline__ int owner(const int32_t *off, int N, int H, int64_t x) {
@@ -28,13 +28,16 @@ __device__ __forceinline__ int owner(const int32_t *off, int N, int H, int64_t x
 }
 
 __device__ Cut place(const int32_t *off, int N, int H, int64_t total, int64_t x) {
-    Cut r{x, N, 0, 0, 0, 0, 0};
+    Cut r{};
+    r.x = x;
+    r.n = N;
     if (x >= total) {
         r.x = total;
         return r;
     }
     r.n = owner(off, N, H, x);
-    const int64_t nc = off[r.n + 1] - off[r.n], rest = x - (int64_t)off[r.n] * H;
+    r.nc = off[r.n + 1] - off[r.n];
+    const int64_t nc = r.nc, rest = x - (int64_t)off[r.n] * H;
     r.h = (int)(rest / nc);
     r.c = (int)(rest - r.h * nc);
     r.inner = r.c > 0;
@@ -152,10 +155,13 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
             }
             r = place(chunks, N, H, total, x);
             if (r.inner) {
-                const int nc = chunks[r.n + 1] - chunks[r.n];
-                if (!split || nc <= min_range)
-                    r = place(chunks, N, H, total, r.x + (2 * r.c >= nc ? nc - r.c : -r.c));
+                if (!split || r.nc <= min_range)
+                    r = place(chunks, N, H, total, r.x + (2 * r.c >= r.nc ? r.nc - r.c : -r.c));
             }
+        }
+        if (r.nc) {
+            r.begin = cu[r.n];
+            r.stop = cu[r.n + 1];
         }
         s_cut[i] = r;
     }
@@ -167,9 +173,8 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
                 ++r.before;
             for (int j = i + 1; j < ranges && s_cut[j].inner && s_cut[j].n == r.n && s_cut[j].h == r.h; ++j)
                 ++r.inner;
-            const int64_t nc = chunks[r.n + 1] - chunks[r.n];
             r.handed = n_flags > 0 && r.inner == 1 && r.before == 0 &&
-                       r.c <= s_cut[i + 1].x - r.x - (nc - r.c);
+                       r.c <= s_cut[i + 1].x - r.x - (r.nc - r.c);
         }
         cuts[i] = r;
     }
