@@ -60,29 +60,43 @@ struct Item {
     int n, h;
     int part;                 // kHead, kTail: of a unit whose one cut is handed on
     int c0, c1, nc;           // of nc
-    int64_t t0, t1;           // tokens [t0, t1) of the packed tensors
+    int t0, t1;               // tokens [t0, t1) of the packed tensors
 };
 
-__device__ __forceinline__ void set_tokens(Item &it, int chunk, int64_t begin, int64_t end) {
-    it.t0 = begin + (int64_t)it.c0 * chunk;
-    it.t1 = min(begin + (int64_t)it.c1 * chunk, end);
+__device__ __forceinline__ void set_tokens(Item &it, int chunk, int begin, int stop) {
+    it.t0 = begin + it.c0 * chunk;
+    it.t1 = it.c1 == it.nc ? stop : begin + it.c1 * chunk;
 }
 
 // Walks the items of the range between two cuts.  The heads of a sequence follow each other, so
-// what is known of the sequence is kept: its reads take microseconds beside a busy memory.
+// what is known of the sequence is kept: its reads take microseconds beside a busy memory.  (Little
+// of it, in 32 bits: every role holds one in registers.)
 struct Walk {
-    const Plan &p;
-    int64_t x, end;
-    int lane;
+    int left;                 // chunks of the range
     int n, h, c;
     int nc;                   // chunks of sequence n, 0: not read yet
-    int64_t begin, stop;      // its tokens
-    __device__ __forceinline__ Walk(const Plan &plan, int range, int lane_)
-        : p(plan), x(plan.cuts[range].x), end(plan.cuts[range + 1].x), lane(lane_), n(plan.cuts[range].n),
-          h(plan.cuts[range].h), c(plan.cuts[range].c), nc(plan.cuts[range].nc),
-          begin(plan.cuts[range].begin), stop(plan.cuts[range].stop) {}
-    __device__ __forceinline__ bool next(Item &it) {
-        if (x >= end) return false;
+    int begin, stop;          // its tokens
+    __device__ __forceinline__ Walk(const Plan &p, int range, int lane) {
+        const Cut &b = p.cuts[range];
+        left = (int)(p.cuts[range + 1].x - b.x);
+        n = b.n;
+        h = b.h * p.lanes + lane;
+        c = b.c;
+        nc = b.nc;
+        begin = b.begin;
+        stop = b.stop;
+    }
+    __device__ __forceinline__ void skip(const Plan &p, int chunks) {   // to the end of the unit
+        left -= chunks;
+        c = 0;
+        if ((h += p.lanes) >= p.H) {
+            h -= p.H;
+            ++n;
+            nc = 0;
+        }
+    }
+    __device__ __forceinline__ bool next(const Plan &p, Item &it) {
+        if (left <= 0) return false;
         if (nc == 0) {
             while ((nc = p.off[n + 1] - p.off[n]) == 0) ++n;   // (sequences without tokens)
             begin = p.cu[n];
@@ -90,18 +104,12 @@ struct Walk {
         }
         it.part = Item::kWhole;
         it.n = n;
-        it.h = h * p.lanes + lane;
+        it.h = h;
         it.c0 = c;
         it.nc = nc;
-        it.c1 = (int)min((int64_t)nc, c + (end - x));
+        it.c1 = min(nc, c + left);
         set_tokens(it, p.chunk, begin, stop);
-        x += it.c1 - c;
-        c = 0;
-        if ((++h) * p.lanes == p.H) {
-            h = 0;
-            ++n;
-            nc = 0;
-        }
+        skip(p, it.c1 - c);
         return true;
     }
 };
@@ -198,25 +206,28 @@ __device__ __forceinline__ Start start_state(const Plan &p, const Item &it, int 
 // took 34 of 224 us.)
 struct Items {
     Walk walk;
-    Item tail;
-    bool head, has_tail;
+    enum { kFirst, kWalk, kLast } at;
     __device__ __forceinline__ Items(const Plan &p, int range, int lane) : walk(p, range, lane) {
-        const Cut &e = p.cuts[range + 1];
-        head = e.handed;
-        has_tail = p.cuts[range].handed;
-        if (has_tail) walk.next(tail);
-        tail.part = Item::kTail;
-        if (head) walk.end -= e.c;
+        at = p.cuts[range + 1].handed ? kFirst : kWalk;
+        if (p.cuts[range].handed) walk.skip(p, walk.nc - walk.c);
+        if (at == kFirst) walk.left -= p.cuts[range + 1].c;
     }
     __device__ __forceinline__ bool next(const Plan &p, int range, int lane, Item &it) {
-        if (head) {
-            head = false;
+        if (at == kFirst) {
+            at = kWalk;
             return before_cut(p, range + 1, lane, it);
         }
-        if (walk.next(it)) return true;
-        if (!has_tail) return false;
-        has_tail = false;
-        it = tail;
+        if (at == kLast) return false;
+        if (walk.next(p, it)) return true;
+        at = kLast;
+        const Cut &b = p.cuts[range];
+        if (!b.handed) return false;
+        it.part = Item::kTail;
+        it.n = b.n;
+        it.h = b.h * p.lanes + lane;
+        it.c0 = b.c;
+        it.c1 = it.nc = b.nc;
+        set_tokens(it, p.chunk, b.begin, b.stop);
         return true;
     }
 };

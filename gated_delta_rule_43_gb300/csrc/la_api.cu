@@ -105,7 +105,8 @@ LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t Hk, int32_t dk, int3
 bool la_sizes_ok(int64_t T, int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t dv) {
     return N >= 0 && T >= 0 && H > 0 && Hk > 0 && H % Hk == 0 && (T == 0 || N > 0) &&
            T < ((int64_t)1 << 31) && T <= ((int64_t)1 << 40) / ((int64_t)H * (dk > dv ? dk : dv)) &&
-           (int64_t)N * H <= 0x7fffffffLL;
+           (int64_t)N * H <= 0x7fffffffLL &&
+           (T / la::kSimtChunk + N) * (int64_t)H <= 0x7fffffffLL;   // (chunks are counted in 32 bits)
 }
 
 }  // namespace

@@ -270,9 +270,9 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
     const int j0 = blk * DVB;
     Item it;
     Walk walk(p, range, 0);   // (one lane)
-    bool more = OUT ? walk.next(it) : before_cut(p, range + 1, 0, it);
+    bool more = OUT ? walk.next(p, it) : before_cut(p, range + 1, 0, it);
 
-    for (; more; more = OUT && walk.next(it)) {
+    for (; more; more = OUT && walk.next(p, it)) {
         const int h = it.h;
         const int hk = h / (p.H / p.Hk);
         const int64_t nh = ((int64_t)it.n * p.H + h) * dkdv;

@@ -533,7 +533,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 const uint32_t b = gi & 1, ph = (gi >> 1) & 1, sb = si & 1;
                 const bool next = c + 1 < chunks;
                 const int at_chunk = OUT ? c + 1 : chunks - 2 - c;
-                const int len = next ? (int)min((int64_t)C, it.t1 - it.t0 - (int64_t)at_chunk * C) : C;
+                const int len = next ? min(C, it.t1 - it.t0 - at_chunk * C) : C;
                 if (next) {
                     const bool half_done = OUT && c >= 0;   // (K~^T of chunk c: its first half)
                     ok = wait.warp(kGate + b, ph, kFullK + sb, (si >> 1) & 1,
@@ -802,7 +802,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             }
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
                 const uint32_t b = gi & 1, sb = si & 1, before = ((si - 2) >> 1) & 1;
-                const int32_t t0 = (int32_t)(it.t0 + (int64_t)(OUT ? c : chunks - 1 - c) * C);
+                const int32_t t0 = it.t0 + (OUT ? c : chunks - 1 - c) * C;
                 uint8_t *qk = sm + sb * M::kQK;
                 ok = behind_start(sb);
                 if (ok && si >= 2) ok = wait.warp(kFreeK + sb, before);
@@ -848,7 +848,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             float log_sum = 0.f;
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
                 const uint32_t b = gi & 1;
-                const int64_t t0 = it.t0 + (int64_t)(OUT ? c : chunks - 1 - c) * C;
+                const int64_t t0 = it.t0 + (OUT ? c : chunks - 1 - c) * C;
                 const int len = (int)min((int64_t)C, it.t1 - t0);
                 float x[4], pre[4], suf[4];
                 int bad = -1;
@@ -914,7 +914,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
             si += start.steps;
             for (int c = 0; c < chunks; ++c, ++gi, ++si) {
                 const uint32_t b = gi & 1, sb = si & 1;
-                const int64_t t0 = it.t0 + (int64_t)c * C;
+                const int64_t t0 = it.t0 + c * C;
                 const int len = (int)min((int64_t)C, it.t1 - t0);
                 const uint32_t so = M::kV + b * M::kVBytes;
                 if (ends && c + 1 == chunks) {
