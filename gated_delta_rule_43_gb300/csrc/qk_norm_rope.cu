@@ -33,19 +33,15 @@ struct Side {
     float scale;
 };
 
-// Eight channels as they lie in memory, and as fp32
+// Eight channels as they lie in memory, and as fp32 in pairs
 template <typename T> struct Raw;
 template <> struct Raw<__nv_bfloat16> {
     uint4 u;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
+    __device__ __forceinline__ void get(float2 (&x)[4]) const {
         const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __bfloat1622float2(b[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
+        for (int i = 0; i < 4; ++i) x[i] = __bfloat1622float2(b[i]);
     }
 };
 template <> struct Raw<float> {
@@ -54,20 +50,42 @@ template <> struct Raw<float> {
         a = reinterpret_cast<const float4 *>(p)[0];
         b = reinterpret_cast<const float4 *>(p)[1];
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    __device__ __forceinline__ void get(float2 (&x)[4]) const {
+        x[0] = make_float2(a.x, a.y); x[1] = make_float2(a.z, a.w);
+        x[2] = make_float2(b.x, b.y); x[3] = make_float2(b.z, b.w);
     }
 };
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float2 (&x)[4]) {
     uint4 u;
     __nv_bfloat162 *b = reinterpret_cast<__nv_bfloat162 *>(&u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(x[i].x, x[i].y);
     *reinterpret_cast<uint4 *>(p) = u;
 }
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store8(float *p, const float2 (&x)[4]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+}
+
+// Two products, two products and sums in one instruction: with single ones the arithmetic
+// takes as long as the memory
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
 }
 
 // f turns of 2 pi radians, in units of 2^-64 turn, modulo one turn, rounded down in magnitude.
@@ -103,6 +121,47 @@ qk_norm_rope_kernel(Side q, Side k, int64_t T_tot, int tokens, int parts, int no
     const int64_t t0 = (int64_t)(blockIdx.x / parts) * tokens;
     const int part = blockIdx.x % parts;
     const int here = (int)min((int64_t)tokens, T_tot - t0), pairs = rot / 2;
+    const int lane = threadIdx.x & 31, j = lane % LPR, row = lane / LPR;
+    const bool turned = 16 * j < rot;
+    const int c0 = turned ? (interleaved ? 16 * j : 8 * j) : 16 * j;
+    const int c1 = turned ? (interleaved ? c0 + 8 : rot / 2 + c0) : c0 + 8;
+    const int all = q.heads + k.heads;
+    const int h0 = (int)((int64_t)all * part / parts), h1 = (int)((int64_t)all * (part + 1) / parts);
+    const int rows = here * (h1 - h0);
+    // (the first turn's rows are on their way while the angles are worked out)
+    Raw<T> xa[kAhead], xb[kAhead];
+    T *dst[kAhead];
+    int tok[kAhead];   // -1: none
+    bool is_k[kAhead];
+    auto fetch = [&](int m, int r) {
+        tok[m] = -1;
+        dst[m] = nullptr;
+        is_k[m] = false;
+        xa[m] = Raw<T>{};
+        xb[m] = Raw<T>{};
+        if (r < rows) {
+            int h = r, token = 0;   // (at most kTokens)
+#pragma unroll
+            for (int i = 1; i < kTokens; ++i) {
+                const bool past = h >= h1 - h0;
+                h -= past ? h1 - h0 : 0;
+                token += past;
+            }
+            h += h0;
+            tok[m] = token;
+            is_k[m] = h >= q.heads;
+            const Side &s = is_k[m] ? k : q;
+            const int64_t t = t0 + token, hh = is_k[m] ? h - q.heads : h;
+            const T *src = (const T *)s.x + t * s.xs + hh * D;
+            dst[m] = (T *)s.y + t * s.ys + hh * D;
+            xa[m].load(src + c0);
+            xb[m].load(src + c1);
+        }
+    };
+    constexpr int kTurn = kWarps * RPW * kAhead;
+    int r0 = (threadIdx.x >> 5) * RPW * kAhead;
+#pragma unroll
+    for (int m = 0; m < kAhead; ++m) fetch(m, r0 + m * RPW + row);
     for (int x = threadIdx.x; x < here * pairs; x += kThreads) {
         const int t = x / pairs, i = x - t * pairs;
         // position * turns modulo 2^64: the angle's fraction of a turn, in [-1/2, 1/2)
@@ -114,105 +173,77 @@ qk_norm_rope_kernel(Side q, Side k, int64_t T_tot, int tokens, int parts, int no
         s_sin[t][i] = sn * rope_scale;
     }
     __syncthreads();
-    const int lane = threadIdx.x & 31, j = lane % LPR, row = lane / LPR;
-    const bool turned = 16 * j < rot;
-    const int c0 = turned ? (interleaved ? 16 * j : 8 * j) : 16 * j;
-    const int c1 = turned ? (interleaved ? c0 + 8 : rot / 2 + c0) : c0 + 8;
-    const int all = q.heads + k.heads;
-    const int h0 = (int)((int64_t)all * part / parts), h1 = (int)((int64_t)all * (part + 1) / parts);
-    const int rows = here * (h1 - h0);
-    for (int r0 = (threadIdx.x >> 5) * RPW * kAhead; r0 < rows; r0 += kWarps * RPW * kAhead) {
-        Raw<T> xa[kAhead], xb[kAhead];
-        T *dst[kAhead];
-        int tok[kAhead];
-        bool is_k[kAhead];
+    for (; r0 < rows; r0 += kTurn) {
 #pragma unroll
         for (int m = 0; m < kAhead; ++m) {
-            const int r = r0 + m * RPW + row;
-            tok[m] = -1;
-            dst[m] = nullptr;
-            is_k[m] = false;
-            xa[m] = Raw<T>{};
-            xb[m] = Raw<T>{};
-            if (r < rows) {
-                tok[m] = r / (h1 - h0);
-                const int h = h0 + r - tok[m] * (h1 - h0);
-                is_k[m] = h >= q.heads;
-                const Side &s = is_k[m] ? k : q;
-                const int64_t t = t0 + tok[m], hh = is_k[m] ? h - q.heads : h;
-                const T *src = (const T *)s.x + t * s.xs + hh * D;
-                dst[m] = (T *)s.y + t * s.ys + hh * D;
-                xa[m].load(src + c0);
-                xb[m].load(src + c1);
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < kAhead; ++m) {
-            float a[8], b[8];
+            float2 a[4], b[4];
             xa[m].get(a);
             xb[m].get(b);
-            const float *w = is_k[m] ? k.w : q.w;
-            float scale = is_k[m] ? k.scale : q.scale;
+            const int t = tok[m];
+            const bool of_k = is_k[m];
+            T *const to = dst[m];
+            const float *w = of_k ? k.w : q.w;
+            float factor = of_k ? k.scale : q.scale;   // rotation is linear: first the factors
             if (norm != KDA_NORM_NONE) {
-                float sum = 0.f;
+                float2 sums = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum += a[i] * a[i] + b[i] * b[i];
+                for (int i = 0; i < 4; ++i) sums = fma2(a[i], a[i], fma2(b[i], b[i], sums));
+                float sum = sums.x + sums.y;
 #pragma unroll
                 for (int d = LPR / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const float n = rsqrtf((norm == KDA_NORM_RMS ? sum * (1.f / D) : sum) + eps);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    a[i] *= n;
-                    b[i] *= n;
-                }
+                factor *= rsqrtf((norm == KDA_NORM_RMS ? sum * (1.f / D) : sum) + eps);
             }
-            if (tok[m] < 0) continue;
+            if (t < 0) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = mul2(a[i], make_float2(factor, factor));
+                b[i] = mul2(b[i], make_float2(factor, factor));
+            }
             if (w) {
                 Raw<float> wa, wb;
                 wa.load(w + c0);
                 wb.load(w + c1);
-                float fa[8], fb[8];
+                float2 fa[4], fb[4];
                 wa.get(fa);
                 wb.get(fb);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    a[i] *= fa[i];
-                    b[i] *= fb[i];
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = mul2(a[i], fa[i]);
+                    b[i] = mul2(b[i], fb[i]);
                 }
             }
             if (turned) {
                 Raw<float> rc, rs;
-                rc.load(&s_cos[tok[m]][8 * j]);
-                rs.load(&s_sin[tok[m]][8 * j]);
-                float cs[8], sn[8];
+                rc.load(&s_cos[t][8 * j]);
+                rs.load(&s_sin[t][8 * j]);
+                float2 cs[4], sn[4];
                 rc.get(cs);
                 rs.get(sn);
                 if (interleaved) {
+                    auto turn = [](float2 &x, float c, float s) {
+                        x = make_float2(x.x * c - x.y * s, x.y * c + x.x * s);
+                    };
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x0 = a[2 * i], y0 = a[2 * i + 1], x1 = b[2 * i], y1 = b[2 * i + 1];
-                        a[2 * i] = x0 * cs[i] - y0 * sn[i];
-                        a[2 * i + 1] = y0 * cs[i] + x0 * sn[i];
-                        b[2 * i] = x1 * cs[4 + i] - y1 * sn[4 + i];
-                        b[2 * i + 1] = y1 * cs[4 + i] + x1 * sn[4 + i];
+                    for (int i = 0; i < 2; ++i) {
+                        turn(a[2 * i], cs[i].x, sn[i].x);
+                        turn(a[2 * i + 1], cs[i].y, sn[i].y);
+                        turn(b[2 * i], cs[2 + i].x, sn[2 + i].x);
+                        turn(b[2 * i + 1], cs[2 + i].y, sn[2 + i].y);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float x = a[i], y = b[i];
-                        a[i] = x * cs[i] - y * sn[i];
-                        b[i] = y * cs[i] + x * sn[i];
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 x = a[i], y = b[i];
+                        a[i] = fma2(x, cs[i], mul2(y, make_float2(-sn[i].x, -sn[i].y)));
+                        b[i] = fma2(y, cs[i], mul2(x, sn[i]));
                     }
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                a[i] *= scale;
-                b[i] *= scale;
-            }
-            store8(dst[m] + c0, a);
-            store8(dst[m] + c1, b);
+            store8(to + c0, a);
+            store8(to + c1, b);
         }
+#pragma unroll
+        for (int m = 0; m < kAhead; ++m) fetch(m, r0 + kTurn + m * RPW + row);
     }
 }
 
