@@ -4,10 +4,12 @@
 // heads inside sequences, stand in one row of `total` chunks.  The row is cut into `ranges`
 // equal parts, one for each CTA (CTA group on the CUDA cores), wherever that falls: every SM
 // has the same work whatever the lengths are.  (A unit counts as `unit_cost` chunks more than it
-// has, for its states.)  A cut inside a unit is an inner boundary: a
-// first pass forms the state that the tokens before it, back to the unit's start or the cut
-// before, leave there; a scan along the cuts of each unit turns these into the states at the
-// cuts; and the output pass starts its ranges from them.
+// has, for its states.)  The state at a cut inside a unit comes from one of these:
+//   - the unit is cut once and its first part is handed on (see Items);
+//   - else a first pass forms what the tokens before the cut, back to the unit's start or the cut
+//     before, leave there, and the range behind starts from all of the unit's cuts up to its own
+//     (p.compose), or, where those can be many or the initial states are overwritten, a scan
+//     along the cuts has put them together (6 us).
 // A cut moves out of a unit of at most min_range chunks to its nearer end: for so few chunks the
 // extra pass costs more than the evener load gives.  When there are more SMs than work, every
 // unit has a range of its own, and one of at least 2 min_range chunks several, of min_range or

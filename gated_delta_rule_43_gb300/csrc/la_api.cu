@@ -154,7 +154,7 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     float *bnd_log = (float *)(ws + L.log_off), *bnd = (float *)(ws + L.bnd_off);
     const int64_t dkdv = (int64_t)dk * dv;
     // On the tensor cores a range can put its start state together from what the cuts before it
-    // hold: 64 KB a cut against a scan of about 7 us.  A unit has at most ranges * lanes / H + 1 cuts (the
+    // hold: 64 KB a cut (0.8 us) against a scan of about 7 us.  A unit has at most ranges * lanes / H + 1 cuts (the
     // cuts are even, and H units are as long as the longest).  In place the initial states may
     // be gone by then; the scan keeps copies.
     const bool in_place = initial_state && initial_state == final_state;

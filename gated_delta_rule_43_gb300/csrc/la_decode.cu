@@ -5,6 +5,8 @@
 // everything else is 1% of that.  A CTA owns a block of value columns of one (sequence,
 // head); a thread holds R rows x 4 columns, so a warp's loads are whole 128-byte lines, all
 // issued before the first is used, and the columns' outputs are joined in shared memory.
+// 256 sequences of 32 heads (1.08 GB): 159 us, 6.8 TB/s, a plain copy's rate.  One sequence: 4 us,
+// launch and memory latency.
 #include "kda_common.cuh"
 
 namespace kda {

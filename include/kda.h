@@ -330,22 +330,23 @@ kda_status kda_gate_cumsum(const void *z, const float *A_log, const int32_t *cu_
 
 /*
  * Bytes of workspace kda_la_chunk_fwd needs (0 for arguments it would reject).  The
- * workspace holds the status word, the plan of the packed sequences and the states at
- * the inner segment boundaries; it needs no initialisation.
+ * workspace holds the status word, the plan of the packed sequences and the states at the
+ * cuts inside sequences; it needs no initialisation.
  */
 size_t kda_la_chunk_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H,
                                        int32_t Hk, int32_t dk, int32_t dv, int32_t dtype);
 
 /*
  * Chunked prefill over packed variable-length sequences (arguments as kda_chunk_fwd where
- * they have the same names).  Every sequence is cut into segments of equal length; a first
- * pass forms each segment's own contribution to the state (all segments but a sequence's
- * last), a scan turns these into the segments' start states, and a second pass walks the
- * segments in parallel.  Inside a segment the tokens go through dense products over
+ * they have the same names).  The chunks of all heads and sequences are dealt out evenly over
+ * the SMs.  Where that cuts a sequence, the state at the cut is handed on by the SM before it
+ * or, in long sequences, formed by a first pass over the tokens before the cut.  Inside its
+ * share an SM goes through dense products over
  * chunks.  The result equals the token-by-token recurrence up to rounding: states are
  * accumulated and kept in fp32; with bf16 storage the scores and the copy of the state
  * that meets the queries are rounded to bf16 (the state that is carried on is not).
  *   initial_state, final_state  [num_seqs, H, dk, dv] fp32 or NULL; may be the same buffer
+ * Sizes: total_tokens below 2^31, and at most 2^31 - 1 chunks of 32 tokens over all heads.
  * Device-found errors: KDA_ERR_SEQLENS (the offending sequence is skipped),
  * KDA_ERR_DECAY_RANGE (a g that is positive or NaN; info = token * H + head, or the head
  * when g is [H]; that head's outputs are not meaningful), KDA_ERR_TIMEOUT.

@@ -174,6 +174,22 @@ def test_split_calls_and_single_tokens_agree_with_one_call():
     assert U.rel(S, rS) <= U.TOL_S
 
 
+def test_captured_in_a_graph():
+    args = gpu(*U.make(MANY[:11], 16, 4, 64, 64, BF, seed=21, speed=0.01))
+    kda.la_chunk_fwd(*args)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, S = kda.la_chunk_fwd(*args)
+        o1 = kda.la_decode_step(*(x[:11].contiguous() for x in args[:4]), S)
+    for seed in (22, 23):
+        for x, y in zip(args, U.make(MANY[:11], 16, 4, 64, 64, BF, seed=seed, speed=0.01)):
+            x.copy_(y)
+        graph.replay()
+        ro, rS = kda.la_chunk_fwd(*args, check=True)
+        r1 = kda.la_decode_step(*(x[:11] for x in args[:4]), rS)
+        assert torch.equal(o, ro) and torch.equal(S, rS) and torch.equal(o1, r1)
+
+
 def test_repeatable_on_another_stream_with_a_reused_workspace():
     args = gpu(*U.make([700, 90, 1], 4, 4, 128, 128, BF, seed=11))
     N, H = 3, 4
