@@ -49,6 +49,12 @@ def test_prefill(lib):
         assert call(**kw) == INVALID, kw
 
 
+def test_prefill_of_more_chunks_than_can_be_counted(lib):
+    size = lib.kda_la_chunk_fwd_workspace_size
+    assert size(1 << 28, 1 << 22, 100, 100, 32, 32, kda.KDA_F32) > 0
+    assert size(1 << 28, 1 << 24, 100, 100, 32, 32, kda.KDA_F32) == 0
+
+
 def test_decode(lib):
     base = dict(q=A, k=2 * A, v=3 * A, g=4 * A, S=5 * A)
     tail = dict(H=4, Hk=2, dk=64, dv=64, dtype=kda.KDA_F32, qs=128, ks=128, vs=256, gpt=0)
