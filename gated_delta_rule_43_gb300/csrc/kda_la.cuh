@@ -10,11 +10,16 @@
 //     before, leave there, and the range behind starts from all of the unit's cuts up to its own
 //     (p.compose), or, where those can be many or the initial states are overwritten, a scan
 //     along the cuts has put them together (6 us).
-// A cut moves out of a unit of at most min_range chunks to its nearer end: for so few chunks the
-// extra pass costs more than the evener load gives.  When there are more SMs than work, every
-// unit has a range of its own, and one of at least 2 min_range chunks several, of min_range or
-// more.  Chunks are 128 tokens on the tensor cores and 32 on the CUDA cores; min_range is 1024
-// and 128 tokens, about where a walk costs as much as the first pass and the scan.
+// A cut moves out of a unit of at most 512 tokens (64 on the CUDA cores) to its nearer end: for
+// so few another start costs more than the evener load gives (40 sequences of 700 tokens, 4 heads:
+// with 256, 512, 1024 tokens 55, 55, 63 us; 8 heads of 8192, whose pieces it bounds: 51, 48, 48).
+// Nothing is cut in calls of at most 1024 tokens (128): the kernels it takes cost as much as it
+// gives (8 heads of 600 tokens: 27 us, cut 29; of 1000: 31 and 29).  When there are more SMs than work,
+// every unit has a range of its own, and a longer one several.  On the tensor cores these are of
+// sqrt(chunks) / 2 chunks, since every range adds a state that others read (8 heads of 2000 tokens
+// in pieces of 2, 4, 8 chunks: 32, 38, 51 us; 2 heads of 16384: 55, 48, 55); on the CUDA cores,
+// where a chunk takes longest, of two (a head of 4096 tokens in pieces of 1, 2, 4: 69, 51, 67 us).
+// Chunks are 128 tokens on the tensor cores and 32 on the CUDA cores.
 //
 // Value heads that share queries and keys are walked side by side: `lanes` CTAs take the same
 // range of the row of every lanes-th head, so that what one of them reads the others find in
@@ -27,8 +32,8 @@
 namespace kda {
 namespace la {
 
-constexpr int kTcChunk = 128, kTcMinRange = 8;
-constexpr int kSimtChunk = 32, kSimtMinRange = 4;
+constexpr int kTcChunk = 128, kTcUncut = 512, kTcSplit = 1024;
+constexpr int kSimtChunk = 32, kSimtUncut = 64, kSimtSplit = 128;
 constexpr int kMaxRanges = 512;   // (the plan's shared memory)
 
 // A place in the row of chunks: before chunk c of head h of sequence n.  (What a walk needs of the

@@ -9,7 +9,7 @@
 
 namespace kda {
 cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off, int unit_cost,
-                           int chunk, int min_range, la::Cut *cuts, int ranges, int split, uint32_t *flags, int n_flags, StatusWord *st, const float *h0, float *hT,
+                           int chunk, int uncut, la::Cut *cuts, int ranges, int split, uint32_t *flags, int n_flags, StatusWord *st, const float *h0, float *hT,
                            int H, int lanes, int64_t dkdv, cudaStream_t s);
 cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
                            int64_t dkdv, cudaStream_t s);
@@ -69,27 +69,26 @@ bool stride_ok(int64_t stride, int64_t T, int32_t heads, int32_t D, int32_t dtyp
 }
 
 struct LaLayout {
-    int lanes, ranges, chunk, min_range;
+    int lanes, ranges, chunk, uncut;   // uncut: chunks
     bool split;
     int flags;                // states that may be handed on, and a count of CTAs (tensor cores)
     size_t cuts_off, off_off, log_off, flag_off, bnd_off, total;
 };
 
-// One range of one lane an SM, and no more than there can be chunks.  Sequences are cut only where
-// one may be longer than a range of the least length (the lengths are on the device).  On the
+// One range of one lane an SM, and no more than there can be chunks.  On the
 // tensor cores all heads that share queries and keys are lanes, or as many of them as leave no
 // more than 1/24 of the SMs over; the CUDA cores are not bound by what they read.
 LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t dv, int32_t dtype, int sms) {
     LaLayout L{};
     L.chunk = dtype == KDA_BF16 ? la::kTcChunk : la::kSimtChunk;
-    L.min_range = dtype == KDA_BF16 ? la::kTcMinRange : la::kSimtMinRange;
+    L.uncut = (dtype == KDA_BF16 ? la::kTcUncut : la::kSimtUncut) / L.chunk;
     if (sms > la::kMaxRanges) sms = la::kMaxRanges;
     L.lanes = dtype == KDA_BF16 ? H / Hk : 1;
     while ((H / Hk) % L.lanes != 0 || L.lanes > sms || sms % L.lanes * 24 > sms) --L.lanes;
     const int64_t most = (T / L.chunk + N) * (int64_t)(H / L.lanes);
     sms /= L.lanes;
     L.ranges = (int)(most < 1 ? 1 : most < sms ? most : sms);
-    L.split = L.ranges > 1 && T > L.min_range * L.chunk;
+    L.split = L.ranges > 1 && T > (dtype == KDA_BF16 ? la::kTcSplit : la::kSimtSplit);
     const size_t all = (size_t)L.ranges * L.lanes;
     L.cuts_off = kHeaderBytes;
     L.off_off = L.cuts_off + round_up(sizeof(la::Cut) * ((size_t)L.ranges + 1), 256);
@@ -165,7 +164,7 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     // packed sequences: 11.6k cycles beside 5.4k of a chunk).
     const int unit_cost = (initial_state ? 1 : 0) + (final_state ? 1 : 0);
     cudaError_t e = launch_la_plan(cu_seqlens, num_seqs, total_tokens, off, unit_cost, L.chunk,
-                                   L.min_range, cuts, L.ranges, L.split, p.flags, L.flags, st, initial_state, final_state, H, L.lanes, dkdv, s);
+                                   L.uncut, cuts, L.ranges, L.split, p.flags, L.flags, st, initial_state, final_state, H, L.lanes, dkdv, s);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (total_tokens == 0) return KDA_OK;
     CUtensorMap maps[8];

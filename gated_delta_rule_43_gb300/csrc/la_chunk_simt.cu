@@ -48,14 +48,15 @@ __device__ Cut place(const int32_t *off, int N, int H, int64_t total, int64_t x)
 }
 
 // Ranges a unit of nc chunks is worth when there are SMs to spare
-__device__ __forceinline__ int pieces(int nc, int split, int min_range) {
-    return nc == 0 ? 0 : !split || nc < 2 * min_range ? 1 : nc / min_range;
+__device__ __forceinline__ int pieces(int nc, int split, int chunk) {
+    const int length = chunk == kTcChunk ? max(2, (int)(0.5f * sqrtf((float)nc))) : 2;
+    return nc == 0 ? 0 : !split || nc < 2 * length ? 1 : nc / length;
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
 la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *off,
                int32_t *piece_off, int32_t *cost_off, int unit_cost, int chunk,
-               int min_range, Cut *cuts, int ranges, int split, uint32_t *flags, int n_flags,
+               int uncut, Cut *cuts, int ranges, int split, uint32_t *flags, int n_flags,
                StatusWord *st, const float *h0, float *S_out, int all_heads, int H,
                int64_t dkdv4) {   // H: heads of a lane
     let_next_start();
@@ -100,7 +101,7 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
                 report(st, KDA_ERR_SEQLENS, n, 2);
             else
                 own.x = (int)((e - b + chunk - 1) / chunk);
-            own.y = pieces(own.x, split, min_range);
+            own.y = pieces(own.x, split, chunk);
             own.z = own.x ? own.x + unit_cost : 0;
         }
         int3 x = own;   // inclusive warp scan
@@ -135,7 +136,7 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
     const int64_t cost = (int64_t)carry.z * H;
     // SMs to spare: every unit gets its own range, a long one several.  Else equal parts
     // (without a first pass nothing can be cut: the units are dealt out whole).
-    const bool spare = fine <= ranges && total < (int64_t)ranges * min_range;
+    const bool spare = fine <= ranges && total < (int64_t)ranges * uncut;
     for (int i = tid; i <= ranges; i += kPlanThreads) {
         Cut r;
         if (spare) {
@@ -158,7 +159,7 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
             }
             r = place(chunks, N, H, total, x);
             if (r.inner) {
-                if (!split || r.nc <= min_range)
+                if (!split || r.nc <= uncut)
                     r = place(chunks, N, H, total, r.x + (2 * r.c >= r.nc ? r.nc - r.c : -r.c));
             }
         }
@@ -470,13 +471,13 @@ static cudaError_t launch_dims(bool out, const Plan &p, const float *q, const fl
 }  // namespace la
 
 cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off, int unit_cost,
-                           int chunk, int min_range, la::Cut *cuts, int ranges, int split, uint32_t *flags, int n_flags, StatusWord *st, const float *h0, float *hT,
+                           int chunk, int uncut, la::Cut *cuts, int ranges, int split, uint32_t *flags, int n_flags, StatusWord *st, const float *h0, float *hT,
                            int H, int lanes, int64_t dkdv, cudaStream_t s) {
     float *S_out = hT != h0 ? hT : nullptr;   // an in-place update leaves empty ones as they are
     const int64_t nh = (int64_t)N * H;
     const int grid = S_out ? 1 + (int)(nh < 255 ? nh : 255) : 1;
     la::la_plan_kernel<<<grid, la::kPlanThreads, 0, s>>>(
-        cu, N, T_tot, off, off + N + 1, off + 2 * (N + 1), unit_cost, chunk, min_range, cuts, ranges, split,
+        cu, N, T_tot, off, off + N + 1, off + 2 * (N + 1), unit_cost, chunk, uncut, cuts, ranges, split,
         flags, n_flags, st, h0, S_out, H, H / lanes, dkdv / 4);
     return cudaGetLastError();
 }
