@@ -13,7 +13,7 @@ cudaError_t launch_la_plan(const int32_t *cu, int N, int64_t T_tot, int32_t *off
                            int H, int lanes, int64_t dkdv, cudaStream_t s);
 cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const float *bnd_log,
                            int64_t dkdv, cudaStream_t s);
-cudaError_t launch_la_simt(bool out, int dk, int dv, const la::Plan &p, const float *q,
+cudaError_t launch_la_simt(bool out, bool whole, int dk, int dv, const la::Plan &p, const float *q,
                            const float *k, const float *v, int64_t qs, int64_t ks, int64_t vs,
                            const float *g, int gpt, const float *h0, float *hT, float *o,
                            float *bnd, float *bnd_log, StatusWord *st, cudaStream_t s);
@@ -172,11 +172,12 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
         la_tensor_maps(maps, q, k, v, o, initial_state, final_state, L.split ? bnd : nullptr, p,
                        total_tokens, dk, dv, q_stride, k_stride, v_stride) != cudaSuccess)
         return KDA_ERR_CUDA;
+    const bool whole = L.ranges == sm_count();
     auto pass = [&](bool out) {
         if (dtype == KDA_BF16)
             return launch_la_tc(out, p, maps, g, g_per_token, initial_state != nullptr,
                                 final_state != nullptr, o, dk, dv, bnd, bnd_log, st, s);
-        return launch_la_simt(out, dk, dv, p, (const float *)q, (const float *)k, (const float *)v,
+        return launch_la_simt(out, whole, dk, dv, p, (const float *)q, (const float *)k, (const float *)v,
                               q_stride, k_stride, v_stride, g, g_per_token, initial_state,
                               final_state, (float *)o, bnd, bnd_log, st, s);
     };

@@ -8,8 +8,8 @@
 // a suffix sum keeps its relative precision next to the chunk's end, where the weights
 // matter, however fast the earlier tokens decay.
 // Bound by fp32 arithmetic fed from shared memory, and in small calls by the steps before each
-// other: three sequences of 1000, 37 and 513 tokens, 4 heads of 64 x 128, 47 us (plan 5, first
-// pass 12, scan 6, outputs 30, each begun before the one before has ended).
+// other: three sequences of 1000, 37 and 513 tokens, 4 heads of 64 x 128, 45 us (plan 7, first
+// pass 9, scan 6, outputs 24).
 #include "kda_la.cuh"
 
 namespace kda {
@@ -452,12 +452,11 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
     }
 }
 
-template <int DK, int DV>
-static cudaError_t launch_dims(bool out, const Plan &p, const float *q, const float *k,
-                               const float *v, int64_t qs, int64_t ks, int64_t vs, const float *g,
-                               int gpt, const float *h0, float *hT, float *o, float *bnd,
-                               float *bnd_log, StatusWord *st, cudaStream_t s) {
-    constexpr int DVB = DV < 64 ? DV : 64;
+template <int DK, int DV, int DVB>
+static cudaError_t launch_columns(bool out, const Plan &p, const float *q, const float *k,
+                                  const float *v, int64_t qs, int64_t ks, int64_t vs, const float *g,
+                                  int gpt, const float *h0, float *hT, float *o, float *bnd,
+                                  float *bnd_log, StatusWord *st, cudaStream_t s) {
     constexpr size_t bytes = sizeof(Smem<DK, DVB>);
     auto *f = out ? la_chunk_simt_kernel<DK, DV, DVB, true> : la_chunk_simt_kernel<DK, DV, DVB, false>;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
@@ -466,6 +465,16 @@ static cudaError_t launch_dims(bool out, const Plan &p, const float *q, const fl
     f<<<ranges * (DV / DVB), kThreads, bytes, s>>>(p, q, k, v, qs, ks, vs, g, gpt, h0, hT, o, bnd,
                                                    bnd_log, st);
     return cudaGetLastError();
+}
+
+// Columns in blocks of at most 64, a CTA each; or, where there are as many ranges as SMs, all
+// columns in one, so that the scores are formed once (20 sequences of 500 tokens, 8 heads of
+// 128 x 128: 273 us, 360 in blocks; 3 of 1000, 37 and 513, 4 heads of 64 x 128: 45 and 49; with
+// fewer ranges the blocks keep more SMs busy).
+template <int DK, int DV, typename... A>
+static cudaError_t launch_dims(bool whole, A... args) {
+    if (DV > 64 && whole) return launch_columns<DK, DV, DV>(args...);
+    return launch_columns<DK, DV, (DV < 64 ? DV : 64)>(args...);
 }
 
 }  // namespace la
@@ -490,13 +499,13 @@ cudaError_t launch_la_scan(const la::Plan &p, const float *h0, float *bnd, const
                             dkdv / 4);
 }
 
-cudaError_t launch_la_simt(bool out, int dk, int dv, const la::Plan &p, const float *q,
+cudaError_t launch_la_simt(bool out, bool whole, int dk, int dv, const la::Plan &p, const float *q,
                            const float *k, const float *v, int64_t qs, int64_t ks, int64_t vs,
                            const float *g, int gpt, const float *h0, float *hT, float *o,
                            float *bnd, float *bnd_log, StatusWord *st, cudaStream_t s) {
 #define KDA_LA(DK_, DV_)                                                                       \
     if (dk == DK_ && dv == DV_)                                                                \
-        return la::launch_dims<DK_, DV_>(out, p, q, k, v, qs, ks, vs, g, gpt, h0, hT, o, bnd,  \
+        return la::launch_dims<DK_, DV_>(whole, out, p, q, k, v, qs, ks, vs, g, gpt, h0, hT, o, bnd,  \
                                          bnd_log, st, s);
     KDA_LA(32, 32) KDA_LA(32, 64) KDA_LA(32, 128)
     KDA_LA(64, 32) KDA_LA(64, 64) KDA_LA(64, 128)
