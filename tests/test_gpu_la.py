@@ -75,6 +75,12 @@ def test_many_heads_of_many_segments_in_place(dtype):
     assert U.rel(o, ro) <= U.TOL_O[dtype] and U.rel(h0, rS) <= U.TOL_S
 
 
+@pytest.mark.parametrize("dk", [32, 64, 128])
+@pytest.mark.parametrize("h0", [True, False])
+def test_single_precision_with_a_range_an_sm(dk, h0):
+    check(U.make([2500, 37, 0, 600], 4, 2, dk, 128, F32, seed=dk, h0=h0, speed=0.02))
+
+
 MANY = [1300, 1500, 1250, 0, 1700, 900, 1600, 1, 1100, 2000, 1290, 1410, 300, 1820]
 
 
