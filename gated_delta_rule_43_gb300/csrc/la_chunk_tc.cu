@@ -303,8 +303,8 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
         if (tid == 0) *tslot = place;
         __syncthreads();
         place = *tslot;
-        __syncthreads();   // (its place is used from here on)
     }
+    __syncthreads();   // the slot has been read by all: from here on its place is a chunk's decay
     const int range = place / p.lanes, side = place % p.lanes;
     const bool work = OUT ? p.cuts[range].x < p.cuts[range + 1].x
                           : p.cuts[range + 1].inner != 0 && !p.cuts[range + 1].handed;
