@@ -6,7 +6,10 @@
 //   S' = exp(G_C) S + (K * exp(g_{s+1} + ... + g_C))^T V
 // The state product's weights come from suffix sums, not from differences of prefix sums:
 // a suffix sum keeps its relative precision next to the chunk's end, where the weights
-// matter, however fast the earlier tokens decay.
+// matter, however fast the earlier tokens decay.  The scores do need differences, and behind a few
+// resets G is in the thousands: it is kept as the sum of two fp32 (each addition with its rounding,
+// Knuth's two-sum), so that D is as exact behind resets as without any (outputs 3e-8 off by it; with
+// plain prefix sums 2e-5 at a reset every four tokens).
 // Bound by fp32 arithmetic fed from shared memory, and in small calls by the steps before each
 // other: three sequences of 1000, 37 and 513 tokens, 4 heads of 64 x 128, 45 us (plan 7, first
 // pass 9, scan 6, outputs 24).
@@ -236,7 +239,7 @@ template <int DK, int DVB> struct Smem {
     float v[C][DVB];
     float S[DK][DVB];
     float p[C][C + 4];
-    float G[C], eG[C], w[C];            // prefix sums, their exponentials, weights to the end
+    float G[C], Glo[C], eG[C], w[C];    // prefix sums (two parts), their exponentials, weights to the end
     float total, total_log;             // the chunk's decay and its log
 };
 
@@ -245,6 +248,13 @@ __device__ __forceinline__ void fma4(float (&acc)[4], float a, const float4 &b) 
     acc[1] += a * b.y;
     acc[2] += a * b.z;
     acc[3] += a * b.w;
+}
+
+// hi + lo += x + y, the rounding of the larger parts' sum kept in the smaller one
+__device__ __forceinline__ void add2(float &hi, float &lo, float x, float y) {
+    const float sum = __fadd_rn(hi, x), of_x = __fsub_rn(sum, hi);
+    lo = __fadd_rn(__fadd_rn(lo, y), __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, of_x)), __fsub_rn(x, of_x)));
+    hi = sum;
 }
 
 // OUT: outputs and final states of the CTA's range.  Else what the end of the range leaves at
@@ -338,17 +348,19 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
                 if (!log_decay_ok(x) && blk == 0)
                     report(st, KDA_ERR_DECAY_RANGE, g_per_token ? (t0 + tid) * p.H + h : h, 30);
                 float pre = x < kLogZero ? kLogZero : x;   // (a comparison, so that NaN spreads)
-                float suf = x;
+                float pre_lo = 0.f, suf = x;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const float a = __shfl_up_sync(0xffffffffu, pre, d);
+                    const float a_lo = __shfl_up_sync(0xffffffffu, pre_lo, d);
                     const float b = __shfl_down_sync(0xffffffffu, suf, d);
-                    if (tid >= d) pre += a;
+                    if (tid >= d) add2(pre, pre_lo, a, a_lo);
                     if (tid + d < 32) suf += b;
                 }
                 const float after = __shfl_down_sync(0xffffffffu, suf, 1);
                 sm.G[tid] = pre;
-                sm.eG[tid] = expf(pre);
+                sm.Glo[tid] = pre_lo;
+                sm.eG[tid] = expf(pre + pre_lo);
                 sm.w[tid] = tid == 31 ? 1.f : expf(after);
                 if (tid == 0) {
                     sm.total_log = suf;
@@ -380,7 +392,7 @@ la_chunk_simt_kernel(Plan p, const float *__restrict__ q, const float *__restric
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
                         const int t = ta + 16 * m, s = sa + 16 * n;
-                        sm.p[t][s] = t >= s ? acc[m][n] * expf(sm.G[t] - sm.G[s]) : 0.f;
+                        sm.p[t][s] = t >= s ? acc[m][n] * expf((sm.G[t] - sm.G[s]) + (sm.Glo[t] - sm.Glo[s])) : 0.f;
                     }
                 __syncthreads();
                 float oi[OR][4] = {}, oa[OR][4] = {};
