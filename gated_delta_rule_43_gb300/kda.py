@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI.  PyTorch supplies device memory and the stream.
 There is no CPU fallback: if the library is missing or no GPU is present the
-calls raise.
+calls raise.  Calls run on the current device: tensors or a stream of
+another one are refused.
 """
 from __future__ import annotations
 
@@ -110,13 +111,30 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _check_current(device):
+    """The library launches on the current device: a call with another device's tensors would
+    run there with foreign addresses, unordered with the work that made them."""
+    if device != _current_device():
+        raise ValueError(f"the tensors live on cuda:{device}, but cuda:{_current_device()} is "
+                         f"current: make the call under torch.cuda.device({device})")
+
+
 def _check_cuda(*ts):
+    device = None
     for t in ts:
         if t is not None:
             if not t.is_cuda:
                 raise ValueError("every tensor must live on a CUDA device (no CPU fallback)")
             if not t.is_contiguous():
                 raise ValueError("tensors must be contiguous")
+            if device is None:
+                device = t.get_device()
+                _check_current(device)
+            elif t.get_device() != device:
+                raise ValueError("every tensor must live on one CUDA device")
 
 
 def _expect(name, t, shape, dtype=None):
@@ -385,6 +403,9 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _raw_stream(stream, device):
     if stream is not None:
+        of = getattr(stream, "device", None)
+        if of is not None and of.index != device:
+            raise ValueError(f"the stream is of {of}, the tensors live on cuda:{device}")
         return stream.cuda_stream
     return _current_raw_stream(device)
 
@@ -394,10 +415,12 @@ def _off_gpu():
 
 
 def _same_gpu(q, *ts):
-    """The index of q's GPU; every tensor given lives there."""
+    """The index of q's GPU, which is the current one; every tensor given lives there."""
     device = q.get_device()
     if device < 0:
         _off_gpu()
+    if device != _current_device():
+        _check_current(device)
     for t in ts:
         if t is not None and t.get_device() != device:
             _off_gpu()
@@ -714,6 +737,8 @@ def state_pool_compact(pool, live, *, new_index=None, n_live=None, workspace=Non
 
 def query_status(workspace, stream=None, *, raise_on_error: bool = False):
     """(code, info) recorded in `workspace` by the last call (synchronises the stream)."""
+    if workspace.is_cuda:
+        _check_current(workspace.get_device())
     info = ctypes.c_int64(0)
     rc = load().kda_query_status(_ptr(workspace), _stream(stream), ctypes.byref(info))
     if raise_on_error and rc != KDA_OK:
