@@ -94,16 +94,23 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
     for (int i = tid; i < n_flags; i += kPlanThreads) flags[i] = 0;
     if (tid == 0 && (cu[0] != 0 || (int64_t)cu[N] != T_tot)) report(st, KDA_ERR_SEQLENS, N, 1);
     int3 carry = make_int3(0, 0, 0);   // chunks, pieces, costs
-    auto add = [](int3 &x, const int3 &y) { x.x += y.x; x.y += y.y; x.z += y.z; };
+    auto add = [](int3 &x, const int3 &y) {   // (sums that do not fit are not used, see below)
+        x.x = (int)((uint32_t)x.x + (uint32_t)y.x);
+        x.y = (int)((uint32_t)x.y + (uint32_t)y.y);
+        x.z = (int)((uint32_t)x.z + (uint32_t)y.z);
+    };
+    bool bad = false;
     for (int base = 0; base < N; base += kPlanThreads) {
         const int n = base + tid;
         int3 own = make_int3(0, 0, 0);
         if (n < N) {
             const int64_t b = cu[n], e = cu[n + 1];
-            if (b < 0 || e < b || e > T_tot)
+            if (b < 0 || e < b || e > T_tot) {
                 report(st, KDA_ERR_SEQLENS, n, 2);
-            else
+                bad = true;
+            } else {
                 own.x = (int)((e - b + chunk - 1) / chunk);
+            }
             own.y = pieces(own.x, split, chunk);
             own.z = own.x ? own.x + unit_cost : 0;
         }
@@ -134,7 +141,21 @@ la_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_tot, int32_t *of
         parts[N] = carry.y;
         costs[N] = carry.z;
     }
-    __syncthreads();
+    // Where an offending sequence lets the others overlap, what they add up to has no bound by the
+    // call's sizes (nor have the sums): then none is gone through.
+    if (__syncthreads_or(bad)) {
+        __shared__ unsigned long long s_tokens;
+        if (tid == 0) s_tokens = 0;
+        __syncthreads();
+        unsigned long long tokens = 0;
+        for (int n = tid; n < N; n += kPlanThreads) {
+            const int64_t b = cu[n], e = cu[n + 1];
+            if (b >= 0 && e >= b && e <= T_tot) tokens += e - b;
+        }
+        atomicAdd(&s_tokens, tokens);
+        __syncthreads();
+        if (s_tokens > (unsigned long long)T_tot) carry = make_int3(0, 0, 0);
+    }
     const int64_t total = (int64_t)carry.x * H, fine = (int64_t)carry.y * H;
     const int64_t cost = (int64_t)carry.z * H;
     // SMs to spare: every unit gets its own range, a long one several.  Else equal parts

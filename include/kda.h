@@ -347,7 +347,9 @@ size_t kda_la_chunk_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, i
  * that meets the queries are rounded to bf16 (the state that is carried on is not).
  *   initial_state, final_state  [num_seqs, H, dk, dv] fp32 or NULL; may be the same buffer
  * Sizes: total_tokens below 2^31, and at most 2^31 - 1 chunks of 32 tokens over all heads.
- * Device-found errors: KDA_ERR_SEQLENS (the offending sequence is skipped),
+ * Device-found errors: KDA_ERR_SEQLENS (the offending sequence is skipped; all are where the
+ * lengths of the others add up to more than total_tokens: nothing is written then but final
+ * states of sequences that are offending or empty),
  * KDA_ERR_DECAY_RANGE (a g that is positive or NaN; info = token * H + head, or the head
  * when g is [H]; that head's outputs are not meaningful), KDA_ERR_TIMEOUT.
  */
