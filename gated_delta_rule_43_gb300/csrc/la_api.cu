@@ -101,6 +101,14 @@ LaLayout la_layout(int64_t T, int32_t N, int32_t H, int32_t Hk, int32_t dk, int3
     return L;
 }
 
+// Ranges that hold work, on the CUDA cores: all, or with SMs to spare the pieces that the plan
+// cuts, counted for sequences of the mean length (the lengths are on the device).
+int64_t busy_ranges(const LaLayout &L, int64_t T, int32_t N, int32_t H) {
+    const int64_t each = (T + (int64_t)N * L.chunk - 1) / ((int64_t)N * L.chunk);   // chunks
+    const int64_t pieces = N * (int64_t)H * (L.split && each >= 4 ? each / 2 : 1);
+    return pieces < L.ranges ? pieces : L.ranges;
+}
+
 bool la_sizes_ok(int64_t T, int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t dv) {
     return N >= 0 && T >= 0 && H > 0 && Hk > 0 && H % Hk == 0 && (T == 0 || N > 0) &&
            T < ((int64_t)1 << 31) && T <= ((int64_t)1 << 40) / ((int64_t)H * (dk > dv ? dk : dv)) &&
@@ -172,7 +180,8 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
         la_tensor_maps(maps, q, k, v, o, initial_state, final_state, L.split ? bnd : nullptr, p,
                        total_tokens, dk, dv, q_stride, k_stride, v_stride) != cudaSuccess)
         return KDA_ERR_CUDA;
-    const bool whole = L.ranges == sm_count();
+    // With two column blocks a range, one wave of CTAs: see launch_dims
+    const bool whole = busy_ranges(L, total_tokens, num_seqs, H) * 2 > sm_count();
     auto pass = [&](bool out) {
         if (dtype == KDA_BF16)
             return launch_la_tc(out, p, maps, g, g_per_token, initial_state != nullptr,

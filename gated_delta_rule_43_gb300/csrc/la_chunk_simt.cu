@@ -500,10 +500,12 @@ static cudaError_t launch_columns(bool out, const Plan &p, const float *q, const
     return cudaGetLastError();
 }
 
-// Columns in blocks of at most 64, a CTA each; or, where there are as many ranges as SMs, all
-// columns in one, so that the scores are formed once (20 sequences of 500 tokens, 8 heads of
-// 128 x 128: 273 us, 360 in blocks; 3 of 1000, 37 and 513, 4 heads of 64 x 128: 45 and 49; with
-// fewer ranges the blocks keep more SMs busy).
+// Columns in blocks of at most 64, a CTA each; or, where two blocks of every range that holds work
+// would be more CTAs than SMs, all columns in one, so that the scores are formed once.  (All, in
+// blocks: 20 sequences of 500 tokens, 8 heads of 128 x 128: 267 us, 360; 3 of 1000, 37 and 513, 4
+// heads of 64 x 128, 96 busy ranges: 39, 41; 4 of 300, 4 heads of 128 x 128, 80 busy: 43, 53; one of
+// 2500, 2 heads, 78 busy: 63, 70.  With fewer, blocks keep more SMs busy: one of 2432, 76 busy: 52,
+// 42; one of 600, 8 heads, 72 busy: 54, 42.)
 template <int DK, int DV, typename... A>
 static cudaError_t launch_dims(bool whole, A... args) {
     if (DV > 64 && whole) return launch_columns<DK, DV, DV>(args...);

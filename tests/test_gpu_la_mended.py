@@ -40,3 +40,35 @@ def test_sequences_beside_an_offending_one_are(dtype):
     ro, _ = U.la_ref(*(x.cpu() for x in (q[:100], k[:100], v[:100], g[:100])),
                      torch.tensor([0, 100]), h0[:1].cpu())
     assert U.rel(o[:100], ro) <= U.TOL_O[dtype] and (o[100:] == 7).all()
+
+
+def time_of(args, calls=20, turns=20):
+    """The least time of a call, in us, of calls replayed from a graph."""
+    q, k, v, g, cu, h0 = gpu(*args)
+    o, S = torch.empty_like(v), torch.empty_like(h0)
+    N, H, dk, dv = h0.shape
+    ws = kda.alloc_workspace(kda.load().kda_la_chunk_fwd_workspace_size(
+        q.shape[0], N, H, q.shape[1], dk, dv, kda._DT[q.dtype]), DEV)
+    call = lambda: kda.la_chunk_fwd(q, k, v, g, cu, h0, o=o, final_state=S, workspace=ws)  # noqa: E731
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(calls):
+            call()
+    best = float("inf")
+    for _ in range(turns):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) / calls * 1e3)
+    return best
+
+
+def test_column_blocks_where_few_ranges_hold_work():
+    """One sequence of 600 tokens and 8 heads has as many ranges as SMs by its size and work for
+    72 of them: it takes about as long as one of 575 tokens (one chunk in 18 less, and one piece
+    in nine of two chunks instead of three: up to 1.3), not 1.6 times as long."""
+    short, longer = (time_of(U.make([n], 8, 8, 128, 128, F32, seed=5)) for n in (575, 600))
+    assert longer <= 1.4 * short
