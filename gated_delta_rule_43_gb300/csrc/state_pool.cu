@@ -30,7 +30,7 @@ __device__ __forceinline__ void copy_part(float4 *dst, const float4 *src, int64_
 
 // Copy i = task / parts of n, its part task % parts: a CTA a task.  A copy whose indices break
 // the rules is left out: every CTA looks through the n indices for another copy with this
-// destination, or one that reads it.
+// destination, or one that reads it (which a copy of a slot to itself does not disturb).
 __global__ void __launch_bounds__(kThreads)
 copy_kernel(float4 *__restrict__ pool, int P, int64_t vecs, const int32_t *__restrict__ src_idx,
             const int32_t *__restrict__ dst_idx, int n, int parts, int64_t per, StatusWord *st) {
@@ -38,7 +38,7 @@ copy_kernel(float4 *__restrict__ pool, int P, int64_t vecs, const int32_t *__res
     const int src = src_idx[i], dst = dst_idx[i];
     bool bad = src < -1 || src >= P || dst < 0 || dst >= P;
     for (int m = threadIdx.x; m < n && !bad; m += kThreads)
-        bad = m != i && (dst_idx[m] == dst || src_idx[m] == dst);
+        bad = m != i && (dst_idx[m] == dst || (src_idx[m] == dst && src != dst));
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0 && part == 0) report(st, KDA_ERR_INVALID_ARG, i, 32);
         return;

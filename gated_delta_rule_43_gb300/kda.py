@@ -686,9 +686,9 @@ def _check_pool(pool):
 def state_pool_copy(pool, src_idx, dst_idx, *, workspace=None, stream=None, check: bool = False):
     """Slot dst_idx[i] of the pool [P, ...] fp32 becomes slot src_idx[i], or zeros where
     src_idx[i] is -1 (kda_state_pool_copy): copies, forks and clears.  No destination may be
-    named twice or be another copy's source; copies that break this or leave the pool are
-    left out, and recorded in the workspace's status word when there is one (check=True
-    raises)."""
+    named twice or be another copy's source (a slot copied to itself may be); copies that
+    break this or leave the pool are left out, and recorded in the workspace's status word
+    when there is one (check=True raises)."""
     lib = _lib or load()
     slots, elems = _check_pool(pool)
     if src_idx.dim() != 1:

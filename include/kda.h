@@ -426,7 +426,8 @@ size_t kda_state_pool_workspace_size(int32_t P);
  * that breaks this (each of those that share a destination; the one whose destination is
  * read by another), or whose index lies outside the pool, is left out and recorded as
  * KDA_ERR_INVALID_ARG (info = i) in the workspace's status word when a workspace (>=
- * kda_decode_workspace_size() bytes) is given.  src == dst is a copy that does nothing.
+ * kda_decode_workspace_size() bytes) is given.  src == dst is a copy that does nothing; others
+ * may read that slot, but not write it.
  */
 kda_status kda_state_pool_copy(float *pool, int32_t P, int64_t slot_elems,
                                const int32_t *src_idx, const int32_t *dst_idx, int32_t n,

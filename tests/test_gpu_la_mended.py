@@ -72,3 +72,21 @@ def test_column_blocks_where_few_ranges_hold_work():
     in nine of two chunks instead of three: up to 1.3), not 1.6 times as long."""
     short, longer = (time_of(U.make([n], 8, 8, 128, 128, F32, seed=5)) for n in (575, 600))
     assert longer <= 1.4 * short
+
+
+def idx(*x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def test_a_fork_may_include_its_own_slot():
+    """3 -> 3 does nothing and disturbs nobody who reads slot 3."""
+    pool = torch.randn(8, 2, 32, 32, device=DEV)
+    want = pool.clone()
+    want[5], want[0] = want[3], want[3]
+    kda.state_pool_copy(pool, idx(3, 3, 3, 7), idx(3, 5, 0, 7), check=True)
+    assert torch.equal(pool, want)
+    with pytest.raises(kda.KdaError) as e:   # but 1 -> 3 would write it
+        kda.state_pool_copy(pool, idx(3, 1, 4), idx(3, 3, 6), check=True)
+    want[6] = want[4]
+    assert e.value.code == kda.KDA_ERR_INVALID_ARG and e.value.info in (0, 1)
+    assert torch.equal(pool, want)
