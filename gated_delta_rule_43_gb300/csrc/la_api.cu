@@ -34,7 +34,8 @@ cudaError_t launch_qk(int dtype, int D, const void *q, const void *k, void *qo, 
                       float q_scale, float k_scale, const int32_t *pos, const float *inv_freq,
                       int rot, int interleaved, float rope_scale, int sms, cudaStream_t s);
 cudaError_t launch_pool_copy(float *p, int P, int64_t elems, const int32_t *src,
-                             const int32_t *dst, int n, StatusWord *st, cudaStream_t s);
+                             const int32_t *dst, int n, uint32_t *marks, StatusWord *st,
+                             cudaStream_t s);
 cudaError_t launch_pool_compact(float *p, int P, int64_t elems, const uint8_t *live,
                                 int32_t *new_index, int32_t *n_live, int32_t *moves, int sms,
                                 cudaStream_t s);
@@ -300,13 +301,18 @@ kda_status kda_state_pool_copy(float *pool, int32_t P, int64_t slot_elems,
     if (!pool_ok(pool, P, slot_elems) || n < 0 || n > (1 << 24)) return KDA_ERR_INVALID_ARG;
     if (n > 0 && (!src_idx || !dst_idx || !aligned(src_idx, 4) || !aligned(dst_idx, 4)))
         return KDA_ERR_INVALID_ARG;
+    // Without room for marks the check of the copies against each other is quadratic: 2^16 of them
+    // take 10 ms
+    const bool room = workspace && workspace_bytes >= kda_state_pool_workspace_size(P);
+    if (n > (1 << 16) && !room) return KDA_ERR_INVALID_ARG;
     if (workspace && (workspace_bytes < kHeaderBytes || !aligned(workspace, 256)))
         return KDA_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     if (workspace && cudaMemsetAsync(workspace, 0, sizeof(StatusWord), s) != cudaSuccess)
         return KDA_ERR_CUDA;
     if (n == 0) return KDA_OK;
-    return cuda_status(launch_pool_copy(pool, P, slot_elems, src_idx, dst_idx, n,
+    uint32_t *marks = room ? (uint32_t *)((uint8_t *)workspace + kHeaderBytes) : nullptr;
+    return cuda_status(launch_pool_copy(pool, P, slot_elems, src_idx, dst_idx, n, marks,
                                         (StatusWord *)workspace, s));
 }
 

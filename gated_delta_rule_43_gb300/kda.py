@@ -688,7 +688,8 @@ def state_pool_copy(pool, src_idx, dst_idx, *, workspace=None, stream=None, chec
     src_idx[i] is -1 (kda_state_pool_copy): copies, forks and clears.  No destination may be
     named twice or be another copy's source (a slot copied to itself may be); copies that
     break this or leave the pool are left out, and recorded in the workspace's status word
-    when there is one (check=True raises)."""
+    when there is one (check=True raises).  More than 65536 copies need one of
+    kda_state_pool_workspace_size(P) bytes where one is given."""
     lib = _lib or load()
     slots, elems = _check_pool(pool)
     if src_idx.dim() != 1:
@@ -698,8 +699,10 @@ def state_pool_copy(pool, src_idx, dst_idx, *, workspace=None, stream=None, chec
     da = _dense("dst_idx", dst_idx, (n,), torch.int32)
     device = _same_gpu(pool, src_idx, dst_idx, workspace)
     wa, wb = None, 0
-    if workspace is not None or check:
-        workspace, wa, wb = _workspace(pool, lib.kda_decode_workspace_size(), workspace, stream)
+    many = n > 2048   # room for a mark a slot: checked against each other in linear time
+    if workspace is not None or check or many:
+        need = lib.kda_state_pool_workspace_size(slots) if many else lib.kda_decode_workspace_size()
+        workspace, wa, wb = _workspace(pool, need, workspace, stream)
     rc = lib.kda_state_pool_copy(pool.data_ptr(), slots, elems, sa, da, n, wa, wb,
                                  _raw_stream(stream, device))
     if rc != KDA_OK:

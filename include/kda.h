@@ -415,7 +415,8 @@ kda_status kda_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_o
                             float k_scale, const int32_t *positions, const float *inv_freq,
                             int32_t rot_dim, int32_t layout, float rope_scale, void *stream);
 
-/* Bytes of workspace kda_state_pool_compact needs for a pool of P slots. */
+/* Bytes of workspace kda_state_pool_compact, and kda_state_pool_copy for many copies, need for a
+ * pool of P slots. */
 size_t kda_state_pool_workspace_size(int32_t P);
 
 /*
@@ -427,7 +428,8 @@ size_t kda_state_pool_workspace_size(int32_t P);
  * read by another), or whose index lies outside the pool, is left out and recorded as
  * KDA_ERR_INVALID_ARG (info = i) in the workspace's status word when a workspace (>=
  * kda_decode_workspace_size() bytes) is given.  src == dst is a copy that does nothing; others
- * may read that slot, but not write it.
+ * may read that slot, but not write it.  The copies are checked against each other in linear time
+ * where the workspace has kda_state_pool_workspace_size(P) bytes; without, n is at most 65536.
  */
 kda_status kda_state_pool_copy(float *pool, int32_t P, int64_t slot_elems,
                                const int32_t *src_idx, const int32_t *dst_idx, int32_t n,

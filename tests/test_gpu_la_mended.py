@@ -90,3 +90,35 @@ def test_a_fork_may_include_its_own_slot():
     want[6] = want[4]
     assert e.value.code == kda.KDA_ERR_INVALID_ARG and e.value.info in (0, 1)
     assert torch.equal(pool, want)
+
+
+@pytest.mark.parametrize("n", [2048, 2049, 20000, 100000])
+def test_many_copies_with_some_that_break_the_rules(n):
+    """Beyond some thousand copies they are checked by marks, with the same answers."""
+    P = 2 * n
+    gen = torch.Generator().manual_seed(n)
+    p = torch.randperm(P, generator=gen).to(torch.int32)
+    src, dst = p[:n].clone(), p[n:].clone()
+    src[:50] = dst[:50]                      # to themselves
+    src[50:60] = dst[:10]                    # ... and read by others
+    src[100:200] = -1                        # cleared
+    src[200], src[201], dst[202], dst[203] = P, -2, -1, P
+    dst[300] = dst[301]                      # one destination twice
+    src[400] = dst[401]                      # 401 writes what 400 reads
+    bad = {200, 201, 202, 203, 300, 301, 401}
+    pool = torch.randn(P, 8, generator=gen)
+    want = pool.clone()
+    good = torch.ones(n, dtype=torch.bool)
+    good[list(bad)] = False
+    s, d = src[good].long(), dst[good].long()
+    want[d] = torch.where((s >= 0)[:, None], pool[s.clamp_min(0)], torch.zeros(()))
+    pool = pool.to(DEV)
+    with pytest.raises(kda.KdaError) as e:
+        kda.state_pool_copy(pool, src.to(DEV), dst.to(DEV), check=True)
+    assert e.value.code == kda.KDA_ERR_INVALID_ARG and e.value.info in bad
+    assert torch.equal(pool.cpu(), want)
+    pool.copy_(torch.randn(P, 8, generator=gen))
+    want = pool.cpu()
+    want[d] = torch.where((s >= 0)[:, None], want[s.clamp_min(0)], torch.zeros(()))
+    kda.state_pool_copy(pool, src[good].to(DEV), dst[good].to(DEV), check=True)
+    assert torch.equal(pool.cpu(), want)
