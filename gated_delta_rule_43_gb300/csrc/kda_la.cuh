@@ -59,6 +59,7 @@ struct Plan {
     int in_place;             // the final states overwrite the initial ones
     int compose;              // no scan: ranges put their start states together themselves
     uint32_t *flags;          // states handed on, as the states of the cuts; then the CTAs begun (or null)
+    int left_out;             // tests: the range (times lanes, plus lane) whose first load of keys is left out, or -1
 };
 
 // The chunks [c0, c1) of one unit.

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "kda_la.cuh"
@@ -110,6 +111,9 @@ int64_t busy_ranges(const LaLayout &L, int64_t T, int32_t N, int32_t H) {
     return pieces < L.ranges ? pieces : L.ranges;
 }
 
+// Test hook (kda_test_la_fault): what the next call leaves out.
+std::atomic<int> g_la_left_out{-1};
+
 bool la_sizes_ok(int64_t T, int32_t N, int32_t H, int32_t Hk, int32_t dk, int32_t dv) {
     return N >= 0 && T >= 0 && H > 0 && Hk > 0 && H % Hk == 0 && (T == 0 || N > 0) &&
            T < ((int64_t)1 << 31) && T <= ((int64_t)1 << 40) / ((int64_t)H * (dk > dv ? dk : dv)) &&
@@ -167,8 +171,10 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
     // be gone by then; the scan keeps copies.
     const bool in_place = initial_state && initial_state == final_state;
     const bool compose = dtype == KDA_BF16 && !in_place && L.ranges * L.lanes / H + 1 <= 12;
+    const int left_out = dtype == KDA_BF16 ? g_la_left_out.exchange(-1) : -1;
     const la::Plan p{cu_seqlens, off, cuts, num_seqs, H, Hk, L.lanes, L.ranges, L.chunk,
-                     in_place, compose, L.flags ? (uint32_t *)(ws + L.flag_off) : nullptr};
+                     in_place, compose, L.flags ? (uint32_t *)(ws + L.flag_off) : nullptr,
+                     left_out};
     // A unit's states cost about as much as a chunk each (64 KB in, 64 KB out; measured on 16
     // packed sequences: 11.6k cycles beside 5.4k of a chunk).
     const int unit_cost = (initial_state ? 1 : 0) + (final_state ? 1 : 0);
@@ -197,6 +203,12 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     return cuda_status(pass(true));
+}
+
+kda_status kda_test_la_fault(int32_t part) {
+    if (part < -1) return KDA_ERR_INVALID_ARG;
+    g_la_left_out = part;
+    return KDA_OK;
 }
 
 static kda_status la_decode_impl(const void *q, const void *k, const void *v, const float *g,

@@ -60,7 +60,8 @@ constexpr int C = kTcChunk;
 constexpr int kThreads = 512;
 constexpr int kRowWarps = 4, kStateWarps = 8;
 constexpr int kMmaWarp = 12, kLoadWarp = 13, kGateWarp = 14, kStoreWarp = 15;
-constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint64_t kHandedNs = 1000000000ull;   // limit of the wait for a state that is handed on
+constexpr uint64_t kDrainNs = 100000000ull;     // ... for what a CTA that gives up has in flight
 
 // What one chunk's decays give, for one stage.
 struct Gates {
@@ -194,11 +195,13 @@ __device__ __forceinline__ void split2(uint32_t x, uint2 w, uint32_t &hi, uint32
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// Waits that end: a limited number of tries (each may sleep in hardware, none is shorter than
-// 20 cycles: at least 20 ms).  Small code, for there are many of them.
+// Waits that end, after two seconds or a little more: what is behind the wait for a state that is
+// handed on gives up after it.
 struct Waits {
     uint32_t bar;   // shared-memory address of the first barrier
-    __device__ __forceinline__ bool operator()(int which, uint32_t parity) const {
+    // A whole warp on one barrier: its tries sleep in hardware (3.7 us, measured where nothing
+    // arrives), so they are counted: 2.2 s.  Small code, for there are many of them.
+    __device__ __forceinline__ bool warp(int which, uint32_t parity) const {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p, q;\n\t.reg .u32 i;\n\t"
@@ -207,29 +210,55 @@ struct Waits {
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "@p bra done_%=;\n\t"
             "add.u32 i, i, 1;\n\t"
-            "setp.lt.u32 q, i, 2000000;\n\t"
+            "setp.lt.u32 q, i, 600000;\n\t"
             "@q bra again_%=;\n"
             "done_%=:\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
             : "r"(bar + 8 * which), "r"(parity)
             : "memory");
-        return ok != 0;
-    }
-    // the same for a whole warp
-    __device__ __forceinline__ bool warp(int which, uint32_t parity) const {
-        return __all_sync(0xffffffffu, (*this)(which, parity));
+        return __all_sync(0xffffffffu, ok != 0);
     }
     // Several at a time, a lane each: beside the products' reads of shared memory each look at a
-    // barrier takes 200 cycles, so they are not taken in turn.
+    // barrier takes 200 cycles, so they are not taken in turn.  Such tries do not sleep (70 to 100
+    // ns each), so time is what is counted: t counts tries in its lowest 8 bits, every 256th looks
+    // at the clock, and the first look stands in the bits above.  (In all waits this is too much code
+    // for the instruction cache: packed prompts 8% slower.)
+    __device__ __forceinline__ bool lanes(int which, uint32_t parity) const {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 t, now;\n\t"
+            "mov.u32 t, 0;\n"
+            "again_%=:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "@p bra done_%=;\n\t"
+            "add.u32 t, t, 1;\n\t"
+            "and.b32 now, t, 255;\n\t"
+            "setp.ne.u32 q, now, 0;\n\t"
+            "@q bra again_%=;\n\t"
+            "mov.u32 now, %%globaltimer_lo;\n\t"
+            "setp.eq.u32 q, t, 256;\n\t"
+            "@q and.b32 t, now, 0xffffff00;\n\t"
+            "sub.u32 now, now, t;\n\t"
+            "setp.lt.u32 q, now, 2000000000;\n\t"
+            "@q bra again_%=;\n"
+            "done_%=:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar + 8 * which), "r"(parity)
+            : "memory");
+        return __all_sync(0xffffffffu, ok != 0);
+    }
     __device__ __forceinline__ bool warp(int w0, uint32_t p0, int w1, uint32_t p1) const {
         const bool one = threadIdx.x & 1;
-        return warp(one ? w1 : w0, one ? p1 : p0);
+        return lanes(one ? w1 : w0, one ? p1 : p0);
     }
     __device__ __forceinline__ bool warp(int w0, uint32_t p0, int w1, uint32_t p1, int w2, uint32_t p2,
                                          int w3, uint32_t p3) const {
-        const bool two = threadIdx.x & 2;
-        return warp(two ? w2 : w0, two ? p2 : p0, two ? w3 : w1, two ? p3 : p1);
+        const bool one = threadIdx.x & 1, two = threadIdx.x & 2;
+        const int wa = two ? w2 : w0, wb = two ? w3 : w1;
+        const uint32_t pa = two ? p2 : p0, pb = two ? p3 : p1;
+        return lanes(one ? wb : wa, one ? pb : pa);
     }
 };
 
@@ -790,7 +819,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         uint32_t flag;
                         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(flag) : "l"(p.flags + start.index(s)) : "memory");
                         there = flag != 0;
-                        if ((i & 63u) == 0 && globaltimer_ns() - t0 > kWaitNs) break;
+                        if ((i & 63u) == 0 && globaltimer_ns() - t0 > kHandedNs) break;
                     }
                     ok = __all_sync(0xffffffffu, there);
                     if (!ok) return;
@@ -805,7 +834,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                         tma_load_3d(sm + sb * M::kQK + x * dk * 128, start.in_bnd(s) ? &tbnd : &th0, 32 * x,
                                     0, start.index(s), full);
                 }
-                ++issued_k;
+                issued_k = fs + 1;
                 start_in |= 1u << sb;
                 __syncwarp();
             }
@@ -816,14 +845,14 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                 ok = behind_start(sb);
                 if (ok && si >= 2) ok = wait.warp(kFreeK + sb, before);
                 if (!ok) break;
-                if (lane == 0) {
+                if (lane == 0 && !(gi == 0 && range * p.lanes + side == p.left_out)) {
                     uint64_t *full = &bar[kFullK + sb];
                     mbar_arrive_expect_tx(full, M::kK);
 #pragma unroll
                     for (int x = 0; x < DKP / 64; ++x)
                         tma_load_3d(qk + M::kK + x * 16384, &tk, 64 * x, hk, t0, full);
                 }
-                ++issued_k;
+                issued_k = si + 1;
                 __syncwarp();
                 if (OUT) {
                     if (si >= 2) ok = wait.warp(kFreeQ + sb, before);
@@ -847,7 +876,7 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
                     for (int x = 0; x < DVP / 64; ++x)
                         tma_load_3d(sm + M::kV + b * M::kVBytes + x * 16384, &tv, 64 * x, h, t0, full);
                 }
-                ++issued_v;
+                issued_v = gi + 1;
                 __syncwarp();
             }
         });
@@ -1003,21 +1032,23 @@ la_chunk_tc_kernel(Plan p, const __grid_constant__ CUtensorMap tq,
     if (__syncthreads_or(!ok)) {
         // an expired wait: what is in flight ends (each wait bounded again) before the tensor
         // memory is released and the CTA leaves
+        tmem_st_wait();
+        tc_fence_before();
         if (warp == kMmaWarp) {
             tc_fence_after();   // (on a barrier whose role has stopped, at whichever phase it is)
             const uint32_t phase = mbar_try_wait(&bar[kEndFree], 0) ? 1 : 0;
             __syncwarp();
             if (elect_one()) umma_commit(&bar[kEndFree]);
             __syncwarp();
-            mbar_wait(&bar[kEndFree], phase, kWaitNs);
+            mbar_wait(&bar[kEndFree], phase, kDrainNs);
         }
         if (warp == kLoadWarp) {   // (only each stage's last load can be in flight)
             for (uint32_t x = issued_q >= 2 ? issued_q - 2 : 0; x < issued_q; ++x)
-                mbar_wait(&bar[kFullQ + (x & 1)], (x >> 1) & 1, kWaitNs);
+                mbar_wait(&bar[kFullQ + (x & 1)], (x >> 1) & 1, kDrainNs);
             for (uint32_t x = issued_k >= 2 ? issued_k - 2 : 0; x < issued_k; ++x)
-                mbar_wait(&bar[kFullK + (x & 1)], (x >> 1) & 1, kWaitNs);
+                mbar_wait(&bar[kFullK + (x & 1)], (x >> 1) & 1, kDrainNs);
             for (uint32_t x = issued_v >= 2 ? issued_v - 2 : 0; x < issued_v; ++x)
-                mbar_wait(&bar[kFullV + (x & 1)], (x >> 1) & 1, kWaitNs);
+                mbar_wait(&bar[kFullV + (x & 1)], (x >> 1) & 1, kDrainNs);
         }
         __syncthreads();
     }

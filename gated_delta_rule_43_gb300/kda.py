@@ -54,6 +54,7 @@ SIGNATURES = {
     "kda_la_chunk_fwd_workspace_size": (SZ, [I64, I32, I32, I32, I32, I32, I32]),
     "kda_la_chunk_fwd": (I32, [P, P, P, P, P, I32, I64, I32, I32, I32, I32, I32, I64, I64, I64,
                                I32, P, P, P, P, SZ, P]),
+    "kda_test_la_fault": (I32, [I32]),
     "kda_la_decode_step": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I64, I64, I64,
                                  I32, P]),
     "kda_la_decode_step_indexed": (I32, [P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32,

@@ -362,6 +362,15 @@ kda_status kda_la_chunk_fwd(const void *q, const void *k, const void *v, const f
                             size_t workspace_bytes, void *stream);
 
 /*
+ * Test hook for failure detection, as kda_test_chain_fault: in the next bf16 kda_la_chunk_fwd call
+ * of this process that launches anything, whoever works on part `part` of the row of chunks (0 ..;
+ * -1: nobody) leaves out its first load of keys.  Its waits then expire (2.2 s), the call reports
+ * KDA_ERR_TIMEOUT (info: a CTA whose wait expired), and the next call is as ever.
+ * KDA_ERR_INVALID_ARG for part < -1.
+ */
+kda_status kda_test_la_fault(int32_t part);
+
+/*
  * One token for each of N sequences against its state [N, H, dk, dv], updated in place.
  * g is [N, H] (g_per_token != 0) or [H].  Memory-bound: the state is read once and written
  * once.  g is used as it is (no range check; a NaN spreads as in the definition).

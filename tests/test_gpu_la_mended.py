@@ -1,4 +1,6 @@
 """Cases of the decayed linear attention and the state pool that were once answered wrongly."""
+import time
+
 import pytest
 import torch
 
@@ -122,3 +124,48 @@ def test_many_copies_with_some_that_break_the_rules(n):
     want[d] = torch.where((s >= 0)[:, None], want[s.clamp_min(0)], torch.zeros(()))
     kda.state_pool_copy(pool, src[good].to(DEV), dst[good].to(DEV), check=True)
     assert torch.equal(pool.cpu(), want)
+
+
+# What a call's waits are for: nothing but its own tiles; states at cuts formed by a first pass, put
+# together by the ranges behind or (in place) by a scan; states handed on from SM to SM.
+WAITS = {"whole": ([17, 1, 0, 150, 96], 8, 8, 128, False), "cuts": ([4000, 300], 4, 4, 128, False),
+         "scan": ([2900, 1300], 16, 4, 64, True),
+         "handed": ([1300, 1500, 1250, 0, 1700, 900, 1600, 1, 1100, 2000, 1290], 16, 16, 128, False)}
+
+
+@pytest.mark.parametrize("case", WAITS)
+def test_expired_waits_are_reported_and_the_next_call_is_clean(case):
+    """One CTA leaves out its first load of keys: its waits expire, after a second at least, the call
+    ends with KDA_ERR_TIMEOUT, and the next one on the same workspace is right."""
+    lens, H, Hk, D, in_place = WAITS[case]
+    args = U.make(lens, H, Hk, D, D, BF, seed=30, speed=0.01)
+    q, k, v, g, cu, h0 = gpu(*args)
+    lib = kda.load()
+    ws = kda.alloc_workspace(lib.kda_la_chunk_fwd_workspace_size(q.shape[0], len(lens), H, Hk, D, D,
+                                                                 kda.KDA_BF16), DEV)
+
+    def call():
+        s = h0.clone()
+        return kda.la_chunk_fwd(q, k, v, g, cu, s, final_state=s if in_place else None, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    part = 0
+    if case == "handed":   # the range before the first cut whose state is handed on: the plan's cuts
+        cuts = ws[256:256 + 48 * 153].view(torch.int32).view(-1, 12)   # stand behind the status word
+        handed = cuts[:, 10].nonzero()
+        assert len(handed)
+        part = int(handed[0]) - 1
+    assert lib.kda_test_la_fault(part) == kda.KDA_OK
+    t0 = time.perf_counter()
+    call()
+    code, info = kda.query_status(ws)
+    took = time.perf_counter() - t0
+    assert code == kda.KDA_ERR_TIMEOUT and 0 <= info < 1024
+    assert 1.0 <= took < 20.0
+    if case == "handed":   # the wait for what that CTA would have handed on ends before those behind it
+        site = int(ws[4:8].view(torch.int32).item())
+        assert site == 41 + 13   # (the load warp)
+    o, S = call()
+    assert kda.query_status(ws) == (kda.KDA_OK, 0)
+    ro, rS = U.la_ref(*args)
+    assert U.rel(o, ro) <= U.TOL_O[BF] and U.rel(S, rS) <= U.TOL_S
