@@ -18,7 +18,9 @@
 //
 // exp(G_t - G_s) is never a quotient of far-apart numbers: with R the value of G at the end
 // of the 32-token block of s, it is exp(G_t - R) exp(R - G_s), two factors of at most one,
-// for the blocks before that of t, and is formed token by token inside t's own block.
+// for the blocks before that of t, and is formed token by token inside t's own block.  A reset (-inf)
+// counts as -104 in G, so behind many of them its last bit is larger: 1e-4 of the outputs at a reset
+// every two tokens (emulated), against 2e-3 of their rounding to bf16.
 //
 // One CTA an SM walks its range (see kda_la.cuh), every role for itself through the same
 // items and chunks:
@@ -32,16 +34,17 @@
 // Two stages of q, k and v (32 KB each, each free as soon as its own readers are done) and the
 // 32 KB image of S fill the SM's shared memory; scores / P, O, K~^T V and K~^T (hi, lo) fill
 // its tensor memory.  Loops stay loops: the roles' code shares one instruction cache
-// (unrolled, a chunk took 13k cycles), and what a role keeps in registers stays below its 128
-// (local memory is shared by 512 threads in 28 KB of L1: next to nothing of it cost 20%).
+// (unrolled, a chunk took 13k cycles), and what a role keeps in registers stays near its 128 (the
+// compiler reports 60 bytes of spills a thread in the output kernels of 128 value columns; local memory
+// is shared by 512 threads in 28 KB of L1, and with the items' walk in it a call took 20% longer).
 //
 // What bounds it.  Outputs take 4.5k cycles a chunk: 2.6k of products on the tensor cores, among
 // dependent steps of 0.2 to 1.2k (scores -> P -> outputs; K~^T V -> S -> its image -> Q S).
 // Reading and writing the tiles alone takes 3.9k where four heads share queries and keys and
 // 6.0k where none do (6.2 TB/s), less what the first pass left in L2.  The first pass (K~^T V
 // only) takes 2.9k, its tiles at 6.4 TB/s.  Measured: 36k packed tokens of 32 heads on 8
-// query/key heads 199 us, 65536 tokens of 16 heads 272 us (first pass 98), 8192 tokens of 32 heads
-// 85 us (first pass 28, of which 6 before the first product).
+// query/key heads 203 us, 65536 tokens of 16 heads 277 us (first pass 100), 8192 tokens of 32 heads
+// 86 us (first pass 29, of which 6 before the first product).
 #include <cuda.h>
 #include <string.h>
 

@@ -10,14 +10,16 @@
 // them) of a few tokens: first each thread works out one angle's cosine and sine, which the
 // heads of a token share, into shared memory; then each warp goes through rows, the loads of several
 // rows in flight.  8192 tokens of 32 + 32 heads of 128 (268 MB): 50.0 us, 5.4 TB/s; a plain copy of
-// as much takes 43.  (Three CTAs an SM: with two 58 us, with four, in 64 registers, 63; two
+// as much takes 43.  In fp32 83 us, 6.4 TB/s, a copy 79.  With weights and rotated in neighbouring pairs
+// (half of each head) 65 and 120 us: every row reads its weights again.  (Three CTAs an SM: with two 58 us, with four, in 64 registers, 63; two
 // tokens a CTA 52.)
 //
 // The rotation's angle is a whole number of turns plus a fraction, and only the fraction
 // counts.  The rate in turns per position is held as a 64-bit binary fraction, so position *
 // rate modulo one turn is one integer product, exact but for the rate's own last bit
 // (2^-64 turns a position); a product in fp32 would be off by 0.06 rad at position 10^6.
-// The fraction itself is formed in integers too: 24 bits of inv_freq times 128 of 1 / (2 pi).
+// The fraction itself is formed in integers too: 24 bits of inv_freq times 128 of 1 / (2 pi), as in
+// Payne and Hanek's reduction (1983).
 #include "kda_common.cuh"
 
 namespace kda {

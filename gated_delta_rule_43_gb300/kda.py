@@ -598,8 +598,10 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str = "none",
     factor (positions are interpolated), "base" raises the base so that only the slowest
     rate is divided by it, and "parts" divides the rates that turn less than ``slow_turns``
     times over the original length, keeps those that turn more than ``fast_turns`` times,
-    and blends linearly in between; it returns rope_scale = 1 + 0.1 ln(factor), which
-    sharpens the scores of the longer context (1 for the others).
+    and blends in between, linearly in the number of turns; it returns rope_scale =
+    1 + 0.1 ln(factor), which sharpens the scores of the longer context (1 for the others).
+    A model that was trained with other rates (a blend linear in the channel's index, for
+    one) brings its own: qk_norm_rope takes any table.
     """
     if rot_dim < 0 or rot_dim % 2:
         raise ValueError("rot_dim must be even")

@@ -343,8 +343,12 @@ size_t kda_la_chunk_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, i
  * or, in long sequences, formed by a first pass over the tokens before the cut.  Inside its
  * share an SM goes through dense products over
  * chunks.  The result equals the token-by-token recurrence up to rounding: states are
- * accumulated and kept in fp32; with bf16 storage the scores and the copy of the state
- * that meets the queries are rounded to bf16 (the state that is carried on is not).
+ * accumulated and kept in fp32.  With bf16 storage the scores and the copy of the state
+ * that meets the queries are rounded to bf16.  The state that is carried on is not, but the keys
+ * with their decays enter it as sums of two bf16 (2^-17 of their value; final states 3e-6 to 4e-6 off
+ * in relative L2).  A v that is not finite makes the outputs of its whole chunk (128 tokens, 32 in
+ * fp32 storage, counted from the sequence's start) not finite, of that head, the tokens before it
+ * among them; earlier chunks, other heads and other sequences keep their values.
  *   initial_state, final_state  [num_seqs, H, dk, dv] fp32 or NULL; may be the same buffer
  * Sizes: total_tokens below 2^31, and at most 2^31 - 1 chunks of 32 tokens over all heads.
  * Device-found errors: KDA_ERR_SEQLENS (the offending sequence is skipped; all are where the

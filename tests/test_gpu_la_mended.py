@@ -169,3 +169,19 @@ def test_expired_waits_are_reported_and_the_next_call_is_clean(case):
     assert kda.query_status(ws) == (kda.KDA_OK, 0)
     ro, rS = U.la_ref(*args)
     assert U.rel(o, ro) <= U.TOL_O[BF] and U.rel(S, rS) <= U.TOL_S
+
+
+@pytest.mark.parametrize("dtype,chunk", [(BF, 128), (F32, 32)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_value_that_is_not_finite_stays_in_its_chunk_and_head(dtype, chunk, bad):
+    """Chunks are products: zeros meet such a value too.  What lies before its chunk, and other heads,
+    are right."""
+    args = list(U.make([300, 70], 2, 1, 64, 64, dtype, seed=8, speed=0.05))
+    ro, rS = U.la_ref(*args)
+    args[2][200, 1] = bad
+    o, S = kda.la_chunk_fwd(*gpu(*args), check=True)
+    first = 200 // chunk * chunk
+    assert U.rel(o[:first], ro[:first]) <= U.TOL_O[dtype]
+    assert U.rel(o[:, 0], ro[:, 0]) <= U.TOL_O[dtype] and U.rel(S[:, 0], rS[:, 0]) <= U.TOL_S
+    assert U.rel(o[300:], ro[300:]) <= U.TOL_O[dtype] and U.rel(S[1], rS[1]) <= U.TOL_S
+    assert not torch.isfinite(o[200:300, 1]).any()
