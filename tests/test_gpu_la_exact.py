@@ -55,3 +55,13 @@ def test_single_precision_of_resets_in_a_long_sequence():
     args[3][::7, 0] = -float("inf")
     args[3][5::300, 1] = -float("inf")
     check(args)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [1023, 1024, 1025, 3000])
+def test_more_sequences_than_the_plan_keeps_beside_it(dtype, N):
+    """The plan's sums stand in shared memory up to 1024 sequences, behind the workspace's header
+    beyond."""
+    lens = [(7 * n) % 5 for n in range(N)]
+    lens[N // 2], lens[-1] = 700, 130
+    check(U.make(lens, 2, 1, 32, 32, dtype, seed=N, speed=0.2))
