@@ -1,0 +1,823 @@
+// paged_attn_tc.cu -- attention of a chunk of new tokens over paged keys and values on the sm_103a
+// tensor cores (bf16 operands, fp32 accumulation), heads of 64 and 128.
+//
+//   S = Q K^T;   m_i the running maximum of a row;   P = 2^(f S - f m), f = scale log2(e)
+//   O = sum over blocks of P V,   l = sum of P,   o = O / l
+// The query heads that share a key/value head are rows beside each other (row = token * group + head), so
+// that a block of keys is read once for all of them: an item is 256 such rows of one sequence and
+// key/value head, in two tiles of 128, and goes through the blocks of 128 keys that it sees.  4 D flops a
+// row and key against 4 D bytes a key: with 256 rows a block takes 2048 cycles of products and 64 KB.
+//
+// The running maximum only moves when it would grow by more than 2^8: until then P is up to 256 times
+// larger than it could be, which neither bf16 nor the fp32 sums mind, and O is not rescaled.
+//
+// The work.  A plan lists the tiles of all sequences, with the blocks that each sees, heads inside tiles, in
+// one row and cuts it into equal ranges, one an SM, wherever that falls: with few rows against a
+// long context the SMs share the keys of one item.  What a cut leaves on both sides is kept in the
+// workspace (O, m, l in fp32) and joined by a second kernel.
+//
+// One CTA an SM:
+//   warps 0-3, 4-7   the rows of the two tiles: scores out of tensor memory, P into it (over the scores of
+//                    the keys from 64 on), outputs; the next item's queries into the place of this one's after the last scores
+//   warp 8           issues the products        warp 9    loads keys and values, page by page
+//   warp 10          goes through the range's items for everyone
+//   warp 11          zeroes the values behind a sequence's end (slots that nobody has written)
+// Products of one tile run while the other's scores become weights: P0 V, Q0 K', P1 V, Q1 K', ...
+#include "kda_paged_tc.cuh"
+
+namespace kda {
+namespace paged {
+namespace tc {
+
+constexpr int BK = 128;             // keys of a block
+constexpr int kRows = 256;          // rows of an item
+constexpr int kThreads = 384;
+constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kEndWarp = 11;
+constexpr int kItemCost = 2;        // an item's queries and outputs, in blocks
+constexpr int kUncut = 6;           // blocks of an item that is not cut
+constexpr int kRing = 4;            // items known ahead
+constexpr float kGrow = 8.f;        // log2 of what the maximum may grow before O is rescaled
+
+// A place in the row of blocks: before block k of the blocks that head h of tile `tile` (the t-th of
+// sequence n) sees.  k > 0: inside an item.
+struct Cut {
+    int32_t tile, n, t, h, k;
+};
+__device__ __forceinline__ bool same_item(const Cut &a, const Cut &b) { return a.tile == b.tile && a.h == b.h; }
+
+struct Plan {
+    int32_t *tiles;           // [N + 1]: tiles of the sequences before n
+    int64_t *cost;            // [tiles + 1]: that of the tiles before
+    Cut *cuts;                // [ranges + 1]
+    float *part;              // [2 * ranges][rows][D]: what a cut leaves, behind a range's begin, before its end
+    float2 *ml;               // [2 * ranges][rows]
+    int ranges, rows;         // rows: of an item, at most
+    int64_t most;             // tiles that there is room for
+};
+
+// What everything about tile t of a sequence follows from.
+struct Tile {
+    Span s;
+    int row0, rows;           // of the sequence's len * group
+    int first, last;          // positions of the first and last row's tokens
+};
+__device__ __forceinline__ Tile tile_of(const Span &s, int t, int group) {
+    Tile r;
+    r.s = s;
+    r.row0 = t * kRows;
+    r.rows = (int)min((int64_t)kRows, (int64_t)s.len * group - r.row0);
+    r.first = s.pos + r.row0 / group;
+    r.last = s.pos + (r.row0 + r.rows - 1) / group;
+    return r;
+}
+__device__ __forceinline__ KeyBlocks blocks_of(const Tile &t, int window, int sinks) {
+    return key_blocks(max(0, t.first), t.last, window, sinks, BK);
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Inclusive sums over a block's threads; returns the total.
+template <typename T> __device__ __forceinline__ T block_scan(T &x, T *warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warps[warp] = x;
+    __syncthreads();
+    T before = 0, total = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before += warps[w];
+        total += warps[w];
+    }
+    x += before;
+    return total;
+}
+
+// The last n in [0, count) with a[n] <= x
+template <typename T> __device__ __forceinline__ int last_at_most(const T *a, int count, T x) {
+    int lo = 0, hi = count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+paged_plan_kernel(Cache c, Plan p, int group, int window, int sinks, StatusWord *st) {
+    __shared__ int64_t warps[kPlanThreads / 32];
+    let_next_start();
+    const int tid = threadIdx.x;
+    if (tid == 0) *st = StatusWord{0, 0, 0};
+    __syncthreads();
+    check_spans(c, st);
+    int64_t tiles = 0, rows = 0;
+    for (int n0 = 0; n0 < c.N; n0 += kPlanThreads) {
+        const int n = n0 + tid;
+        int64_t x = 0, len = 0;
+        if (n < c.N) {
+            len = span_of(c, n).len;
+            x = (len * group + kRows - 1) / kRows;
+        }
+        const int64_t mine = x, some = block_scan(x, warps);
+        if (n < c.N && tiles + x < ((int64_t)1 << 31)) p.tiles[n] = (int)(tiles + x - mine);
+        rows += block_scan(len, warps);
+        tiles += some;
+    }
+    // sequences that overlap (of a cu_seqlens that is not ascending, which has been reported): their
+    // work would have no bound
+    if (rows > c.T || tiles > p.most) tiles = 0;
+    if (tid == 0) p.tiles[c.N] = (int)tiles;
+    __syncthreads();
+    int64_t total = 0;
+    for (int64_t i0 = 0; i0 < tiles; i0 += kPlanThreads) {
+        const int64_t i = i0 + tid;
+        int64_t x = 0;
+        if (i < tiles) {
+            int n = last_at_most(p.tiles, c.N, (int)i);
+            const Tile t = tile_of(span_of(c, n), (int)i - p.tiles[n], group);
+            x = (int64_t)c.Hk * (kItemCost + blocks_of(t, window, sinks).count);
+        }
+        const int64_t mine = x, some = block_scan(x, warps);
+        if (i < tiles) p.cost[i] = total + x - mine;
+        total += some;
+    }
+    if (tid == 0) p.cost[tiles] = total;
+    __syncthreads();
+    // ranges of at least as much as an item that is not cut
+    const int64_t share = max((total + p.ranges - 1) / p.ranges, (int64_t)kUncut);
+    for (int i = tid; i <= p.ranges; i += kPlanThreads) {
+        const int64_t x = min((int64_t)i * share, total);
+        Cut cut{(int)tiles, c.N, 0, 0, 0};
+        if (x < total) {
+            cut.tile = last_at_most(p.cost, (int)tiles, x);
+            const int64_t rest = x - p.cost[cut.tile];
+            const int each = (int)((p.cost[cut.tile + 1] - p.cost[cut.tile]) / c.Hk), count = each - kItemCost;
+            cut.h = (int)(rest / each);
+            cut.k = (int)(rest - (int64_t)cut.h * each) - kItemCost;
+            bool next = false;   // to the item's nearer end
+            if (count <= kUncut) next = 2 * cut.k > count;
+            else if (cut.k > count - 2) next = true;
+            if (cut.k < 2 || next || count <= kUncut) cut.k = 0;
+            if (next && ++cut.h == c.Hk) {
+                cut.h = 0;
+                ++cut.tile;
+            }
+            if (cut.tile < tiles) {
+                cut.n = last_at_most(p.tiles, c.N, cut.tile);
+                cut.t = cut.tile - p.tiles[cut.n];
+            } else {
+                cut.n = c.N;
+            }
+        }
+        p.cuts[i] = cut;
+    }
+}
+
+// What the roles need of an item.
+struct alignas(16) Item {
+    int n;                    // -1: no more
+    int h, row0, rows;
+    int tok0, pos0;           // the sequence's first new token: its row of q, its position
+    int k0, k1;               // of the list of blocks
+    int k1a;                  // ... for the first tile, whose rows stand earlier
+    int sinks, from;          // the list (KeyBlocks)
+    int first, last;          // positions of the first and last token
+    int ctx;
+    int slot;                 // of Plan.part, or -1: the whole item
+    __device__ __forceinline__ int block(int k) const { return k < sinks ? k : from + k - sinks; }
+    __device__ __forceinline__ int end(int tile) const {
+        return tile == 0 ? k1a : rows > 128 ? k1 : k0;
+    }
+};
+
+template <int D> struct Map {
+    static constexpr uint32_t kTile = 128 * D * 2;           // of keys, values or a tile's queries
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr uint32_t kQ = 0, kKV = 2 * kTile;
+    static constexpr uint32_t kItems = kKV + kStages * kTile;
+    static constexpr uint32_t kBar = kItems + kRing * (uint32_t)sizeof(Item);
+    // barriers
+    static constexpr int kFull = 0, kFree = kStages, kQFull = 2 * kStages, kSReady = kQFull + 2,
+                         kPReady = kSReady + 2, kODone = kPReady + 2, kItemFull = kODone + 2,
+                         kItemFree = kItemFull + kRing, kFixAsked = kItemFree + kRing, kFixed = kFixAsked + 1,
+                         kDrain = kFixed + 1, kBars = kDrain + 1;
+    static constexpr uint32_t kSlot = kBar + kBars * 8, kBytes = kSlot + 16;
+    static_assert(sizeof(Item) % 8 == 0 && kBytes <= 232448 && kItems % 1024 == 0, "layout");
+};
+
+// Position in a ring of barriers: stage, and the parity of its fill.
+struct Ring {
+    uint32_t stage = 0, phase = 0;
+    __device__ __forceinline__ void step(uint32_t stages) {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                  const __nv_bfloat16 *__restrict__ q, int64_t q_stride, __nv_bfloat16 *__restrict__ o, int group,
+                  float scale, int window, int sinks, StatusWord *st) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    using M = Map<D>;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    let_next_start();
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + M::kBar);
+    Item *items = reinterpret_cast<Item *>(sm + M::kItems);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + M::kSlot);
+    const uint32_t base = smem_u32(sm), bars = base + M::kBar;
+    if (base & 1023u) {   // the operand images need their alignment
+        wait_for_previous();
+        if (tid == 0) report(st, KDA_ERR_CUDA, 0, 70);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < M::kStages; ++i) {
+            mbar_init(&bar[M::kFull + i], 1);
+            mbar_init(&bar[M::kFree + i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar[M::kQFull + i], 4);
+            mbar_init(&bar[M::kSReady + i], 1);
+            mbar_init(&bar[M::kPReady + i], 4);
+            mbar_init(&bar[M::kODone + i], 1);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&bar[M::kItemFull + i], 1);
+            mbar_init(&bar[M::kItemFree + i], kRowWarps + 3);
+        }
+        mbar_init(&bar[M::kFixAsked], 1);
+        mbar_init(&bar[M::kFixed], 1);
+        mbar_init(&bar[M::kDrain], 1);
+        fence_mbar_init();
+    }
+    constexpr uint32_t kCols = 512;
+    if (warp == kMmaWarp) {
+        tmem_alloc(tslot, kCols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        tma_prefetch_map(&tk);
+        tma_prefetch_map(&tv);
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    wait_for_previous();
+    bool ok = true;
+    auto wait = [&](int which, uint32_t parity) {
+        ok = ok && wait_warp(bars + 8 * which, parity);
+        return ok;
+    };
+    // Each role goes through the items for itself; role(item) returns with ok false when a wait expired.
+    auto each_item = [&](auto role) {
+        Ring at;
+        while (wait(M::kItemFull + at.stage, at.phase)) {
+            const Item &it = items[at.stage];   // (read where it is used: registers are few)
+            if (it.n < 0) break;
+            role(it);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[M::kItemFree + at.stage]);
+            at.step(kRing);
+            if (!ok) break;
+        }
+    };
+    Ring kv;            // fills of the ring of keys and values (keys, values, keys, ...)
+    uint32_t loads = 0; // (load warp) fills issued
+
+    if (warp < kRowWarps) {
+        const int tile = warp >> 2;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tSl = tmem + 128 * tile + lanes, tOl = tmem + 256 + D * tile + lanes;
+        const float f = scale * kLog2e;
+        uint32_t s_phase = 0, o_phase = 0;
+        // The queries of this warp's rows of the item at `at`: a row's address by its lane, its 16-byte
+        // pieces side by side.
+        auto load_queries = [&](const Ring &at) {
+            if (!wait(M::kItemFull + at.stage, at.phase)) return;
+            const Item &it = items[at.stage];
+            const int row = 128 * tile + 32 * (warp & 3);
+            if (it.n < 0 || it.end(tile) == it.k0) return;
+            if (row < it.rows) {
+                const int mine = it.row0 + min(row + lane, it.rows - 1), token = mine / group;
+                const int64_t from = (int64_t)(it.tok0 + token) * q_stride + (int64_t)(it.h * group + mine - token * group) * D;
+                constexpr int U = D / 8;   // pieces of a row
+#pragma unroll 4
+                for (int i = 0; i < U; ++i) {
+                    const int r = (32 * i + lane) / U, x = lane % U;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     base + M::kQ + tile * M::kTile + sw128_offset(32 * (warp & 3) + r, 8 * x, 128)),
+                                 "l"(q + __shfl_sync(0xffffffffu, from, r) + 8 * x)
+                                 : "memory");
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_proxy_async();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[M::kQFull + tile]);
+            __syncwarp();
+        };
+        Ring at_next;
+        load_queries(at_next);
+        each_item([&](const Item &it) {
+            at_next.step(kRing);
+            const int r = 128 * tile + 32 * (warp & 3) + lane;
+            const bool live = r - lane < it.rows, mine = r < it.rows;   // (of a whole warp; this row)
+            const int pos = it.pos0 + (it.row0 + min(r, it.rows - 1)) / group;
+            const int pos_lo = __shfl_sync(0xffffffffu, pos, 0), pos_hi = __shfl_sync(0xffffffffu, pos, 31);
+            const int lowest = window > 0 ? max(pos - window, -1) : -1;   // keys above it are in the window
+            const int end = it.end(tile);
+            float m = -INFINITY, l = 0.f;   // m: of the scores as they come
+            for (int k = it.k0; k < end; ++k) {
+                if (!wait(M::kSReady + tile, s_phase)) return;
+                s_phase ^= 1;
+                tc_fence_after();
+                if (live) {
+                    const int key0 = it.block(k) * BK;
+                    // are there keys that one of the warp's rows does not see?
+                    const bool edge = key0 + BK - 1 > pos_lo ||
+                                      (window > 0 && key0 <= pos_hi - window && key0 + BK - 1 >= sinks);
+                    const int upto = pos - key0, above = lowest - key0, first = sinks - key0;
+                    // scores of 32 keys, -inf where this row does not see the key
+                    auto hide = [&](float(&s)[32], int j0) {
+                        if (!edge) return;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            s[j] = j0 + j <= upto && (j0 + j > above || j0 + j < first) ? s[j] : -INFINITY;
+                    };
+                    float top = -INFINITY;
+                    auto highest = [&](const float(&s)[32]) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) top = max3(top, s[j], s[j + 1]);
+                    };
+                    float sa[32], sb[32];
+                    tmem_ld32(tSl, sa);
+                    tmem_ld32(tSl + 32, sb);
+                    tmem_ld_wait();
+                    hide(sa, 0);
+                    hide(sb, 32);
+                    highest(sa);
+                    highest(sb);
+                    tmem_ld32(tSl + 64, sa);
+                    tmem_ld32(tSl + 96, sb);
+                    tmem_ld_wait();
+                    hide(sa, 64);
+                    hide(sb, 96);
+                    highest(sa);
+                    highest(sb);
+                    if (k == it.k0) {
+                        m = top;
+                    } else if (__any_sync(0xffffffffu, mine && top > m && !((top - m) * f <= kGrow))) {
+                        const float grown = fmaxf(m, top);
+                        const float keep = m == grown ? 1.f : ex2((m - grown) * f);
+                        m = grown;
+                        l *= keep;
+#pragma unroll 1
+                        for (int j = 0; j < D; j += 16) {
+                            float x[16];
+                            uint32_t y[16];
+                            tmem_ld16(tOl + j, x);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * keep);
+                            tmem_st16(tOl + j, y);
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : -m * f;
+                    const float2 f2 = make_float2(f, f), ref2 = make_float2(ref, ref);
+                    float2 sum = make_float2(0.f, 0.f), sum1 = sum;
+                    // Weights of 32 keys, over scores that this row has read: those of the keys from 64 on
+                    // are in registers still, the others are read again (holding all 128 spills).
+                    auto weigh = [&](const float(&s)[32], int j0) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float2 x = fma2(make_float2(s[j], s[j + 1]), f2, ref2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            if (j & 2) sum1 = add2(sum1, x);
+                            else sum = add2(sum, x);
+                            w[j / 2] = pack2(x.x, x.y);
+                        }
+                        tmem_st16(tSl + 64 + j0 / 2, w);
+                    };
+                    weigh(sa, 64);
+                    tmem_ld32(tSl, sa);
+                    weigh(sb, 96);
+                    tmem_ld_wait();
+                    tmem_ld32(tSl + 32, sb);
+                    hide(sa, 0);
+                    weigh(sa, 0);
+                    tmem_ld_wait();
+                    hide(sb, 32);
+                    weigh(sb, 32);
+                    sum = add2(sum, sum1);
+                    l += sum.x + sum.y;
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[M::kPReady + tile]);
+                __syncwarp();
+            }
+            const bool any = end > it.k0;
+            load_queries(at_next);   // (the last scores are there: their queries have been read)
+            if (any) {
+                if (!wait(M::kODone + tile, o_phase)) return;
+                o_phase ^= 1;
+                tc_fence_after();
+            }
+            if (!live) return;
+            if (it.slot >= 0) {
+                const int64_t at = (int64_t)it.slot * p.rows + r;
+                if (mine) p.ml[at] = make_float2(m == -INFINITY ? 0.f : m * f, any ? l : 0.f);
+                if (any) {
+#pragma unroll 1
+                    for (int j = 0; j < D; j += 32) {
+                        float x[32];
+                        tmem_ld32(tOl + j, x);
+                        tmem_ld_wait();
+                        if (mine)
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<float4 *>(p.part + at * D + j + i) =
+                                    make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    }
+                }
+            } else {
+                const float inv = l != 0.f ? 1.f / l : 0.f;   // (no visible key: zeros)
+                const int token = pos - it.pos0, head = it.h * group + (it.row0 + r) - token * group;
+                __nv_bfloat16 *to = o + ((int64_t)(it.tok0 + token) * c.Hk * group + head) * D;
+#pragma unroll 1
+                for (int j = 0; j < D; j += 32) {
+                    float x[32];
+                    if (any) {
+                        tmem_ld32(tOl + j, x);
+                        tmem_ld_wait();
+                    }
+                    if (mine)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint4 u = make_uint4(0, 0, 0, 0);
+                            if (any && l != 0.f) {
+                                u.x = pack2(x[i] * inv, x[i + 1] * inv);
+                                u.y = pack2(x[i + 2] * inv, x[i + 3] * inv);
+                                u.z = pack2(x[i + 4] * inv, x[i + 5] * inv);
+                                u.w = pack2(x[i + 6] * inv, x[i + 7] * inv);
+                            }
+                            *reinterpret_cast<uint4 *>(to + j + i) = u;
+                        }
+                }
+            }
+            tc_fence_before();
+        });
+    } else {
+        if (warp == kEndWarp) {
+            uint32_t phase = 0;
+            each_item([&](const Item &it) {
+                // the values behind the sequence's end, in the last block that reaches past it
+                for (int k = it.k0; k < it.k1; ++k) {
+                    const int left = it.ctx - it.block(k) * BK;   // (only of the list's last block below 128)
+                    if (left < BK && (it.ctx & ((1 << c.shift) - 1)) != 0) {
+                        if (!wait(M::kFixAsked, phase)) return;
+                        phase ^= 1;
+                        Ring at = kv;
+                        for (int i = 0; i < 2 * (k - it.k0) + 1; ++i) at.step(M::kStages);
+                        constexpr int U = D / 8;   // 16-byte pieces of a row
+                        for (int x = left * U + lane; x < BK * U; x += 32)
+                            *reinterpret_cast<uint4 *>(sm + M::kKV + at.stage * M::kTile + sw128_offset(x / U, 8 * (x % U), BK)) =
+                                make_uint4(0, 0, 0, 0);
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[M::kFixed]);
+                        __syncwarp();
+                    }
+                }
+                for (int i = 0; i < 2 * (it.k1 - it.k0); ++i) kv.step(M::kStages);
+            });
+        } else if (warp == kMmaWarp) {
+            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, fix_phase = 0;
+            constexpr uint32_t id_s = idesc_bf16(128, BK, false, false), id_o = idesc_bf16(128, D, false, true);
+            const uint64_t dq0 = sdesc_sw128(base + M::kQ, 16, 1024), dk0 = sdesc_sw128(base + M::kKV, 16, 1024),
+                           dv0 = sdesc_sw128(base + M::kKV, BK * 128, 1024);
+            auto scores = [&](int tile, uint32_t stage) {   // S = Q K^T
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                    umma_bf16(tmem + 128 * tile, desc_add(dq0, tile * M::kTile + (s >> 2) * 16384 + (s & 3) * 32),
+                              desc_add(dk0, stage * M::kTile + (s >> 2) * 16384 + (s & 3) * 32), id_s, s > 0);
+            };
+            each_item([&](const Item &it) {
+                const int n0 = it.end(0) - it.k0, n1 = it.end(1) - it.k0, blocks = it.k1 - it.k0;
+                if (blocks == 0) return;
+                Ring key = kv;
+                if (!wait(M::kFull + key.stage, key.phase)) return;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if ((i ? n1 : n0) == 0) continue;
+                    if (!wait(M::kQFull + i, q_phase[i])) return;
+                    q_phase[i] ^= 1;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        scores(i, key.stage);
+                        umma_commit(&bar[M::kSReady + i]);
+                    }
+                    __syncwarp();
+                }
+                if (elect_one()) umma_commit(&bar[M::kFree + key.stage]);
+                __syncwarp();
+                for (int j = 0; j < blocks; ++j) {
+                    Ring val = key;
+                    val.step(M::kStages);
+                    key = val;
+                    key.step(M::kStages);
+                    if (!wait(M::kFull + val.stage, val.phase)) return;
+                    if (it.ctx - it.block(it.k0 + j) * BK < BK && (it.ctx & ((1 << c.shift) - 1)) != 0) {
+                        if (lane == 0) mbar_arrive(&bar[M::kFixAsked]);
+                        __syncwarp();
+                        if (!wait(M::kFixed, fix_phase)) return;
+                        fix_phase ^= 1;
+                    }
+                    bool key_there = false;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int n = i ? n1 : n0;
+                        if (j >= n) continue;
+                        if (!wait(M::kPReady + i, p_phase[i])) return;
+                        p_phase[i] ^= 1;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int s = 0; s < BK / 16; ++s)
+                                umma_bf16_ts(tmem + 256 + D * i, tmem + 128 * i + 64 + 8 * s, desc_add(dv0, val.stage * M::kTile + s * 2048), id_o,
+                                             j > 0 || s > 0);
+                            if (j + 1 == n) umma_commit(&bar[M::kODone + i]);
+                        }
+                        __syncwarp();
+                        if (j + 1 < n) {
+                            if (!key_there && !wait(M::kFull + key.stage, key.phase)) return;
+                            key_there = true;
+                            if (elect_one()) {
+                                scores(i, key.stage);
+                                umma_commit(&bar[M::kSReady + i]);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (elect_one()) {
+                        umma_commit(&bar[M::kFree + val.stage]);
+                        if (j + 1 < blocks) umma_commit(&bar[M::kFree + key.stage]);
+                    }
+                    __syncwarp();
+                }
+                kv = key;
+            });
+        } else if (warp == kLoadWarp) {
+            const int rows = min(BK, 1 << c.shift), boxes = BK / rows;
+            each_item([&](const Item &it) {
+                // the page that holds the rows of this lane's box in block k; -1: a row that nobody sees
+                auto page_of = [&](int k) {
+                    if (k >= it.k1 || lane >= boxes) return -1;
+                    const int key = it.block(k) * BK + lane * rows;
+                    const bool seen = key <= it.last && (window <= 0 || key < sinks ||
+                                                         key + rows > max(0, it.first) - window + 1);
+                    return seen ? c.table[(int64_t)it.n * c.width + (key >> c.shift)] : c.P;
+                };
+                int next = page_of(it.k0);
+                for (int k = it.k0; k < it.k1; ++k) {
+                    int page = next;
+                    next = page_of(k + 1);
+                    const int key = it.block(k) * BK + lane * rows;
+                    if (lane < boxes && (page < 0 || page > c.P || (page == c.P && key <= it.last &&
+                        (window <= 0 || key < sinks || key + rows > max(0, it.first) - window + 1)))) {
+                        report(st, KDA_ERR_INVALID_ARG, it.n, 71);
+                        page = c.P;   // (past the last: zeros)
+                    }
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        if (!wait(M::kFree + kv.stage, kv.phase ^ 1)) return;
+                        if (lane == 0) mbar_arrive_expect_tx(&bar[M::kFull + kv.stage], M::kTile);
+                        __syncwarp();
+                        if (lane < boxes) {
+#pragma unroll
+                            for (int x = 0; x < D / 64; ++x)
+                                tma_load_page(base + M::kKV + kv.stage * M::kTile + x * 16384 + lane * rows * 128, v ? &tv : &tk,
+                                              64 * x, key & ((1 << c.shift) - 1), it.h, page,
+                                              bars + 8 * (M::kFull + kv.stage));
+                        }
+                        __syncwarp();
+                        kv.step(M::kStages);
+                        ++loads;
+                    }
+                }
+            });
+        } else if (warp == kItemWarp) {
+            Ring at;
+            Cut from = p.cuts[blockIdx.x];
+            const Cut to = p.cuts[blockIdx.x + 1];
+            const int tiles = p.tiles[c.N];
+            Span s{0, 0, 0};
+            int known = -1;
+            while (true) {
+                const bool more = from.tile < tiles && (from.tile < to.tile || (from.tile == to.tile &&
+                                                        (from.h < to.h || (from.h == to.h && from.k < to.k))));
+                Item it;
+                it.n = -1;
+                if (more) {
+                    if (known != from.n) {
+                        s = span_of(c, from.n);
+                        known = from.n;
+                    }
+                    const Tile t = tile_of(s, from.t, group);
+                    const KeyBlocks kb = blocks_of(t, window, sinks);
+                    it.n = from.n;
+                    it.h = from.h;
+                    it.row0 = t.row0;
+                    it.rows = t.rows;
+                    it.tok0 = s.begin;
+                    it.pos0 = s.pos;
+                    it.k0 = from.k;
+                    it.k1 = same_item(from, to) ? min(to.k, kb.count) : kb.count;
+                    const int last = t.s.pos + (t.row0 + min(t.rows, 128) - 1) / group;
+                    it.k1a = last < 0 ? it.k0 : max(it.k0, min(it.k1, kb.sinks + last / BK + 1 - kb.from));
+                    it.sinks = kb.sinks;
+                    it.from = kb.from;
+                    it.first = t.first;
+                    it.last = t.last;
+                    it.ctx = s.pos + s.len;
+                    it.slot = it.k0 > 0 ? 2 * (int)blockIdx.x : it.k1 < kb.count ? 2 * (int)blockIdx.x + 1 : -1;
+                }
+                if (!wait(M::kItemFree + at.stage, at.phase ^ 1)) break;
+                if (lane == 0) {
+                    items[at.stage] = it;
+                    mbar_arrive(&bar[M::kItemFull + at.stage]);
+                }
+                __syncwarp();
+                if (!more) break;
+                at.step(kRing);
+                from.k = 0;
+                if (++from.h == c.Hk) {
+                    from.h = 0;
+                    ++from.tile;
+                    ++from.t;
+                    if (from.tile < tiles) {
+                        // the next sequence with tiles, 32 a step
+                        while (p.tiles[from.n + 1] <= from.tile) {
+                            const int n = from.n + 1 + lane;
+                            const uint32_t past = __ballot_sync(0xffffffffu, n < c.N && p.tiles[n + 1] <= from.tile);
+                            from.n += 1 + __popc(past);
+                            from.n = min(from.n, c.N - 1);
+                            from.t = 0;
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (!ok && lane == 0) report(st, KDA_ERR_TIMEOUT, blockIdx.x, 72 + warp);
+    if (__syncthreads_or(!ok)) {
+        // an expired wait: what is in flight ends (each wait bounded again) before the tensor memory is
+        // released and the CTA leaves
+        tmem_st_wait();
+        tc_fence_before();
+        if (warp == kMmaWarp) {
+            tc_fence_after();
+            if (elect_one()) umma_commit(&bar[M::kDrain]);
+            __syncwarp();
+            mbar_wait(&bar[M::kDrain], 0, kDrainNs);
+        }
+        if (warp == kLoadWarp)   // (only each stage's last load can be in flight)
+            for (uint32_t x = loads >= (uint32_t)M::kStages ? loads - M::kStages : 0; x < loads; ++x)
+                mbar_wait(&bar[M::kFull + x % M::kStages], (x / M::kStages) & 1, kDrainNs);
+        __syncthreads();
+    }
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+// What the cuts inside one item have left, put together: a CTA for 32 rows of the item that the cut is
+// the first inside of.
+template <int D>
+__global__ void __launch_bounds__(256)
+paged_join_kernel(Cache c, Plan p, __nv_bfloat16 *__restrict__ o, int group) {
+    constexpr int V = D / 32;
+    const int cut = blockIdx.x + 1, lane = threadIdx.x & 31;
+    wait_for_previous();
+    const Cut here = p.cuts[cut];
+    if (here.k == 0) return;
+    const Cut before = p.cuts[cut - 1];
+    if (same_item(here, before) && before.k > 0) return;
+    const Tile t = tile_of(span_of(c, here.n), here.t, group);
+    int last = cut;   // the last cut inside the item
+    while (last < p.ranges && p.cuts[last + 1].k > 0 && same_item(p.cuts[last + 1], here)) ++last;
+    for (int r = blockIdx.y * 32 + (threadIdx.x >> 5); r < min(t.rows, (int)blockIdx.y * 32 + 32); r += 8) {
+        const int64_t first = (int64_t)(2 * (cut - 1) + 1) * p.rows + r;
+        float2 a = p.ml[first];
+        float top = a.y != 0.f ? a.x : -INFINITY;
+        for (int i = cut; i <= last; ++i) {
+            const float2 b = p.ml[(int64_t)(2 * i) * p.rows + r];
+            if (b.y != 0.f) top = fmaxf(top, b.x);
+        }
+        float l = 0.f, x[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = 0.f;
+        for (int i = cut - 1; i <= last; ++i) {
+            const int64_t at = i < cut ? first : (int64_t)(2 * i) * p.rows + r;
+            const float2 b = p.ml[at];
+            if (b.y == 0.f) continue;   // (its sums may be anything)
+            const float e = ex2(b.x - top);
+            l += e * b.y;
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] += e * p.part[at * D + lane * V + j];
+        }
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        const int at = t.row0 + r, token = at / group;
+        __nv_bfloat16 *to = o + ((int64_t)(t.s.begin + token) * c.Hk * group + here.h * group + at - token * group) * D +
+                            lane * V;
+#pragma unroll
+        for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t *>(to + j) = pack2(x[j] * inv, x[j + 1] * inv);
+    }
+}
+
+struct Layout {
+    int64_t most;
+    int ranges, rows;
+    size_t tiles, cost, cuts, ml, part, total;
+};
+static Layout layout_of(const Cache &c, int group, int D, int sms) {
+    Layout L;
+    const int64_t rows = c.cu ? (int64_t)c.T * group : group;
+    L.most = c.cu ? rows / kRows + c.N : c.N * ((rows + kRows - 1) / kRows);
+    L.rows = (int)(rows < kRows ? rows : kRows);
+    L.ranges = sms;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    L.tiles = kHeaderBytes;
+    L.cost = L.tiles + up(sizeof(int32_t) * ((size_t)c.N + 1));
+    L.cuts = L.cost + up(sizeof(int64_t) * ((size_t)L.most + 1));
+    L.ml = L.cuts + up(sizeof(Cut) * ((size_t)L.ranges + 1));
+    L.part = L.ml + up(sizeof(float2) * 2 * L.ranges * L.rows);
+    L.total = L.part + sizeof(float) * 2 * L.ranges * L.rows * D;
+    return L;
+}
+
+// Shared memory above 48 KB, once per kernel and device.
+template <int D> static cudaError_t allow_smem() {
+    static std::mutex mutex;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Map<D>::kBytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
+template <int D>
+static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, int group, float scale, int window,
+                          int sinks, uint8_t *ws, int sms, cudaStream_t s) {
+    const Layout L = layout_of(c, group, D, sms);
+    const Plan p{(int32_t *)(ws + L.tiles), (int64_t *)(ws + L.cost), (Cut *)(ws + L.cuts), (float *)(ws + L.part),
+                 (float2 *)(ws + L.ml), L.ranges, L.rows, L.most};
+    StatusWord *st = (StatusWord *)ws;
+    CUtensorMap tk, tv;
+    cudaError_t e = page_map(&tk, c, c.k, D, false);
+    if (e == cudaSuccess) e = page_map(&tv, c, c.v, D, false);
+    if (e == cudaSuccess) e = allow_smem<D>();
+    if (e != cudaSuccess) return e;
+    paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(c, p, group, window, sinks, st);
+    e = cudaGetLastError();
+    if (e == cudaSuccess)
+        e = launch_after(paged_attn_kernel<D>, dim3(L.ranges), dim3(kThreads), Map<D>::kBytes, s, c, p, tk, tv,
+                         (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks, st);
+    if (e == cudaSuccess && L.ranges > 1)
+        e = launch_after(paged_join_kernel<D>, dim3(L.ranges - 1, (L.rows + 31) / 32), dim3(256), 0, s, c, p,
+                         (__nv_bfloat16 *)o, group);
+    return e;
+}
+
+}  // namespace tc
+}  // namespace paged
+
+size_t paged_tc_bytes(const paged::Cache &c, int group, int D, int sms) {
+    return paged::tc::layout_of(c, group, D, sms).total;
+}
+
+cudaError_t launch_paged_tc(int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group, float scale,
+                            int window, int sinks, void *ws, int sms, cudaStream_t s) {
+    return D == 128 ? paged::tc::launch<128>(c, q, qs, o, group, scale, window, sinks, (uint8_t *)ws, sms, s)
+                    : paged::tc::launch<64>(c, q, qs, o, group, scale, window, sinks, (uint8_t *)ws, sms, s);
+}
+
+}  // namespace kda

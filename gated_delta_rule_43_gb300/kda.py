@@ -21,8 +21,9 @@ LIB_PATH = os.path.join(_PKG, "libkda.so")
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_DECAY_RANGE = 0, 1, 2, 3
 KDA_ERR_TIMEOUT, KDA_ERR_CUDA, KDA_ERR_SEQLENS = 4, 5, 6
-KDA_F32, KDA_BF16 = 0, 1
+KDA_F32, KDA_BF16, KDA_E4M3 = 0, 1, 2
 _DT = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
+_E4M3 = torch.float8_e4m3fn
 _F32 = torch.float32
 _NORM = {"none": 0, "l2": 1, "rms": 2}
 _LAYOUT = {"half": 0, "interleaved": 1}
@@ -64,7 +65,21 @@ SIGNATURES = {
     "kda_state_pool_workspace_size": (SZ, [I32]),
     "kda_state_pool_copy": (I32, [P, I32, I64, P, P, I32, P, SZ, P]),
     "kda_state_pool_compact": (I32, [P, I32, I64, P, P, P, P, SZ, P]),
+    "kda_kv_cache_write": (I32, [P, P, P, I64, I32, I64, I64, P, SZ, P]),
+    "kda_kv_cache_read": (I32, [P, P, P, I64, I32, P, SZ, P]),
+    "kda_paged_attn_workspace_size": (SZ, [P, I64, I32, I32]),
+    "kda_paged_attn_fwd": (I32, [P, P, I64, P, I64, I32, I32, F32, I32, I32, P, SZ, P]),
+    "kda_paged_attn_decode_step": (I32, [P, P, I64, P, I32, I32, F32, I32, I32, P, SZ, P]),
 }
+
+
+class PagedCache(ctypes.Structure):
+    """kda_paged_cache: one description of a paged key/value cache for the calls that touch it."""
+    _fields_ = [("cu_seqlens", P), ("kv_lens", P), ("block_table", P), ("k_pages", P),
+                ("v_pages", P), ("k_scales", P), ("v_scales", P), ("page_stride", I64),
+                ("scale_stride", I64), ("num_seqs", I32), ("table_width", I32),
+                ("num_pages", I32), ("page_size", I32), ("Hk", I32), ("D", I32), ("dtype", I32)]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -739,6 +754,201 @@ def state_pool_compact(pool, live, *, new_index=None, n_live=None, workspace=Non
     if rc != KDA_OK:
         raise KdaError(rc, "kda_state_pool_compact")
     return new_index, n_live
+
+
+def _pages_stride(name, t, shape, dtype):
+    """Pages (or their scales) whose first dimension alone may be strided; that stride."""
+    if t.shape != shape or t.dtype != dtype:
+        _expect(name, t, shape, dtype)
+    s, packed = t.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] > 1 and s[i] != packed:
+            raise ValueError(f"{name}: everything inside a page must be packed (strides {s})")
+        packed *= shape[i]
+    return s[0] if shape[0] > 1 else packed
+
+
+def _paged(k_pages, v_pages, block_table, kv_lens, cu_seqlens, k_scales, v_scales):
+    """The checked description of a cache, and its (Hk, D, dtype)."""
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages and v_pages must be [P, Hk, page_size, D]")
+    shape, dtype = k_pages.shape, k_pages.dtype
+    if dtype is not _E4M3 and dtype not in _DT:
+        raise TypeError(f"k_pages has dtype {dtype}; fp32, bf16 and float8_e4m3fn are supported")
+    stride = _pages_stride("k_pages", k_pages, shape, dtype)
+    if _pages_stride("v_pages", v_pages, shape, dtype) != stride:
+        raise ValueError("k_pages and v_pages must have the same stride from page to page")
+    scale_stride = 0
+    if dtype is _E4M3:
+        if k_scales is None or v_scales is None:
+            raise ValueError("e4m3 pages need k_scales and v_scales [P, Hk, page_size]")
+        scale_stride = _pages_stride("k_scales", k_scales, shape[:3], _F32)
+        if _pages_stride("v_scales", v_scales, shape[:3], _F32) != scale_stride:
+            raise ValueError("k_scales and v_scales must have the same stride from page to page")
+    elif k_scales is not None or v_scales is not None:
+        raise ValueError("scales go with e4m3 pages only")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [N, pages]")
+    N, width = block_table.shape
+    ta = _dense("block_table", block_table, (N, width), torch.int32)
+    la = _dense("kv_lens", kv_lens, (N,), torch.int32)
+    ca = None if cu_seqlens is None else _dense("cu_seqlens", cu_seqlens, (N + 1,), torch.int32)
+    return PagedCache(ca, la, ta, k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scales),
+                      _addr(v_scales), stride, scale_stride, N, width, shape[0], shape[2], shape[1],
+                      shape[3], KDA_E4M3 if dtype is _E4M3 else _DT[dtype]), shape[1], shape[3], dtype
+
+
+def _paged_dtype(name, dtype, cache_dtype):
+    if dtype not in _DT:
+        raise TypeError(f"{name} has dtype {dtype}; fp32 and bf16 are supported")
+    if cache_dtype is not _E4M3 and cache_dtype != dtype:
+        raise TypeError(f"{name} has dtype {dtype}, the pages {cache_dtype}")
+    return dtype
+
+
+def kv_cache_write(k, v, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, *, k_scales=None,
+                   v_scales=None, workspace=None, stream=None, check: bool = False):
+    """New keys and values into the pages of a cache (kda_kv_cache_write).
+
+    k, v [T, Hk, D] fp32 or bf16 (tokens may be slices of wider rows); k_pages, v_pages
+    [P, Hk, page_size, D] of the same dtype or float8_e4m3fn, with k_scales, v_scales
+    [P, Hk, page_size] fp32 (all written in place; only the page dimension may be strided);
+    block_table [N, pages], kv_lens [N] and cu_seqlens [N + 1] (None: one token a sequence)
+    int32.  The call's tokens are the last of each sequence's kv_lens[n].  With a workspace (or
+    check=True) sequences and pages that do not fit are recorded; they are skipped either way.
+    """
+    lib = _lib or load()
+    cache, Hk, D, ct = _paged(k_pages, v_pages, block_table, kv_lens, cu_seqlens, k_scales, v_scales)
+    if k.dim() != 3:
+        raise ValueError("k and v must be [T, Hk, D]")
+    dtype = _paged_dtype("k", k.dtype, ct)
+    T = k.shape[0]
+    if cu_seqlens is None and T != cache.num_seqs:
+        raise ValueError(f"{T} tokens for {cache.num_seqs} sequences need cu_seqlens")
+    ks, vs = _rows("k", k, T, Hk, D, dtype), _rows("v", v, T, Hk, D, dtype)
+    device = _same_gpu(k, v, k_pages, v_pages, block_table, kv_lens, cu_seqlens, k_scales, v_scales,
+                       workspace)
+    wa, wb = None, 0
+    if workspace is not None or check:
+        workspace, wa, wb = _workspace(k, lib.kda_decode_workspace_size(), workspace, stream)
+    rc = lib.kda_kv_cache_write(ctypes.byref(cache), k.data_ptr(), v.data_ptr(), T, _DT[dtype], ks, vs,
+                                wa, wb, _raw_stream(stream, device))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_kv_cache_write")
+    if check:
+        query_status(workspace, stream, raise_on_error=True)
+
+
+def kv_cache_read(k_pages, v_pages, block_table, kv_lens, cu_seqlens, *, total_tokens: int,
+                  dtype=None, k_scales=None, v_scales=None, k=None, v=None, workspace=None,
+                  stream=None, check: bool = False):
+    """The last tokens of each sequence, cu_seqlens[n + 1] - cu_seqlens[n] of them, out of their
+    pages (kda_kv_cache_read; the cache as kv_cache_write has it).  Returns packed k, v
+    [total_tokens, Hk, D] in ``dtype`` (None: the pages' own, bf16 for e4m3).  Rows that belong to
+    no sequence are not written."""
+    lib = _lib or load()
+    cache, Hk, D, ct = _paged(k_pages, v_pages, block_table, kv_lens, cu_seqlens, k_scales, v_scales)
+    if dtype is None:
+        dtype = k.dtype if k is not None else torch.bfloat16 if ct is _E4M3 else ct
+    _paged_dtype("k", dtype, ct)
+    shape = (total_tokens, Hk, D)
+    if k is not None:
+        _dense("k", k, shape, dtype)
+    if v is not None:
+        _dense("v", v, shape, dtype)
+    device = _same_gpu(k_pages, v_pages, block_table, kv_lens, cu_seqlens, k_scales, v_scales, k, v,
+                       workspace)
+    if cu_seqlens is None and total_tokens != cache.num_seqs:
+        raise ValueError(f"{total_tokens} tokens for {cache.num_seqs} sequences need cu_seqlens")
+    if k is None:
+        k = _new(k_pages, shape, dtype, stream)
+    if v is None:
+        v = _new(k_pages, shape, dtype, stream)
+    wa, wb = None, 0
+    if workspace is not None or check:
+        workspace, wa, wb = _workspace(k, lib.kda_decode_workspace_size(), workspace, stream)
+    rc = lib.kda_kv_cache_read(ctypes.byref(cache), k.data_ptr(), v.data_ptr(), total_tokens,
+                               _DT[dtype], wa, wb, _raw_stream(stream, device))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_kv_cache_read")
+    if check:
+        query_status(workspace, stream, raise_on_error=True)
+    return k, v
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_workspace_size(device, N, width, pages, page_size, Hk, D, cache_dt, T, H, dt, decode):
+    cache = PagedCache(None if decode else 256, None, None, None, None, None, None, 0, 0, N, width,
+                       pages, page_size, Hk, D, cache_dt)
+    return load().kda_paged_attn_workspace_size(ctypes.byref(cache), T, H, dt)
+
+
+def _paged_attn(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, scale, window, sinks,
+                k_scales, v_scales, o, workspace, stream, check):
+    lib = _lib or load()
+    cache, Hk, D, ct = _paged(k_pages, v_pages, block_table, kv_lens, cu_seqlens, k_scales, v_scales)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, H, D]")
+    dtype = _paged_dtype("q", q.dtype, ct)
+    T, H, _ = q.shape
+    decode = cu_seqlens is None
+    if decode and T != cache.num_seqs:
+        raise ValueError(f"q has {T} rows for {cache.num_seqs} sequences")
+    if H % Hk:
+        raise ValueError(f"{H} query heads cannot share {Hk} key/value heads")
+    qs = _rows("q", q, T, H, D, dtype)
+    if o is not None:
+        _dense("o", o, (T, H, D), dtype)
+    device = _same_gpu(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, k_scales, v_scales, o,
+                       workspace)
+    if o is None:
+        o = _new(q, (T, H, D), dtype, stream)
+    dt = _DT[dtype]
+    need = 0
+    if workspace is None:
+        need = _paged_workspace_size(device, cache.num_seqs, cache.table_width, cache.num_pages,
+                                     cache.page_size, Hk, D, cache.dtype, T, H, dt, decode)
+    workspace, wa, wb = _workspace(q, need, workspace, stream)
+    if decode:
+        name = "kda_paged_attn_decode_step"
+        rc = lib.kda_paged_attn_decode_step(ctypes.byref(cache), q.data_ptr(), qs, o.data_ptr(), H, dt,
+                                            scale, window, sinks, wa, wb, _raw_stream(stream, device))
+    else:
+        name = "kda_paged_attn_fwd"
+        rc = lib.kda_paged_attn_fwd(ctypes.byref(cache), q.data_ptr(), qs, o.data_ptr(), T, H, dt,
+                                    scale, window, sinks, wa, wb, _raw_stream(stream, device))
+    if rc != KDA_OK:
+        raise KdaError(rc, name)
+    if check:
+        query_status(workspace, stream, raise_on_error=True)
+    return o
+
+
+def paged_attn_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, *, scale: float = 1.0,
+                   window: int = 0, sinks: int = 0, k_scales=None, v_scales=None, o=None,
+                   workspace=None, stream=None, check: bool = False):
+    """Attention of a chunk of new tokens a sequence over its whole paged context
+    (kda_paged_attn_fwd; the cache as kv_cache_write has it, the new tokens written before).
+
+    q [T, H, D] (tokens may be slices of wider rows), Hk divides H; causal; scale multiplies the
+    scores (1 for queries that qk_norm_rope has scaled); window > 0: a token sees the last
+    ``window`` positions, its own among them, and the first ``sinks``.  Returns o [T, H, D]; rows
+    that belong to no sequence are not written.
+    """
+    if cu_seqlens is None:
+        raise ValueError("paged_attn_fwd needs cu_seqlens (one token a sequence: "
+                         "paged_attn_decode_step)")
+    return _paged_attn(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, scale, window, sinks,
+                       k_scales, v_scales, o, workspace, stream, check)
+
+
+def paged_attn_decode_step(q, k_pages, v_pages, block_table, kv_lens, *, scale: float = 1.0,
+                           window: int = 0, sinks: int = 0, k_scales=None, v_scales=None, o=None,
+                           workspace=None, stream=None, check: bool = False):
+    """paged_attn_fwd for one new token a sequence, the last of its kv_lens[n]
+    (kda_paged_attn_decode_step): q, o [N, H, D].  A sequence without tokens gets zeros."""
+    return _paged_attn(q, k_pages, v_pages, block_table, kv_lens, None, scale, window, sinks, k_scales,
+                       v_scales, o, workspace, stream, check)
 
 
 def query_status(workspace, stream=None, *, raise_on_error: bool = False):

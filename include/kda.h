@@ -54,7 +54,8 @@ typedef enum kda_status {
     KDA_ERR_SEQLENS = 6      /* cu_seqlens not 0-based, decreasing, or not ending at T_tot */
 } kda_status;
 
-typedef enum kda_dtype { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
+/* (KDA_E4M3: the pages of a key/value cache only) */
+typedef enum kda_dtype { KDA_F32 = 0, KDA_BF16 = 1, KDA_E4M3 = 2 } kda_dtype;
 
 /* Version of this ABI (bumped on any signature change). */
 int32_t kda_abi_version(void);
@@ -459,6 +460,101 @@ kda_status kda_state_pool_copy(float *pool, int32_t P, int64_t slot_elems,
 kda_status kda_state_pool_compact(float *pool, int32_t P, int64_t slot_elems,
                                   const uint8_t *live, int32_t *new_index, int32_t *n_live,
                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Paged keys and values.  The softmax-attention layers of a hybrid model keep the keys and values
+ * of every token beside the fixed-size states above, in pages of one pool (the other half of the
+ * paged cache of the dev.to page, section "Infrastructure and Training/Inference Mechanics",
+ * "Serving Engine").  One description of the cache serves the calls that write it, read it back and
+ * attend to it:
+ *
+ *   k_pages, v_pages   [num_pages, Hk, page_size, D]   dtype; page_stride elements from one page to
+ *                      the next (a multiple of 16 bytes, at least Hk * page_size * D), so that both
+ *                      may be halves of one pool [num_pages, 2, Hk, page_size, D]
+ *   k_scales, v_scales [num_pages, Hk, page_size] fp32, scale_stride from page to page, with dtype
+ *                      KDA_E4M3 (NULL otherwise): a row of D values stands for scale * e4m3.  Scales
+ *                      are powers of two, so scale * e4m3 is a bf16 exactly.
+ *   block_table        [num_seqs, table_width] int32: position j of sequence n lies in slot
+ *                      j % page_size of page block_table[n][j / page_size].  Entries that hold no
+ *                      position in use are not read (any value may stand there).
+ *   kv_lens            [num_seqs] int32: the tokens of each sequence, those of this call among them
+ *   cu_seqlens         [num_seqs + 1] int32, 0 = cu[0] <= ... <= cu[num_seqs] <= total_tokens: the rows of
+ *                      this call's tokens; NULL: one token a sequence, row n.  Rows at and behind
+ *                      cu[num_seqs] are left as they are.
+ *
+ * This call's tokens are a sequence's last: token i of len stands at position kv_lens[n] - len + i.  A
+ * token whose position comes out below 0 is padding (a short sequence padded at its left; a
+ * sequence without tokens, kv_lens[n] = 0, in a batch of fixed size): it is not written, reads back
+ * as zeros and its attention is zeros.
+ *
+ * page_size: a power of two, 16 ..= 1024.  D in {32, 64, 128}.  The cache's dtype is that of the
+ * call's tensors, or KDA_E4M3.  Sizes: total_tokens, table_width * page_size and (attention)
+ * total_tokens * H / Hk below 2^31.  The struct is read during the call only.
+ * Device-found errors: KDA_ERR_SEQLENS (info = the sequence: its rows or its length do not fit; it is
+ * skipped, its rows are not written), KDA_ERR_INVALID_ARG (info = the sequence: a page outside
+ * the pool; such a page is not touched and counts as zeros).
+ */
+typedef struct kda_paged_cache {
+    const int32_t *cu_seqlens;
+    const int32_t *kv_lens;
+    const int32_t *block_table;
+    void *k_pages, *v_pages;
+    float *k_scales, *v_scales;
+    int64_t page_stride, scale_stride;
+    int32_t num_seqs, table_width;
+    int32_t num_pages, page_size, Hk, D;
+    int32_t dtype;
+} kda_paged_cache;
+
+/*
+ * New keys and values k, v [total_tokens, Hk, D] (dtype KDA_F32 or KDA_BF16, token strides as
+ * kda_la_chunk_fwd; tokens may repeat, stride 0) into their pages.  With an e4m3 cache each row of D values is
+ * stored as e4m3(x / s) and s = 2^e, the least with max|x| <= 448 s (e in -100 ..= 119; 1 for a row of
+ * zeros): one rounding, to nearest.  An infinity is stored as 448 s of the row's finite
+ * values, a NaN as a NaN.  No two tokens of a call may share a slot (sequences may share pages that
+ * are only read).  workspace: NULL, or >= kda_decode_workspace_size() bytes for the status word.
+ */
+kda_status kda_kv_cache_write(const kda_paged_cache *cache, const void *k, const void *v,
+                              int64_t total_tokens, int32_t dtype, int64_t k_stride,
+                              int64_t v_stride, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * The tokens' keys and values out of their pages into packed k, v [total_tokens, Hk, D] (dtype KDA_F32 or
+ * KDA_BF16), with the same places as kda_kv_cache_write; len = kv_lens reads whole sequences.
+ */
+kda_status kda_kv_cache_read(const kda_paged_cache *cache, void *k, void *v, int64_t total_tokens,
+                             int32_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of the two calls below (0 for sizes that they would reject).  Only the sizes
+ * of the cache are looked at, and whether cu_seqlens is NULL. */
+size_t kda_paged_attn_workspace_size(const kda_paged_cache *cache, int64_t total_tokens, int32_t H,
+                                     int32_t dtype);
+
+/*
+ * Softmax attention of a chunk of new tokens over their sequences' whole paged context, the new
+ * tokens among it (write them first):
+ *   o_i = sum_j w_ij v_j / sum_j w_ij,  w_ij = exp(scale q_i k_j)
+ * over the positions j <= pos_i that are visible: all with window = 0, else pos_i - window < j or
+ * j < sinks (the last `window` positions, the token's own among them, and the first `sinks`).
+ * Query head h reads key/value head h / (H / Hk).  A row that sees nothing (padding) is zeros.
+ *   q [total_tokens, H, D] dtype, token stride q_stride; o [total_tokens, H, D] packed
+ *   scale: positive and finite (1 for queries that kda_qk_norm_rope has scaled); window, sinks >= 0
+ * Pages that no token of the call sees are not read.  With bf16 storage the weights are rounded to
+ * bf16 before they meet the values; sums, maxima and products are fp32.  A key or value that is
+ * visible to one token and not finite may spread to other tokens of the call that stand close to it and do not
+ * see it (their weight for it is 0, and 0 * inf is NaN); values in slots past kv_lens never do.
+ */
+kda_status kda_paged_attn_fwd(const kda_paged_cache *cache, const void *q, int64_t q_stride, void *o,
+                              int64_t total_tokens, int32_t H, int32_t dtype, float scale,
+                              int32_t window, int32_t sinks, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* The same for one new token a sequence: q, o [num_seqs, H, D]; cache->cu_seqlens is NULL. */
+kda_status kda_paged_attn_decode_step(const kda_paged_cache *cache, const void *q,
+                                      int64_t q_stride, void *o, int32_t H, int32_t dtype,
+                                      float scale, int32_t window, int32_t sinks,
+                                      void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Waits for `stream`, then returns the status recorded in `workspace` by the
