@@ -14,8 +14,8 @@ cudaError_t launch_paged_simt(int dtype, int cache_dtype, int D, const paged::Ca
                               void *o, int group, float scale, int window, int sinks, float *part, int sms,
                               StatusWord *st, cudaStream_t s);
 size_t paged_tc_bytes(const paged::Cache &c, int group, int D, int sms);
-cudaError_t launch_paged_tc(int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group, float scale,
-                            int window, int sinks, void *ws, int sms, cudaStream_t s);
+cudaError_t launch_paged_tc(bool e4m3, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
+                            float scale, int window, int sinks, void *ws, int sms, cudaStream_t s);
 }  // namespace kda
 
 using namespace kda;
@@ -93,7 +93,7 @@ bool attn_sizes_ok(const kda_paged_cache *p, int64_t T, int32_t H) {
 
 // bf16 heads of 64 and 128 go to the tensor cores (a pool without pages has nothing to load from).
 bool on_tensor_cores(const kda_paged_cache *p, int32_t dtype) {
-    return dtype == KDA_BF16 && p->dtype == KDA_BF16 && p->D >= 64 && p->num_pages > 0;
+    return dtype == KDA_BF16 && p->D >= 64 && p->num_pages > 0;
 }
 
 size_t attn_bytes(const kda_paged_cache *p, int64_t T, int32_t H, int32_t dtype) {
@@ -116,8 +116,8 @@ kda_status attn(const kda_paged_cache *p, const void *q, int64_t qs, void *o, in
     cudaStream_t s = (cudaStream_t)stream;
     StatusWord *st = (StatusWord *)workspace;
     if (T > 0 && p->num_seqs > 0 && on_tensor_cores(p, dtype))
-        return cuda_status(launch_paged_tc(p->D, make(p, T), q, qs, o, H / p->Hk, scale, window, sinks, workspace,
-                                           sm_count(), s));
+        return cuda_status(launch_paged_tc(p->dtype == KDA_E4M3, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window,
+                                           sinks, workspace, sm_count(), s));
     const kda_status e = clear(st, s);
     if (e != KDA_OK || T == 0 || p->num_seqs == 0) return e;
     return cuda_status(launch_paged_simt(dtype, p->dtype, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window, sinks,

@@ -22,6 +22,8 @@
 //   warp 8           issues the products        warp 9    loads keys and values, page by page
 //   warp 10          goes through the range's items for everyone
 //   warp 11          zeroes the values behind a sequence's end (slots that nobody has written)
+//   warps 12-15      (e4m3 pages) make the operands out of the bytes that warp 9 loads: scale * e4m3 is a bf16
+//                    exactly, so the products are those of a bf16 cache
 // Products of one tile run while the other's scores become weights: P0 V, Q0 K', P1 V, Q1 K', ...
 #include "kda_paged_tc.cuh"
 
@@ -31,8 +33,8 @@ namespace tc {
 
 constexpr int BK = 128;             // keys of a block
 constexpr int kRows = 256;          // rows of an item
-constexpr int kThreads = 384;
-constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kEndWarp = 11;
+template <bool E4M3> constexpr int kThreads = E4M3 ? 512 : 384;
+constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kEndWarp = 11, kMakeWarp = 12;
 constexpr int kItemCost = 2;        // an item's queries and outputs, in blocks
 constexpr int kUncut = 6;           // blocks of an item that is not cut
 constexpr int kRing = 4;            // items known ahead
@@ -195,17 +197,19 @@ struct alignas(16) Item {
     }
 };
 
-template <int D> struct Map {
+template <int D, bool E4M3> struct Map {
     static constexpr uint32_t kTile = 128 * D * 2;           // of keys, values or a tile's queries
-    static constexpr int kStages = D == 128 ? 5 : 8;
-    static constexpr uint32_t kQ = 0, kKV = 2 * kTile;
-    static constexpr uint32_t kItems = kKV + kStages * kTile;
+    static constexpr uint32_t kRawTile = E4M3 ? 128 * D : 0; // of keys or values as they lie in e4m3 pages
+    static constexpr int kStages = D == 64 ? 8 : E4M3 ? 4 : 5, kRaws = E4M3 ? D == 64 ? 4 : 2 : 0;
+    static constexpr uint32_t kQ = 0, kKV = 2 * kTile, kRaw = kKV + kStages * kTile;
+    static constexpr uint32_t kItems = kRaw + kRaws * kRawTile;
     static constexpr uint32_t kBar = kItems + kRing * (uint32_t)sizeof(Item);
     // barriers
     static constexpr int kFull = 0, kFree = kStages, kQFull = 2 * kStages, kSReady = kQFull + 2,
                          kPReady = kSReady + 2, kODone = kPReady + 2, kItemFull = kODone + 2,
                          kItemFree = kItemFull + kRing, kFixAsked = kItemFree + kRing, kFixed = kFixAsked + 1,
-                         kDrain = kFixed + 1, kBars = kDrain + 1;
+                         kDrain = kFixed + 1, kRawFull = kDrain + 1, kRawFree = kRawFull + kRaws,
+                         kBars = kRawFree + kRaws;
     static constexpr uint32_t kSlot = kBar + kBars * 8, kBytes = kSlot + 16;
     static_assert(sizeof(Item) % 8 == 0 && kBytes <= 232448 && kItems % 1024 == 0, "layout");
 };
@@ -221,13 +225,13 @@ struct Ring {
     }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kThreads<E4M3>, 1)
 paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const __nv_bfloat16 *__restrict__ q, int64_t q_stride, __nv_bfloat16 *__restrict__ o, int group,
                   float scale, int window, int sinks, StatusWord *st) {
     extern __shared__ __align__(1024) uint8_t sm[];
-    using M = Map<D>;
+    using M = Map<D, E4M3>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     let_next_start();
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + M::kBar);
@@ -241,7 +245,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
     }
     if (tid == 0) {
         for (int i = 0; i < M::kStages; ++i) {
-            mbar_init(&bar[M::kFull + i], 1);
+            mbar_init(&bar[M::kFull + i], E4M3 ? 4 : 1);
             mbar_init(&bar[M::kFree + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -252,7 +256,11 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&bar[M::kItemFull + i], 1);
-            mbar_init(&bar[M::kItemFree + i], kRowWarps + 3);
+            mbar_init(&bar[M::kItemFree + i], kRowWarps + (E4M3 ? 6 : 3));
+        }
+        for (int i = 0; i < M::kRaws; ++i) {
+            mbar_init(&bar[M::kRawFull + i], 1);
+            mbar_init(&bar[M::kRawFree + i], 4);
         }
         mbar_init(&bar[M::kFixAsked], 1);
         mbar_init(&bar[M::kFixed], 1);
@@ -483,7 +491,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
     } else {
         if (warp == kEndWarp) {
             uint32_t phase = 0;
-            each_item([&](const Item &it) {
+            if (!E4M3) each_item([&](const Item &it) {
                 // the values behind the sequence's end, in the last block that reaches past it
                 for (int k = it.k0; k < it.k1; ++k) {
                     const int left = it.ctx - it.block(k) * BK;   // (only of the list's last block below 128)
@@ -540,7 +548,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     key = val;
                     key.step(M::kStages);
                     if (!wait(M::kFull + val.stage, val.phase)) return;
-                    if (it.ctx - it.block(it.k0 + j) * BK < BK && (it.ctx & ((1 << c.shift) - 1)) != 0) {
+                    if (!E4M3 && it.ctx - it.block(it.k0 + j) * BK < BK && (it.ctx & ((1 << c.shift) - 1)) != 0) {
                         if (lane == 0) mbar_arrive(&bar[M::kFixAsked]);
                         __syncwarp();
                         if (!wait(M::kFixed, fix_phase)) return;
@@ -603,18 +611,26 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     }
 #pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
-                        if (!wait(M::kFree + kv.stage, kv.phase ^ 1)) return;
-                        if (lane == 0) mbar_arrive_expect_tx(&bar[M::kFull + kv.stage], M::kTile);
+                        // (e4m3 pages go through a ring of their own)
+                        const uint32_t full = E4M3 ? M::kRawFull : M::kFull, free = E4M3 ? M::kRawFree : M::kFree;
+                        if (!wait(free + kv.stage, kv.phase ^ 1)) return;
+                        if (lane == 0) mbar_arrive_expect_tx(&bar[full + kv.stage], E4M3 ? M::kRawTile : M::kTile);
                         __syncwarp();
                         if (lane < boxes) {
+                            const int row = key & ((1 << c.shift) - 1);
+                            const uint32_t done = bars + 8 * (full + kv.stage);
+                            if (E4M3) {
+                                tma_load_page(base + M::kRaw + kv.stage * M::kRawTile + lane * rows * D, v ? &tv : &tk, 0, row,
+                                              it.h, page, done);
+                            } else {
 #pragma unroll
-                            for (int x = 0; x < D / 64; ++x)
-                                tma_load_page(base + M::kKV + kv.stage * M::kTile + x * 16384 + lane * rows * 128, v ? &tv : &tk,
-                                              64 * x, key & ((1 << c.shift) - 1), it.h, page,
-                                              bars + 8 * (M::kFull + kv.stage));
+                                for (int x = 0; x < D / 64; ++x)
+                                    tma_load_page(base + M::kKV + kv.stage * M::kTile + x * 16384 + lane * rows * 128,
+                                                  v ? &tv : &tk, 64 * x, row, it.h, page, done);
+                            }
                         }
                         __syncwarp();
-                        kv.step(M::kStages);
+                        kv.step(E4M3 ? M::kRaws : M::kStages);
                         ++loads;
                     }
                 }
@@ -680,6 +696,76 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     }
                 }
             }
+        } else if (E4M3) {
+            // this thread's row of a block: its page, then (a block later) its scales, ahead of their use
+            const int row = tid - 32 * kMakeWarp;
+            Ring raw;
+            each_item([&](const Item &it) {
+                const int lowest = window > 0 ? max(0, it.first) - window : -1;   // keys above it are in someone's window
+                auto slot_of = [&](int k, int &page) {   // of the block's row, with a page to look up
+                    const int key = it.block(k) * BK + row;
+                    page = -1;
+                    if (k < it.k1 && key <= it.last && (key > lowest || key < sinks))
+                        page = c.table[(int64_t)it.n * c.width + (key >> c.shift)];
+                };
+                auto scales_of = [&](int k, int page, float &ks, float &vs) {
+                    ks = vs = 0.f;   // (what nobody sees, and a page outside the pool, count as zeros)
+                    if (page >= 0 && page < c.P) {
+                        const int key = it.block(k) * BK + row;
+                        const int64_t at = page * c.scale_stride + ((int64_t)it.h << c.shift) + (key & ((1 << c.shift) - 1));
+                        ks = c.ks[at];
+                        vs = c.vs[at];
+                    }
+                };
+                int page, next_page;
+                float ks, vs;
+                slot_of(it.k0, page);
+                slot_of(it.k0 + 1, next_page);
+                scales_of(it.k0, page, ks, vs);
+                for (int k = it.k0; k < it.k1; ++k) {
+                    const bool seen = page >= 0 && page < c.P;
+                    const float now[2] = {ks, vs};
+                    page = next_page;
+                    slot_of(k + 2, next_page);
+                    scales_of(k + 1, page, ks, vs);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        if (!wait(M::kRawFull + raw.stage, raw.phase)) return;
+                        if (!wait(M::kFree + kv.stage, kv.phase ^ 1)) return;
+                        const uint8_t *from = sm + M::kRaw + raw.stage * M::kRawTile + row * D;
+                        uint8_t *to = sm + M::kKV + kv.stage * M::kTile;
+                        const float s = now[v];
+#pragma unroll 4
+                        for (int x = 0; x < D / 16; ++x) {
+                            // 16 bytes (their places swizzled by the load) become 16 bf16
+                            const int place = D == 128 ? x ^ (row & 7) : x ^ ((row >> 1) & 3);
+                            const uint4 in = *reinterpret_cast<const uint4 *>(from + 16 * place);
+                            const uint32_t word[4] = {in.x, in.y, in.z, in.w};
+                            uint32_t out[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                                    (__nv_fp8x2_storage_t)(word[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+                                const float2 y = __half22float2(__half2(h));
+                                out[i] = seen ? pack2(y.x * s, y.y * s) : 0u;
+                            }
+                            *reinterpret_cast<uint4 *>(to + sw128_offset(row, 16 * x, BK)) =
+                                make_uint4(out[0], out[1], out[2], out[3]);
+                            *reinterpret_cast<uint4 *>(to + sw128_offset(row, 16 * x + 8, BK)) =
+                                make_uint4(out[4], out[5], out[6], out[7]);
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bar[M::kFull + kv.stage]);
+                            mbar_arrive(&bar[M::kRawFree + raw.stage]);
+                        }
+                        __syncwarp();
+                        raw.step(M::kRaws);
+                        kv.step(M::kStages);
+                    }
+                }
+            });
         }
     }
     if (!ok && lane == 0) report(st, KDA_ERR_TIMEOUT, blockIdx.x, 72 + warp);
@@ -694,9 +780,11 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             __syncwarp();
             mbar_wait(&bar[M::kDrain], 0, kDrainNs);
         }
-        if (warp == kLoadWarp)   // (only each stage's last load can be in flight)
-            for (uint32_t x = loads >= (uint32_t)M::kStages ? loads - M::kStages : 0; x < loads; ++x)
-                mbar_wait(&bar[M::kFull + x % M::kStages], (x / M::kStages) & 1, kDrainNs);
+        if (warp == kLoadWarp) {   // (only each stage's last load can be in flight)
+            constexpr uint32_t stages = E4M3 ? M::kRaws : M::kStages, full = E4M3 ? M::kRawFull : M::kFull;
+            for (uint32_t x = loads >= stages ? loads - stages : 0; x < loads; ++x)
+                mbar_wait(&bar[full + x % stages], (x / stages) & 1, kDrainNs);
+        }
         __syncthreads();
     }
     if (warp == kMmaWarp) {
@@ -771,7 +859,7 @@ static Layout layout_of(const Cache &c, int group, int D, int sms) {
 }
 
 // Shared memory above 48 KB, once per kernel and device.
-template <int D> static cudaError_t allow_smem() {
+template <int D, bool E4M3> static cudaError_t allow_smem() {
     static std::mutex mutex;
     static bool done[64] = {};
     int dev = 0;
@@ -779,12 +867,13 @@ template <int D> static cudaError_t allow_smem() {
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mutex);
     if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-    e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Map<D>::kBytes);
+    e = cudaFuncSetAttribute(paged_attn_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Map<D, E4M3>::kBytes);
     if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
     return e;
 }
 
-template <int D>
+template <int D, bool E4M3>
 static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, int group, float scale, int window,
                           int sinks, uint8_t *ws, int sms, cudaStream_t s) {
     const Layout L = layout_of(c, group, D, sms);
@@ -792,14 +881,14 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
                  (float2 *)(ws + L.ml), L.ranges, L.rows, L.most};
     StatusWord *st = (StatusWord *)ws;
     CUtensorMap tk, tv;
-    cudaError_t e = page_map(&tk, c, c.k, D, false);
-    if (e == cudaSuccess) e = page_map(&tv, c, c.v, D, false);
-    if (e == cudaSuccess) e = allow_smem<D>();
+    cudaError_t e = page_map(&tk, c, c.k, D, E4M3);
+    if (e == cudaSuccess) e = page_map(&tv, c, c.v, D, E4M3);
+    if (e == cudaSuccess) e = allow_smem<D, E4M3>();
     if (e != cudaSuccess) return e;
     paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(c, p, group, window, sinks, st);
     e = cudaGetLastError();
     if (e == cudaSuccess)
-        e = launch_after(paged_attn_kernel<D>, dim3(L.ranges), dim3(kThreads), Map<D>::kBytes, s, c, p, tk, tv,
+        e = launch_after(paged_attn_kernel<D, E4M3>, dim3(L.ranges), dim3(kThreads<E4M3>), Map<D, E4M3>::kBytes, s, c, p, tk, tv,
                          (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks, st);
     if (e == cudaSuccess && L.ranges > 1)
         e = launch_after(paged_join_kernel<D>, dim3(L.ranges - 1, (L.rows + 31) / 32), dim3(256), 0, s, c, p,
@@ -814,10 +903,15 @@ size_t paged_tc_bytes(const paged::Cache &c, int group, int D, int sms) {
     return paged::tc::layout_of(c, group, D, sms).total;
 }
 
-cudaError_t launch_paged_tc(int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group, float scale,
-                            int window, int sinks, void *ws, int sms, cudaStream_t s) {
-    return D == 128 ? paged::tc::launch<128>(c, q, qs, o, group, scale, window, sinks, (uint8_t *)ws, sms, s)
-                    : paged::tc::launch<64>(c, q, qs, o, group, scale, window, sinks, (uint8_t *)ws, sms, s);
+cudaError_t launch_paged_tc(bool e4m3, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
+                            float scale, int window, int sinks, void *ws, int sms, cudaStream_t s) {
+    using paged::tc::launch;
+    uint8_t *w = (uint8_t *)ws;
+    if (e4m3)
+        return D == 128 ? launch<128, true>(c, q, qs, o, group, scale, window, sinks, w, sms, s)
+                        : launch<64, true>(c, q, qs, o, group, scale, window, sinks, w, sms, s);
+    return D == 128 ? launch<128, false>(c, q, qs, o, group, scale, window, sinks, w, sms, s)
+                    : launch<64, false>(c, q, qs, o, group, scale, window, sinks, w, sms, s);
 }
 
 }  // namespace kda
