@@ -19,6 +19,46 @@ using namespace sm100;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kDrainNs = 100000000ull;   // limit of a wait of a CTA that has given up
 
+constexpr int BK = 128;             // keys of a block
+
+// A place in the row of blocks: before block k of the blocks that head h of tile `tile` (the t-th of
+// sequence n) sees.  k > 0: inside an item.
+struct Cut {
+    int32_t tile, n, t, h, k;
+};
+__device__ __forceinline__ bool same_item(const Cut &a, const Cut &b) { return a.tile == b.tile && a.h == b.h; }
+
+struct Plan {
+    int32_t *tiles;           // [N + 1]: tiles of the sequences before n
+    int64_t *cost;            // [tiles + 1]: that of the tiles before
+    Cut *cuts;                // [ranges + 1]
+    float *part;              // [2 * ranges][rows][D]: what a cut leaves, behind a range's begin, before its end
+    float2 *ml;               // [2 * ranges][rows]
+    int ranges, rows;         // rows: of an item, at most
+    int each;                 // rows of a tile
+    StatusWord *found;        // [ranges]: what each range has to report (single tokens; or null)
+    int64_t most;             // tiles that there is room for
+};
+
+// What everything about tile t of a sequence follows from.
+struct Tile {
+    Span s;
+    int row0, rows;           // of the sequence's len * group
+    int first, last;          // positions of the first and last row's tokens
+};
+__device__ __forceinline__ Tile tile_of(const Span &s, int t, int group, int each) {
+    Tile r;
+    r.s = s;
+    r.row0 = t * each;
+    r.rows = (int)min((int64_t)each, (int64_t)s.len * group - r.row0);
+    r.first = s.pos + r.row0 / group;
+    r.last = s.pos + (r.row0 + r.rows - 1) / group;
+    return r;
+}
+__device__ __forceinline__ KeyBlocks blocks_of(const Tile &t, int window, int sinks) {
+    return key_blocks(max(0, t.first), t.last, window, sinks, BK);
+}
+
 // Waits of a whole warp on one barrier, which end: a try that finds nothing sleeps in hardware (3.7 us,
 // measured), so tries are counted: 2.2 s.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
@@ -131,6 +171,17 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, siz
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// Position in a ring of barriers: stage, and the parity of its fill.
+struct Ring {
+    uint32_t stage = 0, phase = 0;
+    __device__ __forceinline__ void step(uint32_t stages) {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -165,6 +216,9 @@ inline cudaError_t page_map(CUtensorMap *m, const Cache &c, const void *pages, i
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+// Joins what the cuts inside items have left, behind the kernel that left it.
+cudaError_t launch_join(int D, const Cache &c, const Plan &p, void *o, int group, StatusWord *st, cudaStream_t s);
 
 }  // namespace tc
 }  // namespace paged

@@ -31,7 +31,6 @@ namespace kda {
 namespace paged {
 namespace tc {
 
-constexpr int BK = 128;             // keys of a block
 constexpr int kRows = 256;          // rows of an item
 template <bool E4M3> constexpr int kThreads = E4M3 ? 512 : 384;
 constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kEndWarp = 11, kMakeWarp = 12;
@@ -39,42 +38,6 @@ constexpr int kItemCost = 2;        // an item's queries and outputs, in blocks
 constexpr int kUncut = 6;           // blocks of an item that is not cut
 constexpr int kRing = 4;            // items known ahead
 constexpr float kGrow = 8.f;        // log2 of what the maximum may grow before O is rescaled
-
-// A place in the row of blocks: before block k of the blocks that head h of tile `tile` (the t-th of
-// sequence n) sees.  k > 0: inside an item.
-struct Cut {
-    int32_t tile, n, t, h, k;
-};
-__device__ __forceinline__ bool same_item(const Cut &a, const Cut &b) { return a.tile == b.tile && a.h == b.h; }
-
-struct Plan {
-    int32_t *tiles;           // [N + 1]: tiles of the sequences before n
-    int64_t *cost;            // [tiles + 1]: that of the tiles before
-    Cut *cuts;                // [ranges + 1]
-    float *part;              // [2 * ranges][rows][D]: what a cut leaves, behind a range's begin, before its end
-    float2 *ml;               // [2 * ranges][rows]
-    int ranges, rows;         // rows: of an item, at most
-    int64_t most;             // tiles that there is room for
-};
-
-// What everything about tile t of a sequence follows from.
-struct Tile {
-    Span s;
-    int row0, rows;           // of the sequence's len * group
-    int first, last;          // positions of the first and last row's tokens
-};
-__device__ __forceinline__ Tile tile_of(const Span &s, int t, int group) {
-    Tile r;
-    r.s = s;
-    r.row0 = t * kRows;
-    r.rows = (int)min((int64_t)kRows, (int64_t)s.len * group - r.row0);
-    r.first = s.pos + r.row0 / group;
-    r.last = s.pos + (r.row0 + r.rows - 1) / group;
-    return r;
-}
-__device__ __forceinline__ KeyBlocks blocks_of(const Tile &t, int window, int sinks) {
-    return key_blocks(max(0, t.first), t.last, window, sinks, BK);
-}
 
 constexpr int kPlanThreads = 1024;
 
@@ -141,7 +104,7 @@ paged_plan_kernel(Cache c, Plan p, int group, int window, int sinks, StatusWord 
         int64_t x = 0;
         if (i < tiles) {
             int n = last_at_most(p.tiles, c.N, (int)i);
-            const Tile t = tile_of(span_of(c, n), (int)i - p.tiles[n], group);
+            const Tile t = tile_of(span_of(c, n), (int)i - p.tiles[n], group, kRows);
             x = (int64_t)c.Hk * (kItemCost + blocks_of(t, window, sinks).count);
         }
         const int64_t mine = x, some = block_scan(x, warps);
@@ -212,17 +175,6 @@ template <int D, bool E4M3> struct Map {
                          kBars = kRawFree + kRaws;
     static constexpr uint32_t kSlot = kBar + kBars * 8, kBytes = kSlot + 16;
     static_assert(sizeof(Item) % 8 == 0 && kBytes <= 232448 && kItems % 1024 == 0, "layout");
-};
-
-// Position in a ring of barriers: stage, and the parity of its fill.
-struct Ring {
-    uint32_t stage = 0, phase = 0;
-    __device__ __forceinline__ void step(uint32_t stages) {
-        if (++stage == stages) {
-            stage = 0;
-            phase ^= 1;
-        }
-    }
 };
 
 template <int D, bool E4M3>
@@ -652,7 +604,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         s = span_of(c, from.n);
                         known = from.n;
                     }
-                    const Tile t = tile_of(s, from.t, group);
+                    const Tile t = tile_of(s, from.t, group, kRows);
                     const KeyBlocks kb = blocks_of(t, window, sinks);
                     it.n = from.n;
                     it.h = from.h;
@@ -797,15 +749,30 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
 // the first inside of.
 template <int D>
 __global__ void __launch_bounds__(256)
-paged_join_kernel(Cache c, Plan p, __nv_bfloat16 *__restrict__ o, int group) {
+paged_join_kernel(Cache c, Plan p, __nv_bfloat16 *__restrict__ o, int group, StatusWord *st) {
     constexpr int V = D / 32;
     const int cut = blockIdx.x + 1, lane = threadIdx.x & 31;
     wait_for_previous();
+    if (p.found && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {   // the first of what was found
+        StatusWord first{0, 0, 0};
+        for (int i0 = 0; i0 < p.ranges && first.code == 0; i0 += 32) {
+            StatusWord x{0, 0, 0};
+            if (i0 + lane < p.ranges) x = p.found[i0 + lane];
+            const uint32_t some = __ballot_sync(0xffffffffu, x.code != 0);
+            if (some == 0) continue;
+            const int l = __ffs(some) - 1;
+            first.code = __shfl_sync(0xffffffffu, x.code, l);
+            first.site = __shfl_sync(0xffffffffu, x.site, l);
+            first.info = __shfl_sync(0xffffffffu, x.info, l);
+        }
+        if (lane == 0) *st = first;
+    }
+    if (cut >= p.ranges) return;
     const Cut here = p.cuts[cut];
     if (here.k == 0) return;
     const Cut before = p.cuts[cut - 1];
     if (same_item(here, before) && before.k > 0) return;
-    const Tile t = tile_of(span_of(c, here.n), here.t, group);
+    const Tile t = tile_of(span_of(c, here.n), here.t, group, p.each);
     int last = cut;   // the last cut inside the item
     while (last < p.ranges && p.cuts[last + 1].k > 0 && same_item(p.cuts[last + 1], here)) ++last;
     for (int r = blockIdx.y * 32 + (threadIdx.x >> 5); r < min(t.rows, (int)blockIdx.y * 32 + 32); r += 8) {
@@ -835,6 +802,12 @@ paged_join_kernel(Cache c, Plan p, __nv_bfloat16 *__restrict__ o, int group) {
 #pragma unroll
         for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t *>(to + j) = pack2(x[j] * inv, x[j + 1] * inv);
     }
+}
+
+cudaError_t launch_join(int D, const Cache &c, const Plan &p, void *o, int group, StatusWord *st, cudaStream_t s) {
+    const dim3 grid(p.ranges > 1 ? p.ranges - 1 : 1, (p.rows + 31) / 32);
+    return D == 128 ? launch_after(paged_join_kernel<128>, grid, dim3(256), 0, s, c, p, (__nv_bfloat16 *)o, group, st)
+                    : launch_after(paged_join_kernel<64>, grid, dim3(256), 0, s, c, p, (__nv_bfloat16 *)o, group, st);
 }
 
 struct Layout {
@@ -878,7 +851,7 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
                           int sinks, uint8_t *ws, int sms, cudaStream_t s) {
     const Layout L = layout_of(c, group, D, sms);
     const Plan p{(int32_t *)(ws + L.tiles), (int64_t *)(ws + L.cost), (Cut *)(ws + L.cuts), (float *)(ws + L.part),
-                 (float2 *)(ws + L.ml), L.ranges, L.rows, L.most};
+                 (float2 *)(ws + L.ml), L.ranges, L.rows, kRows, nullptr, L.most};
     StatusWord *st = (StatusWord *)ws;
     CUtensorMap tk, tv;
     cudaError_t e = page_map(&tk, c, c.k, D, E4M3);
@@ -890,10 +863,7 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
     if (e == cudaSuccess)
         e = launch_after(paged_attn_kernel<D, E4M3>, dim3(L.ranges), dim3(kThreads<E4M3>), Map<D, E4M3>::kBytes, s, c, p, tk, tv,
                          (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks, st);
-    if (e == cudaSuccess && L.ranges > 1)
-        e = launch_after(paged_join_kernel<D>, dim3(L.ranges - 1, (L.rows + 31) / 32), dim3(256), 0, s, c, p,
-                         (__nv_bfloat16 *)o, group);
-    return e;
+    return e == cudaSuccess ? launch_join(D, c, p, o, group, st, s) : e;
 }
 
 }  // namespace tc

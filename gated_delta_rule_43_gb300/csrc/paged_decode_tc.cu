@@ -1,0 +1,777 @@
+// paged_decode_tc.cu -- attention of one new token a sequence over paged keys and values on the sm_103a
+// tensor cores, heads of 64 and 128.
+//
+//   S^T = K Q^T,  P = 2^(f S - f m),  O^T = V^T P^T     (formulas: paged_attn_tc.cu)
+// Memory-bound: each key and value is read once, for all query heads that share it.  These are few, so
+// keys and channels are the products' 128 rows and the heads their columns: a tile of 128 keys goes from
+// its pages into shared memory and is an operand as it lies there, in bf16 or in e4m3.
+//
+// e4m3 pages meet e4m3 queries and weights, of which there are two each: x = hi + lo / 16, hi = e4m3(x), lo =
+// e4m3(16 (x - hi)), in columns of their own.  Together they hold the 8 bits of a bf16, down to 2^-22 of
+// the largest (rows of queries are scaled by a power of two, weights by 2^8 below their largest), so the
+// keys' and values' bytes need no conversion: nothing but the products touches them.  A key's scale
+// multiplies its scores, a value's is part of its weight.
+//
+// A piece of up to 8 tiles is gone through twice, keys, then values: all its scores stand in tensor memory
+// before the first weight is formed, so its maximum is known and nothing that the tensor cores add up
+// is rescaled.  Pieces are joined in registers, a thread a channel.
+//
+// The work is cut as for chunks (kda_paged_tc.cuh): an item is a sequence, a key/value head and up to `each`
+// query heads; each CTA finds its own range (a scan over the lengths, 1 us) instead of waiting for a
+// plan.  What cuts inside items leave is joined by paged_join_kernel.
+//
+//   warps 0-3   scores -> weights; outputs      warp 4   products       warp 5   loads
+//   warp 6      goes through the items          warp 7   queries        warp 8   zeroes slots behind the end
+#include "kda_paged_tc.cuh"
+
+namespace kda {
+namespace paged {
+namespace tc {
+namespace one {
+
+constexpr int kThreads = 288;
+constexpr int kMmaWarp = 4, kLoadWarp = 5, kItemWarp = 6, kQueryWarp = 7;   // (the last zeroes)
+constexpr int kTiles = 8;           // of a piece
+constexpr int kItemCost = 1;        // an item's queries and outputs, in tiles
+constexpr int kUncut = 2;           // tiles of an item that is not cut
+constexpr int kRing = 4;            // items known ahead
+
+struct alignas(16) Item {
+    int n;                    // -1: no more
+    int h, row0, rows;        // query heads row0 .. of the group
+    int pos, ctx;
+    int k0, k1, sinks, from;  // tiles [k0, k1) of the list (KeyBlocks)
+    int slot;                 // of Plan.part, or -1: the whole item
+    int pad;
+    __device__ __forceinline__ int tile(int k) const { return k < sinks ? k : from + k - sinks; }
+};
+// Piece u of an item's tiles
+__device__ __forceinline__ int pieces(int tiles) { return (tiles + kTiles - 1) / kTiles; }
+__device__ __forceinline__ int piece_at(int tiles, int count, int u) { return tiles * u / count; }
+
+template <int D, int NR, bool E4M3> struct Map {
+    static constexpr int N = E4M3 ? 2 * NR : 16;             // columns of a product
+    static constexpr uint32_t kTile = 128 * D * (E4M3 ? 1 : 2);
+    static constexpr uint32_t kQBytes = 4096, kPTile = N * (E4M3 ? 128 : 256);
+    static constexpr uint32_t kQ = 0, kP = 2 * kQBytes, kKV = kP + kTiles * kPTile;
+    static constexpr uint32_t kSmall = 4096;                 // what stands behind the ring
+    static constexpr int kFit = (232448 - kKV - kSmall) / kTile, kStages = kFit > 16 ? 16 : kFit;
+    static constexpr uint32_t kItems = kKV + kStages * kTile;
+    static constexpr uint32_t kQf = kItems + kRing * sizeof(Item);     // [2][16]: a query row's factor
+    static constexpr uint32_t kRed = kQf + 128;                        // [2][4][32]: warps' maxima, sums
+    static constexpr uint32_t kBar = kRed + 1024;
+    static constexpr int kFull = 0, kFree = kStages, kQFull = 2 * kStages, kQFree = kQFull + 2, kSReady = kQFree + 2,
+                         kPReady = kSReady + 1, kODone = kPReady + 1, kOFree = kODone + 1, kItemFull = kOFree + 1,
+                         kItemFree = kItemFull + kRing, kFixAsked = kItemFree + kRing, kFixed = kFixAsked + 1,
+                         kDrain = kFixed + 1, kBars = kDrain + 1;
+    static constexpr uint32_t kFound = kBar + kBars * 8, kCuts = kFound + 16, kScan = kCuts + 48, kSlot = kScan + 80,
+                              kBytes = kSlot + 16;
+    static_assert(kKV % 1024 == 0 && kPTile % 1024 == 0 && kBytes <= 232448 && kBytes - kItems <= kSmall && kFound % 8 == 0 &&
+                      N * (E4M3 ? 128 : 2 * D) <= kQBytes && sizeof(Cut) <= 24,
+                  "layout");
+};
+
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor of kind::f8f6f4 with e4m3 A and B and an fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major) {
+    return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Largest of a warp, by an order of the bits as integers (a NaN is above all)
+__device__ __forceinline__ float warp_top(float x) {
+    int i = __float_as_int(x);
+    i ^= (i >> 31) & 0x7fffffff;
+    i = __reduce_max_sync(0xffffffffu, i);
+    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+// x[0], x[1] as two e4m3 each: hi in the low, lo in the high half; hi + lo / 16 is x but for 2^-8 of it
+__device__ __forceinline__ uint32_t split_e4m3(float a, float b) {
+    const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3)));
+    const __nv_fp8x2_storage_t lo =
+        __nv_cvt_float2_to_fp8x2(make_float2(16.f * (a - back.x), 16.f * (b - back.y)), __NV_SATFINITE, __NV_E4M3);
+    return (uint32_t)hi | (uint32_t)lo << 16;
+}
+
+// The place `x` of a row of items whose costs follow from the lengths; the caller's thread holds sequences
+// [n0, n1), which begin at `before`.
+__device__ __forceinline__ Cut cut_at(const Cache &c, int64_t x, int n0, int n1, int64_t before, int groups, int window,
+                                      int sinks) {
+    Cut cut{0, n0, 0, 0, 0};
+    for (int n = n0; n < n1; ++n) {
+        const Span s = span_of(c, n);
+        if (s.len == 0) continue;
+        const int count = key_blocks(max(0, s.pos), s.pos, window, sinks, BK).count, each = kItemCost + count;
+        const int64_t cost = (int64_t)groups * c.Hk * each, rest = x - before;
+        before += cost;
+        if (rest >= cost) continue;
+        int item = (int)(rest / each);
+        cut.k = (int)(rest - (int64_t)item * each) - kItemCost;
+        const bool next = count <= kUncut && 2 * cut.k > count;   // to the item's nearer end
+        if (cut.k < 1 || count <= kUncut) cut.k = 0;
+        if (next) ++item;
+        cut.n = n;
+        if (item == groups * c.Hk) {
+            item = 0;
+            ++cut.n;
+        }
+        cut.t = item / c.Hk;
+        cut.h = item - cut.t * c.Hk;
+        cut.tile = cut.n * groups + cut.t;
+        return cut;
+    }
+    return cut;
+}
+
+template <int D, int NR, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                    const __nv_bfloat16 *__restrict__ q, int64_t q_stride, __nv_bfloat16 *__restrict__ o, int group,
+                    float scale, int window, int sinks) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    using M = Map<D, NR, E4M3>;
+    constexpr int N = M::N;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    let_next_start();
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + M::kBar);
+    Item *items = reinterpret_cast<Item *>(sm + M::kItems);
+    StatusWord *st = reinterpret_cast<StatusWord *>(sm + M::kFound);
+    Cut *cuts = reinterpret_cast<Cut *>(sm + M::kCuts);
+    int64_t *sums = reinterpret_cast<int64_t *>(sm + M::kScan);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + M::kSlot);
+    const uint32_t base = smem_u32(sm), bars = base + M::kBar;
+    if (base & 1023u) {   // the operand images need their alignment
+        if (tid == 0) p.found[blockIdx.x] = StatusWord{KDA_ERR_CUDA, 90, 0};
+        return;
+    }
+    const int groups = (group + NR - 1) / NR;
+    if (tid == 0) {
+        *st = StatusWord{0, 0, 0};
+        for (int i = 0; i < M::kStages; ++i) {
+            mbar_init(&bar[M::kFull + i], 1);
+            mbar_init(&bar[M::kFree + i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar[M::kQFull + i], 1);
+            mbar_init(&bar[M::kQFree + i], 5);
+        }
+        mbar_init(&bar[M::kSReady], 1);
+        mbar_init(&bar[M::kPReady], 4);
+        mbar_init(&bar[M::kODone], 1);
+        mbar_init(&bar[M::kOFree], 4);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&bar[M::kItemFull + i], 1);
+            mbar_init(&bar[M::kItemFree + i], 8);
+        }
+        mbar_init(&bar[M::kFixAsked], 1);
+        mbar_init(&bar[M::kFixed], 1);
+        mbar_init(&bar[M::kDrain], 1);
+        fence_mbar_init();
+    }
+    constexpr uint32_t kCols = 512;
+    if (warp == kMmaWarp) {
+        tmem_alloc(tslot, kCols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        tma_prefetch_map(&tk);
+        tma_prefetch_map(&tv);
+    }
+    // This CTA's range: eight warps add up the costs of all sequences, and whoever holds its two ends
+    // writes them down.
+    const int per = (c.N + 255) / 256, n0 = min(c.N, tid * per), n1 = min(c.N, n0 + per);
+    int64_t mine = 0, upto = 0;
+    if (tid < 256) {
+        for (int n = n0; n < n1; ++n) {
+            const Span s = span_of(c, n);
+            if (s.len) mine += (int64_t)groups * c.Hk * (kItemCost + key_blocks(max(0, s.pos), s.pos, window, sinks, BK).count);
+        }
+        upto = mine;
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, i);
+            if (lane >= i) upto += x;
+        }
+        if (lane == 31) sums[warp] = upto;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) check_spans(c, st);
+    int64_t total = 0;
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) upto += sums[w];
+        total += sums[w];
+    }
+    const int64_t share = max((total + p.ranges - 1) / p.ranges, (int64_t)(kItemCost + 1));
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const int64_t x = (int64_t)(blockIdx.x + i) * share;
+        if (x >= total) {
+            if (tid == 0) cuts[i] = Cut{c.N * groups, c.N, 0, 0, 0};
+        } else if (tid < 256 && x >= upto - mine && x < upto) {
+            cuts[i] = cut_at(c, x, n0, n1, upto - mine, groups, window, sinks);
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    if (tid < 2 && (tid == 0 || blockIdx.x + 1 == p.ranges)) p.cuts[blockIdx.x + tid] = cuts[tid];
+    const uint32_t tO = tmem + kTiles * N;
+    bool ok = true;
+    auto wait = [&](int which, uint32_t parity) {
+        ok = ok && wait_warp(bars + 8 * which, parity);
+        return ok;
+    };
+    auto each_item = [&](auto role) {
+        Ring at;
+        while (wait(M::kItemFull + at.stage, at.phase)) {
+            const Item it = items[at.stage];
+            if (it.n < 0) break;
+            role(it);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[M::kItemFree + at.stage]);
+            at.step(kRing);
+            if (!ok) break;
+        }
+    };
+    Ring kv;            // fills of the ring of tiles (a piece's keys, its values, ...)
+    Ring qs;            // of the two places of queries
+    uint32_t loads = 0; // (load warp) fills issued
+
+    if (warp < 4) {
+        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        const float f = scale * kLog2e;
+        uint32_t phase = 0, turn = 0;   // of what happens once a piece; of the maxima's places
+        float *red = reinterpret_cast<float *>(sm + M::kRed);
+        each_item([&](const Item &it) {
+            float run_m[NR], run_l[NR], run_o[NR];
+#pragma unroll
+            for (int g = 0; g < NR; ++g) {
+                run_m[g] = -INFINITY;
+                run_l[g] = run_o[g] = 0.f;
+            }
+            const int tiles = it.k1 - it.k0, count = pieces(tiles);
+            const int lowest = window > 0 ? it.pos - window : -1;   // keys above it are in the window
+            const float *qf = reinterpret_cast<const float *>(sm + M::kQf) + 16 * qs.stage;
+            if (tiles > 0 && !wait(M::kQFull + qs.stage, qs.phase)) return;
+            for (int u = 0; u < count; ++u) {
+                const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
+                // this thread's key of each tile, whether it is visible, and (e4m3) its scales
+                uint32_t seen = 0;
+                float ks[kTiles], ev[kTiles], vs[kTiles];
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    ks[t] = vs[t] = 1.f;
+                    ev[t] = 0.f;
+                    if (t >= many) continue;
+                    const int key = it.tile(first + t) * BK + tid;
+                    const bool see = key <= it.pos && (key > lowest || key < sinks);
+                    seen |= (uint32_t)see << t;
+                    if (E4M3 && see) {
+                        const int page = c.table[(int64_t)it.n * c.width + (key >> c.shift)];
+                        if (page >= 0 && page < c.P) {
+                            const int64_t at = page * c.scale_stride + ((int64_t)it.h << c.shift) + (key & ((1 << c.shift) - 1));
+                            ks[t] = c.ks[at];
+                            vs[t] = c.vs[at];
+                        }
+                    }
+                }
+                if (!wait(M::kSReady, phase)) return;
+                tc_fence_after();
+                // A tile's scores in units of log 2, -inf where the key is not visible
+                auto scores = [&](int t, float(&x)[NR]) {
+                    const bool see = (seen >> t) & 1;
+                    if constexpr (E4M3) {
+                        float y[N];
+                        if constexpr (N == 16) tmem_ld16(tmem + lanes + t * N, y);
+                        else tmem_ld32(tmem + lanes + t * N, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int g = 0; g < NR; ++g)
+                            x[g] = see ? (y[g] + 0.0625f * y[NR + g]) * (ks[t] * qf[g]) : -INFINITY;
+                    } else {
+                        float y[16];
+                        tmem_ld16(tmem + lanes + t * N, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int g = 0; g < NR; ++g) x[g] = see ? y[g] * f : -INFINITY;
+                    }
+                };
+                // The piece's maxima: m of the scores; (e4m3) m2 of the weights with the values' scales
+                float m[NR], m2[NR];
+#pragma unroll
+                for (int g = 0; g < NR; ++g) m[g] = m2[g] = -INFINITY;
+                if (E4M3) {
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t) ev[t] = (float)((int)(__float_as_uint(vs[t]) >> 23) - 127);
+                }
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    if (t >= many) break;
+                    float x[NR];
+                    scores(t, x);
+#pragma unroll
+                    for (int g = 0; g < NR; ++g) {
+                        m[g] = fmaxf(m[g], x[g]);
+                        if (E4M3) m2[g] = fmaxf(m2[g], x[g] + ev[t]);
+                    }
+                }
+                float *place = red + 128 * (turn & 1);
+                ++turn;
+#pragma unroll
+                for (int g = 0; g < NR; ++g) {
+                    if (g >= it.rows) break;
+                    const float a = warp_top(m[g]), b = E4M3 ? warp_top(m2[g]) : 0.f;
+                    if (lane == 0) {
+                        place[32 * warp + g] = a;
+                        if (E4M3) place[32 * warp + 16 + g] = b;
+                    }
+                }
+                named_bar_sync(1, 128);
+                float l[NR];
+#pragma unroll
+                for (int g = 0; g < NR; ++g) {
+                    l[g] = 0.f;
+                    if (g >= it.rows) break;
+                    m[g] = fmaxf(fmaxf(place[g], place[32 + g]), fmaxf(place[64 + g], place[96 + g]));
+                    if (E4M3) m2[g] = fmaxf(fmaxf(place[16 + g], place[48 + g]), fmaxf(place[80 + g], place[112 + g]));
+                }
+                // The weights, as the products' columns
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    if (t >= many) break;
+                    float x[NR];
+                    scores(t, x);
+                    uint8_t *to = sm + M::kP + t * M::kPTile;
+#pragma unroll
+                    for (int g = 0; g < NR; g += 2) {
+                        if (g >= it.rows) break;
+                        const float r0 = m[g] == -INFINITY ? 0.f : m[g], r1 = m[g + 1] == -INFINITY ? 0.f : m[g + 1];
+                        const float p0 = ex2(x[g] - r0), p1 = ex2(x[g + 1] - r1);
+                        l[g] += p0;
+                        l[g + 1] += p1;
+                        if constexpr (E4M3) {
+                            const float s0 = m2[g] == -INFINITY ? 0.f : m2[g] - 8.f, s1 = m2[g + 1] == -INFINITY ? 0.f : m2[g + 1] - 8.f;
+                            const uint32_t w = split_e4m3(ex2(x[g] + ev[t] - s0), ex2(x[g + 1] + ev[t] - s1));
+                            const uint32_t at = tid & 15, piece = tid >> 4;
+                            to[g * 128 + ((piece ^ (g & 7)) << 4) + at] = (uint8_t)w;
+                            to[(g + 1) * 128 + ((piece ^ ((g + 1) & 7)) << 4) + at] = (uint8_t)(w >> 8);
+                            to[(NR + g) * 128 + ((piece ^ (g & 7)) << 4) + at] = (uint8_t)(w >> 16);
+                            to[(NR + g + 1) * 128 + ((piece ^ ((g + 1) & 7)) << 4) + at] = (uint8_t)(w >> 24);
+                        } else {
+                            const uint32_t w = pack2(p0, p1);
+                            *reinterpret_cast<uint16_t *>(to + sw128_offset(g, tid, 16)) = (uint16_t)w;
+                            *reinterpret_cast<uint16_t *>(to + sw128_offset(g + 1, tid, 16)) = (uint16_t)(w >> 16);
+                        }
+                    }
+                }
+                fence_proxy_async();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[M::kPReady]);
+                __syncwarp();
+                if (!wait(M::kODone, phase)) return;
+                phase ^= 1;
+                tc_fence_after();
+                float y[N];
+                if constexpr (N == 16) tmem_ld16(tO + lanes, y);
+                else tmem_ld32(tO + lanes, y);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[M::kOFree]);
+                __syncwarp();
+#pragma unroll
+                for (int g = 0; g < NR; ++g) {
+                    if (g >= it.rows) break;
+                    const float top = fmaxf(run_m[g], m[g]), ref = top == -INFINITY ? 0.f : top;
+                    const float a = ex2(run_m[g] - ref), b = ex2(m[g] - ref);
+                    const float add = E4M3 ? (y[g] + 0.0625f * y[(E4M3 ? NR : 0) + g]) * ex2(m2[g] - 8.f - ref) : y[g] * b;
+                    run_l[g] = run_l[g] * a + l[g] * b;
+                    run_o[g] = run_o[g] * a + add;
+                    run_m[g] = top;
+                }
+            }
+            if (tiles > 0) {
+                if (lane == 0) mbar_arrive(&bar[M::kQFree + qs.stage]);
+                __syncwarp();
+                qs.step(2);
+            }
+            // the sums of all keys' threads
+            float *place = red + 128 * (turn & 1);
+            ++turn;
+#pragma unroll
+            for (int g = 0; g < NR; ++g) {
+                if (g >= it.rows) break;
+                const float x = warp_sum(run_l[g]);
+                if (lane == 0) place[32 * warp + g] = x;
+            }
+            named_bar_sync(1, 128);
+            const int d = D == 128 ? tid : 16 * warp + lane;   // (64 rows of a product stand in 16 lanes of each warp)
+            const bool there = D == 128 || lane < 16;
+#pragma unroll
+            for (int g = 0; g < NR; ++g) {
+                if (g >= it.rows) break;
+                const float l = place[g] + place[32 + g] + place[64 + g] + place[96 + g];
+                if (it.slot >= 0) {
+                    const int64_t at = (int64_t)it.slot * p.rows + g;
+                    if (tid == 0) p.ml[at] = make_float2(run_m[g] == -INFINITY ? 0.f : run_m[g], l);
+                    if (there) p.part[at * D + d] = run_o[g];
+                } else if (there) {
+                    o[((int64_t)it.n * c.Hk * group + it.h * group + it.row0 + g) * D + d] =
+                        __float2bfloat16_rn(l != 0.f ? run_o[g] / l : 0.f);
+                }
+            }
+        });
+    } else if (warp == kMmaWarp) {
+        uint32_t phase = 0, fix_phase = 0;
+        constexpr uint32_t id_s = E4M3 ? idesc_e4m3(128, N, false) : idesc_bf16(128, N, false, false);
+        constexpr uint32_t id_o = E4M3 ? idesc_e4m3(D, N, true) : idesc_bf16(D, N, true, false);
+        // keys: rows of 128 bytes (64 for e4m3 heads of 64), channels along them; values the other way round
+        constexpr bool narrow = E4M3 && D == 64;
+        const uint64_t dk0 = narrow ? sdesc_sw64(base + M::kKV, 16, 512) : sdesc_sw128(base + M::kKV, 16, 1024);
+        const uint64_t dv0 = narrow ? sdesc_sw64(base + M::kKV, 16, 512) : sdesc_sw128(base + M::kKV, BK * 128, 1024);
+        const uint64_t dq0 = sdesc_sw128(base + M::kQ, 16, 1024), dp0 = sdesc_sw128(base + M::kP, 16, 1024);
+        each_item([&](const Item &it) {
+            const int tiles = it.k1 - it.k0, count = pieces(tiles);
+            if (tiles == 0) return;
+            if (!wait(M::kQFull + qs.stage, qs.phase)) return;
+            for (int u = 0; u < count; ++u) {
+                const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
+                for (int t = 0; t < many; ++t) {
+                    if (!wait(M::kFull + kv.stage, kv.phase)) return;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t dk = desc_add(dk0, kv.stage * M::kTile), dq = desc_add(dq0, qs.stage * M::kQBytes);
+                        if constexpr (E4M3) {
+#pragma unroll
+                            for (int s = 0; s < D / 32; ++s)
+                                umma_f8(tmem + t * N, desc_add(dk, s * 32), desc_add(dq, s * 32), id_s, s > 0);
+                        } else {
+#pragma unroll
+                            for (int s = 0; s < D / 16; ++s)
+                                umma_bf16(tmem + t * N, desc_add(dk, (s >> 2) * 16384 + (s & 3) * 32),
+                                          desc_add(dq, (s >> 2) * 2048 + (s & 3) * 32), id_s, s > 0);
+                        }
+                        umma_commit(&bar[M::kFree + kv.stage]);
+                        if (t + 1 == many) {
+                            umma_commit(&bar[M::kSReady]);
+                            if (u + 1 == count) umma_commit(&bar[M::kQFree + qs.stage]);
+                        }
+                    }
+                    __syncwarp();
+                    kv.step(M::kStages);
+                }
+                if (!wait(M::kPReady, phase) || !wait(M::kOFree, phase ^ 1)) return;
+                phase ^= 1;
+                for (int t = 0; t < many; ++t) {
+                    if (!wait(M::kFull + kv.stage, kv.phase)) return;
+                    if (it.ctx - it.tile(first + t) * BK < BK && (it.ctx & ((1 << c.shift) - 1)) != 0) {
+                        if (lane == 0) mbar_arrive(&bar[M::kFixAsked]);
+                        __syncwarp();
+                        if (!wait(M::kFixed, fix_phase)) return;
+                        fix_phase ^= 1;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t dv = desc_add(dv0, kv.stage * M::kTile), dp = desc_add(dp0, t * M::kPTile);
+                        if constexpr (E4M3) {
+#pragma unroll
+                            for (int s = 0; s < BK / 32; ++s)
+                                umma_f8(tO, desc_add(dv, s * 32 * D), desc_add(dp, s * 32), id_o, t > 0 || s > 0);
+                        } else {
+#pragma unroll
+                            for (int s = 0; s < BK / 16; ++s)
+                                umma_bf16(tO, desc_add(dv, s * 2048), desc_add(dp, (s >> 2) * 2048 + (s & 3) * 32), id_o,
+                                          t > 0 || s > 0);
+                        }
+                        umma_commit(&bar[M::kFree + kv.stage]);
+                        if (t + 1 == many) umma_commit(&bar[M::kODone]);
+                    }
+                    __syncwarp();
+                    kv.step(M::kStages);
+                }
+            }
+            qs.step(2);
+        });
+    } else if (warp == kLoadWarp) {
+        const int rows = min(BK, 1 << c.shift), boxes = BK / rows;
+        each_item([&](const Item &it) {
+            const int tiles = it.k1 - it.k0, count = pieces(tiles);
+            for (int u = 0; u < count; ++u) {
+                const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
+                // the pages of this lane's boxes of the piece's tiles; P: rows that nobody sees, or no page
+                int page[kTiles];
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    page[t] = c.P;
+                    if (t >= many || lane >= boxes) continue;
+                    const int key = it.tile(first + t) * BK + lane * rows;
+                    if (key <= it.pos && (window <= 0 || key < sinks || key + rows > it.pos - window + 1))
+                        page[t] = c.table[(int64_t)it.n * c.width + (key >> c.shift)];
+                }
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    if (t >= many || lane >= boxes) continue;
+                    const int key = it.tile(first + t) * BK + lane * rows;
+                    if (key <= it.pos && (window <= 0 || key < sinks || key + rows > it.pos - window + 1) &&
+                        (page[t] < 0 || page[t] >= c.P)) {
+                        report(st, KDA_ERR_INVALID_ARG, it.n, 91);
+                        page[t] = c.P;   // (past the last: zeros)
+                    }
+                }
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t) {
+                        if (t >= many) break;
+                        if (!wait(M::kFree + kv.stage, kv.phase ^ 1)) return;
+                        if (lane == 0) mbar_arrive_expect_tx(&bar[M::kFull + kv.stage], M::kTile);
+                        __syncwarp();
+                        if (lane < boxes) {
+                            const int row = (it.tile(first + t) * BK + lane * rows) & ((1 << c.shift) - 1);
+                            const uint32_t to = base + M::kKV + kv.stage * M::kTile, done = bars + 8 * (M::kFull + kv.stage);
+                            if (E4M3) {
+                                tma_load_page(to + lane * rows * D, v ? &tv : &tk, 0, row, it.h, page[t], done);
+                            } else {
+#pragma unroll
+                                for (int x = 0; x < D / 64; ++x)
+                                    tma_load_page(to + x * 16384 + lane * rows * 128, v ? &tv : &tk, 64 * x, row, it.h, page[t],
+                                                  done);
+                            }
+                        }
+                        __syncwarp();
+                        kv.step(M::kStages);
+                        ++loads;
+                    }
+                }
+            }
+        });
+    } else if (warp == kItemWarp) {
+        Ring at;
+        Cut from = cuts[0];
+        const Cut to = cuts[1];
+        while (true) {
+            Span s{0, 0, 0};
+            while (from.n < c.N && (from.tile < to.tile || (from.tile == to.tile && (from.h < to.h || (from.h == to.h && from.k < to.k))))) {
+                s = span_of(c, from.n);
+                if (s.len) break;
+                ++from.n;   // (a sequence that does not fit)
+                from.t = from.h = from.k = 0;
+                from.tile = from.n * groups;
+            }
+            Item it{};
+            it.n = -1;
+            const bool more = s.len > 0;
+            if (more) {
+                const Tile t = tile_of(s, from.t, group, NR);
+                const KeyBlocks kb = key_blocks(max(0, s.pos), s.pos, window, sinks, BK);
+                it.n = from.n;
+                it.h = from.h;
+                it.row0 = t.row0;
+                it.rows = t.rows;
+                it.pos = s.pos;
+                it.ctx = s.pos + 1;
+                it.k0 = from.k;
+                it.k1 = same_item(from, to) ? min(to.k, kb.count) : kb.count;
+                it.sinks = kb.sinks;
+                it.from = kb.from;
+                it.slot = it.k0 > 0 ? 2 * (int)blockIdx.x : it.k1 < kb.count ? 2 * (int)blockIdx.x + 1 : -1;
+            }
+            if (!wait(M::kItemFree + at.stage, at.phase ^ 1)) break;
+            if (lane == 0) {
+                items[at.stage] = it;
+                mbar_arrive(&bar[M::kItemFull + at.stage]);
+            }
+            __syncwarp();
+            if (!more) break;
+            at.step(kRing);
+            from.k = 0;
+            if (++from.h == c.Hk) {
+                from.h = 0;
+                ++from.tile;
+                if (++from.t == groups) {
+                    from.t = 0;
+                    ++from.n;
+                }
+            }
+        }
+    } else if (warp == kQueryWarp) {
+        each_item([&](const Item &it) {
+            if (it.k1 == it.k0) return;
+            if (!wait(M::kQFree + qs.stage, qs.phase ^ 1)) return;
+            const __nv_bfloat16 *from = q + (int64_t)it.n * q_stride + (int64_t)(it.h * group + it.row0) * D;
+            uint8_t *to = sm + M::kQ + qs.stage * M::kQBytes;
+            float *qf = reinterpret_cast<float *>(sm + M::kQf) + 16 * qs.stage;
+            if constexpr (E4M3) {
+                constexpr int V = D / 32;   // channels a lane
+#pragma unroll 4
+                for (int g = 0; g < it.rows; ++g) {
+                    float x[V], top = 0.f;
+#pragma unroll
+                    for (int j = 0; j < V; j += 2) {
+                        const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162 *>(from + g * D + lane * V + j);
+                        x[j] = __low2float(y);
+                        x[j + 1] = __high2float(y);
+                        top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(x[j + 1])));
+                    }
+                    top = warp_top(top);
+                    // (a row that is not finite has no scale: its factor is NaN, and so is what it gives)
+                    const bool fine = top <= 3.4028234e38f;
+                    const int e = fine && top > 0.f ? scale_exponent(top) : 0;
+                    const float inv = two_to(-e);
+                    uint32_t hi = 0, lo = 0;
+#pragma unroll
+                    for (int j = 0; j < V; j += 2) {
+                        const uint32_t w = split_e4m3(x[j] * inv, x[j + 1] * inv);
+                        hi |= (w & 0xffffu) << (8 * j);
+                        lo |= (w >> 16) << (8 * j);
+                    }
+                    const uint32_t at = lane * V, place = (((at >> 4) ^ (g & 7)) << 4) + (at & 15);
+                    if constexpr (V == 4) {
+                        *reinterpret_cast<uint32_t *>(to + g * 128 + place) = hi;
+                        *reinterpret_cast<uint32_t *>(to + (NR + g) * 128 + place) = lo;
+                    } else {
+                        *reinterpret_cast<uint16_t *>(to + g * 128 + place) = (uint16_t)hi;
+                        *reinterpret_cast<uint16_t *>(to + (NR + g) * 128 + place) = (uint16_t)lo;
+                    }
+                    if (lane == 0) qf[g] = fine ? two_to(e) * scale * kLog2e : __int_as_float(0x7fffffff);
+                }
+            } else {
+                constexpr int U = D / 8;
+                for (int x = lane; x < it.rows * U; x += 32)
+                    *reinterpret_cast<uint4 *>(to + sw128_offset(x / U, 8 * (x % U), 16)) =
+                        *reinterpret_cast<const uint4 *>(from + x * 8);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[M::kQFull + qs.stage]);
+            __syncwarp();
+            qs.step(2);
+        });
+    } else {
+        uint32_t phase = 0;
+        each_item([&](const Item &it) {
+            const int tiles = it.k1 - it.k0;
+            for (int i = 0; i < 2 * tiles - 1; ++i) kv.step(M::kStages);
+            if (tiles > 0) {   // the values behind the sequence's end, in the tile that reaches past it: the last
+                const int left = it.ctx - it.tile(it.k1 - 1) * BK;
+                if (left < BK && (it.ctx & ((1 << c.shift) - 1)) != 0) {
+                    if (!wait(M::kFixAsked, phase)) return;
+                    phase ^= 1;
+                    constexpr int B = D * (E4M3 ? 1 : 2), W = B < 128 ? B : 128, U = W / 16;   // bytes of a row, in columns
+                    for (int x = left * U + lane; x < BK * U; x += 32)
+#pragma unroll
+                        for (int y = 0; y < B / W; ++y)
+                            *reinterpret_cast<uint4 *>(sm + M::kKV + kv.stage * M::kTile + y * BK * W + x * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[M::kFixed]);
+                    __syncwarp();
+                }
+                kv.step(M::kStages);
+            }
+        });
+    }
+    if (!ok && lane == 0) report(st, KDA_ERR_TIMEOUT, blockIdx.x, 92 + warp);
+    if (__syncthreads_or(!ok)) {
+        // an expired wait: what is in flight ends (each wait bounded again) before the tensor memory is
+        // released and the CTA leaves
+        tc_fence_before();
+        if (warp == kMmaWarp) {
+            tc_fence_after();
+            if (elect_one()) umma_commit(&bar[M::kDrain]);
+            __syncwarp();
+            mbar_wait(&bar[M::kDrain], 0, kDrainNs);
+        }
+        if (warp == kLoadWarp)   // (only each stage's last load can be in flight)
+            for (uint32_t x = loads >= (uint32_t)M::kStages ? loads - M::kStages : 0; x < loads; ++x)
+                mbar_wait(&bar[M::kFull + x % M::kStages], (x / M::kStages) & 1, kDrainNs);
+        __syncthreads();
+    }
+    if (tid == 0) p.found[blockIdx.x] = *st;
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+struct Layout {
+    int ranges, rows, each;
+    size_t cuts, found, ml, part, total;
+};
+static Layout layout_of(int group, int D, int sms) {
+    Layout L;
+    L.each = group <= 8 ? 8 : 16;
+    L.rows = group < L.each ? group : L.each;
+    L.ranges = sms;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    L.cuts = kHeaderBytes;
+    L.found = L.cuts + up(sizeof(Cut) * ((size_t)L.ranges + 1));
+    L.ml = L.found + up(sizeof(StatusWord) * L.ranges);
+    L.part = L.ml + up(sizeof(float2) * 2 * L.ranges * L.rows);
+    L.total = L.part + sizeof(float) * 2 * L.ranges * L.rows * D;
+    return L;
+}
+
+// Shared memory above 48 KB, once per kernel and device.
+template <int D, int NR, bool E4M3> static cudaError_t allow_smem() {
+    static std::mutex mutex;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(paged_decode_kernel<D, NR, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Map<D, NR, E4M3>::kBytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
+template <int D, int NR, bool E4M3>
+static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, int group, float scale, int window,
+                          int sinks, uint8_t *ws, int sms, cudaStream_t s) {
+    const Layout L = layout_of(group, D, sms);
+    const Plan p{nullptr, nullptr, (Cut *)(ws + L.cuts), (float *)(ws + L.part), (float2 *)(ws + L.ml), L.ranges, L.rows,
+                 L.each, (StatusWord *)(ws + L.found), 0};
+    CUtensorMap tk, tv;
+    cudaError_t e = page_map(&tk, c, c.k, D, E4M3);
+    if (e == cudaSuccess) e = page_map(&tv, c, c.v, D, E4M3);
+    if (e == cudaSuccess) e = allow_smem<D, NR, E4M3>();
+    if (e != cudaSuccess) return e;
+    paged_decode_kernel<D, NR, E4M3><<<L.ranges, kThreads, Map<D, NR, E4M3>::kBytes, s>>>(
+        c, p, tk, tv, (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_join(D, c, p, o, group, (StatusWord *)ws, s) : e;
+}
+
+}  // namespace one
+}  // namespace tc
+}  // namespace paged
+
+size_t paged_decode_bytes(int group, int D, int sms) { return paged::tc::one::layout_of(group, D, sms).total; }
+
+cudaError_t launch_paged_decode(bool e4m3, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
+                                float scale, int window, int sinks, void *ws, int sms, cudaStream_t s) {
+    using paged::tc::one::launch;
+    uint8_t *w = (uint8_t *)ws;
+#define KDA_ONE(D_, NR_, E_) \
+    if (D == D_ && (group <= 8) == (NR_ == 8) && e4m3 == E_) \
+        return launch<D_, NR_, E_>(c, q, qs, o, group, scale, window, sinks, w, sms, s);
+    KDA_ONE(64, 8, false) KDA_ONE(64, 16, false) KDA_ONE(128, 8, false) KDA_ONE(128, 16, false)
+    KDA_ONE(64, 8, true) KDA_ONE(64, 16, true) KDA_ONE(128, 8, true) KDA_ONE(128, 16, true)
+#undef KDA_ONE
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace kda
