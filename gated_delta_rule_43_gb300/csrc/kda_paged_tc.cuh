@@ -80,12 +80,20 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, ok != 0);
 }
 
-// 32 lanes x 32 consecutive columns of tensor memory into v[0 ..]; nothing may be used before
+// 32 lanes x 4, 8, 16 or 32 consecutive columns of tensor memory; nothing may be used before
 // tmem_ld_wait
-__device__ __forceinline__ void tmem_ld32_at(uint32_t taddr, float *v) {
-    float(&x)[32] = *reinterpret_cast<float(*)[32]>(v);
-    tmem_ld32(taddr, x);
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) { tmem_ld16(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "

@@ -72,8 +72,8 @@ bool cache_ok(const kda_paged_cache *p) {
         return false;
     if (p->dtype == KDA_E4M3)
         return (p->num_pages == 0 || (p->k_scales && p->v_scales && p->k_scales != p->v_scales)) &&
-               aligned(p->k_scales, 4) && aligned(p->v_scales, 4) &&
-               p->scale_stride >= (int64_t)p->Hk * p->page_size &&
+               aligned(p->k_scales, 16) && aligned(p->v_scales, 16) &&
+               p->scale_stride >= (int64_t)p->Hk * p->page_size && p->scale_stride % 4 == 0 &&
                (p->num_pages == 0 || p->scale_stride <= ((int64_t)1 << 58) / p->num_pages);
     return !p->k_scales && !p->v_scales;
 }

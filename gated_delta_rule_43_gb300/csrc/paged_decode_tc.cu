@@ -12,16 +12,19 @@
 // keys' and values' bytes need no conversion: nothing but the products touches them.  A key's scale
 // multiplies its scores, a value's is part of its weight.
 //
-// A piece of up to 8 tiles is gone through twice, keys, then values: all its scores stand in tensor memory
+// A piece of up to 4 tiles is gone through twice, keys, then values: all its scores stand in tensor memory
 // before the first weight is formed, so its maximum is known and nothing that the tensor cores add up
-// is rescaled.  Pieces are joined in registers, a thread a channel.
+// is rescaled.  Pieces are joined in registers, a thread a channel.  Loads and products take the keys of
+// a piece before the values of the one before, so that weights are formed while keys arrive (in pieces of
+// 8, one after the other, with the scales looked up by those who form the weights, 256 sequences of e4m3
+// took 671 us).
 //
 // The work is cut as for chunks (kda_paged_tc.cuh): an item is a sequence, a key/value head and up to `each`
 // query heads; each CTA finds its own range (a scan over the lengths, 1 us) instead of waiting for a
 // plan.  What cuts inside items leave is joined by paged_join_kernel.
 //
 //   warps 0-3   scores -> weights; outputs      warp 4   products       warp 5   loads
-//   warp 6      goes through the items          warp 7   queries        warp 8   zeroes slots behind the end
+//   warp 6      goes through the items          warp 7   queries        warp 8   zeroes values behind the end
 #include "kda_paged_tc.cuh"
 
 namespace kda {
@@ -31,7 +34,7 @@ namespace one {
 
 constexpr int kThreads = 288;
 constexpr int kMmaWarp = 4, kLoadWarp = 5, kItemWarp = 6, kQueryWarp = 7;   // (the last zeroes)
-constexpr int kTiles = 8;           // of a piece
+constexpr int kTiles = 4;           // of a piece
 constexpr int kItemCost = 1;        // an item's queries and outputs, in tiles
 constexpr int kUncut = 2;           // tiles of an item that is not cut
 constexpr int kRing = 4;            // items known ahead
@@ -50,10 +53,12 @@ __device__ __forceinline__ int pieces(int tiles) { return (tiles + kTiles - 1) /
 __device__ __forceinline__ int piece_at(int tiles, int count, int u) { return tiles * u / count; }
 
 template <int D, int NR, bool E4M3> struct Map {
-    static constexpr int N = E4M3 ? 2 * NR : 16;             // columns of a product
+    static constexpr int kCols = E4M3 ? 2 * NR : NR;         // columns in use: heads; (e4m3) their second parts
+    static constexpr int N = kCols < 16 ? 16 : kCols;        // of a product
     static constexpr uint32_t kTile = 128 * D * (E4M3 ? 1 : 2);
     static constexpr uint32_t kQBytes = 4096, kPTile = N * (E4M3 ? 128 : 256);
-    static constexpr uint32_t kQ = 0, kP = 2 * kQBytes, kKV = kP + kTiles * kPTile;
+    static constexpr uint32_t kScaleBytes = E4M3 ? 2 * kTiles * 512 : 0;   // of a piece: keys', then values'
+    static constexpr uint32_t kQ = 0, kP = 2 * kQBytes, kScales = kP + 2 * kTiles * kPTile, kKV = kScales + 2 * kScaleBytes;
     static constexpr uint32_t kSmall = 4096;                 // what stands behind the ring
     static constexpr int kFit = (232448 - kKV - kSmall) / kTile, kStages = kFit > 16 ? 16 : kFit;
     static constexpr uint32_t kItems = kKV + kStages * kTile;
@@ -61,12 +66,13 @@ template <int D, int NR, bool E4M3> struct Map {
     static constexpr uint32_t kRed = kQf + 128;                        // [2][4][32]: warps' maxima, sums
     static constexpr uint32_t kBar = kRed + 1024;
     static constexpr int kFull = 0, kFree = kStages, kQFull = 2 * kStages, kQFree = kQFull + 2, kSReady = kQFree + 2,
-                         kPReady = kSReady + 1, kODone = kPReady + 1, kOFree = kODone + 1, kItemFull = kOFree + 1,
+                         kPReady = kSReady + 2, kODone = kPReady + 2, kItemFull = kODone + 2,
                          kItemFree = kItemFull + kRing, kFixAsked = kItemFree + kRing, kFixed = kFixAsked + 1,
-                         kDrain = kFixed + 1, kBars = kDrain + 1;
+                         kDrain = kFixed + 1, kScFull = kDrain + 1, kScFree = kScFull + 2,
+                         kBars = kScFree + 2;
     static constexpr uint32_t kFound = kBar + kBars * 8, kCuts = kFound + 16, kScan = kCuts + 48, kSlot = kScan + 80,
-                              kBytes = kSlot + 16;
-    static_assert(kKV % 1024 == 0 && kPTile % 1024 == 0 && kBytes <= 232448 && kBytes - kItems <= kSmall && kFound % 8 == 0 &&
+                              kFix = kSlot + 16, kBytes = kFix + 16;
+    static_assert(kStages >= 4 && kKV % 1024 == 0 && kPTile % 1024 == 0 && kBytes <= 232448 && kBytes - kItems <= kSmall && kFound % 8 == 0 &&
                       N * (E4M3 ? 128 : 2 * D) <= kQBytes && sizeof(Cut) <= 24,
                   "layout");
 };
@@ -138,7 +144,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                     float scale, int window, int sinks) {
     extern __shared__ __align__(1024) uint8_t sm[];
     using M = Map<D, NR, E4M3>;
-    constexpr int N = M::N;
+    constexpr int N = M::N, C = M::kCols;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     let_next_start();
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + M::kBar);
@@ -163,13 +169,16 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             mbar_init(&bar[M::kQFull + i], 1);
             mbar_init(&bar[M::kQFree + i], 5);
         }
-        mbar_init(&bar[M::kSReady], 1);
-        mbar_init(&bar[M::kPReady], 4);
-        mbar_init(&bar[M::kODone], 1);
-        mbar_init(&bar[M::kOFree], 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar[M::kSReady + i], 1);
+            mbar_init(&bar[M::kPReady + i], 4);
+            mbar_init(&bar[M::kODone + i], 1);
+            mbar_init(&bar[M::kScFull + i], 1);
+            mbar_init(&bar[M::kScFree + i], 4);
+        }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&bar[M::kItemFull + i], 1);
-            mbar_init(&bar[M::kItemFree + i], 8);
+            mbar_init(&bar[M::kItemFree + i], 7);
         }
         mbar_init(&bar[M::kFixAsked], 1);
         mbar_init(&bar[M::kFixed], 1);
@@ -224,7 +233,8 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
     tc_fence_after();
     const uint32_t tmem = *tslot;
     if (tid < 2 && (tid == 0 || blockIdx.x + 1 == p.ranges)) p.cuts[blockIdx.x + tid] = cuts[tid];
-    const uint32_t tO = tmem + kTiles * N;
+    const uint32_t tO = tmem + 2 * kTiles * N;   // behind two pieces' scores
+    volatile int *fix = reinterpret_cast<volatile int *>(sm + M::kFix);
     bool ok = true;
     auto wait = [&](int which, uint32_t parity) {
         ok = ok && wait_warp(bars + 8 * which, parity);
@@ -233,7 +243,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
     auto each_item = [&](auto role) {
         Ring at;
         while (wait(M::kItemFull + at.stage, at.phase)) {
-            const Item it = items[at.stage];
+            const Item &it = items[at.stage];   // (read where it is used: registers are few)
             if (it.n < 0) break;
             role(it);
             __syncwarp();
@@ -244,162 +254,203 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
     };
     Ring kv;            // fills of the ring of tiles (a piece's keys, its values, ...)
     Ring qs;            // of the two places of queries
-    uint32_t loads = 0; // (load warp) fills issued
+    Ring ps;            // of those of a piece's scores, scales, weights and outputs
+    uint32_t loads = 0, pieces_loaded = 0;   // (load warp) fills issued
 
     if (warp < 4) {
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
         const float f = scale * kLog2e;
-        uint32_t phase = 0, turn = 0;   // of what happens once a piece; of the maxima's places
+        uint32_t turn = 0;   // of the maxima's places
         float *red = reinterpret_cast<float *>(sm + M::kRed);
         each_item([&](const Item &it) {
             float run_m[NR], run_l[NR], run_o[NR];
+            float keep[NR], add[NR];   // what the outputs so far and those of the last piece count for
 #pragma unroll
             for (int g = 0; g < NR; ++g) {
                 run_m[g] = -INFINITY;
-                run_l[g] = run_o[g] = 0.f;
+                run_l[g] = run_o[g] = keep[g] = add[g] = 0.f;
             }
+            Ring done;                 // the last piece's place
+            auto outputs = [&] {
+                if (!wait(M::kODone + done.stage, done.phase)) return false;
+                tc_fence_after();
+                float y[C];
+                tmem_ld(tO + done.stage * N + lanes, y);
+                tmem_ld_wait();
+                tc_fence_before();
+#pragma unroll
+                for (int g = 0; g < NR; ++g)
+                    run_o[g] = run_o[g] * keep[g] + (E4M3 ? y[g] + 0.0625f * y[(E4M3 ? NR : 0) + g] : y[g]) * add[g];
+                return true;
+            };
             const int tiles = it.k1 - it.k0, count = pieces(tiles);
-            const int lowest = window > 0 ? it.pos - window : -1;   // keys above it are in the window
+            const int pos = it.pos, lowest = window > 0 ? pos - window : -1;   // keys above it are in the window
+            // (heads four at a time: a branch a head leaves the chains of instructions one behind the
+            // other, 8.5k cycles a piece where the memory takes 5.8k)
+            const int rows = it.rows;
             const float *qf = reinterpret_cast<const float *>(sm + M::kQf) + 16 * qs.stage;
             if (tiles > 0 && !wait(M::kQFull + qs.stage, qs.phase)) return;
             for (int u = 0; u < count; ++u) {
                 const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
-                // this thread's key of each tile, whether it is visible, and (e4m3) its scales
+                // this thread's key of each tile: whether it is visible, and (e4m3) its scales
                 uint32_t seen = 0;
-                float ks[kTiles], ev[kTiles], vs[kTiles];
+                float ks[kTiles], ev[kTiles];
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    ks[t] = vs[t] = 1.f;
-                    ev[t] = 0.f;
-                    if (t >= many) continue;
                     const int key = it.tile(first + t) * BK + tid;
-                    const bool see = key <= it.pos && (key > lowest || key < sinks);
-                    seen |= (uint32_t)see << t;
-                    if (E4M3 && see) {
-                        const int page = c.table[(int64_t)it.n * c.width + (key >> c.shift)];
-                        if (page >= 0 && page < c.P) {
-                            const int64_t at = page * c.scale_stride + ((int64_t)it.h << c.shift) + (key & ((1 << c.shift) - 1));
-                            ks[t] = c.ks[at];
-                            vs[t] = c.vs[at];
-                        }
+                    seen |= (uint32_t)(t < many && key <= pos && (key > lowest || key < sinks)) << t;
+                }
+                if (E4M3) {
+                    if (!wait(M::kScFull + ps.stage, ps.phase)) return;
+                    const float *sc = reinterpret_cast<const float *>(sm + M::kScales + ps.stage * M::kScaleBytes);
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t) {   // (what is behind the piece's tiles is not seen)
+                        ks[t] = sc[128 * t + tid];
+                        ev[t] = (float)((int)(__float_as_uint(sc[128 * (kTiles + t) + tid]) >> 23) - 127);
                     }
                 }
-                if (!wait(M::kSReady, phase)) return;
+                if (!wait(M::kSReady + ps.stage, ps.phase)) return;
                 tc_fence_after();
-                // A tile's scores in units of log 2, -inf where the key is not visible
-                auto scores = [&](int t, float(&x)[NR]) {
+                // The scores in units of log 2, -inf where the key is not visible, and the piece's maxima: m
+                // of the scores; (e4m3) m2 of the weights with the values' scales
+                const uint32_t tS = tmem + lanes + ps.stage * kTiles * N;
+                // (held from there on for up to 8 heads, read again for 16: registers)
+                constexpr int kHeld = NR <= 8 ? kTiles : 1, kTogether = C <= 16 ? kTiles : 1;
+                float x[kHeld][NR], m[NR], m2[NR];
+                auto scores = [&](const float(&y)[C], int t, float(&x)[NR]) {
                     const bool see = (seen >> t) & 1;
-                    if constexpr (E4M3) {
-                        float y[N];
-                        if constexpr (N == 16) tmem_ld16(tmem + lanes + t * N, y);
-                        else tmem_ld32(tmem + lanes + t * N, y);
-                        tmem_ld_wait();
 #pragma unroll
-                        for (int g = 0; g < NR; ++g)
-                            x[g] = see ? (y[g] + 0.0625f * y[NR + g]) * (ks[t] * qf[g]) : -INFINITY;
-                    } else {
-                        float y[16];
-                        tmem_ld16(tmem + lanes + t * N, y);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int g = 0; g < NR; ++g) x[g] = see ? y[g] * f : -INFINITY;
-                    }
+                    for (int g = 0; g < NR; ++g)
+                        x[g] = !see ? -INFINITY : E4M3 ? (y[g] + 0.0625f * y[(E4M3 ? NR : 0) + g]) * (ks[t] * qf[g]) : y[g] * f;
                 };
-                // The piece's maxima: m of the scores; (e4m3) m2 of the weights with the values' scales
-                float m[NR], m2[NR];
 #pragma unroll
                 for (int g = 0; g < NR; ++g) m[g] = m2[g] = -INFINITY;
-                if (E4M3) {
 #pragma unroll
-                    for (int t = 0; t < kTiles; ++t) ev[t] = (float)((int)(__float_as_uint(vs[t]) >> 23) - 127);
-                }
+                for (int t0 = 0; t0 < kTiles; t0 += kTogether) {
+                    float y[kTogether][C];
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    if (t >= many) break;
-                    float x[NR];
-                    scores(t, x);
+                    for (int t = 0; t < kTogether; ++t) tmem_ld(tS + (t0 + t) * N, y[t]);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int g = 0; g < NR; ++g) {
-                        m[g] = fmaxf(m[g], x[g]);
-                        if (E4M3) m2[g] = fmaxf(m2[g], x[g] + ev[t]);
+                    for (int t = 0; t < kTogether; ++t) {
+                        float(&z)[NR] = x[kHeld > 1 ? t0 + t : 0];
+                        scores(y[t], t0 + t, z);
+#pragma unroll
+                        for (int g = 0; g < NR; ++g) {
+                            m[g] = fmaxf(m[g], z[g]);
+                            if (E4M3) m2[g] = fmaxf(m2[g], z[g] + ev[t0 + t]);
+                        }
                     }
                 }
                 float *place = red + 128 * (turn & 1);
                 ++turn;
 #pragma unroll
-                for (int g = 0; g < NR; ++g) {
-                    if (g >= it.rows) break;
-                    const float a = warp_top(m[g]), b = E4M3 ? warp_top(m2[g]) : 0.f;
+                for (int g0 = 0; g0 < NR; g0 += 4) {
+                    if (g0 >= rows) break;
+                    float a[4], b[4];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        a[g] = warp_top(m[g0 + g]);
+                        if (E4M3) b[g] = warp_top(m2[g0 + g]);
+                    }
                     if (lane == 0) {
-                        place[32 * warp + g] = a;
-                        if (E4M3) place[32 * warp + 16 + g] = b;
+                        *reinterpret_cast<float4 *>(place + 32 * warp + g0) = make_float4(a[0], a[1], a[2], a[3]);
+                        if (E4M3) *reinterpret_cast<float4 *>(place + 32 * warp + 16 + g0) = make_float4(b[0], b[1], b[2], b[3]);
                     }
                 }
                 named_bar_sync(1, 128);
                 float l[NR];
 #pragma unroll
-                for (int g = 0; g < NR; ++g) {
-                    l[g] = 0.f;
-                    if (g >= it.rows) break;
-                    m[g] = fmaxf(fmaxf(place[g], place[32 + g]), fmaxf(place[64 + g], place[96 + g]));
-                    if (E4M3) m2[g] = fmaxf(fmaxf(place[16 + g], place[48 + g]), fmaxf(place[80 + g], place[112 + g]));
+                for (int g0 = 0; g0 < NR; g0 += 4) {
+                    if (g0 >= rows) break;
+#pragma unroll
+                    for (int e = 0; e < (E4M3 ? 2 : 1); ++e) {
+                        float4 w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4 *>(place + 32 * i + 16 * e + g0);
+                        float *to = e ? &m2[g0] : &m[g0];
+                        to[0] = fmaxf(fmaxf(w[0].x, w[1].x), fmaxf(w[2].x, w[3].x));
+                        to[1] = fmaxf(fmaxf(w[0].y, w[1].y), fmaxf(w[2].y, w[3].y));
+                        to[2] = fmaxf(fmaxf(w[0].z, w[1].z), fmaxf(w[2].z, w[3].z));
+                        to[3] = fmaxf(fmaxf(w[0].w, w[1].w), fmaxf(w[2].w, w[3].w));
+                    }
+#pragma unroll
+                    for (int g = g0; g < g0 + 4; ++g) l[g] = 0.f;
                 }
                 // The weights, as the products' columns
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    if (t >= many) break;
-                    float x[NR];
-                    scores(t, x);
-                    uint8_t *to = sm + M::kP + t * M::kPTile;
+                for (int g0 = 0; g0 < NR; g0 += 4) {
+                    if (g0 >= rows) break;
+                    float r[4], r2[4];
 #pragma unroll
-                    for (int g = 0; g < NR; g += 2) {
-                        if (g >= it.rows) break;
-                        const float r0 = m[g] == -INFINITY ? 0.f : m[g], r1 = m[g + 1] == -INFINITY ? 0.f : m[g + 1];
-                        const float p0 = ex2(x[g] - r0), p1 = ex2(x[g + 1] - r1);
-                        l[g] += p0;
-                        l[g + 1] += p1;
+                    for (int g = 0; g < 4; ++g) {
+                        r[g] = m[g0 + g] == -INFINITY ? 0.f : m[g0 + g];
+                        r2[g] = m2[g0 + g] == -INFINITY ? 0.f : m2[g0 + g] - 8.f;
+                    }
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t) {
+                        if constexpr (kHeld == 1) {
+                            float y[C];
+                            tmem_ld(tS + t * N, y);
+                            tmem_ld_wait();
+                            scores(y, t, x[0]);
+                        }
+                        const float(&z)[NR] = x[kHeld > 1 ? t : 0];
+                        uint8_t *to = sm + M::kP + (ps.stage * kTiles + t) * M::kPTile;
+                        float p[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            p[g] = ex2(z[g0 + g] - r[g]);
+                            l[g0 + g] += p[g];
+                        }
                         if constexpr (E4M3) {
-                            const float s0 = m2[g] == -INFINITY ? 0.f : m2[g] - 8.f, s1 = m2[g + 1] == -INFINITY ? 0.f : m2[g + 1] - 8.f;
-                            const uint32_t w = split_e4m3(ex2(x[g] + ev[t] - s0), ex2(x[g + 1] + ev[t] - s1));
-                            const uint32_t at = tid & 15, piece = tid >> 4;
-                            to[g * 128 + ((piece ^ (g & 7)) << 4) + at] = (uint8_t)w;
-                            to[(g + 1) * 128 + ((piece ^ ((g + 1) & 7)) << 4) + at] = (uint8_t)(w >> 8);
-                            to[(NR + g) * 128 + ((piece ^ (g & 7)) << 4) + at] = (uint8_t)(w >> 16);
-                            to[(NR + g + 1) * 128 + ((piece ^ ((g + 1) & 7)) << 4) + at] = (uint8_t)(w >> 24);
+#pragma unroll
+                            for (int g = 0; g < 4; g += 2) {
+                                const uint32_t w = split_e4m3(ex2(z[g0 + g] + ev[t] - r2[g]), ex2(z[g0 + g + 1] + ev[t] - r2[g + 1]));
+                                const uint32_t at = tid & 15, piece = tid >> 4;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {   // (the row's place in its group of 8 is known here)
+                                    const int row = (i & 2 ? NR : 0) + g0 + g + (i & 1);
+                                    to[row * 128 + ((piece ^ (row & 7)) << 4) + at] = (uint8_t)(w >> (8 * i));
+                                }
+                            }
                         } else {
-                            const uint32_t w = pack2(p0, p1);
-                            *reinterpret_cast<uint16_t *>(to + sw128_offset(g, tid, 16)) = (uint16_t)w;
-                            *reinterpret_cast<uint16_t *>(to + sw128_offset(g + 1, tid, 16)) = (uint16_t)(w >> 16);
+#pragma unroll
+                            for (int g = 0; g < 4; g += 2) {
+                                const uint32_t w = pack2(p[g], p[g + 1]);
+                                *reinterpret_cast<uint16_t *>(to + sw128_offset(g0 + g, tid, 16)) = (uint16_t)w;
+                                *reinterpret_cast<uint16_t *>(to + sw128_offset(g0 + g + 1, tid, 16)) = (uint16_t)(w >> 16);
+                            }
                         }
                     }
                 }
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[M::kPReady]);
+                if (lane == 0) {
+                    mbar_arrive(&bar[M::kPReady + ps.stage]);
+                    if (E4M3) mbar_arrive(&bar[M::kScFree + ps.stage]);
+                }
                 __syncwarp();
-                if (!wait(M::kODone, phase)) return;
-                phase ^= 1;
-                tc_fence_after();
-                float y[N];
-                if constexpr (N == 16) tmem_ld16(tO + lanes, y);
-                else tmem_ld32(tO + lanes, y);
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[M::kOFree]);
-                __syncwarp();
+                // the outputs of the piece before, whose product has run meanwhile
+                if (u > 0 && !outputs()) return;
+                done = ps;
+                ps.step(2);
 #pragma unroll
-                for (int g = 0; g < NR; ++g) {
-                    if (g >= it.rows) break;
-                    const float top = fmaxf(run_m[g], m[g]), ref = top == -INFINITY ? 0.f : top;
-                    const float a = ex2(run_m[g] - ref), b = ex2(m[g] - ref);
-                    const float add = E4M3 ? (y[g] + 0.0625f * y[(E4M3 ? NR : 0) + g]) * ex2(m2[g] - 8.f - ref) : y[g] * b;
-                    run_l[g] = run_l[g] * a + l[g] * b;
-                    run_o[g] = run_o[g] * a + add;
-                    run_m[g] = top;
+                for (int g0 = 0; g0 < NR; g0 += 4) {
+                    if (g0 >= rows) break;
+#pragma unroll
+                    for (int g = g0; g < g0 + 4; ++g) {
+                        const float top = fmaxf(run_m[g], m[g]), ref = top == -INFINITY ? 0.f : top;
+                        const float b = ex2(m[g] - ref);
+                        keep[g] = ex2(run_m[g] - ref);
+                        add[g] = E4M3 ? ex2(m2[g] - 8.f - ref) : b;
+                        run_l[g] = run_l[g] * keep[g] + l[g] * b;
+                        run_m[g] = top;
+                    }
                 }
             }
+            if (tiles > 0 && !outputs()) return;
             if (tiles > 0) {
                 if (lane == 0) mbar_arrive(&bar[M::kQFree + qs.stage]);
                 __syncwarp();
@@ -409,17 +460,19 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             float *place = red + 128 * (turn & 1);
             ++turn;
 #pragma unroll
-            for (int g = 0; g < NR; ++g) {
-                if (g >= it.rows) break;
-                const float x = warp_sum(run_l[g]);
-                if (lane == 0) place[32 * warp + g] = x;
+            for (int g0 = 0; g0 < NR; g0 += 4) {
+                if (g0 >= rows) break;
+                float a[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) a[g] = warp_sum(run_l[g0 + g]);
+                if (lane == 0) *reinterpret_cast<float4 *>(place + 32 * warp + g0) = make_float4(a[0], a[1], a[2], a[3]);
             }
             named_bar_sync(1, 128);
             const int d = D == 128 ? tid : 16 * warp + lane;   // (64 rows of a product stand in 16 lanes of each warp)
             const bool there = D == 128 || lane < 16;
 #pragma unroll
             for (int g = 0; g < NR; ++g) {
-                if (g >= it.rows) break;
+                if (g >= rows) break;
                 const float l = place[g] + place[32 + g] + place[64 + g] + place[96 + g];
                 if (it.slot >= 0) {
                     const int64_t at = (int64_t)it.slot * p.rows + g;
@@ -432,7 +485,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             }
         });
     } else if (warp == kMmaWarp) {
-        uint32_t phase = 0, fix_phase = 0;
+        uint32_t fix_phase = 0;
         constexpr uint32_t id_s = E4M3 ? idesc_e4m3(128, N, false) : idesc_bf16(128, N, false, false);
         constexpr uint32_t id_o = E4M3 ? idesc_e4m3(D, N, true) : idesc_bf16(D, N, true, false);
         // keys: rows of 128 bytes (64 for e4m3 heads of 64), channels along them; values the other way round
@@ -440,9 +493,52 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
         const uint64_t dk0 = narrow ? sdesc_sw64(base + M::kKV, 16, 512) : sdesc_sw128(base + M::kKV, 16, 1024);
         const uint64_t dv0 = narrow ? sdesc_sw64(base + M::kKV, 16, 512) : sdesc_sw128(base + M::kKV, BK * 128, 1024);
         const uint64_t dq0 = sdesc_sw128(base + M::kQ, 16, 1024), dp0 = sdesc_sw128(base + M::kP, 16, 1024);
+        // the piece whose values are still to come: its tiles, and what the last lacks (0: nothing)
+        int owed = 0, owed_left = 0;
+        Ring os;   // its place
+        auto values = [&] {
+            if (owed == 0) return;
+            if (!wait(M::kPReady + os.stage, os.phase)) return;
+            for (int t = 0; t < owed; ++t) {
+                if (!wait(M::kFull + kv.stage, kv.phase)) return;
+                if (owed_left && t + 1 == owed) {
+                    if (lane == 0) {
+                        fix[0] = kv.stage;
+                        fix[1] = owed_left;
+                        mbar_arrive(&bar[M::kFixAsked]);
+                    }
+                    __syncwarp();
+                    if (!wait(M::kFixed, fix_phase)) return;
+                    fix_phase ^= 1;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t dv = desc_add(dv0, kv.stage * M::kTile), dp = desc_add(dp0, (os.stage * kTiles + t) * M::kPTile);
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int s = 0; s < BK / 32; ++s)
+                            umma_f8(tO + os.stage * N, desc_add(dv, s * 32 * D), desc_add(dp, s * 32), id_o, t > 0 || s > 0);
+                    } else {
+#pragma unroll
+                        for (int s = 0; s < BK / 16; ++s)
+                            umma_bf16(tO + os.stage * N, desc_add(dv, s * 2048), desc_add(dp, (s >> 2) * 2048 + (s & 3) * 32), id_o,
+                                      t > 0 || s > 0);
+                    }
+                    umma_commit(&bar[M::kFree + kv.stage]);
+                    if (t + 1 == owed) umma_commit(&bar[M::kODone + os.stage]);
+                }
+                __syncwarp();
+                kv.step(M::kStages);
+            }
+            owed = 0;
+            os.step(2);
+        };
         each_item([&](const Item &it) {
             const int tiles = it.k1 - it.k0, count = pieces(tiles);
-            if (tiles == 0) return;
+            if (tiles == 0) {   // (nothing may be owed over items that have none: the ring of items is short)
+                values();
+                return;
+            }
             if (!wait(M::kQFull + qs.stage, qs.phase)) return;
             for (int u = 0; u < count; ++u) {
                 const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
@@ -451,110 +547,140 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                     tc_fence_after();
                     if (elect_one()) {
                         const uint64_t dk = desc_add(dk0, kv.stage * M::kTile), dq = desc_add(dq0, qs.stage * M::kQBytes);
+                        const uint32_t to = tmem + (ps.stage * kTiles + t) * N;
                         if constexpr (E4M3) {
 #pragma unroll
                             for (int s = 0; s < D / 32; ++s)
-                                umma_f8(tmem + t * N, desc_add(dk, s * 32), desc_add(dq, s * 32), id_s, s > 0);
+                                umma_f8(to, desc_add(dk, s * 32), desc_add(dq, s * 32), id_s, s > 0);
                         } else {
 #pragma unroll
                             for (int s = 0; s < D / 16; ++s)
-                                umma_bf16(tmem + t * N, desc_add(dk, (s >> 2) * 16384 + (s & 3) * 32),
+                                umma_bf16(to, desc_add(dk, (s >> 2) * 16384 + (s & 3) * 32),
                                           desc_add(dq, (s >> 2) * 2048 + (s & 3) * 32), id_s, s > 0);
                         }
                         umma_commit(&bar[M::kFree + kv.stage]);
                         if (t + 1 == many) {
-                            umma_commit(&bar[M::kSReady]);
+                            umma_commit(&bar[M::kSReady + ps.stage]);
                             if (u + 1 == count) umma_commit(&bar[M::kQFree + qs.stage]);
                         }
                     }
                     __syncwarp();
                     kv.step(M::kStages);
                 }
-                if (!wait(M::kPReady, phase) || !wait(M::kOFree, phase ^ 1)) return;
-                phase ^= 1;
-                for (int t = 0; t < many; ++t) {
-                    if (!wait(M::kFull + kv.stage, kv.phase)) return;
-                    if (it.ctx - it.tile(first + t) * BK < BK && (it.ctx & ((1 << c.shift) - 1)) != 0) {
-                        if (lane == 0) mbar_arrive(&bar[M::kFixAsked]);
-                        __syncwarp();
-                        if (!wait(M::kFixed, fix_phase)) return;
-                        fix_phase ^= 1;
-                    }
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t dv = desc_add(dv0, kv.stage * M::kTile), dp = desc_add(dp0, t * M::kPTile);
-                        if constexpr (E4M3) {
-#pragma unroll
-                            for (int s = 0; s < BK / 32; ++s)
-                                umma_f8(tO, desc_add(dv, s * 32 * D), desc_add(dp, s * 32), id_o, t > 0 || s > 0);
-                        } else {
-#pragma unroll
-                            for (int s = 0; s < BK / 16; ++s)
-                                umma_bf16(tO, desc_add(dv, s * 2048), desc_add(dp, (s >> 2) * 2048 + (s & 3) * 32), id_o,
-                                          t > 0 || s > 0);
-                        }
-                        umma_commit(&bar[M::kFree + kv.stage]);
-                        if (t + 1 == many) umma_commit(&bar[M::kODone]);
-                    }
-                    __syncwarp();
-                    kv.step(M::kStages);
-                }
+                ps.step(2);
+                values();
+                if (!ok) return;
+                owed = many;
+                const int left = it.ctx - it.tile(first + many - 1) * BK;   // (below BK only in an item's last tile)
+                owed_left = left < BK && (it.ctx & ((1 << c.shift) - 1)) != 0 ? left : 0;
             }
             qs.step(2);
         });
+        if (ok) values();
+        if (lane == 0) {
+            fix[0] = -1;
+            mbar_arrive(&bar[M::kFixAsked]);
+        }
+        __syncwarp();
     } else if (warp == kLoadWarp) {
         const int rows = min(BK, 1 << c.shift), boxes = BK / rows;
+        // the piece whose values are still to be loaded: its tiles, this lane's boxes of them, its head
+        int owed = 0, owed_page[kTiles], owed_row[kTiles], owed_h = 0;
+        auto load = [&](const void *map, int many, const int(&page)[kTiles], const int(&row)[kTiles], int h) {
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                if (t >= many) break;
+                if (!wait(M::kFree + kv.stage, kv.phase ^ 1)) return;
+                if (lane == 0) mbar_arrive_expect_tx(&bar[M::kFull + kv.stage], M::kTile);
+                __syncwarp();
+                if (lane < boxes) {
+                    const uint32_t to = base + M::kKV + kv.stage * M::kTile, done = bars + 8 * (M::kFull + kv.stage);
+                    if (E4M3) {
+                        tma_load_page(to + lane * rows * D, map, 0, row[t], h, page[t], done);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_page(to + x * 16384 + lane * rows * 128, map, 64 * x, row[t], h, page[t], done);
+                    }
+                }
+                __syncwarp();
+                kv.step(M::kStages);
+                ++loads;
+            }
+        };
+        auto owed_values = [&] {
+            if (owed) load(&tv, owed, owed_page, owed_row, owed_h);
+            owed = 0;
+        };
         each_item([&](const Item &it) {
             const int tiles = it.k1 - it.k0, count = pieces(tiles);
+            if (tiles == 0) owed_values();
             for (int u = 0; u < count; ++u) {
                 const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
                 // the pages of this lane's boxes of the piece's tiles; P: rows that nobody sees, or no page
-                int page[kTiles];
+                int page[kTiles], row[kTiles];
+                uint32_t seen = 0;
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
                     page[t] = c.P;
-                    if (t >= many || lane >= boxes) continue;
                     const int key = it.tile(first + t) * BK + lane * rows;
-                    if (key <= it.pos && (window <= 0 || key < sinks || key + rows > it.pos - window + 1))
+                    row[t] = key & ((1 << c.shift) - 1);
+                    if (t < many && lane < boxes && key <= it.pos &&
+                        (window <= 0 || key < sinks || key + rows > it.pos - window + 1)) {
                         page[t] = c.table[(int64_t)it.n * c.width + (key >> c.shift)];
+                        seen |= 1u << t;
+                    }
                 }
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    if (t >= many || lane >= boxes) continue;
-                    const int key = it.tile(first + t) * BK + lane * rows;
-                    if (key <= it.pos && (window <= 0 || key < sinks || key + rows > it.pos - window + 1) &&
-                        (page[t] < 0 || page[t] >= c.P)) {
+                    if (((seen >> t) & 1) && (page[t] < 0 || page[t] >= c.P)) {
                         report(st, KDA_ERR_INVALID_ARG, it.n, 91);
                         page[t] = c.P;   // (past the last: zeros)
                     }
                 }
-#pragma unroll 1
-                for (int v = 0; v < 2; ++v) {
+                if (E4M3) {   // the piece's scales: a box's are one run of memory; no page: zeros
+                    if (!wait(M::kScFree + ps.stage, ps.phase ^ 1)) return;
+                    const uint32_t place = M::kScales + ps.stage * M::kScaleBytes;
+                    uint32_t copies = 0;
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) {
-                        if (t >= many) break;
-                        if (!wait(M::kFree + kv.stage, kv.phase ^ 1)) return;
-                        if (lane == 0) mbar_arrive_expect_tx(&bar[M::kFull + kv.stage], M::kTile);
-                        __syncwarp();
-                        if (lane < boxes) {
-                            const int row = (it.tile(first + t) * BK + lane * rows) & ((1 << c.shift) - 1);
-                            const uint32_t to = base + M::kKV + kv.stage * M::kTile, done = bars + 8 * (M::kFull + kv.stage);
-                            if (E4M3) {
-                                tma_load_page(to + lane * rows * D, v ? &tv : &tk, 0, row, it.h, page[t], done);
-                            } else {
-#pragma unroll
-                                for (int x = 0; x < D / 64; ++x)
-                                    tma_load_page(to + x * 16384 + lane * rows * 128, v ? &tv : &tk, 64 * x, row, it.h, page[t],
-                                                  done);
+                        const bool copied = t < many && lane < boxes && page[t] != c.P;
+                        copies += __popc(__ballot_sync(0xffffffffu, copied));
+                        if (t < many && lane < boxes && !copied)
+                            for (int x = 0; x < rows; x += 4) {
+                                *reinterpret_cast<float4 *>(sm + place + (128 * t + lane * rows + x) * 4) = make_float4(0, 0, 0, 0);
+                                *reinterpret_cast<float4 *>(sm + place + (128 * (kTiles + t) + lane * rows + x) * 4) =
+                                    make_float4(0, 0, 0, 0);
                             }
-                        }
-                        __syncwarp();
-                        kv.step(M::kStages);
-                        ++loads;
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(&bar[M::kScFull + ps.stage], copies * 8 * rows);
+                    __syncwarp();
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t) {
+                        if (t >= many || lane >= boxes || page[t] == c.P) continue;
+                        const int64_t at = page[t] * c.scale_stride + ((int64_t)it.h << c.shift) + row[t];
+                        bulk_g2s(sm + place + (128 * t + lane * rows) * 4, c.ks + at, 4 * rows, &bar[M::kScFull + ps.stage]);
+                        bulk_g2s(sm + place + (128 * (kTiles + t) + lane * rows) * 4, c.vs + at, 4 * rows,
+                                 &bar[M::kScFull + ps.stage]);
+                    }
+                    __syncwarp();
+                    ps.step(2);
+                    ++pieces_loaded;
+                }
+                load(&tk, many, page, row, it.h);
+                if (ok) owed_values();
+                if (!ok) return;
+                owed = many;
+                owed_h = it.h;
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    owed_page[t] = page[t];
+                    owed_row[t] = row[t];
                 }
             }
         });
+        if (ok) owed_values();
     } else if (warp == kItemWarp) {
         Ring at;
         Cut from = cuts[0];
@@ -635,13 +761,13 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                         hi |= (w & 0xffffu) << (8 * j);
                         lo |= (w >> 16) << (8 * j);
                     }
-                    const uint32_t at = lane * V, place = (((at >> 4) ^ (g & 7)) << 4) + (at & 15);
-                    if constexpr (V == 4) {
-                        *reinterpret_cast<uint32_t *>(to + g * 128 + place) = hi;
-                        *reinterpret_cast<uint32_t *>(to + (NR + g) * 128 + place) = lo;
-                    } else {
-                        *reinterpret_cast<uint16_t *>(to + g * 128 + place) = (uint16_t)hi;
-                        *reinterpret_cast<uint16_t *>(to + (NR + g) * 128 + place) = (uint16_t)lo;
+                    const uint32_t at = lane * V;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int row = i * NR + g;
+                        uint8_t *place = to + row * 128 + (((at >> 4) ^ (row & 7)) << 4) + (at & 15);
+                        if constexpr (V == 4) *reinterpret_cast<uint32_t *>(place) = i ? lo : hi;
+                        else *reinterpret_cast<uint16_t *>(place) = (uint16_t)(i ? lo : hi);
                     }
                     if (lane == 0) qf[g] = fine ? two_to(e) * scale * kLog2e : __int_as_float(0x7fffffff);
                 }
@@ -658,29 +784,20 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             qs.step(2);
         });
     } else {
-        uint32_t phase = 0;
-        each_item([&](const Item &it) {
-            const int tiles = it.k1 - it.k0;
-            for (int i = 0; i < 2 * tiles - 1; ++i) kv.step(M::kStages);
-            if (tiles > 0) {   // the values behind the sequence's end, in the tile that reaches past it: the last
-                const int left = it.ctx - it.tile(it.k1 - 1) * BK;
-                if (left < BK && (it.ctx & ((1 << c.shift) - 1)) != 0) {
-                    if (!wait(M::kFixAsked, phase)) return;
-                    phase ^= 1;
-                    constexpr int B = D * (E4M3 ? 1 : 2), W = B < 128 ? B : 128, U = W / 16;   // bytes of a row, in columns
-                    for (int x = left * U + lane; x < BK * U; x += 32)
+        // the values behind a sequence's end, in the tile that the products are about to read
+        for (uint32_t phase = 0; wait(M::kFixAsked, phase); phase ^= 1) {
+            const int stage = fix[0], left = fix[1];
+            if (stage < 0) break;
+            constexpr int B = D * (E4M3 ? 1 : 2), W = B < 128 ? B : 128, U = W / 16;   // bytes of a row, in columns
+            for (int x = left * U + lane; x < BK * U; x += 32)
 #pragma unroll
-                        for (int y = 0; y < B / W; ++y)
-                            *reinterpret_cast<uint4 *>(sm + M::kKV + kv.stage * M::kTile + y * BK * W + x * 16) =
-                                make_uint4(0, 0, 0, 0);
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar[M::kFixed]);
-                    __syncwarp();
-                }
-                kv.step(M::kStages);
-            }
-        });
+                for (int y = 0; y < B / W; ++y)
+                    *reinterpret_cast<uint4 *>(sm + M::kKV + stage * M::kTile + y * BK * W + x * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[M::kFixed]);
+            __syncwarp();
+        }
     }
     if (!ok && lane == 0) report(st, KDA_ERR_TIMEOUT, blockIdx.x, 92 + warp);
     if (__syncthreads_or(!ok)) {
@@ -696,6 +813,9 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
         if (warp == kLoadWarp)   // (only each stage's last load can be in flight)
             for (uint32_t x = loads >= (uint32_t)M::kStages ? loads - M::kStages : 0; x < loads; ++x)
                 mbar_wait(&bar[M::kFull + x % M::kStages], (x / M::kStages) & 1, kDrainNs);
+        if (warp == kLoadWarp && E4M3)
+            for (uint32_t x = pieces_loaded >= 2 ? pieces_loaded - 2 : 0; x < pieces_loaded; ++x)
+                mbar_wait(&bar[M::kScFull + (x & 1)], (x >> 1) & 1, kDrainNs);
         __syncthreads();
     }
     if (tid == 0) p.found[blockIdx.x] = *st;
@@ -711,7 +831,7 @@ struct Layout {
 };
 static Layout layout_of(int group, int D, int sms) {
     Layout L;
-    L.each = group <= 8 ? 8 : 16;
+    L.each = group <= 4 ? 4 : group <= 8 ? 8 : 16;
     L.rows = group < L.each ? group : L.each;
     L.ranges = sms;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -766,10 +886,11 @@ cudaError_t launch_paged_decode(bool e4m3, int D, const paged::Cache &c, const v
     using paged::tc::one::launch;
     uint8_t *w = (uint8_t *)ws;
 #define KDA_ONE(D_, NR_, E_) \
-    if (D == D_ && (group <= 8) == (NR_ == 8) && e4m3 == E_) \
+    if (D == D_ && group <= (NR_ == 16 ? 0x7fffffff : NR_) && e4m3 == E_) \
         return launch<D_, NR_, E_>(c, q, qs, o, group, scale, window, sinks, w, sms, s);
-    KDA_ONE(64, 8, false) KDA_ONE(64, 16, false) KDA_ONE(128, 8, false) KDA_ONE(128, 16, false)
-    KDA_ONE(64, 8, true) KDA_ONE(64, 16, true) KDA_ONE(128, 8, true) KDA_ONE(128, 16, true)
+#define KDA_ONES(D_, E_) KDA_ONE(D_, 4, E_) KDA_ONE(D_, 8, E_) KDA_ONE(D_, 16, E_)
+    KDA_ONES(64, false) KDA_ONES(128, false) KDA_ONES(64, true) KDA_ONES(128, true)
+#undef KDA_ONES
 #undef KDA_ONE
     return cudaErrorInvalidValue;
 }

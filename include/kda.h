@@ -471,8 +471,8 @@ kda_status kda_state_pool_compact(float *pool, int32_t P, int64_t slot_elems,
  *   k_pages, v_pages   [num_pages, Hk, page_size, D]   dtype; page_stride elements from one page to
  *                      the next (a multiple of 16 bytes, at least Hk * page_size * D), so that both
  *                      may be halves of one pool [num_pages, 2, Hk, page_size, D]
- *   k_scales, v_scales [num_pages, Hk, page_size] fp32, scale_stride from page to page, with dtype
- *                      KDA_E4M3 (NULL otherwise): a row of D values stands for scale * e4m3.  Scales
+ *   k_scales, v_scales [num_pages, Hk, page_size] fp32, scale_stride from page to page (a multiple of 4;
+ *                      16-byte aligned), with dtype KDA_E4M3 (NULL otherwise): a row of D values stands for scale * e4m3.  Scales
  *                      are powers of two, so scale * e4m3 is a bf16 exactly.
  *   block_table        [num_seqs, table_width] int32: position j of sequence n lies in slot
  *                      j % page_size of page block_table[n][j / page_size].  Entries that hold no

@@ -36,7 +36,7 @@ BAD_CACHE = [dict(lens=None), dict(table=None), dict(k=None), dict(v=None), dict
              dict(stride=2047), dict(stride=2052), dict(stride=0), dict(stride=1 << 60), dict(ks=6 * A),
              dict(vs=6 * A), dict(dtype=kda.KDA_E4M3), dict(dtype=kda.KDA_E4M3, ks=6 * A, vs=7 * A, ss=31),
              dict(dtype=kda.KDA_E4M3, ks=6 * A, vs=6 * A, ss=32),
-             dict(dtype=kda.KDA_E4M3, ks=6 * A + 2, vs=7 * A, ss=32),
+             dict(dtype=kda.KDA_E4M3, ks=6 * A + 4, vs=7 * A, ss=32), dict(dtype=kda.KDA_E4M3, ks=6 * A, vs=7 * A, ss=33),
              dict(N=-1), dict(width=-1), dict(pages=-1), dict(Hk=0), dict(Hk=-2), dict(width=1 << 27)]
 BAD_TYPES = [dict(D=48), dict(D=256), dict(D=0), dict(ps=8), dict(ps=48), dict(ps=2048), dict(ps=0), dict(ps=-16),
              dict(dtype=kda.KDA_F32), dict(dtype=3), dict(dtype=-1)]
