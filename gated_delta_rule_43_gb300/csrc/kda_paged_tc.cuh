@@ -115,14 +115,27 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
-// 4-D tiled load: the box at (channel, row of the page, head, page); pages past the last read as zeros
-__device__ __forceinline__ void tma_load_page(uint32_t dst, const void *tmap, int32_t c, int32_t row, int32_t head,
-                                              int32_t page, uint32_t bar) {
+// Rows of a run (a page's of one head) from `row` on, channels from c on: one box of page_map.  A run past
+// the last reads as zeros.
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const void *tmap, int32_t c, int32_t row, int32_t run,
+                                              uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(dst), "l"(tmap), "r"(c), "r"(row), "r"(head), "r"(page), "r"(bar)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(tmap), "r"(c), "r"(row), "r"(run), "r"(bar)
         : "memory");
+}
+// Zeroes the rows from `left` on of a tile of 128 rows of BYTES bytes (in columns of at most 128 bytes, one
+// behind the other); a whole warp, before the tile's products.
+template <int BYTES> __device__ __forceinline__ void clear_rows(uint8_t *tile, int left) {
+    constexpr int W = BYTES < 128 ? BYTES : 128, U = W / 16;   // a column's width; its 16-byte pieces
+    for (int x = left * U + (threadIdx.x & 31); x < BK * U; x += 32) {
+#pragma unroll
+        for (int i = 0; i < BYTES / W; ++i)
+            *reinterpret_cast<uint4 *>(tile + i * BK * W + x * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async();
+    __syncwarp();
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -206,21 +219,22 @@ inline EncodeTiledFn encode_tiled() {
     return fn;
 }
 
-// Pages [P, Hk, page size, D] of bf16 or e4m3 in boxes of up to 128 rows of a page x 128 bytes (64 for
-// e4m3 heads of 64), swizzled as the products want them.
+// Pages [P, Hk, page size, D] of bf16 or e4m3 as runs of rows, `page_runs` from one page's to the next's, in
+// boxes of up to 128 rows of a run x 128 bytes (64 for e4m3 heads of 64), swizzled as the products want them.
 inline int box_rows(const Cache &c) { return c.shift >= 7 ? 128 : 1 << c.shift; }
+__host__ __device__ inline int page_runs(const Cache &c, int D) { return (int)((c.stride / D) >> c.shift); }
 inline cudaError_t page_map(CUtensorMap *m, const Cache &c, const void *pages, int D, bool e4m3) {
     EncodeTiledFn enc = encode_tiled();
     if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t e = e4m3 ? 1 : 2;
-    const bool narrow = e4m3 && D == 64;
-    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)1 << c.shift, (cuuint64_t)c.Hk, (cuuint64_t)c.P};
-    const cuuint64_t strides[3] = {D * e, (D * e) << c.shift, (cuuint64_t)c.stride * e};
-    const cuuint32_t box[4] = {(cuuint32_t)(e4m3 ? D : 64), (cuuint32_t)box_rows(c), 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    const CUresult r = enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+    const cuuint64_t row = D * (e4m3 ? 1 : 2);
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)1 << c.shift,
+                                (cuuint64_t)(c.P - 1) * page_runs(c, D) + c.Hk};
+    const cuuint64_t strides[2] = {row, row << c.shift};
+    const cuuint32_t box[3] = {(cuuint32_t)(e4m3 ? D : 64), (cuuint32_t)box_rows(c), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                            const_cast<void *>(pages), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

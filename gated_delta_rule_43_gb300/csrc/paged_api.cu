@@ -67,7 +67,8 @@ bool cache_ok(const kda_paged_cache *p) {
         return false;
     if (p->num_pages > 0 && (!p->k_pages || !p->v_pages || p->k_pages == p->v_pages)) return false;
     if (!aligned(p->k_pages, 16) || !aligned(p->v_pages, 16)) return false;
-    if (p->page_stride < page || p->page_stride * bytes_of(p->dtype) % 16 != 0 ||
+    if (p->page_stride < page || p->page_stride % ((int64_t)p->page_size * p->D) != 0 ||
+        (p->num_pages > 0 && p->page_stride / ((int64_t)p->page_size * p->D) > 0x7fffffff / p->num_pages) ||
         (p->num_pages > 0 && p->page_stride > ((int64_t)1 << 58) / p->num_pages))
         return false;
     if (p->dtype == KDA_E4M3)

@@ -19,9 +19,9 @@
 // One CTA an SM:
 //   warps 0-3, 4-7   the rows of the two tiles: scores out of tensor memory, P into it (over the scores of
 //                    the keys from 64 on), outputs; the next item's queries into the place of this one's after the last scores
-//   warp 8           issues the products        warp 9    loads keys and values, page by page
+//   warp 8           issues the products (and zeroes values behind a sequence's end: slots that nobody has
+//                    written)                   warp 9    loads keys and values, page by page
 //   warp 10          goes through the range's items for everyone
-//   warp 11          zeroes the values behind a sequence's end (slots that nobody has written)
 //   warps 12-15      (e4m3 pages) make the operands out of the bytes that warp 9 loads: scale * e4m3 is a bf16
 //                    exactly, so the products are those of a bf16 cache
 // Products of one tile run while the other's scores become weights: P0 V, Q0 K', P1 V, Q1 K', ...
@@ -33,7 +33,7 @@ namespace tc {
 
 constexpr int kRows = 256;          // rows of an item
 template <bool E4M3> constexpr int kThreads = E4M3 ? 512 : 384;
-constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kEndWarp = 11, kMakeWarp = 12;
+constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kMakeWarp = 12;
 constexpr int kItemCost = 2;        // an item's queries and outputs, in blocks
 constexpr int kUncut = 6;           // blocks of an item that is not cut
 constexpr int kRing = 4;            // items known ahead
@@ -170,8 +170,7 @@ template <int D, bool E4M3> struct Map {
     // barriers
     static constexpr int kFull = 0, kFree = kStages, kQFull = 2 * kStages, kSReady = kQFull + 2,
                          kPReady = kSReady + 2, kODone = kPReady + 2, kItemFull = kODone + 2,
-                         kItemFree = kItemFull + kRing, kFixAsked = kItemFree + kRing, kFixed = kFixAsked + 1,
-                         kDrain = kFixed + 1, kRawFull = kDrain + 1, kRawFree = kRawFull + kRaws,
+                         kItemFree = kItemFull + kRing, kDrain = kItemFree + kRing, kRawFull = kDrain + 1, kRawFree = kRawFull + kRaws,
                          kBars = kRawFree + kRaws;
     static constexpr uint32_t kSlot = kBar + kBars * 8, kBytes = kSlot + 16;
     static_assert(sizeof(Item) % 8 == 0 && kBytes <= 232448 && kItems % 1024 == 0, "layout");
@@ -208,14 +207,12 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&bar[M::kItemFull + i], 1);
-            mbar_init(&bar[M::kItemFree + i], kRowWarps + (E4M3 ? 6 : 3));
+            mbar_init(&bar[M::kItemFree + i], kRowWarps + (E4M3 ? 6 : 2));
         }
         for (int i = 0; i < M::kRaws; ++i) {
             mbar_init(&bar[M::kRawFull + i], 1);
             mbar_init(&bar[M::kRawFree + i], 4);
         }
-        mbar_init(&bar[M::kFixAsked], 1);
-        mbar_init(&bar[M::kFixed], 1);
         mbar_init(&bar[M::kDrain], 1);
         fence_mbar_init();
     }
@@ -441,31 +438,8 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             tc_fence_before();
         });
     } else {
-        if (warp == kEndWarp) {
-            uint32_t phase = 0;
-            if (!E4M3) each_item([&](const Item &it) {
-                // the values behind the sequence's end, in the last block that reaches past it
-                for (int k = it.k0; k < it.k1; ++k) {
-                    const int left = it.ctx - it.block(k) * BK;   // (only of the list's last block below 128)
-                    if (left < BK && (it.ctx & ((1 << c.shift) - 1)) != 0) {
-                        if (!wait(M::kFixAsked, phase)) return;
-                        phase ^= 1;
-                        Ring at = kv;
-                        for (int i = 0; i < 2 * (k - it.k0) + 1; ++i) at.step(M::kStages);
-                        constexpr int U = D / 8;   // 16-byte pieces of a row
-                        for (int x = left * U + lane; x < BK * U; x += 32)
-                            *reinterpret_cast<uint4 *>(sm + M::kKV + at.stage * M::kTile + sw128_offset(x / U, 8 * (x % U), BK)) =
-                                make_uint4(0, 0, 0, 0);
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar[M::kFixed]);
-                        __syncwarp();
-                    }
-                }
-                for (int i = 0; i < 2 * (it.k1 - it.k0); ++i) kv.step(M::kStages);
-            });
-        } else if (warp == kMmaWarp) {
-            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, fix_phase = 0;
+        if (warp == kMmaWarp) {
+            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
             constexpr uint32_t id_s = idesc_bf16(128, BK, false, false), id_o = idesc_bf16(128, D, false, true);
             const uint64_t dq0 = sdesc_sw128(base + M::kQ, 16, 1024), dk0 = sdesc_sw128(base + M::kKV, 16, 1024),
                            dv0 = sdesc_sw128(base + M::kKV, BK * 128, 1024);
@@ -500,11 +474,10 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     key = val;
                     key.step(M::kStages);
                     if (!wait(M::kFull + val.stage, val.phase)) return;
-                    if (!E4M3 && it.ctx - it.block(it.k0 + j) * BK < BK && (it.ctx & ((1 << c.shift) - 1)) != 0) {
-                        if (lane == 0) mbar_arrive(&bar[M::kFixAsked]);
-                        __syncwarp();
-                        if (!wait(M::kFixed, fix_phase)) return;
-                        fix_phase ^= 1;
+                    if (!E4M3) {
+                        const int left = it.ctx - it.block(it.k0 + j) * BK;   // (below BK only in the list's last block)
+                        if (left < BK && (it.ctx & ((1 << c.shift) - 1)) != 0)
+                            clear_rows<2 * D>(sm + M::kKV + val.stage * M::kTile, left);
                     }
                     bool key_there = false;
 #pragma unroll
@@ -541,7 +514,8 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                 kv = key;
             });
         } else if (warp == kLoadWarp) {
-            const int rows = min(BK, 1 << c.shift), boxes = BK / rows;
+            const int rows = min(BK, 1 << c.shift), boxes = BK / rows, runs = page_runs(c, D);
+            const int none = (c.P - 1) * runs + c.Hk;   // past the last run: zeros
             each_item([&](const Item &it) {
                 // the page that holds the rows of this lane's box in block k; -1: a row that nobody sees
                 auto page_of = [&](int k) {
@@ -559,7 +533,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     if (lane < boxes && (page < 0 || page > c.P || (page == c.P && key <= it.last &&
                         (window <= 0 || key < sinks || key + rows > max(0, it.first) - window + 1)))) {
                         report(st, KDA_ERR_INVALID_ARG, it.n, 71);
-                        page = c.P;   // (past the last: zeros)
+                        page = c.P;
                     }
 #pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
@@ -569,17 +543,12 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         if (lane == 0) mbar_arrive_expect_tx(&bar[full + kv.stage], E4M3 ? M::kRawTile : M::kTile);
                         __syncwarp();
                         if (lane < boxes) {
-                            const int row = key & ((1 << c.shift) - 1);
-                            const uint32_t done = bars + 8 * (full + kv.stage);
-                            if (E4M3) {
-                                tma_load_page(base + M::kRaw + kv.stage * M::kRawTile + lane * rows * D, v ? &tv : &tk, 0, row,
-                                              it.h, page, done);
-                            } else {
+                            const int row = key & ((1 << c.shift) - 1), run = page == c.P ? none : page * runs + it.h;
+                            const uint32_t to = base + (E4M3 ? M::kRaw + kv.stage * M::kRawTile : M::kKV + kv.stage * M::kTile) +
+                                                lane * rows * (E4M3 ? D : 128);
 #pragma unroll
-                                for (int x = 0; x < D / 64; ++x)
-                                    tma_load_page(base + M::kKV + kv.stage * M::kTile + x * 16384 + lane * rows * 128,
-                                                  v ? &tv : &tk, 64 * x, row, it.h, page, done);
-                            }
+                            for (int x = 0; x < (E4M3 ? 1 : D / 64); ++x)
+                                tma_load_rows(to + x * 16384, v ? &tv : &tk, 64 * x, row, run, bars + 8 * (full + kv.stage));
                         }
                         __syncwarp();
                         kv.step(E4M3 ? M::kRaws : M::kStages);
@@ -648,7 +617,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     }
                 }
             }
-        } else if (E4M3) {
+        } else if (E4M3 && warp >= kMakeWarp) {
             // this thread's row of a block: its page, then (a block later) its scales, ahead of their use
             const int row = tid - 32 * kMakeWarp;
             Ring raw;

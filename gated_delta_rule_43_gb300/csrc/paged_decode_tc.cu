@@ -23,8 +23,11 @@
 // query heads; each CTA finds its own range (a scan over the lengths, 1 us) instead of waiting for a
 // plan.  What cuts inside items leave is joined by paged_join_kernel.
 //
-//   warps 0-3   scores -> weights; outputs      warp 4   products       warp 5   loads
-//   warp 6      goes through the items          warp 7   queries        warp 8   zeroes values behind the end
+//   warps 0-3, 4-7   every other piece's scores -> weights, and its outputs; what the two have of an item
+//                    meets at its end
+//   warp 8   products (and zeroes values behind a sequence's end: slots that nobody has written)
+//   warp 9   loads of keys and values   warp 10  goes through the items, and loads their queries
+//   warp 11  scales of e4m3 pages
 #include "kda_paged_tc.cuh"
 
 namespace kda {
@@ -32,8 +35,8 @@ namespace paged {
 namespace tc {
 namespace one {
 
-constexpr int kThreads = 288;
-constexpr int kMmaWarp = 4, kLoadWarp = 5, kItemWarp = 6, kQueryWarp = 7;   // (the last zeroes)
+constexpr int kThreads = 384;
+constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10;   // (the last: scales)
 constexpr int kTiles = 4;           // of a piece
 constexpr int kItemCost = 1;        // an item's queries and outputs, in tiles
 constexpr int kUncut = 2;           // tiles of an item that is not cut
@@ -58,20 +61,23 @@ template <int D, int NR, bool E4M3> struct Map {
     static constexpr uint32_t kTile = 128 * D * (E4M3 ? 1 : 2);
     static constexpr uint32_t kQBytes = 4096, kPTile = N * (E4M3 ? 128 : 256);
     static constexpr uint32_t kScaleBytes = E4M3 ? 2 * kTiles * 512 : 0;   // of a piece: keys', then values'
-    static constexpr uint32_t kQ = 0, kP = 2 * kQBytes, kScales = kP + 2 * kTiles * kPTile, kKV = kScales + 2 * kScaleBytes;
-    static constexpr uint32_t kSmall = 4096;                 // what stands behind the ring
+    static constexpr uint32_t kMeet = NR * 512;              // outputs of warps 4-7 at an item's end
+    static constexpr uint32_t kQ = 0, kP = 2 * kQBytes, kScales = kP + 2 * kTiles * kPTile,
+                              kOther = kScales + 2 * kScaleBytes, kKV = (kOther + 2 * kMeet + 1023) / 1024 * 1024;
+    static constexpr uint32_t kSmall = 5120;                 // what stands behind the ring
     static constexpr int kFit = (232448 - kKV - kSmall) / kTile, kStages = kFit > 16 ? 16 : kFit;
     static constexpr uint32_t kItems = kKV + kStages * kTile;
     static constexpr uint32_t kQf = kItems + kRing * sizeof(Item);     // [2][16]: a query row's factor
-    static constexpr uint32_t kRed = kQf + 128;                        // [2][4][32]: warps' maxima, sums
-    static constexpr uint32_t kBar = kRed + 1024;
+    static constexpr uint32_t kRed = kQf + 128;                        // [2 groups][2][4][32]: warps' maxima
+    static constexpr uint32_t kSums = kRed + 2048;                     // [2][8][16]: warps' sums
+    static constexpr uint32_t kTops = kSums + 1024;                    // [2][16]: maxima of warps 4-7
+    static constexpr uint32_t kBar = kTops + 128;
     static constexpr int kFull = 0, kFree = kStages, kQFull = 2 * kStages, kQFree = kQFull + 2, kSReady = kQFree + 2,
                          kPReady = kSReady + 2, kODone = kPReady + 2, kItemFull = kODone + 2,
-                         kItemFree = kItemFull + kRing, kFixAsked = kItemFree + kRing, kFixed = kFixAsked + 1,
-                         kDrain = kFixed + 1, kScFull = kDrain + 1, kScFree = kScFull + 2,
+                         kItemFree = kItemFull + kRing, kDrain = kItemFree + kRing, kScFull = kDrain + 1, kScFree = kScFull + 2,
                          kBars = kScFree + 2;
     static constexpr uint32_t kFound = kBar + kBars * 8, kCuts = kFound + 16, kScan = kCuts + 48, kSlot = kScan + 80,
-                              kFix = kSlot + 16, kBytes = kFix + 16;
+                              kBytes = kSlot + 16;
     static_assert(kStages >= 4 && kKV % 1024 == 0 && kPTile % 1024 == 0 && kBytes <= 232448 && kBytes - kItems <= kSmall && kFound % 8 == 0 &&
                       N * (E4M3 ? 128 : 2 * D) <= kQBytes && sizeof(Cut) <= 24,
                   "layout");
@@ -167,21 +173,19 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[M::kQFull + i], 1);
-            mbar_init(&bar[M::kQFree + i], 5);
+            mbar_init(&bar[M::kQFree + i], 1 + kRowWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[M::kSReady + i], 1);
             mbar_init(&bar[M::kPReady + i], 4);
             mbar_init(&bar[M::kODone + i], 1);
-            mbar_init(&bar[M::kScFull + i], 1);
+            mbar_init(&bar[M::kScFull + i], 32);
             mbar_init(&bar[M::kScFree + i], 4);
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&bar[M::kItemFull + i], 1);
-            mbar_init(&bar[M::kItemFree + i], 7);
+            mbar_init(&bar[M::kItemFree + i], kRowWarps + (E4M3 ? 3 : 2));
         }
-        mbar_init(&bar[M::kFixAsked], 1);
-        mbar_init(&bar[M::kFixed], 1);
         mbar_init(&bar[M::kDrain], 1);
         fence_mbar_init();
     }
@@ -234,7 +238,6 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
     const uint32_t tmem = *tslot;
     if (tid < 2 && (tid == 0 || blockIdx.x + 1 == p.ranges)) p.cuts[blockIdx.x + tid] = cuts[tid];
     const uint32_t tO = tmem + 2 * kTiles * N;   // behind two pieces' scores
-    volatile int *fix = reinterpret_cast<volatile int *>(sm + M::kFix);
     bool ok = true;
     auto wait = [&](int which, uint32_t parity) {
         ok = ok && wait_warp(bars + 8 * which, parity);
@@ -255,34 +258,20 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
     Ring kv;            // fills of the ring of tiles (a piece's keys, its values, ...)
     Ring qs;            // of the two places of queries
     Ring ps;            // of those of a piece's scores, scales, weights and outputs
-    uint32_t loads = 0, pieces_loaded = 0;   // (load warp) fills issued
+    uint32_t loads = 0; // (load warp) fills issued
 
-    if (warp < 4) {
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    if (warp < kRowWarps) {
+        const int side = warp >> 2, quarter = warp & 3, key_at = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const float f = scale * kLog2e;
-        uint32_t turn = 0;   // of the maxima's places
-        float *red = reinterpret_cast<float *>(sm + M::kRed);
+        uint32_t turn = 0, ends = 0;   // of the maxima's places; of those where the two sides meet
         each_item([&](const Item &it) {
             float run_m[NR], run_l[NR], run_o[NR];
-            float keep[NR], add[NR];   // what the outputs so far and those of the last piece count for
 #pragma unroll
             for (int g = 0; g < NR; ++g) {
                 run_m[g] = -INFINITY;
-                run_l[g] = run_o[g] = keep[g] = add[g] = 0.f;
+                run_l[g] = run_o[g] = 0.f;
             }
-            Ring done;                 // the last piece's place
-            auto outputs = [&] {
-                if (!wait(M::kODone + done.stage, done.phase)) return false;
-                tc_fence_after();
-                float y[C];
-                tmem_ld(tO + done.stage * N + lanes, y);
-                tmem_ld_wait();
-                tc_fence_before();
-#pragma unroll
-                for (int g = 0; g < NR; ++g)
-                    run_o[g] = run_o[g] * keep[g] + (E4M3 ? y[g] + 0.0625f * y[(E4M3 ? NR : 0) + g] : y[g]) * add[g];
-                return true;
-            };
             const int tiles = it.k1 - it.k0, count = pieces(tiles);
             const int pos = it.pos, lowest = window > 0 ? pos - window : -1;   // keys above it are in the window
             // (heads four at a time: a branch a head leaves the chains of instructions one behind the
@@ -291,13 +280,17 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             const float *qf = reinterpret_cast<const float *>(sm + M::kQf) + 16 * qs.stage;
             if (tiles > 0 && !wait(M::kQFull + qs.stage, qs.phase)) return;
             for (int u = 0; u < count; ++u) {
+                if (ps.stage != side) {   // the other side's piece
+                    ps.step(2);
+                    continue;
+                }
                 const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
                 // this thread's key of each tile: whether it is visible, and (e4m3) its scales
                 uint32_t seen = 0;
                 float ks[kTiles], ev[kTiles];
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    const int key = it.tile(first + t) * BK + tid;
+                    const int key = it.tile(first + t) * BK + key_at;
                     seen |= (uint32_t)(t < many && key <= pos && (key > lowest || key < sinks)) << t;
                 }
                 if (E4M3) {
@@ -305,8 +298,8 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                     const float *sc = reinterpret_cast<const float *>(sm + M::kScales + ps.stage * M::kScaleBytes);
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) {   // (what is behind the piece's tiles is not seen)
-                        ks[t] = sc[128 * t + tid];
-                        ev[t] = (float)((int)(__float_as_uint(sc[128 * (kTiles + t) + tid]) >> 23) - 127);
+                        ks[t] = sc[128 * t + key_at];
+                        ev[t] = (float)((int)(__float_as_uint(sc[128 * (kTiles + t) + key_at]) >> 23) - 127);
                     }
                 }
                 if (!wait(M::kSReady + ps.stage, ps.phase)) return;
@@ -342,7 +335,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                         }
                     }
                 }
-                float *place = red + 128 * (turn & 1);
+                float *place = reinterpret_cast<float *>(sm + M::kRed) + 256 * side + 128 * (turn & 1);
                 ++turn;
 #pragma unroll
                 for (int g0 = 0; g0 < NR; g0 += 4) {
@@ -354,11 +347,11 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                         if (E4M3) b[g] = warp_top(m2[g0 + g]);
                     }
                     if (lane == 0) {
-                        *reinterpret_cast<float4 *>(place + 32 * warp + g0) = make_float4(a[0], a[1], a[2], a[3]);
-                        if (E4M3) *reinterpret_cast<float4 *>(place + 32 * warp + 16 + g0) = make_float4(b[0], b[1], b[2], b[3]);
+                        *reinterpret_cast<float4 *>(place + 32 * quarter + g0) = make_float4(a[0], a[1], a[2], a[3]);
+                        if (E4M3) *reinterpret_cast<float4 *>(place + 32 * quarter + 16 + g0) = make_float4(b[0], b[1], b[2], b[3]);
                     }
                 }
-                named_bar_sync(1, 128);
+                named_bar_sync(1 + side, 128);
                 float l[NR];
 #pragma unroll
                 for (int g0 = 0; g0 < NR; g0 += 4) {
@@ -407,7 +400,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
 #pragma unroll
                             for (int g = 0; g < 4; g += 2) {
                                 const uint32_t w = split_e4m3(ex2(z[g0 + g] + ev[t] - r2[g]), ex2(z[g0 + g + 1] + ev[t] - r2[g + 1]));
-                                const uint32_t at = tid & 15, piece = tid >> 4;
+                                const uint32_t at = key_at & 15, piece = key_at >> 4;
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {   // (the row's place in its group of 8 is known here)
                                     const int row = (i & 2 ? NR : 0) + g0 + g + (i & 1);
@@ -418,8 +411,8 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
 #pragma unroll
                             for (int g = 0; g < 4; g += 2) {
                                 const uint32_t w = pack2(p[g], p[g + 1]);
-                                *reinterpret_cast<uint16_t *>(to + sw128_offset(g0 + g, tid, 16)) = (uint16_t)w;
-                                *reinterpret_cast<uint16_t *>(to + sw128_offset(g0 + g + 1, tid, 16)) = (uint16_t)(w >> 16);
+                                *reinterpret_cast<uint16_t *>(to + sw128_offset(g0 + g, key_at, 16)) = (uint16_t)w;
+                                *reinterpret_cast<uint16_t *>(to + sw128_offset(g0 + g + 1, key_at, 16)) = (uint16_t)(w >> 16);
                             }
                         }
                     }
@@ -432,13 +425,13 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                     if (E4M3) mbar_arrive(&bar[M::kScFree + ps.stage]);
                 }
                 __syncwarp();
-                // the outputs of the piece before, whose product has run meanwhile
-                if (u > 0 && !outputs()) return;
-                done = ps;
-                ps.step(2);
+                // what the piece's outputs count for, and, once its product is done, these
+                float keep[NR], add[NR];
 #pragma unroll
                 for (int g0 = 0; g0 < NR; g0 += 4) {
-                    if (g0 >= rows) break;
+#pragma unroll
+                    for (int g = g0; g < g0 + 4; ++g) keep[g] = add[g] = 0.f;
+                    if (g0 >= rows) continue;
 #pragma unroll
                     for (int g = g0; g < g0 + 4; ++g) {
                         const float top = fmaxf(run_m[g], m[g]), ref = top == -INFINITY ? 0.f : top;
@@ -449,43 +442,65 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                         run_m[g] = top;
                     }
                 }
+                if (!wait(M::kODone + side, ps.phase)) return;
+                tc_fence_after();
+                float y[C];
+                tmem_ld(tO + side * N + lanes, y);
+                tmem_ld_wait();
+                tc_fence_before();
+#pragma unroll
+                for (int g = 0; g < NR; ++g)
+                    run_o[g] = run_o[g] * keep[g] + (E4M3 ? y[g] + 0.0625f * y[(E4M3 ? NR : 0) + g] : y[g]) * add[g];
+                ps.step(2);
             }
-            if (tiles > 0 && !outputs()) return;
             if (tiles > 0) {
                 if (lane == 0) mbar_arrive(&bar[M::kQFree + qs.stage]);
                 __syncwarp();
                 qs.step(2);
             }
-            // the sums of all keys' threads
-            float *place = red + 128 * (turn & 1);
-            ++turn;
+            // The item's end: warps 4-7 leave what they have, warps 0-3 put it together.  (Two places: one
+            // may be written while the other is still read.)
+            const uint32_t end = ends & 1;
+            ++ends;
+            float *sums = reinterpret_cast<float *>(sm + M::kSums) + 128 * end, *tops = reinterpret_cast<float *>(sm + M::kTops) + 16 * end;
+            float *other = reinterpret_cast<float *>(sm + M::kOther + end * M::kMeet);
 #pragma unroll
             for (int g0 = 0; g0 < NR; g0 += 4) {
                 if (g0 >= rows) break;
                 float a[4];
 #pragma unroll
                 for (int g = 0; g < 4; ++g) a[g] = warp_sum(run_l[g0 + g]);
-                if (lane == 0) *reinterpret_cast<float4 *>(place + 32 * warp + g0) = make_float4(a[0], a[1], a[2], a[3]);
+                if (lane == 0) *reinterpret_cast<float4 *>(sums + 16 * warp + g0) = make_float4(a[0], a[1], a[2], a[3]);
+                if (side == 1) {
+                    if (key_at == 0)
+                        *reinterpret_cast<float4 *>(tops + g0) = make_float4(run_m[g0], run_m[g0 + 1], run_m[g0 + 2], run_m[g0 + 3]);
+#pragma unroll
+                    for (int g = g0; g < g0 + 4; ++g) other[128 * g + key_at] = run_o[g];
+                }
             }
-            named_bar_sync(1, 128);
+            named_bar_sync(3, 256);
+            if (side == 1) return;
             const int d = D == 128 ? tid : 16 * warp + lane;   // (64 rows of a product stand in 16 lanes of each warp)
             const bool there = D == 128 || lane < 16;
 #pragma unroll
             for (int g = 0; g < NR; ++g) {
                 if (g >= rows) break;
-                const float l = place[g] + place[32 + g] + place[64 + g] + place[96 + g];
+                const float m1 = tops[g], top = fmaxf(run_m[g], m1), ref = top == -INFINITY ? 0.f : top;
+                const float a = ex2(run_m[g] - ref), b = ex2(m1 - ref);
+                const float l = a * (sums[g] + sums[16 + g] + sums[32 + g] + sums[48 + g]) +
+                                b * (sums[64 + g] + sums[80 + g] + sums[96 + g] + sums[112 + g]);
+                const float x = a * run_o[g] + b * other[128 * g + tid];
                 if (it.slot >= 0) {
                     const int64_t at = (int64_t)it.slot * p.rows + g;
-                    if (tid == 0) p.ml[at] = make_float2(run_m[g] == -INFINITY ? 0.f : run_m[g], l);
-                    if (there) p.part[at * D + d] = run_o[g];
+                    if (tid == 0) p.ml[at] = make_float2(ref, l);
+                    if (there) p.part[at * D + d] = x;
                 } else if (there) {
                     o[((int64_t)it.n * c.Hk * group + it.h * group + it.row0 + g) * D + d] =
-                        __float2bfloat16_rn(l != 0.f ? run_o[g] / l : 0.f);
+                        __float2bfloat16_rn(l != 0.f ? x / l : 0.f);
                 }
             }
         });
     } else if (warp == kMmaWarp) {
-        uint32_t fix_phase = 0;
         constexpr uint32_t id_s = E4M3 ? idesc_e4m3(128, N, false) : idesc_bf16(128, N, false, false);
         constexpr uint32_t id_o = E4M3 ? idesc_e4m3(D, N, true) : idesc_bf16(D, N, true, false);
         // keys: rows of 128 bytes (64 for e4m3 heads of 64), channels along them; values the other way round
@@ -501,16 +516,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             if (!wait(M::kPReady + os.stage, os.phase)) return;
             for (int t = 0; t < owed; ++t) {
                 if (!wait(M::kFull + kv.stage, kv.phase)) return;
-                if (owed_left && t + 1 == owed) {
-                    if (lane == 0) {
-                        fix[0] = kv.stage;
-                        fix[1] = owed_left;
-                        mbar_arrive(&bar[M::kFixAsked]);
-                    }
-                    __syncwarp();
-                    if (!wait(M::kFixed, fix_phase)) return;
-                    fix_phase ^= 1;
-                }
+                if (owed_left && t + 1 == owed) clear_rows<D * (E4M3 ? 1 : 2)>(sm + M::kKV + kv.stage * M::kTile, owed_left);
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t dv = desc_add(dv0, kv.stage * M::kTile), dp = desc_add(dp0, (os.stage * kTiles + t) * M::kPTile);
@@ -577,16 +583,12 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             qs.step(2);
         });
         if (ok) values();
-        if (lane == 0) {
-            fix[0] = -1;
-            mbar_arrive(&bar[M::kFixAsked]);
-        }
-        __syncwarp();
     } else if (warp == kLoadWarp) {
-        const int rows = min(BK, 1 << c.shift), boxes = BK / rows;
-        // the piece whose values are still to be loaded: its tiles, this lane's boxes of them, its head
-        int owed = 0, owed_page[kTiles], owed_row[kTiles], owed_h = 0;
-        auto load = [&](const void *map, int many, const int(&page)[kTiles], const int(&row)[kTiles], int h) {
+        const int rows = min(BK, 1 << c.shift), boxes = BK / rows, runs = page_runs(c, D);
+        const int none = (c.P - 1) * runs + c.Hk;   // past the last run: zeros
+        // the piece whose values are still to be loaded: its tiles, this lane's boxes of them
+        int owed = 0, owed_run[kTiles], owed_row[kTiles];
+        auto load = [&](const void *map, int many, const int(&run)[kTiles], const int(&row)[kTiles]) {
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
                 if (t >= many) break;
@@ -594,14 +596,10 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                 if (lane == 0) mbar_arrive_expect_tx(&bar[M::kFull + kv.stage], M::kTile);
                 __syncwarp();
                 if (lane < boxes) {
-                    const uint32_t to = base + M::kKV + kv.stage * M::kTile, done = bars + 8 * (M::kFull + kv.stage);
-                    if (E4M3) {
-                        tma_load_page(to + lane * rows * D, map, 0, row[t], h, page[t], done);
-                    } else {
+                    const uint32_t to = base + M::kKV + kv.stage * M::kTile + lane * rows * (E4M3 ? D : 128);
 #pragma unroll
-                        for (int x = 0; x < D / 64; ++x)
-                            tma_load_page(to + x * 16384 + lane * rows * 128, map, 64 * x, row[t], h, page[t], done);
-                    }
+                    for (int x = 0; x < (E4M3 ? 1 : D / 64); ++x)
+                        tma_load_rows(to + x * 16384, map, 64 * x, row[t], run[t], bars + 8 * (M::kFull + kv.stage));
                 }
                 __syncwarp();
                 kv.step(M::kStages);
@@ -609,73 +607,49 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             }
         };
         auto owed_values = [&] {
-            if (owed) load(&tv, owed, owed_page, owed_row, owed_h);
+            if (owed) load(&tv, owed, owed_run, owed_row);
             owed = 0;
         };
         each_item([&](const Item &it) {
-            const int tiles = it.k1 - it.k0, count = pieces(tiles);
+            const int tiles = it.k1 - it.k0, count = pieces(tiles), pos = it.pos;
             if (tiles == 0) owed_values();
-            for (int u = 0; u < count; ++u) {
+            // the pages of this lane's boxes of a piece's tiles, looked up a piece ahead; which of them are
+            // seen by anybody
+            int page[kTiles];
+            uint32_t seen = 0;
+            auto look_up = [&](int u) {
                 const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
-                // the pages of this lane's boxes of the piece's tiles; P: rows that nobody sees, or no page
-                int page[kTiles], row[kTiles];
-                uint32_t seen = 0;
+                seen = 0;
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    page[t] = c.P;
                     const int key = it.tile(first + t) * BK + lane * rows;
-                    row[t] = key & ((1 << c.shift) - 1);
-                    if (t < many && lane < boxes && key <= it.pos &&
-                        (window <= 0 || key < sinks || key + rows > it.pos - window + 1)) {
+                    if (t < many && lane < boxes && key <= pos && (window <= 0 || key < sinks || key + rows > pos - window + 1)) {
                         page[t] = c.table[(int64_t)it.n * c.width + (key >> c.shift)];
                         seen |= 1u << t;
                     }
                 }
+            };
+            if (tiles > 0) look_up(0);
+            for (int u = 0; u < count; ++u) {
+                const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
+                int run[kTiles], row[kTiles];
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    if (((seen >> t) & 1) && (page[t] < 0 || page[t] >= c.P)) {
-                        report(st, KDA_ERR_INVALID_ARG, it.n, 91);
-                        page[t] = c.P;   // (past the last: zeros)
+                    row[t] = (it.tile(first + t) * BK + lane * rows) & ((1 << c.shift) - 1);
+                    run[t] = none;   // rows that nobody sees, or no page
+                    if ((seen >> t) & 1) {
+                        if (page[t] >= 0 && page[t] < c.P) run[t] = page[t] * runs + it.h;
+                        else report(st, KDA_ERR_INVALID_ARG, it.n, 91);
                     }
                 }
-                if (E4M3) {   // the piece's scales: a box's are one run of memory; no page: zeros
-                    if (!wait(M::kScFree + ps.stage, ps.phase ^ 1)) return;
-                    const uint32_t place = M::kScales + ps.stage * M::kScaleBytes;
-                    uint32_t copies = 0;
-#pragma unroll
-                    for (int t = 0; t < kTiles; ++t) {
-                        const bool copied = t < many && lane < boxes && page[t] != c.P;
-                        copies += __popc(__ballot_sync(0xffffffffu, copied));
-                        if (t < many && lane < boxes && !copied)
-                            for (int x = 0; x < rows; x += 4) {
-                                *reinterpret_cast<float4 *>(sm + place + (128 * t + lane * rows + x) * 4) = make_float4(0, 0, 0, 0);
-                                *reinterpret_cast<float4 *>(sm + place + (128 * (kTiles + t) + lane * rows + x) * 4) =
-                                    make_float4(0, 0, 0, 0);
-                            }
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(&bar[M::kScFull + ps.stage], copies * 8 * rows);
-                    __syncwarp();
-#pragma unroll
-                    for (int t = 0; t < kTiles; ++t) {
-                        if (t >= many || lane >= boxes || page[t] == c.P) continue;
-                        const int64_t at = page[t] * c.scale_stride + ((int64_t)it.h << c.shift) + row[t];
-                        bulk_g2s(sm + place + (128 * t + lane * rows) * 4, c.ks + at, 4 * rows, &bar[M::kScFull + ps.stage]);
-                        bulk_g2s(sm + place + (128 * (kTiles + t) + lane * rows) * 4, c.vs + at, 4 * rows,
-                                 &bar[M::kScFull + ps.stage]);
-                    }
-                    __syncwarp();
-                    ps.step(2);
-                    ++pieces_loaded;
-                }
-                load(&tk, many, page, row, it.h);
+                if (u + 1 < count) look_up(u + 1);
+                load(&tk, many, run, row);
                 if (ok) owed_values();
                 if (!ok) return;
                 owed = many;
-                owed_h = it.h;
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    owed_page[t] = page[t];
+                    owed_run[t] = run[t];
                     owed_row[t] = row[t];
                 }
             }
@@ -729,14 +703,12 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                     ++from.n;
                 }
             }
-        }
-    } else if (warp == kQueryWarp) {
-        each_item([&](const Item &it) {
-            if (it.k1 == it.k0) return;
-            if (!wait(M::kQFree + qs.stage, qs.phase ^ 1)) return;
-            const __nv_bfloat16 *from = q + (int64_t)it.n * q_stride + (int64_t)(it.h * group + it.row0) * D;
-            uint8_t *to = sm + M::kQ + qs.stage * M::kQBytes;
+            if (it.k1 == it.k0) continue;
+            // its queries
+            const __nv_bfloat16 *x0 = q + (int64_t)it.n * q_stride + (int64_t)(it.h * group + it.row0) * D;
+            uint8_t *place = sm + M::kQ + qs.stage * M::kQBytes;
             float *qf = reinterpret_cast<float *>(sm + M::kQf) + 16 * qs.stage;
+            if (!wait(M::kQFree + qs.stage, qs.phase ^ 1)) break;
             if constexpr (E4M3) {
                 constexpr int V = D / 32;   // channels a lane
 #pragma unroll 4
@@ -744,14 +716,15 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                     float x[V], top = 0.f;
 #pragma unroll
                     for (int j = 0; j < V; j += 2) {
-                        const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162 *>(from + g * D + lane * V + j);
+                        const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162 *>(x0 + g * D + lane * V + j);
                         x[j] = __low2float(y);
                         x[j + 1] = __high2float(y);
                         top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(x[j + 1])));
                     }
                     top = warp_top(top);
                     // (a row that is not finite has no scale: its factor is NaN, and so is what it gives)
-                    const bool fine = top <= 3.4028234e38f;
+                    const bool fine = __all_sync(0xffffffffu, x[0] - x[0] == 0.f && x[1] - x[1] == 0.f &&
+                                                                  x[V - 1] - x[V - 1] == 0.f && x[V - 2] - x[V - 2] == 0.f);
                     const int e = fine && top > 0.f ? scale_exponent(top) : 0;
                     const float inv = two_to(-e);
                     uint32_t hi = 0, lo = 0;
@@ -761,43 +734,75 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                         hi |= (w & 0xffffu) << (8 * j);
                         lo |= (w >> 16) << (8 * j);
                     }
-                    const uint32_t at = lane * V;
+                    const uint32_t to = lane * V;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int row = i * NR + g;
-                        uint8_t *place = to + row * 128 + (((at >> 4) ^ (row & 7)) << 4) + (at & 15);
-                        if constexpr (V == 4) *reinterpret_cast<uint32_t *>(place) = i ? lo : hi;
-                        else *reinterpret_cast<uint16_t *>(place) = (uint16_t)(i ? lo : hi);
+                        uint8_t *y = place + row * 128 + (((to >> 4) ^ (row & 7)) << 4) + (to & 15);
+                        if constexpr (V == 4) *reinterpret_cast<uint32_t *>(y) = i ? lo : hi;
+                        else *reinterpret_cast<uint16_t *>(y) = (uint16_t)(i ? lo : hi);
                     }
                     if (lane == 0) qf[g] = fine ? two_to(e) * scale * kLog2e : __int_as_float(0x7fffffff);
                 }
             } else {
                 constexpr int U = D / 8;
                 for (int x = lane; x < it.rows * U; x += 32)
-                    *reinterpret_cast<uint4 *>(to + sw128_offset(x / U, 8 * (x % U), 16)) =
-                        *reinterpret_cast<const uint4 *>(from + x * 8);
+                    *reinterpret_cast<uint4 *>(place + sw128_offset(x / U, 8 * (x % U), 16)) =
+                        *reinterpret_cast<const uint4 *>(x0 + x * 8);
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[M::kQFull + qs.stage]);
             __syncwarp();
             qs.step(2);
-        });
-    } else {
-        // the values behind a sequence's end, in the tile that the products are about to read
-        for (uint32_t phase = 0; wait(M::kFixAsked, phase); phase ^= 1) {
-            const int stage = fix[0], left = fix[1];
-            if (stage < 0) break;
-            constexpr int B = D * (E4M3 ? 1 : 2), W = B < 128 ? B : 128, U = W / 16;   // bytes of a row, in columns
-            for (int x = left * U + lane; x < BK * U; x += 32)
-#pragma unroll
-                for (int y = 0; y < B / W; ++y)
-                    *reinterpret_cast<uint4 *>(sm + M::kKV + stage * M::kTile + y * BK * W + x * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[M::kFixed]);
-            __syncwarp();
         }
+    } else if (E4M3) {
+        // a piece's scales: four keys' a lane and tile, their pages looked up a piece ahead
+        each_item([&](const Item &it) {
+            const int tiles = it.k1 - it.k0, count = pieces(tiles), pos = it.pos;
+            int page[kTiles];
+            auto look_up = [&](int u) {
+                const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    const int key = it.tile(first + t) * BK + 4 * lane;
+                    page[t] = -1;
+                    if (t < many && key <= pos && (window <= 0 || key < sinks || key + 4 > pos - window + 1))
+                        page[t] = c.table[(int64_t)it.n * c.width + (key >> c.shift)];
+                }
+            };
+            if (tiles > 0) look_up(0);
+            for (int u = 0; u < count; ++u) {
+                const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
+                int64_t at[kTiles];
+                uint32_t there = 0;
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    const bool fine = page[t] >= 0 && page[t] < c.P;   // (else zeros)
+                    there |= (uint32_t)fine << t;
+                    at[t] = fine ? page[t] * c.scale_stride + ((int64_t)it.h << c.shift) +
+                                       ((it.tile(first + t) * BK + 4 * lane) & ((1 << c.shift) - 1))
+                                 : 0;
+                }
+                if (u + 1 < count) look_up(u + 1);
+                if (!wait(M::kScFree + ps.stage, ps.phase ^ 1)) return;
+                const uint32_t place = base + M::kScales + ps.stage * M::kScaleBytes + 16 * lane;
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    if (t >= many) break;
+                    const uint32_t bytes = (there >> t) & 1 ? 16 : 0;
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place + 512 * (v * kTiles + t)),
+                                     "l"((v ? c.vs : c.ks) + at[t]), "r"(bytes)
+                                     : "memory");
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bars + 8 * (M::kScFull + ps.stage))
+                             : "memory");
+                ps.step(2);
+            }
+        });
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     if (!ok && lane == 0) report(st, KDA_ERR_TIMEOUT, blockIdx.x, 92 + warp);
     if (__syncthreads_or(!ok)) {
@@ -813,9 +818,6 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
         if (warp == kLoadWarp)   // (only each stage's last load can be in flight)
             for (uint32_t x = loads >= (uint32_t)M::kStages ? loads - M::kStages : 0; x < loads; ++x)
                 mbar_wait(&bar[M::kFull + x % M::kStages], (x / M::kStages) & 1, kDrainNs);
-        if (warp == kLoadWarp && E4M3)
-            for (uint32_t x = pieces_loaded >= 2 ? pieces_loaded - 2 : 0; x < pieces_loaded; ++x)
-                mbar_wait(&bar[M::kScFull + (x & 1)], (x >> 1) & 1, kDrainNs);
         __syncthreads();
     }
     if (tid == 0) p.found[blockIdx.x] = *st;

@@ -469,7 +469,7 @@ kda_status kda_state_pool_compact(float *pool, int32_t P, int64_t slot_elems,
  * attend to it:
  *
  *   k_pages, v_pages   [num_pages, Hk, page_size, D]   dtype; page_stride elements from one page to
- *                      the next (a multiple of 16 bytes, at least Hk * page_size * D), so that both
+ *                      the next (a multiple of page_size * D, at least Hk times that), so that both
  *                      may be halves of one pool [num_pages, 2, Hk, page_size, D]
  *   k_scales, v_scales [num_pages, Hk, page_size] fp32, scale_stride from page to page (a multiple of 4;
  *                      16-byte aligned), with dtype KDA_E4M3 (NULL otherwise): a row of D values stands for scale * e4m3.  Scales
@@ -489,7 +489,7 @@ kda_status kda_state_pool_compact(float *pool, int32_t P, int64_t slot_elems,
  *
  * page_size: a power of two, 16 ..= 1024.  D in {32, 64, 128}.  The cache's dtype is that of the
  * call's tensors, or KDA_E4M3.  Sizes: total_tokens, table_width * page_size and (attention)
- * total_tokens * H / Hk below 2^31.  The struct is read during the call only.
+ * total_tokens * H / Hk below 2^31, and so the pool's runs, num_pages * page_stride / (page_size * D).  The struct is read during the call only.
  * Device-found errors: KDA_ERR_SEQLENS (info = the sequence: its rows or its length do not fit; it is
  * skipped, its rows are not written), KDA_ERR_INVALID_ARG (info = the sequence: a page outside
  * the pool; such a page is not touched and counts as zeros).
