@@ -17,13 +17,14 @@
 // workspace (O, m, l in fp32) and joined by a second kernel.
 //
 // One CTA an SM:
-//   warps 0-3, 4-7   the rows of the two tiles: scores out of tensor memory, P into it (over the scores of
-//                    the keys from 64 on), outputs; the next item's queries into the place of this one's after the last scores
-//   warp 8           issues the products (and zeroes values behind a sequence's end: slots that nobody has
-//                    written)                   warp 9    loads keys and values, page by page
-//   warp 10          goes through the range's items for everyone
-//   warps 12-15      (e4m3 pages) make the operands out of the bytes that warp 9 loads: scale * e4m3 is a bf16
-//                    exactly, so the products are those of a bf16 cache
+//   warps 0-7, 8-15  the rows of the two tiles, a thread for each half of a row's keys and of its channels:
+//                    scores out of tensor memory, P into it (over the scores of the half's last 32 keys),
+//                    outputs; the next item's queries into the place of this one's after the last scores
+//   warp 16          issues the products (and zeroes values behind a sequence's end: slots that nobody has
+//                    written)                   warp 17   loads keys and values, page by page
+//   warp 18          goes through the range's items for everyone
+//   warps 20-23      (e4m3 pages) make the operands out of the bytes that warp 17 loads: scale * e4m3 is a
+//                    bf16 exactly, so the products are those of a bf16 cache
 // Products of one tile run while the other's scores become weights: P0 V, Q0 K', P1 V, Q1 K', ...
 #include "kda_paged_tc.cuh"
 
@@ -32,9 +33,9 @@ namespace paged {
 namespace tc {
 
 constexpr int kRows = 256;          // rows of an item
-template <bool E4M3> constexpr int kThreads = E4M3 ? 512 : 384;
-constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kMakeWarp = 12;
-constexpr int kItemCost = 2;        // an item's queries and outputs, in blocks
+template <bool E4M3> constexpr int kThreads = E4M3 ? 768 : 640;
+constexpr int kRowWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kItemWarp = 18, kMakeWarp = 20;
+constexpr int kItemCost = 4;        // an item's queries and outputs, in blocks
 constexpr int kUncut = 6;           // blocks of an item that is not cut
 constexpr int kRing = 4;            // items known ahead
 constexpr float kGrow = 8.f;        // log2 of what the maximum may grow before O is rescaled
@@ -166,7 +167,8 @@ template <int D, bool E4M3> struct Map {
     static constexpr int kStages = D == 64 ? 8 : E4M3 ? 4 : 5, kRaws = E4M3 ? D == 64 ? 4 : 2 : 0;
     static constexpr uint32_t kQ = 0, kKV = 2 * kTile, kRaw = kKV + kStages * kTile;
     static constexpr uint32_t kItems = kRaw + kRaws * kRawTile;
-    static constexpr uint32_t kBar = kItems + kRing * (uint32_t)sizeof(Item);
+    static constexpr uint32_t kTops = kItems + kRing * (uint32_t)sizeof(Item);   // [2 tiles][2 halves][128 rows]
+    static constexpr uint32_t kBar = kTops + 2048;
     // barriers
     static constexpr int kFull = 0, kFree = kStages, kQFull = 2 * kStages, kSReady = kQFull + 2,
                          kPReady = kSReady + 2, kODone = kPReady + 2, kItemFull = kODone + 2,
@@ -200,9 +202,9 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             mbar_init(&bar[M::kFree + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar[M::kQFull + i], 4);
+            mbar_init(&bar[M::kQFull + i], 8);
             mbar_init(&bar[M::kSReady + i], 1);
-            mbar_init(&bar[M::kPReady + i], 4);
+            mbar_init(&bar[M::kPReady + i], 8);
             mbar_init(&bar[M::kODone + i], 1);
         }
         for (int i = 0; i < kRing; ++i) {
@@ -251,87 +253,96 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
     Ring kv;            // fills of the ring of keys and values (keys, values, keys, ...)
     uint32_t loads = 0; // (load warp) fills issued
 
+    // Registers for the rows' threads from the others: launched with 61440 in both forms, 640 threads of 96
+    // (then 512 x 104 + 128 x 64) or 768 of 80 (512 x 88 + 256 x 64).
     if (warp < kRowWarps) {
-        const int tile = warp >> 2;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t tSl = tmem + 128 * tile + lanes, tOl = tmem + 256 + D * tile + lanes;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(E4M3 ? 88 : 104));
+        const int tile = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const uint32_t tSl = tmem + 128 * tile + 64 * half + lanes, tPl = tSl + 32,
+                       tOl = tmem + 256 + D * tile + D / 2 * half + lanes;
         const float f = scale * kLog2e;
+        // What the two halves of a row tell each other.  (Between one time and the next lies a product that
+        // waits for both halves: nothing is written before it has been read.)
+        float *tops = reinterpret_cast<float *>(sm + M::kTops) + 256 * tile + 32 * quarter + lane;
+        auto other_half = [&](float x) {
+            tops[128 * half] = x;
+            named_bar_sync(1 + tile, 256);
+            return tops[128 * (half ^ 1)];
+        };
         uint32_t s_phase = 0, o_phase = 0;
         // The queries of this warp's rows of the item at `at`: a row's address by its lane, its 16-byte
-        // pieces side by side.
-        auto load_queries = [&](const Ring &at) {
-            if (!wait(M::kItemFull + at.stage, at.phase)) return;
+        // pieces side by side, half of them by each half.
+        auto start_queries = [&](const Ring &at) {
+            if (!wait(M::kItemFull + at.stage, at.phase)) return false;
             const Item &it = items[at.stage];
-            const int row = 128 * tile + 32 * (warp & 3);
-            if (it.n < 0 || it.end(tile) == it.k0) return;
+            const int row = 128 * tile + 32 * quarter;
+            if (it.n < 0 || it.end(tile) == it.k0) return false;
             if (row < it.rows) {
                 const int mine = it.row0 + min(row + lane, it.rows - 1), token = mine / group;
                 const int64_t from = (int64_t)(it.tok0 + token) * q_stride + (int64_t)(it.h * group + mine - token * group) * D;
                 constexpr int U = D / 8;   // pieces of a row
 #pragma unroll 4
-                for (int i = 0; i < U; ++i) {
+                for (int i = half * U / 2; i < (half + 1) * U / 2; ++i) {
                     const int r = (32 * i + lane) / U, x = lane % U;
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                     base + M::kQ + tile * M::kTile + sw128_offset(32 * (warp & 3) + r, 8 * x, 128)),
+                                     base + M::kQ + tile * M::kTile + sw128_offset(32 * quarter + r, 8 * x, 128)),
                                  "l"(q + __shfl_sync(0xffffffffu, from, r) + 8 * x)
                                  : "memory");
                 }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_proxy_async();
             }
+            return true;
+        };
+        auto finish_queries = [&] {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[M::kQFull + tile]);
             __syncwarp();
         };
         Ring at_next;
-        load_queries(at_next);
+        if (start_queries(at_next)) finish_queries();
         each_item([&](const Item &it) {
             at_next.step(kRing);
-            const int r = 128 * tile + 32 * (warp & 3) + lane;
+            const int r = 128 * tile + 32 * quarter + lane;
             const bool live = r - lane < it.rows, mine = r < it.rows;   // (of a whole warp; this row)
             const int pos = it.pos0 + (it.row0 + min(r, it.rows - 1)) / group;
             const int pos_lo = __shfl_sync(0xffffffffu, pos, 0), pos_hi = __shfl_sync(0xffffffffu, pos, 31);
             const int lowest = window > 0 ? max(pos - window, -1) : -1;   // keys above it are in the window
-            const int end = it.end(tile);
+            const int end = it.end(tile), begin = it.k0;
             float m = -INFINITY, l = 0.f;   // m: of the scores as they come
-            for (int k = it.k0; k < end; ++k) {
+            for (int k = begin; k < end; ++k) {
                 if (!wait(M::kSReady + tile, s_phase)) return;
                 s_phase ^= 1;
                 tc_fence_after();
+                float s0[32], s1[32], top = -INFINITY;
+                // the half's first and second 32 keys, -inf where this row does not see them
+                const int key0 = it.block(k) * BK + 64 * half;
+                // are there keys that one of the warp's rows does not see?
+                const bool edge = key0 + 63 > pos_lo || (window > 0 && key0 <= pos_hi - window && key0 + 63 >= sinks);
+                auto hide = [&](float(&s)[32], int j0) {
+                    if (!edge) return;
+                    const int upto = pos - key0 - j0, above = lowest - key0 - j0, first = sinks - key0 - j0;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) s[j] = j <= upto && (j > above || j < first) ? s[j] : -INFINITY;
+                };
                 if (live) {
-                    const int key0 = it.block(k) * BK;
-                    // are there keys that one of the warp's rows does not see?
-                    const bool edge = key0 + BK - 1 > pos_lo ||
-                                      (window > 0 && key0 <= pos_hi - window && key0 + BK - 1 >= sinks);
-                    const int upto = pos - key0, above = lowest - key0, first = sinks - key0;
-                    // scores of 32 keys, -inf where this row does not see the key
-                    auto hide = [&](float(&s)[32], int j0) {
-                        if (!edge) return;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            s[j] = j0 + j <= upto && (j0 + j > above || j0 + j < first) ? s[j] : -INFINITY;
-                    };
-                    float top = -INFINITY;
-                    auto highest = [&](const float(&s)[32]) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) top = max3(top, s[j], s[j + 1]);
-                    };
-                    float sa[32], sb[32];
-                    tmem_ld32(tSl, sa);
-                    tmem_ld32(tSl + 32, sb);
+                    tmem_ld32(tSl, s0);
+                    tmem_ld32(tSl + 32, s1);
                     tmem_ld_wait();
-                    hide(sa, 0);
-                    hide(sb, 32);
-                    highest(sa);
-                    highest(sb);
-                    tmem_ld32(tSl + 64, sa);
-                    tmem_ld32(tSl + 96, sb);
-                    tmem_ld_wait();
-                    hide(sa, 64);
-                    hide(sb, 96);
-                    highest(sa);
-                    highest(sb);
-                    if (k == it.k0) {
+                    hide(s0, 0);
+                    hide(s1, 32);
+                    float t2 = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        top = max3(top, s0[j], s0[j + 1]);
+                        t2 = max3(t2, s1[j], s1[j + 1]);
+                    }
+                    top = fmaxf(top, t2);
+                }
+                top = fmaxf(top, other_half(top));
+                if (live) {
+                    if (k == begin) {
                         m = top;
                     } else if (__any_sync(0xffffffffu, mine && top > m && !((top - m) * f <= kGrow))) {
                         const float grown = fmaxf(m, top);
@@ -339,21 +350,20 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         m = grown;
                         l *= keep;
 #pragma unroll 1
-                        for (int j = 0; j < D; j += 16) {
-                            float x[16];
-                            uint32_t y[16];
-                            tmem_ld16(tOl + j, x);
+                        for (int j = 0; j < D / 2; j += 8) {
+                            float x[8];
+                            tmem_ld(tOl + j, x);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * keep);
-                            tmem_st16(tOl + j, y);
+                            for (int i = 0; i < 8; ++i) x[i] *= keep;
+                            tmem_st8(tOl + j, x);
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : -m * f;
                     const float2 f2 = make_float2(f, f), ref2 = make_float2(ref, ref);
                     float2 sum = make_float2(0.f, 0.f), sum1 = sum;
-                    // Weights of 32 keys, over scores that this row has read: those of the keys from 64 on
-                    // are in registers still, the others are read again (holding all 128 spills).
+                    // Over the scores of the second 32 keys, which are in registers still; the first are read
+                    // again (held meanwhile, they spill).
                     auto weigh = [&](const float(&s)[32], int j0) {
                         uint32_t w[16];
 #pragma unroll
@@ -365,18 +375,13 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                             else sum = add2(sum, x);
                             w[j / 2] = pack2(x.x, x.y);
                         }
-                        tmem_st16(tSl + 64 + j0 / 2, w);
+                        tmem_st16(tPl + j0 / 2, w);
                     };
-                    weigh(sa, 64);
-                    tmem_ld32(tSl, sa);
-                    weigh(sb, 96);
+                    tmem_ld32(tSl, s0);
+                    weigh(s1, 32);
                     tmem_ld_wait();
-                    tmem_ld32(tSl + 32, sb);
-                    hide(sa, 0);
-                    weigh(sa, 0);
-                    tmem_ld_wait();
-                    hide(sb, 32);
-                    weigh(sb, 32);
+                    hide(s0, 0);
+                    weigh(s0, 0);
                     sum = add2(sum, sum1);
                     l += sum.x + sum.y;
                     tmem_st_wait();
@@ -386,58 +391,75 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                 if (lane == 0) mbar_arrive(&bar[M::kPReady + tile]);
                 __syncwarp();
             }
-            const bool any = end > it.k0;
-            load_queries(at_next);   // (the last scores are there: their queries have been read)
+            const bool any = end > begin;
+            const bool queries = start_queries(at_next);   // (the last scores are there: their queries have been read)
             if (any) {
                 if (!wait(M::kODone + tile, o_phase)) return;
                 o_phase ^= 1;
                 tc_fence_after();
+                l += other_half(l);
             }
+            if (queries) finish_queries();
             if (!live) return;
             if (it.slot >= 0) {
                 const int64_t at = (int64_t)it.slot * p.rows + r;
-                if (mine) p.ml[at] = make_float2(m == -INFINITY ? 0.f : m * f, any ? l : 0.f);
+                if (mine && half == 0) p.ml[at] = make_float2(m == -INFINITY ? 0.f : m * f, any ? l : 0.f);
                 if (any) {
 #pragma unroll 1
-                    for (int j = 0; j < D; j += 32) {
-                        float x[32];
-                        tmem_ld32(tOl + j, x);
+                    for (int j = 0; j < D / 2; j += 16) {
+                        float x[16];
+                        tmem_ld(tOl + j, x);
                         tmem_ld_wait();
                         if (mine)
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<float4 *>(p.part + at * D + j + i) =
+                            for (int i = 0; i < 16; i += 4)
+                                *reinterpret_cast<float4 *>(p.part + at * D + D / 2 * half + j + i) =
                                     make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                     }
                 }
             } else {
-                const float inv = l != 0.f ? 1.f / l : 0.f;   // (no visible key: zeros)
+                const float inv = any && l != 0.f ? 1.f / l : 0.f;   // (no visible key: zeros)
                 const int token = pos - it.pos0, head = it.h * group + (it.row0 + r) - token * group;
-                __nv_bfloat16 *to = o + ((int64_t)(it.tok0 + token) * c.Hk * group + head) * D;
+                const int64_t to = ((int64_t)(it.tok0 + token) * c.Hk * group + head) * D + D / 2 * half;
+                // 32 channels at a time: four lanes exchange the 16-byte pieces of their four rows, so that they
+                // store a row's 64 bytes side by side (stored row by row, an item's outputs took 4k cycles)
 #pragma unroll 1
-                for (int j = 0; j < D; j += 32) {
+                for (int j = 0; j < D / 2; j += 32) {
                     float x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = 0.f;
                     if (any) {
                         tmem_ld32(tOl + j, x);
                         tmem_ld_wait();
                     }
-                    if (mine)
+                    uint32_t v[4][4];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint4 u = make_uint4(0, 0, 0, 0);
-                            if (any && l != 0.f) {
-                                u.x = pack2(x[i] * inv, x[i + 1] * inv);
-                                u.y = pack2(x[i + 2] * inv, x[i + 3] * inv);
-                                u.z = pack2(x[i + 4] * inv, x[i + 5] * inv);
-                                u.w = pack2(x[i + 6] * inv, x[i + 7] * inv);
+                    for (int i = 0; i < 32; i += 2)
+                        v[i / 8][i / 2 % 4] = inv != 0.f ? pack2(x[i] * inv, x[i + 1] * inv) : 0u;
+#pragma unroll
+                    for (int bit = 1; bit <= 2; bit <<= 1)
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            if (a & bit) continue;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & bit ? v[a][i] : v[a | bit][i], bit);
+                                if (lane & bit) v[a][i] = got;
+                                else v[a | bit][i] = got;
                             }
-                            *reinterpret_cast<uint4 *>(to + j + i) = u;
                         }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {   // row i of the four, this lane's piece
+                        const int64_t at = __shfl_sync(0xffffffffu, to, (lane & ~3) + i) + j + 8 * (lane & 3);
+                        if (r - (lane & 3) + i < it.rows)
+                            *reinterpret_cast<uint4 *>(o + at) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+                    }
                 }
             }
             tc_fence_before();
         });
     } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == kMmaWarp) {
             uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
             constexpr uint32_t id_s = idesc_bf16(128, BK, false, false), id_o = idesc_bf16(128, D, false, true);
@@ -490,7 +512,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         if (elect_one()) {
 #pragma unroll
                             for (int s = 0; s < BK / 16; ++s)
-                                umma_bf16_ts(tmem + 256 + D * i, tmem + 128 * i + 64 + 8 * s, desc_add(dv0, val.stage * M::kTile + s * 2048), id_o,
+                                umma_bf16_ts(tmem + 256 + D * i, tmem + 128 * i + 64 * (s >> 2) + 32 + 8 * (s & 3), desc_add(dv0, val.stage * M::kTile + s * 2048), id_o,
                                              j > 0 || s > 0);
                             if (j + 1 == n) umma_commit(&bar[M::kODone + i]);
                         }
