@@ -43,24 +43,26 @@ constexpr float kGrow = 8.f;        // log2 of what the maximum may grow before 
 constexpr int kPlanThreads = 1024;
 
 // Inclusive sums over a block's threads; returns the total.
-template <typename T> __device__ __forceinline__ T block_scan(T &x, T *warps) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, x, o);
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
+    return x;
+}
+__device__ __forceinline__ int64_t block_scan(int64_t &x, int64_t *warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    x = warp_scan(x);
     __syncthreads();
     if (lane == 31) warps[warp] = x;
     __syncthreads();
-    T before = 0, total = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < warp) before += warps[w];
-        total += warps[w];
-    }
-    x += before;
-    return total;
+    const int64_t upto = warp_scan(warps[lane]);
+    if (warp > 0) x += __shfl_sync(0xffffffffu, upto, warp - 1);
+    return __shfl_sync(0xffffffffu, upto, 31);
 }
+static_assert(kPlanThreads == 1024, "a warp scans the warps");
 
 // The last n in [0, count) with a[n] <= x
 template <typename T> __device__ __forceinline__ int last_at_most(const T *a, int count, T x) {
@@ -73,24 +75,31 @@ template <typename T> __device__ __forceinline__ int last_at_most(const T *a, in
     return lo;
 }
 
+// (What is searched stands in shared memory where it fits: from global memory, the searches' chains of reads
+// made the plan take 8 us.)
+constexpr int kNearSeqs = 2048, kNearTiles = 4096;
 __global__ void __launch_bounds__(kPlanThreads)
 paged_plan_kernel(Cache c, Plan p, int group, int window, int sinks, StatusWord *st) {
     __shared__ int64_t warps[kPlanThreads / 32];
+    __shared__ int64_t near_cost[kNearTiles + 1];
+    __shared__ int32_t near_tiles[kNearSeqs + 1];
     let_next_start();
     const int tid = threadIdx.x;
     if (tid == 0) *st = StatusWord{0, 0, 0};
     __syncthreads();
-    check_spans(c, st);
+    int32_t *first = c.N <= kNearSeqs ? near_tiles : p.tiles;
     int64_t tiles = 0, rows = 0;
     for (int n0 = 0; n0 < c.N; n0 += kPlanThreads) {
         const int n = n0 + tid;
         int64_t x = 0, len = 0;
         if (n < c.N) {
-            len = span_of(c, n).len;
+            const int ctx = c.kv_lens[n], begin = c.cu[n], end = c.cu[n + 1];
+            if (lens_ok(c, begin, end, ctx)) len = end - begin;
+            if (!lens_ok(c, begin, end, ctx) || (n == 0 && begin != 0)) report(st, KDA_ERR_SEQLENS, n, 61);
             x = (len * group + kRows - 1) / kRows;
         }
         const int64_t mine = x, some = block_scan(x, warps);
-        if (n < c.N && tiles + x < ((int64_t)1 << 31)) p.tiles[n] = (int)(tiles + x - mine);
+        if (n < c.N && tiles + x < ((int64_t)1 << 31)) first[n] = p.tiles[n] = (int)(tiles + x - mine);
         rows += block_scan(len, warps);
         tiles += some;
     }
@@ -99,20 +108,21 @@ paged_plan_kernel(Cache c, Plan p, int group, int window, int sinks, StatusWord 
     if (rows > c.T || tiles > p.most) tiles = 0;
     if (tid == 0) p.tiles[c.N] = (int)tiles;
     __syncthreads();
+    int64_t *cost = tiles <= kNearTiles ? near_cost : p.cost;
     int64_t total = 0;
     for (int64_t i0 = 0; i0 < tiles; i0 += kPlanThreads) {
         const int64_t i = i0 + tid;
         int64_t x = 0;
         if (i < tiles) {
-            int n = last_at_most(p.tiles, c.N, (int)i);
-            const Tile t = tile_of(span_of(c, n), (int)i - p.tiles[n], group, kRows);
+            int n = last_at_most(first, c.N, (int)i);
+            const Tile t = tile_of(span_of(c, n), (int)i - first[n], group, kRows);
             x = (int64_t)c.Hk * (kItemCost + blocks_of(t, window, sinks).count);
         }
         const int64_t mine = x, some = block_scan(x, warps);
-        if (i < tiles) p.cost[i] = total + x - mine;
+        if (i < tiles) cost[i] = total + x - mine;
         total += some;
     }
-    if (tid == 0) p.cost[tiles] = total;
+    if (tid == 0) cost[tiles] = total;
     __syncthreads();
     // ranges of at least as much as an item that is not cut
     const int64_t share = max((total + p.ranges - 1) / p.ranges, (int64_t)kUncut);
@@ -120,9 +130,9 @@ paged_plan_kernel(Cache c, Plan p, int group, int window, int sinks, StatusWord 
         const int64_t x = min((int64_t)i * share, total);
         Cut cut{(int)tiles, c.N, 0, 0, 0};
         if (x < total) {
-            cut.tile = last_at_most(p.cost, (int)tiles, x);
-            const int64_t rest = x - p.cost[cut.tile];
-            const int each = (int)((p.cost[cut.tile + 1] - p.cost[cut.tile]) / c.Hk), count = each - kItemCost;
+            cut.tile = last_at_most(cost, (int)tiles, x);
+            const int64_t rest = x - cost[cut.tile];
+            const int each = (int)((cost[cut.tile + 1] - cost[cut.tile]) / c.Hk), count = each - kItemCost;
             cut.h = (int)(rest / each);
             cut.k = (int)(rest - (int64_t)cut.h * each) - kItemCost;
             bool next = false;   // to the item's nearer end
@@ -134,8 +144,8 @@ paged_plan_kernel(Cache c, Plan p, int group, int window, int sinks, StatusWord 
                 ++cut.tile;
             }
             if (cut.tile < tiles) {
-                cut.n = last_at_most(p.tiles, c.N, cut.tile);
-                cut.t = cut.tile - p.tiles[cut.n];
+                cut.n = last_at_most(first, c.N, cut.tile);
+                cut.t = cut.tile - first[cut.n];
             } else {
                 cut.n = c.N;
             }

@@ -468,9 +468,9 @@ def _new(like, shape, dtype, stream):
     """Buffers that a call allocates belong to the stream that it runs on, so that the caching
     allocator hands their memory on in that stream's order."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _workspace(like, nbytes, workspace, stream):
@@ -768,34 +768,46 @@ def _pages_stride(name, t, shape, dtype):
     return s[0] if shape[0] > 1 else packed
 
 
+def _both_strides(name, k, v, shape, dtype):
+    """The stride from page to page of the keys' and the values' tensor.  (Where they are laid out
+    alike and as usual, which is nearly always, one look at each is enough.)"""
+    s = k.stride()
+    if (shape[0] > 1 and s[-1] == 1 and s[-2] == shape[-1] and s[1] == s[2] * shape[2] and k.shape == shape
+            and k.dtype is dtype and v.shape == shape and v.dtype is dtype and v.stride() == s):
+        return s[0]
+    stride = _pages_stride("k" + name, k, shape, dtype)
+    if _pages_stride("v" + name, v, shape, dtype) != stride:
+        raise ValueError(f"k{name} and v{name} must have the same stride from page to page")
+    return stride
+
+
 def _paged(k_pages, v_pages, block_table, kv_lens, cu_seqlens, k_scales, v_scales):
     """The checked description of a cache, and its (Hk, D, dtype)."""
-    if k_pages.dim() != 4:
-        raise ValueError("k_pages and v_pages must be [P, Hk, page_size, D]")
     shape, dtype = k_pages.shape, k_pages.dtype
-    if dtype is not _E4M3 and dtype not in _DT:
-        raise TypeError(f"k_pages has dtype {dtype}; fp32, bf16 and float8_e4m3fn are supported")
-    stride = _pages_stride("k_pages", k_pages, shape, dtype)
-    if _pages_stride("v_pages", v_pages, shape, dtype) != stride:
-        raise ValueError("k_pages and v_pages must have the same stride from page to page")
-    scale_stride = 0
+    if len(shape) != 4:
+        raise ValueError("k_pages and v_pages must be [P, Hk, page_size, D]")
+    pages, Hk, page_size, D = shape
+    stride, scale_stride, ka, va = _both_strides("_pages", k_pages, v_pages, shape, dtype), 0, None, None
     if dtype is _E4M3:
+        dt = KDA_E4M3
         if k_scales is None or v_scales is None:
             raise ValueError("e4m3 pages need k_scales and v_scales [P, Hk, page_size]")
-        scale_stride = _pages_stride("k_scales", k_scales, shape[:3], _F32)
-        if _pages_stride("v_scales", v_scales, shape[:3], _F32) != scale_stride:
-            raise ValueError("k_scales and v_scales must have the same stride from page to page")
-    elif k_scales is not None or v_scales is not None:
-        raise ValueError("scales go with e4m3 pages only")
-    if block_table.dim() != 2:
+        scale_stride = _both_strides("_scales", k_scales, v_scales, shape[:3], _F32)
+        ka, va = k_scales.data_ptr(), v_scales.data_ptr()
+    else:
+        if dtype not in _DT:
+            raise TypeError(f"k_pages has dtype {dtype}; fp32, bf16 and float8_e4m3fn are supported")
+        dt = _DT[dtype]
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("scales go with e4m3 pages only")
+    N, width = block_table.shape if block_table.dim() == 2 else (None, None)
+    if N is None:
         raise ValueError("block_table must be [N, pages]")
-    N, width = block_table.shape
     ta = _dense("block_table", block_table, (N, width), torch.int32)
     la = _dense("kv_lens", kv_lens, (N,), torch.int32)
     ca = None if cu_seqlens is None else _dense("cu_seqlens", cu_seqlens, (N + 1,), torch.int32)
-    return PagedCache(ca, la, ta, k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scales),
-                      _addr(v_scales), stride, scale_stride, N, width, shape[0], shape[2], shape[1],
-                      shape[3], KDA_E4M3 if dtype is _E4M3 else _DT[dtype]), shape[1], shape[3], dtype
+    return PagedCache(ca, la, ta, k_pages.data_ptr(), v_pages.data_ptr(), ka, va, stride, scale_stride, N,
+                      width, pages, page_size, Hk, D, dt), Hk, D, dtype
 
 
 def _paged_dtype(name, dtype, cache_dtype):
