@@ -80,6 +80,32 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, ok != 0);
 }
 
+// The same on up to three barriers at a time, a lane each: every wait of its own costs a warp 100 to 200
+// cycles, whatever it finds.  Such tries do not sleep, so time is what is counted: 2.2 s.
+__device__ __forceinline__ bool wait_warp(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, uint32_t bar2,
+                                          uint32_t parity2) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t bar = lane == 1 ? bar1 : lane == 2 ? bar2 : bar0, parity = lane == 1 ? parity1 : lane == 2 ? parity2 : parity0;
+    uint64_t begin = 0;
+    uint32_t ok = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (!ok)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
+        if (__all_sync(0xffffffffu, ok != 0)) return true;
+        if ((i & 255u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (i == 0) begin = now;
+            else if (__any_sync(0xffffffffu, now - begin > 2200000000ull)) return false;
+        }
+    }
+}
+
 // 32 lanes x 4, 8, 16 or 32 consecutive columns of tensor memory; nothing may be used before
 // tmem_ld_wait
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[4]) {
@@ -108,6 +134,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
                  : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// x as the compiler knows it to be the same in all lanes, so that it goes into a uniform register once, and not
+// with every product that is issued: of a converged warp
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint64_t uniform(uint64_t d) {
+    return (uint64_t)uniform((uint32_t)(d >> 32)) << 32 | uniform((uint32_t)d);
+}
 
 // A in tensor memory (lane = row, column c = K elements 2 c and 2 c + 1)
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,

@@ -473,16 +473,18 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
         if (warp == kMmaWarp) {
             uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
             constexpr uint32_t id_s = idesc_bf16(128, BK, false, false), id_o = idesc_bf16(128, D, false, true);
-            const uint64_t dq0 = sdesc_sw128(base + M::kQ, 16, 1024), dk0 = sdesc_sw128(base + M::kKV, 16, 1024),
+            const uint64_t dq0 = uniform(sdesc_sw128(base + M::kQ, 16, 1024)), dk0 = sdesc_sw128(base + M::kKV, 16, 1024),
                            dv0 = sdesc_sw128(base + M::kKV, BK * 128, 1024);
-            auto scores = [&](int tile, uint32_t stage) {   // S = Q K^T
+            const uint32_t t0 = uniform(tmem);
+            auto scores = [&](int tile, uint64_t dk) {   // S = Q K^T
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
-                    umma_bf16(tmem + 128 * tile, desc_add(dq0, tile * M::kTile + (s >> 2) * 16384 + (s & 3) * 32),
-                              desc_add(dk0, stage * M::kTile + (s >> 2) * 16384 + (s & 3) * 32), id_s, s > 0);
+                    umma_bf16(t0 + 128 * tile, desc_add(dq0, tile * M::kTile + (s >> 2) * 16384 + (s & 3) * 32),
+                              desc_add(dk, (s >> 2) * 16384 + (s & 3) * 32), id_s, s > 0);
             };
+            auto keys_at = [&](uint32_t stage) { return uniform(desc_add(dk0, stage * M::kTile)); };
             each_item([&](const Item &it) {
-                const int n0 = it.end(0) - it.k0, n1 = it.end(1) - it.k0, blocks = it.k1 - it.k0;
+                const int n0 = it.end(0) - it.k0, n1 = it.end(1) - it.k0, blocks = it.k1 - it.k0, ctx = it.ctx;
                 if (blocks == 0) return;
                 Ring key = kv;
                 if (!wait(M::kFull + key.stage, key.phase)) return;
@@ -492,8 +494,9 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     if (!wait(M::kQFull + i, q_phase[i])) return;
                     q_phase[i] ^= 1;
                     tc_fence_after();
+                    const uint64_t dk = keys_at(key.stage);
                     if (elect_one()) {
-                        scores(i, key.stage);
+                        scores(i, dk);
                         umma_commit(&bar[M::kSReady + i]);
                     }
                     __syncwarp();
@@ -505,37 +508,40 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     val.step(M::kStages);
                     key = val;
                     key.step(M::kStages);
-                    if (!wait(M::kFull + val.stage, val.phase)) return;
-                    if (!E4M3) {
-                        const int left = it.ctx - it.block(it.k0 + j) * BK;   // (below BK only in the list's last block)
-                        if (left < BK && (it.ctx & ((1 << c.shift) - 1)) != 0)
-                            clear_rows<2 * D>(sm + M::kKV + val.stage * M::kTile, left);
-                    }
-                    bool key_there = false;
+                    const bool more = j + 1 < blocks;
+                    const uint32_t val_bar = bars + 8 * (M::kFull + val.stage), key_bar = bars + 8 * (M::kFull + key.stage);
+                    const bool clear = !E4M3 && ctx - it.block(it.k0 + j) * BK < BK && (ctx & ((1 << c.shift) - 1)) != 0;
+                    bool there = false;   // the block's values, the next block's keys
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int n = i ? n1 : n0;
                         if (j >= n) continue;
-                        if (!wait(M::kPReady + i, p_phase[i])) return;
+                        const uint32_t p_bar = bars + 8 * (M::kPReady + i);
+                        ok = there ? wait_warp(p_bar, p_phase[i])
+                                   : wait_warp(p_bar, p_phase[i], val_bar, val.phase, more ? key_bar : val_bar,
+                                               more ? key.phase : val.phase);
+                        if (!ok) return;
                         p_phase[i] ^= 1;
+                        // (values behind the sequence's end: only in the list's last block)
+                        if (!there && clear)
+                            clear_rows<2 * D>(sm + M::kKV + val.stage * M::kTile, ctx - it.block(it.k0 + j) * BK);
+                        there = true;
                         tc_fence_after();
+                        const uint64_t dv = uniform(desc_add(dv0, val.stage * M::kTile)), dk = keys_at(key.stage);
+                        const uint32_t onto = uniform((uint32_t)(j > 0));
                         if (elect_one()) {
 #pragma unroll
                             for (int s = 0; s < BK / 16; ++s)
-                                umma_bf16_ts(tmem + 256 + D * i, tmem + 128 * i + 64 * (s >> 2) + 32 + 8 * (s & 3), desc_add(dv0, val.stage * M::kTile + s * 2048), id_o,
-                                             j > 0 || s > 0);
-                            if (j + 1 == n) umma_commit(&bar[M::kODone + i]);
-                        }
-                        __syncwarp();
-                        if (j + 1 < n) {
-                            if (!key_there && !wait(M::kFull + key.stage, key.phase)) return;
-                            key_there = true;
-                            if (elect_one()) {
-                                scores(i, key.stage);
+                                umma_bf16_ts(t0 + 256 + D * i, t0 + 128 * i + 64 * (s >> 2) + 32 + 8 * (s & 3),
+                                             desc_add(dv, s * 2048), id_o, s > 0 ? 1u : onto);
+                            if (j + 1 == n) {
+                                umma_commit(&bar[M::kODone + i]);
+                            } else {
+                                scores(i, dk);
                                 umma_commit(&bar[M::kSReady + i]);
                             }
-                            __syncwarp();
                         }
+                        __syncwarp();
                     }
                     if (elect_one()) {
                         umma_commit(&bar[M::kFree + val.stage]);
