@@ -181,7 +181,7 @@ template <int D, bool E4M3> struct Map {
     static constexpr uint32_t kBar = kTops + 2048;
     // barriers
     static constexpr int kFull = 0, kFree = kStages, kQFull = 2 * kStages, kSReady = kQFull + 2,
-                         kPReady = kSReady + 2, kODone = kPReady + 2, kItemFull = kODone + 2,
+                         kPReady = kSReady + 2 /* [2 parts][2 tiles] */, kODone = kPReady + 4, kItemFull = kODone + 2,
                          kItemFree = kItemFull + kRing, kDrain = kItemFree + kRing, kRawFull = kDrain + 1, kRawFree = kRawFull + kRaws,
                          kBars = kRawFree + kRaws;
     static constexpr uint32_t kSlot = kBar + kBars * 8, kBytes = kSlot + 16;
@@ -215,6 +215,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             mbar_init(&bar[M::kQFull + i], 8);
             mbar_init(&bar[M::kSReady + i], 1);
             mbar_init(&bar[M::kPReady + i], 8);
+            mbar_init(&bar[M::kPReady + 2 + i], 8);
             mbar_init(&bar[M::kODone + i], 1);
         }
         for (int i = 0; i < kRing; ++i) {
@@ -279,6 +280,14 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             tops[128 * half] = x;
             named_bar_sync(1 + tile, 256);
             return tops[128 * (half ^ 1)];
+        };
+        // P goes to its product in two parts, so that the first runs while the second is formed: the last 32
+        // keys of each half, then the first
+        auto part_done = [&](int part) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[M::kPReady + 2 * part + tile]);
+            __syncwarp();
         };
         uint32_t s_phase = 0, o_phase = 0;
         // The queries of this warp's rows of the item at `at`: a row's address by its lane, its 16-byte
@@ -389,17 +398,18 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     };
                     tmem_ld32(tSl, s0);
                     weigh(s1, 32);
+                    tmem_st_wait();
                     tmem_ld_wait();
+                    part_done(0);
                     hide(s0, 0);
                     weigh(s0, 0);
                     sum = add2(sum, sum1);
                     l += sum.x + sum.y;
                     tmem_st_wait();
+                } else {
+                    part_done(0);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[M::kPReady + tile]);
-                __syncwarp();
+                part_done(1);
             }
             const bool any = end > begin;
             const bool queries = start_queries(at_next);   // (the last scores are there: their queries have been read)
@@ -529,11 +539,23 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         tc_fence_after();
                         const uint64_t dv = uniform(desc_add(dv0, val.stage * M::kTile)), dk = keys_at(key.stage);
                         const uint32_t onto = uniform((uint32_t)(j > 0));
+                        // parts: keys 32 .. 63 and 96 .. 127, then the others
                         if (elect_one()) {
 #pragma unroll
                             for (int s = 0; s < BK / 16; ++s)
-                                umma_bf16_ts(t0 + 256 + D * i, t0 + 128 * i + 64 * (s >> 2) + 32 + 8 * (s & 3),
-                                             desc_add(dv, s * 2048), id_o, s > 0 ? 1u : onto);
+                                if (s & 2)
+                                    umma_bf16_ts(t0 + 256 + D * i, t0 + 128 * i + 64 * (s >> 2) + 32 + 8 * (s & 3),
+                                                 desc_add(dv, s * 2048), id_o, s > 2 ? 1u : onto);
+                        }
+                        __syncwarp();
+                        if (!wait(M::kPReady + 2 + i, p_phase[i] ^ 1)) return;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int s = 0; s < BK / 16; ++s)
+                                if (!(s & 2))
+                                    umma_bf16_ts(t0 + 256 + D * i, t0 + 128 * i + 64 * (s >> 2) + 32 + 8 * (s & 3),
+                                                 desc_add(dv, s * 2048), id_o, 1u);
                             if (j + 1 == n) {
                                 umma_commit(&bar[M::kODone + i]);
                             } else {
