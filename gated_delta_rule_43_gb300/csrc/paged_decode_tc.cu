@@ -396,23 +396,27 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                             p[g] = ex2(z[g0 + g] - r[g]);
                             l[g0 + g] += p[g];
                         }
+                        // (neighbouring lanes, that is keys, exchange what they have of these heads, so that each
+                        // stores a head's four bytes, or two bf16, in one)
                         if constexpr (E4M3) {
+                            uint32_t w[2];
 #pragma unroll
-                            for (int g = 0; g < 4; g += 2) {
-                                const uint32_t w = split_e4m3(ex2(z[g0 + g] + ev[t] - r2[g]), ex2(z[g0 + g + 1] + ev[t] - r2[g + 1]));
-                                const uint32_t at = key_at & 15, piece = key_at >> 4;
+                            for (int g = 0; g < 4; g += 2)
+                                w[g / 2] = split_e4m3(ex2(z[g0 + g] + ev[t] - r2[g]), ex2(z[g0 + g + 1] + ev[t] - r2[g + 1]));
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {   // (the row's place in its group of 8 is known here)
-                                    const int row = (i & 2 ? NR : 0) + g0 + g + (i & 1);
-                                    to[row * 128 + ((piece ^ (row & 7)) << 4) + at] = (uint8_t)(w >> (8 * i));
-                                }
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t y = __byte_perm(w[0], w[1], i ? 0x7632 : 0x5410);
+                                y = __byte_perm(y, __shfl_xor_sync(0xffffffffu, y, 1), lane & 1 ? 0x3715 : 0x6240);
+                                y = __byte_perm(y, __shfl_xor_sync(0xffffffffu, y, 2), lane & 2 ? 0x3276 : 0x5410);
+                                const int row = i * NR + g0 + (lane & 3);
+                                *reinterpret_cast<uint32_t *>(to + row * 128 + (((key_at >> 4) ^ (row & 7)) << 4) + (key_at & 12)) = y;
                             }
                         } else {
 #pragma unroll
                             for (int g = 0; g < 4; g += 2) {
-                                const uint32_t w = pack2(p[g], p[g + 1]);
-                                *reinterpret_cast<uint16_t *>(to + sw128_offset(g0 + g, key_at, 16)) = (uint16_t)w;
-                                *reinterpret_cast<uint16_t *>(to + sw128_offset(g0 + g + 1, key_at, 16)) = (uint16_t)(w >> 16);
+                                uint32_t y = pack2(p[g], p[g + 1]);
+                                y = __byte_perm(y, __shfl_xor_sync(0xffffffffu, y, 1), lane & 1 ? 0x3276 : 0x5410);
+                                *reinterpret_cast<uint32_t *>(to + sw128_offset(g0 + g + (lane & 1), key_at & ~1, 16)) = y;
                             }
                         }
                     }
