@@ -285,54 +285,63 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                     continue;
                 }
                 const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
-                // this thread's key of each tile: whether it is visible, and (e4m3) its scales
+                // whether this thread's key of each tile is visible; (e4m3) its scales
                 uint32_t seen = 0;
-                float ks[kTiles], ev[kTiles];
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
                     const int key = it.tile(first + t) * BK + key_at;
                     seen |= (uint32_t)(t < many && key <= pos && (key > lowest || key < sinks)) << t;
                 }
-                if (E4M3) {
-                    if (!wait(M::kScFull + ps.stage, ps.phase)) return;
-                    const float *sc = reinterpret_cast<const float *>(sm + M::kScales + ps.stage * M::kScaleBytes);
-#pragma unroll
-                    for (int t = 0; t < kTiles; ++t) {   // (what is behind the piece's tiles is not seen)
-                        ks[t] = sc[128 * t + key_at];
-                        ev[t] = (float)((int)(__float_as_uint(sc[128 * (kTiles + t) + key_at]) >> 23) - 127);
-                    }
-                }
+                if (E4M3 && !wait(M::kScFull + ps.stage, ps.phase)) return;
+                const float *sc = reinterpret_cast<const float *>(sm + M::kScales + ps.stage * M::kScaleBytes) + key_at;
+                auto key_scale = [&](int t) { return sc[128 * t]; };
+                auto value_log = [&](int t) { return (float)((int)(__float_as_uint(sc[128 * (kTiles + t)]) >> 23) - 127); };
                 if (!wait(M::kSReady + ps.stage, ps.phase)) return;
                 tc_fence_after();
                 // The scores in units of log 2, -inf where the key is not visible, and the piece's maxima: m
                 // of the scores; (e4m3) m2 of the weights with the values' scales
                 const uint32_t tS = tmem + lanes + ps.stage * kTiles * N;
-                // (held from there on for up to 8 heads, read again for 16: registers)
-                constexpr int kHeld = NR <= 8 ? kTiles : 1, kTogether = C <= 16 ? kTiles : 1;
+                // Up to 4 heads: all tiles at once, held from there on.  More: tile by tile in loops that stay
+                // loops, read again for the weights.  (Straight-line code for 8 heads and 4 tiles misses the
+                // instruction cache: 14k cycles a piece.)
+                constexpr bool kAll = NR <= 4;
+                constexpr int kUnroll = kAll ? kTiles : 1, kHeld = kAll ? kTiles : 1;
                 float x[kHeld][NR], m[NR], m2[NR];
                 auto scores = [&](const float(&y)[C], int t, float(&x)[NR]) {
                     const bool see = (seen >> t) & 1;
+                    const float ks = E4M3 ? key_scale(t) : f;
 #pragma unroll
                     for (int g = 0; g < NR; ++g)
-                        x[g] = !see ? -INFINITY : E4M3 ? (y[g] + 0.0625f * y[(E4M3 ? NR : 0) + g]) * (ks[t] * qf[g]) : y[g] * f;
+                        x[g] = !see ? -INFINITY : E4M3 ? (y[g] + 0.0625f * y[(E4M3 ? NR : 0) + g]) * (ks * qf[g]) : y[g] * ks;
                 };
 #pragma unroll
                 for (int g = 0; g < NR; ++g) m[g] = m2[g] = -INFINITY;
+                auto highest = [&](const float(&z)[NR], int t) {
+                    const float ev = E4M3 ? value_log(t) : 0.f;
 #pragma unroll
-                for (int t0 = 0; t0 < kTiles; t0 += kTogether) {
-                    float y[kTogether][C];
+                    for (int g = 0; g < NR; ++g) {
+                        m[g] = fmaxf(m[g], z[g]);
+                        if (E4M3) m2[g] = fmaxf(m2[g], z[g] + ev);
+                    }
+                };
+                if constexpr (kAll) {   // (a tile behind the piece's last is read, but nothing of it is seen)
+                    float y[kTiles][C];
 #pragma unroll
-                    for (int t = 0; t < kTogether; ++t) tmem_ld(tS + (t0 + t) * N, y[t]);
+                    for (int t = 0; t < kTiles; ++t) tmem_ld(tS + t * N, y[t]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int t = 0; t < kTogether; ++t) {
-                        float(&z)[NR] = x[kHeld > 1 ? t0 + t : 0];
-                        scores(y[t], t0 + t, z);
-#pragma unroll
-                        for (int g = 0; g < NR; ++g) {
-                            m[g] = fmaxf(m[g], z[g]);
-                            if (E4M3) m2[g] = fmaxf(m2[g], z[g] + ev[t0 + t]);
-                        }
+                    for (int t = 0; t < kTiles; ++t) {
+                        scores(y[t], t, x[kHeld > 1 ? t : 0]);
+                        highest(x[kHeld > 1 ? t : 0], t);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int t = 0; t < many; ++t) {
+                        float y[C];
+                        tmem_ld(tS + t * N, y);
+                        tmem_ld_wait();
+                        scores(y, t, x[0]);
+                        highest(x[0], t);
                     }
                 }
                 float *place = reinterpret_cast<float *>(sm + M::kRed) + 256 * side + 128 * (turn & 1);
@@ -371,38 +380,35 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                     for (int g = g0; g < g0 + 4; ++g) l[g] = 0.f;
                 }
                 // The weights, as the products' columns
-#pragma unroll
-                for (int g0 = 0; g0 < NR; g0 += 4) {
-                    if (g0 >= rows) break;
-                    float r[4], r2[4];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        r[g] = m[g0 + g] == -INFINITY ? 0.f : m[g0 + g];
-                        r2[g] = m2[g0 + g] == -INFINITY ? 0.f : m2[g0 + g] - 8.f;
+                const int last = kAll ? kTiles : many;
+#pragma unroll kUnroll
+                for (int t = 0; t < last; ++t) {
+                    if constexpr (!kAll) {
+                        float y[C];
+                        tmem_ld(tS + t * N, y);
+                        tmem_ld_wait();
+                        scores(y, t, x[0]);
                     }
+                    const float(&z)[NR] = x[kHeld > 1 ? t : 0];
+                    const float ev = E4M3 ? value_log(t) : 0.f;
+                    uint8_t *to = sm + M::kP + (ps.stage * kTiles + t) * M::kPTile;
 #pragma unroll
-                    for (int t = 0; t < kTiles; ++t) {
-                        if constexpr (kHeld == 1) {
-                            float y[C];
-                            tmem_ld(tS + t * N, y);
-                            tmem_ld_wait();
-                            scores(y, t, x[0]);
-                        }
-                        const float(&z)[NR] = x[kHeld > 1 ? t : 0];
-                        uint8_t *to = sm + M::kP + (ps.stage * kTiles + t) * M::kPTile;
+                    for (int g0 = 0; g0 < NR; g0 += 4) {
+                        if (g0 >= rows) break;
                         float p[4];
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
-                            p[g] = ex2(z[g0 + g] - r[g]);
+                            p[g] = ex2(z[g0 + g] - (m[g0 + g] == -INFINITY ? 0.f : m[g0 + g]));
                             l[g0 + g] += p[g];
                         }
                         // (neighbouring lanes, that is keys, exchange what they have of these heads, so that each
                         // stores a head's four bytes, or two bf16, in one)
                         if constexpr (E4M3) {
-                            uint32_t w[2];
+                            float v[4];
 #pragma unroll
-                            for (int g = 0; g < 4; g += 2)
-                                w[g / 2] = split_e4m3(ex2(z[g0 + g] + ev[t] - r2[g]), ex2(z[g0 + g + 1] + ev[t] - r2[g + 1]));
+                            for (int g = 0; g < 4; ++g)
+                                v[g] = ex2(z[g0 + g] + ev - (m2[g0 + g] == -INFINITY ? 0.f : m2[g0 + g] - 8.f));
+                            const uint32_t w[2] = {split_e4m3(v[0], v[1]), split_e4m3(v[2], v[3])};
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 uint32_t y = __byte_perm(w[0], w[1], i ? 0x7632 : 0x5410);
