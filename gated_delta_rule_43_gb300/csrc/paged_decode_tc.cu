@@ -594,77 +594,62 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
         });
         if (ok) values();
     } else if (warp == kLoadWarp) {
+        // Lane 8 t + b has to do with box b of a piece's tile t: its page is looked up a piece ahead, and the
+        // loop over tiles is short (with every lane holding a box of all tiles, unrolled, a tile took the warp
+        // 800 cycles, more than the memory).
         const int rows = min(BK, 1 << c.shift), boxes = BK / rows, runs = page_runs(c, D);
         const int none = (c.P - 1) * runs + c.Hk;   // past the last run: zeros
-        // the piece whose values are still to be loaded: its tiles, this lane's boxes of them
-        int owed = 0, owed_run[kTiles], owed_row[kTiles];
-        auto load = [&](const void *map, int many, const int(&run)[kTiles], const int(&row)[kTiles]) {
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                if (t >= many) break;
+        const int my_tile = lane >> 3, box = lane & 7;
+        int owed = 0, owed_run = 0, owed_row = 0;   // the piece whose values are still to be loaded
+        auto load = [&](const void *map, int many, int run, int row) {
+#pragma unroll 1
+            for (int t = 0; t < many; ++t) {
                 if (!wait(M::kFree + kv.stage, kv.phase ^ 1)) return;
                 if (lane == 0) mbar_arrive_expect_tx(&bar[M::kFull + kv.stage], M::kTile);
                 __syncwarp();
-                if (lane < boxes) {
-                    const uint32_t to = base + M::kKV + kv.stage * M::kTile + lane * rows * (E4M3 ? D : 128);
+                if (t == my_tile && box < boxes) {
+                    const uint32_t to = base + M::kKV + kv.stage * M::kTile + box * rows * (E4M3 ? D : 128);
 #pragma unroll
                     for (int x = 0; x < (E4M3 ? 1 : D / 64); ++x)
-                        tma_load_rows(to + x * 16384, map, 64 * x, row[t], run[t], bars + 8 * (M::kFull + kv.stage));
+                        tma_load_rows(to + x * 16384, map, 64 * x, row, run, bars + 8 * (M::kFull + kv.stage));
                 }
                 __syncwarp();
                 kv.step(M::kStages);
                 ++loads;
             }
         };
-        auto owed_values = [&] {
-            if (owed) load(&tv, owed, owed_run, owed_row);
-            owed = 0;
-        };
         each_item([&](const Item &it) {
-            const int tiles = it.k1 - it.k0, count = pieces(tiles), pos = it.pos;
-            if (tiles == 0) owed_values();
-            // the pages of this lane's boxes of a piece's tiles, looked up a piece ahead; which of them are
-            // seen by anybody
-            int page[kTiles];
-            uint32_t seen = 0;
+            const int tiles = it.k1 - it.k0, count = pieces(tiles), pos = it.pos, n = it.n, h = it.h;
+            int page = -1;
+            bool seen = false;   // by the token; else no page is needed
+            auto key_of = [&](int u) { return it.tile(it.k0 + piece_at(tiles, count, u) + my_tile) * BK + box * rows; };
             auto look_up = [&](int u) {
-                const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
-                seen = 0;
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    const int key = it.tile(first + t) * BK + lane * rows;
-                    if (t < many && lane < boxes && key <= pos && (window <= 0 || key < sinks || key + rows > pos - window + 1)) {
-                        page[t] = c.table[(int64_t)it.n * c.width + (key >> c.shift)];
-                        seen |= 1u << t;
-                    }
-                }
+                const int many = piece_at(tiles, count, u + 1) - piece_at(tiles, count, u), key = key_of(u);
+                seen = my_tile < many && box < boxes && key <= pos && (window <= 0 || key < sinks || key + rows > pos - window + 1);
+                if (seen) page = c.table[(int64_t)n * c.width + (key >> c.shift)];
             };
             if (tiles > 0) look_up(0);
-            for (int u = 0; u < count; ++u) {
-                const int first = it.k0 + piece_at(tiles, count, u), many = it.k0 + piece_at(tiles, count, u + 1) - first;
-                int run[kTiles], row[kTiles];
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    row[t] = (it.tile(first + t) * BK + lane * rows) & ((1 << c.shift) - 1);
-                    run[t] = none;   // rows that nobody sees, or no page
-                    if ((seen >> t) & 1) {
-                        if (page[t] >= 0 && page[t] < c.P) run[t] = page[t] * runs + it.h;
-                        else report(st, KDA_ERR_INVALID_ARG, it.n, 91);
+            // (a turn more, for the values of the last piece where the next item has none)
+            for (int u = 0; u < count || (tiles == 0 && owed); ++u) {
+                int run = none, row = 0, many = 0;
+                if (u < count) {
+                    many = piece_at(tiles, count, u + 1) - piece_at(tiles, count, u);
+                    row = key_of(u) & ((1 << c.shift) - 1);
+                    if (seen) {
+                        if (page >= 0 && page < c.P) run = page * runs + h;
+                        else report(st, KDA_ERR_INVALID_ARG, n, 91);
                     }
+                    if (u + 1 < count) look_up(u + 1);
+                    load(&tk, many, run, row);
                 }
-                if (u + 1 < count) look_up(u + 1);
-                load(&tk, many, run, row);
-                if (ok) owed_values();
+                if (ok && owed) load(&tv, owed, owed_run, owed_row);
                 if (!ok) return;
                 owed = many;
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    owed_run[t] = run[t];
-                    owed_row[t] = row[t];
-                }
+                owed_run = run;
+                owed_row = row;
             }
         });
-        if (ok) owed_values();
+        if (ok && owed) load(&tv, owed, owed_run, owed_row);
     } else if (warp == kItemWarp) {
         Ring at;
         Cut from = cuts[0];
