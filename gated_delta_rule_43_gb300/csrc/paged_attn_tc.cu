@@ -721,14 +721,14 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                             // 16 bytes (their places swizzled by the load) become 16 bf16
                             const int place = D == 128 ? x ^ (row & 7) : x ^ ((row >> 1) & 3);
                             const uint4 in = *reinterpret_cast<const uint4 *>(from + 16 * place);
-                            const uint32_t word[4] = {in.x, in.y, in.z, in.w};
+                            const uint32_t word[4] = {seen ? in.x : 0u, seen ? in.y : 0u, seen ? in.z : 0u, seen ? in.w : 0u};
                             uint32_t out[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
                                     (__nv_fp8x2_storage_t)(word[i / 2] >> (16 * (i & 1))), __NV_E4M3);
                                 const float2 y = __half22float2(__half2(h));
-                                out[i] = seen ? pack2(y.x * s, y.y * s) : 0u;
+                                out[i] = pack2(y.x * s, y.y * s);
                             }
                             *reinterpret_cast<uint4 *>(to + sw128_offset(row, 16 * x, BK)) =
                                 make_uint4(out[0], out[1], out[2], out[3]);
