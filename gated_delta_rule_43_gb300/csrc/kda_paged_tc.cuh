@@ -106,6 +106,12 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar0, uint32_t parity0, uint3
     }
 }
 
+// For the others of a named barrier, from a warp that leaves its role because a wait expired: whoever stands there
+// or comes there next goes on, to a wait that expires as well.
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t n) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
 // 32 lanes x 4, 8, 16 or 32 consecutive columns of tensor memory; nothing may be used before
 // tmem_ld_wait
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[4]) {

@@ -93,7 +93,7 @@ paged_simt_kernel(Cache c, const TQ *__restrict__ q, int64_t q_stride, TQ *__res
     }
     const int r = tid / 4, quarter = tid % 4;
     const int pos = t.s.pos + (t.first + r) / group;
-    const int lowest = window > 0 ? max(pos - window, -1) : -1;   // keys above it are in the window
+    const int lowest = window > 0 ? max(max(pos, 0) - window, -1) : -1;   // keys above it are in the window
     const KeyBlocks kb = key_blocks(max(0, t.s.pos + t.first / group), t.s.pos + (t.first + t.rows - 1) / group, window,
                                     sinks, BK);
     const int b0 = (int)((int64_t)kb.count * split / splits), b1 = (int)((int64_t)kb.count * (split + 1) / splits);

@@ -327,7 +327,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             const bool live = r - lane < it.rows, mine = r < it.rows;   // (of a whole warp; this row)
             const int pos = it.pos0 + (it.row0 + min(r, it.rows - 1)) / group;
             const int pos_lo = __shfl_sync(0xffffffffu, pos, 0), pos_hi = __shfl_sync(0xffffffffu, pos, 31);
-            const int lowest = window > 0 ? max(pos - window, -1) : -1;   // keys above it are in the window
+            const int lowest = window > 0 ? max(max(pos, 0) - window, -1) : -1;   // keys above it are in the window
             const int end = it.end(tile), begin = it.k0;
             float m = -INFINITY, l = 0.f;   // m: of the scores as they come
             for (int k = begin; k < end; ++k) {
@@ -338,7 +338,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                 // the half's first and second 32 keys, -inf where this row does not see them
                 const int key0 = it.block(k) * BK + 64 * half;
                 // are there keys that one of the warp's rows does not see?
-                const bool edge = key0 + 63 > pos_lo || (window > 0 && key0 <= pos_hi - window && key0 + 63 >= sinks);
+                const bool edge = key0 + 63 > pos_lo || (window > 0 && key0 <= max(pos_hi, 0) - window && key0 + 63 >= sinks);
                 auto hide = [&](float(&s)[32], int j0) {
                     if (!edge) return;
                     const int upto = pos - key0 - j0, above = lowest - key0 - j0, first = sinks - key0 - j0;
@@ -478,6 +478,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             }
             tc_fence_before();
         });
+        if (!ok) named_bar_arrive(1 + tile, 256);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == kMmaWarp) {
@@ -753,6 +754,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
     if (__syncthreads_or(!ok)) {
         // an expired wait: what is in flight ends (each wait bounded again) before the tensor memory is
         // released and the CTA leaves
+        asm volatile("cp.async.wait_all;" ::: "memory");
         tmem_st_wait();
         tc_fence_before();
         if (warp == kMmaWarp) {

@@ -8,7 +8,7 @@
 //
 // e4m3 pages meet e4m3 queries and weights, of which there are two each: x = hi + lo / 16, hi = e4m3(x), lo =
 // e4m3(16 (x - hi)), in columns of their own.  Together they hold the 8 bits of a bf16, down to 2^-22 of
-// the largest (rows of queries are scaled by a power of two, weights by 2^8 below their largest), so the
+// the largest (rows of queries are scaled by a power of two, weights so that their largest is 2^7 to 2^8), so the
 // keys' and values' bytes need no conversion: nothing but the products touches them.  A key's scale
 // multiplies its scores, a value's is part of its weight.
 //
@@ -295,7 +295,12 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                 if (E4M3 && !wait(M::kScFull + ps.stage, ps.phase)) return;
                 const float *sc = reinterpret_cast<const float *>(sm + M::kScales + ps.stage * M::kScaleBytes) + key_at;
                 auto key_scale = [&](int t) { return sc[128 * t]; };
+                // (a value's scale by its exponent, which sets what weights are measured in, and what it is over
+                // that: 1 for a power of two)
                 auto value_log = [&](int t) { return (float)((int)(__float_as_uint(sc[128 * (kTiles + t)]) >> 23) - 127); };
+                auto value_rest = [&](int t) {
+                    return __uint_as_float((__float_as_uint(sc[128 * (kTiles + t)]) & 0x7fffffu) | 0x3f800000u);
+                };
                 if (!wait(M::kSReady + ps.stage, ps.phase)) return;
                 tc_fence_after();
                 // The scores in units of log 2, -inf where the key is not visible, and the piece's maxima: m
@@ -390,7 +395,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                         scores(y, t, x[0]);
                     }
                     const float(&z)[NR] = x[kHeld > 1 ? t : 0];
-                    const float ev = E4M3 ? value_log(t) : 0.f;
+                    const float ev = E4M3 ? value_log(t) : 0.f, rest = E4M3 ? value_rest(t) : 1.f;
                     uint8_t *to = sm + M::kP + (ps.stage * kTiles + t) * M::kPTile;
 #pragma unroll
                     for (int g0 = 0; g0 < NR; g0 += 4) {
@@ -407,7 +412,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                             float v[4];
 #pragma unroll
                             for (int g = 0; g < 4; ++g)
-                                v[g] = ex2(z[g0 + g] + ev - (m2[g0 + g] == -INFINITY ? 0.f : m2[g0 + g] - 8.f));
+                                v[g] = rest * ex2(z[g0 + g] + ev - (m2[g0 + g] == -INFINITY ? 0.f : m2[g0 + g] - 7.f));
                             const uint32_t w[2] = {split_e4m3(v[0], v[1]), split_e4m3(v[2], v[3])};
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
@@ -447,7 +452,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                         const float top = fmaxf(run_m[g], m[g]), ref = top == -INFINITY ? 0.f : top;
                         const float b = ex2(m[g] - ref);
                         keep[g] = ex2(run_m[g] - ref);
-                        add[g] = E4M3 ? ex2(m2[g] - 8.f - ref) : b;
+                        add[g] = E4M3 ? ex2(m2[g] - 7.f - ref) : b;
                         run_l[g] = run_l[g] * keep[g] + l[g] * b;
                         run_m[g] = top;
                     }
@@ -510,6 +515,10 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                 }
             }
         });
+        if (!ok) {
+            named_bar_arrive(1 + side, 128);
+            named_bar_arrive(3, 256);
+        }
     } else if (warp == kMmaWarp) {
         constexpr uint32_t id_s = E4M3 ? idesc_e4m3(128, N, false) : idesc_bf16(128, N, false, false);
         constexpr uint32_t id_o = E4M3 ? idesc_e4m3(D, N, true) : idesc_bf16(D, N, true, false);

@@ -472,8 +472,10 @@ kda_status kda_state_pool_compact(float *pool, int32_t P, int64_t slot_elems,
  *                      the next (a multiple of page_size * D, at least Hk times that), so that both
  *                      may be halves of one pool [num_pages, 2, Hk, page_size, D]
  *   k_scales, v_scales [num_pages, Hk, page_size] fp32, scale_stride from page to page (a multiple of 4;
- *                      16-byte aligned), with dtype KDA_E4M3 (NULL otherwise): a row of D values stands for scale * e4m3.  Scales
- *                      are powers of two, so scale * e4m3 is a bf16 exactly.
+ *                      16-byte aligned), with dtype KDA_E4M3 (NULL otherwise): a row of D values
+ *                      stands for scale * e4m3.  kda_kv_cache_write makes them powers of two, so that
+ *                      scale * e4m3 is a bf16 exactly; other positive scales are taken too, at
+ *                      one more rounding to bf16.
  *   block_table        [num_seqs, table_width] int32: position j of sequence n lies in slot
  *                      j % page_size of page block_table[n][j / page_size].  Entries that hold no
  *                      position in use are not read (any value may stand there).

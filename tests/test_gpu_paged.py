@@ -259,6 +259,71 @@ def test_pools_past_32_bits():
     assert torch.equal(pools[0][16500, 0, 2049 - 2048], k[0, 0])
 
 
+@pytest.mark.parametrize("cache", [BF, E4M3])
+def test_many_sequences_most_without_tokens(cache):
+    """Thousands of sequences, few of them with tokens, and long ones among them."""
+    lens, before = [0] * 3000, [0] * 3000
+    for i, n in enumerate((0, 1, 40, 700, 701, 702, 2047, 2048, 2999)):
+        lens[n], before[n] = 1 + 37 * i, 500 * (i % 3)
+    b = Batch(lens, before, 2, 64, BF, cache, 16, device=DEV)
+    q = b.queries(8)
+    o = kda.paged_attn_fwd(q, *b.cache, b.cu, **b.scales, check=True)
+    U.check_attention(o, b, q)
+    # one token each: those without are padding
+    ctx = b.kv_lens.clone()
+    b.cu, b.T = torch.arange(3001, dtype=torch.int32, device=DEV), 3000
+    one = torch.randn(3000, 8, 64, device=DEV).to(BF)
+    got = kda.paged_attn_decode_step(one, *b.cache, **b.scales, check=True)
+    live = ctx > 0
+    assert not got[~live].any()
+    U.check_attention(got, b, one)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_scales_of_others(D):
+    """Scales that are no powers of two, some tiny, some large."""
+    b = Batch([40, 3], [700, 200], 2, D, BF, E4M3, 32, device=DEV)
+    gen = torch.Generator().manual_seed(1)
+    for s, spread in ((b.k_scales, 0.3), (b.v_scales, 4.0)):
+        s.mul_(torch.exp(spread * torch.randn(s.shape, generator=gen)).to(DEV))
+    q = b.queries(8)
+    # chunks take keys and values rounded to bf16 once, so that is what they are held against
+    k, v = U.values(b.k_pages, b.k_scales), U.values(b.v_pages, b.v_scales)
+    rounded = Batch([40, 3], [700, 200], 2, D, BF, BF, 32, device=DEV)
+    rounded.k_pages, rounded.v_pages, rounded.table = k.to(BF), v.to(BF), b.table
+    U.check_attention(kda.paged_attn_fwd(q, *b.cache, b.cu, **b.scales, check=True), rounded, q)
+    b.cu, b.T, one = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV), 2, q[:2]
+    U.check_attention(kda.paged_attn_decode_step(one, *b.cache, **b.scales, check=True), b, one)
+    rk, rv = kda.kv_cache_read(*b.cache, b.cu, total_tokens=2, dtype=F32, **b.scales, check=True)
+    for t, n, pos in U.places(b):
+        page = int(b.table[n, pos // 32])
+        assert torch.equal(rk[t].double(), k[page, :, pos % 32].float().double())
+        assert torch.equal(rv[t].double(), v[page, :, pos % 32].float().double())
+
+
+@pytest.mark.parametrize("cache", [BF, E4M3])
+def test_what_is_not_finite(cache):
+    """A NaN in a query spoils its own row and head; in a key or a value, those who see it."""
+    b = Batch([100, 5], [300, 10], 2, 128, BF, cache, 16, device=DEV)
+    q = b.queries(8)
+    good = kda.paged_attn_fwd(q, *b.cache, b.cu, **b.scales, check=True)
+    bad = q.clone()
+    bad[7, 3, 5], bad[50, 1, 0] = math.nan, math.inf
+    o = kda.paged_attn_fwd(bad, *b.cache, b.cu, **b.scales)
+    hurt = torch.zeros(105, 8, dtype=torch.bool, device=DEV)
+    hurt[7, 3] = hurt[50, 1] = True
+    assert o[hurt].isnan().all() and torch.equal(o[~hurt], good[~hurt])
+    two = kda.paged_attn_decode_step(bad[6:8], *b.cache, **b.scales)
+    assert two[1, 3].isnan().all() and two[0].isfinite().all() and two[1, 4:].isfinite().all()
+    # a value of the last token of sequence 0, head 0: its last row sees it, sequence 1 and head 1 do not
+    page = int(b.table[0, 399 // 16])
+    b.v_pages.view(torch.uint8)[page, 0, 399 % 16] = 0x7f
+    o = kda.paged_attn_fwd(q, *b.cache, b.cu, **b.scales)
+    if cache is E4M3:
+        assert o[99, :4].isnan().all()
+    assert torch.equal(o[100:], good[100:]) and torch.equal(o[:100, 4:], good[:100, 4:])
+
+
 def code_of(call):
     ws = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
     call(ws)
