@@ -186,6 +186,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&x);
 }
+// 32 bytes, a whole sector of memory, in one store (32-byte aligned)
+__device__ __forceinline__ void store32(void *to, const uint32_t *x) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
 // 2^x by the special-function unit (relative error near 2^-22)
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -17,13 +17,15 @@
 // workspace (O, m, l in fp32) and joined by a second kernel.
 //
 // One CTA an SM:
-//   warps 0-7, 8-15  the rows of the two tiles, a thread for each half of a row's keys and of its channels:
-//                    scores out of tensor memory, P into it (over the scores of the half's last 32 keys),
-//                    outputs; the next item's queries into the place of this one's after the last scores
-//   warp 16          issues the products (and zeroes values behind a sequence's end: slots that nobody has
-//                    written)                   warp 17   loads keys and values, page by page
-//   warp 18          goes through the range's items for everyone
-//   warps 20-23      (e4m3 pages) make the operands out of the bytes that warp 17 loads: scale * e4m3 is a
+//   warps 0-3, 4-7   the rows of the two tiles, a thread each: scores out of tensor memory, P into it, over
+//                    the scores
+//   warp 8           issues the products (and zeroes values behind a sequence's end: slots that nobody has
+//                    written)                   warp 9    loads keys and values, page by page
+//   warp 10          goes through the range's items for everyone
+//   warps 12-15      an item's edges: its queries, into the place of the last one's after the last scores, and
+//                    its outputs, while the next item's first weights are formed (done by the rows' own warps,
+//                    an item cost 10k cycles beside its blocks)
+//   warps 16-19      (e4m3 pages) make the operands out of the bytes that warp 9 loads: scale * e4m3 is a
 //                    bf16 exactly, so the products are those of a bf16 cache
 // Products of one tile run while the other's scores become weights: P0 V, Q0 K', P1 V, Q1 K', ...
 #include "kda_paged_tc.cuh"
@@ -33,9 +35,9 @@ namespace paged {
 namespace tc {
 
 constexpr int kRows = 256;          // rows of an item
-template <bool E4M3> constexpr int kThreads = E4M3 ? 768 : 640;
-constexpr int kRowWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kItemWarp = 18, kMakeWarp = 20;
-constexpr int kItemCost = 4;        // an item's queries and outputs, in blocks
+template <bool E4M3> constexpr int kThreads = E4M3 ? 640 : 512;
+constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kEdgeWarp = 12, kMakeWarp = 16;
+constexpr int kItemCost = 3;        // an item's queries and outputs, in blocks
 constexpr int kUncut = 6;           // blocks of an item that is not cut
 constexpr int kRing = 4;            // items known ahead
 constexpr float kGrow = 8.f;        // log2 of what the maximum may grow before O is rescaled
@@ -177,11 +179,11 @@ template <int D, bool E4M3> struct Map {
     static constexpr int kStages = D == 64 ? 8 : E4M3 ? 4 : 5, kRaws = E4M3 ? D == 64 ? 4 : 2 : 0;
     static constexpr uint32_t kQ = 0, kKV = 2 * kTile, kRaw = kKV + kStages * kTile;
     static constexpr uint32_t kItems = kRaw + kRaws * kRawTile;
-    static constexpr uint32_t kTops = kItems + kRing * (uint32_t)sizeof(Item);   // [2 tiles][2 halves][128 rows]
+    static constexpr uint32_t kTops = kItems + kRing * (uint32_t)sizeof(Item);   // [2 tiles][maximum, sum][128 rows]
     static constexpr uint32_t kBar = kTops + 2048;
     // barriers
-    static constexpr int kFull = 0, kFree = kStages, kQFull = 2 * kStages, kSReady = kQFull + 2,
-                         kPReady = kSReady + 2 /* [2 parts][2 tiles] */, kODone = kPReady + 4, kItemFull = kODone + 2,
+    static constexpr int kFull = 0, kFree = kStages, kQFull = 2 * kStages, kQFree = kQFull + 2, kSReady = kQFree + 2,
+                         kPReady = kSReady + 2 /* [2 parts][2 tiles] */, kODone = kPReady + 4, kOFree = kODone + 2, kEnds = kOFree + 2, kEndsFree = kEnds + 2, kItemFull = kEndsFree + 2,
                          kItemFree = kItemFull + kRing, kDrain = kItemFree + kRing, kRawFull = kDrain + 1, kRawFree = kRawFull + kRaws,
                          kBars = kRawFree + kRaws;
     static constexpr uint32_t kSlot = kBar + kBars * 8, kBytes = kSlot + 16;
@@ -212,15 +214,19 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             mbar_init(&bar[M::kFree + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar[M::kQFull + i], 8);
+            mbar_init(&bar[M::kQFull + i], 4);
+            mbar_init(&bar[M::kQFree + i], 1);
+            mbar_init(&bar[M::kOFree + i], 4);
+            mbar_init(&bar[M::kEnds + i], 4);
+            mbar_init(&bar[M::kEndsFree + i], 4);
             mbar_init(&bar[M::kSReady + i], 1);
-            mbar_init(&bar[M::kPReady + i], 8);
-            mbar_init(&bar[M::kPReady + 2 + i], 8);
+            mbar_init(&bar[M::kPReady + i], 4);
+            mbar_init(&bar[M::kPReady + 2 + i], 4);
             mbar_init(&bar[M::kODone + i], 1);
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&bar[M::kItemFull + i], 1);
-            mbar_init(&bar[M::kItemFree + i], kRowWarps + (E4M3 ? 6 : 2));
+            mbar_init(&bar[M::kItemFree + i], kRowWarps + (E4M3 ? 10 : 6));
         }
         for (int i = 0; i < M::kRaws; ++i) {
             mbar_init(&bar[M::kRawFull + i], 1);
@@ -264,65 +270,24 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
     Ring kv;            // fills of the ring of keys and values (keys, values, keys, ...)
     uint32_t loads = 0; // (load warp) fills issued
 
-    // Registers for the rows' threads from the others: launched with 61440 in both forms, 640 threads of 96
-    // (then 512 x 104 + 128 x 64) or 768 of 80 (512 x 88 + 256 x 64).
+    // Registers for the rows' threads from the others: launched with 512 x 128 = 65536, then 256 x 168 +
+    // 256 x 88, the same; for e4m3 pages 640 x 96 = 61440, then 256 x 144 + 384 x 64, the same.
     if (warp < kRowWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(E4M3 ? 88 : 104));
-        const int tile = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(E4M3 ? 144 : 168));
+        const int tile = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        const uint32_t tSl = tmem + 128 * tile + 64 * half + lanes, tPl = tSl + 32,
-                       tOl = tmem + 256 + D * tile + D / 2 * half + lanes;
+        const uint32_t tS = tmem + 128 * tile + lanes, tO = tmem + 256 + D * tile + lanes;
         const float f = scale * kLog2e;
-        // What the two halves of a row tell each other.  (Between one time and the next lies a product that
-        // waits for both halves: nothing is written before it has been read.)
-        float *tops = reinterpret_cast<float *>(sm + M::kTops) + 256 * tile + 32 * quarter + lane;
-        auto other_half = [&](float x) {
-            tops[128 * half] = x;
-            named_bar_sync(1 + tile, 256);
-            return tops[128 * (half ^ 1)];
-        };
-        // P goes to its product in two parts, so that the first runs while the second is formed: the last 32
-        // keys of each half, then the first
+        // P goes to its product in two parts, so that the first runs while the second is formed
         auto part_done = [&](int part) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[M::kPReady + 2 * part + tile]);
             __syncwarp();
         };
-        uint32_t s_phase = 0, o_phase = 0;
-        // The queries of this warp's rows of the item at `at`: a row's address by its lane, its 16-byte
-        // pieces side by side, half of them by each half.
-        auto start_queries = [&](const Ring &at) {
-            if (!wait(M::kItemFull + at.stage, at.phase)) return false;
-            const Item &it = items[at.stage];
-            const int row = 128 * tile + 32 * quarter;
-            if (it.n < 0 || it.end(tile) == it.k0) return false;
-            if (row < it.rows) {
-                const int mine = it.row0 + min(row + lane, it.rows - 1), token = mine / group;
-                const int64_t from = (int64_t)(it.tok0 + token) * q_stride + (int64_t)(it.h * group + mine - token * group) * D;
-                constexpr int U = D / 8;   // pieces of a row
-#pragma unroll 4
-                for (int i = half * U / 2; i < (half + 1) * U / 2; ++i) {
-                    const int r = (32 * i + lane) / U, x = lane % U;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                     base + M::kQ + tile * M::kTile + sw128_offset(32 * quarter + r, 8 * x, 128)),
-                                 "l"(q + __shfl_sync(0xffffffffu, from, r) + 8 * x)
-                                 : "memory");
-                }
-            }
-            return true;
-        };
-        auto finish_queries = [&] {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[M::kQFull + tile]);
-            __syncwarp();
-        };
-        Ring at_next;
-        if (start_queries(at_next)) finish_queries();
+        uint32_t s_phase = 0;
+        uint32_t ends = 0;   // parity of items with anything for this tile
         each_item([&](const Item &it) {
-            at_next.step(kRing);
             const int r = 128 * tile + 32 * quarter + lane;
             const bool live = r - lane < it.rows, mine = r < it.rows;   // (of a whole warp; this row)
             const int pos = it.pos0 + (it.row0 + min(r, it.rows - 1)) / group;
@@ -334,33 +299,27 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                 if (!wait(M::kSReady + tile, s_phase)) return;
                 s_phase ^= 1;
                 tc_fence_after();
-                float s0[32], s1[32], top = -INFINITY;
-                // the half's first and second 32 keys, -inf where this row does not see them
-                const int key0 = it.block(k) * BK + 64 * half;
-                // are there keys that one of the warp's rows does not see?
-                const bool edge = key0 + 63 > pos_lo || (window > 0 && key0 <= max(pos_hi, 0) - window && key0 + 63 >= sinks);
-                auto hide = [&](float(&s)[32], int j0) {
-                    if (!edge) return;
-                    const int upto = pos - key0 - j0, above = lowest - key0 - j0, first = sinks - key0 - j0;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) s[j] = j <= upto && (j > above || j < first) ? s[j] : -INFINITY;
-                };
                 if (live) {
-                    tmem_ld32(tSl, s0);
-                    tmem_ld32(tSl + 32, s1);
+                    const int key0 = it.block(k) * BK;
+                    float s[4][32];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) tmem_ld32(tS + 32 * b, s[b]);
                     tmem_ld_wait();
-                    hide(s0, 0);
-                    hide(s1, 32);
-                    float t2 = -INFINITY;
+                    // keys that one of the warp's rows does not see: -inf where it is this one
+                    if (key0 + BK - 1 > pos_lo || (window > 0 && key0 <= max(pos_hi, 0) - window && key0 + BK - 1 >= sinks)) {
+                        const int upto = pos - key0, above = lowest - key0, first = sinks - key0;
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        top = max3(top, s0[j], s0[j + 1]);
-                        t2 = max3(t2, s1[j], s1[j + 1]);
+                        for (int j = 0; j < BK; ++j)
+                            s[j / 32][j % 32] = j <= upto && (j > above || j < first) ? s[j / 32][j % 32] : -INFINITY;
                     }
-                    top = fmaxf(top, t2);
-                }
-                top = fmaxf(top, other_half(top));
-                if (live) {
+                    float t[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        t[b] = s[b][0];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) t[b] = max3(t[b], s[b][j], s[b][j + 1]);
+                    }
+                    const float top = max3(fmaxf(t[0], t[1]), t[2], t[3]);
                     if (k == begin) {
                         m = top;
                     } else if (__any_sync(0xffffffffu, mine && top > m && !((top - m) * f <= kGrow))) {
@@ -369,40 +328,36 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         m = grown;
                         l *= keep;
 #pragma unroll 1
-                        for (int j = 0; j < D / 2; j += 8) {
+                        for (int j = 0; j < D; j += 8) {
                             float x[8];
-                            tmem_ld(tOl + j, x);
+                            tmem_ld(tO + j, x);
                             tmem_ld_wait();
 #pragma unroll
                             for (int i = 0; i < 8; ++i) x[i] *= keep;
-                            tmem_st8(tOl + j, x);
+                            tmem_st8(tO + j, x);
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : -m * f;
                     const float2 f2 = make_float2(f, f), ref2 = make_float2(ref, ref);
                     float2 sum = make_float2(0.f, 0.f), sum1 = sum;
-                    // Over the scores of the second 32 keys, which are in registers still; the first are read
-                    // again (held meanwhile, they spill).
-                    auto weigh = [&](const float(&s)[32], int j0) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
                         uint32_t w[16];
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
-                            float2 x = fma2(make_float2(s[j], s[j + 1]), f2, ref2);
+                            float2 x = fma2(make_float2(s[b][j], s[b][j + 1]), f2, ref2);
                             x.x = ex2(x.x);
                             x.y = ex2(x.y);
                             if (j & 2) sum1 = add2(sum1, x);
                             else sum = add2(sum, x);
                             w[j / 2] = pack2(x.x, x.y);
                         }
-                        tmem_st16(tPl + j0 / 2, w);
-                    };
-                    tmem_ld32(tSl, s0);
-                    weigh(s1, 32);
-                    tmem_st_wait();
-                    tmem_ld_wait();
-                    part_done(0);
-                    hide(s0, 0);
-                    weigh(s0, 0);
+                        tmem_st16(tS + 16 * b, w);
+                        if (b == 1) {
+                            tmem_st_wait();
+                            part_done(0);
+                        }
+                    }
                     sum = add2(sum, sum1);
                     l += sum.x + sum.y;
                     tmem_st_wait();
@@ -411,78 +366,21 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                 }
                 part_done(1);
             }
-            const bool any = end > begin;
-            const bool queries = start_queries(at_next);   // (the last scores are there: their queries have been read)
-            if (any) {
-                if (!wait(M::kODone + tile, o_phase)) return;
-                o_phase ^= 1;
-                tc_fence_after();
-                l += other_half(l);
-            }
-            if (queries) finish_queries();
-            if (!live) return;
-            if (it.slot >= 0) {
-                const int64_t at = (int64_t)it.slot * p.rows + r;
-                if (mine && half == 0) p.ml[at] = make_float2(m == -INFINITY ? 0.f : m * f, any ? l : 0.f);
-                if (any) {
-#pragma unroll 1
-                    for (int j = 0; j < D / 2; j += 16) {
-                        float x[16];
-                        tmem_ld(tOl + j, x);
-                        tmem_ld_wait();
-                        if (mine)
-#pragma unroll
-                            for (int i = 0; i < 16; i += 4)
-                                *reinterpret_cast<float4 *>(p.part + at * D + D / 2 * half + j + i) =
-                                    make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                    }
-                }
-            } else {
-                const float inv = any && l != 0.f ? 1.f / l : 0.f;   // (no visible key: zeros)
-                const int token = pos - it.pos0, head = it.h * group + (it.row0 + r) - token * group;
-                const int64_t to = ((int64_t)(it.tok0 + token) * c.Hk * group + head) * D + D / 2 * half;
-                // 32 channels at a time: four lanes exchange the 16-byte pieces of their four rows, so that they
-                // store a row's 64 bytes side by side (stored row by row, an item's outputs took 4k cycles)
-#pragma unroll 1
-                for (int j = 0; j < D / 2; j += 32) {
-                    float x[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = 0.f;
-                    if (any) {
-                        tmem_ld32(tOl + j, x);
-                        tmem_ld_wait();
-                    }
-                    uint32_t v[4][4];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        v[i / 8][i / 2 % 4] = inv != 0.f ? pack2(x[i] * inv, x[i + 1] * inv) : 0u;
-#pragma unroll
-                    for (int bit = 1; bit <= 2; bit <<= 1)
-#pragma unroll
-                        for (int a = 0; a < 4; ++a) {
-                            if (a & bit) continue;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & bit ? v[a][i] : v[a | bit][i], bit);
-                                if (lane & bit) v[a][i] = got;
-                                else v[a | bit][i] = got;
-                            }
-                        }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // row i of the four, this lane's piece
-                        const int64_t at = __shfl_sync(0xffffffffu, to, (lane & ~3) + i) + j + 8 * (lane & 3);
-                        if (r - (lane & 3) + i < it.rows)
-                            *reinterpret_cast<uint4 *>(o + at) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
-                    }
-                }
-            }
-            tc_fence_before();
+            if (end == begin) return;
+            // the row's maximum and sum, for those who store its outputs (and have taken the last item's)
+            if (!wait(M::kEndsFree + tile, ends ^ 1)) return;
+            ends ^= 1;
+            float *tops = reinterpret_cast<float *>(sm + M::kTops) + 256 * tile + 32 * quarter + lane;
+            tops[0] = m == -INFINITY ? 0.f : m * f;
+            tops[128] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[M::kEnds + tile]);
+            __syncwarp();
         });
-        if (!ok) named_bar_arrive(1 + tile, 256);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(E4M3 ? 64 : 88));
         if (warp == kMmaWarp) {
-            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
             constexpr uint32_t id_s = idesc_bf16(128, BK, false, false), id_o = idesc_bf16(128, D, false, true);
             const uint64_t dq0 = uniform(sdesc_sw128(base + M::kQ, 16, 1024)), dk0 = sdesc_sw128(base + M::kKV, 16, 1024),
                            dv0 = sdesc_sw128(base + M::kKV, BK * 128, 1024);
@@ -509,6 +407,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     if (elect_one()) {
                         scores(i, dk);
                         umma_commit(&bar[M::kSReady + i]);
+                        if ((i ? n1 : n0) == 1) umma_commit(&bar[M::kQFree + i]);
                     }
                     __syncwarp();
                 }
@@ -540,13 +439,17 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         tc_fence_after();
                         const uint64_t dv = uniform(desc_add(dv0, val.stage * M::kTile)), dk = keys_at(key.stage);
                         const uint32_t onto = uniform((uint32_t)(j > 0));
-                        // parts: keys 32 .. 63 and 96 .. 127, then the others
+                        if (j == 0) {   // the last item's outputs have been read
+                            if (!wait(M::kOFree + i, o_phase[i] ^ 1)) return;
+                            o_phase[i] ^= 1;
+                            tc_fence_after();
+                        }
                         if (elect_one()) {
 #pragma unroll
                             for (int s = 0; s < BK / 16; ++s)
-                                if (s & 2)
-                                    umma_bf16_ts(t0 + 256 + D * i, t0 + 128 * i + 64 * (s >> 2) + 32 + 8 * (s & 3),
-                                                 desc_add(dv, s * 2048), id_o, s > 2 ? 1u : onto);
+                                if (s < BK / 32)
+                                    umma_bf16_ts(t0 + 256 + D * i, t0 + 128 * i + 8 * s, desc_add(dv, s * 2048), id_o,
+                                                 s > 0 ? 1u : onto);
                         }
                         __syncwarp();
                         if (!wait(M::kPReady + 2 + i, p_phase[i] ^ 1)) return;
@@ -554,14 +457,14 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         if (elect_one()) {
 #pragma unroll
                             for (int s = 0; s < BK / 16; ++s)
-                                if (!(s & 2))
-                                    umma_bf16_ts(t0 + 256 + D * i, t0 + 128 * i + 64 * (s >> 2) + 32 + 8 * (s & 3),
-                                                 desc_add(dv, s * 2048), id_o, 1u);
+                                if (s >= BK / 32)
+                                    umma_bf16_ts(t0 + 256 + D * i, t0 + 128 * i + 8 * s, desc_add(dv, s * 2048), id_o, 1u);
                             if (j + 1 == n) {
                                 umma_commit(&bar[M::kODone + i]);
                             } else {
                                 scores(i, dk);
                                 umma_commit(&bar[M::kSReady + i]);
+                                if (j + 2 == n) umma_commit(&bar[M::kQFree + i]);
                             }
                         }
                         __syncwarp();
@@ -678,6 +581,120 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     }
                 }
             }
+        } else if (warp >= kEdgeWarp && warp < kMakeWarp) {
+            const int quarter = warp - kEdgeWarp;
+            const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+            const float *tops = reinterpret_cast<const float *>(sm + M::kTops) + 32 * quarter + lane;
+            uint32_t q_phase = 3, o_phase = 0;   // a bit a tile
+            // The queries of this warp's rows: a row's address by its lane, its 16-byte pieces side by side
+            auto load_queries = [&](const Ring &at) {
+                if (!wait(M::kItemFull + at.stage, at.phase)) return;
+                const Item &it = items[at.stage];
+                if (it.n < 0) return;
+#pragma unroll 1
+                for (int tile = 0; tile < 2; ++tile) {
+                    if (it.end(tile) == it.k0) continue;
+                    if (!wait(M::kQFree + tile, (q_phase >> tile) & 1)) return;
+                    q_phase ^= 1u << tile;
+                    const int row = 128 * tile + 32 * quarter;
+                    if (row < it.rows) {
+                        const int mine = it.row0 + min(row + lane, it.rows - 1), token = mine / group;
+                        const int64_t from = (int64_t)(it.tok0 + token) * q_stride + (int64_t)(it.h * group + mine - token * group) * D;
+                        constexpr int U = D / 8;   // pieces of a row
+#pragma unroll 4
+                        for (int i = 0; i < U; ++i) {
+                            const int r = (32 * i + lane) / U, x = lane % U;
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                             base + M::kQ + tile * M::kTile + sw128_offset(32 * quarter + r, 8 * x, 128)),
+                                         "l"(q + __shfl_sync(0xffffffffu, from, r) + 8 * x)
+                                         : "memory");
+                        }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        fence_proxy_async();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[M::kQFull + tile]);
+                    __syncwarp();
+                }
+            };
+            Ring at_next;
+            load_queries(at_next);
+            each_item([&](const Item &it) {
+                at_next.step(kRing);
+                load_queries(at_next);
+                float m[2], l[2];
+#pragma unroll
+                for (int tile = 0; tile < 2; ++tile) {
+                    m[tile] = l[tile] = 0.f;
+                    if (it.end(tile) == it.k0) continue;
+                    if (!wait(M::kEnds + tile, (o_phase >> tile) & 1)) return;
+                    m[tile] = tops[256 * tile];
+                    l[tile] = tops[256 * tile + 128];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[M::kEndsFree + tile]);
+                    __syncwarp();
+                }
+#pragma unroll 1
+                for (int tile = 0; tile < 2; ++tile) {
+                    const bool any = it.end(tile) > it.k0;
+                    if (any) {
+                        if (!wait(M::kODone + tile, (o_phase >> tile) & 1)) return;
+                        o_phase ^= 1u << tile;
+                        tc_fence_after();
+                    }
+                    const int r = 128 * tile + 32 * quarter + lane;
+                    const bool live = r - lane < it.rows, mine = r < it.rows;   // (of a whole warp; this row)
+                    const float sum = tile ? l[1] : l[0];
+                    const uint32_t tO = tmem + 256 + D * tile + lanes;
+                    if (live && it.slot >= 0) {
+                        const int64_t at = (int64_t)it.slot * p.rows + r;
+                        if (mine) p.ml[at] = make_float2(tile ? m[1] : m[0], sum);
+                        if (any) {
+#pragma unroll 1
+                            for (int j = 0; j < D; j += 16) {
+                                float x[16];
+                                tmem_ld(tO + j, x);
+                                tmem_ld_wait();
+                                if (mine)
+#pragma unroll
+                                    for (int i = 0; i < 16; i += 4)
+                                        *reinterpret_cast<float4 *>(p.part + at * D + j + i) =
+                                            make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                            }
+                        }
+                    } else if (live) {
+                        const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (no visible key: zeros)
+                        const int token = (it.row0 + min(r, it.rows - 1)) / group, head = it.h * group + (it.row0 + r) - token * group;
+                        __nv_bfloat16 *to = o + ((int64_t)(it.tok0 + token) * c.Hk * group + head) * D;
+                        const bool wide = ((uintptr_t)to & 31) == 0;
+#pragma unroll 1
+                        for (int j = 0; j < D; j += 32) {
+                            float x[32];
+                            if (any) {
+                                tmem_ld32(tO + j, x);
+                                tmem_ld_wait();
+                            }
+                            uint32_t v[16];
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) v[i / 2] = any && inv != 0.f ? pack2(x[i] * inv, x[i + 1] * inv) : 0u;
+                            if (mine && wide) {
+                                store32(to + j, v);
+                                store32(to + j + 16, v + 8);
+                            } else if (mine) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4)
+                                    *reinterpret_cast<uint4 *>(to + j + 2 * i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                            }
+                        }
+                    }
+                    if (any) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[M::kOFree + tile]);
+                        __syncwarp();
+                    }
+                }
+            });
         } else if (E4M3 && warp >= kMakeWarp) {
             // this thread's row of a block: its page, then (a block later) its scales, ahead of their use
             const int row = tid - 32 * kMakeWarp;

@@ -413,6 +413,33 @@ def test_outputs_stay_inside_their_bands():
         assert all(torch.equal(x, bits(t)) for x, t in zip(before, (q, b.k_pages, b.v_pages, b.table)))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_addresses_of_16_bytes(dtype, D):
+    """Inputs and outputs that are aligned to 16 bytes and no more."""
+    b = Batch([150, 9], [30, 1000], 2, D, dtype, dtype, 16, device=DEV)
+    n = 16 // torch.empty(0, dtype=dtype).element_size()
+
+    def off(t):
+        x = torch.empty(t.numel() + n, dtype=t.dtype, device=DEV)[n:].view(t.shape)
+        x.copy_(t)
+        assert x.data_ptr() % 32 == 16
+        return x
+    b.k_pages, b.v_pages = off(b.k_pages), off(b.v_pages)
+    q = off(b.queries(6))
+    o = off(torch.zeros_like(q))
+    kda.paged_attn_fwd(q, *b.cache, b.cu, o=o, check=True)
+    U.check_attention(o, b, q)
+    k, v = off(q[:, :2].contiguous()), off(q[:, 2:4].contiguous())
+    kda.kv_cache_write(k, v, *b.cache, b.cu, check=True)
+    rk, rv = off(torch.zeros_like(k)), off(torch.zeros_like(v))
+    kda.kv_cache_read(*b.cache, b.cu, total_tokens=b.T, k=rk, v=rv, check=True)
+    assert torch.equal(rk, k) and torch.equal(rv, v)
+    b.cu, b.T = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV), 2
+    kda.paged_attn_decode_step(q[:2], *b.cache, o=o[:2], check=True)
+    U.check_attention(o[:2], b, q[:2])
+
+
 @pytest.mark.parametrize("dtype,cache", [(BF, BF), (BF, E4M3), (F32, F32)])
 def test_in_a_graph_on_another_stream(dtype, cache):
     """Write, chunk and decode captured once, replayed with new tokens and lengths."""
