@@ -126,8 +126,8 @@ paged_plan_kernel(Cache c, Plan p, int group, int window, int sinks, StatusWord 
     }
     if (tid == 0) cost[tiles] = total;
     __syncthreads();
-    // ranges of at least as much as an item that is not cut
-    const int64_t share = max((total + p.ranges - 1) / p.ranges, (int64_t)kUncut);
+    // ranges of at least an item of one block
+    const int64_t share = max((total + p.ranges - 1) / p.ranges, (int64_t)kItemCost + 1);
     for (int i = tid; i <= p.ranges; i += kPlanThreads) {
         const int64_t x = min((int64_t)i * share, total);
         Cut cut{(int)tiles, c.N, 0, 0, 0};
@@ -586,7 +586,8 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
             const float *tops = reinterpret_cast<const float *>(sm + M::kTops) + 32 * quarter + lane;
             uint32_t q_phase = 3, o_phase = 0;   // a bit a tile
-            // The queries of this warp's rows: a row's address by its lane, its 16-byte pieces side by side
+            // The queries of this warp's rows: a row's address by its lane, its 16-byte pieces side by side;
+            // both tiles' on their way before the first is waited for
             auto load_queries = [&](const Ring &at) {
                 if (!wait(M::kItemFull + at.stage, at.phase)) return;
                 const Item &it = items[at.stage];
@@ -609,9 +610,16 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                                          "l"(q + __shfl_sync(0xffffffffu, from, r) + 8 * x)
                                          : "memory");
                         }
-                        asm volatile("cp.async.wait_all;" ::: "memory");
-                        fence_proxy_async();
                     }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                }
+                const bool two = it.end(1) > it.k0;
+#pragma unroll 1
+                for (int tile = 0; tile < 2; ++tile) {
+                    if (it.end(tile) == it.k0) continue;
+                    if (tile == 0 && two) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar[M::kQFull + tile]);
                     __syncwarp();
@@ -655,11 +663,13 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                                 float x[16];
                                 tmem_ld(tO + j, x);
                                 tmem_ld_wait();
-                                if (mine)
+                                uint32_t v[16];
 #pragma unroll
-                                    for (int i = 0; i < 16; i += 4)
-                                        *reinterpret_cast<float4 *>(p.part + at * D + j + i) =
-                                            make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(x[i]);
+                                if (mine) {
+                                    store32(p.part + at * D + j, v);
+                                    store32(p.part + at * D + j + 8, v + 8);
+                                }
                             }
                         }
                     } else if (live) {
@@ -795,8 +805,9 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
 
 // What the cuts inside one item have left, put together: a CTA for 32 rows of the item that the cut is
 // the first inside of.
+constexpr int kJoinThreads = 512;
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(Cache c, Plan p, __nv_bfloat16 *__restrict__ o, int group, StatusWord *st) {
     constexpr int V = D / 32;
     const int cut = blockIdx.x + 1, lane = threadIdx.x & 31;
@@ -823,25 +834,38 @@ paged_join_kernel(Cache c, Plan p, __nv_bfloat16 *__restrict__ o, int group, Sta
     const Tile t = tile_of(span_of(c, here.n), here.t, group, p.each);
     int last = cut;   // the last cut inside the item
     while (last < p.ranges && p.cuts[last + 1].k > 0 && same_item(p.cuts[last + 1], here)) ++last;
-    for (int r = blockIdx.y * 32 + (threadIdx.x >> 5); r < min(t.rows, (int)blockIdx.y * 32 + 32); r += 8) {
-        const int64_t first = (int64_t)(2 * (cut - 1) + 1) * p.rows + r;
-        float2 a = p.ml[first];
-        float top = a.y != 0.f ? a.x : -INFINITY;
-        for (int i = cut; i <= last; ++i) {
-            const float2 b = p.ml[(int64_t)(2 * i) * p.rows + r];
-            if (b.y != 0.f) top = fmaxf(top, b.x);
+    // A row a warp, a piece a lane: what the pieces count for at once, then their sums, four on their way.
+    // (One after the other, 19 pieces took 30 us.)
+    const int pieces = last - cut + 2;
+    for (int r = blockIdx.y * 32 + (threadIdx.x >> 5); r < min(t.rows, (int)blockIdx.y * 32 + 32); r += kJoinThreads / 32) {
+        auto place = [&](int i) { return (int64_t)(i == 0 ? 2 * cut - 1 : 2 * (cut - 1 + i)) * p.rows + r; };
+        float top = -INFINITY;
+        for (int i0 = 0; i0 < pieces; i0 += 32) {
+            float2 b = make_float2(0.f, 0.f);
+            if (i0 + lane < pieces) b = p.ml[place(i0 + lane)];
+            float x = b.y != 0.f ? b.x : -INFINITY;
+#pragma unroll
+            for (int i = 16; i > 0; i >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
+            top = fmaxf(top, x);
         }
         float l = 0.f, x[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) x[j] = 0.f;
-        for (int i = cut - 1; i <= last; ++i) {
-            const int64_t at = i < cut ? first : (int64_t)(2 * i) * p.rows + r;
-            const float2 b = p.ml[at];
-            if (b.y == 0.f) continue;   // (its sums may be anything)
-            const float e = ex2(b.x - top);
-            l += e * b.y;
+        for (int i0 = 0; i0 < pieces; i0 += 32) {
+            float2 b = make_float2(0.f, 0.f);
+            if (i0 + lane < pieces) b = p.ml[place(i0 + lane)];
+            const float mine = b.y != 0.f ? ex2(b.x - top) : 0.f;   // (0: its sums may be anything)
+            l += warp_sum(mine * b.y);
+#pragma unroll 4
+            for (int i = 0; i < min(32, pieces - i0); ++i) {
+                const float e = __shfl_sync(0xffffffffu, mine, i);
+                const float *from = p.part + place(i0 + i) * D + lane * V;
 #pragma unroll
-            for (int j = 0; j < V; ++j) x[j] += e * p.part[at * D + lane * V + j];
+                for (int j = 0; j < V; ++j) {
+                    const float y = from[j];
+                    x[j] += e != 0.f ? e * y : 0.f;
+                }
+            }
         }
         const float inv = l != 0.f ? 1.f / l : 0.f;
         const int at = t.row0 + r, token = at / group;
@@ -854,8 +878,8 @@ paged_join_kernel(Cache c, Plan p, __nv_bfloat16 *__restrict__ o, int group, Sta
 
 cudaError_t launch_join(int D, const Cache &c, const Plan &p, void *o, int group, StatusWord *st, cudaStream_t s) {
     const dim3 grid(p.ranges > 1 ? p.ranges - 1 : 1, (p.rows + 31) / 32);
-    return D == 128 ? launch_after(paged_join_kernel<128>, grid, dim3(256), 0, s, c, p, (__nv_bfloat16 *)o, group, st)
-                    : launch_after(paged_join_kernel<64>, grid, dim3(256), 0, s, c, p, (__nv_bfloat16 *)o, group, st);
+    return D == 128 ? launch_after(paged_join_kernel<128>, grid, dim3(kJoinThreads), 0, s, c, p, (__nv_bfloat16 *)o, group, st)
+                    : launch_after(paged_join_kernel<64>, grid, dim3(kJoinThreads), 0, s, c, p, (__nv_bfloat16 *)o, group, st);
 }
 
 struct Layout {
