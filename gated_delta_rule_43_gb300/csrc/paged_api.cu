@@ -2,6 +2,7 @@
 // argument checks, workspace layout, dispatch.
 #include <stdint.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "kda_paged.cuh"
@@ -15,10 +16,10 @@ cudaError_t launch_paged_simt(int dtype, int cache_dtype, int D, const paged::Ca
                               StatusWord *st, cudaStream_t s);
 size_t paged_tc_bytes(const paged::Cache &c, int group, int D, int sms);
 cudaError_t launch_paged_tc(bool e4m3, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
-                            float scale, int window, int sinks, void *ws, int sms, cudaStream_t s);
+                            float scale, int window, int sinks, void *ws, int sms, int left_out, cudaStream_t s);
 size_t paged_decode_bytes(int group, int D, int sms);
 cudaError_t launch_paged_decode(bool e4m3, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
-                                float scale, int window, int sinks, void *ws, int sms, cudaStream_t s);
+                                float scale, int window, int sinks, void *ws, int sms, int left_out, cudaStream_t s);
 }  // namespace kda
 
 using namespace kda;
@@ -95,6 +96,9 @@ bool attn_sizes_ok(const kda_paged_cache *p, int64_t T, int32_t H) {
     return sizes_ok(p, T) && H > 0 && H <= 65536 && H % p->Hk == 0 && T * (H / p->Hk) < ((int64_t)1 << 31);
 }
 
+// Test hook (kda_test_paged_fault): what the next call leaves out.
+std::atomic<int> g_left_out{-1};
+
 // bf16 heads of 64 and 128 go to the tensor cores (a pool without pages has nothing to load from).
 bool on_tensor_cores(const kda_paged_cache *p, int32_t dtype) {
     return dtype == KDA_BF16 && p->D >= 64 && p->num_pages > 0;
@@ -122,7 +126,7 @@ kda_status attn(const kda_paged_cache *p, const void *q, int64_t qs, void *o, in
     StatusWord *st = (StatusWord *)workspace;
     if (T > 0 && p->num_seqs > 0 && on_tensor_cores(p, dtype))
         return cuda_status((p->cu_seqlens ? launch_paged_tc : launch_paged_decode)(
-            p->dtype == KDA_E4M3, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window, sinks, workspace, sm_count(), s));
+            p->dtype == KDA_E4M3, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window, sinks, workspace, sm_count(), g_left_out.exchange(-1), s));
     const kda_status e = clear(st, s);
     if (e != KDA_OK || T == 0 || p->num_seqs == 0) return e;
     return cuda_status(launch_paged_simt(dtype, p->dtype, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window, sinks,
@@ -182,6 +186,12 @@ kda_status kda_paged_attn_decode_step(const kda_paged_cache *cache, const void *
                                       size_t workspace_bytes, void *stream) {
     if (!cache || cache->cu_seqlens) return KDA_ERR_INVALID_ARG;
     return attn(cache, q, q_stride, o, cache->num_seqs, H, dtype, scale, window, sinks, workspace, workspace_bytes, stream);
+}
+
+kda_status kda_test_paged_fault(int32_t part) {
+    if (part < -1) return KDA_ERR_INVALID_ARG;
+    g_left_out = part;
+    return KDA_OK;
 }
 
 }  // extern "C"

@@ -194,7 +194,7 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads<E4M3>, 1)
 paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const __nv_bfloat16 *__restrict__ q, int64_t q_stride, __nv_bfloat16 *__restrict__ o, int group,
-                  float scale, int window, int sinks, StatusWord *st) {
+                  float scale, int window, int sinks, int left_out, StatusWord *st) {
     extern __shared__ __align__(1024) uint8_t sm[];
     using M = Map<D, E4M3>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -504,9 +504,10 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         // (e4m3 pages go through a ring of their own)
                         const uint32_t full = E4M3 ? M::kRawFull : M::kFull, free = E4M3 ? M::kRawFree : M::kFree;
                         if (!wait(free + kv.stage, kv.phase ^ 1)) return;
-                        if (lane == 0) mbar_arrive_expect_tx(&bar[full + kv.stage], E4M3 ? M::kRawTile : M::kTile);
+                        const bool left = loads == 0 && left_out == (int)blockIdx.x;
+                        if (lane == 0 && !left) mbar_arrive_expect_tx(&bar[full + kv.stage], E4M3 ? M::kRawTile : M::kTile);
                         __syncwarp();
-                        if (lane < boxes) {
+                        if (lane < boxes && !left) {
                             const int row = key & ((1 << c.shift) - 1), run = page == c.P ? none : page * runs + it.h;
                             const uint32_t to = base + (E4M3 ? M::kRaw + kv.stage * M::kRawTile : M::kKV + kv.stage * M::kTile) +
                                                 lane * rows * (E4M3 ? D : 128);
@@ -920,7 +921,7 @@ template <int D, bool E4M3> static cudaError_t allow_smem() {
 
 template <int D, bool E4M3>
 static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, int group, float scale, int window,
-                          int sinks, uint8_t *ws, int sms, cudaStream_t s) {
+                          int sinks, uint8_t *ws, int sms, int left_out, cudaStream_t s) {
     const Layout L = layout_of(c, group, D, sms);
     const Plan p{(int32_t *)(ws + L.tiles), (int64_t *)(ws + L.cost), (Cut *)(ws + L.cuts), (float *)(ws + L.part),
                  (float2 *)(ws + L.ml), L.ranges, L.rows, kRows, nullptr, L.most};
@@ -934,7 +935,7 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
     e = cudaGetLastError();
     if (e == cudaSuccess)
         e = launch_after(paged_attn_kernel<D, E4M3>, dim3(L.ranges), dim3(kThreads<E4M3>), Map<D, E4M3>::kBytes, s, c, p, tk, tv,
-                         (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks, st);
+                         (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks, left_out, st);
     return e == cudaSuccess ? launch_join(D, c, p, o, group, st, s) : e;
 }
 
@@ -946,14 +947,14 @@ size_t paged_tc_bytes(const paged::Cache &c, int group, int D, int sms) {
 }
 
 cudaError_t launch_paged_tc(bool e4m3, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
-                            float scale, int window, int sinks, void *ws, int sms, cudaStream_t s) {
+                            float scale, int window, int sinks, void *ws, int sms, int left_out, cudaStream_t s) {
     using paged::tc::launch;
     uint8_t *w = (uint8_t *)ws;
     if (e4m3)
-        return D == 128 ? launch<128, true>(c, q, qs, o, group, scale, window, sinks, w, sms, s)
-                        : launch<64, true>(c, q, qs, o, group, scale, window, sinks, w, sms, s);
-    return D == 128 ? launch<128, false>(c, q, qs, o, group, scale, window, sinks, w, sms, s)
-                    : launch<64, false>(c, q, qs, o, group, scale, window, sinks, w, sms, s);
+        return D == 128 ? launch<128, true>(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s)
+                        : launch<64, true>(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s);
+    return D == 128 ? launch<128, false>(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s)
+                    : launch<64, false>(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s);
 }
 
 }  // namespace kda

@@ -147,7 +147,7 @@ template <int D, int NR, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const __nv_bfloat16 *__restrict__ q, int64_t q_stride, __nv_bfloat16 *__restrict__ o, int group,
-                    float scale, int window, int sinks) {
+                    float scale, int window, int sinks, int left_out) {
     extern __shared__ __align__(1024) uint8_t sm[];
     using M = Map<D, NR, E4M3>;
     constexpr int N = M::N, C = M::kCols;
@@ -167,6 +167,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
     const int groups = (group + NR - 1) / NR;
     if (tid == 0) {
         *st = StatusWord{0, 0, 0};
+        tslot[1] = 0;
         for (int i = 0; i < M::kStages; ++i) {
             mbar_init(&bar[M::kFull + i], 1);
             mbar_init(&bar[M::kFree + i], 1);
@@ -238,6 +239,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
     const uint32_t tmem = *tslot;
     if (tid < 2 && (tid == 0 || blockIdx.x + 1 == p.ranges)) p.cuts[blockIdx.x + tid] = cuts[tid];
     const uint32_t tO = tmem + 2 * kTiles * N;   // behind two pieces' scores
+    volatile int *failed = reinterpret_cast<volatile int *>(tslot + 1);
     bool ok = true;
     auto wait = [&](int which, uint32_t parity) {
         ok = ok && wait_warp(bars + 8 * which, parity);
@@ -265,6 +267,12 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const float f = scale * kLog2e;
         uint32_t turn = 0, ends = 0;   // of the maxima's places; of those where the two sides meet
+        // Named barriers, which have no limit of their own: nobody waits there for a warp that has given up.
+        auto meet = [&](uint32_t id, uint32_t n) {
+            if (__any_sync(0xffffffffu, *failed != 0)) ok = false;
+            else named_bar_sync(id, n);
+            return ok;
+        };
         each_item([&](const Item &it) {
             float run_m[NR], run_l[NR], run_o[NR];
 #pragma unroll
@@ -365,7 +373,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                         if (E4M3) *reinterpret_cast<float4 *>(place + 32 * quarter + 16 + g0) = make_float4(b[0], b[1], b[2], b[3]);
                     }
                 }
-                named_bar_sync(1 + side, 128);
+                if (!meet(1 + side, 128)) return;
                 float l[NR];
 #pragma unroll
                 for (int g0 = 0; g0 < NR; g0 += 4) {
@@ -493,7 +501,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                     for (int g = g0; g < g0 + 4; ++g) other[128 * g + key_at] = run_o[g];
                 }
             }
-            named_bar_sync(3, 256);
+            if (!meet(3, 256)) return;
             if (side == 1) return;
             const int d = D == 128 ? tid : 16 * warp + lane;   // (64 rows of a product stand in 16 lanes of each warp)
             const bool there = D == 128 || lane < 16;
@@ -515,7 +523,10 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                 }
             }
         });
-        if (!ok) {
+        if (!ok) {   // (whoever stands at a barrier goes on; whoever comes to one later sees why not to)
+            if (lane == 0) *failed = 1;
+            __threadfence_block();
+            __syncwarp();
             named_bar_arrive(1 + side, 128);
             named_bar_arrive(3, 256);
         }
@@ -614,9 +625,10 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
 #pragma unroll 1
             for (int t = 0; t < many; ++t) {
                 if (!wait(M::kFree + kv.stage, kv.phase ^ 1)) return;
-                if (lane == 0) mbar_arrive_expect_tx(&bar[M::kFull + kv.stage], M::kTile);
+                const bool left = loads == 0 && left_out == (int)blockIdx.x;
+                if (lane == 0 && !left) mbar_arrive_expect_tx(&bar[M::kFull + kv.stage], M::kTile);
                 __syncwarp();
-                if (t == my_tile && box < boxes) {
+                if (t == my_tile && box < boxes && !left) {
                     const uint32_t to = base + M::kKV + kv.stage * M::kTile + box * rows * (E4M3 ? D : 128);
 #pragma unroll
                     for (int x = 0; x < (E4M3 ? 1 : D / 64); ++x)
@@ -812,6 +824,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
     if (__syncthreads_or(!ok)) {
         // an expired wait: what is in flight ends (each wait bounded again) before the tensor memory is
         // released and the CTA leaves
+        asm volatile("cp.async.wait_all;" ::: "memory");
         tc_fence_before();
         if (warp == kMmaWarp) {
             tc_fence_after();
@@ -866,7 +879,7 @@ template <int D, int NR, bool E4M3> static cudaError_t allow_smem() {
 
 template <int D, int NR, bool E4M3>
 static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, int group, float scale, int window,
-                          int sinks, uint8_t *ws, int sms, cudaStream_t s) {
+                          int sinks, uint8_t *ws, int sms, int left_out, cudaStream_t s) {
     const Layout L = layout_of(group, D, sms);
     const Plan p{nullptr, nullptr, (Cut *)(ws + L.cuts), (float *)(ws + L.part), (float2 *)(ws + L.ml), L.ranges, L.rows,
                  L.each, (StatusWord *)(ws + L.found), 0};
@@ -876,7 +889,7 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
     if (e == cudaSuccess) e = allow_smem<D, NR, E4M3>();
     if (e != cudaSuccess) return e;
     paged_decode_kernel<D, NR, E4M3><<<L.ranges, kThreads, Map<D, NR, E4M3>::kBytes, s>>>(
-        c, p, tk, tv, (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks);
+        c, p, tk, tv, (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks, left_out);
     e = cudaGetLastError();
     return e == cudaSuccess ? launch_join(D, c, p, o, group, (StatusWord *)ws, s) : e;
 }
@@ -888,12 +901,12 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
 size_t paged_decode_bytes(int group, int D, int sms) { return paged::tc::one::layout_of(group, D, sms).total; }
 
 cudaError_t launch_paged_decode(bool e4m3, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
-                                float scale, int window, int sinks, void *ws, int sms, cudaStream_t s) {
+                                float scale, int window, int sinks, void *ws, int sms, int left_out, cudaStream_t s) {
     using paged::tc::one::launch;
     uint8_t *w = (uint8_t *)ws;
 #define KDA_ONE(D_, NR_, E_) \
     if (D == D_ && group <= (NR_ == 16 ? 0x7fffffff : NR_) && e4m3 == E_) \
-        return launch<D_, NR_, E_>(c, q, qs, o, group, scale, window, sinks, w, sms, s);
+        return launch<D_, NR_, E_>(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s);
 #define KDA_ONES(D_, E_) KDA_ONE(D_, 4, E_) KDA_ONE(D_, 8, E_) KDA_ONE(D_, 16, E_)
     KDA_ONES(64, false) KDA_ONES(128, false) KDA_ONES(64, true) KDA_ONES(128, true)
 #undef KDA_ONES

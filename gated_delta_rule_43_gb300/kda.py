@@ -70,6 +70,7 @@ SIGNATURES = {
     "kda_paged_attn_workspace_size": (SZ, [P, I64, I32, I32]),
     "kda_paged_attn_fwd": (I32, [P, P, I64, P, I64, I32, I32, F32, I32, I32, P, SZ, P]),
     "kda_paged_attn_decode_step": (I32, [P, P, I64, P, I32, I32, F32, I32, I32, P, SZ, P]),
+    "kda_test_paged_fault": (I32, [I32]),
 }
 
 

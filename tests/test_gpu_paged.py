@@ -515,3 +515,26 @@ def test_calls_on_two_streams_at_once():
     U.check_attention(got[1], c, qc)
     for i in range(2, 20):
         assert torch.equal(got[i], got[i % 2])
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("cache", [BF, E4M3])
+def test_an_expired_wait_is_reported(cache, decode):
+    """A part that leaves out a load waits for 2.2 s and gives up; the next call on the same workspace
+    is as ever."""
+    b = Batch([1, 1] if decode else [200, 9], [3000, 900], 2, 128, BF, cache, 16, device=DEV)
+    q = b.queries(8)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
+
+    def call():
+        if decode:
+            return kda.paged_attn_decode_step(q, *b.cache, **b.scales, workspace=ws)
+        return kda.paged_attn_fwd(q, *b.cache, b.cu, **b.scales, workspace=ws)
+    good = call()
+    assert kda.query_status(ws)[0] == kda.KDA_OK
+    assert kda.load().kda_test_paged_fault(2) == kda.KDA_OK
+    call()
+    assert kda.query_status(ws) == (kda.KDA_ERR_TIMEOUT, 2)
+    again = call()
+    assert kda.query_status(ws)[0] == kda.KDA_OK and torch.equal(again, good)
+    U.check_attention(again, b, q)

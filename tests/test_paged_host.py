@@ -98,6 +98,11 @@ def test_write_and_read(lib):
         assert read(**kw) == INVALID, kw
 
 
+def test_fault_hook(lib):
+    assert lib.kda_test_paged_fault(-2) == INVALID
+    assert lib.kda_test_paged_fault(3) == lib.kda_test_paged_fault(-1) == OK
+
+
 def test_binding_refuses_what_does_not_fit(lib):
     b = U.Batch([5, 3], [2, 0], 2, 32, U.F32, U.F32)
     e = U.Batch([5, 3], [2, 0], 2, 32, U.F32, U.E4M3)
