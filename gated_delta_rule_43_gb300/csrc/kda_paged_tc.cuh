@@ -169,17 +169,27 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const void *tmap, in
         ::"r"(dst), "l"(tmap), "r"(c), "r"(row), "r"(run), "r"(bar)
         : "memory");
 }
-// Zeroes the rows from `left` on of a tile of 128 rows of BYTES bytes (in columns of at most 128 bytes, one
+// Zeroes rows [begin, end) of a tile of 128 rows of BYTES bytes (in columns of at most 128 bytes, one
 // behind the other); a whole warp, before the tile's products.
-template <int BYTES> __device__ __forceinline__ void clear_rows(uint8_t *tile, int left) {
+template <int BYTES> __device__ __forceinline__ void clear_rows(uint8_t *tile, int begin, int end) {
     constexpr int W = BYTES < 128 ? BYTES : 128, U = W / 16;   // a column's width; its 16-byte pieces
-    for (int x = left * U + (threadIdx.x & 31); x < BK * U; x += 32) {
+    for (int x = begin * U + (threadIdx.x & 31); x < end * U; x += 32) {
 #pragma unroll
         for (int i = 0; i < BYTES / W; ++i)
             *reinterpret_cast<uint4 *>(tile + i * BK * W + x * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async();
     __syncwarp();
+}
+
+// Rows [begin, end) of the tile of keys from key0 on that are neither in a window, the highest position below
+// which is `lowest`, nor among the first tokens: their weights are zeros, but 0 times a value that is not finite
+// is not.  (Whole pages of them are not loaded, but read as zeros.)
+struct Unseen {
+    int begin, end;
+};
+__device__ __forceinline__ Unseen unseen(int key0, int lowest, int sinks) {
+    return Unseen{max(0, sinks - key0), min(BK, lowest + 1 - key0)};
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

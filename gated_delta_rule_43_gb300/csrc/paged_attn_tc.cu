@@ -19,8 +19,9 @@
 // One CTA an SM:
 //   warps 0-3, 4-7   the rows of the two tiles, a thread each: scores out of tensor memory, P into it, over
 //                    the scores
-//   warp 8           issues the products (and zeroes values behind a sequence's end: slots that nobody has
-//                    written)                   warp 9    loads keys and values, page by page
+//   warp 8           issues the products (and zeroes values that may be anything: in slots behind a sequence's
+//                    end and before the windows)
+//   warp 9           loads keys and values, page by page
 //   warp 10          goes through the range's items for everyone
 //   warps 12-15      an item's edges: its queries, into the place of the last one's after the last scores, and
 //                    its outputs, while the next item's first weights are formed (done by the rows' own warps,
@@ -395,6 +396,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             each_item([&](const Item &it) {
                 const int n0 = it.end(0) - it.k0, n1 = it.end(1) - it.k0, blocks = it.k1 - it.k0, ctx = it.ctx;
                 if (blocks == 0) return;
+                const int lowest = window > 0 ? max(max(0, it.first) - window, -1) : -1;   // keys above it are in someone's window
                 Ring key = kv;
                 if (!wait(M::kFull + key.stage, key.phase)) return;
 #pragma unroll
@@ -420,7 +422,11 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     key.step(M::kStages);
                     const bool more = j + 1 < blocks;
                     const uint32_t val_bar = bars + 8 * (M::kFull + val.stage), key_bar = bars + 8 * (M::kFull + key.stage);
-                    const bool clear = !E4M3 && ctx - it.block(it.k0 + j) * BK < BK && (ctx & ((1 << c.shift) - 1)) != 0;
+                    // (bf16) values that may be anything: behind the sequence's end, which is in the list's last block,
+                    // and before the windows
+                    const int key0 = it.block(it.k0 + j) * BK;
+                    const bool tail = ctx - key0 < BK && (ctx & ((1 << c.shift) - 1)) != 0;
+                    const Unseen gap = unseen(key0, lowest, sinks);
                     bool there = false;   // the block's values, the next block's keys
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -432,9 +438,10 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                                                more ? key.phase : val.phase);
                         if (!ok) return;
                         p_phase[i] ^= 1;
-                        // (values behind the sequence's end: only in the list's last block)
-                        if (!there && clear)
-                            clear_rows<2 * D>(sm + M::kKV + val.stage * M::kTile, ctx - it.block(it.k0 + j) * BK);
+                        if (!E4M3 && !there) {
+                            if (tail) clear_rows<2 * D>(sm + M::kKV + val.stage * M::kTile, ctx - key0, BK);
+                            if (gap.begin < gap.end) clear_rows<2 * D>(sm + M::kKV + val.stage * M::kTile, gap.begin, gap.end);
+                        }
                         there = true;
                         tc_fence_after();
                         const uint64_t dv = uniform(desc_add(dv0, val.stage * M::kTile)), dk = keys_at(key.stage);

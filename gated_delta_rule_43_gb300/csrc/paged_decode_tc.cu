@@ -25,7 +25,8 @@
 //
 //   warps 0-3, 4-7   every other piece's scores -> weights, and its outputs; what the two have of an item
 //                    meets at its end
-//   warp 8   products (and zeroes values behind a sequence's end: slots that nobody has written)
+//   warp 8   products (and zeroes values that may be anything: in slots behind a sequence's end and before
+//            the window)
 //   warp 9   loads of keys and values   warp 10  goes through the items, and loads their queries
 //   warp 11  scales of e4m3 pages
 #include "kda_paged_tc.cuh"
@@ -538,15 +539,22 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
         const uint64_t dk0 = narrow ? sdesc_sw64(base + M::kKV, 16, 512) : sdesc_sw128(base + M::kKV, 16, 1024);
         const uint64_t dv0 = narrow ? sdesc_sw64(base + M::kKV, 16, 512) : sdesc_sw128(base + M::kKV, BK * 128, 1024);
         const uint64_t dq0 = sdesc_sw128(base + M::kQ, 16, 1024), dp0 = sdesc_sw128(base + M::kP, 16, 1024);
-        // the piece whose values are still to come: its tiles, and what the last lacks (0: nothing)
-        int owed = 0, owed_left = 0;
+        // the piece whose values are still to come: its tiles, and what the last lacks (0: nothing); (with a
+        // window) its first tile's place in the list, and the list
+        int owed = 0, owed_left = 0, owed_first = 0, owed_sinks = 0, owed_from = 0, owed_lowest = -1;
         Ring os;   // its place
         auto values = [&] {
             if (owed == 0) return;
             if (!wait(M::kPReady + os.stage, os.phase)) return;
             for (int t = 0; t < owed; ++t) {
                 if (!wait(M::kFull + kv.stage, kv.phase)) return;
-                if (owed_left && t + 1 == owed) clear_rows<D * (E4M3 ? 1 : 2)>(sm + M::kKV + kv.stage * M::kTile, owed_left);
+                if (owed_left && t + 1 == owed) clear_rows<D * (E4M3 ? 1 : 2)>(sm + M::kKV + kv.stage * M::kTile, owed_left, BK);
+                if (owed_lowest >= 0) {
+                    const int k = owed_first + t;
+                    const Unseen gap = unseen((k < owed_sinks ? k : owed_from + k - owed_sinks) * BK, owed_lowest, sinks);
+                    if (gap.begin < gap.end)
+                        clear_rows<D * (E4M3 ? 1 : 2)>(sm + M::kKV + kv.stage * M::kTile, gap.begin, gap.end);
+                }
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t dv = desc_add(dv0, kv.stage * M::kTile), dp = desc_add(dp0, (os.stage * kTiles + t) * M::kPTile);
@@ -607,6 +615,10 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                 values();
                 if (!ok) return;
                 owed = many;
+                owed_first = first;
+                owed_sinks = it.sinks;
+                owed_from = it.from;
+                owed_lowest = window > 0 ? it.pos - window : -1;   // (keys above it are in the window)
                 const int left = it.ctx - it.tile(first + many - 1) * BK;   // (below BK only in an item's last tile)
                 owed_left = left < BK && (it.ctx & ((1 << c.shift) - 1)) != 0 ? left : 0;
             }

@@ -545,7 +545,8 @@ size_t kda_paged_attn_workspace_size(const kda_paged_cache *cache, int64_t total
  * Pages that no token of the call sees are not read.  With bf16 storage the weights are rounded to
  * bf16 before they meet the values; sums, maxima and products are fp32.  A key or value that is
  * visible to one token and not finite may spread to other tokens of the call that stand close to it and do not
- * see it (their weight for it is 0, and 0 * inf is NaN); values in slots past kv_lens never do.
+ * see it (their weight for it is 0, and 0 * inf is NaN); what stands in slots past kv_lens, or is seen by no
+ * token of the call, never does.
  */
 kda_status kda_paged_attn_fwd(const kda_paged_cache *cache, const void *q, int64_t q_stride, void *o,
                               int64_t total_tokens, int32_t H, int32_t dtype, float scale,

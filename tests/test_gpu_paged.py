@@ -538,3 +538,32 @@ def test_an_expired_wait_is_reported(cache, decode):
     again = call()
     assert kda.query_status(ws)[0] == kda.KDA_OK and torch.equal(again, good)
     U.check_attention(again, b, q)
+
+
+def spoil(b, seen):
+    """Keys, values and scales of the positions that no token sees become NaN; seen(n, ctx) -> bool [ctx]."""
+    for n, c in enumerate(b.kv_lens.tolist()):
+        j = torch.arange(c)[~seen(n, c)].to(DEV)
+        page, slot = b.table[n, j // b.ps].long(), j % b.ps
+        for pages, scales in ((b.k_pages, b.k_scales), (b.v_pages, b.v_scales)):
+            raw = torch.full((len(j), b.Hk, b.D), math.nan, device=DEV).to(pages.dtype)
+            pages.view(torch.uint8)[page, :, slot] = raw.view(torch.uint8)
+            if scales is not None:
+                scales[page, :, slot] = math.nan
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 2), (100, 4), (250, 200), (128, 130)])
+@pytest.mark.parametrize("ps", [16, 256])
+def test_what_the_windows_have_passed_may_be_anything(dtype, cache, window, sinks, ps):
+    for D, group in ((64, 4), (128, 2)):
+        b = Batch([1, 3, 0, 60], [600, 1300, 4, 777], 2, D, dtype, cache, ps, seed=window, device=DEV)
+        q = b.queries(2 * group)
+        spoil(b, lambda n, c: (torch.arange(c) < sinks) | (torch.arange(c) > c - b.lens[n] - window))
+        o = kda.paged_attn_fwd(q, *b.cache, b.cu, window=window, sinks=sinks, **b.scales, check=True)
+        U.check_attention(o, b, q, window=window, sinks=sinks)
+        b = Batch([1] * 4, [600, 1300, 0, 255], 2, D, dtype, cache, ps, seed=window, device=DEV)
+        q = b.queries(2 * group)
+        spoil(b, lambda n, c: (torch.arange(c) < sinks) | (torch.arange(c) >= c - window))
+        o = kda.paged_attn_decode_step(q, *b.cache, window=window, sinks=sinks, **b.scales, check=True)
+        U.check_attention(o, b, q, window=window, sinks=sinks)
