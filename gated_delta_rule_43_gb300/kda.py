@@ -907,8 +907,10 @@ def _paged_attn(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, scale, wi
     decode = cu_seqlens is None
     if decode and T != cache.num_seqs:
         raise ValueError(f"q has {T} rows for {cache.num_seqs} sequences")
-    if H % Hk:
+    if Hk < 1 or H % Hk:
         raise ValueError(f"{H} query heads cannot share {Hk} key/value heads")
+    if max(abs(window), abs(sinks)) > 0x7fffffff:   # (ctypes would take them modulo 2^32)
+        raise ValueError(f"window {window} and sinks {sinks} must be below 2^31")
     qs = _rows("q", q, T, H, D, dtype)
     if o is not None:
         _dense("o", o, (T, H, D), dtype)

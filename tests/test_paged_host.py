@@ -212,3 +212,19 @@ def test_scales_are_the_least_powers_of_two():
     s = U.quantise(x)[1]
     want = [1.0, 2.0, 2.0, 2.0 ** -8, 2.0 ** -7, 1.0, 2.0 ** -100, 2.0 ** 119 if 3e38 <= 448 * 2.0 ** 119 else 2.0 ** 120]
     assert s.tolist()[:7] == want[:7] and s[7] == 2.0 ** 119
+
+
+@pytest.mark.parametrize("kw", [dict(window=1 << 32), dict(window=(1 << 32) + 5), dict(window=-(1 << 32)),
+                                dict(sinks=(1 << 40) + 1)])
+def test_binding_refuses_what_int32_cannot_hold(lib, kw):
+    b = U.Batch([5, 3], [2, 0], 2, 32, U.F32, U.F32)
+    for call in (lambda: kda.paged_attn_fwd(b.queries(4), *b.cache, b.cu, **kw),
+                 lambda: kda.paged_attn_decode_step(b.queries(4)[:2], *b.cache, **kw)):
+        with pytest.raises(ValueError, match="below 2.31"):
+            call()
+
+
+def test_binding_refuses_pages_without_heads(lib):
+    b = U.Batch([5, 3], [2, 0], 2, 32, U.F32, U.F32)
+    with pytest.raises(ValueError, match="share 0"):
+        kda.paged_attn_fwd(b.queries(4), b.k_pages[:, :0], b.v_pages[:, :0], b.table, b.kv_lens, b.cu)
