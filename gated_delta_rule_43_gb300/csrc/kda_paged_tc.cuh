@@ -280,7 +280,9 @@ inline EncodeTiledFn encode_tiled() {
 }
 
 // Pages [P, Hk, page size, D] of bf16 or e4m3 as runs of rows, `page_runs` from one page's to the next's, in
-// boxes of up to 128 rows of a run x 128 bytes (64 for e4m3 heads of 64), swizzled as the products want them.
+// boxes of up to 128 rows of a run x 128 bytes (64 for e4m3 heads of up to 64), swizzled as the products want them.
+// Heads of 32 stand in the boxes of heads of 64: what a box has beyond a row reads as zeros.
+constexpr int in_tile(int D) { return D < 64 ? 64 : D; }   // a head's channels in shared and tensor memory
 inline int box_rows(const Cache &c) { return c.shift >= 7 ? 128 : 1 << c.shift; }
 __host__ __device__ inline int page_runs(const Cache &c, int D) { return (int)((c.stride / D) >> c.shift); }
 inline cudaError_t page_map(CUtensorMap *m, const Cache &c, const void *pages, int D, bool e4m3) {
@@ -290,11 +292,11 @@ inline cudaError_t page_map(CUtensorMap *m, const Cache &c, const void *pages, i
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)1 << c.shift,
                                 (cuuint64_t)(c.P - 1) * page_runs(c, D) + c.Hk};
     const cuuint64_t strides[2] = {row, row << c.shift};
-    const cuuint32_t box[3] = {(cuuint32_t)(e4m3 ? D : 64), (cuuint32_t)box_rows(c), 1};
+    const cuuint32_t box[3] = {(cuuint32_t)(e4m3 ? in_tile(D) : 64), (cuuint32_t)box_rows(c), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                            const_cast<void *>(pages), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           e4m3 && D <= 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

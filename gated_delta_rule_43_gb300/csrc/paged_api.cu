@@ -99,10 +99,8 @@ bool attn_sizes_ok(const kda_paged_cache *p, int64_t T, int32_t H) {
 // Test hook (kda_test_paged_fault): what the next call leaves out.
 std::atomic<int> g_left_out{-1};
 
-// bf16 heads of 64 and 128 go to the tensor cores (a pool without pages has nothing to load from).
-bool on_tensor_cores(const kda_paged_cache *p, int32_t dtype) {
-    return dtype == KDA_BF16 && p->D >= 64 && p->num_pages > 0;
-}
+// bf16 goes to the tensor cores (a pool without pages has nothing to load from).
+bool on_tensor_cores(const kda_paged_cache *p, int32_t dtype) { return dtype == KDA_BF16 && p->num_pages > 0; }
 
 size_t attn_bytes(const kda_paged_cache *p, int64_t T, int32_t H, int32_t dtype) {
     const paged::Cache c = make(p, T);

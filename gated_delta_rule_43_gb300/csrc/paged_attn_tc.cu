@@ -1,5 +1,5 @@
 // paged_attn_tc.cu -- attention of a chunk of new tokens over paged keys and values on the sm_103a
-// tensor cores (bf16 operands, fp32 accumulation), heads of 64 and 128.
+// tensor cores (bf16 operands, fp32 accumulation).
 //
 //   S = Q K^T;   m_i the running maximum of a row;   P = 2^(f S - f m), f = scale log2(e)
 //   O = sum over blocks of P V,   l = sum of P,   o = O / l
@@ -191,12 +191,13 @@ template <int D, bool E4M3> struct Map {
     static_assert(sizeof(Item) % 8 == 0 && kBytes <= 232448 && kItems % 1024 == 0, "layout");
 };
 
-template <int D, bool E4M3>
+template <int DIM, bool E4M3>
 __global__ void __launch_bounds__(kThreads<E4M3>, 1)
 paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const __nv_bfloat16 *__restrict__ q, int64_t q_stride, __nv_bfloat16 *__restrict__ o, int group,
                   float scale, int window, int sinks, int left_out, StatusWord *st) {
     extern __shared__ __align__(1024) uint8_t sm[];
+    constexpr int D = in_tile(DIM);   // (channels beyond DIM are products' columns that nobody reads)
     using M = Map<D, E4M3>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     let_next_start();
@@ -329,7 +330,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         m = grown;
                         l *= keep;
 #pragma unroll 1
-                        for (int j = 0; j < D; j += 8) {
+                        for (int j = 0; j < DIM; j += 8) {
                             float x[8];
                             tmem_ld(tO + j, x);
                             tmem_ld_wait();
@@ -388,7 +389,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             const uint32_t t0 = uniform(tmem);
             auto scores = [&](int tile, uint64_t dk) {   // S = Q K^T
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s)
+                for (int s = 0; s < DIM / 16; ++s)
                     umma_bf16(t0 + 128 * tile, desc_add(dq0, tile * M::kTile + (s >> 2) * 16384 + (s & 3) * 32),
                               desc_add(dk, (s >> 2) * 16384 + (s & 3) * 32), id_s, s > 0);
             };
@@ -485,7 +486,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                 kv = key;
             });
         } else if (warp == kLoadWarp) {
-            const int rows = min(BK, 1 << c.shift), boxes = BK / rows, runs = page_runs(c, D);
+            const int rows = min(BK, 1 << c.shift), boxes = BK / rows, runs = page_runs(c, DIM);
             const int none = (c.P - 1) * runs + c.Hk;   // past the last run: zeros
             each_item([&](const Item &it) {
                 // the page that holds the rows of this lane's box in block k; -1: a row that nobody sees
@@ -608,8 +609,8 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     const int row = 128 * tile + 32 * quarter;
                     if (row < it.rows) {
                         const int mine = it.row0 + min(row + lane, it.rows - 1), token = mine / group;
-                        const int64_t from = (int64_t)(it.tok0 + token) * q_stride + (int64_t)(it.h * group + mine - token * group) * D;
-                        constexpr int U = D / 8;   // pieces of a row
+                        const int64_t from = (int64_t)(it.tok0 + token) * q_stride + (int64_t)(it.h * group + mine - token * group) * DIM;
+                        constexpr int U = DIM / 8;   // pieces of a row
 #pragma unroll 4
                         for (int i = 0; i < U; ++i) {
                             const int r = (32 * i + lane) / U, x = lane % U;
@@ -667,7 +668,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         if (mine) p.ml[at] = make_float2(tile ? m[1] : m[0], sum);
                         if (any) {
 #pragma unroll 1
-                            for (int j = 0; j < D; j += 16) {
+                            for (int j = 0; j < DIM; j += 16) {
                                 float x[16];
                                 tmem_ld(tO + j, x);
                                 tmem_ld_wait();
@@ -675,18 +676,18 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(x[i]);
                                 if (mine) {
-                                    store32(p.part + at * D + j, v);
-                                    store32(p.part + at * D + j + 8, v + 8);
+                                    store32(p.part + at * DIM + j, v);
+                                    store32(p.part + at * DIM + j + 8, v + 8);
                                 }
                             }
                         }
                     } else if (live) {
                         const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (no visible key: zeros)
                         const int token = (it.row0 + min(r, it.rows - 1)) / group, head = it.h * group + (it.row0 + r) - token * group;
-                        __nv_bfloat16 *to = o + ((int64_t)(it.tok0 + token) * c.Hk * group + head) * D;
+                        __nv_bfloat16 *to = o + ((int64_t)(it.tok0 + token) * c.Hk * group + head) * DIM;
                         const bool wide = ((uintptr_t)to & 31) == 0;
 #pragma unroll 1
-                        for (int j = 0; j < D; j += 32) {
+                        for (int j = 0; j < DIM; j += 32) {
                             float x[32];
                             if (any) {
                                 tmem_ld32(tO + j, x);
@@ -753,7 +754,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                         uint8_t *to = sm + M::kKV + kv.stage * M::kTile;
                         const float s = now[v];
 #pragma unroll 4
-                        for (int x = 0; x < D / 16; ++x) {
+                        for (int x = 0; x < DIM / 16; ++x) {
                             // 16 bytes (their places swizzled by the load) become 16 bf16
                             const int place = D == 128 ? x ^ (row & 7) : x ^ ((row >> 1) & 3);
                             const uint4 in = *reinterpret_cast<const uint4 *>(from + 16 * place);
@@ -880,14 +881,17 @@ paged_join_kernel(Cache c, Plan p, __nv_bfloat16 *__restrict__ o, int group, Sta
         __nv_bfloat16 *to = o + ((int64_t)(t.s.begin + token) * c.Hk * group + here.h * group + at - token * group) * D +
                             lane * V;
 #pragma unroll
-        for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t *>(to + j) = pack2(x[j] * inv, x[j + 1] * inv);
+        for (int j = 0; j < V; j += 2) {
+            if constexpr (V == 1) *to = __float2bfloat16_rn(x[0] * inv);
+            else *reinterpret_cast<uint32_t *>(to + j) = pack2(x[j] * inv, x[j + 1] * inv);
+        }
     }
 }
 
 cudaError_t launch_join(int D, const Cache &c, const Plan &p, void *o, int group, StatusWord *st, cudaStream_t s) {
     const dim3 grid(p.ranges > 1 ? p.ranges - 1 : 1, (p.rows + 31) / 32);
-    return D == 128 ? launch_after(paged_join_kernel<128>, grid, dim3(kJoinThreads), 0, s, c, p, (__nv_bfloat16 *)o, group, st)
-                    : launch_after(paged_join_kernel<64>, grid, dim3(kJoinThreads), 0, s, c, p, (__nv_bfloat16 *)o, group, st);
+    return launch_after(D == 128 ? paged_join_kernel<128> : D == 64 ? paged_join_kernel<64> : paged_join_kernel<32>, grid,
+                        dim3(kJoinThreads), 0, s, c, p, (__nv_bfloat16 *)o, group, st);
 }
 
 struct Layout {
@@ -921,7 +925,7 @@ template <int D, bool E4M3> static cudaError_t allow_smem() {
     std::lock_guard<std::mutex> lock(mutex);
     if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
     e = cudaFuncSetAttribute(paged_attn_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)Map<D, E4M3>::kBytes);
+                             (int)Map<in_tile(D), E4M3>::kBytes);
     if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
     return e;
 }
@@ -941,7 +945,8 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
     paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(c, p, group, window, sinks, st);
     e = cudaGetLastError();
     if (e == cudaSuccess)
-        e = launch_after(paged_attn_kernel<D, E4M3>, dim3(L.ranges), dim3(kThreads<E4M3>), Map<D, E4M3>::kBytes, s, c, p, tk, tv,
+        e = launch_after(paged_attn_kernel<D, E4M3>, dim3(L.ranges), dim3(kThreads<E4M3>),
+                         Map<in_tile(D), E4M3>::kBytes, s, c, p, tk, tv,
                          (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks, left_out, st);
     return e == cudaSuccess ? launch_join(D, c, p, o, group, st, s) : e;
 }
@@ -957,11 +962,9 @@ cudaError_t launch_paged_tc(bool e4m3, int D, const paged::Cache &c, const void 
                             float scale, int window, int sinks, void *ws, int sms, int left_out, cudaStream_t s) {
     using paged::tc::launch;
     uint8_t *w = (uint8_t *)ws;
-    if (e4m3)
-        return D == 128 ? launch<128, true>(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s)
-                        : launch<64, true>(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s);
-    return D == 128 ? launch<128, false>(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s)
-                    : launch<64, false>(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s);
+    const auto run = e4m3 ? (D == 128 ? launch<128, true> : D == 64 ? launch<64, true> : launch<32, true>)
+                          : (D == 128 ? launch<128, false> : D == 64 ? launch<64, false> : launch<32, false>);
+    return run(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s);
 }
 
 }  // namespace kda

@@ -1,5 +1,5 @@
 // paged_decode_tc.cu -- attention of one new token a sequence over paged keys and values on the sm_103a
-// tensor cores, heads of 64 and 128.
+// tensor cores.
 //
 //   S^T = K Q^T,  P = 2^(f S - f m),  O^T = V^T P^T     (formulas: paged_attn_tc.cu)
 // Memory-bound: each key and value is read once, for all query heads that share it.  These are few, so
@@ -144,12 +144,13 @@ __device__ __forceinline__ Cut cut_at(const Cache &c, int64_t x, int n0, int n1,
     return cut;
 }
 
-template <int D, int NR, bool E4M3>
+template <int DIM, int NR, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const __nv_bfloat16 *__restrict__ q, int64_t q_stride, __nv_bfloat16 *__restrict__ o, int group,
                     float scale, int window, int sinks, int left_out) {
     extern __shared__ __align__(1024) uint8_t sm[];
+    constexpr int D = in_tile(DIM);   // (channels beyond DIM are products' rows that nobody reads)
     using M = Map<D, NR, E4M3>;
     constexpr int N = M::N, C = M::kCols;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -505,7 +506,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             if (!meet(3, 256)) return;
             if (side == 1) return;
             const int d = D == 128 ? tid : 16 * warp + lane;   // (64 rows of a product stand in 16 lanes of each warp)
-            const bool there = D == 128 || lane < 16;
+            const bool there = D == 128 || (lane < 16 && d < DIM);
 #pragma unroll
             for (int g = 0; g < NR; ++g) {
                 if (g >= rows) break;
@@ -517,9 +518,9 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                 if (it.slot >= 0) {
                     const int64_t at = (int64_t)it.slot * p.rows + g;
                     if (tid == 0) p.ml[at] = make_float2(ref, l);
-                    if (there) p.part[at * D + d] = x;
+                    if (there) p.part[at * DIM + d] = x;
                 } else if (there) {
-                    o[((int64_t)it.n * c.Hk * group + it.h * group + it.row0 + g) * D + d] =
+                    o[((int64_t)it.n * c.Hk * group + it.h * group + it.row0 + g) * DIM + d] =
                         __float2bfloat16_rn(l != 0.f ? x / l : 0.f);
                 }
             }
@@ -594,11 +595,11 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                         const uint32_t to = tmem + (ps.stage * kTiles + t) * N;
                         if constexpr (E4M3) {
 #pragma unroll
-                            for (int s = 0; s < D / 32; ++s)
+                            for (int s = 0; s < DIM / 32; ++s)
                                 umma_f8(to, desc_add(dk, s * 32), desc_add(dq, s * 32), id_s, s > 0);
                         } else {
 #pragma unroll
-                            for (int s = 0; s < D / 16; ++s)
+                            for (int s = 0; s < DIM / 16; ++s)
                                 umma_bf16(to, desc_add(dk, (s >> 2) * 16384 + (s & 3) * 32),
                                           desc_add(dq, (s >> 2) * 2048 + (s & 3) * 32), id_s, s > 0);
                         }
@@ -629,7 +630,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
         // Lane 8 t + b has to do with box b of a piece's tile t: its page is looked up a piece ahead, and the
         // loop over tiles is short (with every lane holding a box of all tiles, unrolled, a tile took the warp
         // 800 cycles, more than the memory).
-        const int rows = min(BK, 1 << c.shift), boxes = BK / rows, runs = page_runs(c, D);
+        const int rows = min(BK, 1 << c.shift), boxes = BK / rows, runs = page_runs(c, DIM);
         const int none = (c.P - 1) * runs + c.Hk;   // past the last run: zeros
         const int my_tile = lane >> 3, box = lane & 7;
         int owed = 0, owed_run = 0, owed_row = 0;   // the piece whose values are still to be loaded
@@ -733,18 +734,19 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             }
             if (it.k1 == it.k0) continue;
             // its queries
-            const __nv_bfloat16 *x0 = q + (int64_t)it.n * q_stride + (int64_t)(it.h * group + it.row0) * D;
+            const __nv_bfloat16 *x0 = q + (int64_t)it.n * q_stride + (int64_t)(it.h * group + it.row0) * DIM;
             uint8_t *place = sm + M::kQ + qs.stage * M::kQBytes;
             float *qf = reinterpret_cast<float *>(sm + M::kQf) + 16 * qs.stage;
             if (!wait(M::kQFree + qs.stage, qs.phase ^ 1)) break;
             if constexpr (E4M3) {
-                constexpr int V = D / 32;   // channels a lane
+                constexpr int V = D / 32;   // channels a lane (heads of 32: the last 16 lanes have zeros)
 #pragma unroll 4
                 for (int g = 0; g < it.rows; ++g) {
                     float x[V], top = 0.f;
 #pragma unroll
                     for (int j = 0; j < V; j += 2) {
-                        const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162 *>(x0 + g * D + lane * V + j);
+                        __nv_bfloat162 y = __floats2bfloat162_rn(0.f, 0.f);
+                        if (D == DIM || lane * V < DIM) y = *reinterpret_cast<const __nv_bfloat162 *>(x0 + g * DIM + lane * V + j);
                         x[j] = __low2float(y);
                         x[j + 1] = __high2float(y);
                         top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(x[j + 1])));
@@ -773,7 +775,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                     if (lane == 0) qf[g] = fine ? two_to(e) * scale * kLog2e : __int_as_float(0x7fffffff);
                 }
             } else {
-                constexpr int U = D / 8;
+                constexpr int U = DIM / 8;
                 for (int x = lane; x < it.rows * U; x += 32)
                     *reinterpret_cast<uint4 *>(place + sw128_offset(x / U, 8 * (x % U), 16)) =
                         *reinterpret_cast<const uint4 *>(x0 + x * 8);
@@ -884,7 +886,7 @@ template <int D, int NR, bool E4M3> static cudaError_t allow_smem() {
     std::lock_guard<std::mutex> lock(mutex);
     if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
     e = cudaFuncSetAttribute(paged_decode_kernel<D, NR, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)Map<D, NR, E4M3>::kBytes);
+                             (int)Map<in_tile(D), NR, E4M3>::kBytes);
     if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
     return e;
 }
@@ -900,7 +902,7 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
     if (e == cudaSuccess) e = page_map(&tv, c, c.v, D, E4M3);
     if (e == cudaSuccess) e = allow_smem<D, NR, E4M3>();
     if (e != cudaSuccess) return e;
-    paged_decode_kernel<D, NR, E4M3><<<L.ranges, kThreads, Map<D, NR, E4M3>::kBytes, s>>>(
+    paged_decode_kernel<D, NR, E4M3><<<L.ranges, kThreads, Map<in_tile(D), NR, E4M3>::kBytes, s>>>(
         c, p, tk, tv, (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks, left_out);
     e = cudaGetLastError();
     return e == cudaSuccess ? launch_join(D, c, p, o, group, (StatusWord *)ws, s) : e;
@@ -920,7 +922,7 @@ cudaError_t launch_paged_decode(bool e4m3, int D, const paged::Cache &c, const v
     if (D == D_ && group <= (NR_ == 16 ? 0x7fffffff : NR_) && e4m3 == E_) \
         return launch<D_, NR_, E_>(c, q, qs, o, group, scale, window, sinks, w, sms, left_out, s);
 #define KDA_ONES(D_, E_) KDA_ONE(D_, 4, E_) KDA_ONE(D_, 8, E_) KDA_ONE(D_, 16, E_)
-    KDA_ONES(64, false) KDA_ONES(128, false) KDA_ONES(64, true) KDA_ONES(128, true)
+    KDA_ONES(32, false) KDA_ONES(64, false) KDA_ONES(128, false) KDA_ONES(32, true) KDA_ONES(64, true) KDA_ONES(128, true)
 #undef KDA_ONES
 #undef KDA_ONE
     return cudaErrorInvalidValue;
