@@ -301,8 +301,87 @@ inline cudaError_t page_map(CUtensorMap *m, const Cache &c, const void *pages, i
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Single tokens.  An item is a sequence, a key/value head and up to `each` query heads; costs follow from the
+// lengths, so each CTA finds its own range.
+namespace one {
+
+constexpr int kItemCost = 1;        // an item's queries and outputs, in tiles
+constexpr int kUncut = 2;           // tiles of an item that is not cut
+
+// The place `x` of a row of items whose costs follow from the lengths; the caller's thread holds sequences
+// [n0, n1), which begin at `before`.
+__device__ __forceinline__ Cut cut_at(const Cache &c, int64_t x, int n0, int n1, int64_t before, int groups, int window,
+                                      int sinks) {
+    Cut cut{0, n0, 0, 0, 0};
+    for (int n = n0; n < n1; ++n) {
+        const Span s = span_of(c, n);
+        if (s.len == 0) continue;
+        const int count = key_blocks(max(0, s.pos), s.pos, window, sinks, BK).count, each = kItemCost + count;
+        const int64_t cost = (int64_t)groups * c.Hk * each, rest = x - before;
+        before += cost;
+        if (rest >= cost) continue;
+        int item = (int)(rest / each);
+        cut.k = (int)(rest - (int64_t)item * each) - kItemCost;
+        const bool next = count <= kUncut && 2 * cut.k > count;   // to the item's nearer end
+        if (cut.k < 1 || count <= kUncut) cut.k = 0;
+        if (next) ++item;
+        cut.n = n;
+        if (item == groups * c.Hk) {
+            item = 0;
+            ++cut.n;
+        }
+        cut.t = item / c.Hk;
+        cut.h = item - cut.t * c.Hk;
+        cut.tile = cut.n * groups + cut.t;
+        return cut;
+    }
+    return cut;
+}
+
+// Eight warps add up the costs of all sequences, and whoever holds the two ends of this CTA's range writes them
+// down: cuts[0], cuts[1].  All threads, 256 at least; sums: of eight warps.
+__device__ __forceinline__ void own_range(const Cache &c, int ranges, int groups, int window, int sinks, int64_t *sums,
+                                          Cut *cuts, StatusWord *st) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (c.N + 255) / 256, n0 = min(c.N, tid * per), n1 = min(c.N, n0 + per);
+    int64_t mine = 0, upto = 0;
+    if (tid < 256) {
+        for (int n = n0; n < n1; ++n) {
+            const Span s = span_of(c, n);
+            if (s.len) mine += (int64_t)groups * c.Hk * (kItemCost + key_blocks(max(0, s.pos), s.pos, window, sinks, BK).count);
+        }
+        upto = mine;
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, i);
+            if (lane >= i) upto += x;
+        }
+        if (lane == 31) sums[warp] = upto;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) check_spans(c, st);
+    int64_t total = 0;
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) upto += sums[w];
+        total += sums[w];
+    }
+    const int64_t share = max((total + ranges - 1) / ranges, (int64_t)(kItemCost + 1));
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const int64_t x = (int64_t)(blockIdx.x + i) * share;
+        if (x >= total) {
+            if (tid == 0) cuts[i] = Cut{c.N * groups, c.N, 0, 0, 0};
+        } else if (tid < 256 && x >= upto - mine && x < upto) {
+            cuts[i] = cut_at(c, x, n0, n1, upto - mine, groups, window, sinks);
+        }
+    }
+    __syncthreads();
+}
+
+}  // namespace one
+
 // Joins what the cuts inside items have left, behind the kernel that left it.
-cudaError_t launch_join(int D, const Cache &c, const Plan &p, void *o, int group, StatusWord *st, cudaStream_t s);
+cudaError_t launch_join(bool f32, int D, const Cache &c, const Plan &p, void *o, int group, StatusWord *st, cudaStream_t s);
 
 }  // namespace tc
 }  // namespace paged

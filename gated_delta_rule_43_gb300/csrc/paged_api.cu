@@ -20,6 +20,9 @@ cudaError_t launch_paged_tc(bool e4m3, int D, const paged::Cache &c, const void 
 size_t paged_decode_bytes(int group, int D, int sms);
 cudaError_t launch_paged_decode(bool e4m3, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
                                 float scale, int window, int sinks, void *ws, int sms, int left_out, cudaStream_t s);
+size_t paged_decode_simt_bytes(bool e4m3, int group, int D, int sms);
+cudaError_t launch_paged_decode_simt(bool e4m3, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
+                                     float scale, int window, int sinks, void *ws, int sms, cudaStream_t s);
 }  // namespace kda
 
 using namespace kda;
@@ -106,6 +109,7 @@ size_t attn_bytes(const kda_paged_cache *p, int64_t T, int32_t H, int32_t dtype)
     const paged::Cache c = make(p, T);
     if (on_tensor_cores(p, dtype) && !p->cu_seqlens) return paged_decode_bytes(H / p->Hk, p->D, sm_count());
     if (on_tensor_cores(p, dtype)) return paged_tc_bytes(c, H / p->Hk, p->D, sm_count());
+    if (dtype == KDA_F32 && !p->cu_seqlens) return paged_decode_simt_bytes(p->dtype == KDA_E4M3, H / p->Hk, p->D, sm_count());
     return kHeaderBytes + paged_simt_bytes(c, H / p->Hk, p->D, sm_count());
 }
 
@@ -125,6 +129,9 @@ kda_status attn(const kda_paged_cache *p, const void *q, int64_t qs, void *o, in
     if (T > 0 && p->num_seqs > 0 && on_tensor_cores(p, dtype))
         return cuda_status((p->cu_seqlens ? launch_paged_tc : launch_paged_decode)(
             p->dtype == KDA_E4M3, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window, sinks, workspace, sm_count(), g_left_out.exchange(-1), s));
+    if (T > 0 && p->num_seqs > 0 && dtype == KDA_F32 && !p->cu_seqlens)
+        return cuda_status(launch_paged_decode_simt(p->dtype == KDA_E4M3, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window,
+                                                    sinks, workspace, sm_count(), s));
     const kda_status e = clear(st, s);
     if (e != KDA_OK || T == 0 || p->num_seqs == 0) return e;
     return cuda_status(launch_paged_simt(dtype, p->dtype, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window, sinks,

@@ -815,9 +815,9 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
 // What the cuts inside one item have left, put together: a CTA for 32 rows of the item that the cut is
 // the first inside of.
 constexpr int kJoinThreads = 512;
-template <int D>
+template <typename TO, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-paged_join_kernel(Cache c, Plan p, __nv_bfloat16 *__restrict__ o, int group, StatusWord *st) {
+paged_join_kernel(Cache c, Plan p, TO *__restrict__ o, int group, StatusWord *st) {
     constexpr int V = D / 32;
     const int cut = blockIdx.x + 1, lane = threadIdx.x & 31;
     wait_for_previous();
@@ -878,20 +878,25 @@ paged_join_kernel(Cache c, Plan p, __nv_bfloat16 *__restrict__ o, int group, Sta
         }
         const float inv = l != 0.f ? 1.f / l : 0.f;
         const int at = t.row0 + r, token = at / group;
-        __nv_bfloat16 *to = o + ((int64_t)(t.s.begin + token) * c.Hk * group + here.h * group + at - token * group) * D +
-                            lane * V;
+        TO *to = o + ((int64_t)(t.s.begin + token) * c.Hk * group + here.h * group + at - token * group) * D + lane * V;
+        if constexpr (sizeof(TO) == 2 && V > 1) {
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            if constexpr (V == 1) *to = __float2bfloat16_rn(x[0] * inv);
-            else *reinterpret_cast<uint32_t *>(to + j) = pack2(x[j] * inv, x[j + 1] * inv);
+            for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t *>(to + j) = pack2(x[j] * inv, x[j + 1] * inv);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) to[j] = from_f<TO>(x[j] * inv);
         }
     }
 }
 
-cudaError_t launch_join(int D, const Cache &c, const Plan &p, void *o, int group, StatusWord *st, cudaStream_t s) {
+template <typename TO>
+static cudaError_t join(int D, const Cache &c, const Plan &p, void *o, int group, StatusWord *st, cudaStream_t s) {
     const dim3 grid(p.ranges > 1 ? p.ranges - 1 : 1, (p.rows + 31) / 32);
-    return launch_after(D == 128 ? paged_join_kernel<128> : D == 64 ? paged_join_kernel<64> : paged_join_kernel<32>, grid,
-                        dim3(kJoinThreads), 0, s, c, p, (__nv_bfloat16 *)o, group, st);
+    return launch_after(D == 128 ? paged_join_kernel<TO, 128> : D == 64 ? paged_join_kernel<TO, 64> : paged_join_kernel<TO, 32>,
+                        grid, dim3(kJoinThreads), 0, s, c, p, (TO *)o, group, st);
+}
+cudaError_t launch_join(bool f32, int D, const Cache &c, const Plan &p, void *o, int group, StatusWord *st, cudaStream_t s) {
+    return f32 ? join<float>(D, c, p, o, group, st, s) : join<__nv_bfloat16>(D, c, p, o, group, st, s);
 }
 
 struct Layout {
@@ -948,7 +953,7 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
         e = launch_after(paged_attn_kernel<D, E4M3>, dim3(L.ranges), dim3(kThreads<E4M3>),
                          Map<in_tile(D), E4M3>::kBytes, s, c, p, tk, tv,
                          (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks, left_out, st);
-    return e == cudaSuccess ? launch_join(D, c, p, o, group, st, s) : e;
+    return e == cudaSuccess ? launch_join(false, D, c, p, o, group, st, s) : e;
 }
 
 }  // namespace tc

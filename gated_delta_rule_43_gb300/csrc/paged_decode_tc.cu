@@ -39,8 +39,6 @@ namespace one {
 constexpr int kThreads = 384;
 constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10;   // (the last: scales)
 constexpr int kTiles = 4;           // of a piece
-constexpr int kItemCost = 1;        // an item's queries and outputs, in tiles
-constexpr int kUncut = 2;           // tiles of an item that is not cut
 constexpr int kRing = 4;            // items known ahead
 
 struct alignas(16) Item {
@@ -114,36 +112,6 @@ __device__ __forceinline__ uint32_t split_e4m3(float a, float b) {
     return (uint32_t)hi | (uint32_t)lo << 16;
 }
 
-// The place `x` of a row of items whose costs follow from the lengths; the caller's thread holds sequences
-// [n0, n1), which begin at `before`.
-__device__ __forceinline__ Cut cut_at(const Cache &c, int64_t x, int n0, int n1, int64_t before, int groups, int window,
-                                      int sinks) {
-    Cut cut{0, n0, 0, 0, 0};
-    for (int n = n0; n < n1; ++n) {
-        const Span s = span_of(c, n);
-        if (s.len == 0) continue;
-        const int count = key_blocks(max(0, s.pos), s.pos, window, sinks, BK).count, each = kItemCost + count;
-        const int64_t cost = (int64_t)groups * c.Hk * each, rest = x - before;
-        before += cost;
-        if (rest >= cost) continue;
-        int item = (int)(rest / each);
-        cut.k = (int)(rest - (int64_t)item * each) - kItemCost;
-        const bool next = count <= kUncut && 2 * cut.k > count;   // to the item's nearer end
-        if (cut.k < 1 || count <= kUncut) cut.k = 0;
-        if (next) ++item;
-        cut.n = n;
-        if (item == groups * c.Hk) {
-            item = 0;
-            ++cut.n;
-        }
-        cut.t = item / c.Hk;
-        cut.h = item - cut.t * c.Hk;
-        cut.tile = cut.n * groups + cut.t;
-        return cut;
-    }
-    return cut;
-}
-
 template <int DIM, int NR, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -202,41 +170,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
         tma_prefetch_map(&tk);
         tma_prefetch_map(&tv);
     }
-    // This CTA's range: eight warps add up the costs of all sequences, and whoever holds its two ends
-    // writes them down.
-    const int per = (c.N + 255) / 256, n0 = min(c.N, tid * per), n1 = min(c.N, n0 + per);
-    int64_t mine = 0, upto = 0;
-    if (tid < 256) {
-        for (int n = n0; n < n1; ++n) {
-            const Span s = span_of(c, n);
-            if (s.len) mine += (int64_t)groups * c.Hk * (kItemCost + key_blocks(max(0, s.pos), s.pos, window, sinks, BK).count);
-        }
-        upto = mine;
-#pragma unroll
-        for (int i = 1; i < 32; i <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, i);
-            if (lane >= i) upto += x;
-        }
-        if (lane == 31) sums[warp] = upto;
-    }
-    __syncthreads();
-    if (blockIdx.x == 0) check_spans(c, st);
-    int64_t total = 0;
-    for (int w = 0; w < 8; ++w) {
-        if (w < warp) upto += sums[w];
-        total += sums[w];
-    }
-    const int64_t share = max((total + p.ranges - 1) / p.ranges, (int64_t)(kItemCost + 1));
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-        const int64_t x = (int64_t)(blockIdx.x + i) * share;
-        if (x >= total) {
-            if (tid == 0) cuts[i] = Cut{c.N * groups, c.N, 0, 0, 0};
-        } else if (tid < 256 && x >= upto - mine && x < upto) {
-            cuts[i] = cut_at(c, x, n0, n1, upto - mine, groups, window, sinks);
-        }
-    }
-    __syncthreads();
+    own_range(c, p.ranges, groups, window, sinks, sums, cuts, st);
     tc_fence_after();
     const uint32_t tmem = *tslot;
     if (tid < 2 && (tid == 0 || blockIdx.x + 1 == p.ranges)) p.cuts[blockIdx.x + tid] = cuts[tid];
@@ -905,7 +839,7 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
     paged_decode_kernel<D, NR, E4M3><<<L.ranges, kThreads, Map<in_tile(D), NR, E4M3>::kBytes, s>>>(
         c, p, tk, tv, (const __nv_bfloat16 *)q, qs, (__nv_bfloat16 *)o, group, scale, window, sinks, left_out);
     e = cudaGetLastError();
-    return e == cudaSuccess ? launch_join(D, c, p, o, group, (StatusWord *)ws, s) : e;
+    return e == cudaSuccess ? launch_join(false, D, c, p, o, group, (StatusWord *)ws, s) : e;
 }
 
 }  // namespace one
