@@ -97,8 +97,5 @@ __device__ __forceinline__ KeyBlocks key_blocks(int first, int last, int window,
     return b;
 }
 
-template <typename T> __device__ __forceinline__ float stored_to_f(T x) { return to_f(x); }
-template <> __device__ __forceinline__ float stored_to_f<__nv_fp8_e4m3>(__nv_fp8_e4m3 x) { return (float)x; }
-
 }  // namespace paged
 }  // namespace kda

@@ -1,19 +1,20 @@
-// paged_attn_simt.cu -- attention over a paged cache on the CUDA cores, in fp32: single-precision
-// storage and heads of 32.
+// paged_attn_simt.cu -- attention of a chunk of new tokens over a paged cache in single precision, on the CUDA cores
+// (and of anything over a pool without pages, which tensor maps cannot describe).
 //
 //   o_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = exp(scale q_i k_j - m_i),   m_i the largest exponent
 // One pass over the keys with the running maximum and sum.  The query heads that share a key/value head
 // are rows beside each other (row = token * group + head), so that keys are read once for all of
-// them.  A CTA takes 32 rows and goes through blocks of 32 keys staged in shared memory as fp32; four
-// threads share a row.  Where there are few rows, `splits` CTAs share their keys and a second kernel
-// joins what they found.
+// them.  A CTA takes 64 rows and goes through blocks of 32 keys staged in shared memory as fp32; a thread has 4
+// rows and 4 keys of the scores, and of the outputs 4 rows and every eighth four channels, so that it multiplies 8 to 13 times
+// for every 16 bytes that it reads from there.  Where there are few rows, `splits` CTAs share their keys and a
+// second kernel joins what they found.
 #include "kda_paged.cuh"
 
 namespace kda {
 namespace paged {
 namespace simt {
 
-constexpr int BR = 32, BK = 32, kThreads = 128;
+constexpr int BR = 64, BK = 32, kThreads = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Rows [first, first + rows) of sequence n's len * group.
@@ -21,7 +22,7 @@ struct Tile {
     int n, first, rows;
     Span s;
 };
-// The `tile`-th tile of 32 rows in the batch; a whole warp.  False past the last.
+// The `tile`-th tile of 64 rows in the batch; a whole warp.  False past the last.
 __device__ __forceinline__ bool find_tile(const Cache &c, int tile, int group, Tile &r) {
     const int lane = threadIdx.x & 31;
     int64_t before = 0;
@@ -53,157 +54,236 @@ __device__ __forceinline__ bool find_tile(const Cache &c, int tile, int group, T
     return false;
 }
 
-template <int D> struct Shared {
-    float q[BR][D + 4];
-    float k[BK][D + 4];
-    float v[BK][D + 4];
-    float p[BR][BK + 4];
+// Where a key lies: -1: nowhere, or nobody sees it (zeros).
+struct Place {
+    int64_t at;
+    float ks, vs;
+};
+struct Found {
     Tile tile;
     int there;
 };
+template <int D> struct Shared {   // (D = 128: 76800 bytes, three CTAs an SM)
+    float q[BR][D + 4];
+    float k[BK][D + 4];
+    float v[BK][D];
+    union {
+        float p[BR][BK + 4];
+        Found found;   // (before the first weights)
+    };
+    Place places[BK];
+};
+
+// V stored values as fp32, times s
+__device__ __forceinline__ void widen(const uint4 &x, float s, float (&y)[4], float) {
+    y[0] = __uint_as_float(x.x);
+    y[1] = __uint_as_float(x.y);
+    y[2] = __uint_as_float(x.z);
+    y[3] = __uint_as_float(x.w);
+}
+__device__ __forceinline__ void widen(const uint4 &x, float s, float (&y)[8], __nv_bfloat16) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[2 * i] = __uint_as_float(w[i] << 16);
+        y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void widen(const uint4 &x, float s, float (&y)[16], __nv_fp8_e4m3) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 z = __half22float2(__half2(
+            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3)));
+        y[2 * i] = z.x * s;
+        y[2 * i + 1] = z.y * s;
+    }
+}
 
 template <typename TQ, typename TC, int D>
 __global__ void __launch_bounds__(kThreads)
 paged_simt_kernel(Cache c, const TQ *__restrict__ q, int64_t q_stride, TQ *__restrict__ o, int group, float scale,
                   int window, int sinks, int splits, float *__restrict__ part, StatusWord *st) {
+    constexpr int V = 16 / sizeof(TC), R = 4, C = D / 32;   // values a load; rows a thread; channels of it, in fours
     extern __shared__ __align__(16) uint8_t raw[];
     Shared<D> &sm = *reinterpret_cast<Shared<D> *>(raw);
     const int tid = threadIdx.x, H = c.Hk * group;
-    const int tile = blockIdx.x / c.Hk, h = blockIdx.x % c.Hk, split = blockIdx.y;
+    const int tile = (gridDim.x - 1 - blockIdx.x) / c.Hk, h = (gridDim.x - 1 - blockIdx.x) % c.Hk, split = blockIdx.y;
     if (blockIdx.x == 0 && split == 0) check_spans(c, st);
     if (tid < 32) {
         Tile t;
         const bool there = find_tile(c, tile, group, t);
         if (tid == 0) {
-            sm.there = there;
-            if (there) sm.tile = t;
+            sm.found.there = there;
+            if (there) sm.found.tile = t;
         }
     }
     __syncthreads();
-    if (!sm.there) return;
-    const Tile t = sm.tile;
+    if (!sm.found.there) return;
+    const Tile t = sm.found.tile;
+    const float f = scale * kLog2e;
     for (int x = tid; x < BR * D; x += kThreads) {
         const int r = x / D, d = x % D;
         float y = 0.f;
         if (r < t.rows) {
             const int at = t.first + r;
-            y = to_f(q[(int64_t)(t.s.begin + at / group) * q_stride + (int64_t)(h * group + at % group) * D + d]);
+            y = to_f(q[(int64_t)(t.s.begin + at / group) * q_stride + (int64_t)(h * group + at % group) * D + d]) * f;
         }
         sm.q[r][d] = y;
     }
-    const int r = tid / 4, quarter = tid % 4;
-    const int pos = t.s.pos + (t.first + r) / group;
-    const int lowest = window > 0 ? max(max(pos, 0) - window, -1) : -1;   // keys above it are in the window
-    const KeyBlocks kb = key_blocks(max(0, t.s.pos + t.first / group), t.s.pos + (t.first + t.rows - 1) / group, window,
-                                    sinks, BK);
+    // this thread's rows r0 + 16 i, keys k0 + 8 j of a block, channels 4 k0 + 32 j
+    const int r0 = tid / 8, k0 = tid % 8;
+    const int first = max(0, t.s.pos + t.first / group);    // the earliest token's position
+    const KeyBlocks kb = key_blocks(first, t.s.pos + (t.first + t.rows - 1) / group, window, sinks, BK);
     const int b0 = (int)((int64_t)kb.count * split / splits), b1 = (int)((int64_t)kb.count * (split + 1) / splits);
-    float m = -INFINITY, l = 0.f, acc[D / 4];
-#pragma unroll
-    for (int j = 0; j < D / 4; ++j) acc[j] = 0.f;
-    const float f = scale * kLog2e;
     const int ctx = t.s.pos + t.s.len;
+    int pos[R], lowest[R];   // keys above lowest are in the row's window
+    float m[R], l[R], acc[R][C][4];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        pos[i] = t.s.pos + (t.first + min(r0 + 16 * i, t.rows - 1)) / group;
+        lowest[i] = window > 0 ? max(max(pos[i], 0) - window, -1) : -1;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < C; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
+    }
+    auto look_up = [&](int b) {   // the place of block b's key tid
+        const int key = kb.block(b) * BK + tid;
+        Place y{-1, 0.f, 0.f};
+        const bool seen = key < ctx && (window <= 0 || key < sinks || key > first - window);   // (what nobody sees may be anything)
+        if (seen) {
+            const int page = c.table[(int64_t)t.n * c.width + (key >> c.shift)];
+            if (page >= 0 && page < c.P) {
+                const int64_t at = ((int64_t)h << c.shift) + (key & ((1 << c.shift) - 1));
+                y.at = page * c.stride + at * D;
+                if (sizeof(TC) == 1) {
+                    y.ks = c.ks[page * c.scale_stride + at];
+                    y.vs = c.vs[page * c.scale_stride + at];
+                }
+            } else {
+                report(st, KDA_ERR_INVALID_ARG, t.n, 64);
+            }
+        }
+        return y;
+    };
+    if (tid < BK && b0 < b1) sm.places[tid] = look_up(b0);
+    __syncthreads();
     for (int b = b0; b < b1; ++b) {
         const int key0 = kb.block(b) * BK;
-        __syncthreads();
-        for (int x = tid; x < BK * D / 4; x += kThreads) {
-            const int j = x / (D / 4), d = x % (D / 4) * 4, key = key0 + j;
-            float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-            if (key < ctx) {
-                const int page = c.table[(int64_t)t.n * c.width + (key >> c.shift)];
-                const bool seen = window <= 0 || key < sinks || key > max(0, t.s.pos + t.first / group) - window;
-                if (page >= 0 && page < c.P) {
-                    const int64_t at = ((int64_t)h << c.shift) + (key & ((1 << c.shift) - 1));
-                    const TC *ka = (const TC *)c.k + page * c.stride + at * D + d;
-                    const TC *va = (const TC *)c.v + page * c.stride + at * D + d;
-                    float sk = 1.f, sv = 1.f;
-                    if (sizeof(TC) == 1) {
-                        sk = c.ks[page * c.scale_stride + at];
-                        sv = c.vs[page * c.scale_stride + at];
-                    }
-                    if (seen) {   // (what nobody sees may be anything)
-                        kx = make_float4(stored_to_f(ka[0]) * sk, stored_to_f(ka[1]) * sk, stored_to_f(ka[2]) * sk,
-                                         stored_to_f(ka[3]) * sk);
-                        vx = make_float4(stored_to_f(va[0]) * sv, stored_to_f(va[1]) * sv, stored_to_f(va[2]) * sv,
-                                         stored_to_f(va[3]) * sv);
-                    }
-                } else if (seen) {
-                    report(st, KDA_ERR_INVALID_ARG, t.n, 64);
-                }
+#pragma unroll 4
+        for (int x = tid; x < BK * D / V; x += kThreads) {
+            const int j = x / (D / V), d = x % (D / V) * V;
+            const Place y = sm.places[j];
+            uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
+            if (y.at >= 0) {
+                kx = __ldg(reinterpret_cast<const uint4 *>((const TC *)c.k + y.at + d));
+                vx = __ldg(reinterpret_cast<const uint4 *>((const TC *)c.v + y.at + d));
             }
-            *reinterpret_cast<float4 *>(&sm.k[j][d]) = kx;
-            *reinterpret_cast<float4 *>(&sm.v[j][d]) = vx;
+            float kf[V], vf[V];
+            widen(kx, y.ks, kf, TC());
+            widen(vx, y.vs, vf, TC());
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                *reinterpret_cast<float4 *>(&sm.k[j][d + i]) = make_float4(kf[i], kf[i + 1], kf[i + 2], kf[i + 3]);
+                *reinterpret_cast<float4 *>(&sm.v[j][d + i]) = make_float4(vf[i], vf[i + 1], vf[i + 2], vf[i + 3]);
+            }
         }
         __syncthreads();
-        float s[8];
+        Place next{-1, 0.f, 0.f};   // (on its way while the scores are formed)
+        if (tid < BK && b + 1 < b1) next = look_up(b + 1);
+        float s[R][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = 0.f;
-#pragma unroll 4
+        for (int i = 0; i < R; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll 2
         for (int d = 0; d < D; d += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(&sm.q[r][d]);
+            float4 x[R];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float4 y = *reinterpret_cast<const float4 *>(&sm.k[quarter + 4 * j][d]);
-                s[j] += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+            for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const float4 *>(&sm.q[r0 + 16 * i][d]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 y = *reinterpret_cast<const float4 *>(&sm.k[k0 + 8 * j][d]);
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    s[i][j] = fmaf(x[i].x, y.x, fmaf(x[i].y, y.y, fmaf(x[i].z, y.z, fmaf(x[i].w, y.w, s[i][j]))));
             }
         }
-        float top = m;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int key = key0 + quarter + 4 * j;
-            s[j] = key <= pos && (key > lowest || key < sinks) ? s[j] * f : -INFINITY;
-            top = fmaxf(top, s[j]);
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float keep = exp2f(m - ref);
-        m = top;
-        float sum = 0.f;
+        for (int i = 0; i < R; ++i) {
+            float top = m[i];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float p = exp2f(s[j] - ref);
-            sum += p;
-            sm.p[r][quarter + 4 * j] = p;
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        l = l * keep + sum;
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < D / 4; ++j) acc[j] *= keep;
-#pragma unroll 4
-        for (int j = 0; j < BK; ++j) {
-            const float p = sm.p[r][j];
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-                const float4 y = *reinterpret_cast<const float4 *>(&sm.v[j][16 * d + 4 * quarter]);
-                acc[4 * d] += p * y.x;
-                acc[4 * d + 1] += p * y.y;
-                acc[4 * d + 2] += p * y.z;
-                acc[4 * d + 3] += p * y.w;
+            for (int j = 0; j < 4; ++j) {
+                const int key = key0 + k0 + 8 * j;
+                s[i][j] = key <= pos[i] && (key > lowest[i] || key < sinks) ? s[i][j] : -INFINITY;
+                top = fmaxf(top, s[i][j]);
             }
+#pragma unroll
+            for (int x = 1; x < 8; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float ref = top == -INFINITY ? 0.f : top;
+            const float keep = exp2f(m[i] - ref);
+            m[i] = top;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[i][j] - ref);
+                sum += p;
+                sm.p[r0 + 16 * i][k0 + 8 * j] = p;
+            }
+            l[i] = l[i] * keep + sum;   // (of this thread's keys: joined at the end)
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[i][j][x] *= keep;
         }
-    }
-    if (r >= t.rows) return;
-    if (splits > 1) {   // [tile, head][split][row]: D sums, the maximum, the sum of weights
-        float *to = part + (((int64_t)blockIdx.x * splits + split) * BR + r) * (D + 4);
+        __syncwarp();   // (a warp's rows are its own)
+#pragma unroll 2
+        for (int k = 0; k < BK; k += 4) {
+            float4 p[R];
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-            *reinterpret_cast<float4 *>(to + 16 * d + 4 * quarter) =
-                make_float4(acc[4 * d], acc[4 * d + 1], acc[4 * d + 2], acc[4 * d + 3]);
-        if (quarter == 0) {
-            to[D] = m;
-            to[D + 1] = l;
+            for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4 *>(&sm.p[r0 + 16 * i][k]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    const float4 y = *reinterpret_cast<const float4 *>(&sm.v[k + x][4 * k0 + 32 * j]);
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const float w = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
+                        acc[i][j][0] = fmaf(w, y.x, acc[i][j][0]);
+                        acc[i][j][1] = fmaf(w, y.y, acc[i][j][1]);
+                        acc[i][j][2] = fmaf(w, y.z, acc[i][j][2]);
+                        acc[i][j][3] = fmaf(w, y.w, acc[i][j][3]);
+                    }
+                }
         }
-        return;
+        if (tid < BK) sm.places[tid] = next;
+        __syncthreads();
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;   // (no visible key: zeros)
-    const int at = t.first + r;
-    TQ *to = o + ((int64_t)(t.s.begin + at / group) * H + h * group + at % group) * D;
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d)
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) to[16 * d + 4 * quarter + j] = from_f<TQ>(l != 0.f ? acc[4 * d + j] * inv : 0.f);
+        for (int x = 1; x < 8; x *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+        const int r = r0 + 16 * i;
+        if (r >= t.rows) continue;
+        if (splits > 1) {   // [tile, head][split][row]: D sums, the maximum, the sum of weights
+            float *to = part + (((int64_t)blockIdx.x * splits + split) * BR + r) * (D + 4);
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                *reinterpret_cast<float4 *>(to + 32 * j + 4 * k0) = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+            if (k0 == 0) {
+                to[D] = m[i];
+                to[D + 1] = l[i];
+            }
+            continue;
+        }
+        const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;   // (no visible key: zeros)
+        const int at = t.first + r;
+        TQ *to = o + ((int64_t)(t.s.begin + at / group) * H + h * group + at % group) * D;
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) to[32 * j + 4 * k0 + x] = from_f<TQ>(l[i] != 0.f ? acc[i][j][x] * inv : 0.f);
+    }
 }
 
 template <typename TQ, int D>
@@ -211,10 +291,10 @@ __global__ void __launch_bounds__(kThreads)
 paged_simt_join(Cache c, TQ *__restrict__ o, int group, int splits, const float *__restrict__ part) {
     __shared__ Tile tile;
     __shared__ int there;
-    const int tid = threadIdx.x, h = blockIdx.x % c.Hk, H = c.Hk * group;
+    const int tid = threadIdx.x, h = (gridDim.x - 1 - blockIdx.x) % c.Hk, H = c.Hk * group;
     if (tid < 32) {
         Tile t;
-        const bool found = find_tile(c, blockIdx.x / c.Hk, group, t);
+        const bool found = find_tile(c, (gridDim.x - 1 - blockIdx.x) / c.Hk, group, t);
         if (tid == 0) {
             there = found;
             if (found) tile = t;
