@@ -7,7 +7,8 @@
 // them.  A CTA takes 64 rows and goes through blocks of 32 keys staged in shared memory as fp32; a thread has 4
 // rows and 4 keys of the scores, and of the outputs 4 rows and every eighth four channels, so that it multiplies 8 to 13 times
 // for every 16 bytes that it reads from there.  Where there are few rows, `splits` CTAs share their keys and a
-// second kernel joins what they found.
+// second kernel joins what they found.  4096 new tokens, 8 heads on 2 of 128: 1.0 ms, 34 TFLOP/s of the 74 that fp32
+// multiply-adds reach; the stores that stage a block and the reads of it are what the rest goes to.
 #include "kda_paged.cuh"
 
 namespace kda {
@@ -286,39 +287,59 @@ paged_simt_kernel(Cache c, const TQ *__restrict__ q, int64_t q_stride, TQ *__res
     }
 }
 
+// A row a warp, a split a lane: what the splits count for at once, then their sums, four on their way.  (An
+// element a thread, one split after the other, 40 of them took 400 us.)
 template <typename TQ, int D>
 __global__ void __launch_bounds__(kThreads)
 paged_simt_join(Cache c, TQ *__restrict__ o, int group, int splits, const float *__restrict__ part) {
-    __shared__ Tile tile;
-    __shared__ int there;
-    const int tid = threadIdx.x, h = (gridDim.x - 1 - blockIdx.x) % c.Hk, H = c.Hk * group;
+    constexpr int V = D / 32;
+    __shared__ Found found;
+    const int tid = threadIdx.x, lane = tid & 31, h = (gridDim.x - 1 - blockIdx.x) % c.Hk, H = c.Hk * group;
     if (tid < 32) {
         Tile t;
-        const bool found = find_tile(c, (gridDim.x - 1 - blockIdx.x) / c.Hk, group, t);
+        const bool there = find_tile(c, (gridDim.x - 1 - blockIdx.x) / c.Hk, group, t);
         if (tid == 0) {
-            there = found;
-            if (found) tile = t;
+            found.there = there;
+            if (there) found.tile = t;
         }
     }
     __syncthreads();
-    if (!there) return;
-    for (int x = tid; x < tile.rows * D; x += kThreads) {
-        const int r = x / D, d = x % D;
+    if (!found.there) return;
+    const Tile t = found.tile;
+    for (int r = blockIdx.y * (kThreads / 32) + tid / 32; r < t.rows; r += gridDim.y * (kThreads / 32)) {
         const float *from = part + ((int64_t)blockIdx.x * splits * BR + r) * (D + 4);
         const int64_t step = (int64_t)BR * (D + 4);
         float top = -INFINITY;
-        for (int s = 0; s < splits; ++s) top = fmaxf(top, from[s * step + D]);
-        float sum = 0.f, l = 0.f;
-        for (int s = 0; s < splits; ++s) {
-            const float w = from[s * step + D + 1];
-            if (w == 0.f) continue;
-            const float e = exp2f(from[s * step + D] - top);
-            l += e * w;
-            sum += e * from[s * step + d];
+        for (int s = lane; s < splits; s += 32)
+            if (from[s * step + D + 1] != 0.f) top = fmaxf(top, from[s * step + D]);
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        float l = 0.f, sum[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] = 0.f;
+        for (int s0 = 0; s0 < splits; s0 += 32) {
+            float mine = 0.f;   // (0: its sums may be anything)
+            if (s0 + lane < splits) {
+                const float w = from[(s0 + lane) * step + D + 1];
+                if (w != 0.f) mine = exp2f(from[(s0 + lane) * step + D] - top);
+                l += mine * w;
+            }
+#pragma unroll 4
+            for (int s = s0; s < min(splits, s0 + 32); ++s) {
+                const float e = __shfl_sync(0xffffffffu, mine, s - s0);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float y = from[s * step + lane * V + j];
+                    sum[j] += e != 0.f ? e * y : 0.f;
+                }
+            }
         }
-        const int at = tile.first + r;
-        o[((int64_t)(tile.s.begin + at / group) * H + h * group + at % group) * D + d] =
-            from_f<TQ>(l != 0.f ? sum / l : 0.f);
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
+        const int at = t.first + r;
+        TQ *to = o + ((int64_t)(t.s.begin + at / group) * H + h * group + at % group) * D + lane * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) to[j] = from_f<TQ>(l != 0.f ? sum[j] / l : 0.f);
     }
 }
 
@@ -326,12 +347,14 @@ paged_simt_join(Cache c, TQ *__restrict__ o, int group, int splits, const float 
 static int64_t tiles_of(const Cache &c, int group) {
     return c.cu ? (int64_t)c.T * group / BR + c.N : c.N * (int64_t)((group + BR - 1) / BR);
 }
-// CTAs that share a tile's keys: enough for two a multiprocessor, each with 256 keys or more.
+// CTAs that share a tile's keys: enough for four a multiprocessor, each with 128 keys or more.  (Three are there
+// at once with D = 128, four or five with less.  With 2, 3, 4, 6 a multiprocessor 4096 new tokens, 8 heads on 2 of 128,
+// take 1231, 1234, 997, 1008 us; 2048 tokens 331, 331, 350, 335; of 64: 195, 196, 160, 176.)
 static int splits_of(const Cache &c, int group, int sms) {
     const int64_t ctas = tiles_of(c, group) * c.Hk;
     if (ctas == 0) return 1;
-    int64_t s = (2 * sms + ctas - 1) / ctas;
-    const int64_t most = (((int64_t)c.width << c.shift) + 255) / 256;
+    int64_t s = (4 * sms + ctas - 1) / ctas;
+    const int64_t most = (((int64_t)c.width << c.shift) + 127) / 128;
     s = s < most ? s : most;
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
@@ -346,7 +369,8 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
     if (e != cudaSuccess) return e;
     paged_simt_kernel<TQ, TC, D><<<dim3((unsigned)ctas, splits), kThreads, sizeof(Shared<D>), s>>>(
         c, (const TQ *)q, qs, (TQ *)o, group, scale, window, sinks, splits, part, st);
-    if (splits > 1) paged_simt_join<TQ, D><<<(unsigned)ctas, kThreads, 0, s>>>(c, (TQ *)o, group, splits, part);
+    if (splits > 1)
+        paged_simt_join<TQ, D><<<dim3((unsigned)ctas, 4), kThreads, 0, s>>>(c, (TQ *)o, group, splits, part);
     return cudaGetLastError();
 }
 
