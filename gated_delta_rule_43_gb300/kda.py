@@ -129,6 +129,8 @@ def _stream(stream):
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
 
 
 def _check_current(device):
@@ -469,9 +471,9 @@ def _new(like, shape, dtype, stream):
     """Buffers that a call allocates belong to the stream that it runs on, so that the caching
     allocator hands their memory on in that stream's order."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _workspace(like, nbytes, workspace, stream):
@@ -918,20 +920,31 @@ def _paged_attn(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, scale, wi
                        workspace)
     if o is None:
         o = _new(q, (T, H, D), dtype, stream)
-    dt = _DT[dtype]
+    dt, raw = _DT[dtype], _raw_stream(stream, device)
     need = 0
     if workspace is None:
         need = _paged_workspace_size(device, cache.num_seqs, cache.table_width, cache.num_pages,
                                      cache.page_size, Hk, D, cache.dtype, T, H, dt, decode)
-    workspace, wa, wb = _workspace(q, need, workspace, stream)
-    if decode:
-        name = "kda_paged_attn_decode_step"
-        rc = lib.kda_paged_attn_decode_step(ctypes.byref(cache), q.data_ptr(), qs, o.data_ptr(), H, dt,
-                                            scale, window, sinks, wa, wb, _raw_stream(stream, device))
+    own = 0
+    if workspace is None and not check and need and _raw_alloc is not None:
+        # Nobody looks at it afterwards, so it need not be a tensor (1 us, not 7); handed on in the
+        # stream's order like one.
+        own, wb = _raw_alloc(need, raw), need
+        wa = own
     else:
-        name = "kda_paged_attn_fwd"
-        rc = lib.kda_paged_attn_fwd(ctypes.byref(cache), q.data_ptr(), qs, o.data_ptr(), T, H, dt,
-                                    scale, window, sinks, wa, wb, _raw_stream(stream, device))
+        workspace, wa, wb = _workspace(q, need, workspace, stream)
+    try:
+        if decode:
+            name = "kda_paged_attn_decode_step"
+            rc = lib.kda_paged_attn_decode_step(ctypes.byref(cache), q.data_ptr(), qs, o.data_ptr(), H, dt,
+                                                scale, window, sinks, wa, wb, raw)
+        else:
+            name = "kda_paged_attn_fwd"
+            rc = lib.kda_paged_attn_fwd(ctypes.byref(cache), q.data_ptr(), qs, o.data_ptr(), T, H, dt,
+                                        scale, window, sinks, wa, wb, raw)
+    finally:
+        if own:
+            _raw_delete(own)
     if rc != KDA_OK:
         raise KdaError(rc, name)
     if check:

@@ -175,6 +175,7 @@ def fake(monkeypatch):
     monkeypatch.setattr(kda, "_lib", library)
     monkeypatch.setattr(kda, "_current_device", lambda: 0, raising=False)
     monkeypatch.setattr(kda, "_current_raw_stream", lambda device: 0)
+    monkeypatch.setattr(kda, "_raw_alloc", None)
     monkeypatch.setattr(kda, "_new", lambda like, shape, dtype, stream: torch.empty(shape, dtype=dtype))
     kda._paged_workspace_size.cache_clear()
     yield library
