@@ -567,3 +567,92 @@ def test_what_the_windows_have_passed_may_be_anything(dtype, cache, window, sink
         spoil(b, lambda n, c: (torch.arange(c) < sinks) | (torch.arange(c) >= c - window))
         o = kda.paged_attn_decode_step(q, *b.cache, window=window, sinks=sinks, **b.scales, check=True)
         U.check_attention(o, b, q, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("cache", [F32, E4M3])
+def test_single_precision_reports_what_does_not_fit(cache):
+    b = Batch([1] * 5, [700, 60, 0, 5, 1500], 2, 64, F32, cache, 16, seed=3, device=DEV)
+    q = b.queries(8)
+    good = kda.paged_attn_decode_step(q, *b.cache, **b.scales, check=True)
+    table, lens = b.table.clone(), b.kv_lens.clone()
+    b.table[1, 2] = b.P
+    o = torch.zeros_like(good)
+    call = lambda ws: kda.paged_attn_decode_step(q, *b.cache, **b.scales, o=o, workspace=ws)  # noqa: E731
+    assert code_of(call) == (kda.KDA_ERR_INVALID_ARG, 1)
+    others = [0, 2, 3, 4]
+    assert torch.equal(o[others], good[others]) and o.isfinite().all()
+    b.table = table
+    for bad in (-3, 1 << 20):
+        b.kv_lens[3] = bad
+        o.fill_(7.0)
+        assert code_of(call) == (kda.KDA_ERR_SEQLENS, 3)
+        assert (o[3] == 7).all() and torch.equal(o[[0, 1, 2, 4]], good[[0, 1, 2, 4]])
+        b.kv_lens = lens.clone()
+    assert code_of(call)[0] == kda.KDA_OK
+    assert torch.equal(o, good)
+    q[2, 5, 1] = math.nan
+    o = kda.paged_attn_decode_step(q, *b.cache, **b.scales)
+    hurt = torch.zeros(5, 8, dtype=torch.bool, device=DEV)
+    hurt[2, 5] = True
+    assert o[hurt].isnan().all() and torch.equal(o[~hurt], good[~hurt])
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("D", [32, 128])
+def test_single_tokens_stay_inside_their_bands(dtype, cache, D):
+    b = Batch([1] * 9, [3000, 13, 0, 1000, 128, 127, 1, 40, 2222], 2, D, dtype, cache, 16, device=DEV)
+    q = b.queries(10)
+    before = [bits(t).clone() for t in (q, b.k_pages, b.v_pages, b.table)]
+    band = torch.full((9 * 10 * D + 2048,), 7.0, dtype=dtype, device=DEV)
+    o = band[1024:-1024].view(9, 10, D)
+    need = kda._paged_workspace_size(0, 9, b.table.shape[1], b.P, 16, 2, D, kda.KDA_E4M3 if cache is E4M3 else
+                                     kda._DT[dtype], 9, 10, kda._DT[dtype], True)
+    ws = torch.full((need + 8192,), 77, dtype=torch.uint8, device=DEV)
+    kda.paged_attn_decode_step(q, *b.cache, **b.scales, o=o, workspace=ws[4096:4096 + need], check=True)
+    U.check_attention(o, b, q)
+    assert (band[:1024] == 7).all() and (band[-1024:] == 7).all()
+    assert (ws[:4096] == 77).all() and (ws[4096 + need:] == 77).all()
+    assert all(torch.equal(x, bits(t)) for x, t in zip(before, (q, b.k_pages, b.v_pages, b.table)))
+
+
+@pytest.mark.parametrize("cache", [F32, E4M3])
+def test_single_precision_of_many_sequences(cache):
+    """More items than CTAs, most of them short, among them some without tokens; and one long one."""
+    before = [(37 * i) % 150 for i in range(700)]
+    before[350] = 9000
+    b = Batch([1] * 700, before, 1, 32, F32, cache, 16, seed=5, device=DEV)
+    b.kv_lens[::7] = 0
+    q = b.queries(3)
+    o = kda.paged_attn_decode_step(q, *b.cache, **b.scales, check=True)
+    assert not o[::7].any()
+    U.check_attention(o, b, q)
+
+
+def test_two_graphs_take_turns():
+    """Captured with workspaces of their own making, replayed in any order, on the stream's data of then."""
+    b = Batch([1] * 4, [500, 3, 1200, 64], 2, 128, BF, BF, 16, device=DEV)
+    c = Batch([30, 1, 200], [100, 900, 0], 2, 64, F32, F32, 32, device=DEV)
+    qb, qc = b.queries(8), c.queries(4)
+    want = [[], []]
+    other = [b.queries(8, seed=9), c.queries(4, seed=9)]
+    for x, y in ((qb, qc), other):
+        want[0].append(kda.paged_attn_decode_step(x, *b.cache, check=True))
+        want[1].append(kda.paged_attn_fwd(y, *c.cache, c.cu, check=True))
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for call in (lambda: kda.paged_attn_decode_step(qb, *b.cache), lambda: kda.paged_attn_fwd(qc, *c.cache, c.cu)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call())
+        graphs.append(g)
+    for turn in (0, 1, 0):
+        if turn:
+            qb.copy_(other[0])
+            qc.copy_(other[1])
+        for i in (1, 0, 0, 1):
+            outs[i].fill_(7.0)
+            graphs[i].replay()
+        assert torch.equal(outs[0], want[0][turn]) and torch.equal(outs[1], want[1][turn])
+        if turn:
+            qb.copy_(b.queries(8))
+            qc.copy_(c.queries(4))
