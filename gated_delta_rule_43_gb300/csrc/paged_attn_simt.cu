@@ -7,7 +7,7 @@
 // them.  A CTA takes 64 rows and goes through blocks of 32 keys staged in shared memory as fp32; a thread has 4
 // rows and 4 keys of the scores, and of the outputs 4 rows and every eighth four channels, so that it multiplies 8 to 13 times
 // for every 16 bytes that it reads from there.  Where there are few rows, `splits` CTAs share their keys and a
-// second kernel joins what they found.  4096 new tokens, 8 heads on 2 of 128: 1.0 ms, 34 TFLOP/s of the 74 that fp32
+// second kernel joins what they found.  4096 new tokens, 8 heads on 2 of 128: 0.98 ms, 35 TFLOP/s of the 74 that fp32
 // multiply-adds reach; the stores that stage a block and the reads of it are what the rest goes to.
 #include "kda_paged.cuh"
 
@@ -196,7 +196,7 @@ paged_simt_kernel(Cache c, const TQ *__restrict__ q, int64_t q_stride, TQ *__res
         float s[R][4];
 #pragma unroll
         for (int i = 0; i < R; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
         for (int d = 0; d < D; d += 4) {
             float4 x[R];
 #pragma unroll
@@ -237,7 +237,7 @@ paged_simt_kernel(Cache c, const TQ *__restrict__ q, int64_t q_stride, TQ *__res
                 for (int x = 0; x < 4; ++x) acc[i][j][x] *= keep;
         }
         __syncwarp();   // (a warp's rows are its own)
-#pragma unroll 2
+#pragma unroll 4
         for (int k = 0; k < BK; k += 4) {
             float4 p[R];
 #pragma unroll
@@ -288,7 +288,7 @@ paged_simt_kernel(Cache c, const TQ *__restrict__ q, int64_t q_stride, TQ *__res
 }
 
 // A row a warp, a split a lane: what the splits count for at once, then their sums, four on their way.  (An
-// element a thread, one split after the other, 40 of them took 400 us.)
+// element a thread, one split after the other, 40 of them took 400 us; four rows a warp 25 us longer than one.)
 template <typename TQ, int D>
 __global__ void __launch_bounds__(kThreads)
 paged_simt_join(Cache c, TQ *__restrict__ o, int group, int splits, const float *__restrict__ part) {
@@ -349,7 +349,7 @@ static int64_t tiles_of(const Cache &c, int group) {
 }
 // CTAs that share a tile's keys: enough for four a multiprocessor, each with 128 keys or more.  (Three are there
 // at once with D = 128, four or five with less.  With 2, 3, 4, 6 a multiprocessor 4096 new tokens, 8 heads on 2 of 128,
-// take 1231, 1234, 997, 1008 us; 2048 tokens 331, 331, 350, 335; of 64: 195, 196, 160, 176.)
+// took 1231, 1234, 997, 1008 us; 2048 tokens 331, 331, 350, 335; of 64: 195, 196, 160, 176.)
 static int splits_of(const Cache &c, int group, int sms) {
     const int64_t ctas = tiles_of(c, group) * c.Hk;
     if (ctas == 0) return 1;
@@ -370,7 +370,7 @@ static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, in
     paged_simt_kernel<TQ, TC, D><<<dim3((unsigned)ctas, splits), kThreads, sizeof(Shared<D>), s>>>(
         c, (const TQ *)q, qs, (TQ *)o, group, scale, window, sinks, splits, part, st);
     if (splits > 1)
-        paged_simt_join<TQ, D><<<dim3((unsigned)ctas, 4), kThreads, 0, s>>>(c, (TQ *)o, group, splits, part);
+        paged_simt_join<TQ, D><<<dim3((unsigned)ctas, BR * 32 / kThreads), kThreads, 0, s>>>(c, (TQ *)o, group, splits, part);
     return cudaGetLastError();
 }
 

@@ -33,7 +33,7 @@
 // What bounds it: the chain scores -> weights -> product of each tile, two of which share one tensor pipe.  With D =
 // 128 a block takes 3.3k to 3.5k cycles, 2063 of them products (54 % of the tensor pipe's time; the
 // special-function unit is at 27 %).  8192 tokens, 32 heads on 8 of 128, bf16: 451 to 463 us, 1.19 to 1.22 PFLOP/s; 512
-// tokens behind 65000: 410 to 418 us, 1.31 to 1.33; 16 chunks with prefixes from e4m3 pages 0.94 to 0.95, the making of
+// tokens behind 65000: 410 to 448 us, 1.22 to 1.33; 16 chunks with prefixes from e4m3 pages 0.94 to 0.97, the making of
 // operands beside it (51 % of all issue slots).  D = 64: 0.85 (the rows' own time), with a window of 1024 0.44.
 #include "kda_paged_tc.cuh"
 
