@@ -97,7 +97,10 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar0, uint32_t parity0, uint3
                 : "=r"(ok)
                 : "r"(bar), "r"(parity)
                 : "memory");
-        if (__all_sync(0xffffffffu, ok != 0)) return true;
+        if (__all_sync(0xffffffffu, ok != 0)) {
+            __syncwarp();   // (what one lane has seen arrive, all may use: a vote orders no memory)
+            return true;
+        }
         if ((i & 255u) == 0) {
             const uint64_t now = globaltimer_ns();
             if (i == 0) begin = now;
