@@ -53,9 +53,10 @@ struct alignas(16) Item {
     int pad;
     __device__ __forceinline__ int tile(int k) const { return k < sinks ? k : from + k - sinks; }
 };
-// Piece u of an item's tiles
+// Pieces of an item's tiles, and where piece u begins: the first few have a tile more than the others.  (tiles * u /
+// count would pass 32 bits from 92681 tiles on.)
 __device__ __forceinline__ int pieces(int tiles) { return (tiles + kTiles - 1) / kTiles; }
-__device__ __forceinline__ int piece_at(int tiles, int count, int u) { return tiles * u / count; }
+__device__ __forceinline__ int piece_at(int tiles, int count, int u) { return u * (tiles / count) + min(u, tiles % count); }
 
 template <int D, int NR, bool E4M3> struct Map {
     static constexpr int kCols = E4M3 ? 2 * NR : NR;         // columns in use: heads; (e4m3) their second parts
