@@ -29,27 +29,25 @@ struct Cache {
 };
 
 // The new tokens of sequence n and where they stand: rows [begin, begin + len), the first at position
-// `pos`.  A sequence that does not fit has len 0.
+// `pos`.  A sequence that does not fit (the first one also where it does not begin at 0) has len 0.
 struct Span {
     int begin, len, pos;
 };
-__device__ __forceinline__ bool lens_ok(const Cache &c, int begin, int end, int ctx) {
-    return begin >= 0 && begin <= end && end <= c.T && ctx >= 0 && ctx <= ((int64_t)c.width << c.shift);
+__device__ __forceinline__ bool lens_ok(const Cache &c, int n, int begin, int end, int ctx) {
+    return (n > 0 || begin == 0) && begin >= 0 && begin <= end && end <= c.T && ctx >= 0 && ctx <= ((int64_t)c.width << c.shift);
 }
 __device__ __forceinline__ Span span_of(const Cache &c, int n) {
     const int ctx = c.kv_lens[n], begin = c.cu ? c.cu[n] : n, end = c.cu ? c.cu[n + 1] : n + 1;
-    if (!lens_ok(c, begin, end, ctx)) return Span{0, 0, 0};
+    if (!lens_ok(c, n, begin, end, ctx)) return Span{0, 0, 0};
     return Span{begin, end - begin, ctx - (end - begin)};
 }
 
-// Reports sequences that do not fit, and a cu_seqlens that does not begin at 0; all threads of one
-// block.
+// Reports sequences that do not fit; all threads of one block.
 __device__ __forceinline__ void check_spans(const Cache &c, StatusWord *st) {
     if (!st) return;
     for (int n = threadIdx.x; n < c.N; n += blockDim.x) {
         const int begin = c.cu ? c.cu[n] : n, end = c.cu ? c.cu[n + 1] : n + 1;
-        if (!lens_ok(c, begin, end, c.kv_lens[n]) || (n == 0 && begin != 0))
-            report(st, KDA_ERR_SEQLENS, n, 61);
+        if (!lens_ok(c, n, begin, end, c.kv_lens[n])) report(st, KDA_ERR_SEQLENS, n, 61);
     }
 }
 

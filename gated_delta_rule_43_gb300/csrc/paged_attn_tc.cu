@@ -103,8 +103,8 @@ paged_plan_kernel(Cache c, Plan p, int group, int window, int sinks, StatusWord 
         int64_t x = 0, len = 0;
         if (n < c.N) {
             const int ctx = c.kv_lens[n], begin = c.cu[n], end = c.cu[n + 1];
-            if (lens_ok(c, begin, end, ctx)) len = end - begin;
-            if (!lens_ok(c, begin, end, ctx) || (n == 0 && begin != 0)) report(st, KDA_ERR_SEQLENS, n, 61);
+            if (lens_ok(c, n, begin, end, ctx)) len = end - begin;
+            else report(st, KDA_ERR_SEQLENS, n, 61);
             x = (len * group + kRows - 1) / kRows;
         }
         const int64_t mine = x, some = block_scan(x, warps);

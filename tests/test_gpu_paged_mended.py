@@ -4,10 +4,11 @@ import torch
 
 from gated_delta_rule_43_gb300 import kda
 from tests import paged_util as U
-from tests.paged_util import BF, E4M3
+from tests.paged_util import BF, E4M3, F32
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+KINDS = [(BF, BF), (BF, E4M3), (F32, F32), (F32, E4M3)]
 
 
 @pytest.mark.parametrize("cache", [BF, E4M3])
@@ -26,3 +27,42 @@ def test_single_tokens_behind_the_longest_context(cache):
     # 2 * 27595 * 2^-24 = 3.3e-3; beside that the roundings of any call (check_attention).
     slack = 2.0 ** -8 * (want.abs() + size) + 3.4e-3 * size + 1e-30
     assert got.isfinite().all() and ((got - want).abs() <= slack).all()
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8)
+
+
+def status_of(call):
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
+    call(ws)
+    return kda.query_status(ws)
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_a_first_sequence_that_does_not_begin_at_0_is_skipped(dtype, cache):
+    b = U.Batch([20, 10, 5], [0, 40, 7], 2, 64, dtype, cache, 16, device=DEV)
+    q, bad = b.queries(4), torch.tensor([1, 20, 30, 35], dtype=torch.int32, device=DEV)
+    good = kda.paged_attn_fwd(q, *b.cache, b.cu, **b.scales, check=True)
+    o = torch.full_like(good, 7.0)
+    assert status_of(lambda ws: kda.paged_attn_fwd(q, *b.cache, bad, **b.scales, o=o, workspace=ws)) == \
+        (kda.KDA_ERR_SEQLENS, 0)
+    assert (o[:20] == 7).all() and torch.equal(o[20:], good[20:])
+    want = kda.kv_cache_read(*b.cache, b.cu, total_tokens=35, **b.scales, check=True)
+    got = [torch.full_like(t, 7.0) for t in want]
+    assert status_of(lambda ws: kda.kv_cache_read(*b.cache, bad, total_tokens=35, **b.scales, k=got[0], v=got[1],
+                                                  workspace=ws)) == (kda.KDA_ERR_SEQLENS, 0)
+    for g, w in zip(got, want):
+        assert (g[:20] == 7).all() and torch.equal(g[20:], w[20:])
+    pools = [t for t in (b.k_pages, b.v_pages, b.k_scales, b.v_scales) if t is not None]
+    before = [t.clone() for t in pools]
+    k, v = q[:, :2], q[:, 2:]
+    kda.kv_cache_write(k, v, *b.cache, b.cu, **b.scales, check=True)
+    want = [t.clone() for t in pools]
+    own = b.table[0, :2].long()
+    for t, x, w in zip(pools, before, want):
+        t.copy_(x)
+        w[own] = x[own]
+    assert status_of(lambda ws: kda.kv_cache_write(k, v, *b.cache, bad, **b.scales, workspace=ws)) == \
+        (kda.KDA_ERR_SEQLENS, 0)
+    assert all(torch.equal(bits(t), bits(w)) for t, w in zip(pools, want))
