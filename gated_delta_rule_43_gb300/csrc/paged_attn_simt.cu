@@ -63,7 +63,30 @@ struct Place {
 struct Found {
     Tile tile;
     int there;
+    int64_t rows[kThreads / 32 - 1];   // of all sequences, added up by three warps
 };
+// The `tile`-th tile for a whole block.  False past the last, and where the sequences have more rows than there
+// are (of a cu_seqlens that goes back, which has been reported): none is gone through then.
+__device__ __forceinline__ bool find(const Cache &c, int tile, int group, Found &found) {
+    const int tid = threadIdx.x;
+    if (tid < 32) {
+        Tile t;
+        const bool there = find_tile(c, tile, group, t);
+        if (tid == 0) {
+            found.there = there;
+            if (there) found.tile = t;
+        }
+    } else {
+        int64_t rows = 0;
+        for (int n = tid - 32; n < c.N; n += kThreads - 32) rows += span_of(c, n).len;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
+        if (tid % 32 == 0) found.rows[tid / 32 - 1] = rows;
+    }
+    __syncthreads();
+    return found.there && found.rows[0] + found.rows[1] + found.rows[2] <= c.T;
+}
+static_assert(kThreads == 128, "three warps beside the first");
 template <int D> struct Shared {   // (D = 128: 76800 bytes, three CTAs an SM)
     float q[BR][D + 4];
     float k[BK][D + 4];
@@ -111,16 +134,7 @@ paged_simt_kernel(Cache c, const TQ *__restrict__ q, int64_t q_stride, TQ *__res
     const int tid = threadIdx.x, H = c.Hk * group;
     const int tile = (gridDim.x - 1 - blockIdx.x) / c.Hk, h = (gridDim.x - 1 - blockIdx.x) % c.Hk, split = blockIdx.y;
     if (blockIdx.x == 0 && split == 0) check_spans(c, st);
-    if (tid < 32) {
-        Tile t;
-        const bool there = find_tile(c, tile, group, t);
-        if (tid == 0) {
-            sm.found.there = there;
-            if (there) sm.found.tile = t;
-        }
-    }
-    __syncthreads();
-    if (!sm.found.there) return;
+    if (!find(c, tile, group, sm.found)) return;
     const Tile t = sm.found.tile;
     const float f = scale * kLog2e;
     for (int x = tid; x < BR * D; x += kThreads) {
@@ -295,16 +309,7 @@ paged_simt_join(Cache c, TQ *__restrict__ o, int group, int splits, const float 
     constexpr int V = D / 32;
     __shared__ Found found;
     const int tid = threadIdx.x, lane = tid & 31, h = (gridDim.x - 1 - blockIdx.x) % c.Hk, H = c.Hk * group;
-    if (tid < 32) {
-        Tile t;
-        const bool there = find_tile(c, (gridDim.x - 1 - blockIdx.x) / c.Hk, group, t);
-        if (tid == 0) {
-            found.there = there;
-            if (there) found.tile = t;
-        }
-    }
-    __syncthreads();
-    if (!found.there) return;
+    if (!find(c, (gridDim.x - 1 - blockIdx.x) / c.Hk, group, found)) return;
     const Tile t = found.tile;
     for (int r = blockIdx.y * (kThreads / 32) + tid / 32; r < t.rows; r += gridDim.y * (kThreads / 32)) {
         const float *from = part + ((int64_t)blockIdx.x * splits * BR + r) * (D + 4);

@@ -493,8 +493,10 @@ kda_status kda_state_pool_compact(float *pool, int32_t P, int64_t slot_elems,
  * call's tensors, or KDA_E4M3.  Sizes: total_tokens, table_width * page_size and (attention)
  * total_tokens * H / Hk below 2^31, and so the pool's runs, num_pages * page_stride / (page_size * D).  The struct is read during the call only.
  * Device-found errors: KDA_ERR_SEQLENS (info = the sequence: its rows or its length do not fit; it is
- * skipped, its rows are not written), KDA_ERR_INVALID_ARG (info = the sequence: a page outside
- * the pool; such a page is not touched and counts as zeros).
+ * skipped, its rows are not written; kda_paged_attn_fwd skips all where the lengths of the others add up to
+ * more than total_tokens; a row that several sequences of a cu_seqlens that goes back claim is any one's or
+ * nobody's), KDA_ERR_INVALID_ARG (info = the sequence: a page outside
+ * the pool; such a page is not touched and counts as zeros).  A call with total_tokens = 0 looks at nothing.
  */
 typedef struct kda_paged_cache {
     const int32_t *cu_seqlens;

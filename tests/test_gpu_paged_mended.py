@@ -66,3 +66,24 @@ def test_a_first_sequence_that_does_not_begin_at_0_is_skipped(dtype, cache):
     assert status_of(lambda ws: kda.kv_cache_write(k, v, *b.cache, bad, **b.scales, workspace=ws)) == \
         (kda.KDA_ERR_SEQLENS, 0)
     assert all(torch.equal(bits(t), bits(w)) for t, w in zip(pools, want))
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_sequences_of_more_tokens_than_there_are_rows(dtype, cache):
+    """A cu_seqlens that goes back: sequence 1 does not fit, and 0 and 2 have 40 tokens in 35 rows. Nothing is
+    written; with rows enough for 40 both are gone through (rows that both claim have the values of either)."""
+    b = U.Batch([20, 10, 20], [0, 40, 30], 2, 64, dtype, cache, 16, device=DEV)
+    bad = torch.tensor([0, 20, 15, 35], dtype=torch.int32, device=DEV)
+    q = b.queries(4)
+    for rows in (35, 50):
+        o = torch.full((rows, 4, 64), 7.0, dtype=dtype, device=DEV)
+        assert status_of(lambda ws: kda.paged_attn_fwd(q[:rows], *b.cache, bad, **b.scales, o=o, workspace=ws)) == \
+            (kda.KDA_ERR_SEQLENS, 1)
+        if rows == 35:
+            assert (o == 7).all()
+            continue
+        b.cu, b.T = torch.tensor([0, 20, 20, 50], dtype=torch.int32, device=DEV), 50
+        first = kda.paged_attn_fwd(q, b.k_pages, b.v_pages, b.table[:1], b.kv_lens[:1], b.cu[:2], **b.scales, check=True)
+        last = kda.paged_attn_fwd(q[15:35], b.k_pages, b.v_pages, b.table[2:].contiguous(), b.kv_lens[2:],
+                                  torch.tensor([0, 20], dtype=torch.int32, device=DEV), **b.scales, check=True)
+        assert torch.equal(o[:15], first[:15]) and torch.equal(o[20:35], last[5:]) and (o[35:] == 7).all()
