@@ -134,8 +134,9 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
     int64_t *sums = reinterpret_cast<int64_t *>(sm + M::kScan);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + M::kSlot);
     const uint32_t base = smem_u32(sm), bars = base + M::kBar;
-    if (base & 1023u) {   // the operand images need their alignment
+    if (base & 1023u) {   // the operand images need their alignment; nothing is left to be joined
         if (tid == 0) p.found[blockIdx.x] = StatusWord{KDA_ERR_CUDA, 90, 0};
+        if (tid < 2 && (tid == 0 || blockIdx.x + 1 == p.ranges)) p.cuts[blockIdx.x + tid] = Cut{0, 0, 0, 0, 0};
         return;
     }
     const int groups = (group + NR - 1) / NR;

@@ -50,3 +50,13 @@ def test_pieces_of_any_length(pieces, tiles):
         begin, end = begin_of(tiles, u), begin_of(tiles, u + 1)
         assert 0 <= begin < end <= begin + most and end <= tiles, u
     assert begin_of(tiles, 0) == 0 and begin_of(tiles, count) == tiles
+
+
+def test_a_call_that_gives_up_leaves_nothing_to_be_joined():
+    """The exit for shared memory that is not aligned (which no launch of today takes): the join reads the row of
+    cuts, which is the workspace's old content unless the exit writes it."""
+    code = source("paged_decode_tc.cu")
+    start = code.index("if (base & 1023u)")
+    leave = statements(code[start:])[0]
+    assert "return;" in leave
+    assert re.search(r"p\.cuts\[[^;]*\] = Cut\{0, 0, 0, 0, 0\};", leave[:leave.index("return;")])
