@@ -323,16 +323,10 @@ __device__ __forceinline__ Cut cut_at(const Cache &c, int64_t x, int n0, int n1,
         const int64_t cost = (int64_t)groups * c.Hk * each, rest = x - before;
         before += cost;
         if (rest >= cost) continue;
-        int item = (int)(rest / each);
+        const int item = (int)(rest / each);
         cut.k = (int)(rest - (int64_t)item * each) - kItemCost;
-        const bool next = count <= kUncut && 2 * cut.k > count;   // to the item's nearer end
-        if (cut.k < 1 || count <= kUncut) cut.k = 0;
-        if (next) ++item;
+        if (cut.k < 1 || count <= kUncut) cut.k = 0;   // to the item's begin
         cut.n = n;
-        if (item == groups * c.Hk) {
-            item = 0;
-            ++cut.n;
-        }
         cut.t = item / c.Hk;
         cut.h = item - cut.t * c.Hk;
         cut.tile = cut.n * groups + cut.t;

@@ -920,8 +920,8 @@ struct Layout {
 };
 static Layout layout_of(const Cache &c, int group, int D, int sms) {
     Layout L;
-    const int64_t rows = c.cu ? (int64_t)c.T * group : group;
-    L.most = c.cu ? rows / kRows + c.N : c.N * ((rows + kRows - 1) / kRows);
+    const int64_t rows = (int64_t)c.T * group;
+    L.most = rows / kRows + c.N;
     L.rows = (int)(rows < kRows ? rows : kRows);
     L.ranges = sms;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
