@@ -11,9 +11,9 @@ namespace kda {
 cudaError_t launch_kv_cache(bool write, int dtype, int cache_dtype, int D, const paged::Cache &c, void *k, void *v,
                             int64_t ks, int64_t vs, StatusWord *st, cudaStream_t s);
 size_t paged_simt_bytes(const paged::Cache &c, int group, int D, int sms);
-cudaError_t launch_paged_simt(int dtype, int cache_dtype, int D, const paged::Cache &c, const void *q, int64_t qs,
-                              void *o, int group, float scale, int window, int sinks, float *part, int sms,
-                              StatusWord *st, cudaStream_t s);
+cudaError_t launch_paged_simt(int cache_dtype, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
+                              float scale, int window, int sinks, float *part, int sms, StatusWord *st, cudaStream_t s);
+cudaError_t launch_paged_none(int64_t row_bytes, const paged::Cache &c, void *o, int group, StatusWord *st, cudaStream_t s);
 size_t paged_tc_bytes(const paged::Cache &c, int group, int D, int sms);
 cudaError_t launch_paged_tc(bool e4m3, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
                             float scale, int window, int sinks, void *ws, int sms, int left_out, cudaStream_t s);
@@ -102,15 +102,15 @@ bool attn_sizes_ok(const kda_paged_cache *p, int64_t T, int32_t H) {
 // Test hook (kda_test_paged_fault): what the next call leaves out.
 std::atomic<int> g_left_out{-1};
 
-// bf16 goes to the tensor cores (a pool without pages has nothing to load from).
-bool on_tensor_cores(const kda_paged_cache *p, int32_t dtype) { return dtype == KDA_BF16 && p->num_pages > 0; }
-
+// bf16 goes to the tensor cores, fp32 to the CUDA cores; a pool without pages has nothing to load (and no tensor
+// map).
 size_t attn_bytes(const kda_paged_cache *p, int64_t T, int32_t H, int32_t dtype) {
+    if (p->num_pages == 0) return kHeaderBytes;
     const paged::Cache c = make(p, T);
-    if (on_tensor_cores(p, dtype) && !p->cu_seqlens) return paged_decode_bytes(H / p->Hk, p->D, sm_count());
-    if (on_tensor_cores(p, dtype)) return paged_tc_bytes(c, H / p->Hk, p->D, sm_count());
-    if (dtype == KDA_F32 && !p->cu_seqlens) return paged_decode_simt_bytes(p->dtype == KDA_E4M3, H / p->Hk, p->D, sm_count());
-    return kHeaderBytes + paged_simt_bytes(c, H / p->Hk, p->D, sm_count());
+    const int group = H / p->Hk, sms = sm_count();
+    if (dtype == KDA_BF16) return p->cu_seqlens ? paged_tc_bytes(c, group, p->D, sms) : paged_decode_bytes(group, p->D, sms);
+    if (!p->cu_seqlens) return paged_decode_simt_bytes(p->dtype == KDA_E4M3, group, p->D, sms);
+    return kHeaderBytes + paged_simt_bytes(c, group, p->D, sms);
 }
 
 kda_status attn(const kda_paged_cache *p, const void *q, int64_t qs, void *o, int64_t T, int32_t H, int32_t dtype,
@@ -126,15 +126,18 @@ kda_status attn(const kda_paged_cache *p, const void *q, int64_t qs, void *o, in
     if (p->num_seqs > 0 && !cache_ok(p)) return KDA_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     StatusWord *st = (StatusWord *)workspace;
-    if (T > 0 && p->num_seqs > 0 && on_tensor_cores(p, dtype))
+    const bool e4m3 = p->dtype == KDA_E4M3, some = T > 0 && p->num_seqs > 0;
+    const int group = H / p->Hk;
+    if (some && p->num_pages > 0 && dtype == KDA_BF16)
         return cuda_status((p->cu_seqlens ? launch_paged_tc : launch_paged_decode)(
-            p->dtype == KDA_E4M3, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window, sinks, workspace, sm_count(), g_left_out.exchange(-1), s));
-    if (T > 0 && p->num_seqs > 0 && dtype == KDA_F32 && !p->cu_seqlens)
-        return cuda_status(launch_paged_decode_simt(p->dtype == KDA_E4M3, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window,
-                                                    sinks, workspace, sm_count(), s));
+            e4m3, p->D, make(p, T), q, qs, o, group, scale, window, sinks, workspace, sm_count(), g_left_out.exchange(-1), s));
+    if (some && p->num_pages > 0 && !p->cu_seqlens)
+        return cuda_status(launch_paged_decode_simt(e4m3, p->D, make(p, T), q, qs, o, group, scale, window, sinks, workspace,
+                                                    sm_count(), s));
     const kda_status e = clear(st, s);
-    if (e != KDA_OK || T == 0 || p->num_seqs == 0) return e;
-    return cuda_status(launch_paged_simt(dtype, p->dtype, p->D, make(p, T), q, qs, o, H / p->Hk, scale, window, sinks,
+    if (e != KDA_OK || !some) return e;
+    if (p->num_pages == 0) return cuda_status(launch_paged_none(p->D * bytes_of(dtype), make(p, T), o, group, st, s));
+    return cuda_status(launch_paged_simt(p->dtype, p->D, make(p, T), q, qs, o, group, scale, window, sinks,
                                          (float *)((uint8_t *)workspace + kHeaderBytes), sm_count(), st, s));
 }
 

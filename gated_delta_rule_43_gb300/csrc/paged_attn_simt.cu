@@ -1,5 +1,5 @@
-// paged_attn_simt.cu -- attention of a chunk of new tokens over a paged cache in single precision, on the CUDA cores
-// (and of anything over a pool without pages, which tensor maps cannot describe).
+// paged_attn_simt.cu -- attention of a chunk of new tokens over a paged cache in single precision, on the CUDA cores;
+// and any attention over a pool without pages.
 //
 //   o_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = exp(scale q_i k_j - m_i),   m_i the largest exponent
 // One pass over the keys with the running maximum and sum.  The query heads that share a key/value head
@@ -105,14 +105,6 @@ __device__ __forceinline__ void widen(const uint4 &x, float s, float (&y)[4], fl
     y[2] = __uint_as_float(x.z);
     y[3] = __uint_as_float(x.w);
 }
-__device__ __forceinline__ void widen(const uint4 &x, float s, float (&y)[8], __nv_bfloat16) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[2 * i] = __uint_as_float(w[i] << 16);
-        y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
 __device__ __forceinline__ void widen(const uint4 &x, float s, float (&y)[16], __nv_fp8_e4m3) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -124,9 +116,9 @@ __device__ __forceinline__ void widen(const uint4 &x, float s, float (&y)[16], _
     }
 }
 
-template <typename TQ, typename TC, int D>
+template <typename TC, int D>
 __global__ void __launch_bounds__(kThreads)
-paged_simt_kernel(Cache c, const TQ *__restrict__ q, int64_t q_stride, TQ *__restrict__ o, int group, float scale,
+paged_simt_kernel(Cache c, const float *__restrict__ q, int64_t q_stride, float *__restrict__ o, int group, float scale,
                   int window, int sinks, int splits, float *__restrict__ part, StatusWord *st) {
     constexpr int V = 16 / sizeof(TC), R = 4, C = D / 32;   // values a load; rows a thread; channels of it, in fours
     extern __shared__ __align__(16) uint8_t raw[];
@@ -142,7 +134,7 @@ paged_simt_kernel(Cache c, const TQ *__restrict__ q, int64_t q_stride, TQ *__res
         float y = 0.f;
         if (r < t.rows) {
             const int at = t.first + r;
-            y = to_f(q[(int64_t)(t.s.begin + at / group) * q_stride + (int64_t)(h * group + at % group) * D + d]) * f;
+            y = q[(int64_t)(t.s.begin + at / group) * q_stride + (int64_t)(h * group + at % group) * D + d] * f;
         }
         sm.q[r][d] = y;
     }
@@ -293,19 +285,19 @@ paged_simt_kernel(Cache c, const TQ *__restrict__ q, int64_t q_stride, TQ *__res
         }
         const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;   // (no visible key: zeros)
         const int at = t.first + r;
-        TQ *to = o + ((int64_t)(t.s.begin + at / group) * H + h * group + at % group) * D;
+        float *to = o + ((int64_t)(t.s.begin + at / group) * H + h * group + at % group) * D;
 #pragma unroll
         for (int j = 0; j < C; ++j)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) to[32 * j + 4 * k0 + x] = from_f<TQ>(l[i] != 0.f ? acc[i][j][x] * inv : 0.f);
+            for (int x = 0; x < 4; ++x) to[32 * j + 4 * k0 + x] = l[i] != 0.f ? acc[i][j][x] * inv : 0.f;
     }
 }
 
 // A row a warp, a split a lane: what the splits count for at once, then their sums, four on their way.  (An
 // element a thread, one split after the other, 40 of them took 400 us; four rows a warp 25 us longer than one.)
-template <typename TQ, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
-paged_simt_join(Cache c, TQ *__restrict__ o, int group, int splits, const float *__restrict__ part) {
+paged_simt_join(Cache c, float *__restrict__ o, int group, int splits, const float *__restrict__ part) {
     constexpr int V = D / 32;
     __shared__ Found found;
     const int tid = threadIdx.x, lane = tid & 31, h = (gridDim.x - 1 - blockIdx.x) % c.Hk, H = c.Hk * group;
@@ -342,9 +334,25 @@ paged_simt_join(Cache c, TQ *__restrict__ o, int group, int splits, const float 
 #pragma unroll
         for (int x = 16; x > 0; x /= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
         const int at = t.first + r;
-        TQ *to = o + ((int64_t)(t.s.begin + at / group) * H + h * group + at % group) * D + lane * V;
+        float *to = o + ((int64_t)(t.s.begin + at / group) * H + h * group + at % group) * D + lane * V;
 #pragma unroll
-        for (int j = 0; j < V; ++j) to[j] = from_f<TQ>(l != 0.f ? sum[j] / l : 0.f);
+        for (int j = 0; j < V; ++j) to[j] = l != 0.f ? sum[j] / l : 0.f;
+    }
+}
+
+// Over a pool without pages: every page is outside it, so that what tokens see counts as zeros and is reported.
+// `pieces`: 16-byte pieces of a row.
+__global__ void __launch_bounds__(kThreads)
+paged_none_kernel(Cache c, uint4 *__restrict__ o, int group, int pieces, StatusWord *st) {
+    __shared__ Found found;
+    const int tile = blockIdx.x / c.Hk, h = blockIdx.x % c.Hk, H = c.Hk * group;
+    if (blockIdx.x == 0) check_spans(c, st);
+    if (!find(c, tile, group, found)) return;
+    const Tile t = found.tile;
+    if (threadIdx.x == 0 && t.s.pos + (t.first + t.rows - 1) / group >= 0) report(st, KDA_ERR_INVALID_ARG, t.n, 64);
+    for (int x = threadIdx.x; x < t.rows * pieces; x += kThreads) {
+        const int at = t.first + x / pieces;
+        o[((int64_t)(t.s.begin + at / group) * H + h * group + at % group) * pieces + x % pieces] = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -364,18 +372,18 @@ static int splits_of(const Cache &c, int group, int sms) {
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
-template <typename TQ, typename TC, int D>
+template <typename TC, int D>
 static cudaError_t launch(const Cache &c, const void *q, int64_t qs, void *o, int group, float scale, int window,
                           int sinks, int splits, float *part, StatusWord *st, cudaStream_t s) {
     const int64_t ctas = tiles_of(c, group) * c.Hk;
     if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<TQ, TC, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<TC, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)sizeof(Shared<D>));
     if (e != cudaSuccess) return e;
-    paged_simt_kernel<TQ, TC, D><<<dim3((unsigned)ctas, splits), kThreads, sizeof(Shared<D>), s>>>(
-        c, (const TQ *)q, qs, (TQ *)o, group, scale, window, sinks, splits, part, st);
+    paged_simt_kernel<TC, D><<<dim3((unsigned)ctas, splits), kThreads, sizeof(Shared<D>), s>>>(
+        c, (const float *)q, qs, (float *)o, group, scale, window, sinks, splits, part, st);
     if (splits > 1)
-        paged_simt_join<TQ, D><<<dim3((unsigned)ctas, BR * 32 / kThreads), kThreads, 0, s>>>(c, (TQ *)o, group, splits, part);
+        paged_simt_join<D><<<dim3((unsigned)ctas, BR * 32 / kThreads), kThreads, 0, s>>>(c, (float *)o, group, splits, part);
     return cudaGetLastError();
 }
 
@@ -388,24 +396,24 @@ size_t paged_simt_bytes(const paged::Cache &c, int group, int D, int sms) {
     return (size_t)paged::simt::tiles_of(c, group) * c.Hk * splits * paged::simt::BR * (D + 4) * sizeof(float);
 }
 
-cudaError_t launch_paged_simt(int dtype, int cache_dtype, int D, const paged::Cache &c, const void *q, int64_t qs,
-                              void *o, int group, float scale, int window, int sinks, float *part, int sms,
-                              StatusWord *st, cudaStream_t s) {
+cudaError_t launch_paged_simt(int cache_dtype, int D, const paged::Cache &c, const void *q, int64_t qs, void *o, int group,
+                              float scale, int window, int sinks, float *part, int sms, StatusWord *st, cudaStream_t s) {
     const int splits = paged::simt::splits_of(c, group, sms);
-#define KDA_PAGED(TQ_, TC_, D_)                                                                                   \
-    if (D == D_)                                                                                                  \
-        return paged::simt::launch<TQ_, TC_, D_>(c, q, qs, o, group, scale, window, sinks, splits, part, st, s);
-#define KDA_PAGED_D(TQ_, TC_) KDA_PAGED(TQ_, TC_, 32) KDA_PAGED(TQ_, TC_, 64) KDA_PAGED(TQ_, TC_, 128)
-    if (dtype == KDA_F32) {
-        if (cache_dtype == KDA_E4M3) { KDA_PAGED_D(float, __nv_fp8_e4m3) }
-        else { KDA_PAGED_D(float, float) }
-    } else {
-        if (cache_dtype == KDA_E4M3) { KDA_PAGED_D(__nv_bfloat16, __nv_fp8_e4m3) }
-        else { KDA_PAGED_D(__nv_bfloat16, __nv_bfloat16) }
-    }
+#define KDA_PAGED(TC_, D_) \
+    if (D == D_) return paged::simt::launch<TC_, D_>(c, q, qs, o, group, scale, window, sinks, splits, part, st, s);
+#define KDA_PAGED_D(TC_) KDA_PAGED(TC_, 32) KDA_PAGED(TC_, 64) KDA_PAGED(TC_, 128)
+    if (cache_dtype == KDA_E4M3) { KDA_PAGED_D(__nv_fp8_e4m3) }
+    else { KDA_PAGED_D(float) }
 #undef KDA_PAGED_D
 #undef KDA_PAGED
     return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_paged_none(int64_t row_bytes, const paged::Cache &c, void *o, int group, StatusWord *st, cudaStream_t s) {
+    const int64_t ctas = paged::simt::tiles_of(c, group) * c.Hk;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+    paged::simt::paged_none_kernel<<<(unsigned)ctas, paged::simt::kThreads, 0, s>>>(c, (uint4 *)o, group, (int)(row_bytes / 16), st);
+    return cudaGetLastError();
 }
 
 }  // namespace kda

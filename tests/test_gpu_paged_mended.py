@@ -87,3 +87,35 @@ def test_sequences_of_more_tokens_than_there_are_rows(dtype, cache):
         last = kda.paged_attn_fwd(q[15:35], b.k_pages, b.v_pages, b.table[2:].contiguous(), b.kv_lens[2:],
                                   torch.tensor([0, 20], dtype=torch.int32, device=DEV), **b.scales, check=True)
         assert torch.equal(o[:15], first[:15]) and torch.equal(o[20:35], last[5:]) and (o[35:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_a_pool_without_pages(dtype, cache, D):
+    """Every page is outside it: what would be there counts as zeros and is reported."""
+    pages = torch.empty(0, 2, 16, D, dtype=cache, device=DEV)
+    scales = {} if cache is not E4M3 else dict(k_scales=torch.empty(0, 2, 16, device=DEV),
+                                               v_scales=torch.empty(0, 2, 16, device=DEV))
+    q = torch.randn(40, 6, D, device=DEV).to(dtype)
+    cu = torch.tensor([0, 5, 5, 30, 37], dtype=torch.int32, device=DEV)
+    table = torch.zeros(4, 3, dtype=torch.int32, device=DEV)
+    for lens, code in (([0, 0, 0, 0], (kda.KDA_OK, 0)), ([0, 0, 30, 0], (kda.KDA_ERR_INVALID_ARG, 2)),
+                       ([0, 0, 0, 49], (kda.KDA_ERR_SEQLENS, 3))):
+        kv_lens = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        o = torch.full_like(q, 7.0)
+        assert status_of(lambda ws: kda.paged_attn_fwd(q, pages, pages.clone(), table, kv_lens, cu, **scales, o=o,
+                                                       workspace=ws)) == code
+        skipped = code[0] == kda.KDA_ERR_SEQLENS
+        assert not o[:30].any() and (o[37:] == 7).all()
+        assert (o[30:37] == 7).all() if skipped else not o[30:37].any()
+        k = torch.full((40, 2, D), 7.0, dtype=dtype, device=DEV)
+        v = k.clone()
+        got = status_of(lambda ws: kda.kv_cache_write(k, v, pages, pages.clone(), table, kv_lens, cu, **scales, workspace=ws))
+        assert got == code
+        got = status_of(lambda ws: kda.kv_cache_read(pages, pages.clone(), table, kv_lens, cu, total_tokens=40, k=k, v=v,
+                                                     **scales, workspace=ws))
+        assert got == code and not k[:30].any() and not v[:30].any() and (k[37:] == 7).all()
+        one = torch.full((4, 6, D), 7.0, dtype=dtype, device=DEV)
+        assert status_of(lambda ws: kda.paged_attn_decode_step(q[:4], pages, pages.clone(), table, kv_lens, **scales, o=one,
+                                                               workspace=ws)) == code
+        assert not one[:3].any() and ((one[3] == 7).all() if skipped else not one[3].any())
