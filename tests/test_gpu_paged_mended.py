@@ -1,4 +1,6 @@
 """The paged cache and its attention: cases that once went wrong, or that nothing looked at."""
+import math
+
 import pytest
 import torch
 
@@ -87,6 +89,62 @@ def test_sequences_of_more_tokens_than_there_are_rows(dtype, cache):
         last = kda.paged_attn_fwd(q[15:35], b.k_pages, b.v_pages, b.table[2:].contiguous(), b.kv_lens[2:],
                                   torch.tensor([0, 20], dtype=torch.int32, device=DEV), **b.scales, check=True)
         assert torch.equal(o[:15], first[:15]) and torch.equal(o[20:35], last[5:]) and (o[35:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_what_is_not_finite_reaches_those_who_see_it(dtype, cache):
+    """A NaN in the key, then in the value, of one position and head: the tokens that see it, and no other head or
+    sequence; a key's no token before it either."""
+    for name in ("k_pages", "v_pages"):
+        b = U.Batch([100, 5], [300, 10], 2, 128, dtype, cache, 16, device=DEV)
+        q = b.queries(8)
+        good = kda.paged_attn_fwd(q, *b.cache, b.cu, **b.scales, check=True)
+        pages = getattr(b, name)
+        nan = torch.full((128,), math.nan, device=DEV).to(pages.dtype)
+        bits_of = pages.view(torch.uint8)
+        bits_of[int(b.table[0, 380 // 16]), 0, 380 % 16] = nan.view(torch.uint8)
+        o = kda.paged_attn_fwd(q, *b.cache, b.cu, **b.scales, check=True)
+        assert o[80:100, :4].isnan().all()
+        assert torch.equal(o[100:], good[100:]) and torch.equal(o[:, 4:], good[:, 4:])
+        if name == "k_pages":
+            assert torch.equal(o[:80, :4], good[:80, :4])
+        one = kda.paged_attn_decode_step(q[98:100], b.k_pages, b.v_pages, b.table[[0, 0]].contiguous(),
+                                         torch.tensor([399, 381], dtype=torch.int32, device=DEV), **b.scales, check=True)
+        assert one[:, :4].isnan().all() and one[:, 4:].isfinite().all()
+        one = kda.paged_attn_decode_step(q[99:100], b.k_pages, b.v_pages, b.table[:1], b.kv_lens[:1], window=19,
+                                         **b.scales, check=True)
+        assert one.isfinite().all()      # (positions 381 on: the window has passed it)
+        one = kda.paged_attn_decode_step(q[79:80], b.k_pages, b.v_pages, b.table[:1],
+                                         torch.tensor([380], dtype=torch.int32, device=DEV), **b.scales, check=True)
+        assert one.isfinite().all()      # (behind the sequence's end)
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_a_serving_loop_over_pages_of_nan(dtype, cache):
+    """A prompt in two chunks, then single tokens, in pages that held NaN: no slot counts before it is written."""
+    H, Hk, D, ps, total, first, second = 8, 2, 128, 16, 200, 77, 100
+    gen = torch.Generator(device=DEV).manual_seed(12)
+    x = torch.randn(total, H + 2 * Hk, D, device=DEV, generator=gen).to(dtype)
+    q = x[:, :H] * D ** -0.5
+    b = U.Batch([total], [0], Hk, D, dtype, cache, ps, device=DEV)
+    for t in (b.k_pages, b.v_pages):
+        t.view(torch.uint8).copy_(torch.full(t.shape, math.nan, device=DEV).to(t.dtype).view(torch.uint8))
+        assert t.float().isnan().all()
+    for t in (b.k_scales, b.v_scales):
+        if t is not None:
+            t.fill_(math.nan)
+    out = []
+    cuts = [0, first, first + second] + list(range(first + second + 1, total + 1))
+    for a, e in zip(cuts, cuts[1:]):
+        lens = torch.tensor([e], dtype=torch.int32, device=DEV)
+        cu = torch.tensor([0, e - a], dtype=torch.int32, device=DEV)
+        cache = (b.k_pages, b.v_pages, b.table, lens)
+        kda.kv_cache_write(x[a:e, H:H + Hk], x[a:e, H + Hk:], *cache, cu, **b.scales, check=True)
+        if e - a > 1:
+            out.append(kda.paged_attn_fwd(q[a:e], *cache, cu, **b.scales, check=True))
+        else:
+            out.append(kda.paged_attn_decode_step(q[a:e], *cache, **b.scales, check=True))
+    U.check_attention(torch.cat(out), b, q)
 
 
 @pytest.mark.parametrize("dtype,cache", KINDS)
