@@ -2,7 +2,8 @@
 // on the CUDA cores.
 //
 //   o = sum_j w_j v_j / sum_j w_j,   w_j = 2^(s_j - m),   s_j = scale log2(e) q k_j
-// Memory-bound: each key and value is read once for up to NR query heads that share it, 16 bytes a lane, so a
+// Memory-bound: each key and value is read once for up to NR query heads that share it (NR = 8, 4 from e4m3 pages:
+// more are further items, which read it again), 16 bytes a lane, so a
 // row of D values takes L = D / V lanes and a warp's load G = 32 / L rows.  Each lane multiplies its V channels of
 // U rows with those of the NR queries, and the U * NR sums over the L lanes of a row are put together by halves: a
 // lane passes on the half that is its neighbour's, so that each ends up with U * NR / L scores of its own, one

@@ -2,12 +2,13 @@
 // tensor cores.
 //
 //   S^T = K Q^T,  P = 2^(f S - f m),  O^T = V^T P^T     (formulas: paged_attn_tc.cu)
-// Memory-bound: each key and value is read once, for all query heads that share it.  These are few, so
+// Memory-bound: each key and value is read once for up to 16 query heads that share it (more are further items: 64
+// heads on one read it four times).  These are few, so
 // keys and channels are the products' 128 rows and the heads their columns: a tile of 128 keys goes from
 // its pages into shared memory and is an operand as it lies there, in bf16 or in e4m3.
 //
 // e4m3 pages meet e4m3 queries and weights, of which there are two each: x = hi + lo / 16, hi = e4m3(x), lo =
-// e4m3(16 (x - hi)), in columns of their own.  Together they hold the 8 bits of a bf16, down to 2^-22 of
+// e4m3(16 (x - hi)), in columns of their own.  Together they hold the 8 bits of a bf16, down to 2^-21 of
 // the largest (rows of queries are scaled by a power of two, weights so that their largest is 2^7 to 2^8), so the
 // keys' and values' bytes need no conversion: nothing but the products touches them.  A key's scale
 // multiplies its scores, a value's is part of its weight.

@@ -473,9 +473,10 @@ kda_status kda_state_pool_compact(float *pool, int32_t P, int64_t slot_elems,
  *                      may be halves of one pool [num_pages, 2, Hk, page_size, D]
  *   k_scales, v_scales [num_pages, Hk, page_size] fp32, scale_stride from page to page (a multiple of 4;
  *                      16-byte aligned), with dtype KDA_E4M3 (NULL otherwise): a row of D values
- *                      stands for scale * e4m3.  kda_kv_cache_write makes them powers of two, so that
- *                      scale * e4m3 is a bf16 exactly; other positive scales are taken too, at
- *                      one more rounding to bf16.
+ *                      stands for scale * e4m3.  kda_kv_cache_write makes them powers of two, 2^-100 to 2^119,
+ *                      so that scale * e4m3 is a bf16 exactly; other scales from 2^-100 to 2^119 are taken
+ *                      too, at one more rounding to bf16 in kda_paged_attn_fwd.  (Below 2^-100 a value may count as
+ *                      zero.)
  *   block_table        [num_seqs, table_width] int32: position j of sequence n lies in slot
  *                      j % page_size of page block_table[n][j / page_size].  Entries that hold no
  *                      position in use are not read (any value may stand there).
@@ -545,7 +546,9 @@ size_t kda_paged_attn_workspace_size(const kda_paged_cache *cache, int64_t total
  *   q [total_tokens, H, D] dtype, token stride q_stride; o [total_tokens, H, D] packed
  *   scale: positive and finite (1 for queries that kda_qk_norm_rope has scaled); window, sinks >= 0
  * Pages that no token of the call sees are not read.  With bf16 storage the weights are rounded to
- * bf16 before they meet the values; sums, maxima and products are fp32.  A key or value that is
+ * bf16 before they meet the values (in kda_paged_attn_decode_step from e4m3 pages they, and the queries, are sums of
+ * two e4m3: off by 2^-8 of themselves, or by 2^-21 of the largest of a row or of 512 keys' weights where that is
+ * more); sums, maxima and products are fp32.  A key or value that is
  * visible to one token and not finite may spread to other tokens of the call that stand close to it and do not
  * see it (their weight for it is 0, and 0 * inf is NaN); what stands in slots past kv_lens, or is seen by no
  * token of the call, never does.

@@ -177,3 +177,45 @@ def test_a_pool_without_pages(dtype, cache, D):
         assert status_of(lambda ws: kda.paged_attn_decode_step(q[:4], pages, pages.clone(), table, kv_lens, **scales, o=one,
                                                                workspace=ws)) == code
         assert not one[:3].any() and ((one[3] == 7).all() if skipped else not one[3].any())
+
+
+def test_small_weights_beside_a_large_one():
+    """One key whose weight is 2^16 to 2^22 times the others' and whose value is zero in half of the channels, where
+    the output is the others' sum; from e4m3 pages, where a weight is a sum of two e4m3 (off by 2^-8 of itself, or by
+    2^-21 of the largest weight times scale of its 512 keys)."""
+    b = U.Batch([1], [1999], 1, 64, BF, E4M3, 16, device=DEV)
+    q = torch.zeros(1, 4, 64, dtype=BF, device=DEV)
+    q[0, :, 0] = torch.tensor([16.0, 18.0, 20.0, 22.0], device=DEV)
+    k = torch.randn(2000, 1, 64, device=DEV) * 0.05
+    k[:, 0, 0] = 0
+    k[777, 0, 0] = math.log(2.0)
+    v = torch.randn(2000, 1, 64, device=DEV)
+    v[777, 0, ::2] = 0
+    kda.kv_cache_write(k.to(BF), v.to(BF), *b.cache, torch.tensor([0, 2000], dtype=torch.int32, device=DEV),
+                       **b.scales, check=True)
+    got = kda.paged_attn_decode_step(q, *b.cache, **b.scales, check=True).double()
+    want, size = U.attention(b, q)
+    page, slot = b.table[0, torch.arange(2000, device=DEV) // 16].long(), torch.arange(2000, device=DEV) % 16
+    keys = U.values(b.k_pages, b.k_scales)[page, 0, slot]
+    scale, byte = b.v_scales[page, 0, slot].double(), b.v_pages[page, 0, slot].double().abs()
+    w = torch.softmax(q[0].double() @ keys.T, -1)                                    # [4, 2000]
+    floor = 2.0 ** -21 * (w * scale).amax(-1, keepdim=True) * byte.sum(0)[None]      # [4, 64]
+    slack = 2.0 ** -8 * (want.abs() + size) + 2e-5 * size + floor[None] + 1e-30
+    assert ((got - want).abs() <= slack).all()
+
+
+@pytest.mark.parametrize("shift", [-93, 90])
+def test_scales_far_from_one(shift):
+    """Values whose scales are 2^-101 to 2^-99, and around 2^83, through every call."""
+    b = U.Batch([40, 1], [700, 2000], 2, 64, BF, E4M3, 16, device=DEV)
+    far = b.v_scales * 2.0 ** shift
+    assert 2.0 ** -101 <= far[far.isfinite()].min() and far[far.isfinite()].max() < 2.0 ** 100
+    q, back = b.queries(8), 2.0 ** -shift
+    scales = dict(k_scales=b.k_scales, v_scales=far)
+    U.check_attention(kda.paged_attn_fwd(q, *b.cache, b.cu, **scales, check=True).double() * back, b, q)
+    _, v = kda.kv_cache_read(*b.cache, b.cu, total_tokens=41, **b.scales, check=True)
+    _, w = kda.kv_cache_read(*b.cache, b.cu, total_tokens=41, **scales, check=True)
+    assert torch.equal(v.double(), w.double() * back)
+    b.cu, b.T = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV), 2
+    q = q[39:].contiguous()
+    U.check_attention(kda.paged_attn_decode_step(q, *b.cache, **scales, check=True).double() * back, b, q)
