@@ -219,3 +219,46 @@ def test_scales_far_from_one(shift):
     b.cu, b.T = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV), 2
     q = q[39:].contiguous()
     U.check_attention(kda.paged_attn_decode_step(q, *b.cache, **scales, check=True).double() * back, b, q)
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("D", [32, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (0, 3), (9, 2)])
+def test_padding_at_the_left_in_every_type(dtype, cache, D, window, sinks):
+    """Sequences of fewer tokens than rows, some of them across a tile; first tokens without a window count for nothing."""
+    lens, before = [8, 300, 40, 1, 150], [-3, -290, -40, 0, -1]
+    b = U.Batch(lens, before, 2, D, dtype, cache, 16, seed=D, device=DEV)
+    q = b.queries(6)
+    o = kda.paged_attn_fwd(q, *b.cache, b.cu, window=window, sinks=sinks, **b.scales, check=True)
+    U.check_attention(o, b, q, window=window, sinks=sinks)
+    k, v = kda.kv_cache_read(*b.cache, b.cu, total_tokens=b.T, **b.scales, check=True)
+    for row, n, pos in U.places(b):
+        if pos < 0:
+            assert not o[row].any() and not k[row].any() and not v[row].any()
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_windows_and_first_tokens_at_the_end_of_int32(dtype, cache):
+    most = (1 << 31) - 1
+    b = U.Batch([5, 200, 0, 9], [600, 13, 4, -9], 2, 64, dtype, cache, 16, device=DEV)
+    q = b.queries(8)
+    one = U.Batch([1] * 4, [600, 13, 0, 130], 2, 64, dtype, cache, 16, device=DEV)
+    one.kv_lens[2] = 0
+    p = one.queries(8)
+    for window, sinks in ((most, most), (most, 0), (1, most)):
+        o = kda.paged_attn_fwd(q, *b.cache, b.cu, window=window, sinks=sinks, **b.scales, check=True)
+        U.check_attention(o, b, q)
+        o = kda.paged_attn_decode_step(p, *one.cache, window=window, sinks=sinks, **one.scales, check=True)
+        U.check_attention(o, one, p)
+
+
+@pytest.mark.parametrize("cache", [BF, E4M3])
+def test_more_tiles_than_the_plan_keeps_in_shared_memory(cache):
+    """Chunks of 1 to 4 tiles of 256 rows, more than 4096 in all, over fewer and over more than 2048 sequences."""
+    for N, most in ((2000, 60), (3000, 30)):
+        lens = [1 + (7 * n) % most for n in range(N)]
+        assert sum(-(-16 * m // 256) for m in lens) > 4096
+        b = U.Batch(lens, [(5 * n) % 40 for n in range(N)], 1, 32, BF, cache, 16, device=DEV)
+        q = b.queries(16)
+        o = kda.paged_attn_fwd(q, *b.cache, b.cu, **b.scales, check=True)
+        U.check_attention(o, b, q)
