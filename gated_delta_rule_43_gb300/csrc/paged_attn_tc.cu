@@ -34,7 +34,12 @@
 // 128 a block takes 3.3k to 3.5k cycles, 2063 of them products (54 % of the tensor pipe's time; the
 // special-function unit is at 27 %).  8192 tokens, 32 heads on 8 of 128, bf16: 451 to 463 us, 1.19 to 1.22 PFLOP/s; 512
 // tokens behind 65000: 410 to 448 us, 1.22 to 1.33; 16 chunks with prefixes from e4m3 pages 0.94 to 0.97, the making of
-// operands beside it (51 % of all issue slots).  D = 64: 0.85 (the rows' own time), with a window of 1024 0.44.
+// operands beside it (51 % of all issue slots).  D = 64: 0.85 (the rows' own time), with a window of 1024 0.44.  Many
+// sequences of few new tokens cost as if they had 128 rows each: 256 of 4 tokens behind 512 to 8192 take 726 us from bf16
+// pages (6.3 TB/s), 1148 from e4m3 (2.1).
+//
+// A row's thread holds 128 scores in 168 registers (144 beside e4m3 pages) and spills: 176 bytes for heads of 128, 96 of
+// 64, 80 of 32; from e4m3 pages 460, 340, 332.
 #include "kda_paged_tc.cuh"
 
 namespace kda {

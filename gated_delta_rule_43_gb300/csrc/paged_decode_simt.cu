@@ -12,7 +12,8 @@
 //
 // The work is cut as for the tensor cores (paged_decode_tc.cu), into two ranges an SM.  A CTA's eight
 // warps take every eighth unit of 32 keys, each with its own maxima, and meet at an item's end.  64 sequences of
-// 512 to 8192 tokens, 32 heads on 8 of 128, fp32: 391 us, 5.8 TB/s; 4 of 300 to 20000, 8 heads of 64: 40 us.
+// 512 to 8192 tokens, 32 heads on 8 of 128, fp32: 391 to 399 us, 5.7 to 5.8 TB/s (four heads an item spill 108 bytes; from
+// e4m3 pages 351); 4 of 300 to 20000, 8 heads of 64: 40 us.
 #include "kda_paged_tc.cuh"
 
 namespace kda {
