@@ -38,8 +38,8 @@
 // sequences of few new tokens cost as if they had 128 rows each: 256 of 4 tokens behind 512 to 8192 take 726 us from bf16
 // pages (6.3 TB/s), 1148 from e4m3 (2.1).
 //
-// A row's thread holds 128 scores in 168 registers (144 beside e4m3 pages) and spills: 176 bytes for heads of 128, 96 of
-// 64, 80 of 32; from e4m3 pages 460, 340, 332.
+// A row's thread holds 128 scores in 168 registers (144 beside e4m3 pages) and spills: 204 bytes for heads of 128, 128 of
+// 64, 116 of 32; from e4m3 pages 484, 396, 364.
 #include "kda_paged_tc.cuh"
 
 namespace kda {
@@ -53,6 +53,10 @@ constexpr int kItemCost = 3;        // an item's queries and outputs, in blocks
 constexpr int kUncut = 6;           // blocks of an item that is not cut
 constexpr int kRing = 4;            // items known ahead
 constexpr float kGrow = 8.f;        // log2 of what the maximum may grow before O is rescaled
+// Blocks that O adds up: the tensor cores cut off what does not fit beside a large sum, 7e-7 of it a block (262144
+// tokens in one sum lost 1.4e-3, 4 M 2.4e-2), so what 256 blocks have left (1.7e-4) is put aside in fp32, and their weights'
+// sum with it.  9728 new tokens, 4 heads of 64 on one, behind 1 M others: 11.2 ms, 11.0 in one sum.
+constexpr int kSum = 256;
 
 constexpr int kPlanThreads = 1024;
 
@@ -183,7 +187,21 @@ struct alignas(16) Item {
     __device__ __forceinline__ int end(int tile) const {
         return tile == 0 ? k1a : rows > 128 ? k1 : k0;
     }
+    // Of Plan.part, where a row puts its sums aside: the item's own, or that of the range's last item, which
+    // is still to come.
+    __device__ __forceinline__ int aside() const { return 2 * (int)blockIdx.x + (k0 > 0 ? 0 : 1); }
 };
+// x += by * from[0 .. 7] (32-byte aligned; not looked at with by = 0)
+__device__ __forceinline__ void add_aside(const float *from, float by, float (&x)[8]) {
+    float y[8];
+    if (by == 0.f) return;
+    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3]), "=f"(y[4]), "=f"(y[5]), "=f"(y[6]), "=f"(y[7])
+                 : "l"(from)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fmaf(by, y[i], x[i]);
+}
 
 template <int D, bool E4M3> struct Map {
     static constexpr uint32_t kTile = 128 * D * 2;           // of keys, values or a tile's queries
@@ -311,81 +329,114 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             const int lowest = window > 0 ? max(max(pos, 0) - window, -1) : -1;   // keys above it are in the window
             const int end = it.end(tile), begin = it.k0;
             float m = -INFINITY, l = 0.f;   // m: of the scores as they come
-            for (int k = begin; k < end; ++k) {
-                if (!wait(M::kSReady + tile, s_phase)) return;
-                s_phase ^= 1;
-                tc_fence_after();
-                if (live) {
-                    const int key0 = it.block(k) * BK;
-                    float s[4][32];
+            for (int k = begin; k < end;) {
+                const int stop = min(end, k + kSum);
+                if (k > begin && live) {
+                    // O, complete before this block's scores are, and l to what the row has put aside, in units of the
+                    // present maximum
+                    if (!wait(M::kSReady + tile, s_phase)) return;
+                    tc_fence_after();
+                    const int64_t at = (int64_t)it.aside() * p.rows + r;
+                    const float now = m * f;
+                    float2 was = make_float2(-INFINITY, 0.f);   // (nothing yet)
+                    if (mine && k - begin > kSum) was = p.ml[at];
+                    const float by = was.x == -INFINITY ? 0.f : ex2(was.x - now);
+                    if (mine) p.ml[at] = make_float2(now, fmaf(by, was.y, l));
+                    l = 0.f;
+#pragma unroll 1
+                    for (int j = 0; j < DIM; j += 8) {
+                        float x[8];
+                        tmem_ld(tO + j, x);
+                        tmem_ld_wait();
+                        add_aside(p.part + at * DIM + j, by, x);
+                        uint32_t v[8];
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) tmem_ld32(tS + 32 * b, s[b]);
-                    tmem_ld_wait();
-                    // keys that one of the warp's rows does not see: -inf where it is this one
-                    if (key0 + BK - 1 > pos_lo || (window > 0 && key0 <= max(pos_hi, 0) - window && key0 + BK - 1 >= sinks)) {
-                        // (bits of a word at a time: compared key by key, a masked block took 2000 cycles more than others, and
-                        // its code cost those 200)
-                        const int upto = pos - key0, above = lowest - key0, first = sinks - key0;
+                        for (int i = 0; i < 8; ++i) {
+                            v[i] = __float_as_uint(x[i]);
+                            x[i] = 0.f;
+                        }
+                        if (mine) store32(p.part + at * DIM + j, v);
+                        __syncwarp();
+                        tmem_st8(tO + j, x);
+                    }
+                    tmem_st_wait();
+                }
+                for (; k < stop; ++k) {
+                    if (!wait(M::kSReady + tile, s_phase)) return;
+                    s_phase ^= 1;
+                    tc_fence_after();
+                    if (live) {
+                        const int key0 = it.block(k) * BK;
+                        float s[4][32];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) tmem_ld32(tS + 32 * b, s[b]);
+                        tmem_ld_wait();
+                        // keys that one of the warp's rows does not see: -inf where it is this one
+                        if (key0 + BK - 1 > pos_lo || (window > 0 && key0 <= max(pos_hi, 0) - window && key0 + BK - 1 >= sinks)) {
+                            // (bits of a word at a time: compared key by key, a masked block took 2000 cycles more than others, and
+                            // its code cost those 200)
+                            const int upto = pos - key0, above = lowest - key0, first = sinks - key0;
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                const uint32_t see = bits_upto(upto - 32 * b) & (~bits_upto(above - 32 * b) | bits_upto(first - 1 - 32 * b));
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) s[b][j] = see & (1u << j) ? s[b][j] : -INFINITY;
+                            }
+                        }
+                        float t[4];
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            const uint32_t see = bits_upto(upto - 32 * b) & (~bits_upto(above - 32 * b) | bits_upto(first - 1 - 32 * b));
+                            t[b] = s[b][0];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) s[b][j] = see & (1u << j) ? s[b][j] : -INFINITY;
+                            for (int j = 0; j < 32; j += 2) t[b] = max3(t[b], s[b][j], s[b][j + 1]);
                         }
-                    }
-                    float t[4];
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        t[b] = s[b][0];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) t[b] = max3(t[b], s[b][j], s[b][j + 1]);
-                    }
-                    const float top = max3(fmaxf(t[0], t[1]), t[2], t[3]);
-                    if (k == begin) {
-                        m = top;
-                    } else if (__any_sync(0xffffffffu, mine && top > m && !((top - m) * f <= kGrow))) {
-                        const float grown = fmaxf(m, top);
-                        const float keep = m == grown ? 1.f : ex2((m - grown) * f);
-                        m = grown;
-                        l *= keep;
+                        const float top = max3(fmaxf(t[0], t[1]), t[2], t[3]);
+                        if (k == begin) {
+                            m = top;
+                        } else if (__any_sync(0xffffffffu, mine && top > m && !((top - m) * f <= kGrow))) {
+                            const float grown = fmaxf(m, top);
+                            const float keep = m == grown ? 1.f : ex2((m - grown) * f);
+                            m = grown;
+                            l *= keep;
 #pragma unroll 1
-                        for (int j = 0; j < DIM; j += 8) {
-                            float x[8];
-                            tmem_ld(tO + j, x);
-                            tmem_ld_wait();
+                            for (int j = 0; j < DIM; j += 8) {
+                                float x[8];
+                                tmem_ld(tO + j, x);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] *= keep;
-                            tmem_st8(tO + j, x);
+                                for (int i = 0; i < 8; ++i) x[i] *= keep;
+                                tmem_st8(tO + j, x);
+                            }
                         }
+                        const float ref = m == -INFINITY ? 0.f : -m * f;
+                        const float2 f2 = make_float2(f, f), ref2 = make_float2(ref, ref);
+                        float2 sum = make_float2(0.f, 0.f), sum1 = sum;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                float2 x = fma2(make_float2(s[b][j], s[b][j + 1]), f2, ref2);
+                                x.x = ex2(x.x);
+                                x.y = ex2(x.y);
+                                if (j & 2) sum1 = add2(sum1, x);
+                                else sum = add2(sum, x);
+                                w[j / 2] = pack2(x.x, x.y);
+                            }
+                            tmem_st16(tS + 16 * b, w);
+                            if (b == 1) {
+                                tmem_st_wait();
+                                part_done(0);
+                            }
+                        }
+                        sum = add2(sum, sum1);
+                        l += sum.x + sum.y;
+                        tmem_st_wait();
+                    } else {
+                        part_done(0);
                     }
-                    const float ref = m == -INFINITY ? 0.f : -m * f;
-                    const float2 f2 = make_float2(f, f), ref2 = make_float2(ref, ref);
-                    float2 sum = make_float2(0.f, 0.f), sum1 = sum;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            float2 x = fma2(make_float2(s[b][j], s[b][j + 1]), f2, ref2);
-                            x.x = ex2(x.x);
-                            x.y = ex2(x.y);
-                            if (j & 2) sum1 = add2(sum1, x);
-                            else sum = add2(sum, x);
-                            w[j / 2] = pack2(x.x, x.y);
-                        }
-                        tmem_st16(tS + 16 * b, w);
-                        if (b == 1) {
-                            tmem_st_wait();
-                            part_done(0);
-                        }
-                    }
-                    sum = add2(sum, sum1);
-                    l += sum.x + sum.y;
-                    tmem_st_wait();
-                } else {
-                    part_done(0);
+                    part_done(1);
                 }
-                part_done(1);
             }
             if (end == begin) return;
             // the row's maximum and sum, for those who store its outputs (and have taken the last item's)
@@ -680,8 +731,24 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     }
                     const int r = 128 * tile + 32 * quarter + lane;
                     const bool live = r - lane < it.rows, mine = r < it.rows;   // (of a whole warp; this row)
-                    const float sum = tile ? l[1] : l[0];
+                    float sum = tile ? l[1] : l[0];
                     const uint32_t tO = tmem + 256 + D * tile + lanes;
+                    if (live && it.end(tile) - it.k0 > kSum) {   // with what the row has put aside
+                        const int64_t at = (int64_t)it.aside() * p.rows + r;
+                        const float2 was = mine ? p.ml[at] : make_float2(-INFINITY, 0.f);
+                        const float by = was.x == -INFINITY ? 0.f : ex2(was.x - (tile ? m[1] : m[0]));
+                        sum = fmaf(by, was.y, sum);
+#pragma unroll 1
+                        for (int j = 0; j < DIM; j += 8) {
+                            float x[8];
+                            tmem_ld(tO + j, x);
+                            tmem_ld_wait();
+                            add_aside(p.part + at * DIM + j, by, x);
+                            __syncwarp();
+                            tmem_st8(tO + j, x);
+                        }
+                        tmem_st_wait();
+                    }
                     if (live && it.slot >= 0) {
                         const int64_t at = (int64_t)it.slot * p.rows + r;
                         if (mine) p.ml[at] = make_float2(tile ? m[1] : m[0], sum);

@@ -262,3 +262,49 @@ def test_more_tiles_than_the_plan_keeps_in_shared_memory(cache):
         q = b.queries(16)
         o = kda.paged_attn_fwd(q, *b.cache, b.cu, **b.scales, check=True)
         U.check_attention(o, b, q)
+
+
+@pytest.mark.parametrize("cache", [BF, E4M3])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("T", [512, 29184])
+@pytest.mark.parametrize("grow", [False, True])
+def test_chunks_behind_millions_of_tokens(cache, D, T, grow):
+    """4 M tokens in two pages, over and over: a sum that is added up block after block must not lose what is
+    small beside it (32768 blocks; the tensor cores cut off what does not fit, which took 2.4 % off in one
+    sum). With 512 new tokens the SMs share items, with 29184 they have three each. `grow`: the second half's
+    first page brings a score that everything before is small beside."""
+    H, ps, width = 4, 1024, 4096
+    gen = torch.Generator(device=DEV).manual_seed(D)
+    k = torch.randn(2, 1, ps, D, device=DEV, generator=gen)
+    v = 1.0 + 0.25 * torch.randn(2, 1, ps, D, device=DEV, generator=gen)
+    q = torch.randn(T, H, D, device=DEV, generator=gen) * (2.0 * D ** -0.5)
+    if grow:
+        q.zero_()
+        q[:, :, 0] = torch.tensor([3.5, 4.0, 4.5, 5.0], device=DEV)
+        k[:, :, :, 0] = 0
+        k[1, 0, 5, 0] = 2.25
+    scales = {}
+    if cache is E4M3:
+        scales = dict(k_scales=torch.full((2, 1, ps), 2.0 ** -6, device=DEV), v_scales=torch.full((2, 1, ps), 2.0 ** -6, device=DEV))
+        k, v = k * 64, v * 64
+    k, v, q = k.to(cache), v.to(cache), q.to(BF)
+    half = 3 * width // 4
+    table = (torch.arange(width, device=DEV) >= half).to(torch.int32)[None].contiguous()
+    lens = torch.tensor([width * ps], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    o = kda.paged_attn_fwd(q, k, v, table, lens, cu, **scales, check=True)
+    rows = torch.cat([torch.arange(0, T, max(1, T // 300)), torch.tensor([T - 1])]).to(DEV)
+    keys, vals = (U.values(t, scales.get(n)).reshape(2 * ps, D) for t, n in ((k, "k_scales"), (v, "v_scales")))
+    # how often a token sees each of the 2048 different keys
+    seen = width * ps - T + rows + 1 - half * ps
+    times = torch.cat([torch.full((len(rows), ps), float(half), device=DEV, dtype=torch.float64),
+                       (seen[:, None] // ps + (torch.arange(ps, device=DEV) < seen[:, None] % ps)).double()], 1)
+    w = torch.einsum("thd,jd->thj", q[rows].double(), keys)
+    w = times[:, None] * torch.exp(w - w.amax(-1, keepdim=True))
+    want = torch.einsum("thj,jd->thd", w / w.sum(-1, keepdim=True), vals)
+    size = torch.einsum("thj,jd->thd", w / w.sum(-1, keepdim=True), vals.abs())
+    # as check_attention, and the sums' own: 256 blocks of 8 products each, at most 2^-23 of the sum cut off a product,
+    # then 128 such sums at 2^-24; a sum of weights of 32768 blocks, 2^-24 of it a block at most.
+    slack = 2.0 ** -8 * (want.abs() + size) + (2e-5 + 2048 * 2.0 ** -23 + (128 + 32768) * 2.0 ** -24) * size
+    off = (o[rows].double() - want).abs() - slack
+    assert o.isfinite().all() and off.max() <= 0, f"{off.max():.3e} over; mean off by {((o[rows].double() - want) / want).mean():.2e}"
