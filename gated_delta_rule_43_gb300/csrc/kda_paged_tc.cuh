@@ -61,7 +61,8 @@ __device__ __forceinline__ KeyBlocks blocks_of(const Tile &t, int window, int si
 
 // Waits of a whole warp on one barrier, which end: a try that finds nothing sleeps in hardware (3.7 us,
 // measured), so tries are counted: 2.2 s.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+constexpr uint32_t kTries = 600000;
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t tries = kTries) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .u32 i;\n\t"
@@ -70,14 +71,20 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "@p bra done_%=;\n\t"
         "add.u32 i, i, 1;\n\t"
-        "setp.lt.u32 q, i, 600000;\n\t"
+        "setp.lt.u32 q, i, %3;\n\t"
         "@q bra again_%=;\n"
         "done_%=:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(tries)
         : "memory");
     return __all_sync(0xffffffffu, ok != 0);
+}
+
+// Those of a wait that ends only with an item: 2.2 s for every 2^18 of the blocks that the longest may have (2^18 blocks
+// take the slowest kernel about half a second).
+__device__ __forceinline__ uint32_t item_tries(const Cache &c) {
+    return kTries * (1 + (((uint32_t)c.width << c.shift) >> 25));   // (width << shift is below 2^31)
 }
 
 // The same on up to three barriers at a time, a lane each: every wait of its own costs a warp 100 to 200

@@ -288,10 +288,14 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
         ok = ok && wait_warp(bars + 8 * which, parity);
         return ok;
     };
+    auto wait_item = [&](int which, uint32_t parity) {
+        ok = ok && wait_warp(bars + 8 * which, parity, item_tries(c));
+        return ok;
+    };
     // Each role goes through the items for itself; role(item) returns with ok false when a wait expired.
     auto each_item = [&](auto role) {
         Ring at;
-        while (wait(M::kItemFull + at.stage, at.phase)) {
+        while (wait_item(M::kItemFull + at.stage, at.phase)) {
             const Item &it = items[at.stage];   // (read where it is used: registers are few)
             if (it.n < 0) break;
             role(it);
@@ -635,7 +639,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     it.ctx = s.pos + s.len;
                     it.slot = it.k0 > 0 ? 2 * (int)blockIdx.x : it.k1 < kb.count ? 2 * (int)blockIdx.x + 1 : -1;
                 }
-                if (!wait(M::kItemFree + at.stage, at.phase ^ 1)) break;
+                if (!wait_item(M::kItemFree + at.stage, at.phase ^ 1)) break;
                 if (lane == 0) {
                     items[at.stage] = it;
                     mbar_arrive(&bar[M::kItemFull + at.stage]);
@@ -668,13 +672,13 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             // The queries of this warp's rows: a row's address by its lane, its 16-byte pieces side by side;
             // both tiles' on their way before the first is waited for
             auto load_queries = [&](const Ring &at) {
-                if (!wait(M::kItemFull + at.stage, at.phase)) return;
+                if (!wait_item(M::kItemFull + at.stage, at.phase)) return;
                 const Item &it = items[at.stage];
                 if (it.n < 0) return;
 #pragma unroll 1
                 for (int tile = 0; tile < 2; ++tile) {
                     if (it.end(tile) == it.k0) continue;
-                    if (!wait(M::kQFree + tile, (q_phase >> tile) & 1)) return;
+                    if (!wait_item(M::kQFree + tile, (q_phase >> tile) & 1)) return;
                     q_phase ^= 1u << tile;
                     const int row = 128 * tile + 32 * quarter;
                     if (row < it.rows) {
@@ -714,7 +718,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                 for (int tile = 0; tile < 2; ++tile) {
                     m[tile] = l[tile] = 0.f;
                     if (it.end(tile) == it.k0) continue;
-                    if (!wait(M::kEnds + tile, (o_phase >> tile) & 1)) return;
+                    if (!wait_item(M::kEnds + tile, (o_phase >> tile) & 1)) return;
                     m[tile] = tops[256 * tile];
                     l[tile] = tops[256 * tile + 128];
                     __syncwarp();

@@ -188,9 +188,13 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
         ok = ok && wait_warp(bars + 8 * which, parity);
         return ok;
     };
+    auto wait_item = [&](int which, uint32_t parity) {
+        ok = ok && wait_warp(bars + 8 * which, parity, item_tries(c));
+        return ok;
+    };
     auto each_item = [&](auto role) {
         Ring at;
-        while (wait(M::kItemFull + at.stage, at.phase)) {
+        while (wait_item(M::kItemFull + at.stage, at.phase)) {
             const Item &it = items[at.stage];   // (read where it is used: registers are few)
             if (it.n < 0) break;
             role(it);
@@ -656,7 +660,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
                 it.from = kb.from;
                 it.slot = it.k0 > 0 ? 2 * (int)blockIdx.x : it.k1 < kb.count ? 2 * (int)blockIdx.x + 1 : -1;
             }
-            if (!wait(M::kItemFree + at.stage, at.phase ^ 1)) break;
+            if (!wait_item(M::kItemFree + at.stage, at.phase ^ 1)) break;
             if (lane == 0) {
                 items[at.stage] = it;
                 mbar_arrive(&bar[M::kItemFull + at.stage]);
@@ -678,7 +682,7 @@ paged_decode_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, con
             const __nv_bfloat16 *x0 = q + (int64_t)it.n * q_stride + (int64_t)(it.h * group + it.row0) * DIM;
             uint8_t *place = sm + M::kQ + qs.stage * M::kQBytes;
             float *qf = reinterpret_cast<float *>(sm + M::kQf) + 16 * qs.stage;
-            if (!wait(M::kQFree + qs.stage, qs.phase ^ 1)) break;
+            if (!wait_item(M::kQFree + qs.stage, qs.phase ^ 1)) break;
             if constexpr (E4M3) {
                 constexpr int V = D / 32;   // channels a lane (heads of 32: the last 16 lanes have zeros)
 #pragma unroll 4

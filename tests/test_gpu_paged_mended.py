@@ -308,3 +308,45 @@ def test_chunks_behind_millions_of_tokens(cache, D, T, grow):
     slack = 2.0 ** -8 * (want.abs() + size) + (2e-5 + 2048 * 2.0 ** -23 + (128 + 32768) * 2.0 ** -24) * size
     off = (o[rows].double() - want).abs() - slack
     assert o.isfinite().all() and off.max() <= 0, f"{off.max():.3e} over; mean off by {((o[rows].double() - want) / want).mean():.2e}"
+
+
+def test_an_item_that_takes_longer_than_a_wait():
+    """2^28 tokens, one page over and over, and as many items as SMs: 2097152 blocks each, 2.9 s, where a wait ends
+    after 2.2. Whoever waits for an item's end has to wait longer."""
+    H, D, ps, T, width = 4, 64, 1024, 9728, 1 << 18
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    k = torch.randn(1, 1, ps, D, device=DEV, generator=gen).to(BF)
+    v = (1.0 + 0.25 * torch.randn(1, 1, ps, D, device=DEV, generator=gen)).to(BF)
+    q = (torch.randn(T, H, D, device=DEV, generator=gen) * (2.0 * D ** -0.5)).to(BF)
+    table = torch.zeros(1, width, dtype=torch.int32, device=DEV)
+    lens = torch.tensor([width * ps], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    o = kda.paged_attn_fwd(q, k, v, table, lens, cu, check=True)
+    rows = torch.arange(0, T, 31, device=DEV)
+    w = torch.softmax(torch.einsum("thd,jd->thj", q[rows].double(), k[0, 0].double()), -1)
+    want, size = (torch.einsum("thj,jd->thd", w, x) for x in (v[0, 0].double(), v[0, 0].double().abs()))
+    # as check_attention; 256 blocks of 8 products, 2^-23 of the sum each; 8192 such sums, of values and of weights, at 2^-24; a
+    # token sees 262134 to 262144 whole pages and part of one more: 1 / 262134 of a weight
+    slack = 2.0 ** -8 * (want.abs() + size) + (2e-5 + 2048 * 2.0 ** -23 + 2 * 8448 * 2.0 ** -24 + 4e-6) * size
+    assert o.isfinite().all() and ((o[rows].double() - want).abs() <= slack).all()
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_an_expired_wait_is_reported_with_a_wide_table(decode):
+    """A table with room for 2^25 tokens: waits for an item's end have twice the limit, and end as well."""
+    b = U.Batch([1, 1] if decode else [200, 9], [3000, 900], 2, 128, BF, BF, 16, device=DEV)
+    wide = torch.full((2, 1 << 21), 1 << 30, dtype=torch.int32, device=DEV)
+    wide[:, :b.table.shape[1]] = b.table
+    q = b.queries(8)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
+
+    def call():
+        if decode:
+            return kda.paged_attn_decode_step(q, b.k_pages, b.v_pages, wide, b.kv_lens, workspace=ws)
+        return kda.paged_attn_fwd(q, b.k_pages, b.v_pages, wide, b.kv_lens, b.cu, workspace=ws)
+    good = call()
+    U.check_attention(good, b, q)
+    assert kda.load().kda_test_paged_fault(2) == kda.KDA_OK
+    call()
+    assert kda.query_status(ws) == (kda.KDA_ERR_TIMEOUT, 2)
+    assert torch.equal(call(), good) and kda.query_status(ws)[0] == kda.KDA_OK
