@@ -38,8 +38,8 @@
 // sequences of few new tokens cost as if they had 128 rows each: 256 of 4 tokens behind 512 to 8192 take 726 us from bf16
 // pages (6.3 TB/s), 1148 from e4m3 (2.1).
 //
-// A row's thread holds 128 scores in 168 registers (144 beside e4m3 pages) and spills: 204 bytes for heads of 128, 128 of
-// 64, 116 of 32; from e4m3 pages 484, 396, 364.
+// A row's thread holds 128 scores in 168 registers (144 beside e4m3 pages) and spills: 176 bytes for heads of 128, 96 of
+// 64, 60 of 32; from e4m3 pages 380, 276, 252.
 #include "kda_paged_tc.cuh"
 
 namespace kda {
@@ -51,12 +51,12 @@ template <bool E4M3> constexpr int kThreads = E4M3 ? 640 : 512;
 constexpr int kRowWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kEdgeWarp = 12, kMakeWarp = 16;
 constexpr int kItemCost = 3;        // an item's queries and outputs, in blocks
 constexpr int kUncut = 6;           // blocks of an item that is not cut
+// Blocks in one sum: the tensor cores cut off what does not fit beside a large one, 7e-7 of it a block (262144 tokens in
+// one sum lost 1.4e-3, 4 M 2.4e-2), so a range's share of an item is gone through in links of up to 256 blocks (1.7e-4),
+// which are joined in fp32.  They also bound how long anyone waits for an item.
+constexpr int kSum = 256;
 constexpr int kRing = 4;            // items known ahead
 constexpr float kGrow = 8.f;        // log2 of what the maximum may grow before O is rescaled
-// Blocks that O adds up: the tensor cores cut off what does not fit beside a large sum, 7e-7 of it a block (262144
-// tokens in one sum lost 1.4e-3, 4 M 2.4e-2), so what 256 blocks have left (1.7e-4) is put aside in fp32, and their weights'
-// sum with it.  9728 new tokens, 4 heads of 64 on one, behind 1 M others: 11.2 ms, 11.0 in one sum.
-constexpr int kSum = 256;
 
 constexpr int kPlanThreads = 1024;
 
@@ -183,25 +183,15 @@ struct alignas(16) Item {
     int first, last;          // positions of the first and last token
     int ctx;
     int slot;                 // of Plan.part, or -1: the whole item
+    int chain;                // bit 0: links of it came before, bit 1: more come
+    // Of Plan.part, where the links before leave what they have: the item's own slot, or that of the range's last
+    // item, which is still to come.
+    int aside;
     __device__ __forceinline__ int block(int k) const { return k < sinks ? k : from + k - sinks; }
     __device__ __forceinline__ int end(int tile) const {
         return tile == 0 ? k1a : rows > 128 ? k1 : k0;
     }
-    // Of Plan.part, where a row puts its sums aside: the item's own, or that of the range's last item, which
-    // is still to come.
-    __device__ __forceinline__ int aside() const { return 2 * (int)blockIdx.x + (k0 > 0 ? 0 : 1); }
 };
-// x += by * from[0 .. 7] (32-byte aligned; not looked at with by = 0)
-__device__ __forceinline__ void add_aside(const float *from, float by, float (&x)[8]) {
-    float y[8];
-    if (by == 0.f) return;
-    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3]), "=f"(y[4]), "=f"(y[5]), "=f"(y[6]), "=f"(y[7])
-                 : "l"(from)
-                 : "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf(by, y[i], x[i]);
-}
 
 template <int D, bool E4M3> struct Map {
     static constexpr uint32_t kTile = 128 * D * 2;           // of keys, values or a tile's queries
@@ -288,14 +278,10 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
         ok = ok && wait_warp(bars + 8 * which, parity);
         return ok;
     };
-    auto wait_item = [&](int which, uint32_t parity) {
-        ok = ok && wait_warp(bars + 8 * which, parity, item_tries(c));
-        return ok;
-    };
     // Each role goes through the items for itself; role(item) returns with ok false when a wait expired.
     auto each_item = [&](auto role) {
         Ring at;
-        while (wait_item(M::kItemFull + at.stage, at.phase)) {
+        while (wait(M::kItemFull + at.stage, at.phase)) {
             const Item &it = items[at.stage];   // (read where it is used: registers are few)
             if (it.n < 0) break;
             role(it);
@@ -333,114 +319,81 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             const int lowest = window > 0 ? max(max(pos, 0) - window, -1) : -1;   // keys above it are in the window
             const int end = it.end(tile), begin = it.k0;
             float m = -INFINITY, l = 0.f;   // m: of the scores as they come
-            for (int k = begin; k < end;) {
-                const int stop = min(end, k + kSum);
-                if (k > begin && live) {
-                    // O, complete before this block's scores are, and l to what the row has put aside, in units of the
-                    // present maximum
-                    if (!wait(M::kSReady + tile, s_phase)) return;
-                    tc_fence_after();
-                    const int64_t at = (int64_t)it.aside() * p.rows + r;
-                    const float now = m * f;
-                    float2 was = make_float2(-INFINITY, 0.f);   // (nothing yet)
-                    if (mine && k - begin > kSum) was = p.ml[at];
-                    const float by = was.x == -INFINITY ? 0.f : ex2(was.x - now);
-                    if (mine) p.ml[at] = make_float2(now, fmaf(by, was.y, l));
-                    l = 0.f;
-#pragma unroll 1
-                    for (int j = 0; j < DIM; j += 8) {
-                        float x[8];
-                        tmem_ld(tO + j, x);
-                        tmem_ld_wait();
-                        add_aside(p.part + at * DIM + j, by, x);
-                        uint32_t v[8];
+            for (int k = begin; k < end; ++k) {
+                if (!wait(M::kSReady + tile, s_phase)) return;
+                s_phase ^= 1;
+                tc_fence_after();
+                if (live) {
+                    const int key0 = it.block(k) * BK;
+                    float s[4][32];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            v[i] = __float_as_uint(x[i]);
-                            x[i] = 0.f;
+                    for (int b = 0; b < 4; ++b) tmem_ld32(tS + 32 * b, s[b]);
+                    tmem_ld_wait();
+                    // keys that one of the warp's rows does not see: -inf where it is this one
+                    if (key0 + BK - 1 > pos_lo || (window > 0 && key0 <= max(pos_hi, 0) - window && key0 + BK - 1 >= sinks)) {
+                        // (bits of a word at a time: compared key by key, a masked block took 2000 cycles more than others, and
+                        // its code cost those 200)
+                        const int upto = pos - key0, above = lowest - key0, first = sinks - key0;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const uint32_t see = bits_upto(upto - 32 * b) & (~bits_upto(above - 32 * b) | bits_upto(first - 1 - 32 * b));
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) s[b][j] = see & (1u << j) ? s[b][j] : -INFINITY;
                         }
-                        if (mine) store32(p.part + at * DIM + j, v);
-                        __syncwarp();
-                        tmem_st8(tO + j, x);
                     }
+                    float t[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        t[b] = s[b][0];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) t[b] = max3(t[b], s[b][j], s[b][j + 1]);
+                    }
+                    const float top = max3(fmaxf(t[0], t[1]), t[2], t[3]);
+                    if (k == begin) {
+                        m = top;
+                    } else if (__any_sync(0xffffffffu, mine && top > m && !((top - m) * f <= kGrow))) {
+                        const float grown = fmaxf(m, top);
+                        const float keep = m == grown ? 1.f : ex2((m - grown) * f);
+                        m = grown;
+                        l *= keep;
+#pragma unroll 1
+                        for (int j = 0; j < DIM; j += 8) {
+                            float x[8];
+                            tmem_ld(tO + j, x);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] *= keep;
+                            tmem_st8(tO + j, x);
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : -m * f;
+                    const float2 f2 = make_float2(f, f), ref2 = make_float2(ref, ref);
+                    float2 sum = make_float2(0.f, 0.f), sum1 = sum;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float2 x = fma2(make_float2(s[b][j], s[b][j + 1]), f2, ref2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            if (j & 2) sum1 = add2(sum1, x);
+                            else sum = add2(sum, x);
+                            w[j / 2] = pack2(x.x, x.y);
+                        }
+                        tmem_st16(tS + 16 * b, w);
+                        if (b == 1) {
+                            tmem_st_wait();
+                            part_done(0);
+                        }
+                    }
+                    sum = add2(sum, sum1);
+                    l += sum.x + sum.y;
                     tmem_st_wait();
+                } else {
+                    part_done(0);
                 }
-                for (; k < stop; ++k) {
-                    if (!wait(M::kSReady + tile, s_phase)) return;
-                    s_phase ^= 1;
-                    tc_fence_after();
-                    if (live) {
-                        const int key0 = it.block(k) * BK;
-                        float s[4][32];
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) tmem_ld32(tS + 32 * b, s[b]);
-                        tmem_ld_wait();
-                        // keys that one of the warp's rows does not see: -inf where it is this one
-                        if (key0 + BK - 1 > pos_lo || (window > 0 && key0 <= max(pos_hi, 0) - window && key0 + BK - 1 >= sinks)) {
-                            // (bits of a word at a time: compared key by key, a masked block took 2000 cycles more than others, and
-                            // its code cost those 200)
-                            const int upto = pos - key0, above = lowest - key0, first = sinks - key0;
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) {
-                                const uint32_t see = bits_upto(upto - 32 * b) & (~bits_upto(above - 32 * b) | bits_upto(first - 1 - 32 * b));
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) s[b][j] = see & (1u << j) ? s[b][j] : -INFINITY;
-                            }
-                        }
-                        float t[4];
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            t[b] = s[b][0];
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2) t[b] = max3(t[b], s[b][j], s[b][j + 1]);
-                        }
-                        const float top = max3(fmaxf(t[0], t[1]), t[2], t[3]);
-                        if (k == begin) {
-                            m = top;
-                        } else if (__any_sync(0xffffffffu, mine && top > m && !((top - m) * f <= kGrow))) {
-                            const float grown = fmaxf(m, top);
-                            const float keep = m == grown ? 1.f : ex2((m - grown) * f);
-                            m = grown;
-                            l *= keep;
-#pragma unroll 1
-                            for (int j = 0; j < DIM; j += 8) {
-                                float x[8];
-                                tmem_ld(tO + j, x);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) x[i] *= keep;
-                                tmem_st8(tO + j, x);
-                            }
-                        }
-                        const float ref = m == -INFINITY ? 0.f : -m * f;
-                        const float2 f2 = make_float2(f, f), ref2 = make_float2(ref, ref);
-                        float2 sum = make_float2(0.f, 0.f), sum1 = sum;
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            uint32_t w[16];
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                float2 x = fma2(make_float2(s[b][j], s[b][j + 1]), f2, ref2);
-                                x.x = ex2(x.x);
-                                x.y = ex2(x.y);
-                                if (j & 2) sum1 = add2(sum1, x);
-                                else sum = add2(sum, x);
-                                w[j / 2] = pack2(x.x, x.y);
-                            }
-                            tmem_st16(tS + 16 * b, w);
-                            if (b == 1) {
-                                tmem_st_wait();
-                                part_done(0);
-                            }
-                        }
-                        sum = add2(sum, sum1);
-                        l += sum.x + sum.y;
-                        tmem_st_wait();
-                    } else {
-                        part_done(0);
-                    }
-                    part_done(1);
-                }
+                part_done(1);
             }
             if (end == begin) return;
             // the row's maximum and sum, for those who store its outputs (and have taken the last item's)
@@ -609,12 +562,13 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             const Cut to = p.cuts[blockIdx.x + 1];
             const int tiles = p.tiles[c.N];
             Span s{0, 0, 0};
-            int known = -1;
+            int known = -1, begin = from.k;   // the first link's first block
             while (true) {
                 const bool more = from.tile < tiles && (from.tile < to.tile || (from.tile == to.tile &&
                                                         (from.h < to.h || (from.h == to.h && from.k < to.k))));
                 Item it;
                 it.n = -1;
+                it.chain = 0;
                 if (more) {
                     if (known != from.n) {
                         s = span_of(c, from.n);
@@ -629,7 +583,9 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     it.tok0 = s.begin;
                     it.pos0 = s.pos;
                     it.k0 = from.k;
-                    it.k1 = same_item(from, to) ? min(to.k, kb.count) : kb.count;
+                    const int k1 = same_item(from, to) ? min(to.k, kb.count) : kb.count;   // of the last link
+                    it.k1 = min(k1, it.k0 + kSum);
+                    it.chain = (it.k0 > begin ? 1 : 0) + (it.k1 < k1 ? 2 : 0);
                     const int last = t.s.pos + (t.row0 + min(t.rows, 128) - 1) / group;
                     it.k1a = last < 0 ? it.k0 : max(it.k0, min(it.k1, kb.sinks + last / BK + 1 - kb.from));
                     it.sinks = kb.sinks;
@@ -637,9 +593,10 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     it.first = t.first;
                     it.last = t.last;
                     it.ctx = s.pos + s.len;
-                    it.slot = it.k0 > 0 ? 2 * (int)blockIdx.x : it.k1 < kb.count ? 2 * (int)blockIdx.x + 1 : -1;
+                    it.slot = begin > 0 ? 2 * (int)blockIdx.x : k1 < kb.count ? 2 * (int)blockIdx.x + 1 : -1;
+                    it.aside = 2 * (int)blockIdx.x + (begin > 0 ? 0 : 1);
                 }
-                if (!wait_item(M::kItemFree + at.stage, at.phase ^ 1)) break;
+                if (!wait(M::kItemFree + at.stage, at.phase ^ 1)) break;
                 if (lane == 0) {
                     items[at.stage] = it;
                     mbar_arrive(&bar[M::kItemFull + at.stage]);
@@ -647,7 +604,11 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                 __syncwarp();
                 if (!more) break;
                 at.step(kRing);
-                from.k = 0;
+                if (it.chain & 2) {
+                    from.k = it.k1;
+                    continue;
+                }
+                from.k = begin = 0;
                 if (++from.h == c.Hk) {
                     from.h = 0;
                     ++from.tile;
@@ -672,13 +633,13 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
             // The queries of this warp's rows: a row's address by its lane, its 16-byte pieces side by side;
             // both tiles' on their way before the first is waited for
             auto load_queries = [&](const Ring &at) {
-                if (!wait_item(M::kItemFull + at.stage, at.phase)) return;
+                if (!wait(M::kItemFull + at.stage, at.phase)) return;
                 const Item &it = items[at.stage];
                 if (it.n < 0) return;
 #pragma unroll 1
                 for (int tile = 0; tile < 2; ++tile) {
                     if (it.end(tile) == it.k0) continue;
-                    if (!wait_item(M::kQFree + tile, (q_phase >> tile) & 1)) return;
+                    if (!wait(M::kQFree + tile, (q_phase >> tile) & 1)) return;
                     q_phase ^= 1u << tile;
                     const int row = 128 * tile + 32 * quarter;
                     if (row < it.rows) {
@@ -718,7 +679,7 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                 for (int tile = 0; tile < 2; ++tile) {
                     m[tile] = l[tile] = 0.f;
                     if (it.end(tile) == it.k0) continue;
-                    if (!wait_item(M::kEnds + tile, (o_phase >> tile) & 1)) return;
+                    if (!wait(M::kEnds + tile, (o_phase >> tile) & 1)) return;
                     m[tile] = tops[256 * tile];
                     l[tile] = tops[256 * tile + 128];
                     __syncwarp();
@@ -735,65 +696,58 @@ paged_attn_kernel(Cache c, Plan p, const __grid_constant__ CUtensorMap tk, const
                     }
                     const int r = 128 * tile + 32 * quarter + lane;
                     const bool live = r - lane < it.rows, mine = r < it.rows;   // (of a whole warp; this row)
-                    float sum = tile ? l[1] : l[0];
+                    const float sum = tile ? l[1] : l[0];
                     const uint32_t tO = tmem + 256 + D * tile + lanes;
-                    if (live && it.end(tile) - it.k0 > kSum) {   // with what the row has put aside
-                        const int64_t at = (int64_t)it.aside() * p.rows + r;
-                        const float2 was = mine ? p.ml[at] : make_float2(-INFINITY, 0.f);
-                        const float by = was.x == -INFINITY ? 0.f : ex2(was.x - (tile ? m[1] : m[0]));
-                        sum = fmaf(by, was.y, sum);
+                    if (live) {
+                        // with what the links before have left, in units of the larger maximum; to `aside` if more is to
+                        // come or to be joined
+                        const int64_t at = (int64_t)it.aside * p.rows + r;
+                        const bool stored = it.slot >= 0 || (it.chain & 2);
+                        float2 was = make_float2(0.f, 0.f);
+                        if (mine && (it.chain & 1)) was = p.ml[at];
+                        const float own = tile ? m[1] : m[0], top = was.y == 0.f ? own : sum == 0.f ? was.x : fmaxf(was.x, own);
+                        const float a = sum != 0.f ? ex2(own - top) : 0.f, by = was.y != 0.f ? ex2(was.x - top) : 0.f;
+                        const float total = a * sum + by * was.y, inv = total != 0.f ? 1.f / total : 0.f;   // (no visible key: zeros)
+                        if (mine && stored) p.ml[at] = make_float2(top, total);
+                        const int token = (it.row0 + min(r, it.rows - 1)) / group, head = it.h * group + (it.row0 + r) - token * group;
+                        __nv_bfloat16 *to = o + ((int64_t)(it.tok0 + token) * c.Hk * group + head) * DIM;
+                        const bool wide = ((uintptr_t)to & 31) == 0;
 #pragma unroll 1
-                        for (int j = 0; j < DIM; j += 8) {
-                            float x[8];
-                            tmem_ld(tO + j, x);
-                            tmem_ld_wait();
-                            add_aside(p.part + at * DIM + j, by, x);
-                            __syncwarp();
-                            tmem_st8(tO + j, x);
-                        }
-                        tmem_st_wait();
-                    }
-                    if (live && it.slot >= 0) {
-                        const int64_t at = (int64_t)it.slot * p.rows + r;
-                        if (mine) p.ml[at] = make_float2(tile ? m[1] : m[0], sum);
-                        if (any) {
-#pragma unroll 1
-                            for (int j = 0; j < DIM; j += 16) {
-                                float x[16];
+                        for (int j = 0; j < DIM; j += 16) {
+                            float x[16];
+                            if (any) {
                                 tmem_ld(tO + j, x);
                                 tmem_ld_wait();
-                                uint32_t v[16];
+                            }
+                            if (by != 0.f) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4) {
+                                    const float4 y = *reinterpret_cast<const float4 *>(p.part + at * DIM + j + i);
+                                    x[i] = (a != 0.f ? a * x[i] : 0.f) + by * y.x;
+                                    x[i + 1] = (a != 0.f ? a * x[i + 1] : 0.f) + by * y.y;
+                                    x[i + 2] = (a != 0.f ? a * x[i + 2] : 0.f) + by * y.z;
+                                    x[i + 3] = (a != 0.f ? a * x[i + 3] : 0.f) + by * y.w;
+                                }
+                            }
+                            uint32_t v[16];
+                            if (stored) {
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(x[i]);
                                 if (mine) {
                                     store32(p.part + at * DIM + j, v);
                                     store32(p.part + at * DIM + j + 8, v + 8);
                                 }
-                            }
-                        }
-                    } else if (live) {
-                        const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (no visible key: zeros)
-                        const int token = (it.row0 + min(r, it.rows - 1)) / group, head = it.h * group + (it.row0 + r) - token * group;
-                        __nv_bfloat16 *to = o + ((int64_t)(it.tok0 + token) * c.Hk * group + head) * DIM;
-                        const bool wide = ((uintptr_t)to & 31) == 0;
-#pragma unroll 1
-                        for (int j = 0; j < DIM; j += 32) {
-                            float x[32];
-                            if (any) {
-                                tmem_ld32(tO + j, x);
-                                tmem_ld_wait();
-                            }
-                            uint32_t v[16];
+                            } else {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) v[i / 2] = any && inv != 0.f ? pack2(x[i] * inv, x[i + 1] * inv) : 0u;
-                            if (mine && wide) {
-                                store32(to + j, v);
-                                store32(to + j + 16, v + 8);
-                            } else if (mine) {
-#pragma unroll
-                                for (int i = 0; i < 16; i += 4)
-                                    *reinterpret_cast<uint4 *>(to + j + 2 * i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                                for (int i = 0; i < 16; i += 2) v[i / 2] = inv != 0.f ? pack2(x[i] * inv, x[i + 1] * inv) : 0u;
+                                if (mine && wide) {
+                                    store32(to + j, v);
+                                } else if (mine) {
+                                    *reinterpret_cast<uint4 *>(to + j) = make_uint4(v[0], v[1], v[2], v[3]);
+                                    *reinterpret_cast<uint4 *>(to + j + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                                }
                             }
+                            __syncwarp();
                         }
                     }
                     if (any) {

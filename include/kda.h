@@ -567,8 +567,8 @@ kda_status kda_paged_attn_decode_step(const kda_paged_cache *cache, const void *
 /*
  * Test hook for failure detection, as kda_test_la_fault: in the next attention call of this process that
  * runs on the tensor cores (bf16), whoever works on part `part` of the work (0 ..; -1:
- * nobody) leaves out its first load of keys, if it has any.  Its waits then expire (2.2 s each; up to 143 s where
- * block_table has room for 2^25 tokens a sequence and more), the
+ * nobody) leaves out its first load of keys, if it has any.  Its waits then expire (2.2 s each; for single tokens with a
+ * block_table of 2^25 tokens a sequence and more up to 143 s), the
  * call reports KDA_ERR_TIMEOUT (info: the part), and the next call is as ever.  KDA_ERR_INVALID_ARG for
  * part < -1.
  */

@@ -333,7 +333,7 @@ def test_an_item_that_takes_longer_than_a_wait():
 
 @pytest.mark.parametrize("decode", [False, True])
 def test_an_expired_wait_is_reported_with_a_wide_table(decode):
-    """A table with room for 2^25 tokens: waits for an item's end have twice the limit, and end as well."""
+    """A table with room for 2^25 tokens: single tokens' waits for an item's end have twice the limit, and end as well."""
     b = U.Batch([1, 1] if decode else [200, 9], [3000, 900], 2, 128, BF, BF, 16, device=DEV)
     wide = torch.full((2, 1 << 21), 1 << 30, dtype=torch.int32, device=DEV)
     wide[:, :b.table.shape[1]] = b.table
