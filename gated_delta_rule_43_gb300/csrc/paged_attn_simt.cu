@@ -7,7 +7,7 @@
 // them.  A CTA takes 64 rows and goes through blocks of 32 keys staged in shared memory as fp32; a thread has 4
 // rows and 4 keys of the scores, and of the outputs 4 rows and every eighth four channels, so that it multiplies 8 to 13 times
 // for every 16 bytes that it reads from there.  Where there are few rows, `splits` CTAs share their keys and a
-// second kernel joins what they found.  4096 new tokens, 8 heads on 2 of 128: 0.98 ms, 35 TFLOP/s of the 74 that fp32
+// second kernel joins what they found.  4096 new tokens, 8 heads on 2 of 128: 0.98 to 1.0 ms (0.97 from e4m3 pages), 35 TFLOP/s of the 74 that fp32
 // multiply-adds reach; the stores that stage a block and the reads of it are what the rest goes to.
 #include "kda_paged.cuh"
 
@@ -16,6 +16,10 @@ namespace paged {
 namespace simt {
 
 constexpr int BR = 64, BK = 32, kThreads = 128;
+// Blocks in one sum (8192 keys): a longer one leaves out what is small beside it (behind 1 M tokens 9e-5 on average, 3.7e-4 at
+// most; 65536 8e-6; with 1024 blocks a sum 2.7e-5 behind 1 M), so sums go to the outputs' place, in fp32 as they are, and begin again.  (Sums of weights have 32 times fewer terms.)  Then 8e-6
+// behind 1 M.
+constexpr int kSum = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Rows [first, first + rows) of sequence n's len * group.
@@ -117,7 +121,7 @@ __device__ __forceinline__ void widen(const uint4 &x, float s, float (&y)[16], _
 }
 
 template <typename TC, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, D == 128 ? 3 : D == 32 && sizeof(TC) == 1 ? 5 : 4)
 paged_simt_kernel(Cache c, const float *__restrict__ q, int64_t q_stride, float *__restrict__ o, int group, float scale,
                   int window, int sinks, int splits, float *__restrict__ part, StatusWord *st) {
     constexpr int V = 16 / sizeof(TC), R = 4, C = D / 32;   // values a load; rows a thread; channels of it, in fours
@@ -155,6 +159,27 @@ paged_simt_kernel(Cache c, const float *__restrict__ q, int64_t q_stride, float 
 #pragma unroll
         for (int j = 0; j < C; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
     }
+    // A row's outputs: o, or [tile, head][split][row] of `part`: D sums, the maximum, the sum of weights
+    auto place = [&](int r) {
+        const int at = t.first + r;
+        return splits > 1 ? part + (((int64_t)blockIdx.x * splits + split) * BR + r) * (D + 4)
+                          : o + ((int64_t)(t.s.begin + at / group) * H + h * group + at % group) * D;
+    };
+    // Adds what stands in the outputs' place to the sums (a thread's own elements); its maximum stands behind the
+    // row's queries
+    auto take = [&](int i) {
+        const float was = sm.q[r0 + 16 * i][D], by = was == -INFINITY ? 0.f : exp2f(was - m[i]);
+        if (by == 0.f || r0 + 16 * i >= t.rows) return;
+        const float *from = place(r0 + 16 * i);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const float4 y = *reinterpret_cast<const float4 *>(from + 32 * j + 4 * k0);
+            acc[i][j][0] = fmaf(by, y.x, acc[i][j][0]);
+            acc[i][j][1] = fmaf(by, y.y, acc[i][j][1]);
+            acc[i][j][2] = fmaf(by, y.z, acc[i][j][2]);
+            acc[i][j][3] = fmaf(by, y.w, acc[i][j][3]);
+        }
+    };
     auto look_up = [&](int b) {   // the place of block b's key tid
         const int key = kb.block(b) * BK + tid;
         Place y{-1, 0.f, 0.f};
@@ -176,104 +201,123 @@ paged_simt_kernel(Cache c, const float *__restrict__ q, int64_t q_stride, float 
     };
     if (tid < BK && b0 < b1) sm.places[tid] = look_up(b0);
     __syncthreads();
-    for (int b = b0; b < b1; ++b) {
-        const int key0 = kb.block(b) * BK;
-#pragma unroll 4
-        for (int x = tid; x < BK * D / V; x += kThreads) {
-            const int j = x / (D / V), d = x % (D / V) * V;
-            const Place y = sm.places[j];
-            uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-            if (y.at >= 0) {
-                kx = __ldg(reinterpret_cast<const uint4 *>((const TC *)c.k + y.at + d));
-                vx = __ldg(reinterpret_cast<const uint4 *>((const TC *)c.v + y.at + d));
-            }
-            float kf[V], vf[V];
-            widen(kx, y.ks, kf, TC());
-            widen(vx, y.vs, vf, TC());
+    for (int b = b0; b < b1;) {
+        const int stop = min(b1, b + kSum);
+        if (b > b0) {
 #pragma unroll
-            for (int i = 0; i < V; i += 4) {
-                *reinterpret_cast<float4 *>(&sm.k[j][d + i]) = make_float4(kf[i], kf[i + 1], kf[i + 2], kf[i + 3]);
-                *reinterpret_cast<float4 *>(&sm.v[j][d + i]) = make_float4(vf[i], vf[i + 1], vf[i + 2], vf[i + 3]);
-            }
-        }
-        __syncthreads();
-        Place next{-1, 0.f, 0.f};   // (on its way while the scores are formed)
-        if (tid < BK && b + 1 < b1) next = look_up(b + 1);
-        float s[R][4];
-#pragma unroll
-        for (int i = 0; i < R; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll 4
-        for (int d = 0; d < D; d += 4) {
-            float4 x[R];
-#pragma unroll
-            for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const float4 *>(&sm.q[r0 + 16 * i][d]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 y = *reinterpret_cast<const float4 *>(&sm.k[k0 + 8 * j][d]);
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-                    s[i][j] = fmaf(x[i].x, y.x, fmaf(x[i].y, y.y, fmaf(x[i].z, y.z, fmaf(x[i].w, y.w, s[i][j]))));
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            float top = m[i];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int key = key0 + k0 + 8 * j;
-                s[i][j] = key <= pos[i] && (key > lowest[i] || key < sinks) ? s[i][j] : -INFINITY;
-                top = fmaxf(top, s[i][j]);
-            }
-#pragma unroll
-            for (int x = 1; x < 8; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float ref = top == -INFINITY ? 0.f : top;
-            const float keep = exp2f(m[i] - ref);
-            m[i] = top;
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p = exp2f(s[i][j] - ref);
-                sum += p;
-                sm.p[r0 + 16 * i][k0 + 8 * j] = p;
-            }
-            l[i] = l[i] * keep + sum;   // (of this thread's keys: joined at the end)
-#pragma unroll
-            for (int j = 0; j < C; ++j)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) acc[i][j][x] *= keep;
-        }
-        __syncwarp();   // (a warp's rows are its own)
-#pragma unroll 4
-        for (int k = 0; k < BK; k += 4) {
-            float4 p[R];
-#pragma unroll
-            for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4 *>(&sm.p[r0 + 16 * i][k]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int i = 0; i < R; ++i) {
+                if (b - b0 > kSum) take(i);
+                __syncwarp();   // (a warp's rows are its own)
+                if (k0 == 0) sm.q[r0 + 16 * i][D] = m[i];
+                float *to = place(r0 + 16 * i);
 #pragma unroll
                 for (int j = 0; j < C; ++j) {
-                    const float4 y = *reinterpret_cast<const float4 *>(&sm.v[k + x][4 * k0 + 32 * j]);
-#pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        const float w = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
-                        acc[i][j][0] = fmaf(w, y.x, acc[i][j][0]);
-                        acc[i][j][1] = fmaf(w, y.y, acc[i][j][1]);
-                        acc[i][j][2] = fmaf(w, y.z, acc[i][j][2]);
-                        acc[i][j][3] = fmaf(w, y.w, acc[i][j][3]);
-                    }
+                    if (r0 + 16 * i < t.rows)
+                        *reinterpret_cast<float4 *>(to + 32 * j + 4 * k0) = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+                    acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
                 }
+            }
         }
-        if (tid < BK) sm.places[tid] = next;
-        __syncthreads();
+        for (; b < stop; ++b) {
+            const int key0 = kb.block(b) * BK;
+#pragma unroll 4
+            for (int x = tid; x < BK * D / V; x += kThreads) {
+                const int j = x / (D / V), d = x % (D / V) * V;
+                const Place y = sm.places[j];
+                uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
+                if (y.at >= 0) {
+                    kx = __ldg(reinterpret_cast<const uint4 *>((const TC *)c.k + y.at + d));
+                    vx = __ldg(reinterpret_cast<const uint4 *>((const TC *)c.v + y.at + d));
+                }
+                float kf[V], vf[V];
+                widen(kx, y.ks, kf, TC());
+                widen(vx, y.vs, vf, TC());
+#pragma unroll
+                for (int i = 0; i < V; i += 4) {
+                    *reinterpret_cast<float4 *>(&sm.k[j][d + i]) = make_float4(kf[i], kf[i + 1], kf[i + 2], kf[i + 3]);
+                    *reinterpret_cast<float4 *>(&sm.v[j][d + i]) = make_float4(vf[i], vf[i + 1], vf[i + 2], vf[i + 3]);
+                }
+            }
+            __syncthreads();
+            Place next{-1, 0.f, 0.f};   // (on its way while the scores are formed)
+            if (tid < BK && b + 1 < b1) next = look_up(b + 1);
+            float s[R][4];
+#pragma unroll
+            for (int i = 0; i < R; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll 4
+            for (int d = 0; d < D; d += 4) {
+                float4 x[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const float4 *>(&sm.q[r0 + 16 * i][d]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 y = *reinterpret_cast<const float4 *>(&sm.k[k0 + 8 * j][d]);
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        s[i][j] = fmaf(x[i].x, y.x, fmaf(x[i].y, y.y, fmaf(x[i].z, y.z, fmaf(x[i].w, y.w, s[i][j]))));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float top = m[i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int key = key0 + k0 + 8 * j;
+                    s[i][j] = key <= pos[i] && (key > lowest[i] || key < sinks) ? s[i][j] : -INFINITY;
+                    top = fmaxf(top, s[i][j]);
+                }
+#pragma unroll
+                for (int x = 1; x < 8; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                const float ref = top == -INFINITY ? 0.f : top;
+                const float keep = exp2f(m[i] - ref);
+                m[i] = top;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = exp2f(s[i][j] - ref);
+                    sum += p;
+                    sm.p[r0 + 16 * i][k0 + 8 * j] = p;
+                }
+                l[i] = l[i] * keep + sum;   // (of this thread's keys: joined at the end)
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[i][j][x] *= keep;
+            }
+            __syncwarp();   // (a warp's rows are its own)
+#pragma unroll 4
+            for (int k = 0; k < BK; k += 4) {
+                float4 p[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4 *>(&sm.p[r0 + 16 * i][k]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int j = 0; j < C; ++j) {
+                        const float4 y = *reinterpret_cast<const float4 *>(&sm.v[k + x][4 * k0 + 32 * j]);
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+                            const float w = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
+                            acc[i][j][0] = fmaf(w, y.x, acc[i][j][0]);
+                            acc[i][j][1] = fmaf(w, y.y, acc[i][j][1]);
+                            acc[i][j][2] = fmaf(w, y.z, acc[i][j][2]);
+                            acc[i][j][3] = fmaf(w, y.w, acc[i][j][3]);
+                        }
+                    }
+            }
+            if (tid < BK) sm.places[tid] = next;
+            __syncthreads();
+        }
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
+        if (b1 - b0 > kSum) take(i);
 #pragma unroll
         for (int x = 1; x < 8; x *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
         const int r = r0 + 16 * i;
         if (r >= t.rows) continue;
-        if (splits > 1) {   // [tile, head][split][row]: D sums, the maximum, the sum of weights
-            float *to = part + (((int64_t)blockIdx.x * splits + split) * BR + r) * (D + 4);
+        float *to = place(r);
+        if (splits > 1) {
 #pragma unroll
             for (int j = 0; j < C; ++j)
                 *reinterpret_cast<float4 *>(to + 32 * j + 4 * k0) = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
@@ -284,8 +328,6 @@ paged_simt_kernel(Cache c, const float *__restrict__ q, int64_t q_stride, float 
             continue;
         }
         const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;   // (no visible key: zeros)
-        const int at = t.first + r;
-        float *to = o + ((int64_t)(t.s.begin + at / group) * H + h * group + at % group) * D;
 #pragma unroll
         for (int j = 0; j < C; ++j)
 #pragma unroll

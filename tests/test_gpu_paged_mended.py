@@ -350,3 +350,36 @@ def test_an_expired_wait_is_reported_with_a_wide_table(decode):
     call()
     assert kda.query_status(ws) == (kda.KDA_ERR_TIMEOUT, 2)
     assert torch.equal(call(), good) and kda.query_status(ws)[0] == kda.KDA_OK
+
+
+@pytest.mark.parametrize("cache", [F32, E4M3])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("T", [40, 2432])
+def test_chunks_in_fp32_behind_a_million_tokens(cache, D, T):
+    """8192 keys over and over, with weights of very different sizes: one sum of a million of them leaves out what is
+    small beside it (3.7e-4 at most, 9e-5 on average). With 40 new tokens 64 CTAs share the keys, with 2432 few or none do."""
+    H, ps, width, pages = 4, 1024, 1024, 8
+    gen = torch.Generator(device=DEV).manual_seed(D)
+    k = torch.randn(pages, 1, ps, D, device=DEV, generator=gen)
+    v = 1.0 + 0.25 * torch.randn(pages, 1, ps, D, device=DEV, generator=gen)
+    q = torch.randn(T, H, D, device=DEV, generator=gen) * (2.0 * D ** -0.5)
+    scales = {}
+    if cache is E4M3:
+        scales = dict(k_scales=torch.full((pages, 1, ps), 2.0 ** -6, device=DEV),
+                      v_scales=torch.full((pages, 1, ps), 2.0 ** -6, device=DEV))
+        k, v = (k * 64).to(cache), (v * 64).to(cache)
+    table = (torch.arange(width, device=DEV) % pages).to(torch.int32)[None].contiguous()
+    lens = torch.tensor([width * ps], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    o = kda.paged_attn_fwd(q, k, v, table, lens, cu, **scales, check=True)
+    rows = torch.arange(0, T, max(1, T // 150), device=DEV)
+    keys, vals = (U.values(t, scales.get(n)).reshape(pages * ps, D) for t, n in ((k, "k_scales"), (v, "v_scales")))
+    seen = width * ps - T + rows + 1
+    times = (seen[:, None] // (pages * ps) + (torch.arange(pages * ps, device=DEV) < seen[:, None] % (pages * ps))).double()
+    w = torch.einsum("thd,jd->thj", q[rows].double(), keys)
+    w = times[:, None] * torch.exp(w - w.amax(-1, keepdim=True))
+    want, size = (torch.einsum("thj,jd->thd", w / w.sum(-1, keepdim=True), x) for x in (vals, vals.abs()))
+    # check_attention's 2e-5 of the sum of |w v|: half of it for the exponents, half for sums of 8192 keys, each of
+    # which rounds by 2^-25 of the sum so far: sqrt(8192) * 2^-25 = 2.7e-6 where they fall either way
+    off = (o[rows].double() - want).abs() - 2e-5 * size
+    assert o.isfinite().all() and off.max() <= 0, f"{off.max():.3e} over; mean off by {((o[rows].double() - want) / want).mean():.2e}"
