@@ -383,3 +383,42 @@ def test_chunks_in_fp32_behind_a_million_tokens(cache, D, T):
     # which rounds by 2^-25 of the sum so far: sqrt(8192) * 2^-25 = 2.7e-6 where they fall either way
     off = (o[rows].double() - want).abs() - 2e-5 * size
     assert o.isfinite().all() and off.max() <= 0, f"{off.max():.3e} over; mean off by {((o[rows].double() - want) / want).mean():.2e}"
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70000, 130), (40000, 20000)])
+def test_long_items_of_random_pages(dtype, cache, window, sinks):
+    """Contexts of 90000 tokens whose pages are all different, items that are not shared between SMs: joined links, through
+    a window and first tokens too."""
+    H, Hk, D, ps, ctx = 4, 1, 64, 64, 90000
+    T = 9728 if dtype is BF else 2432
+    gen = torch.Generator(device=DEV).manual_seed(window)
+    pages = -(-ctx // ps)
+    scales, pools = {}, []
+    for name in ("k_scales", "v_scales"):
+        x = torch.randn(pages, Hk, ps, D, device=DEV, generator=gen)
+        x[-1, :, ctx % ps:] = math.nan
+        if cache is E4M3:
+            scales[name] = torch.exp2(torch.randint(-8, -4, (pages, Hk, ps), device=DEV, generator=gen).float())
+            pools.append((x * 64).to(cache))
+        else:
+            pools.append(x.to(cache))
+    table = torch.randperm(pages, device=DEV, generator=gen).to(torch.int32)
+    k, v = (torch.empty_like(x.view(torch.uint8)).index_copy_(0, table.long(), x.view(torch.uint8)).view(cache) for x in pools)
+    stored = {n: torch.empty_like(s).index_copy_(0, table.long(), s) for n, s in scales.items()}
+    q = (torch.randn(T, H, D, device=DEV, generator=gen) * (2.0 * D ** -0.5)).to(dtype)
+    o = kda.paged_attn_fwd(q, k, v, table[None].contiguous(), torch.tensor([ctx], dtype=torch.int32, device=DEV),
+                           torch.tensor([0, T], dtype=torch.int32, device=DEV), window=window, sinks=sinks, **stored, check=True)
+    rows = torch.cat([torch.arange(0, T, max(1, T // 60)), torch.tensor([T - 1])]).to(DEV)
+    keys, vals = (U.values(x, scales.get(n)).reshape(-1, D)[:ctx] for x, n in zip(pools, ("k_scales", "v_scales")))
+    pos, j = ctx - T + rows[:, None], torch.arange(ctx, device=DEV)[None]
+    see = j <= pos
+    if window:
+        see &= (j > pos - window) | (j < sinks)
+    w = torch.einsum("thd,jd->thj", q[rows].double(), keys).masked_fill(~see[:, None], -math.inf).softmax(-1)
+    want, size = (torch.einsum("thj,jd->thd", w, x) for x in (vals, vals.abs()))
+    # as check_attention, and for bf16 what a link's products cut off (256 blocks of 8 products, 2^-23 of the sum each)
+    slack = 2e-5 * size + 1e-30
+    if dtype is BF:
+        slack += 2.0 ** -8 * (want.abs() + size) + 2048 * 2.0 ** -23 * size
+    assert o.isfinite().all() and ((o[rows].double() - want).abs() <= slack).all()
