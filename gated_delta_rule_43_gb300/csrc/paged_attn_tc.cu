@@ -10,6 +10,8 @@
 //
 // The running maximum only moves when it would grow by more than 2^8: until then P is up to 256 times
 // larger than it could be, which neither bf16 nor the fp32 sums mind, and O is not rescaled.
+// P is rounded to bf16 for its product (a product takes two operands of one type; P in two parts would cost a second product),
+// l is the sum before that: 2.1e-3 of relative L2 against 64 bits, of which rounding the outputs is 1.7e-3.
 //
 // The work.  A plan lists the tiles of all sequences, with the blocks that each sees, heads inside tiles, in
 // one row and cuts it into equal ranges, one an SM, wherever that falls: with few rows against a
@@ -33,7 +35,7 @@
 // What bounds it: the chain scores -> weights -> product of each tile, two of which share one tensor pipe.  With D =
 // 128 a block takes 3.3k to 3.5k cycles, 2063 of them products (54 % of the tensor pipe's time; the
 // special-function unit is at 27 %).  8192 tokens, 32 heads on 8 of 128, bf16: 451 to 463 us, 1.19 to 1.22 PFLOP/s; 512
-// tokens behind 65000: 410 to 448 us, 1.22 to 1.33; 16 chunks with prefixes from e4m3 pages 0.94 to 0.97, the making of
+// tokens behind 65000: 410 to 458 us, 1.20 to 1.33; 16 chunks with prefixes from e4m3 pages 0.94 to 0.97, the making of
 // operands beside it (51 % of all issue slots).  D = 64: 0.85 (the rows' own time), with a window of 1024 0.44.  Many
 // sequences of few new tokens cost as if they had 128 rows each: 256 of 4 tokens behind 512 to 8192 take 726 us from bf16
 // pages (6.3 TB/s), 1148 from e4m3 (2.1).

@@ -13,6 +13,8 @@
 // keys' and values' bytes need no conversion: nothing but the products touches them.  A key's scale
 // multiplies its scores, a value's is part of its weight.
 //
+// bf16 pages meet weights that are rounded to bf16 once; their sum is of those before the rounding.
+//
 // A piece of up to 4 tiles is gone through twice, keys, then values: all its scores stand in tensor memory
 // before the first weight is formed, so its maximum is known and nothing that the tensor cores add up
 // is rescaled.  Pieces are joined in registers, a thread a channel.  Loads and products take the keys of
