@@ -26,7 +26,7 @@
 // query heads; each CTA finds its own range (a scan over the lengths, 1 us) instead of waiting for a
 // plan.  What cuts inside items leave is joined by paged_join_kernel.
 //
-// 256 sequences of 512 to 8192 tokens, 32 heads on 8 of 128: 359 to 374 us from e4m3 pages, 6.4 to 6.6 TB/s; 660 us
+// 256 sequences of 512 to 8192 tokens, 32 heads on 8 of 128: 359 to 374 us from e4m3 pages, 6.3 to 6.6 TB/s; 660 us
 // from bf16, 6.9 TB/s.  64 heads 436 us, 128 heads 680 (e4m3; the weights' instructions), 256 heads 1313 (1385 from bf16: read
 // twice), heads of 64 311.
 //
